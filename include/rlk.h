@@ -47,8 +47,11 @@
  *     caller zeroes; may be NULL) as bit (1 << code): RLK_ERR_TARGET_RANGE
  *     for an active row whose target no shard owns (that row's outputs are
  *     NaN), RLK_ERR_TIMEOUT if a pipeline wait ran out (outputs undefined;
- *     the kernel returns instead of hanging).
- *   - T == 0 is a no-op returning RLK_OK; T < 0 or T > RLK_MAX_ROWS returns
+ *     the kernel returns instead of hanging), RLK_ERR_INVALID_ARG for
+ *     sequence offsets that do not ascend within [0, T], RLK_ERR_NONFINITE
+ *     for a gradient norm that is not finite.
+ *   - T == 0 is a no-op returning RLK_OK (the losses and sums of the
+ *     training-step calls still get their value for no tokens, 0); T < 0 or T > RLK_MAX_ROWS returns
  *     RLK_ERR_INVALID_ARG (kernels index rows in 32 bits and step past
  *     the last row by less than 2^20).
  *   - Inactive rows (active_mask[t] == 0) give out_logprob = out_lse = 0 and
@@ -79,7 +82,8 @@ typedef enum rlk_status {
     RLK_ERR_WORKSPACE = 4,     /* workspace smaller than rlk_workspace_size() */
     RLK_ERR_CUDA = 5,          /* a CUDA runtime/driver call failed (launch, device query) */
     RLK_ERR_TARGET_RANGE = 6,  /* device-detected: active row whose target no shard owns */
-    RLK_ERR_TIMEOUT = 7        /* device-detected: a bounded pipeline wait gave up */
+    RLK_ERR_TIMEOUT = 7,       /* device-detected: a bounded pipeline wait gave up */
+    RLK_ERR_NONFINITE = 8      /* device-detected: the gradient norm is infinite or NaN */
 } rlk_status_t;
 
 /* Per-token record of one vocabulary shard (16 bytes). */
@@ -97,6 +101,7 @@ typedef struct rlk_partial {
 #define RLK_MAX_ROWS 2146435072       /* 2^31 - 2^20: the largest T (rows) any call takes */
 #define RLK_DTYPE_F32 0               /* logits element types for the materialised-logits calls */
 #define RLK_DTYPE_BF16 1
+#define RLK_DTYPE_F16 2               /* gradients of rlk_grad_norm and rlk_grad_clip only */
 
 /* "rlk-linlogp-v1": names the numeric contract above. */
 const char* rlk_contract_id(void);
@@ -365,6 +370,160 @@ rlk_status_t rlk_linear_logprob_backward_from_logits(
  */
 rlk_status_t rlk_rmsnorm(const void* x, const void* residual, const void* gamma, float eps,
                          int64_t T, int64_t H, void* out, void* residual_out, rlk_stream_t stream);
+
+/*
+ * Backward of rlk_rmsnorm: with x the row that was normalised (rlk_rmsnorm's
+ * residual_out where it added a residual, its x where it did not) and rstd the
+ * forward's own (same tree, same rsqrt, same bits), per row
+ *   up_i    = grad_out_i * gamma_i
+ *   c       = rstd^2 / H * sum_i up_i * x_i           (fp32, pairwise over the features)
+ *   grad_x_i = rstd * (up_i - x_i * c) + grad_residual_i
+ *   grad_gamma_i = sum over the rows of grad_out_i * x_i * rstd
+ * in fp32, each grad_x element rounded once to its type.  grad_residual is
+ * the gradient that reached residual_out from further on (NULL where there
+ * is none); grad_x is then the gradient of both x and residual.  A row's
+ * grad_x does not depend on the batch around it; grad_gamma is the sum of
+ * min(T, 304) ranges of consecutive rows, in an order that T alone fixes.
+ * (The blog's sections 3.3 and 4.2 ask for a backward with the forward's
+ * numeric discipline; the strict-path table's "RMSNorm" row.)
+ *
+ *   grad_out       device, [T][H] of grad_out_dtype (RLK_DTYPE_F32 -- rlk_linear_logprob_backward's
+ *                  grad_hidden -- or RLK_DTYPE_BF16)
+ *   x, gamma       device, bf16 [T][H] and [H]
+ *   eps            as in the forward
+ *   grad_residual  device, [T][H] of grad_x_dtype, or NULL
+ *   grad_x         device, [T][H] of grad_x_dtype (RLK_DTYPE_F32 or RLK_DTYPE_BF16); may be
+ *                  grad_residual, or grad_out where the types are the same
+ *   grad_gamma     device, float [H], or NULL to skip; all zeros when T == 0
+ *   workspace      >= rlk_rmsnorm_backward_workspace_size(T, H) bytes, 256-byte aligned
+ *                  (NULL allowed when grad_gamma is NULL)
+ *   H              multiple of 64, at most 8192; every pointer 16-byte aligned
+ */
+size_t rlk_rmsnorm_backward_workspace_size(int64_t T, int64_t H);
+rlk_status_t rlk_rmsnorm_backward(const void* grad_out, int grad_out_dtype, const void* x,
+                                  const void* gamma, float eps, const void* grad_residual,
+                                  int64_t T, int64_t H, void* grad_x, int grad_x_dtype,
+                                  float* grad_gamma, void* workspace, size_t workspace_bytes,
+                                  rlk_stream_t stream);
+
+/*
+ * Clipped policy loss with a KL term, and its gradient with respect to the
+ * new log-probabilities, over packed sequences (the reinforcement-learning
+ * step that the pages' strict path serves: vime's trainer compares the
+ * rollout's logprobs with the training side's).  Per active token, with
+ * d = logprob - old_logprob, r = e^d and A its advantage:
+ *   s = min(r A, clamp(r, 1 - clip_low, 1 + clip_high) A)
+ *   s = max(s, dual_clip A)                    where dual_clip > 0 and A < 0
+ *   k = d' (k1), d'^2 / 2 (k2) or e^-d' - 1 + d' (k3), d' = logprob - ref_logprob
+ *   loss   = scale * sum_t w_t (-s_t + kl_coef k_t)
+ *   grad_t = scale * w_t (-(r A where s follows r, else 0) + kl_coef dk/dlogprob)
+ * with w_t = 1 (RLK_REDUCE_SUM), 1 / (active tokens) (RLK_REDUCE_TOKEN_MEAN)
+ * or 1 / (n_seqs * active tokens of t's sequence) (RLK_REDUCE_SEQ_MEAN; a
+ * sequence without active tokens adds 0 and still counts).  Whether a token
+ * is clipped is decided on the exact d, not on a rounded ratio.
+ *
+ * A token takes part if its mask is nonzero and it lies in
+ * [seq_offsets[0], seq_offsets[n_seqs]); any other token's inputs are not
+ * used (they may be NaN) and its grad is 0.  Per-token terms are fp32; their
+ * sums run over fixed ranges of 1024 tokens and then in fp64, so the results
+ * are the same bits on every run.  T == 0 gives loss and stats 0.
+ *
+ *   logprob, old_logprob  device, float [T]
+ *   ref_logprob   device, float [T], or NULL (then kl_coef must be 0)
+ *   advantages    device, float [T], or [n_seqs] with advantages_per_seq
+ *   active_mask   device, uint8 [T] or NULL
+ *   seq_offsets   device, int32 [n_seqs + 1], ascending within [0, T], or NULL for one sequence
+ *                 of all T tokens (n_seqs must be 1); offsets that are not ascending set
+ *                 RLK_ERR_INVALID_ARG in *dev_status and make loss and stats NaN
+ *   clip_low, clip_high  >= 0;  dual_clip  0 (off) or > 1;  kl_kind  RLK_KL_K1 .. RLK_KL_K3
+ *   out_loss      device, float [1]
+ *   out_stats     device, float [4]: sums (with weights w_t, without scale) of -s, of k, of the
+ *                 clipped tokens and of old_logprob - logprob
+ *   grad_logprob  device, float [T], or NULL for the loss alone
+ *   workspace     >= rlk_policy_loss_workspace_size(T, n_seqs) bytes, 256-byte aligned
+ */
+#define RLK_KL_K1 1
+#define RLK_KL_K2 2
+#define RLK_KL_K3 3
+#define RLK_REDUCE_SUM 0
+#define RLK_REDUCE_TOKEN_MEAN 1
+#define RLK_REDUCE_SEQ_MEAN 2
+size_t rlk_policy_loss_workspace_size(int64_t T, int64_t n_seqs);
+rlk_status_t rlk_policy_loss(const float* logprob, const float* old_logprob,
+                             const float* ref_logprob, const float* advantages,
+                             int advantages_per_seq, const uint8_t* active_mask,
+                             const int32_t* seq_offsets, int64_t n_seqs, int64_t T,
+                             double clip_low, double clip_high, double dual_clip, int kl_kind,
+                             double kl_coef, int reduction, double scale, float* out_loss,
+                             float* out_stats, float* grad_logprob, void* workspace,
+                             size_t workspace_bytes, int32_t* dev_status, rlk_stream_t stream);
+
+/*
+ * Preference loss on paired log ratios, and its gradient with respect to the
+ * log-probabilities, over 2 * n_pairs packed sequences.  With m_q the sum of
+ * logprob - ref_logprob over sequence q's active tokens (their mean with
+ * length_normalize; 0 where there are none), h = m_chosen - m_rejected and
+ * z = beta h - margin, per pair
+ *   RLK_PREF_SIGMOID  l = -(1 - label_smoothing) log sig(z) - label_smoothing log sig(-z)
+ *   RLK_PREF_HINGE    l = max(0, 1 - z)
+ *   RLK_PREF_IPO      l = (h - 1 / (2 beta))^2
+ * and loss = scale * (mean of l over the pairs; 0 when n_pairs == 0).  Pair i
+ * is sequences (2i, 2i + 1) with RLK_PAIRS_ADJACENT and (i, n_pairs + i) with
+ * RLK_PAIRS_HALVES, the chosen one first.  A pair's loss, rewards and
+ * gradients do not depend on where its sequences lie in the batch.
+ *
+ *   ref_logprob   device, float [T], or NULL (no reference: its terms are 0)
+ *   seq_offsets   device, int32 [2 * n_pairs + 1], ascending within [0, T], else
+ *                 RLK_ERR_INVALID_ARG in *dev_status and loss NaN
+ *   beta          > 0;  label_smoothing in [0, 1], 0 unless SIGMOID;  margin 0 with IPO
+ *   out_loss      device, float [1];  out_pair_loss  device, float [n_pairs]
+ *   out_rewards   device, float [2 * n_pairs]: beta m_q, in sequence order
+ *   grad_logprob  device, float [T], or NULL; 0 for inactive tokens and those of no sequence
+ *   n_pairs       at most 2^30
+ */
+#define RLK_PREF_SIGMOID 0
+#define RLK_PREF_HINGE 1
+#define RLK_PREF_IPO 2
+#define RLK_PAIRS_ADJACENT 0
+#define RLK_PAIRS_HALVES 1
+rlk_status_t rlk_preference_loss(const float* logprob, const float* ref_logprob,
+                                 const uint8_t* active_mask, const int32_t* seq_offsets,
+                                 int64_t n_pairs, int64_t T, int layout, int kind, double beta,
+                                 double label_smoothing, double margin, int length_normalize,
+                                 double scale, float* out_loss, float* out_pair_loss,
+                                 float* out_rewards, float* grad_logprob, int32_t* dev_status,
+                                 rlk_stream_t stream);
+
+/*
+ * Global gradient norm over many tensors, and clipping by it:
+ *   norm  = sqrt(sum of g^2 over all elements of all tensors)
+ *   scale = max_norm / norm where norm is finite and above max_norm, else 1
+ *   out   = RN(g * scale), rounded once to the tensor's type
+ * Squares and the sums over each tensor's 16384-element chunks are fp32 (so
+ * |g| above 1.8e19 makes the norm infinite and |g| below 1e-23 counts as 0),
+ * the sum of the chunks' fp64; the order depends on the tensors' sizes alone,
+ * not on their addresses.  A norm that is not finite leaves scale at 1 (the
+ * gradients keep their values) and sets RLK_ERR_NONFINITE in *dev_status.
+ *
+ *   grads, outs   HOST arrays of n_tensors DEVICE pointers, each aligned to its element size.
+ *                 outs[i] may be grads[i] (in place: nothing is written when scale is 1); any
+ *                 other overlap of an output with an input or output is RLK_ERR_INVALID_ARG
+ *   numels        HOST, elements per tensor (0 allowed; at most 2^40)
+ *   dtypes        HOST, RLK_DTYPE_F32, RLK_DTYPE_BF16 or RLK_DTYPE_F16 per tensor
+ *   max_norm      >= 0 (infinity allowed)
+ *   out_norm, out_scale  device, float [1] each
+ *   workspace     >= rlk_grad_norm_workspace_size(numels, n_tensors) bytes, 256-byte aligned
+ * The host arrays are read before the call returns.
+ */
+size_t rlk_grad_norm_workspace_size(const int64_t* numels, int64_t n_tensors);
+rlk_status_t rlk_grad_norm(const void* const* grads, const int64_t* numels,
+                           const int32_t* dtypes, int64_t n_tensors, float* out_norm,
+                           void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                           rlk_stream_t stream);
+rlk_status_t rlk_grad_clip(const void* const* grads, void* const* outs, const int64_t* numels,
+                           const int32_t* dtypes, int64_t n_tensors, double max_norm,
+                           float* out_norm, float* out_scale, void* workspace,
+                           size_t workspace_bytes, int32_t* dev_status, rlk_stream_t stream);
 
 /*
  * Same result as rlk_linear_logprob (same kernels, same bits), for callers

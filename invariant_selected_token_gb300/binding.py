@@ -9,6 +9,7 @@ to.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import List, Optional, Sequence, Tuple
@@ -20,11 +21,12 @@ LIB_PATH = os.path.join(HERE, "librlk.so")
 
 STATUS_NAMES = {0: "RLK_OK", 1: "RLK_ERR_INVALID_ARG", 2: "RLK_ERR_UNSUPPORTED",
                 3: "RLK_ERR_ALIGNMENT", 4: "RLK_ERR_WORKSPACE", 5: "RLK_ERR_CUDA",
-                6: "RLK_ERR_TARGET_RANGE", 7: "RLK_ERR_TIMEOUT"}
+                6: "RLK_ERR_TARGET_RANGE", 7: "RLK_ERR_TIMEOUT", 8: "RLK_ERR_NONFINITE"}
 RLK_ERR_INVALID_ARG = 1
 RLK_ERR_ALIGNMENT = 3
 RLK_ERR_TARGET_RANGE = 6
 RLK_ERR_TIMEOUT = 7
+RLK_ERR_NONFINITE = 8
 VOCAB_TILE = 128
 
 EXPORTED = ["rlk_contract_id", "rlk_build_fingerprint", "rlk_status_string", "rlk_shard_range",
@@ -33,7 +35,10 @@ EXPORTED = ["rlk_contract_id", "rlk_build_fingerprint", "rlk_status_string", "rl
             "rlk_linear_logprob_static_ws", "rlk_logits_logprob", "rlk_log_softmax",
             "rlk_backward_workspace_size", "rlk_linear_logprob_backward", "rlk_rmsnorm",
             "rlk_debug_primitive_hash", "rlk_linear_logprob_save_logits",
-            "rlk_linear_logprob_backward_from_logits"]
+            "rlk_linear_logprob_backward_from_logits", "rlk_rmsnorm_backward_workspace_size",
+            "rlk_rmsnorm_backward", "rlk_policy_loss_workspace_size", "rlk_policy_loss",
+            "rlk_preference_loss", "rlk_grad_norm_workspace_size", "rlk_grad_norm",
+            "rlk_grad_clip"]
 DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
@@ -96,6 +101,26 @@ def lib() -> ctypes.CDLL:
         L.rlk_log_softmax.argtypes = [P, i32, i64, P, i64, i64, P, P, P, sz, P, P]
         L.rlk_debug_primitive_hash.restype = i32
         L.rlk_debug_primitive_hash.argtypes = [i32, ctypes.c_uint32, ctypes.c_uint64, P, P]
+        dbl = ctypes.c_double
+        L.rlk_rmsnorm_backward_workspace_size.restype = sz
+        L.rlk_rmsnorm_backward_workspace_size.argtypes = [i64, i64]
+        L.rlk_rmsnorm_backward.restype = i32
+        L.rlk_rmsnorm_backward.argtypes = [P, i32, P, P, ctypes.c_float, P, i64, i64, P, i32, P, P,
+                                           sz, P]
+        L.rlk_policy_loss_workspace_size.restype = sz
+        L.rlk_policy_loss_workspace_size.argtypes = [i64, i64]
+        L.rlk_policy_loss.restype = i32
+        L.rlk_policy_loss.argtypes = [P, P, P, P, i32, P, P, i64, i64, dbl, dbl, dbl, i32, dbl,
+                                      i32, dbl, P, P, P, P, sz, P, P]
+        L.rlk_preference_loss.restype = i32
+        L.rlk_preference_loss.argtypes = [P, P, P, P, i64, i64, i32, i32, dbl, dbl, dbl, i32, dbl,
+                                          P, P, P, P, P, P]
+        L.rlk_grad_norm_workspace_size.restype = sz
+        L.rlk_grad_norm_workspace_size.argtypes = [P, i64]
+        L.rlk_grad_norm.restype = i32
+        L.rlk_grad_norm.argtypes = [P, P, P, i64, P, P, sz, P, P]
+        L.rlk_grad_clip.restype = i32
+        L.rlk_grad_clip.argtypes = [P, P, P, P, i64, dbl, P, P, P, sz, P, P]
         _lib = L
     return _lib
 
@@ -472,6 +497,253 @@ def rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6,
                                  _ptr(residual_out if want_residual_out else None),
                                  _stream(dev, stream)), "rlk_rmsnorm")
     return out, (residual_out if want_residual_out else None)
+
+
+# ----------------------------------------------------------------- training step
+KL_KINDS = {"k1": 1, "k2": 2, "k3": 3}
+REDUCTIONS = {"sum": 0, "token_mean": 1, "seq_mean": 2}
+PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "ipo": 2}
+PAIR_LAYOUTS = {"adjacent": 0, "halves": 1}
+GRAD_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _choice(table, key, name: str) -> int:
+    if key not in table:
+        raise ValueError("%s must be one of %s, got %r" % (name, sorted(table), key))
+    return table[key]
+
+
+def _alloc_on(device, stream):
+    """Allocate the call's buffers on the stream that will use them, so torch's allocator does
+    not hand them out again before that stream is done with them."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _workspace(given: Optional[torch.Tensor], n: int, device) -> torch.Tensor:
+    if given is None:
+        return torch.empty(max(256, n), dtype=torch.uint8, device=device)
+    _require(given, torch.uint8, "workspace", device)
+    return given
+
+
+def _status_word(status: Optional[torch.Tensor], device):
+    if status is not None:
+        _require(status, torch.int32, "status", device)
+    return _ptr(status)
+
+
+def rmsnorm_backward(grad_out: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor,
+                     eps: float = 1e-6, grad_residual: Optional[torch.Tensor] = None,
+                     want_gamma: bool = True, grad_dtype: Optional[torch.dtype] = None,
+                     grad_x: Optional[torch.Tensor] = None,
+                     grad_gamma: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """Backward of rmsnorm -> (grad_x [T, H], grad_gamma fp32 [H] or None).
+
+    x is the tensor that was normalised: rmsnorm's residual_out where it added a residual.
+    grad_out is fp32 (linear_logprob_backward's grad_hidden) or bf16; grad_x has grad_dtype
+    (fp32 or bf16; grad_out's type by default) and, with grad_residual of the same type added,
+    is the gradient of both x and the residual.  grad_x may be grad_residual itself."""
+    _require(x, torch.bfloat16, "x", ndim=2)
+    dev = x.device
+    _require(gamma, torch.bfloat16, "gamma", dev, ndim=1)
+    if grad_out.dtype not in DTYPES:
+        raise TypeError("grad_out must be float32 or bfloat16")
+    _require(grad_out, grad_out.dtype, "grad_out", dev, ndim=2)
+    if grad_dtype is None:
+        grad_dtype = grad_out.dtype if grad_x is None else grad_x.dtype
+    if grad_dtype not in DTYPES:
+        raise TypeError("grad_dtype must be float32 or bfloat16")
+    T, H = x.shape
+    if grad_out.shape != x.shape or gamma.shape[0] != H:
+        raise ValueError("shape mismatch")
+    if grad_residual is not None:
+        _require(grad_residual, grad_dtype, "grad_residual", dev, ndim=2)
+        if grad_residual.shape != x.shape:
+            raise ValueError("shape mismatch")
+    with _on(dev), _alloc_on(dev, stream):
+        if grad_x is None:
+            grad_x = torch.empty((T, H), dtype=grad_dtype, device=dev)
+        _require(grad_x, grad_dtype, "grad_x", dev, ndim=2)
+        if want_gamma:
+            if grad_gamma is None:
+                grad_gamma = torch.empty(H, dtype=torch.float32, device=dev)
+            _require(grad_gamma, torch.float32, "grad_gamma", dev, ndim=1)
+            workspace = _workspace(workspace, lib().rlk_rmsnorm_backward_workspace_size(T, H), dev)
+        if grad_x.shape != x.shape or (want_gamma and grad_gamma.shape[0] != H):
+            raise ValueError("shape mismatch")
+        _check(lib().rlk_rmsnorm_backward(
+            _ptr(grad_out), DTYPES[grad_out.dtype], _ptr(x), _ptr(gamma), float(eps),
+            _ptr(grad_residual), T, H, _ptr(grad_x), DTYPES[grad_dtype],
+            _ptr(grad_gamma if want_gamma else None), _ptr(workspace),
+            0 if workspace is None else workspace.numel(), _stream(dev, stream)),
+            "rlk_rmsnorm_backward")
+    return grad_x, (grad_gamma if want_gamma else None)
+
+
+def policy_loss_workspace_size(T: int, n_seqs: int = 1) -> int:
+    return int(lib().rlk_policy_loss_workspace_size(T, n_seqs))
+
+
+def policy_loss(logprob: torch.Tensor, old_logprob: torch.Tensor, advantages: torch.Tensor,
+                ref_logprob: Optional[torch.Tensor] = None,
+                active: Optional[torch.Tensor] = None,
+                seq_offsets: Optional[torch.Tensor] = None, advantages_per_seq: bool = False,
+                clip_low: float = 0.2, clip_high: float = 0.2, dual_clip: float = 0.0,
+                kl: str = "k3", kl_coef: float = 0.0, reduction: str = "token_mean",
+                scale: float = 1.0, want_grad: bool = True,
+                grad_logprob: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None,
+                status: Optional[torch.Tensor] = None, stream=None):
+    """Clipped policy loss with a KL term -> (loss [], stats [4], grad_logprob [T] or None).
+
+    fp32 logprob, old_logprob (and ref_logprob) [T]; advantages [T], or one per sequence with
+    advantages_per_seq; seq_offsets int32 [n_seqs + 1] on the device (None: one sequence of all
+    tokens).  stats holds the weighted sums of -surrogate, KL, clipped tokens and
+    old_logprob - logprob; grad_logprob goes straight into linear_logprob_backward."""
+    _require(logprob, torch.float32, "logprob", ndim=1)
+    dev, T = logprob.device, logprob.shape[0]
+    _require(old_logprob, torch.float32, "old_logprob", dev, ndim=1)
+    _require(advantages, torch.float32, "advantages", dev, ndim=1)
+    if ref_logprob is not None:
+        _require(ref_logprob, torch.float32, "ref_logprob", dev, ndim=1)
+    if active is not None:
+        _require(active, torch.uint8, "active", dev, ndim=1)
+    n_seqs = 1
+    if seq_offsets is not None:
+        _require(seq_offsets, torch.int32, "seq_offsets", dev, ndim=1)
+        n_seqs = seq_offsets.shape[0] - 1
+    if (old_logprob.shape[0] != T or (ref_logprob is not None and ref_logprob.shape[0] != T)
+            or (active is not None and active.shape[0] != T)
+            or advantages.shape[0] != (n_seqs if advantages_per_seq else T)):
+        raise ValueError("shape mismatch")
+    kl_kind, red = _choice(KL_KINDS, kl, "kl"), _choice(REDUCTIONS, reduction, "reduction")
+    with _on(dev), _alloc_on(dev, stream):
+        out = torch.empty(5, dtype=torch.float32, device=dev)
+        if want_grad:
+            if grad_logprob is None:
+                grad_logprob = torch.empty(T, dtype=torch.float32, device=dev)
+            _require(grad_logprob, torch.float32, "grad_logprob", dev, ndim=1)
+            if grad_logprob.shape[0] != T:
+                raise ValueError("shape mismatch")
+        workspace = _workspace(workspace, policy_loss_workspace_size(T, n_seqs), dev)
+        loss, stats = out[0], out[1:]
+        _check(lib().rlk_policy_loss(
+            _ptr(logprob), _ptr(old_logprob), _ptr(ref_logprob), _ptr(advantages),
+            int(advantages_per_seq), _ptr(active), _ptr(seq_offsets), n_seqs, T, clip_low,
+            clip_high, dual_clip, kl_kind, kl_coef, red, scale, _ptr(loss), _ptr(stats),
+            _ptr(grad_logprob if want_grad else None), _ptr(workspace), workspace.numel(),
+            _status_word(status, dev), _stream(dev, stream)), "rlk_policy_loss")
+    return loss, stats, (grad_logprob if want_grad else None)
+
+
+def preference_loss(logprob: torch.Tensor, seq_offsets: torch.Tensor,
+                    ref_logprob: Optional[torch.Tensor] = None,
+                    active: Optional[torch.Tensor] = None, beta: float = 0.1,
+                    kind: str = "sigmoid", label_smoothing: float = 0.0, margin: float = 0.0,
+                    length_normalize: bool = False, layout: str = "adjacent",
+                    scale: float = 1.0, want_grad: bool = True,
+                    grad_logprob: Optional[torch.Tensor] = None,
+                    status: Optional[torch.Tensor] = None, stream=None):
+    """Preference loss on paired log ratios -> (loss [], pair_loss [P], rewards [2 P],
+    grad_logprob [T] or None).
+
+    The batch holds 2 P packed sequences (seq_offsets int32 [2 P + 1] on the device); pair i is
+    sequences (2 i, 2 i + 1) with layout "adjacent" and (i, P + i) with "halves", the chosen one
+    first."""
+    _require(logprob, torch.float32, "logprob", ndim=1)
+    dev, T = logprob.device, logprob.shape[0]
+    _require(seq_offsets, torch.int32, "seq_offsets", dev, ndim=1)
+    n_seqs = seq_offsets.shape[0] - 1
+    if n_seqs < 0 or n_seqs % 2:
+        raise ValueError("seq_offsets must hold an even number of sequences")
+    if ref_logprob is not None:
+        _require(ref_logprob, torch.float32, "ref_logprob", dev, ndim=1)
+    if active is not None:
+        _require(active, torch.uint8, "active", dev, ndim=1)
+    if ((ref_logprob is not None and ref_logprob.shape[0] != T)
+            or (active is not None and active.shape[0] != T)):
+        raise ValueError("shape mismatch")
+    kind_code = _choice(PREFERENCE_KINDS, kind, "kind")
+    layout_code = _choice(PAIR_LAYOUTS, layout, "layout")
+    P = n_seqs // 2
+    with _on(dev), _alloc_on(dev, stream):
+        loss = torch.empty((), dtype=torch.float32, device=dev)
+        pair_loss = torch.empty(P, dtype=torch.float32, device=dev)
+        rewards = torch.empty(n_seqs, dtype=torch.float32, device=dev)
+        if want_grad:
+            if grad_logprob is None:
+                grad_logprob = torch.empty(T, dtype=torch.float32, device=dev)
+            _require(grad_logprob, torch.float32, "grad_logprob", dev, ndim=1)
+            if grad_logprob.shape[0] != T:
+                raise ValueError("shape mismatch")
+        _check(lib().rlk_preference_loss(
+            _ptr(logprob), _ptr(ref_logprob), _ptr(active), _ptr(seq_offsets), P, T, layout_code,
+            kind_code, beta, label_smoothing, margin, int(length_normalize), scale, _ptr(loss),
+            _ptr(pair_loss), _ptr(rewards), _ptr(grad_logprob if want_grad else None),
+            _status_word(status, dev), _stream(dev, stream)), "rlk_preference_loss")
+    return loss, pair_loss, rewards, (grad_logprob if want_grad else None)
+
+
+def _grad_arrays(grads, name: str):
+    """(device, host arrays of pointers, sizes and types) of a list of gradients."""
+    grads = list(grads)
+    n = len(grads)
+    if n == 0:
+        return None, None, None, None, 0
+    dev = grads[0].device
+    for g in grads:
+        if g.dtype not in GRAD_DTYPES:
+            raise TypeError("%s must be float32, bfloat16 or float16" % name)
+        _require(g, g.dtype, name, dev)
+    ptrs = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
+    sizes = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
+    types = (ctypes.c_int32 * n)(*[GRAD_DTYPES[g.dtype] for g in grads])
+    return dev, ptrs, sizes, types, n
+
+
+def grad_norm(grads: Sequence[torch.Tensor], workspace: Optional[torch.Tensor] = None,
+              status: Optional[torch.Tensor] = None, device=None, stream=None) -> torch.Tensor:
+    """sqrt of the sum of squares over all the tensors (fp32, bf16 or fp16, contiguous) as a
+    0-dim fp32 tensor.  `device` says where an empty list's norm goes."""
+    dev, ptrs, sizes, types, n = _grad_arrays(grads, "grads")
+    dev = torch.device(device if dev is None else dev)
+    with _on(dev), _alloc_on(dev, stream):
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+        workspace = _workspace(workspace, lib().rlk_grad_norm_workspace_size(sizes, n), dev)
+        _check(lib().rlk_grad_norm(ptrs, sizes, types, n, _ptr(norm), _ptr(workspace),
+                                   workspace.numel(), _status_word(status, dev), _stream(dev, stream)),
+               "rlk_grad_norm")
+    return norm
+
+
+def clip_grads(grads: Sequence[torch.Tensor], max_norm: float,
+               out: Optional[Sequence[torch.Tensor]] = None,
+               workspace: Optional[torch.Tensor] = None,
+               status: Optional[torch.Tensor] = None, device=None, stream=None):
+    """Scale the gradients by min(1, max_norm / norm), in place or into the tensors of `out`
+    (same sizes and types) -> (norm [], scale []).  With a norm that is not finite the values
+    stay as they are, scale is 1 and the status word gets RLK_ERR_NONFINITE."""
+    grads = list(grads)
+    dev, ptrs, sizes, types, n = _grad_arrays(grads, "grads")
+    dev = torch.device(device if dev is None else dev)
+    outs = ptrs
+    if out is not None:
+        out = list(out)
+        if len(out) != n or any(o.shape != g.shape or o.dtype != g.dtype
+                                for o, g in zip(out, grads)):
+            raise ValueError("out must hold one tensor of the same shape and type per gradient")
+        out_dev, outs, _, _, _ = _grad_arrays(out, "out")
+        if n and out_dev != dev:
+            raise ValueError("out is on %s, expected %s" % (out_dev, dev))
+    with _on(dev), _alloc_on(dev, stream):
+        res = torch.empty(2, dtype=torch.float32, device=dev)
+        norm, scale = res[0], res[1]
+        workspace = _workspace(workspace, lib().rlk_grad_norm_workspace_size(sizes, n), dev)
+        _check(lib().rlk_grad_clip(ptrs, outs, sizes, types, n, max_norm, _ptr(norm), _ptr(scale),
+                                   _ptr(workspace), workspace.numel(), _status_word(status, dev),
+                                   _stream(dev, stream)), "rlk_grad_clip")
+    return norm, scale
 
 
 PRIMITIVES = {"exp": 0, "exp_x2": 1, "log": 2, "rsqrt": 3}

@@ -25,8 +25,9 @@ LIB = os.path.join(HERE, "librlk.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 SOURCES = ["rlk_logits.cu", "rlk_logits_mat.cu", "rlk_merge.cu", "rlk_gemm.cu", "rlk_rmsnorm.cu",
-           "rlk_api.cu", "rlk_static_ws.cu", "rlk_debug.cu"]
-HEADERS = ["rlk_ptx.cuh", "rlk_contract.cuh", "rlk_internal.h"]
+           "rlk_api.cu", "rlk_static_ws.cu", "rlk_debug.cu", "rlk_policy.cu", "rlk_pref.cu",
+           "rlk_clip.cu", "rlk_rmsnorm_bwd.cu"]
+HEADERS = ["rlk_ptx.cuh", "rlk_contract.cuh", "rlk_internal.h", "rlk_train.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CONTRACT_FLAGS = ["-ftz=false", "-prec-div=true", "-prec-sqrt=true", "-fmad=false"]

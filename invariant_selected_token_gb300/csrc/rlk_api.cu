@@ -4,16 +4,22 @@
 // status code, nothing falls back to another path ("vLLM RL-Kernel v0.1.0",
 // strict path; the vime ablation-matrix issue, "strict: unsupported 时 fail
 // closed").
+#include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
+#include <limits>
 #include <mutex>
+#include <new>
+#include <vector>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
 #include "rlk_internal.h"
+#include "rlk_train.cuh"
 
 #ifndef RLK_GIT_REV
 #define RLK_GIT_REV "unknown"
@@ -433,6 +439,129 @@ rlk_status_t backward_gemms(const void* hidden, const void* W, int64_t T, int64_
     return RLK_OK;
 }
 
+// ---------------------------------------------------------------- training-step operators
+// A double as the sum of two floats (2^-48 relative).
+float2 split_two(double v) {
+    const float hi = float(v);
+    const float lo = std::isfinite(hi) ? float(v - double(hi)) : 0.0f;
+    return make_float2(hi, lo);
+}
+
+struct PolicyLayout {
+    size_t counts, parts, total;
+};
+
+PolicyLayout policy_layout_of(int64_t T, int64_t n_seqs) {
+    PolicyLayout l;
+    const int64_t rows = n_seqs > rlk::kPolicyCountBlocks ? n_seqs : rlk::kPolicyCountBlocks;
+    const int64_t units = (T + rlk::kPolicyUnit - 1) / rlk::kPolicyUnit;
+    l.counts = 0;
+    l.parts = align256(size_t(rows) * sizeof(int32_t));
+    l.total = l.parts + align256(size_t(units) * sizeof(float4));
+    return l;
+}
+
+int64_t clip_chunks(int64_t n) { return (n + rlk::kClipChunk - 1) / rlk::kClipChunk; }
+
+size_t clip_element_size(int dtype) { return dtype == RLK_DTYPE_F32 ? 4 : 2; }
+
+rlk_status_t clip_checks(const void* const* grads, const int64_t* numels, const int32_t* dtypes,
+                         int64_t n, const void* workspace, size_t workspace_bytes) {
+    if (n < 0 || n > (int64_t(1) << 24)) return RLK_ERR_INVALID_ARG;
+    if (n > 0 && (!grads || !numels || !dtypes)) return RLK_ERR_INVALID_ARG;
+    int64_t chunks = 0;
+    for (int64_t i = 0; i < n; ++i) {
+        if (numels[i] < 0) return RLK_ERR_INVALID_ARG;
+        if (numels[i] > (int64_t(1) << 40)) return RLK_ERR_UNSUPPORTED;
+        if (dtypes[i] != RLK_DTYPE_F32 && dtypes[i] != RLK_DTYPE_BF16 && dtypes[i] != RLK_DTYPE_F16)
+            return RLK_ERR_UNSUPPORTED;
+        if (numels[i] == 0) continue;
+        if (!grads[i]) return RLK_ERR_INVALID_ARG;
+        if (!aligned(grads[i], clip_element_size(dtypes[i]))) return RLK_ERR_ALIGNMENT;
+        chunks += clip_chunks(numels[i]);
+    }
+    if (chunks > 0 && !workspace) return RLK_ERR_INVALID_ARG;
+    if (!aligned(workspace, 256)) return RLK_ERR_ALIGNMENT;
+    if (workspace_bytes < align256(size_t(chunks) * sizeof(float))) return RLK_ERR_WORKSPACE;
+    return RLK_OK;
+}
+
+// Whether outputs overlap each other, or an input that is not the same tensor in place.
+rlk_status_t clip_overlap_check(const void* const* grads, void* const* outs, const int64_t* numels,
+                                const int32_t* dtypes, int64_t n) {
+    struct Range {
+        uintptr_t b, e;
+        bool operator<(const Range& o) const { return b < o.b; }
+    };
+    std::vector<Range> held;
+    try {
+        held.reserve(size_t(n));
+    } catch (const std::bad_alloc&) {
+        return RLK_ERR_INVALID_ARG;
+    }
+    auto bytes = [&](int64_t i) { return uintptr_t(numels[i]) * clip_element_size(dtypes[i]); };
+    for (int64_t i = 0; i < n; ++i) {
+        if (numels[i] == 0) continue;
+        const uintptr_t b = reinterpret_cast<uintptr_t>(outs[i]);
+        held.push_back({b, b + bytes(i)});
+    }
+    if (!std::is_sorted(held.begin(), held.end())) std::sort(held.begin(), held.end());
+    for (size_t i = 1; i < held.size(); ++i)
+        if (held[i].b < held[i - 1].e) return RLK_ERR_INVALID_ARG;
+    for (int64_t i = 0; i < n; ++i) {
+        if (numels[i] == 0 || grads[i] == outs[i]) continue;
+        const uintptr_t b = reinterpret_cast<uintptr_t>(grads[i]), e = b + bytes(i);
+        // the first output that ends behind b
+        auto it = std::upper_bound(held.begin(), held.end(), Range{b, b});
+        if (it != held.begin() && (it - 1)->e > b) return RLK_ERR_INVALID_ARG;
+        if (it != held.end() && it->b < e) return RLK_ERR_INVALID_ARG;
+    }
+    return RLK_OK;
+}
+
+// Calls fn(table, first chunk of the table) for every table of the tensors; stops at an error.
+template <typename Fn>
+cudaError_t for_each_clip_table(const void* const* grads, void* const* outs, const int64_t* numels,
+                                const int32_t* dtypes, int64_t n, Fn fn) {
+    rlk::ClipTable t;
+    int64_t base = 0;
+    t.count = 0;
+    t.first[0] = 0;
+    for (int64_t i = 0; i < n; ++i) {
+        if (numels[i] == 0) continue;
+        const int64_t c = clip_chunks(numels[i]);
+        if (t.count == rlk::kClipTable || t.first[t.count] + c > (int64_t(1) << 30)) {
+            const cudaError_t e = fn(t, base);
+            if (e != cudaSuccess) return e;
+            base += t.first[t.count];
+            t.count = 0;
+        }
+        t.e[t.count].in = grads[i];
+        t.e[t.count].out = outs ? outs[i] : nullptr;
+        t.e[t.count].n = numels[i];
+        t.dtype[t.count] = uint8_t(dtypes[i]);
+        t.first[t.count + 1] = t.first[t.count] + int32_t(c);
+        ++t.count;
+    }
+    return t.count ? fn(t, base) : cudaSuccess;
+}
+
+rlk_status_t run_grad_norm(const void* const* grads, const int64_t* numels, const int32_t* dtypes,
+                           int64_t n, double max_norm, float* out_norm, float* out_scale,
+                           float* partials, int32_t* dev_status, cudaStream_t stream) {
+    int64_t chunks = 0;
+    for (int64_t i = 0; i < n; ++i) chunks += clip_chunks(numels[i]);
+    if (for_each_clip_table(grads, nullptr, numels, dtypes, n,
+                            [&](const rlk::ClipTable& t, int64_t base) {
+                                return rlk::launch_grad_sumsq(t, partials + base, stream);
+                            }) != cudaSuccess)
+        return RLK_ERR_CUDA;
+    return rlk::launch_grad_norm_final(partials, chunks, max_norm, out_norm, out_scale, dev_status,
+                                       stream) == cudaSuccess
+               ? RLK_OK
+               : RLK_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -454,6 +583,7 @@ const char* rlk_status_string(int status) {
         case RLK_ERR_CUDA: return "RLK_ERR_CUDA";
         case RLK_ERR_TARGET_RANGE: return "RLK_ERR_TARGET_RANGE";
         case RLK_ERR_TIMEOUT: return "RLK_ERR_TIMEOUT";
+        case RLK_ERR_NONFINITE: return "RLK_ERR_NONFINITE";
         default: return "RLK_ERR_UNKNOWN";
     }
 }
@@ -815,6 +945,230 @@ rlk_status_t rlk_rmsnorm(const void* x, const void* residual, const void* gamma,
     a.res_out = static_cast<uint16_t*>(residual_out);
     return rlk::launch_rmsnorm(a, dev->sm_count, reinterpret_cast<cudaStream_t>(stream)) ==
                    cudaSuccess
+               ? RLK_OK
+               : RLK_ERR_CUDA;
+}
+
+size_t rlk_rmsnorm_backward_workspace_size(int64_t T, int64_t H) {
+    if (T < 0 || T > RLK_MAX_ROWS || H < 64 || H % 64 != 0 || H > 8192) return 0;
+    const int64_t ranges = T < rlk::kRmsBwdBlocks ? T : rlk::kRmsBwdBlocks;
+    return align256(size_t(ranges) * size_t(H) * sizeof(float));
+}
+
+rlk_status_t rlk_rmsnorm_backward(const void* grad_out, int grad_out_dtype, const void* x,
+                                  const void* gamma, float eps, const void* grad_residual,
+                                  int64_t T, int64_t H, void* grad_x, int grad_x_dtype,
+                                  float* grad_gamma, void* workspace, size_t workspace_bytes,
+                                  rlk_stream_t stream) {
+    if (T < 0 || T > RLK_MAX_ROWS) return RLK_ERR_INVALID_ARG;
+    if (H < 64 || H % 64 != 0 || H > 8192) return RLK_ERR_UNSUPPORTED;
+    if ((grad_out_dtype != RLK_DTYPE_F32 && grad_out_dtype != RLK_DTYPE_BF16) ||
+        (grad_x_dtype != RLK_DTYPE_F32 && grad_x_dtype != RLK_DTYPE_BF16))
+        return RLK_ERR_UNSUPPORTED;
+    if (!(eps > 0.0f) || !(eps < 3.0e38f)) return RLK_ERR_INVALID_ARG;
+    if (T > 0 && (!grad_out || !x || !gamma || !grad_x)) return RLK_ERR_INVALID_ARG;
+    if (T > 0 && grad_gamma && !workspace) return RLK_ERR_INVALID_ARG;
+    if (grad_x == grad_out && grad_x && grad_x_dtype != grad_out_dtype) return RLK_ERR_INVALID_ARG;
+    if (!aligned(grad_out, 16) || !aligned(x, 16) || !aligned(gamma, 16) ||
+        !aligned(grad_residual, 16) || !aligned(grad_x, 16) || !aligned(grad_gamma, 16) ||
+        !aligned(workspace, 256))
+        return RLK_ERR_ALIGNMENT;
+    if (grad_gamma && workspace_bytes < rlk_rmsnorm_backward_workspace_size(T, H))
+        return RLK_ERR_WORKSPACE;
+    if (T == 0 && !grad_gamma) return RLK_OK;
+    DeviceState* dev = nullptr;
+    rlk_status_t s = device_check(&dev);
+    if (s != RLK_OK) return s;
+    rlk::RmsBwdArgs a;
+    a.grad_out = grad_out;
+    a.x = static_cast<const uint16_t*>(x);
+    a.gamma = static_cast<const uint16_t*>(gamma);
+    a.grad_res = grad_residual;
+    a.grad_x = grad_x;
+    a.grad_gamma = grad_gamma;
+    a.parts = static_cast<float*>(workspace);
+    a.eps = eps;
+    a.T = int(T);
+    a.H = int(H);
+    a.go_dtype = grad_out_dtype;
+    a.gx_dtype = grad_x_dtype;
+    return rlk::launch_rmsnorm_backward(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? RLK_OK
+               : RLK_ERR_CUDA;
+}
+
+size_t rlk_policy_loss_workspace_size(int64_t T, int64_t n_seqs) {
+    if (T < 0 || T > RLK_MAX_ROWS || n_seqs < 0 || n_seqs > RLK_MAX_ROWS) return 0;
+    return policy_layout_of(T, n_seqs).total;
+}
+
+rlk_status_t rlk_policy_loss(const float* logprob, const float* old_logprob,
+                             const float* ref_logprob, const float* advantages,
+                             int advantages_per_seq, const uint8_t* active_mask,
+                             const int32_t* seq_offsets, int64_t n_seqs, int64_t T,
+                             double clip_low, double clip_high, double dual_clip, int kl_kind,
+                             double kl_coef, int reduction, double scale, float* out_loss,
+                             float* out_stats, float* grad_logprob, void* workspace,
+                             size_t workspace_bytes, int32_t* dev_status, rlk_stream_t stream) {
+    if (T < 0 || T > RLK_MAX_ROWS || n_seqs < 0 || n_seqs > RLK_MAX_ROWS)
+        return RLK_ERR_INVALID_ARG;
+    if (!seq_offsets && n_seqs != 1) return RLK_ERR_INVALID_ARG;
+    if (T > 0 && (!logprob || !old_logprob)) return RLK_ERR_INVALID_ARG;
+    if (!advantages && (advantages_per_seq ? n_seqs : T) > 0) return RLK_ERR_INVALID_ARG;
+    if (!out_loss || !out_stats || !workspace) return RLK_ERR_INVALID_ARG;
+    if (!(clip_low >= 0.0) || !(clip_high >= 0.0) || !std::isfinite(clip_low) ||
+        !std::isfinite(clip_high) || !std::isfinite(kl_coef) || !std::isfinite(scale))
+        return RLK_ERR_INVALID_ARG;
+    if (dual_clip != 0.0 && (!(dual_clip > 1.0) || !std::isfinite(dual_clip)))
+        return RLK_ERR_INVALID_ARG;
+    if (!ref_logprob && kl_coef != 0.0 && T > 0) return RLK_ERR_INVALID_ARG;
+    if (kl_kind < RLK_KL_K1 || kl_kind > RLK_KL_K3) return RLK_ERR_UNSUPPORTED;
+    if (reduction < RLK_REDUCE_SUM || reduction > RLK_REDUCE_SEQ_MEAN) return RLK_ERR_UNSUPPORTED;
+    if (!aligned(logprob, 4) || !aligned(old_logprob, 4) || !aligned(ref_logprob, 4) ||
+        !aligned(advantages, 4) || !aligned(seq_offsets, 4) || !aligned(out_loss, 4) ||
+        !aligned(out_stats, 4) || !aligned(grad_logprob, 4) || !aligned(workspace, 256))
+        return RLK_ERR_ALIGNMENT;
+    const PolicyLayout l = policy_layout_of(T, n_seqs);
+    if (workspace_bytes < l.total) return RLK_ERR_WORKSPACE;
+    DeviceState* dev = nullptr;
+    rlk_status_t s = device_check(&dev);
+    if (s != RLK_OK) return s;
+    rlk::PolicyArgs a;
+    a.logprob = logprob;
+    a.old_logprob = old_logprob;
+    a.ref_logprob = ref_logprob;
+    a.advantages = advantages;
+    a.active = active_mask;
+    a.offsets = seq_offsets;
+    a.T = int(T);
+    a.n_seqs = int(n_seqs);
+    a.adv_per_seq = advantages_per_seq != 0;
+    a.kl_kind = kl_kind;
+    a.reduction = reduction;
+    const double none = -std::numeric_limits<double>::infinity();
+    a.log_high = split_two(std::log1p(clip_high));
+    a.log_low = split_two(clip_low < 1.0 ? std::log1p(-clip_low) : none);
+    a.log_dual = split_two(dual_clip > 0.0 ? std::log(dual_clip) : none);
+    a.ratio_high = float(1.0 + clip_high);
+    a.ratio_low = float(1.0 - clip_low);
+    a.dual = float(dual_clip);
+    a.kl_coef = float(kl_coef);
+    a.scale = scale;
+    a.kl_coef64 = kl_coef;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.counts = reinterpret_cast<int32_t*>(ws + l.counts);
+    a.parts = reinterpret_cast<float4*>(ws + l.parts);
+    a.out_loss = out_loss;
+    a.out_stats = out_stats;
+    a.grad = grad_logprob;
+    a.status = dev_status;
+    return rlk::launch_policy_loss(a, dev->sm_count, reinterpret_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? RLK_OK
+               : RLK_ERR_CUDA;
+}
+
+rlk_status_t rlk_preference_loss(const float* logprob, const float* ref_logprob,
+                                 const uint8_t* active_mask, const int32_t* seq_offsets,
+                                 int64_t n_pairs, int64_t T, int layout, int kind, double beta,
+                                 double label_smoothing, double margin, int length_normalize,
+                                 double scale, float* out_loss, float* out_pair_loss,
+                                 float* out_rewards, float* grad_logprob, int32_t* dev_status,
+                                 rlk_stream_t stream) {
+    if (T < 0 || T > RLK_MAX_ROWS || n_pairs < 0 || n_pairs > (int64_t(1) << 30))
+        return RLK_ERR_INVALID_ARG;
+    if (layout != RLK_PAIRS_ADJACENT && layout != RLK_PAIRS_HALVES) return RLK_ERR_UNSUPPORTED;
+    if (kind < RLK_PREF_SIGMOID || kind > RLK_PREF_IPO) return RLK_ERR_UNSUPPORTED;
+    if (!seq_offsets || !out_loss || (T > 0 && !logprob)) return RLK_ERR_INVALID_ARG;
+    if (n_pairs > 0 && (!out_pair_loss || !out_rewards)) return RLK_ERR_INVALID_ARG;
+    if (!(beta > 0.0) || !std::isfinite(beta) || !std::isfinite(margin) || !std::isfinite(scale))
+        return RLK_ERR_INVALID_ARG;
+    if (!(label_smoothing >= 0.0 && label_smoothing <= 1.0)) return RLK_ERR_INVALID_ARG;
+    if ((kind != RLK_PREF_SIGMOID && label_smoothing != 0.0) ||
+        (kind == RLK_PREF_IPO && margin != 0.0))
+        return RLK_ERR_INVALID_ARG;
+    if (!aligned(logprob, 4) || !aligned(ref_logprob, 4) || !aligned(seq_offsets, 4) ||
+        !aligned(out_loss, 4) || !aligned(out_pair_loss, 4) || !aligned(out_rewards, 4) ||
+        !aligned(grad_logprob, 4))
+        return RLK_ERR_ALIGNMENT;
+    DeviceState* dev = nullptr;
+    rlk_status_t s = device_check(&dev);
+    if (s != RLK_OK) return s;
+    rlk::PreferenceArgs a;
+    a.logprob = logprob;
+    a.ref_logprob = ref_logprob;
+    a.active = active_mask;
+    a.offsets = seq_offsets;
+    a.T = int(T);
+    a.n_pairs = int(n_pairs);
+    a.halves = layout == RLK_PAIRS_HALVES;
+    a.kind = kind;
+    a.length_normalize = length_normalize != 0;
+    a.beta = beta;
+    a.label_smoothing = label_smoothing;
+    a.margin = margin;
+    a.scale = scale;
+    a.out_loss = out_loss;
+    a.out_pair_loss = out_pair_loss;
+    a.out_rewards = out_rewards;
+    a.grad = grad_logprob;
+    a.status = dev_status;
+    return rlk::launch_preference_loss(a, dev->sm_count, reinterpret_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? RLK_OK
+               : RLK_ERR_CUDA;
+}
+
+size_t rlk_grad_norm_workspace_size(const int64_t* numels, int64_t n_tensors) {
+    if (n_tensors < 0 || (n_tensors > 0 && !numels)) return 0;
+    int64_t chunks = 0;
+    for (int64_t i = 0; i < n_tensors; ++i) {
+        if (numels[i] < 0 || numels[i] > (int64_t(1) << 40)) return 0;
+        chunks += clip_chunks(numels[i]);
+    }
+    return align256(size_t(chunks) * sizeof(float));
+}
+
+rlk_status_t rlk_grad_norm(const void* const* grads, const int64_t* numels,
+                           const int32_t* dtypes, int64_t n_tensors, float* out_norm,
+                           void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                           rlk_stream_t stream) {
+    if (!out_norm) return RLK_ERR_INVALID_ARG;
+    rlk_status_t s = clip_checks(grads, numels, dtypes, n_tensors, workspace, workspace_bytes);
+    if (s != RLK_OK) return s;
+    if (!aligned(out_norm, 4)) return RLK_ERR_ALIGNMENT;
+    DeviceState* dev = nullptr;
+    if ((s = device_check(&dev)) != RLK_OK) return s;
+    return run_grad_norm(grads, numels, dtypes, n_tensors, 0.0, out_norm, nullptr,
+                         static_cast<float*>(workspace), dev_status,
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+rlk_status_t rlk_grad_clip(const void* const* grads, void* const* outs, const int64_t* numels,
+                           const int32_t* dtypes, int64_t n_tensors, double max_norm,
+                           float* out_norm, float* out_scale, void* workspace,
+                           size_t workspace_bytes, int32_t* dev_status, rlk_stream_t stream) {
+    if (!out_norm || !out_scale || (n_tensors > 0 && !outs) || !(max_norm >= 0.0))
+        return RLK_ERR_INVALID_ARG;
+    rlk_status_t s = clip_checks(grads, numels, dtypes, n_tensors, workspace, workspace_bytes);
+    if (s != RLK_OK) return s;
+    if (!aligned(out_norm, 4) || !aligned(out_scale, 4)) return RLK_ERR_ALIGNMENT;
+    for (int64_t i = 0; i < n_tensors; ++i) {
+        if (numels[i] == 0) continue;
+        if (!outs[i]) return RLK_ERR_INVALID_ARG;
+        if (!aligned(outs[i], clip_element_size(dtypes[i]))) return RLK_ERR_ALIGNMENT;
+    }
+    if ((s = clip_overlap_check(grads, outs, numels, dtypes, n_tensors)) != RLK_OK) return s;
+    DeviceState* dev = nullptr;
+    if ((s = device_check(&dev)) != RLK_OK) return s;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if ((s = run_grad_norm(grads, numels, dtypes, n_tensors, max_norm, out_norm, out_scale,
+                           static_cast<float*>(workspace), dev_status, st)) != RLK_OK)
+        return s;
+    return for_each_clip_table(grads, outs, numels, dtypes, n_tensors,
+                               [&](const rlk::ClipTable& t, int64_t) {
+                                   return rlk::launch_grad_scale(t, out_scale, st);
+                               }) == cudaSuccess
                ? RLK_OK
                : RLK_ERR_CUDA;
 }

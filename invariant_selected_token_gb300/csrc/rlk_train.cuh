@@ -1,0 +1,221 @@
+// Shared by the training-step operators (policy loss, preference loss,
+// gradient clipping, RMSNorm backward): the launch interface between the host
+// dispatcher and their kernels, and the device arithmetic they have in common.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include "../../include/rlk.h"
+
+namespace rlk {
+
+// ---------------------------------------------------------------- launches
+struct PolicyArgs {
+    const float* logprob;     // [T]
+    const float* old_logprob; // [T]
+    const float* ref_logprob; // [T] or nullptr
+    const float* advantages;  // [T], or [n_seqs] when adv_per_seq
+    const uint8_t* active;    // [T] or nullptr
+    const int32_t* offsets;   // [n_seqs + 1] or nullptr (one sequence [0, T))
+    int T, n_seqs;
+    int adv_per_seq;
+    int kl_kind, reduction;
+    // log(1 + clip_high), log(1 - clip_low), log(dual_clip), each as a sum of two floats
+    float2 log_high, log_low, log_dual;
+    float ratio_high, ratio_low, dual;  // 1 + clip_high, 1 - clip_low, dual_clip (0 = off)
+    float kl_coef;
+    double scale, kl_coef64;
+    int32_t* counts;          // workspace: active tokens per sequence or per block
+    float4* parts;            // workspace: one (policy, kl, clipped, -d) sum per unit
+    float* out_loss;          // [1]
+    float* out_stats;         // [4]
+    float* grad;              // [T] or nullptr
+    int32_t* status;
+};
+
+constexpr int kPolicyUnit = 1024;         // tokens per partial sum
+constexpr int kPolicyCountBlocks = 256;   // blocks counting a token mean's active tokens
+cudaError_t launch_policy_loss(const PolicyArgs& a, int num_sms, cudaStream_t stream);
+
+struct PreferenceArgs {
+    const float* logprob;     // [T]
+    const float* ref_logprob; // [T] or nullptr
+    const uint8_t* active;    // [T] or nullptr
+    const int32_t* offsets;   // [2 * n_pairs + 1]
+    int T, n_pairs;
+    int halves;               // pair i = sequences (i, n_pairs + i), else (2i, 2i + 1)
+    int kind, length_normalize;
+    double beta, label_smoothing, margin, scale;
+    float* out_loss;          // [1]
+    float* out_pair_loss;     // [n_pairs]
+    float* out_rewards;       // [2 * n_pairs], sequence order
+    float* grad;              // [T] or nullptr
+    int32_t* status;
+};
+cudaError_t launch_preference_loss(const PreferenceArgs& a, int num_sms, cudaStream_t stream);
+
+// Tensors of one launch: pointers and sizes travel by value in the kernel's parameters, so a
+// captured launch holds them and nothing has to be copied to the device first.
+constexpr int kClipTable = 640;
+struct ClipEntry {
+    const void* in;
+    void* out;
+    int64_t n;
+};
+struct ClipTable {
+    ClipEntry e[kClipTable];
+    int32_t first[kClipTable + 1];  // each tensor's first chunk within this launch
+    uint8_t dtype[kClipTable];
+    int count;
+};
+constexpr int kClipChunk = 16384;   // elements per partial sum
+cudaError_t launch_grad_sumsq(const ClipTable& t, float* partials, cudaStream_t stream);
+// norm, scale = the two outputs (either may be nullptr)
+cudaError_t launch_grad_norm_final(const float* partials, int64_t n, double max_norm,
+                                   float* out_norm, float* out_scale, int32_t* status,
+                                   cudaStream_t stream);
+cudaError_t launch_grad_scale(const ClipTable& t, const float* scale, cudaStream_t stream);
+
+struct RmsBwdArgs {
+    const void* grad_out;     // [T][H] fp32 or bf16
+    const uint16_t* x;        // bf16 [T][H], the normalised rows' inputs
+    const uint16_t* gamma;    // bf16 [H]
+    const void* grad_res;     // [T][H] of grad_x's type, or nullptr
+    void* grad_x;             // [T][H] fp32 or bf16
+    float* grad_gamma;        // [H] or nullptr
+    float* parts;             // workspace [blocks][H]
+    float eps;
+    int T, H;
+    int go_dtype, gx_dtype;   // RLK_DTYPE_*
+};
+constexpr int kRmsBwdBlocks = 304;  // row ranges whose grad_gamma sums are formed apart
+cudaError_t launch_rmsnorm_backward(const RmsBwdArgs& a, cudaStream_t stream);
+
+// ---------------------------------------------------------------- device arithmetic
+// a - b as the unevaluated sum of its rounded value and the rounding error, exactly
+// (Moller-Knuth two-sum); the error is 0 where the difference is not finite.
+__device__ __forceinline__ float2 two_diff(float a, float b) {
+    const float s = __fsub_rn(a, b);
+    const float t = __fsub_rn(s, a);
+    const float e = __fsub_rn(__fsub_rn(a, __fsub_rn(s, t)), __fadd_rn(b, t));
+    return make_float2(s, fabsf(s) < CUDART_INF_F ? e : 0.0f);
+}
+
+// (hi, lo) += x with the rounding error kept in lo.
+__device__ __forceinline__ void two_add(float2& acc, float x) {
+    const float s = __fadd_rn(acc.x, x);
+    const float t = __fsub_rn(s, acc.x);
+    const float e = __fadd_rn(__fsub_rn(acc.x, __fsub_rn(s, t)), __fsub_rn(x, t));
+    acc.x = s;
+    acc.y = __fadd_rn(acc.y, fabsf(s) < CUDART_INF_F ? e : 0.0f);
+}
+
+__device__ __forceinline__ bool above(float2 d, float2 border) {
+    return d.x > border.x || (d.x == border.x && d.y > border.y);
+}
+__device__ __forceinline__ bool below(float2 d, float2 border) {
+    return d.x < border.x || (d.x == border.x && d.y < border.y);
+}
+
+// exp over the whole fp32 range, NaN kept: the contract's reduction and polynomial (Cody-Waite,
+// degree-7 Taylor), scaled by 2^n in two factors so that n = 128 and subnormal results are
+// formed too; beyond the range the result is +inf or +0.
+__device__ __forceinline__ float exp_any(float x) {
+    const float xc = fminf(fmaxf(x, -104.0f), 89.0f);
+    const float t = __fmaf_rn(xc, 0x1.715476p+0f, 0x1.8p+23f);
+    const float n = __fsub_rn(t, 0x1.8p+23f);
+    const int ni = __float_as_int(t) - __float_as_int(0x1.8p+23f);
+    float r = __fmaf_rn(-n, 0x1.62e430p-1f, xc);
+    r = __fmaf_rn(-n, -0x1.05c610p-29f, r);
+    float p = 0x1.a01a02p-13f;
+    p = __fmaf_rn(p, r, 0x1.6c16c2p-10f);
+    p = __fmaf_rn(p, r, 0x1.111112p-7f);
+    p = __fmaf_rn(p, r, 0x1.555556p-5f);
+    p = __fmaf_rn(p, r, 0x1.555556p-3f);
+    p = __fmaf_rn(p, r, 0.5f);
+    p = __fmaf_rn(p, r, 1.0f);
+    p = __fmaf_rn(p, r, 1.0f);
+    const int half = ni >> 1;
+    p = __fmul_rn(p, __int_as_float((half + 127) << 23));
+    p = __fmul_rn(p, __int_as_float((ni - half + 127) << 23));
+    return x != x ? x : p;
+}
+
+// e^u - 1 - u.  Near 0 the difference cancels, so there it is its Taylor series
+// u^2 (1/2 + u/6 + ... + u^7/9!): the first term left out is below 2^-28 of the sum.
+__device__ __forceinline__ float exp_minus_1_minus(float u) {
+    float p = 0x1.71de3ap-19f;             // 1/9!
+    p = __fmaf_rn(p, u, 0x1.a01a02p-16f);  // 1/8!
+    p = __fmaf_rn(p, u, 0x1.a01a02p-13f);  // 1/7!
+    p = __fmaf_rn(p, u, 0x1.6c16c2p-10f);  // 1/6!
+    p = __fmaf_rn(p, u, 0x1.111112p-7f);   // 1/5!
+    p = __fmaf_rn(p, u, 0x1.555556p-5f);   // 1/4!
+    p = __fmaf_rn(p, u, 0x1.555556p-3f);   // 1/3!
+    p = __fmaf_rn(p, u, 0.5f);             // 1/2!
+    const float near = __fmul_rn(__fmul_rn(u, u), p);
+    const float far = __fsub_rn(__fsub_rn(exp_any(u), 1.0f), u);
+    return fabsf(u) < 0.5f ? near : far;
+}
+
+// log(1 + e) for e in [0, 1]: 2 atanh(v), v = e / (2 + e) <= 1/3, by the odd series through
+// v^17 (the next term is below 2^-32 of the sum).
+__device__ __forceinline__ float log_1_plus(float e) {
+    const float v = __fdiv_rn(e, __fadd_rn(2.0f, e));
+    const float q = __fmul_rn(v, v);
+    float p = 0x1.e1e1e2p-4f;              // 2/17
+    p = __fmaf_rn(p, q, 0x1.111112p-3f);   // 2/15
+    p = __fmaf_rn(p, q, 0x1.3b13b2p-3f);   // 2/13
+    p = __fmaf_rn(p, q, 0x1.745d18p-3f);   // 2/11
+    p = __fmaf_rn(p, q, 0x1.c71c72p-3f);   // 2/9
+    p = __fmaf_rn(p, q, 0x1.24924ap-2f);   // 2/7
+    p = __fmaf_rn(p, q, 0x1.99999ap-2f);   // 2/5
+    p = __fmaf_rn(p, q, 0x1.555556p-1f);   // 2/3
+    return __fmaf_rn(__fmul_rn(p, q), v, __fmul_rn(2.0f, v));
+}
+
+__device__ __forceinline__ void report_status(int32_t* status, int code) {
+    if (status) atomicOr(status, 1 << code);
+}
+
+// The last s in [0, n) with offsets[s] <= t (0 where there is none), found by a whole warp in
+// ceil(log32 n) dependent loads; every lane gets it.  With offsets that do not ascend the result
+// is still in [0, n).
+__device__ __forceinline__ int warp_find_seq(const int32_t* offsets, int n, int t) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32;
+        const int64_t p = lo + static_cast<int64_t>(lane) * step;
+        const bool left = p < hi && (lane == 0 || offsets[p] <= t);
+        const int k = 31 - __clz(__ballot_sync(0xffffffffu, left) | 1u);
+        lo += k * step;
+        hi = hi - lo < step ? hi : lo + step;
+    }
+    return lo;
+}
+
+// The same within [lo, hi], one thread alone.
+__device__ __forceinline__ int find_seq(const int32_t* offsets, int lo, int hi, int t) {
+    while (lo < hi) {
+        const int mid = lo + (hi - lo + 1) / 2;
+        if (offsets[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v = __dadd_rn(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+}  // namespace rlk
