@@ -9,7 +9,6 @@ to.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import List, Optional, Sequence, Tuple
@@ -500,36 +499,66 @@ def rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6,
 
 
 # ----------------------------------------------------------------- training step
+# Small batches of these calls take a few microseconds on the device, so their marshalling is
+# kept short: one check per tensor that passes its address on as a plain integer, and no device
+# or stream context where the tensors' device is current and the stream is its current one.
 KL_KINDS = {"k1": 1, "k2": 2, "k3": 3}
 REDUCTIONS = {"sum": 0, "token_mean": 1, "seq_mean": 2}
 PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "ipo": 2}
 PAIR_LAYOUTS = {"adjacent": 0, "halves": 1}
 GRAD_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _choice(table, key, name: str) -> int:
-    if key not in table:
+    code = table.get(key)
+    if code is None:
         raise ValueError("%s must be one of %s, got %r" % (name, sorted(table), key))
-    return table[key]
+    return code
 
 
-def _alloc_on(device, stream):
-    """Allocate the call's buffers on the stream that will use them, so torch's allocator does
-    not hand them out again before that stream is done with them."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _addr(t: torch.Tensor, dtype, name: str, index: int, shape) -> int:
+    """Device address of a contiguous tensor of this type, device and shape; raises otherwise."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
+            and t.shape == shape and t.is_contiguous()):
+        return t.data_ptr()
+    _require(t, dtype, name, torch.device("cuda", index), len(shape))
+    raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
-def _workspace(given: Optional[torch.Tensor], n: int, device) -> torch.Tensor:
-    if given is None:
-        return torch.empty(max(256, n), dtype=torch.uint8, device=device)
-    _require(given, torch.uint8, "workspace", device)
-    return given
+def _opt_addr(t: Optional[torch.Tensor], dtype, name: str, index: int, shape):
+    return None if t is None else _addr(t, dtype, name, index, shape)
 
 
-def _status_word(status: Optional[torch.Tensor], device):
-    if status is not None:
-        _require(status, torch.int32, "status", device)
-    return _ptr(status)
+def _status_addr(status: Optional[torch.Tensor], index: int):
+    if status is None:
+        return None
+    _require(status, torch.int32, "status", torch.device("cuda", index))
+    return status.data_ptr()
+
+
+def _call_on(device, stream, call):
+    """call(raw stream), on the device and with `stream` current: what the call allocates then
+    belongs to the stream that uses it, and torch does not hand it out again too early."""
+    if stream is None and _raw_stream is not None and _current_device() == device.index:
+        return call(_raw_stream(device.index))
+    with _on(device):
+        if stream is None:
+            return call(torch.cuda.current_stream(device).cuda_stream)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+
+
+def _workspace(given: Optional[torch.Tensor], n: int, device):
+    """(address, bytes, tensor) of the caller's workspace or of a new one."""
+    if given is not None:
+        _require(given, torch.uint8, "workspace", device)
+        return given.data_ptr(), given.numel(), given
+    if n == 0:
+        return None, 0, None
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    return ws.data_ptr(), n, ws
 
 
 def rmsnorm_backward(grad_out: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor,
@@ -546,39 +575,39 @@ def rmsnorm_backward(grad_out: torch.Tensor, x: torch.Tensor, gamma: torch.Tenso
     is the gradient of both x and the residual.  grad_x may be grad_residual itself."""
     _require(x, torch.bfloat16, "x", ndim=2)
     dev = x.device
-    _require(gamma, torch.bfloat16, "gamma", dev, ndim=1)
-    if grad_out.dtype not in DTYPES:
-        raise TypeError("grad_out must be float32 or bfloat16")
-    _require(grad_out, grad_out.dtype, "grad_out", dev, ndim=2)
+    idx, shape = dev.index, x.shape
+    T, H = shape
+    go_code = DTYPES.get(getattr(grad_out, "dtype", None))
+    if go_code is None:
+        raise TypeError("grad_out must be a float32 or bfloat16 tensor")
     if grad_dtype is None:
         grad_dtype = grad_out.dtype if grad_x is None else grad_x.dtype
-    if grad_dtype not in DTYPES:
-        raise TypeError("grad_dtype must be float32 or bfloat16")
-    T, H = x.shape
-    if grad_out.shape != x.shape or gamma.shape[0] != H:
-        raise ValueError("shape mismatch")
-    if grad_residual is not None:
-        _require(grad_residual, grad_dtype, "grad_residual", dev, ndim=2)
-        if grad_residual.shape != x.shape:
-            raise ValueError("shape mismatch")
-    with _on(dev), _alloc_on(dev, stream):
-        if grad_x is None:
-            grad_x = torch.empty((T, H), dtype=grad_dtype, device=dev)
-        _require(grad_x, grad_dtype, "grad_x", dev, ndim=2)
+    gx_code = DTYPES.get(grad_dtype)
+    if gx_code is None:
+        raise TypeError("grad_x must be float32 or bfloat16")
+    a_go = _addr(grad_out, grad_out.dtype, "grad_out", idx, shape)
+    a_gamma = _addr(gamma, torch.bfloat16, "gamma", idx, (H,))
+    a_res = _opt_addr(grad_residual, grad_dtype, "grad_residual", idx, shape)
+    a_gx = _opt_addr(grad_x, grad_dtype, "grad_x", idx, shape)
+    a_gg = _opt_addr(grad_gamma, torch.float32, "grad_gamma", idx, (H,)) if want_gamma else None
+    L = lib()
+
+    def call(st):
+        gx, gg, p_gx, p_gg = grad_x, grad_gamma if want_gamma else None, a_gx, a_gg
+        if gx is None:
+            gx = torch.empty(shape, dtype=grad_dtype, device=dev)
+            p_gx = gx.data_ptr()
+        p_ws = ws_n = 0
         if want_gamma:
-            if grad_gamma is None:
-                grad_gamma = torch.empty(H, dtype=torch.float32, device=dev)
-            _require(grad_gamma, torch.float32, "grad_gamma", dev, ndim=1)
-            workspace = _workspace(workspace, lib().rlk_rmsnorm_backward_workspace_size(T, H), dev)
-        if grad_x.shape != x.shape or (want_gamma and grad_gamma.shape[0] != H):
-            raise ValueError("shape mismatch")
-        _check(lib().rlk_rmsnorm_backward(
-            _ptr(grad_out), DTYPES[grad_out.dtype], _ptr(x), _ptr(gamma), float(eps),
-            _ptr(grad_residual), T, H, _ptr(grad_x), DTYPES[grad_dtype],
-            _ptr(grad_gamma if want_gamma else None), _ptr(workspace),
-            0 if workspace is None else workspace.numel(), _stream(dev, stream)),
-            "rlk_rmsnorm_backward")
-    return grad_x, (grad_gamma if want_gamma else None)
+            if gg is None:
+                gg = torch.empty(H, dtype=torch.float32, device=dev)
+                p_gg = gg.data_ptr()
+            p_ws, ws_n, ws = _workspace(workspace, L.rlk_rmsnorm_backward_workspace_size(T, H), dev)
+        _check(L.rlk_rmsnorm_backward(a_go, go_code, x.data_ptr(), a_gamma, eps, a_res, T, H,
+                                      p_gx, gx_code, p_gg, p_ws, ws_n, st),
+               "rlk_rmsnorm_backward")
+        return gx, gg
+    return _call_on(dev, stream, call)
 
 
 def policy_loss_workspace_size(T: int, n_seqs: int = 1) -> int:
@@ -601,40 +630,37 @@ def policy_loss(logprob: torch.Tensor, old_logprob: torch.Tensor, advantages: to
     advantages_per_seq; seq_offsets int32 [n_seqs + 1] on the device (None: one sequence of all
     tokens).  stats holds the weighted sums of -surrogate, KL, clipped tokens and
     old_logprob - logprob; grad_logprob goes straight into linear_logprob_backward."""
-    _require(logprob, torch.float32, "logprob", ndim=1)
-    dev, T = logprob.device, logprob.shape[0]
-    _require(old_logprob, torch.float32, "old_logprob", dev, ndim=1)
-    _require(advantages, torch.float32, "advantages", dev, ndim=1)
-    if ref_logprob is not None:
-        _require(ref_logprob, torch.float32, "ref_logprob", dev, ndim=1)
-    if active is not None:
-        _require(active, torch.uint8, "active", dev, ndim=1)
-    n_seqs = 1
+    f32 = torch.float32
+    _require(logprob, f32, "logprob", ndim=1)
+    dev, shape = logprob.device, logprob.shape
+    idx, T = dev.index, shape[0]
+    n_seqs, a_off = 1, None
     if seq_offsets is not None:
-        _require(seq_offsets, torch.int32, "seq_offsets", dev, ndim=1)
-        n_seqs = seq_offsets.shape[0] - 1
-    if (old_logprob.shape[0] != T or (ref_logprob is not None and ref_logprob.shape[0] != T)
-            or (active is not None and active.shape[0] != T)
-            or advantages.shape[0] != (n_seqs if advantages_per_seq else T)):
-        raise ValueError("shape mismatch")
-    kl_kind, red = _choice(KL_KINDS, kl, "kl"), _choice(REDUCTIONS, reduction, "reduction")
-    with _on(dev), _alloc_on(dev, stream):
-        out = torch.empty(5, dtype=torch.float32, device=dev)
-        if want_grad:
-            if grad_logprob is None:
-                grad_logprob = torch.empty(T, dtype=torch.float32, device=dev)
-            _require(grad_logprob, torch.float32, "grad_logprob", dev, ndim=1)
-            if grad_logprob.shape[0] != T:
-                raise ValueError("shape mismatch")
-        workspace = _workspace(workspace, policy_loss_workspace_size(T, n_seqs), dev)
-        loss, stats = out[0], out[1:]
-        _check(lib().rlk_policy_loss(
-            _ptr(logprob), _ptr(old_logprob), _ptr(ref_logprob), _ptr(advantages),
-            int(advantages_per_seq), _ptr(active), _ptr(seq_offsets), n_seqs, T, clip_low,
-            clip_high, dual_clip, kl_kind, kl_coef, red, scale, _ptr(loss), _ptr(stats),
-            _ptr(grad_logprob if want_grad else None), _ptr(workspace), workspace.numel(),
-            _status_word(status, dev), _stream(dev, stream)), "rlk_policy_loss")
-    return loss, stats, (grad_logprob if want_grad else None)
+        _require(seq_offsets, torch.int32, "seq_offsets", dev, 1)
+        n_seqs, a_off = seq_offsets.shape[0] - 1, seq_offsets.data_ptr()
+    a_old = _addr(old_logprob, f32, "old_logprob", idx, shape)
+    a_adv = _addr(advantages, f32, "advantages", idx, (n_seqs,) if advantages_per_seq else shape)
+    a_ref = _opt_addr(ref_logprob, f32, "ref_logprob", idx, shape)
+    a_act = _opt_addr(active, torch.uint8, "active", idx, shape)
+    a_grad = _opt_addr(grad_logprob, f32, "grad_logprob", idx, shape) if want_grad else None
+    a_status = _status_addr(status, idx)
+    kl_code, red = _choice(KL_KINDS, kl, "kl"), _choice(REDUCTIONS, reduction, "reduction")
+    L = lib()
+
+    def call(st):
+        loss = torch.empty((), dtype=f32, device=dev)
+        stats = torch.empty(4, dtype=f32, device=dev)
+        grad, p_grad = grad_logprob if want_grad else None, a_grad
+        if want_grad and grad is None:
+            grad = torch.empty(T, dtype=f32, device=dev)
+            p_grad = grad.data_ptr()
+        p_ws, ws_n, ws = _workspace(workspace, L.rlk_policy_loss_workspace_size(T, n_seqs), dev)
+        _check(L.rlk_policy_loss(logprob.data_ptr(), a_old, a_ref, a_adv, advantages_per_seq,
+                                 a_act, a_off, n_seqs, T, clip_low, clip_high, dual_clip, kl_code,
+                                 kl_coef, red, scale, loss.data_ptr(), stats.data_ptr(), p_grad,
+                                 p_ws, ws_n, a_status, st), "rlk_policy_loss")
+        return loss, stats, grad
+    return _call_on(dev, stream, call)
 
 
 def preference_loss(logprob: torch.Tensor, seq_offsets: torch.Tensor,
@@ -651,70 +677,77 @@ def preference_loss(logprob: torch.Tensor, seq_offsets: torch.Tensor,
     The batch holds 2 P packed sequences (seq_offsets int32 [2 P + 1] on the device); pair i is
     sequences (2 i, 2 i + 1) with layout "adjacent" and (i, P + i) with "halves", the chosen one
     first."""
-    _require(logprob, torch.float32, "logprob", ndim=1)
-    dev, T = logprob.device, logprob.shape[0]
-    _require(seq_offsets, torch.int32, "seq_offsets", dev, ndim=1)
+    f32 = torch.float32
+    _require(logprob, f32, "logprob", ndim=1)
+    dev, shape = logprob.device, logprob.shape
+    idx, T = dev.index, shape[0]
+    _require(seq_offsets, torch.int32, "seq_offsets", dev, 1)
     n_seqs = seq_offsets.shape[0] - 1
     if n_seqs < 0 or n_seqs % 2:
         raise ValueError("seq_offsets must hold an even number of sequences")
-    if ref_logprob is not None:
-        _require(ref_logprob, torch.float32, "ref_logprob", dev, ndim=1)
-    if active is not None:
-        _require(active, torch.uint8, "active", dev, ndim=1)
-    if ((ref_logprob is not None and ref_logprob.shape[0] != T)
-            or (active is not None and active.shape[0] != T)):
-        raise ValueError("shape mismatch")
+    P = n_seqs // 2
+    a_ref = _opt_addr(ref_logprob, f32, "ref_logprob", idx, shape)
+    a_act = _opt_addr(active, torch.uint8, "active", idx, shape)
+    a_grad = _opt_addr(grad_logprob, f32, "grad_logprob", idx, shape) if want_grad else None
+    a_status = _status_addr(status, idx)
     kind_code = _choice(PREFERENCE_KINDS, kind, "kind")
     layout_code = _choice(PAIR_LAYOUTS, layout, "layout")
-    P = n_seqs // 2
-    with _on(dev), _alloc_on(dev, stream):
-        loss = torch.empty((), dtype=torch.float32, device=dev)
-        pair_loss = torch.empty(P, dtype=torch.float32, device=dev)
-        rewards = torch.empty(n_seqs, dtype=torch.float32, device=dev)
-        if want_grad:
-            if grad_logprob is None:
-                grad_logprob = torch.empty(T, dtype=torch.float32, device=dev)
-            _require(grad_logprob, torch.float32, "grad_logprob", dev, ndim=1)
-            if grad_logprob.shape[0] != T:
-                raise ValueError("shape mismatch")
-        _check(lib().rlk_preference_loss(
-            _ptr(logprob), _ptr(ref_logprob), _ptr(active), _ptr(seq_offsets), P, T, layout_code,
-            kind_code, beta, label_smoothing, margin, int(length_normalize), scale, _ptr(loss),
-            _ptr(pair_loss), _ptr(rewards), _ptr(grad_logprob if want_grad else None),
-            _status_word(status, dev), _stream(dev, stream)), "rlk_preference_loss")
-    return loss, pair_loss, rewards, (grad_logprob if want_grad else None)
+    L = lib()
+
+    def call(st):
+        loss = torch.empty((), dtype=f32, device=dev)
+        pair_loss = torch.empty(P, dtype=f32, device=dev)
+        rewards = torch.empty(n_seqs, dtype=f32, device=dev)
+        grad, p_grad = grad_logprob if want_grad else None, a_grad
+        if want_grad and grad is None:
+            grad = torch.empty(T, dtype=f32, device=dev)
+            p_grad = grad.data_ptr()
+        _check(L.rlk_preference_loss(logprob.data_ptr(), a_ref, a_act, seq_offsets.data_ptr(), P,
+                                     T, layout_code, kind_code, beta, label_smoothing, margin,
+                                     length_normalize, scale, loss.data_ptr(),
+                                     pair_loss.data_ptr(), rewards.data_ptr(), p_grad, a_status,
+                                     st), "rlk_preference_loss")
+        return loss, pair_loss, rewards, grad
+    return _call_on(dev, stream, call)
 
 
-def _grad_arrays(grads, name: str):
-    """(device, host arrays of pointers, sizes and types) of a list of gradients."""
-    grads = list(grads)
+def _grad_pointers(grads, name: str):
+    """(device, host arrays of pointers, sizes and types, count) of a list of gradients."""
     n = len(grads)
     if n == 0:
         return None, None, None, None, 0
+    if not isinstance(grads[0], torch.Tensor):
+        raise TypeError("%s must be torch tensors" % name)
     dev = grads[0].device
+    idx, codes = dev.index, []
     for g in grads:
-        if g.dtype not in GRAD_DTYPES:
-            raise TypeError("%s must be float32, bfloat16 or float16" % name)
-        _require(g, g.dtype, name, dev)
-    ptrs = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
-    sizes = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
-    types = (ctypes.c_int32 * n)(*[GRAD_DTYPES[g.dtype] for g in grads])
-    return dev, ptrs, sizes, types, n
+        code = GRAD_DTYPES.get(getattr(g, "dtype", None))
+        if code is None or not g.is_cuda or g.get_device() != idx or not g.is_contiguous():
+            if code is None:
+                raise TypeError("%s must be float32, bfloat16 or float16 tensors" % name)
+            _require(g, g.dtype, name, dev)
+        codes.append(code)
+    return (dev, (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads]),
+            (ctypes.c_int64 * n)(*[g.numel() for g in grads]), (ctypes.c_int32 * n)(*codes), n)
 
 
 def grad_norm(grads: Sequence[torch.Tensor], workspace: Optional[torch.Tensor] = None,
               status: Optional[torch.Tensor] = None, device=None, stream=None) -> torch.Tensor:
     """sqrt of the sum of squares over all the tensors (fp32, bf16 or fp16, contiguous) as a
     0-dim fp32 tensor.  `device` says where an empty list's norm goes."""
-    dev, ptrs, sizes, types, n = _grad_arrays(grads, "grads")
-    dev = torch.device(device if dev is None else dev)
-    with _on(dev), _alloc_on(dev, stream):
+    dev, ptrs, sizes, types, n = _grad_pointers(list(grads), "grads")
+    if dev is None:
+        dev = _cuda_device(device)
+    a_status = _status_addr(status, dev.index)
+    L = lib()
+
+    def call(st):
         norm = torch.empty((), dtype=torch.float32, device=dev)
-        workspace = _workspace(workspace, lib().rlk_grad_norm_workspace_size(sizes, n), dev)
-        _check(lib().rlk_grad_norm(ptrs, sizes, types, n, _ptr(norm), _ptr(workspace),
-                                   workspace.numel(), _status_word(status, dev), _stream(dev, stream)),
+        p_ws, ws_n, ws = _workspace(workspace, L.rlk_grad_norm_workspace_size(sizes, n), dev)
+        _check(L.rlk_grad_norm(ptrs, sizes, types, n, norm.data_ptr(), p_ws, ws_n, a_status, st),
                "rlk_grad_norm")
-    return norm
+        return norm
+    return _call_on(dev, stream, call)
 
 
 def clip_grads(grads: Sequence[torch.Tensor], max_norm: float,
@@ -725,25 +758,37 @@ def clip_grads(grads: Sequence[torch.Tensor], max_norm: float,
     (same sizes and types) -> (norm [], scale []).  With a norm that is not finite the values
     stay as they are, scale is 1 and the status word gets RLK_ERR_NONFINITE."""
     grads = list(grads)
-    dev, ptrs, sizes, types, n = _grad_arrays(grads, "grads")
-    dev = torch.device(device if dev is None else dev)
+    dev, ptrs, sizes, types, n = _grad_pointers(grads, "grads")
+    if dev is None:
+        dev = _cuda_device(device)
     outs = ptrs
     if out is not None:
         out = list(out)
-        if len(out) != n or any(o.shape != g.shape or o.dtype != g.dtype
-                                for o, g in zip(out, grads)):
+        out_dev, outs, _, out_types, out_n = _grad_pointers(out, "out")
+        if out_n != n or any([o.shape != g.shape or o.dtype is not g.dtype
+                              for o, g in zip(out, grads)]):
             raise ValueError("out must hold one tensor of the same shape and type per gradient")
-        out_dev, outs, _, _, _ = _grad_arrays(out, "out")
         if n and out_dev != dev:
             raise ValueError("out is on %s, expected %s" % (out_dev, dev))
-    with _on(dev), _alloc_on(dev, stream):
-        res = torch.empty(2, dtype=torch.float32, device=dev)
-        norm, scale = res[0], res[1]
-        workspace = _workspace(workspace, lib().rlk_grad_norm_workspace_size(sizes, n), dev)
-        _check(lib().rlk_grad_clip(ptrs, outs, sizes, types, n, max_norm, _ptr(norm), _ptr(scale),
-                                   _ptr(workspace), workspace.numel(), _status_word(status, dev),
-                                   _stream(dev, stream)), "rlk_grad_clip")
-    return norm, scale
+    a_status = _status_addr(status, dev.index)
+    L = lib()
+
+    def call(st):
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+        scale = torch.empty((), dtype=torch.float32, device=dev)
+        p_ws, ws_n, ws = _workspace(workspace, L.rlk_grad_norm_workspace_size(sizes, n), dev)
+        _check(L.rlk_grad_clip(ptrs, outs, sizes, types, n, max_norm, norm.data_ptr(),
+                               scale.data_ptr(), p_ws, ws_n, a_status, st), "rlk_grad_clip")
+        return norm, scale
+    return _call_on(dev, stream, call)
+
+
+def _cuda_device(device) -> torch.device:
+    """`device` with its index; the current CUDA device for None."""
+    dev = torch.device("cuda" if device is None else device)
+    if dev.type != "cuda":
+        raise ValueError("device must be a CUDA device")
+    return dev if dev.index is not None else torch.device("cuda", torch.cuda.current_device())
 
 
 PRIMITIVES = {"exp": 0, "exp_x2": 1, "log": 2, "rsqrt": 3}

@@ -448,15 +448,16 @@ float2 split_two(double v) {
 }
 
 struct PolicyLayout {
-    size_t counts, parts, total;
+    size_t ticket, counts, parts, total;
 };
 
 PolicyLayout policy_layout_of(int64_t T, int64_t n_seqs) {
-    PolicyLayout l;
+    PolicyLayout l = {0, 0, 0, 0};
+    if (rlk::policy_one_launch(T, n_seqs)) return l;
     const int64_t rows = n_seqs > rlk::kPolicyCountBlocks ? n_seqs : rlk::kPolicyCountBlocks;
     const int64_t units = (T + rlk::kPolicyUnit - 1) / rlk::kPolicyUnit;
-    l.counts = 0;
-    l.parts = align256(size_t(rows) * sizeof(int32_t));
+    l.counts = 256;
+    l.parts = l.counts + align256(size_t(rows) * sizeof(int32_t));
     l.total = l.parts + align256(size_t(units) * sizeof(float4));
     return l;
 }
@@ -1015,7 +1016,7 @@ rlk_status_t rlk_policy_loss(const float* logprob, const float* old_logprob,
     if (!seq_offsets && n_seqs != 1) return RLK_ERR_INVALID_ARG;
     if (T > 0 && (!logprob || !old_logprob)) return RLK_ERR_INVALID_ARG;
     if (!advantages && (advantages_per_seq ? n_seqs : T) > 0) return RLK_ERR_INVALID_ARG;
-    if (!out_loss || !out_stats || !workspace) return RLK_ERR_INVALID_ARG;
+    if (!out_loss || !out_stats) return RLK_ERR_INVALID_ARG;
     if (!(clip_low >= 0.0) || !(clip_high >= 0.0) || !std::isfinite(clip_low) ||
         !std::isfinite(clip_high) || !std::isfinite(kl_coef) || !std::isfinite(scale))
         return RLK_ERR_INVALID_ARG;
@@ -1029,6 +1030,7 @@ rlk_status_t rlk_policy_loss(const float* logprob, const float* old_logprob,
         !aligned(out_stats, 4) || !aligned(grad_logprob, 4) || !aligned(workspace, 256))
         return RLK_ERR_ALIGNMENT;
     const PolicyLayout l = policy_layout_of(T, n_seqs);
+    if (l.total > 0 && !workspace) return RLK_ERR_INVALID_ARG;
     if (workspace_bytes < l.total) return RLK_ERR_WORKSPACE;
     DeviceState* dev = nullptr;
     rlk_status_t s = device_check(&dev);
@@ -1056,6 +1058,7 @@ rlk_status_t rlk_policy_loss(const float* logprob, const float* old_logprob,
     a.scale = scale;
     a.kl_coef64 = kl_coef;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.ticket = reinterpret_cast<int32_t*>(ws + l.ticket);
     a.counts = reinterpret_cast<int32_t*>(ws + l.counts);
     a.parts = reinterpret_cast<float4*>(ws + l.parts);
     a.out_loss = out_loss;
@@ -1107,7 +1110,8 @@ rlk_status_t rlk_preference_loss(const float* logprob, const float* ref_logprob,
     a.beta = beta;
     a.label_smoothing = label_smoothing;
     a.margin = margin;
-    a.scale = scale;
+    a.half_over_beta = 0.5 / beta;
+    a.scale_per_pair = n_pairs > 0 ? scale / double(n_pairs) : 0.0;
     a.out_loss = out_loss;
     a.out_pair_loss = out_pair_loss;
     a.out_rewards = out_rewards;

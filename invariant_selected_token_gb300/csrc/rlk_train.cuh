@@ -29,6 +29,7 @@ struct PolicyArgs {
     float ratio_high, ratio_low, dual;  // 1 + clip_high, 1 - clip_low, dual_clip (0 = off)
     float kl_coef;
     double scale, kl_coef64;
+    int32_t* ticket;          // workspace of the two-launch path: CTAs that are done
     int32_t* counts;          // workspace: active tokens per sequence or per block
     float4* parts;            // workspace: one (policy, kl, clipped, -d) sum per unit
     float* out_loss;          // [1]
@@ -39,6 +40,8 @@ struct PolicyArgs {
 
 constexpr int kPolicyUnit = 1024;         // tokens per partial sum
 constexpr int kPolicyCountBlocks = 256;   // blocks counting a token mean's active tokens
+// Whether a batch runs as one cluster, without a workspace.
+bool policy_one_launch(int64_t T, int64_t n_seqs);
 cudaError_t launch_policy_loss(const PolicyArgs& a, int num_sms, cudaStream_t stream);
 
 struct PreferenceArgs {
@@ -49,13 +52,16 @@ struct PreferenceArgs {
     int T, n_pairs;
     int halves;               // pair i = sequences (i, n_pairs + i), else (2i, 2i + 1)
     int kind, length_normalize;
-    double beta, label_smoothing, margin, scale;
+    double beta, label_smoothing, margin;
+    double half_over_beta;    // 1 / (2 beta)
+    double scale_per_pair;    // scale / n_pairs
     float* out_loss;          // [1]
     float* out_pair_loss;     // [n_pairs]
     float* out_rewards;       // [2 * n_pairs], sequence order
     float* grad;              // [T] or nullptr
     int32_t* status;
 };
+constexpr int64_t kPreferenceClusterTokens = 65536;  // largest batch that one cluster does alone
 cudaError_t launch_preference_loss(const PreferenceArgs& a, int num_sms, cudaStream_t stream);
 
 // Tensors of one launch: pointers and sizes travel by value in the kernel's parameters, so a

@@ -33,7 +33,7 @@ def test_status_name(L):
 
 def test_policy_loss_refusals(L):
     ok = dict(lp=0x1000, old=0x2000, ref=0x3000, adv=0x4000, per_seq=0, act=0x5000, off=0x6000,
-              S=2, T=10, cl=0.2, ch=0.2, dual=0.0, kl=3, klc=0.1, red=1, scale=1.0, loss=0x7000,
+              S=2, T=100000, cl=0.2, ch=0.2, dual=0.0, kl=3, klc=0.1, red=1, scale=1.0, loss=0x7000,
               stats=0x8000, grad=0x9000, ws=0x10000, wsb=1 << 20)
 
     def call(**kw):
@@ -55,6 +55,9 @@ def test_policy_loss_refusals(L):
     refused(call, WORKSPACE, wsb=100)
     assert L.rlk_policy_loss_workspace_size(-1, 1) == 0
     assert L.rlk_policy_loss_workspace_size(10, -1) == 0
+    assert L.rlk_policy_loss_workspace_size(65536, 8192) == 0  # one launch, no workspace
+    assert L.rlk_policy_loss_workspace_size(65537, 1) > 0
+    assert L.rlk_policy_loss_workspace_size(10, 8193) > 8193 * 4
     assert L.rlk_policy_loss_workspace_size(1 << 20, 1 << 14) >= (1 << 14) * 4 + (1 << 10) * 16
 
 
