@@ -382,8 +382,9 @@ rlk_status_t rlk_rmsnorm(const void* x, const void* residual, const void* gamma,
  * in fp32, each grad_x element rounded once to its type.  grad_residual is
  * the gradient that reached residual_out from further on (NULL where there
  * is none); grad_x is then the gradient of both x and residual.  A row's
- * grad_x does not depend on the batch around it; grad_gamma is the sum of
- * min(T, 304) ranges of consecutive rows, in an order that T alone fixes.
+ * grad_x does not depend on the batch around it; grad_gamma is summed over
+ * ranges of consecutive rows and then over the ranges, in an order that T
+ * and H alone fix.
  * (The blog's sections 3.3 and 4.2 ask for a backward with the forward's
  * numeric discipline; the strict-path table's "RMSNorm" row.)
  *
@@ -502,8 +503,8 @@ rlk_status_t rlk_preference_loss(const float* logprob, const float* ref_logprob,
  *   out   = RN(g * scale), rounded once to the tensor's type
  * Squares and the sums over each tensor's 16384-element chunks are fp32 (so
  * |g| above 1.8e19 makes the norm infinite and |g| below 1e-23 counts as 0),
- * the sum of the chunks' fp64; the order depends on the tensors' sizes alone,
- * not on their addresses.  A norm that is not finite leaves scale at 1 (the
+ * the sum of the chunks' fp64; the order depends on the tensors' sizes and
+ * types alone, not on their addresses.  A norm that is not finite leaves scale at 1 (the
  * gradients keep their values) and sets RLK_ERR_NONFINITE in *dev_status.
  *
  *   grads, outs   HOST arrays of n_tensors DEVICE pointers, each aligned to its element size.
@@ -513,7 +514,8 @@ rlk_status_t rlk_preference_loss(const float* logprob, const float* ref_logprob,
  *   dtypes        HOST, RLK_DTYPE_F32, RLK_DTYPE_BF16 or RLK_DTYPE_F16 per tensor
  *   max_norm      >= 0 (infinity allowed)
  *   out_norm, out_scale  device, float [1] each
- *   workspace     >= rlk_grad_norm_workspace_size(numels, n_tensors) bytes, 256-byte aligned
+ *   workspace     >= rlk_grad_norm_workspace_size(numels, n_tensors) bytes, 256-byte aligned; that
+ *                 is 0 for small sets (48 chunks in 64 tensors), then NULL is allowed
  * The host arrays are read before the call returns.
  */
 size_t rlk_grad_norm_workspace_size(const int64_t* numels, int64_t n_tensors);

@@ -466,11 +466,44 @@ int64_t clip_chunks(int64_t n) { return (n + rlk::kClipChunk - 1) / rlk::kClipCh
 
 size_t clip_element_size(int dtype) { return dtype == RLK_DTYPE_F32 ? 4 : 2; }
 
+// How the tensors are spread over launches: a table is full at kClipTable tensors or 2^30 chunks.
+struct ClipPlan {
+    int64_t tensors = 0, chunks = 0, slots = 0;
+    bool one_launch() const {
+        return chunks <= rlk::kClipClusterChunks && tensors <= rlk::ClipTableSmall::kSize;
+    }
+};
+
+constexpr int64_t kClipMostChunks = int64_t(1) << 30;
+
+ClipPlan clip_plan_of(const int64_t* numels, int64_t n) {
+    ClipPlan p;
+    int64_t count = 0, chunks = 0;
+    auto flush = [&] {
+        p.slots += chunks < rlk::kClipSlots ? chunks : rlk::kClipSlots;
+        count = chunks = 0;
+    };
+    for (int64_t i = 0; i < n; ++i) {
+        if (numels[i] == 0) continue;
+        const int64_t c = clip_chunks(numels[i]);
+        if (count == rlk::ClipTable::kSize || chunks + c > kClipMostChunks) flush();
+        ++count;
+        chunks += c;
+        ++p.tensors;
+        p.chunks += c;
+    }
+    flush();
+    return p;
+}
+
+size_t clip_workspace_of(const ClipPlan& p) {
+    return p.one_launch() ? 0 : align256(size_t(p.slots) * sizeof(double));
+}
+
 rlk_status_t clip_checks(const void* const* grads, const int64_t* numels, const int32_t* dtypes,
-                         int64_t n, const void* workspace, size_t workspace_bytes) {
+                         int64_t n, const void* workspace, size_t workspace_bytes, ClipPlan* plan) {
     if (n < 0 || n > (int64_t(1) << 24)) return RLK_ERR_INVALID_ARG;
     if (n > 0 && (!grads || !numels || !dtypes)) return RLK_ERR_INVALID_ARG;
-    int64_t chunks = 0;
     for (int64_t i = 0; i < n; ++i) {
         if (numels[i] < 0) return RLK_ERR_INVALID_ARG;
         if (numels[i] > (int64_t(1) << 40)) return RLK_ERR_UNSUPPORTED;
@@ -479,11 +512,12 @@ rlk_status_t clip_checks(const void* const* grads, const int64_t* numels, const 
         if (numels[i] == 0) continue;
         if (!grads[i]) return RLK_ERR_INVALID_ARG;
         if (!aligned(grads[i], clip_element_size(dtypes[i]))) return RLK_ERR_ALIGNMENT;
-        chunks += clip_chunks(numels[i]);
     }
-    if (chunks > 0 && !workspace) return RLK_ERR_INVALID_ARG;
+    *plan = clip_plan_of(numels, n);
+    const size_t need = clip_workspace_of(*plan);
+    if (need > 0 && !workspace) return RLK_ERR_INVALID_ARG;
     if (!aligned(workspace, 256)) return RLK_ERR_ALIGNMENT;
-    if (workspace_bytes < align256(size_t(chunks) * sizeof(float))) return RLK_ERR_WORKSPACE;
+    if (workspace_bytes < need) return RLK_ERR_WORKSPACE;
     return RLK_OK;
 }
 
@@ -520,21 +554,19 @@ rlk_status_t clip_overlap_check(const void* const* grads, void* const* outs, con
     return RLK_OK;
 }
 
-// Calls fn(table, first chunk of the table) for every table of the tensors; stops at an error.
-template <typename Fn>
+// Calls fn(table) for every table of the tensors, split as clip_plan_of counts; stops at an error.
+template <typename Table, typename Fn>
 cudaError_t for_each_clip_table(const void* const* grads, void* const* outs, const int64_t* numels,
                                 const int32_t* dtypes, int64_t n, Fn fn) {
-    rlk::ClipTable t;
-    int64_t base = 0;
+    Table t;
     t.count = 0;
     t.first[0] = 0;
     for (int64_t i = 0; i < n; ++i) {
         if (numels[i] == 0) continue;
         const int64_t c = clip_chunks(numels[i]);
-        if (t.count == rlk::kClipTable || t.first[t.count] + c > (int64_t(1) << 30)) {
-            const cudaError_t e = fn(t, base);
+        if (t.count == Table::kSize || t.first[t.count] + c > kClipMostChunks) {
+            const cudaError_t e = fn(t);
             if (e != cudaSuccess) return e;
-            base += t.first[t.count];
             t.count = 0;
         }
         t.e[t.count].in = grads[i];
@@ -544,23 +576,33 @@ cudaError_t for_each_clip_table(const void* const* grads, void* const* outs, con
         t.first[t.count + 1] = t.first[t.count] + int32_t(c);
         ++t.count;
     }
-    return t.count ? fn(t, base) : cudaSuccess;
+    return fn(t);
 }
 
-rlk_status_t run_grad_norm(const void* const* grads, const int64_t* numels, const int32_t* dtypes,
-                           int64_t n, double max_norm, float* out_norm, float* out_scale,
-                           float* partials, int32_t* dev_status, cudaStream_t stream) {
-    int64_t chunks = 0;
-    for (int64_t i = 0; i < n; ++i) chunks += clip_chunks(numels[i]);
-    if (for_each_clip_table(grads, nullptr, numels, dtypes, n,
-                            [&](const rlk::ClipTable& t, int64_t base) {
-                                return rlk::launch_grad_sumsq(t, partials + base, stream);
-                            }) != cudaSuccess)
-        return RLK_ERR_CUDA;
-    return rlk::launch_grad_norm_final(partials, chunks, max_norm, out_norm, out_scale, dev_status,
-                                       stream) == cudaSuccess
-               ? RLK_OK
-               : RLK_ERR_CUDA;
+// The norm, and with o.scale the scaled tensors.
+cudaError_t run_clip(const void* const* grads, void* const* outs, const int64_t* numels,
+                     const int32_t* dtypes, int64_t n, const ClipPlan& plan, const rlk::ClipOut& o,
+                     double* slots, cudaStream_t stream) {
+    if (plan.one_launch())
+        return for_each_clip_table<rlk::ClipTableSmall>(
+            grads, outs, numels, dtypes, n,
+            [&](const rlk::ClipTableSmall& t) { return rlk::launch_clip_cluster(t, o, stream); });
+    int64_t base = 0;
+    cudaError_t e = for_each_clip_table<rlk::ClipTable>(
+        grads, outs, numels, dtypes, n, [&](const rlk::ClipTable& t) {
+            const cudaError_t r = rlk::launch_grad_sumsq(t, slots + base, stream);
+            base += std::min<int64_t>(t.first[t.count], rlk::kClipSlots);
+            return r;
+        });
+    if (e != cudaSuccess) return e;
+    if (!o.scale) return rlk::launch_grad_norm(slots, int(plan.slots), o, stream);
+    bool write = true;
+    return for_each_clip_table<rlk::ClipTable>(
+        grads, outs, numels, dtypes, n, [&](const rlk::ClipTable& t) {
+            const cudaError_t r = rlk::launch_grad_scale(t, slots, int(plan.slots), o, write, stream);
+            write = false;
+            return r;
+        });
 }
 
 }  // namespace
@@ -952,8 +994,7 @@ rlk_status_t rlk_rmsnorm(const void* x, const void* residual, const void* gamma,
 
 size_t rlk_rmsnorm_backward_workspace_size(int64_t T, int64_t H) {
     if (T < 0 || T > RLK_MAX_ROWS || H < 64 || H % 64 != 0 || H > 8192) return 0;
-    const int64_t ranges = T < rlk::kRmsBwdBlocks ? T : rlk::kRmsBwdBlocks;
-    return align256(size_t(ranges) * size_t(H) * sizeof(float));
+    return align256(size_t(rlk::rmsnorm_backward_ranges(T, H)) * size_t(H) * sizeof(float));
 }
 
 rlk_status_t rlk_rmsnorm_backward(const void* grad_out, int grad_out_dtype, const void* x,
@@ -1125,12 +1166,9 @@ rlk_status_t rlk_preference_loss(const float* logprob, const float* ref_logprob,
 
 size_t rlk_grad_norm_workspace_size(const int64_t* numels, int64_t n_tensors) {
     if (n_tensors < 0 || (n_tensors > 0 && !numels)) return 0;
-    int64_t chunks = 0;
-    for (int64_t i = 0; i < n_tensors; ++i) {
+    for (int64_t i = 0; i < n_tensors; ++i)
         if (numels[i] < 0 || numels[i] > (int64_t(1) << 40)) return 0;
-        chunks += clip_chunks(numels[i]);
-    }
-    return align256(size_t(chunks) * sizeof(float));
+    return clip_workspace_of(clip_plan_of(numels, n_tensors));
 }
 
 rlk_status_t rlk_grad_norm(const void* const* grads, const int64_t* numels,
@@ -1138,14 +1176,18 @@ rlk_status_t rlk_grad_norm(const void* const* grads, const int64_t* numels,
                            void* workspace, size_t workspace_bytes, int32_t* dev_status,
                            rlk_stream_t stream) {
     if (!out_norm) return RLK_ERR_INVALID_ARG;
-    rlk_status_t s = clip_checks(grads, numels, dtypes, n_tensors, workspace, workspace_bytes);
+    ClipPlan plan;
+    rlk_status_t s = clip_checks(grads, numels, dtypes, n_tensors, workspace, workspace_bytes, &plan);
     if (s != RLK_OK) return s;
     if (!aligned(out_norm, 4)) return RLK_ERR_ALIGNMENT;
     DeviceState* dev = nullptr;
     if ((s = device_check(&dev)) != RLK_OK) return s;
-    return run_grad_norm(grads, numels, dtypes, n_tensors, 0.0, out_norm, nullptr,
-                         static_cast<float*>(workspace), dev_status,
-                         reinterpret_cast<cudaStream_t>(stream));
+    const rlk::ClipOut o = {out_norm, nullptr, dev_status, 0.0};
+    return run_clip(grads, nullptr, numels, dtypes, n_tensors, plan, o,
+                    static_cast<double*>(workspace), reinterpret_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? RLK_OK
+               : RLK_ERR_CUDA;
 }
 
 rlk_status_t rlk_grad_clip(const void* const* grads, void* const* outs, const int64_t* numels,
@@ -1154,7 +1196,8 @@ rlk_status_t rlk_grad_clip(const void* const* grads, void* const* outs, const in
                            size_t workspace_bytes, int32_t* dev_status, rlk_stream_t stream) {
     if (!out_norm || !out_scale || (n_tensors > 0 && !outs) || !(max_norm >= 0.0))
         return RLK_ERR_INVALID_ARG;
-    rlk_status_t s = clip_checks(grads, numels, dtypes, n_tensors, workspace, workspace_bytes);
+    ClipPlan plan;
+    rlk_status_t s = clip_checks(grads, numels, dtypes, n_tensors, workspace, workspace_bytes, &plan);
     if (s != RLK_OK) return s;
     if (!aligned(out_norm, 4) || !aligned(out_scale, 4)) return RLK_ERR_ALIGNMENT;
     for (int64_t i = 0; i < n_tensors; ++i) {
@@ -1165,14 +1208,10 @@ rlk_status_t rlk_grad_clip(const void* const* grads, void* const* outs, const in
     if ((s = clip_overlap_check(grads, outs, numels, dtypes, n_tensors)) != RLK_OK) return s;
     DeviceState* dev = nullptr;
     if ((s = device_check(&dev)) != RLK_OK) return s;
-    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if ((s = run_grad_norm(grads, numels, dtypes, n_tensors, max_norm, out_norm, out_scale,
-                           static_cast<float*>(workspace), dev_status, st)) != RLK_OK)
-        return s;
-    return for_each_clip_table(grads, outs, numels, dtypes, n_tensors,
-                               [&](const rlk::ClipTable& t, int64_t) {
-                                   return rlk::launch_grad_scale(t, out_scale, st);
-                               }) == cudaSuccess
+    const rlk::ClipOut o = {out_norm, out_scale, dev_status, max_norm};
+    return run_clip(grads, outs, numels, dtypes, n_tensors, plan, o,
+                    static_cast<double*>(workspace), reinterpret_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
                ? RLK_OK
                : RLK_ERR_CUDA;
 }

@@ -66,25 +66,36 @@ cudaError_t launch_preference_loss(const PreferenceArgs& a, int num_sms, cudaStr
 
 // Tensors of one launch: pointers and sizes travel by value in the kernel's parameters, so a
 // captured launch holds them and nothing has to be copied to the device first.
-constexpr int kClipTable = 640;
 struct ClipEntry {
     const void* in;
     void* out;
     int64_t n;
 };
-struct ClipTable {
-    ClipEntry e[kClipTable];
-    int32_t first[kClipTable + 1];  // each tensor's first chunk within this launch
-    uint8_t dtype[kClipTable];
+template <int kMost>
+struct ClipTableOf {
+    static constexpr int kSize = kMost;
+    ClipEntry e[kMost];
+    int32_t first[kMost + 1];  // each tensor's first chunk within this launch
+    uint8_t dtype[kMost];
     int count;
 };
-constexpr int kClipChunk = 16384;   // elements per partial sum
-cudaError_t launch_grad_sumsq(const ClipTable& t, float* partials, cudaStream_t stream);
-// norm, scale = the two outputs (either may be nullptr)
-cudaError_t launch_grad_norm_final(const float* partials, int64_t n, double max_norm,
-                                   float* out_norm, float* out_scale, int32_t* status,
-                                   cudaStream_t stream);
-cudaError_t launch_grad_scale(const ClipTable& t, const float* scale, cudaStream_t stream);
+using ClipTable = ClipTableOf<640>;
+using ClipTableSmall = ClipTableOf<64>;
+struct ClipOut {
+    float* norm;
+    float* scale;             // nullptr: the norm alone is wanted
+    int32_t* status;
+    double max_norm;
+};
+constexpr int kClipChunk = 16384;       // elements per partial sum
+constexpr int kClipSlots = 152 * 6;     // partial sums of a launch, CTAs of the large kernels
+constexpr int kClipClusterChunks = 48;  // largest set that one cluster does in one launch
+cudaError_t launch_clip_cluster(const ClipTableSmall& t, const ClipOut& o, cudaStream_t stream);
+cudaError_t launch_grad_sumsq(const ClipTable& t, double* slots, cudaStream_t stream);
+cudaError_t launch_grad_norm(const double* slots, int n, const ClipOut& o, cudaStream_t stream);
+// write: this launch stores norm and scale
+cudaError_t launch_grad_scale(const ClipTable& t, const double* slots, int n, const ClipOut& o,
+                              bool write, cudaStream_t stream);
 
 struct RmsBwdArgs {
     const void* grad_out;     // [T][H] fp32 or bf16
@@ -98,7 +109,12 @@ struct RmsBwdArgs {
     int T, H;
     int go_dtype, gx_dtype;   // RLK_DTYPE_*
 };
-constexpr int kRmsBwdBlocks = 304;  // row ranges whose grad_gamma sums are formed apart
+// Ranges of rows whose grad_gamma sums are formed apart, a CTA each: two 512-thread CTAs per SM,
+// or one of 1024 threads where a row needs that many.
+inline int rmsnorm_backward_ranges(int64_t T, int64_t H) {
+    const int most = H > 4096 ? 152 : 304;
+    return T < most ? static_cast<int>(T) : most;
+}
 cudaError_t launch_rmsnorm_backward(const RmsBwdArgs& a, cudaStream_t stream);
 
 // ---------------------------------------------------------------- device arithmetic

@@ -120,7 +120,8 @@ def test_grad_clip_refusals(L):
         if norm_only:
             return L.rlk_grad_norm(p, s, t, n, norm, ws, wsb, None, None)
         return L.rlk_grad_clip(p, o, s, t, n, max_norm, norm, scale, ws, wsb, None, None)
-    for kw in (dict(ptrs=(None, 0x20000)), dict(sizes=(-1, 16)), dict(norm=None), dict(ws=None)):
+    for kw in (dict(ptrs=(None, 0x20000)), dict(sizes=(-1, 16)), dict(norm=None),
+               dict(sizes=(1 << 20, 16), ws=None)):
         refused(call, INVALID, **kw)
         refused(call, INVALID, norm_only=True, **kw)
     for kw in (dict(scale=None), dict(max_norm=-1.0), dict(max_norm=math.nan),
@@ -137,7 +138,11 @@ def test_grad_clip_refusals(L):
     for kw in (dict(ptrs=(0x10002, 0x20000)), dict(ptrs=(0x10000, 0x20001)),
                dict(outs=(0x30002, 0x40000)), dict(ws=0x110)):
         refused(call, ALIGNMENT, **kw)
-    refused(call, WORKSPACE, wsb=4)
+    refused(call, WORKSPACE, sizes=(1 << 20, 16), ptrs=(0x10000, 0x10000000), wsb=4)
+    small = (ctypes.c_int64 * 2)(47 * 16384, 16384)
+    assert L.rlk_grad_norm_workspace_size(small, 2) == 0  # one launch, no workspace
+    small[1] = 16385
+    assert L.rlk_grad_norm_workspace_size(small, 2) >= 49 * 8
     sizes = (ctypes.c_int64 * 2)(-1, 4)
     assert L.rlk_grad_norm_workspace_size(sizes, 2) == 0
     assert L.rlk_grad_norm_workspace_size(None, 2) == 0
