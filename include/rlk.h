@@ -442,7 +442,7 @@ rlk_status_t rlk_rmsnorm_backward(const void* grad_out, int grad_out_dtype, cons
  *                 clipped tokens and of old_logprob - logprob
  *   grad_logprob  device, float [T], or NULL for the loss alone
  *   workspace     >= rlk_policy_loss_workspace_size(T, n_seqs) bytes, 256-byte aligned; that is 0
- *                 for small batches (up to 65536 tokens and 8192 sequences), then NULL is allowed
+ *                 for small batches (up to 32768 tokens and 1024 sequences), then NULL is allowed
  */
 #define RLK_KL_K1 1
 #define RLK_KL_K2 2

@@ -9,7 +9,9 @@ to.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
 import os
 from typing import List, Optional, Sequence, Tuple
 
@@ -509,6 +511,7 @@ PAIR_LAYOUTS = {"adjacent": 0, "halves": 1}
 GRAD_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_dtype = operator.attrgetter("dtype")
 
 
 def _choice(table, key, name: str) -> int:
@@ -711,40 +714,50 @@ def preference_loss(logprob: torch.Tensor, seq_offsets: torch.Tensor,
     return _call_on(dev, stream, call)
 
 
-def _grad_pointers(grads, name: str):
-    """(device, host arrays of pointers, sizes and types, count) of a list of gradients."""
-    n = len(grads)
-    if n == 0:
-        return None, None, None, None, 0
-    if not isinstance(grads[0], torch.Tensor):
+def _grad_list(grads, name: str):
+    """(device, sizes, types and pointers as lists) of a list of contiguous gradients on one
+    device; lists of hundreds of tensors go through the C loops of map()."""
+    if not grads:
+        return None, [], [], []
+    if not all(isinstance(g, torch.Tensor) for g in grads):
         raise TypeError("%s must be torch tensors" % name)
     dev = grads[0].device
-    idx, codes = dev.index, []
-    for g in grads:
-        code = GRAD_DTYPES.get(getattr(g, "dtype", None))
-        if code is None or not g.is_cuda or g.get_device() != idx or not g.is_contiguous():
-            if code is None:
+    dtypes = list(map(_get_dtype, grads))
+    if (set(map(torch.Tensor.get_device, grads)) != {dev.index} or dev.type != "cuda"
+            or not all(map(torch.Tensor.is_contiguous, grads)) or not GRAD_DTYPES.keys() >= set(dtypes)):
+        for g in grads:
+            if g.dtype not in GRAD_DTYPES:
                 raise TypeError("%s must be float32, bfloat16 or float16 tensors" % name)
             _require(g, g.dtype, name, dev)
-        codes.append(code)
-    return (dev, (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads]),
-            (ctypes.c_int64 * n)(*[g.numel() for g in grads]), (ctypes.c_int32 * n)(*codes), n)
+    return (dev, list(map(torch.Tensor.numel, grads)), dtypes,
+            array.array("Q", map(torch.Tensor.data_ptr, grads)))
+
+
+def _host_addr(a):
+    return a.buffer_info()[0] if len(a) else None
+
+
+def _host_arrays(sizes, dtypes):
+    return array.array("q", sizes), array.array("i", map(GRAD_DTYPES.__getitem__, dtypes))
 
 
 def grad_norm(grads: Sequence[torch.Tensor], workspace: Optional[torch.Tensor] = None,
               status: Optional[torch.Tensor] = None, device=None, stream=None) -> torch.Tensor:
     """sqrt of the sum of squares over all the tensors (fp32, bf16 or fp16, contiguous) as a
     0-dim fp32 tensor.  `device` says where an empty list's norm goes."""
-    dev, ptrs, sizes, types, n = _grad_pointers(list(grads), "grads")
+    dev, sizes, dtypes, ptrs = _grad_list(list(grads), "grads")
     if dev is None:
         dev = _cuda_device(device)
     a_status = _status_addr(status, dev.index)
+    n = len(sizes)
+    sizes, types = _host_arrays(sizes, dtypes)
+    h_ptrs, h_sizes, h_types = (_host_addr(a) for a in (ptrs, sizes, types))
     L = lib()
 
     def call(st):
         norm = torch.empty((), dtype=torch.float32, device=dev)
-        p_ws, ws_n, ws = _workspace(workspace, L.rlk_grad_norm_workspace_size(sizes, n), dev)
-        _check(L.rlk_grad_norm(ptrs, sizes, types, n, norm.data_ptr(), p_ws, ws_n, a_status, st),
+        p_ws, ws_n, ws = _workspace(workspace, L.rlk_grad_norm_workspace_size(h_sizes, n), dev)
+        _check(L.rlk_grad_norm(h_ptrs, h_sizes, h_types, n, norm.data_ptr(), p_ws, ws_n, a_status, st),
                "rlk_grad_norm")
         return norm
     return _call_on(dev, stream, call)
@@ -757,27 +770,27 @@ def clip_grads(grads: Sequence[torch.Tensor], max_norm: float,
     """Scale the gradients by min(1, max_norm / norm), in place or into the tensors of `out`
     (same sizes and types) -> (norm [], scale []).  With a norm that is not finite the values
     stay as they are, scale is 1 and the status word gets RLK_ERR_NONFINITE."""
-    grads = list(grads)
-    dev, ptrs, sizes, types, n = _grad_pointers(grads, "grads")
+    dev, sizes, dtypes, ptrs = _grad_list(list(grads), "grads")
     if dev is None:
         dev = _cuda_device(device)
     outs = ptrs
     if out is not None:
-        out = list(out)
-        out_dev, outs, _, out_types, out_n = _grad_pointers(out, "out")
-        if out_n != n or any([o.shape != g.shape or o.dtype is not g.dtype
-                              for o, g in zip(out, grads)]):
-            raise ValueError("out must hold one tensor of the same shape and type per gradient")
-        if n and out_dev != dev:
+        out_dev, out_sizes, out_dtypes, outs = _grad_list(list(out), "out")
+        if out_sizes != sizes or out_dtypes != dtypes:
+            raise ValueError("out must hold one tensor of the same size and type per gradient")
+        if out_dev is not None and out_dev != dev:
             raise ValueError("out is on %s, expected %s" % (out_dev, dev))
     a_status = _status_addr(status, dev.index)
+    n = len(sizes)
+    sizes, types = _host_arrays(sizes, dtypes)
+    h_ptrs, h_outs, h_sizes, h_types = (_host_addr(a) for a in (ptrs, outs, sizes, types))
     L = lib()
 
     def call(st):
         norm = torch.empty((), dtype=torch.float32, device=dev)
         scale = torch.empty((), dtype=torch.float32, device=dev)
-        p_ws, ws_n, ws = _workspace(workspace, L.rlk_grad_norm_workspace_size(sizes, n), dev)
-        _check(L.rlk_grad_clip(ptrs, outs, sizes, types, n, max_norm, norm.data_ptr(),
+        p_ws, ws_n, ws = _workspace(workspace, L.rlk_grad_norm_workspace_size(h_sizes, n), dev)
+        _check(L.rlk_grad_clip(h_ptrs, h_outs, h_sizes, h_types, n, max_norm, norm.data_ptr(),
                                scale.data_ptr(), p_ws, ws_n, a_status, st), "rlk_grad_clip")
         return norm, scale
     return _call_on(dev, stream, call)

@@ -15,11 +15,11 @@
 // rounded ratio could go either way next to the border.
 //
 // The weights need counts of active tokens before the first gradient, so
-// there are two passes over the mask and one over everything else.  Up to
-// kClusterTokens tokens one cluster of 8 CTAs does it all in one launch, the
-// counts and partial sums meeting in its shared memory; beyond, a counting
-// launch is followed by one CTA per unit of 1024 tokens, the last of which
-// adds up the units.  Both add the same numbers in the same order.
+// the mask is read before anything else is formed.  Up to 4096 tokens one
+// CTA, up to 32768 one cluster of 8 does it all in one launch, its threads
+// holding their tokens meanwhile; beyond, a counting launch is followed by one
+// CTA per unit of 1024 tokens, the last of which adds up the units.  All add
+// the same numbers in the same order.
 #include <cooperative_groups.h>
 
 #include "rlk_ptx.cuh"
@@ -32,10 +32,8 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256;               // threads of a unit
 constexpr int kPer = kPolicyUnit / kThreads;
-constexpr int kCluster = 8;                 // CTAs of the one-launch path
-constexpr int kGroups = 4;                  // units that one of them works on at a time
-constexpr int64_t kClusterTokens = 65536;   // largest batch of the one-launch path
-constexpr int kClusterSeqs = 8192;          // and its most sequences (their counts in shared memory)
+constexpr int kCluster = 8;                 // most CTAs of the one-launch path
+constexpr int kGroups = 4;                  // units that one of them takes
 
 struct Bounds {
     int first, last;   // tokens outside [first, last) belong to no sequence
@@ -120,63 +118,67 @@ __device__ __forceinline__ TokenTerms token_terms(const PolicyArgs& a, float lp,
     return o;
 }
 
-// One unit's tokens by one of its 8 warps: gradients out, the warp's sums of the four stats
-// returned to every lane.  A warp takes 128 consecutive tokens; everything is loaded before
-// anything is used, inactive tokens too (their values are dropped, never multiplied).
-template <typename CountOf>
-__device__ __forceinline__ float4 policy_warp(const PolicyArgs& a, int64_t unit, int warp,
-                                              const Bounds& bd, float w_all, CountOf count_of) {
-    const int lane = threadIdx.x & 31;
-    const int64_t t0 = unit * kPolicyUnit + warp * (kPer * 32);
-    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (t0 >= a.T) return sum;
+// The tokens of one of a unit's 8 warps: 128 consecutive ones, lane l taking every 32nd.
+// Everything is loaded before anything is used, inactive tokens too (their values are dropped,
+// never multiplied).
+struct WarpTokens {
+    int64_t t0;
     float lp[kPer], old[kPer], ref[kPer], adv[kPer];
     bool on[kPer];
+    __device__ __forceinline__ int64_t token(int i) const { return t0 + i * 32 + (threadIdx.x & 31); }
+    __device__ __forceinline__ void load(const PolicyArgs& a, int64_t unit, int warp) {
+        t0 = unit * kPolicyUnit + warp * (kPer * 32);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int64_t t = t0 + i * 32 + lane;
-        const bool in = t < a.T;
-        lp[i] = in ? a.logprob[t] : 0.0f;
-        old[i] = in ? a.old_logprob[t] : 0.0f;
-        ref[i] = in && a.ref_logprob ? a.ref_logprob[t] : 0.0f;
-        adv[i] = in && !a.adv_per_seq ? a.advantages[t] : 0.0f;
-        on[i] = in && t >= bd.first && t < bd.last && (!a.active || a.active[t] != 0);
+        for (int i = 0; i < kPer; ++i) {
+            const int64_t t = token(i);
+            const bool in = t < a.T;
+            lp[i] = in ? a.logprob[t] : 0.0f;
+            old[i] = in ? a.old_logprob[t] : 0.0f;
+            ref[i] = in && a.ref_logprob ? a.ref_logprob[t] : 0.0f;
+            adv[i] = in && !a.adv_per_seq ? a.advantages[t] : 0.0f;
+            on[i] = in && (!a.active || a.active[t] != 0);
+        }
     }
-    const bool by_seq = a.offsets && (a.adv_per_seq || a.reduction == RLK_REDUCE_SEQ_MEAN);
-    int seq_lo = 0, seq_hi = 0;
-    if (by_seq) {
-        const int64_t tl = t0 + kPer * 32 - 1;
-        seq_lo = warp_find_seq(a.offsets, a.n_seqs, static_cast<int>(t0));
-        seq_hi = warp_find_seq(a.offsets, a.n_seqs, static_cast<int>(tl < a.T ? tl : a.T - 1));
-        if (seq_hi < seq_lo) seq_hi = seq_lo;
+    // tokens of no sequence take no part
+    __device__ __forceinline__ void cut(const Bounds& b) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) on[i] = on[i] && token(i) >= b.first && token(i) < b.last;
     }
+};
+
+// Gradients of a warp's tokens out; its sums of the four stats, on every lane.  seq_of(i) is
+// token i's sequence, count_of(s) and adv_of(s) that one's active tokens and advantage.
+template <typename SeqOf, typename CountOf, typename AdvOf>
+__device__ __forceinline__ float4 policy_warp(const PolicyArgs& a, const WarpTokens& k, float w_all, SeqOf seq_of,
+                                              CountOf count_of, AdvOf adv_of) {
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const float scale = static_cast<float>(a.scale);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int64_t t = t0 + i * 32 + lane;
         float g = 0.0f;
-        if (on[i]) {
-            const int s = by_seq ? find_seq(a.offsets, seq_lo, seq_hi, static_cast<int>(t)) : 0;
-            float w = w_all;
+        if (k.on[i]) {
+            float w = w_all, adv = k.adv[i];
             if (a.reduction == RLK_REDUCE_SEQ_MEAN) {
-                const int n = count_of(s);
-                w = __fdiv_rn(1.0f, __fmul_rn(static_cast<float>(a.n_seqs),
-                                              static_cast<float>(n > 1 ? n : 1)));
+                const int n = count_of(seq_of(i));
+                w = __fdiv_rn(1.0f, __fmul_rn(static_cast<float>(a.n_seqs), static_cast<float>(n > 1 ? n : 1)));
             }
-            if (a.adv_per_seq) adv[i] = a.advantages[s];
-            const TokenTerms o = token_terms(a, lp[i], old[i], ref[i], adv[i]);
+            if (a.adv_per_seq) adv = adv_of(seq_of(i));
+            const TokenTerms o = token_terms(a, k.lp[i], k.old[i], k.ref[i], adv);
             sum.x = __fmaf_rn(w, o.policy, sum.x);
             sum.y = __fmaf_rn(w, o.kl, sum.y);
             sum.z = __fmaf_rn(w, o.clipped, sum.z);
             sum.w = __fmaf_rn(w, o.neg_d, sum.w);
             g = __fmul_rn(__fmul_rn(scale, w), o.slope);
         }
-        if (a.grad && t < a.T) a.grad[t] = g;
+        if (a.grad && k.token(i) < a.T) a.grad[k.token(i)] = g;
     }
-    sum.x = warp_sum(sum.x);
-    sum.y = warp_sum(sum.y);
-    sum.z = warp_sum(sum.z);
-    sum.w = warp_sum(sum.w);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        sum.x = __fadd_rn(sum.x, __shfl_xor_sync(0xffffffffu, sum.x, o));
+        sum.y = __fadd_rn(sum.y, __shfl_xor_sync(0xffffffffu, sum.y, o));
+        sum.z = __fadd_rn(sum.z, __shfl_xor_sync(0xffffffffu, sum.z, o));
+        sum.w = __fadd_rn(sum.w, __shfl_xor_sync(0xffffffffu, sum.w, o));
+    }
     return sum;
 }
 
@@ -192,116 +194,145 @@ __device__ __forceinline__ float token_weight(const PolicyArgs& a, int n) {
     return a.reduction == RLK_REDUCE_TOKEN_MEAN ? __fdiv_rn(1.0f, static_cast<float>(n > 1 ? n : 1)) : 1.0f;
 }
 
-// Offsets that descend or leave [0, T], seen by any of `threads` threads.
-__device__ __forceinline__ bool offsets_bad(const PolicyArgs& a, int thread, int threads) {
-    bool bad = false;
-    if (a.offsets) {
-        for (int64_t s = thread; s <= a.n_seqs; s += threads) {
-            const int b = a.offsets[s], e = s < a.n_seqs ? a.offsets[s + 1] : a.T;
-            bad |= b < 0 || e < b || e > a.T;
-        }
-    }
-    return bad;
+// The units' sums are added like this: slot j takes units j, j + 256, ... in ascending order, the
+// 32 slots of a warp are added by a shuffle tree, the 8 warps' sums in order, all in fp64.
+__device__ __forceinline__ void write_stat(const PolicyArgs& a, int k, double v, bool bad) {
+    a.out_stats[k] = bad ? CUDART_NAN_F : static_cast<float>(v);
 }
-
-// The loss from the units' sums, by the first 256 threads of a CTA (all of it calls).
-__device__ __forceinline__ void policy_finish(const PolicyArgs& a, const float4* parts, int64_t units,
-                                              bool bad, double (*smem)[4]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (threadIdx.x < kThreads) {
-        double v[4] = {0.0, 0.0, 0.0, 0.0};
-        for (int64_t u = threadIdx.x; u < units; u += kThreads) {
-            const float4 p = parts[u];
-            v[0] += static_cast<double>(p.x);
-            v[1] += static_cast<double>(p.y);
-            v[2] += static_cast<double>(p.z);
-            v[3] += static_cast<double>(p.w);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[k] = warp_sum(v[k]);
-            if (lane == 0) smem[warp][k] = v[k];
-        }
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        double s[4];
-        for (int k = 0; k < 4; ++k) {
-            s[k] = smem[0][k];
-            for (int i = 1; i < kThreads / 32; ++i) s[k] += smem[i][k];
-        }
-        const float nan = CUDART_NAN_F;
-        *a.out_loss = bad ? nan : static_cast<float>(a.scale * (s[0] + a.kl_coef64 * s[1]));
-        for (int k = 0; k < 4; ++k) a.out_stats[k] = bad ? nan : static_cast<float>(s[k]);
-        if (bad) report_status(a.status, RLK_ERR_INVALID_ARG);
-    }
+__device__ __forceinline__ void write_loss(const PolicyArgs& a, double policy, double kl, bool bad) {
+    *a.out_loss = bad ? CUDART_NAN_F : static_cast<float>(a.scale * (policy + a.kl_coef64 * kl));
+    if (bad) report_status(a.status, RLK_ERR_INVALID_ARG);
 }
 
 // ---------------------------------------------------------------- one launch
-// Dynamic shared memory: int counts[n_seqs] (seq_mean with a mask).
-__global__ void __launch_bounds__(kGroups * kThreads) k_policy_cluster(const PolicyArgs a) {
-    extern __shared__ int counts[];
-    __shared__ float4 parts[kClusterTokens / kPolicyUnit];   // the first CTA's are used
+constexpr int kLaunchSeqs = 1024;  // most sequences of the one-launch path: kept in shared memory
+
+// The last s in [0, n) with offsets[s] <= t, in shared memory.
+__device__ __forceinline__ int seq_in(const int32_t* offsets, int n, int t) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (offsets[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// One cluster of kCtas CTAs, 4 units each: a thread holds its 4 tokens from the first load to
+// the gradient, and the counts that the weights need come from the masks it holds.
+template <int kCtas>
+__global__ void __launch_bounds__(kGroups * kThreads) k_policy_one(const PolicyArgs a) {
+    constexpr int kAll = kGroups * kThreads;
+    static_assert(kCtas * kGroups <= 32, "a lane per unit");
+    __shared__ int32_t offsets[kLaunchSeqs + 1];
+    __shared__ float adv[kLaunchSeqs];
+    __shared__ int counts[kLaunchSeqs];
+    __shared__ int totals[kLaunchSeqs];
+    __shared__ float4 parts[32];           // the first CTA's are used
     __shared__ float4 warps[kGroups][kThreads / 32];
-    __shared__ double finish[kThreads / 32][4];
     __shared__ int active_here;
-    cg::cluster_group cluster = cg::this_cluster();
-    cluster.barrier_arrive();
-    const int rank = static_cast<int>(cluster.block_rank());
+    const int rank = kCtas > 1 ? static_cast<int>(blockIdx.x) : 0;
     const int lane = threadIdx.x & 31, group = threadIdx.x / kThreads;
     const int warp = (threadIdx.x % kThreads) >> 5;
-    const int64_t units = (static_cast<int64_t>(a.T) + kPolicyUnit - 1) / kPolicyUnit;
-    const Bounds bd = bounds_of(a);
-    const bool masked = a.active != nullptr;
-    const bool by_seq = a.reduction == RLK_REDUCE_SEQ_MEAN;
+    const int unit = rank * kGroups + group;
+    WarpTokens k;
+    k.load(a, unit, warp);
+    const bool masked = a.active != nullptr, by_mean = a.reduction == RLK_REDUCE_SEQ_MEAN;
+    const bool by_seq = a.offsets && (a.adv_per_seq || by_mean);
+    Bounds bd = {0, a.T};
+    bool bad = false;
+    if (a.offsets) {
+        bd = bounds_of(a);
+        for (int s = threadIdx.x; s <= a.n_seqs; s += kAll) {
+            const int b = a.offsets[s], e = s < a.n_seqs ? a.offsets[s + 1] : a.T;
+            bad |= b < 0 || e < b || e > a.T;
+            offsets[s] = b;
+        }
+    }
+    for (int s = threadIdx.x; s < a.n_seqs; s += kAll) {
+        counts[s] = 0;
+        if (a.adv_per_seq) adv[s] = a.advantages[s];
+    }
+    if (threadIdx.x == 0) active_here = 0;
+    bad = __syncthreads_or(bad);
+    k.cut(bd);
+    int seq[kPer] = {};
+    if (by_seq) {
+        // a warp's 128 tokens: mostly of one sequence
+        const int64_t tl = k.t0 + kPer * 32 - 1;
+        const int lo = k.t0 < a.T ? seq_in(offsets, a.n_seqs, static_cast<int>(k.t0)) : 0;
+        const int hi = k.t0 < a.T ? seq_in(offsets, a.n_seqs, static_cast<int>(tl < a.T ? tl : a.T - 1)) : 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            seq[i] = lo;
+            if (hi > lo && k.on[i]) seq[i] = lo + seq_in(offsets + lo, hi - lo + 1, static_cast<int>(k.token(i)));
+        }
+    }
     int n_all = bd.last - bd.first;
     if (masked && a.reduction != RLK_REDUCE_SUM) {
-        // each CTA counts an eighth of the tokens (token_mean) or of the sequences (seq_mean)
-        if (threadIdx.x == 0) active_here = 0;
-        __syncthreads();
-        if (by_seq) {
-            cluster.barrier_wait();  // every CTA has started: its shared memory may be written
-            for (int s = rank * (kGroups * kThreads / 32) + (threadIdx.x >> 5); s < a.n_seqs;
-                 s += kCluster * (kGroups * kThreads / 32)) {
-                const int64_t b = a.offsets ? a.offsets[s] : 0, e = a.offsets ? a.offsets[s + 1] : a.T;
-                const int n = __reduce_add_sync(0xffffffffu, count_active(a.active, b, e, a.T, lane, 32));
-                // every CTA keeps all counts
-                if (lane < kCluster) *cluster.map_shared_rank(counts + s, lane) = n;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int n = __popc(__ballot_sync(0xffffffffu, k.on[i]));
+            const int s0 = __shfl_sync(0xffffffffu, seq[i], 0);
+            if (!by_mean) {
+                if (lane == 0 && n) atomicAdd(&active_here, n);
+            } else if (__all_sync(0xffffffffu, seq[i] == s0)) {
+                if (lane == 0 && n) atomicAdd(&counts[s0], n);
+            } else if (k.on[i]) {
+                atomicAdd(&counts[seq[i]], 1);
+            }
+        }
+        if constexpr (kCtas > 1) {
+            cg::cluster_group cluster = cg::this_cluster();
+            cluster.sync();
+            if (by_mean) {
+                for (int s = threadIdx.x; s < a.n_seqs; s += kAll) {
+                    int n = 0;
+#pragma unroll
+                    for (int c = 0; c < kCtas; ++c) n += cluster.map_shared_rank(counts, c)[s];
+                    totals[s] = n;
+                }
+                __syncthreads();
+            } else {
+                n_all = __reduce_add_sync(0xffffffffu, lane < kCtas ? *cluster.map_shared_rank(&active_here, lane % kCtas) : 0);
             }
         } else {
-            int n = count_active(a.active, bd.first, bd.last, a.T,
-                                 rank * (kGroups * kThreads) + threadIdx.x, kCluster * kGroups * kThreads);
-            n = __reduce_add_sync(0xffffffffu, n);
-            if (lane == 0) atomicAdd(&active_here, n);
-            cluster.barrier_wait();
+            __syncthreads();
+            n_all = active_here;
         }
-        cluster.sync();
-        if (!by_seq) {
-            n_all = 0;
-            for (int c = 0; c < kCluster; ++c) n_all += *cluster.map_shared_rank(&active_here, c);
+    } else if constexpr (kCtas > 1) {
+        cg::this_cluster().sync();  // every CTA has started: its shared memory may be written
+    }
+    const float4 s = policy_warp(
+        a, k, token_weight(a, n_all), [&](int i) { return seq[i]; },
+        [&](int q) {
+            return masked ? (kCtas > 1 ? totals[q] : counts[q]) : (a.offsets ? offsets[q + 1] - offsets[q] : a.T);
+        },
+        [&](int q) { return adv[q]; });
+    if (lane == 0) warps[group][warp] = s;
+    __syncthreads();
+    float4* all_parts = parts;
+    if constexpr (kCtas > 1) all_parts = cg::this_cluster().map_shared_rank(parts, 0);
+    if (threadIdx.x % kThreads < 4)
+        reinterpret_cast<float*>(all_parts + unit)[threadIdx.x % kThreads] =
+            unit_sum(warps[group], threadIdx.x % kThreads);
+    if constexpr (kCtas > 1) cg::this_cluster().sync(); else __syncthreads();
+    if (rank != 0 || threadIdx.x >= 3 * 32) return;
+    // units 0 .. 31 are the first warp's slots of the order above; the rest of it adds zeros.
+    // Warp 0 forms the loss and the two stats in it, warps 1 and 2 the others.
+    const float* p = reinterpret_cast<const float*>(parts + lane);
+    const bool have = lane < kCtas * kGroups;
+    const int w = threadIdx.x >> 5;
+    const double v = warp_sum(have ? static_cast<double>(p[w == 0 ? 0 : w + 1]) : 0.0);
+    if (w == 0) {
+        const double kl = warp_sum(have ? static_cast<double>(p[1]) : 0.0);
+        if (lane == 0) {
+            write_loss(a, v, kl, bad);
+            write_stat(a, 0, v, bad);
+            write_stat(a, 1, kl, bad);
         }
-    } else {
-        cluster.barrier_wait();
+    } else if (lane == 0) {
+        write_stat(a, w + 1, v, bad);
     }
-    const float w_all = token_weight(a, n_all);
-    auto count_of = [&](int s) {
-        return masked ? counts[s] : (a.offsets ? a.offsets[s + 1] - a.offsets[s] : a.T);
-    };
-    float4* const all_parts = cluster.map_shared_rank(parts, 0);
-    for (int64_t u0 = rank * kGroups; u0 < units; u0 += kCluster * kGroups) {
-        const int64_t u = u0 + group;
-        const float4 s = policy_warp(a, u, warp, bd, w_all, count_of);
-        if (lane == 0) warps[group][warp] = s;
-        __syncthreads();
-        if (threadIdx.x % kThreads < 4 && u < units)
-            reinterpret_cast<float*>(all_parts + u)[threadIdx.x % kThreads] =
-                unit_sum(warps[group], threadIdx.x % kThreads);
-        __syncthreads();
-    }
-    cluster.sync();
-    if (rank != 0) return;
-    const bool bad = __syncthreads_or(offsets_bad(a, threadIdx.x, kGroups * kThreads));
-    policy_finish(a, parts, units, bad, finish);
 }
 
 // ---------------------------------------------------------------- two launches
@@ -343,6 +374,9 @@ __global__ void __launch_bounds__(kThreads) k_policy_main(const PolicyArgs a) {
     __shared__ int total;
     __shared__ bool last_here;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t units = (static_cast<int64_t>(a.T) + kPolicyUnit - 1) / kPolicyUnit;
+    WarpTokens k;
+    k.load(a, blockIdx.x, warp);
     const Bounds bd = bounds_of(a);
     if (threadIdx.x == 0) total = 0;
     ptx::grid_dependency_wait();
@@ -355,12 +389,25 @@ __global__ void __launch_bounds__(kThreads) k_policy_main(const PolicyArgs a) {
         n_all = total;
     }
     const float w_all = token_weight(a, n_all);
-    auto count_of = [&](int s) {
-        return a.active ? a.counts[s] : (a.offsets ? a.offsets[s + 1] - a.offsets[s] : a.T);
-    };
-    const int64_t units = (static_cast<int64_t>(a.T) + kPolicyUnit - 1) / kPolicyUnit;
+    const bool by_seq = a.offsets && (a.adv_per_seq || a.reduction == RLK_REDUCE_SEQ_MEAN);
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const float4 s = policy_warp(a, u, warp, bd, w_all, count_of);
+        if (u != blockIdx.x) k.load(a, u, warp);
+        k.cut(bd);
+        int seq[kPer] = {};
+        if (by_seq && k.t0 < a.T) {
+            const int64_t tl = k.t0 + kPer * 32 - 1;
+            const int lo = warp_find_seq(a.offsets, a.n_seqs, static_cast<int>(k.t0));
+            const int hi = warp_find_seq(a.offsets, a.n_seqs, static_cast<int>(tl < a.T ? tl : a.T - 1));
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                seq[i] = hi > lo && k.on[i] ? find_seq(a.offsets, lo, hi, static_cast<int>(k.token(i))) : lo;
+        }
+        const float4 s = policy_warp(
+            a, k, w_all, [&](int i) { return seq[i]; },
+            [&](int q) {
+                return a.active ? a.counts[q] : (a.offsets ? a.offsets[q + 1] - a.offsets[q] : a.T);
+            },
+            [&](int q) { return a.advantages[q]; });
         if (lane == 0) warps[warp] = s;
         __syncthreads();
         if (threadIdx.x < 4) reinterpret_cast<float*>(a.parts + u)[threadIdx.x] = unit_sum(warps, threadIdx.x);
@@ -373,32 +420,66 @@ __global__ void __launch_bounds__(kThreads) k_policy_main(const PolicyArgs a) {
     __syncthreads();
     if (!last_here) return;
     __threadfence();
-    const bool bad = __syncthreads_or(offsets_bad(a, threadIdx.x, kThreads));
-    policy_finish(a, a.parts, units, bad, finish);
+    bool bad = false;
+    if (a.offsets) {
+        for (int64_t s = threadIdx.x; s <= a.n_seqs; s += kThreads) {
+            const int b = a.offsets[s], e = s < a.n_seqs ? a.offsets[s + 1] : a.T;
+            bad |= b < 0 || e < b || e > a.T;
+        }
+    }
+    bad = __syncthreads_or(bad);
+    double v[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 4
+    for (int64_t u = threadIdx.x; u < units; u += kThreads) {
+        const float4 p = a.parts[u];
+        v[0] += static_cast<double>(p.x);
+        v[1] += static_cast<double>(p.y);
+        v[2] += static_cast<double>(p.z);
+        v[3] += static_cast<double>(p.w);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = __dadd_rn(v[c], __shfl_xor_sync(0xffffffffu, v[c], o));
+    }
+    if (lane == 0) {
+        for (int c = 0; c < 4; ++c) finish[warp][c] = v[c];
+    }
+    __syncthreads();
+    if (threadIdx.x < 4) {
+        double s = finish[0][threadIdx.x];
+        for (int i = 1; i < kThreads / 32; ++i) s = __dadd_rn(s, finish[i][threadIdx.x]);
+        write_stat(a, threadIdx.x, s, bad);
+        const double kl = __shfl_sync(0xfu, s, 1);
+        if (threadIdx.x == 0) write_loss(a, s, kl, bad);
+    }
+}
+
+template <int kCtas>
+cudaError_t launch_one(const PolicyArgs& a, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.stream = stream;
+    cfg.gridDim = dim3(kCtas, 1, 1);
+    cfg.blockDim = dim3(kGroups * kThreads, 1, 1);
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kCtas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kCtas > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k_policy_one<kCtas>, a);
 }
 
 }  // namespace
 
 bool policy_one_launch(int64_t T, int64_t n_seqs) {
-    return T <= kClusterTokens && n_seqs <= kClusterSeqs;
+    return T <= kCluster * kGroups * kPolicyUnit && n_seqs <= kLaunchSeqs;
 }
 
 cudaError_t launch_policy_loss(const PolicyArgs& a, int num_sms, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (policy_one_launch(a.T, a.n_seqs)) {
-        cfg.gridDim = dim3(kCluster, 1, 1);
-        cfg.blockDim = dim3(kGroups * kThreads, 1, 1);
-        if (a.active && a.reduction == RLK_REDUCE_SEQ_MEAN) cfg.dynamicSmemBytes = size_t(a.n_seqs) * sizeof(int);
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = kCluster;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        return cudaLaunchKernelEx(&cfg, k_policy_cluster, a);
-    }
+    if (policy_one_launch(a.T, a.n_seqs))
+        return a.T <= kGroups * kPolicyUnit ? launch_one<1>(a, stream) : launch_one<kCluster>(a, stream);
     int rows = 1;
     if (a.active && a.reduction != RLK_REDUCE_SUM)
         rows = a.reduction == RLK_REDUCE_SEQ_MEAN ? a.n_seqs : kPolicyCountBlocks;
@@ -408,11 +489,15 @@ cudaError_t launch_policy_loss(const PolicyArgs& a, int num_sms, cudaStream_t st
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int64_t units = (static_cast<int64_t>(a.T) + kPolicyUnit - 1) / kPolicyUnit;
-    cfg.gridDim = dim3(static_cast<unsigned>(units < most ? units : most), 1, 1);
-    if (units == 0) cfg.gridDim.x = 1;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.stream = stream;
+    cfg.gridDim = dim3(static_cast<unsigned>(units < most ? (units > 0 ? units : 1) : most), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, k_policy_main, a);
 }
 

@@ -63,7 +63,7 @@ struct Raw8 {  // 8 features as loaded
 // every kTeams-th row of its range.  The next row's x and grad_out are loaded before the current
 // one is reduced, so that the reduction and its barrier hide behind them.
 template <int kWarps, int kGo, int kGx>
-__global__ void __launch_bounds__(cta_threads(kWarps)) k_rmsnorm_backward(const RmsBwdArgs a) {
+__global__ void __launch_bounds__(cta_threads(kWarps), kWarps == 32 ? 1 : 2) k_rmsnorm_backward(const RmsBwdArgs a) {
     constexpr int kThreads = cta_threads(kWarps), kTeams = kThreads / 32 / kWarps;
     __shared__ float2 part[2][kThreads / 32];
     __shared__ __align__(16) float dg_teams[kTeams > 1 ? kThreads * 8 : 1];

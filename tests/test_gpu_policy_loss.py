@@ -291,3 +291,25 @@ def test_binding_shape_checks(rlk, cuda_device):
         rlk.policy_loss(x, x, x, seq_offsets=off.long())
     with pytest.raises(rlk.RlkError):
         rlk.policy_loss(x, x, x, kl_coef=0.1)
+
+
+@pytest.mark.parametrize("reduction", ["sum", "token_mean", "seq_mean"])
+def test_every_launch_shape_gives_the_same_bits(rlk, cuda_device, reduction):
+    """The same sequences in batches of 4096, 32768 and 200000 tokens (the others behind the last
+    sequence), which one CTA, one cluster and two launches take; and among 2000 empty sequences."""
+    n, offsets = 4000, [3, 900, 900, 2500, 3990]
+    b = batch(200000, offsets, seed=14, mask=0.7)
+    results = []
+    for T in (4096, 4097, 32768, 32769, 200000):
+        part = {k: (v[:T] if k in ("lp", "old", "ref", "adv_t", "active") else v) for k, v in b.items()}
+        loss, stats, grad = run(rlk, cuda_device, part, True, kl_coef=0.1, reduction=reduction)
+        assert not grad[n:].any()
+        results.append((loss, stats, grad[:n]))
+    for r in results[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(r, results[0]))
+    if reduction != "seq_mean":  # where the number of sequences does not count
+        many = {k: (v[:n] if k in ("lp", "old", "ref", "adv_t", "active") else v) for k, v in b.items()}
+        many["offsets"] = offsets + [3990] * 2000
+        many["adv_s"] = np.concatenate([b["adv_s"], np.full(2000, np.nan, np.float32)])
+        r = run(rlk, cuda_device, many, True, kl_coef=0.1, reduction=reduction)
+        assert all(torch.equal(x, y) for x, y in zip(r, results[0]))

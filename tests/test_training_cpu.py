@@ -55,9 +55,9 @@ def test_policy_loss_refusals(L):
     refused(call, WORKSPACE, wsb=100)
     assert L.rlk_policy_loss_workspace_size(-1, 1) == 0
     assert L.rlk_policy_loss_workspace_size(10, -1) == 0
-    assert L.rlk_policy_loss_workspace_size(65536, 8192) == 0  # one launch, no workspace
-    assert L.rlk_policy_loss_workspace_size(65537, 1) > 0
-    assert L.rlk_policy_loss_workspace_size(10, 8193) > 8193 * 4
+    assert L.rlk_policy_loss_workspace_size(32768, 1024) == 0  # one launch, no workspace
+    assert L.rlk_policy_loss_workspace_size(32769, 1) > 0
+    assert L.rlk_policy_loss_workspace_size(10, 1025) > 1025 * 4
     assert L.rlk_policy_loss_workspace_size(1 << 20, 1 << 14) >= (1 << 14) * 4 + (1 << 10) * 16
 
 
