@@ -482,18 +482,22 @@ rlk_status_t rlk_policy_loss(const float* logprob, const float* old_logprob,
  *   out_rewards   device, float [2 * n_pairs]: beta m_q, in sequence order
  *   grad_logprob  device, float [T], or NULL; 0 for inactive tokens and those of no sequence
  *   n_pairs       at most 2^30
+ *   workspace     >= rlk_preference_loss_workspace_size(T, n_pairs) bytes, 256-byte aligned; that
+ *                 is 0, and NULL allowed, for all but few pairs of many tokens
  */
 #define RLK_PREF_SIGMOID 0
 #define RLK_PREF_HINGE 1
 #define RLK_PREF_IPO 2
 #define RLK_PAIRS_ADJACENT 0
 #define RLK_PAIRS_HALVES 1
+size_t rlk_preference_loss_workspace_size(int64_t T, int64_t n_pairs);
 rlk_status_t rlk_preference_loss(const float* logprob, const float* ref_logprob,
                                  const uint8_t* active_mask, const int32_t* seq_offsets,
                                  int64_t n_pairs, int64_t T, int layout, int kind, double beta,
                                  double label_smoothing, double margin, int length_normalize,
                                  double scale, float* out_loss, float* out_pair_loss,
-                                 float* out_rewards, float* grad_logprob, int32_t* dev_status,
+                                 float* out_rewards, float* grad_logprob, void* workspace,
+                                 size_t workspace_bytes, int32_t* dev_status,
                                  rlk_stream_t stream);
 
 /*

@@ -38,7 +38,7 @@ EXPORTED = ["rlk_contract_id", "rlk_build_fingerprint", "rlk_status_string", "rl
             "rlk_debug_primitive_hash", "rlk_linear_logprob_save_logits",
             "rlk_linear_logprob_backward_from_logits", "rlk_rmsnorm_backward_workspace_size",
             "rlk_rmsnorm_backward", "rlk_policy_loss_workspace_size", "rlk_policy_loss",
-            "rlk_preference_loss", "rlk_grad_norm_workspace_size", "rlk_grad_norm",
+            "rlk_preference_loss", "rlk_preference_loss_workspace_size", "rlk_grad_norm_workspace_size", "rlk_grad_norm",
             "rlk_grad_clip"]
 DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 
@@ -115,7 +115,9 @@ def lib() -> ctypes.CDLL:
                                       i32, dbl, P, P, P, P, sz, P, P]
         L.rlk_preference_loss.restype = i32
         L.rlk_preference_loss.argtypes = [P, P, P, P, i64, i64, i32, i32, dbl, dbl, dbl, i32, dbl,
-                                          P, P, P, P, P, P]
+                                          P, P, P, P, P, sz, P, P]
+        L.rlk_preference_loss_workspace_size.restype = sz
+        L.rlk_preference_loss_workspace_size.argtypes = [i64, i64]
         L.rlk_grad_norm_workspace_size.restype = sz
         L.rlk_grad_norm_workspace_size.argtypes = [P, i64]
         L.rlk_grad_norm.restype = i32
@@ -666,6 +668,10 @@ def policy_loss(logprob: torch.Tensor, old_logprob: torch.Tensor, advantages: to
     return _call_on(dev, stream, call)
 
 
+def preference_loss_workspace_size(T: int, n_pairs: int) -> int:
+    return int(lib().rlk_preference_loss_workspace_size(T, n_pairs))
+
+
 def preference_loss(logprob: torch.Tensor, seq_offsets: torch.Tensor,
                     ref_logprob: Optional[torch.Tensor] = None,
                     active: Optional[torch.Tensor] = None, beta: float = 0.1,
@@ -673,6 +679,7 @@ def preference_loss(logprob: torch.Tensor, seq_offsets: torch.Tensor,
                     length_normalize: bool = False, layout: str = "adjacent",
                     scale: float = 1.0, want_grad: bool = True,
                     grad_logprob: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None,
                     status: Optional[torch.Tensor] = None, stream=None):
     """Preference loss on paired log ratios -> (loss [], pair_loss [P], rewards [2 P],
     grad_logprob [T] or None).
@@ -705,11 +712,12 @@ def preference_loss(logprob: torch.Tensor, seq_offsets: torch.Tensor,
         if want_grad and grad is None:
             grad = torch.empty(T, dtype=f32, device=dev)
             p_grad = grad.data_ptr()
+        p_ws, ws_n, ws = _workspace(workspace, L.rlk_preference_loss_workspace_size(T, P), dev)
         _check(L.rlk_preference_loss(logprob.data_ptr(), a_ref, a_act, seq_offsets.data_ptr(), P,
                                      T, layout_code, kind_code, beta, label_smoothing, margin,
                                      length_normalize, scale, loss.data_ptr(),
-                                     pair_loss.data_ptr(), rewards.data_ptr(), p_grad, a_status,
-                                     st), "rlk_preference_loss")
+                                     pair_loss.data_ptr(), rewards.data_ptr(), p_grad, p_ws, ws_n,
+                                     a_status, st), "rlk_preference_loss")
         return loss, pair_loss, rewards, grad
     return _call_on(dev, stream, call)
 

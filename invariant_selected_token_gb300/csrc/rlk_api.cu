@@ -462,6 +462,20 @@ PolicyLayout policy_layout_of(int64_t T, int64_t n_seqs) {
     return l;
 }
 
+struct PreferenceLayout {
+    size_t ticket, sums, counts, total;
+};
+
+PreferenceLayout preference_layout_of(int64_t T, int64_t n_pairs) {
+    PreferenceLayout l = {0, 0, 0, 0};
+    if (!rlk::preference_split(T, n_pairs)) return l;
+    const size_t chunks = size_t(rlk::preference_chunks(T, n_pairs));
+    l.sums = 256;
+    l.counts = l.sums + align256(chunks * sizeof(double));
+    l.total = l.counts + align256(chunks * sizeof(int32_t));
+    return l;
+}
+
 int64_t clip_chunks(int64_t n) { return (n + rlk::kClipChunk - 1) / rlk::kClipChunk; }
 
 size_t clip_element_size(int dtype) { return dtype == RLK_DTYPE_F32 ? 4 : 2; }
@@ -1112,12 +1126,18 @@ rlk_status_t rlk_policy_loss(const float* logprob, const float* old_logprob,
                : RLK_ERR_CUDA;
 }
 
+size_t rlk_preference_loss_workspace_size(int64_t T, int64_t n_pairs) {
+    if (T < 0 || T > RLK_MAX_ROWS || n_pairs < 0 || n_pairs > (int64_t(1) << 30)) return 0;
+    return preference_layout_of(T, n_pairs).total;
+}
+
 rlk_status_t rlk_preference_loss(const float* logprob, const float* ref_logprob,
                                  const uint8_t* active_mask, const int32_t* seq_offsets,
                                  int64_t n_pairs, int64_t T, int layout, int kind, double beta,
                                  double label_smoothing, double margin, int length_normalize,
                                  double scale, float* out_loss, float* out_pair_loss,
-                                 float* out_rewards, float* grad_logprob, int32_t* dev_status,
+                                 float* out_rewards, float* grad_logprob, void* workspace,
+                                 size_t workspace_bytes, int32_t* dev_status,
                                  rlk_stream_t stream) {
     if (T < 0 || T > RLK_MAX_ROWS || n_pairs < 0 || n_pairs > (int64_t(1) << 30))
         return RLK_ERR_INVALID_ARG;
@@ -1133,8 +1153,11 @@ rlk_status_t rlk_preference_loss(const float* logprob, const float* ref_logprob,
         return RLK_ERR_INVALID_ARG;
     if (!aligned(logprob, 4) || !aligned(ref_logprob, 4) || !aligned(seq_offsets, 4) ||
         !aligned(out_loss, 4) || !aligned(out_pair_loss, 4) || !aligned(out_rewards, 4) ||
-        !aligned(grad_logprob, 4))
+        !aligned(grad_logprob, 4) || !aligned(workspace, 256))
         return RLK_ERR_ALIGNMENT;
+    const PreferenceLayout l = preference_layout_of(T, n_pairs);
+    if (l.total > 0 && !workspace) return RLK_ERR_INVALID_ARG;
+    if (workspace_bytes < l.total) return RLK_ERR_WORKSPACE;
     DeviceState* dev = nullptr;
     rlk_status_t s = device_check(&dev);
     if (s != RLK_OK) return s;
@@ -1157,6 +1180,10 @@ rlk_status_t rlk_preference_loss(const float* logprob, const float* ref_logprob,
     a.out_pair_loss = out_pair_loss;
     a.out_rewards = out_rewards;
     a.grad = grad_logprob;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.ticket = reinterpret_cast<int32_t*>(ws + l.ticket);
+    a.chunk_sums = reinterpret_cast<double*>(ws + l.sums);
+    a.chunk_counts = reinterpret_cast<int32_t*>(ws + l.counts);
     a.status = dev_status;
     return rlk::launch_preference_loss(a, dev->sm_count, reinterpret_cast<cudaStream_t>(stream)) ==
                    cudaSuccess

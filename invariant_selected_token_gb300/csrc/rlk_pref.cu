@@ -15,11 +15,14 @@
 // then a shuffle tree in fp64); chunk g is added to slot g mod 1024 in
 // ascending order, and the slots are added by a fixed tree in fp64.
 //
-// A pair is the work of a team of 1, 2, 4 or 8 CTAs of one cluster.  They
-// meet in the shared memory of the team's first CTA: slots in, the two
-// sequences' slopes out.  Small batches run as one cluster, which also adds
-// up the pairs' losses; larger ones as a cluster per pair and a second launch
-// for that sum.
+// Batches of up to kPreferenceClusterTokens tokens run as one cluster in one
+// launch: a pair is the work of a team of 1, 2, 4 or 8 of its CTAs, which
+// meet in the shared memory of the team's first one (slots in, the two
+// sequences' slopes out), and the first CTA adds up the pairs' losses.
+// Larger batches of many pairs run the same kernel with a team per pair and
+// add up in a second launch.  Larger batches of a few pairs, whose teams
+// would leave most of the device idle, take one launch over all chunks and
+// one over all tokens, whose CTAs each form the slopes they need.
 #include <cooperative_groups.h>
 
 #include "rlk_ptx.cuh"
@@ -35,6 +38,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kChunk = 256;
 constexpr int kSlots = 1024;
 constexpr int kCluster = 8;
+constexpr int kHeldPairs = 512;  // pairs whose losses one cluster keeps in shared memory
 
 struct Span {
     int64_t b, e;
@@ -52,7 +56,8 @@ __device__ __forceinline__ Span span_of(const PreferenceArgs& a, int64_t q) {
 
 // A pair's loss, rewards and slopes from its two sums and counts, by one thread.
 __device__ __forceinline__ void pair_terms(const PreferenceArgs& a, int pair, int64_t q0, int64_t q1,
-                                           double m0, double m1, int n0, int n1, float* slope) {
+                                           double m0, double m1, int n0, int n1, bool write,
+                                           float* slope, float* held_loss) {
     double inv0 = 1.0, inv1 = 1.0;
     if (a.length_normalize) {
         inv0 = 1.0 / (n0 > 1 ? n0 : 1);
@@ -85,122 +90,178 @@ __device__ __forceinline__ void pair_terms(const PreferenceArgs& a, int pair, in
             dh = a.beta * (a.label_smoothing * sp - (1.0 - a.label_smoothing) * sn);
         }
     }
-    a.out_pair_loss[pair] = static_cast<float>(loss);
-    a.out_rewards[q0] = static_cast<float>(a.beta * m0);
-    a.out_rewards[q1] = static_cast<float>(a.beta * m1);
+    if (write) {
+        a.out_pair_loss[pair] = static_cast<float>(loss);
+        a.out_rewards[q0] = static_cast<float>(a.beta * m0);
+        a.out_rewards[q1] = static_cast<float>(a.beta * m1);
+    }
+    if (held_loss) *held_loss = static_cast<float>(loss);
     const double step = a.scale_per_pair * dh;
     slope[0] = static_cast<float>(step * inv0);
     slope[1] = static_cast<float>(-step * inv1);
 }
 
-// The loss from the pairs' losses, by a whole CTA of kThreads.
-__device__ __forceinline__ void preference_finish(const PreferenceArgs& a, double* tmp) {
+__device__ __forceinline__ int64_t chosen_of(const PreferenceArgs& a, int pair) {
+    return a.halves ? pair : 2 * static_cast<int64_t>(pair);
+}
+__device__ __forceinline__ int64_t rejected_of(const PreferenceArgs& a, int pair) {
+    return a.halves ? a.n_pairs + static_cast<int64_t>(pair) : 2 * static_cast<int64_t>(pair) + 1;
+}
+
+// Offsets that descend or leave [0, T], as far as this thread sees.
+__device__ __forceinline__ bool offsets_bad(const PreferenceArgs& a) {
     bool bad = false;
     const int64_t n = 2 * static_cast<int64_t>(a.n_pairs);
     for (int64_t s = threadIdx.x; s <= n; s += kThreads) {
         const int b = a.offsets[s], e = s < n ? a.offsets[s + 1] : a.T;
         bad |= b < 0 || e < b || e > a.T;
     }
+    return bad;
+}
+
+// The loss from the pairs' losses, by a whole CTA.
+__device__ __forceinline__ void preference_finish(const PreferenceArgs& a, const float* losses, bool bad, double* tmp) {
     bad = __syncthreads_or(bad);
     double v = 0.0;
-    for (int i = threadIdx.x; i < a.n_pairs; i += kThreads)
-        v += static_cast<double>(__ldcg(a.out_pair_loss + i));
+    for (int i = threadIdx.x; i < a.n_pairs; i += kThreads) v = __dadd_rn(v, static_cast<double>(losses[i]));
     v = warp_sum(v);
     if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = v;
     __syncthreads();
     if (threadIdx.x == 0) {
         v = 0.0;
-        for (int i = 0; i < kWarps; ++i) v += tmp[i];
+        for (int i = 0; i < kWarps; ++i) v = __dadd_rn(v, tmp[i]);
         if (a.n_pairs > 0) v = a.scale_per_pair * v;
         *a.out_loss = bad ? CUDART_NAN_F : static_cast<float>(v);
         if (bad) report_status(a.status, RLK_ERR_INVALID_ARG);
     }
 }
 
-// One launch of clusters; every `team` CTAs of a cluster take a pair.
-__global__ void __launch_bounds__(kThreads) k_preference(const PreferenceArgs a, int team, int finish) {
+// Sum and active tokens of chunk g of a sequence, by a warp, on every lane.
+__device__ __forceinline__ double chunk_sum(const PreferenceArgs& a, const Span& sp, int64_t g, int* count) {
+    const int lane = threadIdx.x & 31;
+    float lp[kChunk / 32], ref[kChunk / 32];
+    bool on[kChunk / 32];
+#pragma unroll
+    for (int i = 0; i < kChunk / 32; ++i) {
+        const int64_t t = sp.b + g * kChunk + i * 32 + lane;
+        const bool in = t < sp.e;
+        lp[i] = in ? a.logprob[t] : 0.0f;
+        ref[i] = in && a.ref_logprob ? a.ref_logprob[t] : 0.0f;
+        on[i] = in && (!a.active || a.active[t] != 0);
+    }
+    float2 acc = make_float2(0.0f, 0.0f);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kChunk / 32; ++i) {
+        if (!on[i]) continue;
+        ++n;
+        const float2 d = two_diff(lp[i], ref[i]);
+        two_add(acc, d.x);
+        acc.y = __fadd_rn(acc.y, d.y);
+    }
+    *count = __reduce_add_sync(0xffffffffu, n);
+    return warp_sum(static_cast<double>(acc.x) + static_cast<double>(acc.y));
+}
+
+__device__ __forceinline__ int64_t chunks_of(const Span& s) { return (s.e - s.b + kChunk - 1) / kChunk; }
+
+struct PairScratch {
+    double tmp[2][kWarps];
+    int n[2][kWarps];
+};
+
+// Slots of both sequences -> the pair's terms, by a whole CTA; `slope` and the outputs are set
+// by thread 0, so a barrier has to follow.  slot(side, j) and count(side, j) give a slot's sum
+// and its active tokens; slots from chunks_of() on are empty.
+template <typename SlotOf, typename CountOf>
+__device__ __forceinline__ void reduce_pair(const PreferenceArgs& a, int pair, const Span (&sp)[2], SlotOf slot,
+                                            CountOf count, bool write, PairScratch& sc, float* slope, float* held_loss) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int held[2];
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+        const int64_t c = chunks_of(sp[side]);
+        held[side] = c < kSlots ? static_cast<int>(c) : kSlots;
+        if (warp * 32 >= held[side]) continue;  // empty slots add zeros
+        double v = 0.0;
+        int n = 0;
+        for (int i = threadIdx.x; i < held[side]; i += kThreads) {
+            v = __dadd_rn(v, slot(side, i));
+            n += count(side, i);
+        }
+        v = warp_sum(v);
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0) {
+            sc.tmp[side][warp] = v;
+            sc.n[side][warp] = n;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double v[2] = {0.0, 0.0};
+        int n[2] = {0, 0};
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+            for (int i = 0; i < kWarps && i * 32 < held[side]; ++i) {
+                v[side] = __dadd_rn(v[side], sc.tmp[side][i]);
+                n[side] += sc.n[side][i];
+            }
+        }
+        pair_terms(a, pair, chosen_of(a, pair), rejected_of(a, pair), v[0], v[1], n[0], n[1], write, slope, held_loss);
+    }
+}
+
+// ---------------------------------------------------------------- a team of CTAs per pair
+// One launch of clusters; every `team` CTAs of a cluster take a pair at a time.  alone: this is
+// the only cluster, and it also forms the loss.
+__global__ void __launch_bounds__(kThreads) k_preference(const PreferenceArgs a, int team, int alone) {
     __shared__ double slots[2][kSlots];
-    __shared__ int counts[2];
-    __shared__ double tmp[2][kWarps];
+    __shared__ int counts[2][kSlots];
+    __shared__ PairScratch scratch;
     __shared__ float slope[2];
+    __shared__ float losses[kHeldPairs];  // the first CTA's, when alone
     cg::cluster_group cluster = cg::this_cluster();
+    cluster.barrier_arrive();
     const int rank = static_cast<int>(cluster.block_rank()), size = static_cast<int>(cluster.num_blocks());
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int member = rank % team, lead = rank - member;
     const int teams = size / team;
     const int stride = gridDim.x / team;  // pairs in flight
     const int first = static_cast<int>(blockIdx.x) / size * teams + rank / team;
-    double (*const lead_slots)[kSlots] =
-        reinterpret_cast<double (*)[kSlots]>(cluster.map_shared_rank(&slots[0][0], lead));
-    int* const lead_counts = cluster.map_shared_rank(counts, lead);
+    double* const lead_slots = cluster.map_shared_rank(&slots[0][0], lead);
+    int* const lead_counts = cluster.map_shared_rank(&counts[0][0], lead);
     const float* const lead_slope = cluster.map_shared_rank(slope, lead);
+    float* const all_losses = cluster.map_shared_rank(losses, 0);
+    const bool bad = alone && rank == 0 ? offsets_bad(a) : false;
+    cluster.barrier_wait();  // every CTA has started: its shared memory may be written
     const int rounds = (a.n_pairs + stride - 1) / stride;
     for (int r = 0; r < rounds; ++r) {
         const int pair = first + r * stride;
         const bool work = pair < a.n_pairs;
-        const int64_t q[2] = {a.halves ? pair : 2 * static_cast<int64_t>(pair),
-                              a.halves ? a.n_pairs + static_cast<int64_t>(pair) : 2 * static_cast<int64_t>(pair) + 1};
         Span sp[2] = {{0, 0}, {0, 0}};
         if (work) {
-            sp[0] = span_of(a, q[0]);
-            sp[1] = span_of(a, q[1]);
+            sp[0] = span_of(a, chosen_of(a, pair));
+            sp[1] = span_of(a, rejected_of(a, pair));
         }
-        for (int i = threadIdx.x; i < 2 * kSlots; i += kThreads) slots[i / kSlots][i % kSlots] = 0.0;
-        if (threadIdx.x < 2) counts[threadIdx.x] = 0;
-        if (team > 1) cluster.sync(); else __syncthreads();
-#pragma unroll
+#pragma unroll 1
         for (int side = 0; side < 2; ++side) {
-            int n = 0;
-            for (int64_t g = member * kWarps + warp; sp[side].b + g * kChunk < sp[side].e; g += team * kWarps) {
-                float lp[kChunk / 32], ref[kChunk / 32];
-                bool on[kChunk / 32];
-#pragma unroll
-                for (int i = 0; i < kChunk / 32; ++i) {
-                    const int64_t t = sp[side].b + g * kChunk + i * 32 + lane;
-                    const bool in = t < sp[side].e;
-                    lp[i] = in ? a.logprob[t] : 0.0f;
-                    ref[i] = in && a.ref_logprob ? a.ref_logprob[t] : 0.0f;
-                    on[i] = in && (!a.active || a.active[t] != 0);
-                }
-                float2 acc = make_float2(0.0f, 0.0f);
-#pragma unroll
-                for (int i = 0; i < kChunk / 32; ++i) {
-                    if (!on[i]) continue;
-                    ++n;
-                    const float2 d = two_diff(lp[i], ref[i]);
-                    two_add(acc, d.x);
-                    acc.y = __fadd_rn(acc.y, d.y);
-                }
-                const double v = warp_sum(static_cast<double>(acc.x) + static_cast<double>(acc.y));
+            const Span& s = sp[side];
+            for (int64_t g = member * kWarps + warp; s.b + g * kChunk < s.e; g += team * kWarps) {
+                int n;
+                const double v = chunk_sum(a, s, g, &n);
                 if (lane == 0) {
                     // a slot is only ever this warp's
-                    double* const slot = &lead_slots[side][g % kSlots];
-                    *slot = __dadd_rn(*slot, v);
+                    const int at = side * kSlots + static_cast<int>(g % kSlots);
+                    lead_slots[at] = __dadd_rn(g < kSlots ? 0.0 : lead_slots[at], v);
+                    lead_counts[at] = (g < kSlots ? 0 : lead_counts[at]) + n;
                 }
             }
-            n = __reduce_add_sync(0xffffffffu, n);
-            if (lane == 0 && n) atomicAdd(&lead_counts[side], n);  // whole numbers: any order will do
         }
         if (team > 1) cluster.sync(); else __syncthreads();
-        if (member == 0 && work) {
-            double v[2];
-#pragma unroll
-            for (int side = 0; side < 2; ++side) {
-                v[side] = 0.0;
-                for (int i = threadIdx.x; i < kSlots; i += kThreads) v[side] = __dadd_rn(v[side], slots[side][i]);
-                v[side] = warp_sum(v[side]);
-                if (lane == 0) tmp[side][warp] = v[side];
-            }
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                v[0] = v[1] = 0.0;
-                for (int i = 0; i < kWarps; ++i) {
-                    v[0] = __dadd_rn(v[0], tmp[0][i]);
-                    v[1] = __dadd_rn(v[1], tmp[1][i]);
-                }
-                pair_terms(a, pair, q[0], q[1], v[0], v[1], counts[0], counts[1], slope);
-            }
-        }
+        if (member == 0 && work)
+            reduce_pair(a, pair, sp, [&](int side, int j) { return slots[side][j]; },
+                        [&](int side, int j) { return counts[side][j]; }, true, scratch, slope,
+                        alone ? all_losses + pair : nullptr);
         if (team > 1) cluster.sync(); else __syncthreads();
         if (a.grad && work) {
             const int who = member * kThreads + threadIdx.x, all = team * kThreads;
@@ -218,61 +279,224 @@ __global__ void __launch_bounds__(kThreads) k_preference(const PreferenceArgs a,
                 for (int64_t t = span_of(a, 2 * static_cast<int64_t>(a.n_pairs) - 1).e + who; t < a.T; t += all)
                     a.grad[t] = 0.0f;
         }
-        __syncthreads();  // slots, counts and slopes are free for the next round
+        // slots and slope are written again only behind a barrier that everyone reaches after
+        // reading them: with one CTA per team that is this one
+        if (team == 1) __syncthreads();
     }
-    // nobody leaves while its shared memory may be read; the pairs' losses are out
-    if (finish) __threadfence();
-    cluster.sync();
-    if (finish && rank == 0) {
-        if (finish) __threadfence();
-        preference_finish(a, tmp[0]);
-    }
+    cluster.sync();  // nobody leaves while its shared memory may be read; all losses are there
+    if (alone && rank == 0) preference_finish(a, losses, bad, scratch.tmp[0]);
 }
 
 __global__ void __launch_bounds__(kThreads) k_preference_final(const PreferenceArgs a) {
     __shared__ double tmp[kWarps];
+    const bool bad = offsets_bad(a);
     ptx::grid_dependency_wait();
-    preference_finish(a, tmp);
+    preference_finish(a, a.out_pair_loss, bad, tmp);
 }
 
-}  // namespace
+// ---------------------------------------------------------------- all CTAs over all pairs
+constexpr int kSplitSeqs = 64;  // most sequences of this path
 
-cudaError_t launch_preference_loss(const PreferenceArgs& a, int num_sms, cudaStream_t stream) {
-    if (a.n_pairs == 0 && a.grad && a.T > 0) {
-        const cudaError_t e = cudaMemsetAsync(a.grad, 0, size_t(a.T) * sizeof(float), stream);
-        if (e != cudaSuccess) return e;
+// Each sequence's tokens and first chunk in the launches' common numbering; no chunk at all where
+// the offsets descend (the numbering would outgrow the workspace).
+struct SplitMap {
+    Span span[kSplitSeqs];
+    int64_t first[kSplitSeqs + 1];
+    int bad;
+    __device__ __forceinline__ void build(const PreferenceArgs& a) {
+        const int n = 2 * a.n_pairs;
+        if (threadIdx.x == 0) bad = 0;
+        __syncthreads();
+        if (offsets_bad(a)) bad = 1;
+        __syncthreads();
+        if (threadIdx.x < n) {
+            span[threadIdx.x] = span_of(a, threadIdx.x);
+            if (bad) span[threadIdx.x].e = span[threadIdx.x].b;
+        }
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            // two sequences a lane, an inclusive scan over the lanes
+            const int l = threadIdx.x;
+            const int64_t c0 = 2 * l < n ? chunks_of(span[2 * l]) : 0;
+            const int64_t c1 = 2 * l + 1 < n ? chunks_of(span[2 * l + 1]) : 0;
+            int64_t v = c0 + c1;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+                if (l >= o) v += u;
+            }
+            first[2 * l] = v - c0 - c1;
+            first[2 * l + 1] = v - c1;
+            if (l == 31) first[kSplitSeqs] = v;
+        }
+        __syncthreads();
     }
+    // the sequence that holds chunk i (empty ones hold none)
+    __device__ __forceinline__ int seq_of(int64_t i) const {
+        int lo = 0, hi = kSplitSeqs - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (first[mid] <= i) lo = mid; else hi = mid - 1;
+        }
+        return lo;
+    }
+};
+
+__global__ void __launch_bounds__(kThreads) k_preference_chunks(const PreferenceArgs a) {
+    __shared__ SplitMap map;
+    ptx::grid_dependents_launch();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
+    map.build(a);
+    const int64_t total = map.first[kSplitSeqs];
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < total;
+         i += static_cast<int64_t>(gridDim.x) * kWarps) {
+        const int q = map.seq_of(i);
+        int n;
+        const double v = chunk_sum(a, map.span[q], i - map.first[q], &n);
+        if ((threadIdx.x & 31) == 0) {
+            a.chunk_sums[i] = v;
+            a.chunk_counts[i] = n;
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) k_preference_spread(const PreferenceArgs a) {
+    __shared__ SplitMap map;
+    __shared__ PairScratch scratch;
+    __shared__ float slope[2];
+    __shared__ bool last_here;
+    map.build(a);
+    ptx::grid_dependency_wait();
+    auto slopes_of = [&](int pair, bool write) {
+        const int q0 = static_cast<int>(chosen_of(a, pair)), q1 = static_cast<int>(rejected_of(a, pair));
+        const Span sp[2] = {map.span[q0], map.span[q1]};
+        const int64_t at[2] = {map.first[q0], map.first[q1]};
+        __syncthreads();  // the previous pair's slopes have been read
+        reduce_pair(a, pair, sp,
+                    [&](int side, int j) {
+                        double v = 0.0;
+                        const int64_t c = chunks_of(sp[side]);
+                        for (int64_t g = j; g < c; g += kSlots) v = __dadd_rn(v, a.chunk_sums[at[side] + g]);
+                        return v;
+                    },
+                    [&](int side, int j) {
+                        int n = 0;
+                        const int64_t c = chunks_of(sp[side]);
+                        for (int64_t g = j; g < c; g += kSlots) n += a.chunk_counts[at[side] + g];
+                        return n;
+                    },
+                    write, scratch, slope, nullptr);
+        __syncthreads();
+    };
+    // the pairs' own outputs
+    for (int pair = blockIdx.x; pair < a.n_pairs; pair += gridDim.x) slopes_of(pair, true);
+    if (a.grad) {
+        const int64_t total = map.first[kSplitSeqs];
+        const int64_t i0 = total * blockIdx.x / gridDim.x, i1 = total * (blockIdx.x + 1) / gridDim.x;
+        int have = -1;
+        for (int64_t i = i0; i < i1;) {
+            const int q = map.seq_of(i);
+            const int64_t next = map.first[q + 1] < i1 ? map.first[q + 1] : i1;
+            const int pair = a.halves ? q % a.n_pairs : q / 2;
+            const int side = a.halves ? q / a.n_pairs : q % 2;
+            if (pair != have) slopes_of(pair, false);
+            have = pair;
+            const float g = slope[side];
+            const int64_t b = map.span[q].b + (i - map.first[q]) * kChunk;
+            int64_t e = map.span[q].b + (next - map.first[q]) * kChunk;
+            if (e > map.span[q].e) e = map.span[q].e;
+#pragma unroll 4
+            for (int64_t t = b + threadIdx.x; t < e; t += kThreads)
+                a.grad[t] = (a.active && a.active[t] == 0) ? 0.0f : g;
+            i = next;
+        }
+        // tokens before the first and behind the last sequence
+        const int64_t who = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+        const int64_t all = static_cast<int64_t>(gridDim.x) * kThreads;
+        for (int64_t t = who, e = map.span[0].b; t < e; t += all) a.grad[t] = 0.0f;
+        for (int64_t t = map.span[2 * a.n_pairs - 1].e + who; t < a.T; t += all) a.grad[t] = 0.0f;
+    }
+    // the last CTA to come here adds up the pairs
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last_here = atomicAdd(a.ticket, 1) == static_cast<int>(gridDim.x) - 1;
+    __syncthreads();
+    if (!last_here) return;
+    __threadfence();
+    preference_finish(a, a.out_pair_loss, map.bad != 0, scratch.tmp[0]);
+}
+
+cudaError_t launch_clusters(const PreferenceArgs& a, int clusters, int size, int team, int alone, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.stream = stream;
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * size), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    const int64_t mean = a.n_pairs ? a.T / a.n_pairs : 0;  // tokens of a pair, about
-    if (a.T <= kPreferenceClusterTokens || a.n_pairs == 0) {
-        // teams so large that the cluster's CTAs all have a pair
-        int team = kCluster;
-        while (team > 1 && kCluster / team < a.n_pairs) team /= 2;
-        cfg.gridDim = dim3(kCluster, 1, 1);
-        attr[0].val.clusterDim.x = kCluster;
-        return cudaLaunchKernelEx(&cfg, k_preference, a, team, 1);
+    return cudaLaunchKernelEx(&cfg, k_preference, a, team, alone);
+}
+
+cudaError_t launch_after(void (*kernel)(PreferenceArgs), int blocks, const PreferenceArgs& a, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.stream = stream;
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+}  // namespace
+
+bool preference_split(int64_t T, int64_t n_pairs) {
+    return T > kPreferenceClusterTokens && 2 * n_pairs <= kSplitSeqs && n_pairs > 0;
+}
+
+int64_t preference_chunks(int64_t T, int64_t n_pairs) { return T / kChunk + 2 * n_pairs; }
+
+cudaError_t launch_preference_loss(const PreferenceArgs& a, int num_sms, cudaStream_t stream) {
+    if (a.n_pairs == 0) {
+        if (a.grad && a.T > 0) {
+            const cudaError_t e = cudaMemsetAsync(a.grad, 0, size_t(a.T) * sizeof(float), stream);
+            if (e != cudaSuccess) return e;
+        }
+        return launch_clusters(a, 1, 1, 1, 1, stream);
+    }
+    const int64_t mean = a.T / a.n_pairs;  // tokens of a pair, about
+    if (a.T <= kPreferenceClusterTokens && a.n_pairs <= kHeldPairs) {
+        // a CTA for every pair, and several where the pairs are long and few
+        int size = 1, team = 1;
+        while (size < kCluster && size < a.n_pairs) size *= 2;
+        while (size < kCluster && mean / team > kThreads * 8) {
+            size *= 2;
+            team *= 2;
+        }
+        return launch_clusters(a, 1, size, team, 1, stream);
+    }
+    if (preference_split(a.T, a.n_pairs)) {
+        const int64_t chunks = preference_chunks(a.T, a.n_pairs);
+        const int64_t need = (chunks + kWarps - 1) / kWarps;
+        const int most = num_sms * 3;
+        k_preference_chunks<<<static_cast<int>(need < most ? need : most), kThreads, 0, stream>>>(a);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        return launch_after(k_preference_spread, static_cast<int>(need < num_sms * 2 ? need : num_sms * 2), a, stream);
     }
     // CTAs per pair: enough to fill the device, and none with less than 4096 tokens
     int team = 1;
     while (team < kCluster && static_cast<int64_t>(a.n_pairs) * team < num_sms * 2 && mean / (2 * team) >= 4096) team *= 2;
     const int64_t most = static_cast<int64_t>(num_sms) * 16 / team;
-    const int64_t clusters = a.n_pairs < most ? a.n_pairs : most;
-    cfg.gridDim = dim3(static_cast<unsigned>(clusters * team), 1, 1);
-    attr[0].val.clusterDim.x = team;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, k_preference, a, team, 0);
+    const cudaError_t e = launch_clusters(a, static_cast<int>(a.n_pairs < most ? a.n_pairs : most), team, team, 0, stream);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(1, 1, 1);
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    return cudaLaunchKernelEx(&cfg, k_preference_final, a);
+    return launch_after(k_preference_final, 1, a, stream);
 }
 
 }  // namespace rlk

@@ -59,9 +59,16 @@ struct PreferenceArgs {
     float* out_pair_loss;     // [n_pairs]
     float* out_rewards;       // [2 * n_pairs], sequence order
     float* grad;              // [T] or nullptr
+    // workspace of the path over all chunks
+    int32_t* ticket;          // CTAs that are done
+    double* chunk_sums;
+    int32_t* chunk_counts;
     int32_t* status;
 };
-constexpr int64_t kPreferenceClusterTokens = 65536;  // largest batch that one cluster does alone
+constexpr int64_t kPreferenceClusterTokens = 32768;  // largest batch that one cluster does alone
+// Whether a batch takes the path over all chunks, and how many of them it has at most.
+bool preference_split(int64_t T, int64_t n_pairs);
+int64_t preference_chunks(int64_t T, int64_t n_pairs);
 cudaError_t launch_preference_loss(const PreferenceArgs& a, int num_sms, cudaStream_t stream);
 
 // Tensors of one launch: pointers and sizes travel by value in the kernel's parameters, so a

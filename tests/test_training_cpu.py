@@ -63,14 +63,15 @@ def test_policy_loss_refusals(L):
 
 def test_preference_loss_refusals(L):
     ok = dict(lp=0x1000, ref=0x2000, act=0x3000, off=0x4000, P=3, T=10, layout=0, kind=0, beta=0.1,
-              eps=0.0, margin=0.0, scale=1.0, loss=0x5000, pair=0x6000, rew=0x7000, grad=0x8000)
+              eps=0.0, margin=0.0, scale=1.0, loss=0x5000, pair=0x6000, rew=0x7000, grad=0x8000, ws=None,
+              wsb=0)
 
     def call(**kw):
         a = dict(ok, **kw)
         return L.rlk_preference_loss(a["lp"], a["ref"], a["act"], a["off"], a["P"], a["T"],
                                      a["layout"], a["kind"], a["beta"], a["eps"], a["margin"], 0,
-                                     a["scale"], a["loss"], a["pair"], a["rew"], a["grad"], None,
-                                     None)
+                                     a["scale"], a["loss"], a["pair"], a["rew"], a["grad"],
+                                     a["ws"], a["wsb"], None, None)
     for kw in (dict(lp=None), dict(off=None), dict(loss=None), dict(pair=None), dict(rew=None),
                dict(T=-1), dict(T=MAX_ROWS + 1), dict(P=-1), dict(P=(1 << 30) + 1), dict(beta=0.0),
                dict(beta=-1.0), dict(beta=math.inf), dict(beta=math.nan), dict(eps=-0.1),
@@ -79,8 +80,15 @@ def test_preference_loss_refusals(L):
         refused(call, INVALID, **kw)
     for kw in (dict(layout=2), dict(kind=3), dict(kind=-1)):
         refused(call, UNSUPPORTED, **kw)
-    for kw in (dict(lp=0x1001), dict(off=0x4002), dict(rew=0x7002)):
+    for kw in (dict(lp=0x1001), dict(off=0x4002), dict(rew=0x7002), dict(ws=0x10010)):
         refused(call, ALIGNMENT, **kw)
+    # few pairs of many tokens need a workspace
+    refused(call, INVALID, T=100000)
+    refused(call, WORKSPACE, T=100000, ws=0x10000, wsb=100)
+    assert L.rlk_preference_loss_workspace_size(100000, 3) >= 256 + 12 * (100000 // 256)
+    assert L.rlk_preference_loss_workspace_size(100000, 40) == 0
+    assert L.rlk_preference_loss_workspace_size(32768, 3) == 0
+    assert L.rlk_preference_loss_workspace_size(-1, 3) == 0
 
 
 def test_rmsnorm_backward_refusals(L):
