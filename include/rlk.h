@@ -426,8 +426,8 @@ rlk_status_t rlk_rmsnorm_backward(const void* grad_out, int grad_out_dtype, cons
  * A token takes part if its mask is nonzero and it lies in
  * [seq_offsets[0], seq_offsets[n_seqs]); any other token's inputs are not
  * used (they may be NaN) and its grad is 0.  Per-token terms are fp32; their
- * sums run over fixed ranges of 1024 tokens and then in fp64, so the results
- * are the same bits on every run.  T == 0 gives loss and stats 0.
+ * sums run over fixed ranges of 1024 tokens in fp32 and then as pairs of
+ * floats, so the results are the same bits on every run.  T == 0 gives loss and stats 0.
  *
  *   logprob, old_logprob  device, float [T]
  *   ref_logprob   device, float [T], or NULL (then kl_coef must be 0)
@@ -505,9 +505,9 @@ rlk_status_t rlk_preference_loss(const float* logprob, const float* ref_logprob,
  *   norm  = sqrt(sum of g^2 over all elements of all tensors)
  *   scale = max_norm / norm where norm is finite and above max_norm, else 1
  *   out   = RN(g * scale), rounded once to the tensor's type
- * Squares and the sums over each tensor's 16384-element chunks are fp32 (so
- * |g| above 1.8e19 makes the norm infinite and |g| below 1e-23 counts as 0),
- * the sum of the chunks' fp64; the order depends on the tensors' sizes and
+ * Squares and the sums over each tensor's 16384-element chunks are fp32, the
+ * chunks are added as pairs of floats (a norm above 1.8e19 becomes infinite
+ * and |g| below 1e-23 counts as 0); the order depends on the tensors' sizes and
  * types alone, not on their addresses.  A norm that is not finite leaves scale at 1 (the
  * gradients keep their values) and sets RLK_ERR_NONFINITE in *dev_status.
  *

@@ -471,7 +471,7 @@ PreferenceLayout preference_layout_of(int64_t T, int64_t n_pairs) {
     if (!rlk::preference_split(T, n_pairs)) return l;
     const size_t chunks = size_t(rlk::preference_chunks(T, n_pairs));
     l.sums = 256;
-    l.counts = l.sums + align256(chunks * sizeof(double));
+    l.counts = l.sums + align256(chunks * sizeof(float2));
     l.total = l.counts + align256(chunks * sizeof(int32_t));
     return l;
 }
@@ -511,7 +511,7 @@ ClipPlan clip_plan_of(const int64_t* numels, int64_t n) {
 }
 
 size_t clip_workspace_of(const ClipPlan& p) {
-    return p.one_launch() ? 0 : align256(size_t(p.slots) * sizeof(double));
+    return p.one_launch() ? 0 : align256(size_t(p.slots) * sizeof(float2));
 }
 
 rlk_status_t clip_checks(const void* const* grads, const int64_t* numels, const int32_t* dtypes,
@@ -596,7 +596,7 @@ cudaError_t for_each_clip_table(const void* const* grads, void* const* outs, con
 // The norm, and with o.scale the scaled tensors.
 cudaError_t run_clip(const void* const* grads, void* const* outs, const int64_t* numels,
                      const int32_t* dtypes, int64_t n, const ClipPlan& plan, const rlk::ClipOut& o,
-                     double* slots, cudaStream_t stream) {
+                     float2* slots, cudaStream_t stream) {
     if (plan.one_launch())
         return for_each_clip_table<rlk::ClipTableSmall>(
             grads, outs, numels, dtypes, n,
@@ -1115,6 +1115,7 @@ rlk_status_t rlk_policy_loss(const float* logprob, const float* old_logprob,
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.ticket = reinterpret_cast<int32_t*>(ws + l.ticket);
     a.counts = reinterpret_cast<int32_t*>(ws + l.counts);
+    a.weights = reinterpret_cast<float*>(ws + l.counts);
     a.parts = reinterpret_cast<float4*>(ws + l.parts);
     a.out_loss = out_loss;
     a.out_stats = out_stats;
@@ -1182,7 +1183,7 @@ rlk_status_t rlk_preference_loss(const float* logprob, const float* ref_logprob,
     a.grad = grad_logprob;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.ticket = reinterpret_cast<int32_t*>(ws + l.ticket);
-    a.chunk_sums = reinterpret_cast<double*>(ws + l.sums);
+    a.chunk_sums = reinterpret_cast<float2*>(ws + l.sums);
     a.chunk_counts = reinterpret_cast<int32_t*>(ws + l.counts);
     a.status = dev_status;
     return rlk::launch_preference_loss(a, dev->sm_count, reinterpret_cast<cudaStream_t>(stream)) ==
@@ -1211,7 +1212,7 @@ rlk_status_t rlk_grad_norm(const void* const* grads, const int64_t* numels,
     if ((s = device_check(&dev)) != RLK_OK) return s;
     const rlk::ClipOut o = {out_norm, nullptr, dev_status, 0.0};
     return run_clip(grads, nullptr, numels, dtypes, n_tensors, plan, o,
-                    static_cast<double*>(workspace), reinterpret_cast<cudaStream_t>(stream)) ==
+                    static_cast<float2*>(workspace), reinterpret_cast<cudaStream_t>(stream)) ==
                    cudaSuccess
                ? RLK_OK
                : RLK_ERR_CUDA;
@@ -1237,7 +1238,7 @@ rlk_status_t rlk_grad_clip(const void* const* grads, void* const* outs, const in
     if ((s = device_check(&dev)) != RLK_OK) return s;
     const rlk::ClipOut o = {out_norm, out_scale, dev_status, max_norm};
     return run_clip(grads, outs, numels, dtypes, n_tensors, plan, o,
-                    static_cast<double*>(workspace), reinterpret_cast<cudaStream_t>(stream)) ==
+                    static_cast<float2*>(workspace), reinterpret_cast<cudaStream_t>(stream)) ==
                    cudaSuccess
                ? RLK_OK
                : RLK_ERR_CUDA;

@@ -8,8 +8,8 @@
 // into chunks of 16384 elements counted from its first.  With E elements in
 // 16 bytes, class i mod 256 E of a chunk's elements is summed ascending in
 // fp32, the classes by a fixed tree in fp32; chunk c of a launch goes to slot
-// c mod 912 in ascending order in fp64, and the slots are added by a fixed
-// tree in fp64.  An element's class does not depend on its address: 16-byte
+// c mod 912 in ascending order and the slots are added by a fixed tree, both
+// as pairs of floats.  An element's class does not depend on its address: 16-byte
 // loads take whole aligned vectors wherever the tensor starts, and the thread
 // that has a vector owns its elements' classes; only where the classes then
 // lie in the thread's registers changes, and an exchange through shared
@@ -205,41 +205,44 @@ __device__ __forceinline__ void table_scale(const Table& t, int c, float scale) 
     else chunk_scale<RLK_DTYPE_F16>(t.e[k], at, len, scale);
 }
 
-// sqrt of the slots' sum, by a CTA of 256 threads; every thread gets it.
-__device__ __forceinline__ double norm_of(const double* slots, int n, double* smem) {
-    double v = 0.0;
-    for (int i = threadIdx.x; i < n; i += kThreads) v = __dadd_rn(v, slots[i]);
+// The slots' sum by a CTA of 256 threads, and from it (norm, scale); every thread gets them.
+__device__ __forceinline__ float2 norm_and_scale(const float2* slots, int n, double max_norm, float2* smem) {
+    __shared__ float2 result;
+    float2 v = pair_of(0.0f);
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += kThreads) v = pair_add(v, slots[i]);
     v = warp_sum(v);
     if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = 0.0;
-    for (int i = 0; i < kThreads / 32; ++i) v = __dadd_rn(v, smem[i]);
-    return sqrt(v);
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < kThreads / 32; ++i) v = pair_add(v, smem[i]);
+        const float norm = __fsqrt_rn(__fadd_rn(v.x, v.y));
+        const bool shrink = norm < CUDART_INF_F && static_cast<double>(norm) > max_norm;
+        result = make_float2(norm, shrink ? __fdiv_rn(static_cast<float>(max_norm), norm) : 1.0f);
+    }
+    __syncthreads();
+    return result;
 }
 
-__device__ __forceinline__ float scale_of(double norm, double max_norm) {
-    return norm < static_cast<double>(CUDART_INF_F) && norm > max_norm ? static_cast<float>(max_norm / norm) : 1.0f;
-}
-
-__device__ __forceinline__ void write_norm(const ClipOut& o, double norm, float scale) {
-    *o.norm = static_cast<float>(norm);
-    if (o.scale) *o.scale = scale;
-    if (!(norm < static_cast<double>(CUDART_INF_F))) report_status(o.status, RLK_ERR_NONFINITE);
+__device__ __forceinline__ void write_norm(const ClipOut& o, float2 r) {
+    *o.norm = r.x;
+    if (o.scale) *o.scale = r.y;
+    if (!(r.x < CUDART_INF_F)) report_status(o.status, RLK_ERR_NONFINITE);
 }
 
 // ---------------------------------------------------------------- one launch
 __global__ void __launch_bounds__(kThreads) k_clip_cluster(const __grid_constant__ ClipTableSmall t,
                                                            const ClipOut o) {
     __shared__ ClipShared sm;
-    __shared__ double slots[kClipClusterChunks];
-    __shared__ double tmp[kThreads / 32];
+    __shared__ float2 slots[kClipClusterChunks];
+    __shared__ float2 tmp[kThreads / 32];
     cg::cluster_group cluster = cg::this_cluster();
     cluster.barrier_arrive();
     const int rank = static_cast<int>(cluster.block_rank());
     const int total = t.first[t.count];
     bool started = false;
     for (int c = rank; c < total; c += kClipCluster) {
-        const double s = static_cast<double>(table_sumsq(t, c, sm));
+        const float2 s = pair_of(table_sumsq(t, c, sm));
         if (!started) cluster.barrier_wait();  // every CTA has started: its shared memory may be written
         started = true;
         if (threadIdx.x == 0) {
@@ -248,38 +251,39 @@ __global__ void __launch_bounds__(kThreads) k_clip_cluster(const __grid_constant
     }
     if (!started) cluster.barrier_wait();
     cluster.sync();
-    const double norm = norm_of(slots, total, tmp);
-    const float scale = scale_of(norm, o.max_norm);
-    if (rank == 0 && threadIdx.x == 0) write_norm(o, norm, scale);
+    const float2 r = norm_and_scale(slots, total, o.max_norm, tmp);
+    if (rank == 0 && threadIdx.x == 0) write_norm(o, r);
     if (!o.scale) return;
-    for (int c = rank; c < total; c += kClipCluster) table_scale(t, c, scale);
+    for (int c = rank; c < total; c += kClipCluster) table_scale(t, c, r.y);
 }
 
 // ---------------------------------------------------------------- two launches
-__global__ void __launch_bounds__(kThreads) k_grad_sumsq(const __grid_constant__ ClipTable t, double* slots) {
+__global__ void __launch_bounds__(kThreads) k_grad_sumsq(const __grid_constant__ ClipTable t, float2* slots) {
     __shared__ ClipShared sm;
     ptx::grid_dependents_launch();
     const int total = t.first[t.count];
-    double sum = 0.0;
-    for (int c = blockIdx.x; c < total; c += kClipSlots)
-        sum = __dadd_rn(sum, static_cast<double>(table_sumsq(t, c, sm)));
+    float2 sum = pair_of(0.0f);
+    for (int c = blockIdx.x; c < total; c += kClipSlots) {
+        const float s = table_sumsq(t, c, sm);
+        if (threadIdx.x == 0) sum = pair_add(sum, pair_of(s));
+    }
     if (threadIdx.x == 0) slots[blockIdx.x] = sum;
 }
 
-__global__ void __launch_bounds__(kThreads) k_grad_norm(const double* slots, int n, const ClipOut o) {
-    __shared__ double tmp[kThreads / 32];
+__global__ void __launch_bounds__(kThreads) k_grad_norm(const float2* slots, int n, const ClipOut o) {
+    __shared__ float2 tmp[kThreads / 32];
     ptx::grid_dependency_wait();
-    const double norm = norm_of(slots, n, tmp);
-    if (threadIdx.x == 0) write_norm(o, norm, scale_of(norm, o.max_norm));
+    const float2 r = norm_and_scale(slots, n, o.max_norm, tmp);
+    if (threadIdx.x == 0) write_norm(o, r);
 }
 
-__global__ void __launch_bounds__(kThreads) k_grad_scale(const __grid_constant__ ClipTable t, const double* slots,
+__global__ void __launch_bounds__(kThreads) k_grad_scale(const __grid_constant__ ClipTable t, const float2* slots,
                                                          int n, const ClipOut o, int write) {
-    __shared__ double tmp[kThreads / 32];
+    __shared__ float2 tmp[kThreads / 32];
     ptx::grid_dependency_wait();
-    const double norm = norm_of(slots, n, tmp);
-    const float scale = scale_of(norm, o.max_norm);
-    if (write && blockIdx.x == 0 && threadIdx.x == 0) write_norm(o, norm, scale);
+    const float2 r = norm_and_scale(slots, n, o.max_norm, tmp);
+    const float scale = r.y;
+    if (write && blockIdx.x == 0 && threadIdx.x == 0) write_norm(o, r);
     for (int c = t.first[t.count] - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) table_scale(t, c, scale);
 }
 
@@ -314,17 +318,17 @@ cudaError_t launch_clip_cluster(const ClipTableSmall& t, const ClipOut& o, cudaS
     return cudaLaunchKernelEx(&cfg, k_clip_cluster, t, o);
 }
 
-cudaError_t launch_grad_sumsq(const ClipTable& t, double* slots, cudaStream_t stream) {
+cudaError_t launch_grad_sumsq(const ClipTable& t, float2* slots, cudaStream_t stream) {
     const int total = t.first[t.count];
     k_grad_sumsq<<<total < kClipSlots ? total : kClipSlots, kThreads, 0, stream>>>(t, slots);
     return cudaGetLastError();
 }
 
-cudaError_t launch_grad_norm(const double* slots, int n, const ClipOut& o, cudaStream_t stream) {
+cudaError_t launch_grad_norm(const float2* slots, int n, const ClipOut& o, cudaStream_t stream) {
     return launch_after(k_grad_norm, 1, stream, slots, n, o);
 }
 
-cudaError_t launch_grad_scale(const ClipTable& t, const double* slots, int n, const ClipOut& o, bool write,
+cudaError_t launch_grad_scale(const ClipTable& t, const float2* slots, int n, const ClipOut& o, bool write,
                               cudaStream_t stream) {
     const int total = t.first[t.count];
     return launch_after(k_grad_scale, total < kClipSlots ? total : kClipSlots, stream, t, slots, n, o, int(write));

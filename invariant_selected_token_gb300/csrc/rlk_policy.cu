@@ -46,7 +46,7 @@ __device__ __forceinline__ Bounds bounds_of(const PolicyArgs& a) {
     return b;
 }
 
-// [b, e) cut to the batch
+// Active tokens of [b, e), cut to the batch, by `threads` threads.
 __device__ __forceinline__ int count_active(const uint8_t* active, int64_t b, int64_t e, int T,
                                             int thread, int threads) {
     b = b < 0 ? 0 : b;
@@ -57,6 +57,7 @@ __device__ __forceinline__ int count_active(const uint8_t* active, int64_t b, in
     const int64_t body = b + lead < e ? b + lead : e;
     const int64_t words = (e - body) / 16;
     for (int64_t t = b + thread; t < body; t += threads) n += active[t] != 0;
+#pragma unroll 4
     for (int64_t i = thread; i < words; i += threads) {
         const uint4 v = reinterpret_cast<const uint4*>(active + body)[i];
         n += (__popc(__vcmpne4(v.x, 0u)) + __popc(__vcmpne4(v.y, 0u)) +
@@ -146,30 +147,23 @@ struct WarpTokens {
     }
 };
 
-// Gradients of a warp's tokens out; its sums of the four stats, on every lane.  seq_of(i) is
-// token i's sequence, count_of(s) and adv_of(s) that one's active tokens and advantage.
-template <typename SeqOf, typename CountOf, typename AdvOf>
-__device__ __forceinline__ float4 policy_warp(const PolicyArgs& a, const WarpTokens& k, float w_all, SeqOf seq_of,
-                                              CountOf count_of, AdvOf adv_of) {
+// Gradients of a warp's tokens out; its sums of the four stats, on every lane.  Every token is
+// worked on, the inactive ones with zeros for their values, so that the tokens' chains of
+// operations overlap; what an inactive one gives is dropped.
+__device__ __forceinline__ float4 policy_warp(const PolicyArgs& a, const WarpTokens& k, const float (&w)[kPer]) {
     float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const float scale = static_cast<float>(a.scale);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        float g = 0.0f;
-        if (k.on[i]) {
-            float w = w_all, adv = k.adv[i];
-            if (a.reduction == RLK_REDUCE_SEQ_MEAN) {
-                const int n = count_of(seq_of(i));
-                w = __fdiv_rn(1.0f, __fmul_rn(static_cast<float>(a.n_seqs), static_cast<float>(n > 1 ? n : 1)));
-            }
-            if (a.adv_per_seq) adv = adv_of(seq_of(i));
-            const TokenTerms o = token_terms(a, k.lp[i], k.old[i], k.ref[i], adv);
-            sum.x = __fmaf_rn(w, o.policy, sum.x);
-            sum.y = __fmaf_rn(w, o.kl, sum.y);
-            sum.z = __fmaf_rn(w, o.clipped, sum.z);
-            sum.w = __fmaf_rn(w, o.neg_d, sum.w);
-            g = __fmul_rn(__fmul_rn(scale, w), o.slope);
-        }
+        const bool on = k.on[i];
+        const TokenTerms o = token_terms(a, on ? k.lp[i] : 0.0f, on ? k.old[i] : 0.0f, on ? k.ref[i] : 0.0f,
+                                         on ? k.adv[i] : 0.0f);
+        const float wi = on ? w[i] : 0.0f;
+        sum.x = __fmaf_rn(wi, o.policy, sum.x);
+        sum.y = __fmaf_rn(wi, o.kl, sum.y);
+        sum.z = __fmaf_rn(wi, o.clipped, sum.z);
+        sum.w = __fmaf_rn(wi, o.neg_d, sum.w);
+        const float g = on ? __fmul_rn(__fmul_rn(scale, wi), o.slope) : 0.0f;
         if (a.grad && k.token(i) < a.T) a.grad[k.token(i)] = g;
     }
 #pragma unroll
@@ -190,17 +184,22 @@ __device__ __forceinline__ float unit_sum(const float4* warps, int k) {
     return v;
 }
 
+// Weight of the tokens of a sequence with n active ones.
+__device__ __forceinline__ float seq_weight(const PolicyArgs& a, int n) {
+    return __fdiv_rn(1.0f, __fmul_rn(static_cast<float>(a.n_seqs), static_cast<float>(n > 1 ? n : 1)));
+}
 __device__ __forceinline__ float token_weight(const PolicyArgs& a, int n) {
     return a.reduction == RLK_REDUCE_TOKEN_MEAN ? __fdiv_rn(1.0f, static_cast<float>(n > 1 ? n : 1)) : 1.0f;
 }
 
 // The units' sums are added like this: slot j takes units j, j + 256, ... in ascending order, the
-// 32 slots of a warp are added by a shuffle tree, the 8 warps' sums in order, all in fp64.
-__device__ __forceinline__ void write_stat(const PolicyArgs& a, int k, double v, bool bad) {
-    a.out_stats[k] = bad ? CUDART_NAN_F : static_cast<float>(v);
+// 32 slots of a warp are added by a shuffle tree, the 8 warps' sums in order, all as pairs.
+__device__ __forceinline__ void write_stat(const PolicyArgs& a, int k, float2 v, bool bad) {
+    a.out_stats[k] = bad ? CUDART_NAN_F : __fadd_rn(v.x, v.y);
 }
-__device__ __forceinline__ void write_loss(const PolicyArgs& a, double policy, double kl, bool bad) {
-    *a.out_loss = bad ? CUDART_NAN_F : static_cast<float>(a.scale * (policy + a.kl_coef64 * kl));
+__device__ __forceinline__ void write_loss(const PolicyArgs& a, float2 policy, float2 kl, bool bad) {
+    const double sum = __fma_rn(a.kl_coef64, pair_value(kl), pair_value(policy));
+    *a.out_loss = bad ? CUDART_NAN_F : static_cast<float>(__dmul_rn(a.scale, sum));
     if (bad) report_status(a.status, RLK_ERR_INVALID_ARG);
 }
 
@@ -226,7 +225,7 @@ __global__ void __launch_bounds__(kGroups * kThreads) k_policy_one(const PolicyA
     __shared__ int32_t offsets[kLaunchSeqs + 1];
     __shared__ float adv[kLaunchSeqs];
     __shared__ int counts[kLaunchSeqs];
-    __shared__ int totals[kLaunchSeqs];
+    __shared__ float weights[kLaunchSeqs];
     __shared__ float4 parts[32];           // the first CTA's are used
     __shared__ float4 warps[kGroups][kThreads / 32];
     __shared__ int active_here;
@@ -281,33 +280,40 @@ __global__ void __launch_bounds__(kGroups * kThreads) k_policy_one(const PolicyA
                 atomicAdd(&counts[seq[i]], 1);
             }
         }
-        if constexpr (kCtas > 1) {
-            cg::cluster_group cluster = cg::this_cluster();
-            cluster.sync();
-            if (by_mean) {
-                for (int s = threadIdx.x; s < a.n_seqs; s += kAll) {
-                    int n = 0;
-#pragma unroll
-                    for (int c = 0; c < kCtas; ++c) n += cluster.map_shared_rank(counts, c)[s];
-                    totals[s] = n;
-                }
-                __syncthreads();
-            } else {
-                n_all = __reduce_add_sync(0xffffffffu, lane < kCtas ? *cluster.map_shared_rank(&active_here, lane % kCtas) : 0);
-            }
-        } else {
-            __syncthreads();
-            n_all = active_here;
-        }
-    } else if constexpr (kCtas > 1) {
-        cg::this_cluster().sync();  // every CTA has started: its shared memory may be written
     }
-    const float4 s = policy_warp(
-        a, k, token_weight(a, n_all), [&](int i) { return seq[i]; },
-        [&](int q) {
-            return masked ? (kCtas > 1 ? totals[q] : counts[q]) : (a.offsets ? offsets[q + 1] - offsets[q] : a.T);
-        },
-        [&](int q) { return adv[q]; });
+    if constexpr (kCtas > 1) {
+        // the counts are complete, and every CTA has started: its shared memory may be written
+        cg::this_cluster().sync();
+        if (masked && a.reduction == RLK_REDUCE_TOKEN_MEAN)
+            n_all = __reduce_add_sync(
+                0xffffffffu, lane < kCtas ? *cg::this_cluster().map_shared_rank(&active_here, lane % kCtas) : 0);
+    } else {
+        __syncthreads();
+        if (masked && a.reduction == RLK_REDUCE_TOKEN_MEAN) n_all = active_here;
+    }
+    if (by_mean) {
+        for (int s = threadIdx.x; s < a.n_seqs; s += kAll) {
+            int n = a.offsets ? offsets[s + 1] - offsets[s] : a.T;
+            if (masked) {
+                n = counts[s];
+                if constexpr (kCtas > 1) {
+                    n = 0;
+#pragma unroll
+                    for (int c = 0; c < kCtas; ++c) n += cg::this_cluster().map_shared_rank(counts, c)[s];
+                }
+            }
+            weights[s] = seq_weight(a, n);
+        }
+        __syncthreads();
+    }
+    float w[kPer];
+    const float w_all = token_weight(a, n_all);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        w[i] = by_mean ? weights[seq[i]] : w_all;
+        if (a.adv_per_seq) k.adv[i] = adv[seq[i]];
+    }
+    const float4 s = policy_warp(a, k, w);
     if (lane == 0) warps[group][warp] = s;
     __syncthreads();
     float4* all_parts = parts;
@@ -321,93 +327,100 @@ __global__ void __launch_bounds__(kGroups * kThreads) k_policy_one(const PolicyA
     // Warp 0 forms the loss and the two stats in it, warps 1 and 2 the others.
     const float* p = reinterpret_cast<const float*>(parts + lane);
     const bool have = lane < kCtas * kGroups;
-    const int w = threadIdx.x >> 5;
-    const double v = warp_sum(have ? static_cast<double>(p[w == 0 ? 0 : w + 1]) : 0.0);
-    if (w == 0) {
-        const double kl = warp_sum(have ? static_cast<double>(p[1]) : 0.0);
+    const int which = threadIdx.x >> 5;
+    const float2 v = warp_sum(pair_of(have ? p[which == 0 ? 0 : which + 1] : 0.0f));
+    if (which == 0) {
+        const float2 kl = warp_sum(pair_of(have ? p[1] : 0.0f));
         if (lane == 0) {
             write_loss(a, v, kl, bad);
             write_stat(a, 0, v, bad);
             write_stat(a, 1, kl, bad);
         }
     } else if (lane == 0) {
-        write_stat(a, w + 1, v, bad);
+        write_stat(a, which + 1, v, bad);
     }
 }
 
 // ---------------------------------------------------------------- two launches
-// Active tokens of each sequence (seq_mean) or of each block's share of all sequences
+// Each sequence's weight (seq_mean), or the active tokens in each block's share of the sequences
 // (token_mean); and the main kernel's ticket set to 0.
-__global__ void __launch_bounds__(kThreads) k_policy_count(const PolicyArgs a) {
-    __shared__ int smem[kThreads / 32];
+__global__ void __launch_bounds__(1024) k_policy_count(const PolicyArgs a) {
+    __shared__ int smem[32];
+    const int threads = blockDim.x;
     ptx::grid_dependents_launch();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
-    if (!a.active || a.reduction == RLK_REDUCE_SUM) return;
     const bool per_seq = a.reduction == RLK_REDUCE_SEQ_MEAN;
+    if (a.reduction == RLK_REDUCE_SUM || (!per_seq && !a.active)) return;
     const int rows = per_seq ? a.n_seqs : kPolicyCountBlocks;
     for (int s = blockIdx.x; s < rows; s += gridDim.x) {
-        int n;
+        int64_t b = 0, e = a.T;
         if (per_seq) {
-            n = count_active(a.active, a.offsets ? a.offsets[s] : 0, a.offsets ? a.offsets[s + 1] : a.T,
-                             a.T, threadIdx.x, kThreads);
+            if (a.offsets) {
+                b = a.offsets[s];
+                e = a.offsets[s + 1];
+            }
         } else {
             const Bounds bd = bounds_of(a);
             const int64_t len = static_cast<int64_t>(bd.last) - bd.first;
             const int64_t share = ((len + kPolicyCountBlocks - 1) / kPolicyCountBlocks + 15) / 16 * 16;
-            const int64_t b = bd.first + s * share, e = b + share;
-            n = count_active(a.active, b, e < bd.last ? e : bd.last, a.T, threadIdx.x, kThreads);
+            b = bd.first + s * share;
+            e = b + share < bd.last ? b + share : bd.last;
         }
-        n = __reduce_add_sync(0xffffffffu, n);
-        if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = n;
-        __syncthreads();
+        int n = static_cast<int>(e - b);
+        if (a.active) {
+            n = __reduce_add_sync(0xffffffffu, count_active(a.active, b, e, a.T, threadIdx.x, threads));
+            if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = n;
+            __syncthreads();
+            n = 0;
+            for (int i = 0; i < threads / 32; ++i) n += smem[i];
+            __syncthreads();
+        }
         if (threadIdx.x == 0) {
-            for (int i = 1; i < kThreads / 32; ++i) n += smem[i];
-            a.counts[s] = n;
+            if (per_seq) a.weights[s] = seq_weight(a, n);
+            else a.counts[s] = n;
         }
-        __syncthreads();
     }
 }
 
-__global__ void __launch_bounds__(kThreads) k_policy_main(const PolicyArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) k_policy_main(const PolicyArgs a) {
     __shared__ float4 warps[kThreads / 32];
-    __shared__ double finish[kThreads / 32][4];
-    __shared__ int total;
+    __shared__ float2 finish[kThreads / 32][4];
     __shared__ bool last_here;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t units = (static_cast<int64_t>(a.T) + kPolicyUnit - 1) / kPolicyUnit;
     WarpTokens k;
     k.load(a, blockIdx.x, warp);
     const Bounds bd = bounds_of(a);
-    if (threadIdx.x == 0) total = 0;
+    const bool by_mean = a.reduction == RLK_REDUCE_SEQ_MEAN;
+    const bool by_seq = a.offsets && (a.adv_per_seq || by_mean);
     ptx::grid_dependency_wait();
-    __syncthreads();
     int n_all = bd.last - bd.first;
     if (a.active && a.reduction == RLK_REDUCE_TOKEN_MEAN) {
-        const int n = __reduce_add_sync(0xffffffffu, a.counts[threadIdx.x]);
-        if (lane == 0) atomicAdd(&total, n);
-        __syncthreads();
-        n_all = total;
+        static_assert(kPolicyCountBlocks == 256, "two int4 a lane");
+        const int4 c0 = reinterpret_cast<const int4*>(a.counts)[lane];
+        const int4 c1 = reinterpret_cast<const int4*>(a.counts)[lane + 32];
+        n_all = __reduce_add_sync(0xffffffffu, c0.x + c0.y + c0.z + c0.w + c1.x + c1.y + c1.z + c1.w);
     }
     const float w_all = token_weight(a, n_all);
-    const bool by_seq = a.offsets && (a.adv_per_seq || a.reduction == RLK_REDUCE_SEQ_MEAN);
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         if (u != blockIdx.x) k.load(a, u, warp);
         k.cut(bd);
-        int seq[kPer] = {};
+        float w[kPer];
+        int lo = 0, hi = 0;
         if (by_seq && k.t0 < a.T) {
             const int64_t tl = k.t0 + kPer * 32 - 1;
-            const int lo = warp_find_seq(a.offsets, a.n_seqs, static_cast<int>(k.t0));
-            const int hi = warp_find_seq(a.offsets, a.n_seqs, static_cast<int>(tl < a.T ? tl : a.T - 1));
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                seq[i] = hi > lo && k.on[i] ? find_seq(a.offsets, lo, hi, static_cast<int>(k.token(i))) : lo;
+            lo = warp_find_seq(a.offsets, a.n_seqs, static_cast<int>(k.t0));
+            hi = warp_find_seq(a.offsets, a.n_seqs, static_cast<int>(tl < a.T ? tl : a.T - 1));
         }
-        const float4 s = policy_warp(
-            a, k, w_all, [&](int i) { return seq[i]; },
-            [&](int q) {
-                return a.active ? a.counts[q] : (a.offsets ? a.offsets[q + 1] - a.offsets[q] : a.T);
-            },
-            [&](int q) { return a.advantages[q]; });
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            w[i] = w_all;
+            if (!k.on[i]) continue;
+            const int s = hi > lo ? find_seq(a.offsets, lo, hi, static_cast<int>(k.token(i))) : lo;
+            if (by_mean) w[i] = a.weights[s];
+            if (a.adv_per_seq) k.adv[i] = a.advantages[s];
+        }
+        const float4 s = policy_warp(a, k, w);
         if (lane == 0) warps[warp] = s;
         __syncthreads();
         if (threadIdx.x < 4) reinterpret_cast<float*>(a.parts + u)[threadIdx.x] = unit_sum(warps, threadIdx.x);
@@ -428,29 +441,26 @@ __global__ void __launch_bounds__(kThreads) k_policy_main(const PolicyArgs a) {
         }
     }
     bad = __syncthreads_or(bad);
-    double v[4] = {0.0, 0.0, 0.0, 0.0};
+    float2 v[4] = {};
 #pragma unroll 4
     for (int64_t u = threadIdx.x; u < units; u += kThreads) {
         const float4 p = a.parts[u];
-        v[0] += static_cast<double>(p.x);
-        v[1] += static_cast<double>(p.y);
-        v[2] += static_cast<double>(p.z);
-        v[3] += static_cast<double>(p.w);
+        v[0] = pair_add(v[0], pair_of(p.x));
+        v[1] = pair_add(v[1], pair_of(p.y));
+        v[2] = pair_add(v[2], pair_of(p.z));
+        v[3] = pair_add(v[3], pair_of(p.w));
     }
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] = __dadd_rn(v[c], __shfl_xor_sync(0xffffffffu, v[c], o));
-    }
-    if (lane == 0) {
-        for (int c = 0; c < 4; ++c) finish[warp][c] = v[c];
+    for (int c = 0; c < 4; ++c) {
+        v[c] = warp_sum(v[c]);
+        if (lane == 0) finish[warp][c] = v[c];
     }
     __syncthreads();
     if (threadIdx.x < 4) {
-        double s = finish[0][threadIdx.x];
-        for (int i = 1; i < kThreads / 32; ++i) s = __dadd_rn(s, finish[i][threadIdx.x]);
+        float2 s = finish[0][threadIdx.x];
+        for (int i = 1; i < kThreads / 32; ++i) s = pair_add(s, finish[i][threadIdx.x]);
         write_stat(a, threadIdx.x, s, bad);
-        const double kl = __shfl_sync(0xfu, s, 1);
+        const float2 kl = make_float2(__shfl_sync(0xfu, s.x, 1), __shfl_sync(0xfu, s.y, 1));
         if (threadIdx.x == 0) write_loss(a, s, kl, bad);
     }
 }
@@ -481,18 +491,22 @@ cudaError_t launch_policy_loss(const PolicyArgs& a, int num_sms, cudaStream_t st
     if (policy_one_launch(a.T, a.n_seqs))
         return a.T <= kGroups * kPolicyUnit ? launch_one<1>(a, stream) : launch_one<kCluster>(a, stream);
     int rows = 1;
-    if (a.active && a.reduction != RLK_REDUCE_SUM)
-        rows = a.reduction == RLK_REDUCE_SEQ_MEAN ? a.n_seqs : kPolicyCountBlocks;
+    if (a.reduction == RLK_REDUCE_SEQ_MEAN) rows = a.n_seqs;
+    else if (a.active && a.reduction == RLK_REDUCE_TOKEN_MEAN) rows = kPolicyCountBlocks;
     const int most = num_sms * 8;
     if (rows > most) rows = most;
-    k_policy_count<<<rows > 0 ? rows : 1, kThreads, 0, stream>>>(a);
+    // a few long sequences want many threads each
+    const int threads = a.reduction == RLK_REDUCE_SEQ_MEAN && a.T / (a.n_seqs > 0 ? a.n_seqs : 1) > 16384 ? 1024 : kThreads;
+    k_policy_count<<<rows > 0 ? rows : 1, threads, 0, stream>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int64_t units = (static_cast<int64_t>(a.T) + kPolicyUnit - 1) / kPolicyUnit;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.stream = stream;
-    cfg.gridDim = dim3(static_cast<unsigned>(units < most ? (units > 0 ? units : 1) : most), 1, 1);
+    // a CTA per unit, as far as the ticket and the weights' loads stay small against the work
+    const int64_t ctas = units < 4 * most ? units : 4 * most;
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas > 0 ? ctas : 1), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

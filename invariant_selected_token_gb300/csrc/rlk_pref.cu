@@ -11,9 +11,9 @@
 //
 // Order of a sequence's sum, the same wherever the sequence lies in the batch
 // and however many CTAs share it: tokens are counted from its first; a warp
-// sums chunks of 256 of them (a lane takes every 32nd, compensated in fp32,
-// then a shuffle tree in fp64); chunk g is added to slot g mod 1024 in
-// ascending order, and the slots are added by a fixed tree in fp64.
+// sums chunks of 256 of them (a lane takes every 32nd, then a shuffle tree);
+// chunk g is added to slot g mod 1024 in ascending order, and the slots are
+// added by a fixed tree.  All sums are pairs of floats.
 //
 // Batches of up to kPreferenceClusterTokens tokens run as one cluster in one
 // launch: a pair is the work of a team of 1, 2, 4 or 8 of its CTAs, which
@@ -54,51 +54,59 @@ __device__ __forceinline__ Span span_of(const PreferenceArgs& a, int64_t q) {
     return s;
 }
 
-// A pair's loss, rewards and slopes from its two sums and counts, by one thread.
+// A pair's loss, rewards and slopes from its two sums and counts, by one thread.  What cancels
+// (the two sums, z, the distance from 1 / (2 beta)) is formed in fp64, the rest in fp32.
 __device__ __forceinline__ void pair_terms(const PreferenceArgs& a, int pair, int64_t q0, int64_t q1,
-                                           double m0, double m1, int n0, int n1, bool write,
+                                           float2 s0, float2 s1, int n0, int n1, bool write,
                                            float* slope, float* held_loss) {
-    double inv0 = 1.0, inv1 = 1.0;
+    double m0 = pair_value(s0), m1 = pair_value(s1);
+    float inv0 = 1.0f, inv1 = 1.0f;
     if (a.length_normalize) {
-        inv0 = 1.0 / (n0 > 1 ? n0 : 1);
-        inv1 = 1.0 / (n1 > 1 ? n1 : 1);
-        m0 *= inv0;
-        m1 *= inv1;
+        const double c0 = n0 > 1 ? n0 : 1, c1 = n1 > 1 ? n1 : 1;
+        inv0 = __fdiv_rn(1.0f, static_cast<float>(c0));
+        inv1 = __fdiv_rn(1.0f, static_cast<float>(c1));
+        // one Newton step takes the reciprocals from 2^-24 to 2^-47
+        const double r0 = inv0, r1 = inv1;
+        m0 = __dmul_rn(m0, __fma_rn(r0, __fma_rn(-c0, r0, 1.0), r0));
+        m1 = __dmul_rn(m1, __fma_rn(r1, __fma_rn(-c1, r1, 1.0), r1));
     }
-    const double h = m0 - m1;
-    double loss, dh;
+    const double h = __dsub_rn(m0, m1);
+    const float beta = static_cast<float>(a.beta);
+    float loss, dh;
     if (a.kind == RLK_PREF_IPO) {
-        const double off = h - a.half_over_beta;
-        loss = off * off;
-        dh = 2.0 * off;
+        const float off = static_cast<float>(__dsub_rn(h, a.half_over_beta));
+        loss = __fmul_rn(off, off);
+        dh = __fmul_rn(2.0f, off);
     } else {
-        const double zd = a.beta * h - a.margin;
+        const double zd = __fma_rn(a.beta, h, -a.margin);
         if (a.kind == RLK_PREF_HINGE) {
-            loss = zd < 1.0 ? 1.0 - zd : (zd == zd ? 0.0 : zd);
-            dh = zd < 1.0 ? -a.beta : (zd == zd ? 0.0 : zd);
+            const float gap = static_cast<float>(__dsub_rn(1.0, zd));
+            loss = gap > 0.0f ? gap : (gap == gap ? 0.0f : gap);
+            dh = zd < 1.0 ? -beta : (zd == zd ? 0.0f : gap);
         } else {
             // sig(z), sig(-z) and the two logs from e^-|z|, none of which cancels
-            const float z = static_cast<float>(zd);
+            const float z = static_cast<float>(zd), eps = static_cast<float>(a.label_smoothing);
+            const float keep = static_cast<float>(1.0 - a.label_smoothing);
             const float e = exp_any(-fabsf(z));
-            const double soft = static_cast<double>(log_1_plus(e));
-            const double small = static_cast<double>(__fdiv_rn(e, __fadd_rn(1.0f, e)));  // sig(-|z|)
-            const double pos = z >= 0.0f ? static_cast<double>(z) : 0.0;
-            const double neg = z >= 0.0f ? 0.0 : -static_cast<double>(z);
-            loss = (1.0 - a.label_smoothing) * (soft + neg) + a.label_smoothing * (soft + pos);
+            const float soft = log_1_plus(e);
+            const float small = __fdiv_rn(e, __fadd_rn(1.0f, e));  // sig(-|z|)
+            const float large = __fdiv_rn(1.0f, __fadd_rn(1.0f, e));
+            const float near = soft, far = __fadd_rn(soft, fabsf(z));  // -log sig(|z|), -log sig(-|z|)
+            const bool up = z >= 0.0f;
+            loss = __fadd_rn(__fmul_rn(keep, up ? near : far), __fmul_rn(eps, up ? far : near));
             // sig(z) - (1 - eps) = eps sig(z) - (1 - eps) sig(-z)
-            const double sp = z >= 0.0f ? 1.0 - small : small, sn = z >= 0.0f ? small : 1.0 - small;
-            dh = a.beta * (a.label_smoothing * sp - (1.0 - a.label_smoothing) * sn);
+            dh = __fmul_rn(beta, __fsub_rn(__fmul_rn(eps, up ? large : small), __fmul_rn(keep, up ? small : large)));
         }
     }
     if (write) {
-        a.out_pair_loss[pair] = static_cast<float>(loss);
-        a.out_rewards[q0] = static_cast<float>(a.beta * m0);
-        a.out_rewards[q1] = static_cast<float>(a.beta * m1);
+        a.out_pair_loss[pair] = loss;
+        a.out_rewards[q0] = static_cast<float>(__dmul_rn(a.beta, m0));
+        a.out_rewards[q1] = static_cast<float>(__dmul_rn(a.beta, m1));
     }
-    if (held_loss) *held_loss = static_cast<float>(loss);
-    const double step = a.scale_per_pair * dh;
-    slope[0] = static_cast<float>(step * inv0);
-    slope[1] = static_cast<float>(-step * inv1);
+    if (held_loss) *held_loss = loss;
+    const float step = __fmul_rn(static_cast<float>(a.scale_per_pair), dh);
+    slope[0] = __fmul_rn(step, inv0);
+    slope[1] = -__fmul_rn(step, inv1);
 }
 
 __device__ __forceinline__ int64_t chosen_of(const PreferenceArgs& a, int pair) {
@@ -120,24 +128,26 @@ __device__ __forceinline__ bool offsets_bad(const PreferenceArgs& a) {
 }
 
 // The loss from the pairs' losses, by a whole CTA.
-__device__ __forceinline__ void preference_finish(const PreferenceArgs& a, const float* losses, bool bad, double* tmp) {
+__device__ __forceinline__ void preference_finish(const PreferenceArgs& a, const float* losses, bool bad, float2* tmp) {
+    const int warp = threadIdx.x >> 5;
     bad = __syncthreads_or(bad);
-    double v = 0.0;
-    for (int i = threadIdx.x; i < a.n_pairs; i += kThreads) v = __dadd_rn(v, static_cast<double>(losses[i]));
-    v = warp_sum(v);
-    if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = v;
+    if (warp * 32 < a.n_pairs) {  // the other warps would add zeros
+        float2 v = pair_of(0.0f);
+        for (int i = threadIdx.x; i < a.n_pairs; i += kThreads) v = pair_add(v, pair_of(losses[i]));
+        v = warp_sum(v);
+        if ((threadIdx.x & 31) == 0) tmp[warp] = v;
+    }
     __syncthreads();
     if (threadIdx.x == 0) {
-        v = 0.0;
-        for (int i = 0; i < kWarps; ++i) v = __dadd_rn(v, tmp[i]);
-        if (a.n_pairs > 0) v = a.scale_per_pair * v;
-        *a.out_loss = bad ? CUDART_NAN_F : static_cast<float>(v);
+        float2 v = pair_of(0.0f);
+        for (int i = 0; i < kWarps && i * 32 < a.n_pairs; ++i) v = pair_add(v, tmp[i]);
+        *a.out_loss = bad ? CUDART_NAN_F : static_cast<float>(__dmul_rn(a.scale_per_pair, pair_value(v)));
         if (bad) report_status(a.status, RLK_ERR_INVALID_ARG);
     }
 }
 
 // Sum and active tokens of chunk g of a sequence, by a warp, on every lane.
-__device__ __forceinline__ double chunk_sum(const PreferenceArgs& a, const Span& sp, int64_t g, int* count) {
+__device__ __forceinline__ float2 chunk_sum(const PreferenceArgs& a, const Span& sp, int64_t g, int* count) {
     const int lane = threadIdx.x & 31;
     float lp[kChunk / 32], ref[kChunk / 32];
     bool on[kChunk / 32];
@@ -149,24 +159,26 @@ __device__ __forceinline__ double chunk_sum(const PreferenceArgs& a, const Span&
         ref[i] = in && a.ref_logprob ? a.ref_logprob[t] : 0.0f;
         on[i] = in && (!a.active || a.active[t] != 0);
     }
-    float2 acc = make_float2(0.0f, 0.0f);
+    float2 acc[kChunk / 32];
     int n = 0;
 #pragma unroll
     for (int i = 0; i < kChunk / 32; ++i) {
-        if (!on[i]) continue;
-        ++n;
-        const float2 d = two_diff(lp[i], ref[i]);
-        two_add(acc, d.x);
-        acc.y = __fadd_rn(acc.y, d.y);
+        n += on[i];
+        acc[i] = two_diff(on[i] ? lp[i] : 0.0f, on[i] ? ref[i] : 0.0f);
+    }
+#pragma unroll
+    for (int m = kChunk / 64; m >= 1; m >>= 1) {
+#pragma unroll
+        for (int i = 0; i < m; ++i) acc[i] = pair_add(acc[2 * i], acc[2 * i + 1]);
     }
     *count = __reduce_add_sync(0xffffffffu, n);
-    return warp_sum(static_cast<double>(acc.x) + static_cast<double>(acc.y));
+    return warp_sum(acc[0]);
 }
 
 __device__ __forceinline__ int64_t chunks_of(const Span& s) { return (s.e - s.b + kChunk - 1) / kChunk; }
 
 struct PairScratch {
-    double tmp[2][kWarps];
+    float2 tmp[2][kWarps];
     int n[2][kWarps];
 };
 
@@ -183,10 +195,10 @@ __device__ __forceinline__ void reduce_pair(const PreferenceArgs& a, int pair, c
         const int64_t c = chunks_of(sp[side]);
         held[side] = c < kSlots ? static_cast<int>(c) : kSlots;
         if (warp * 32 >= held[side]) continue;  // empty slots add zeros
-        double v = 0.0;
+        float2 v = pair_of(0.0f);
         int n = 0;
         for (int i = threadIdx.x; i < held[side]; i += kThreads) {
-            v = __dadd_rn(v, slot(side, i));
+            v = pair_add(v, slot(side, i));
             n += count(side, i);
         }
         v = warp_sum(v);
@@ -198,12 +210,12 @@ __device__ __forceinline__ void reduce_pair(const PreferenceArgs& a, int pair, c
     }
     __syncthreads();
     if (threadIdx.x == 0) {
-        double v[2] = {0.0, 0.0};
+        float2 v[2] = {pair_of(0.0f), pair_of(0.0f)};
         int n[2] = {0, 0};
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
             for (int i = 0; i < kWarps && i * 32 < held[side]; ++i) {
-                v[side] = __dadd_rn(v[side], sc.tmp[side][i]);
+                v[side] = pair_add(v[side], sc.tmp[side][i]);
                 n[side] += sc.n[side][i];
             }
         }
@@ -215,7 +227,7 @@ __device__ __forceinline__ void reduce_pair(const PreferenceArgs& a, int pair, c
 // One launch of clusters; every `team` CTAs of a cluster take a pair at a time.  alone: this is
 // the only cluster, and it also forms the loss.
 __global__ void __launch_bounds__(kThreads) k_preference(const PreferenceArgs a, int team, int alone) {
-    __shared__ double slots[2][kSlots];
+    __shared__ float2 slots[2][kSlots];
     __shared__ int counts[2][kSlots];
     __shared__ PairScratch scratch;
     __shared__ float slope[2];
@@ -228,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) k_preference(const PreferenceArgs a,
     const int teams = size / team;
     const int stride = gridDim.x / team;  // pairs in flight
     const int first = static_cast<int>(blockIdx.x) / size * teams + rank / team;
-    double* const lead_slots = cluster.map_shared_rank(&slots[0][0], lead);
+    float2* const lead_slots = cluster.map_shared_rank(&slots[0][0], lead);
     int* const lead_counts = cluster.map_shared_rank(&counts[0][0], lead);
     const float* const lead_slope = cluster.map_shared_rank(slope, lead);
     float* const all_losses = cluster.map_shared_rank(losses, 0);
@@ -248,11 +260,11 @@ __global__ void __launch_bounds__(kThreads) k_preference(const PreferenceArgs a,
             const Span& s = sp[side];
             for (int64_t g = member * kWarps + warp; s.b + g * kChunk < s.e; g += team * kWarps) {
                 int n;
-                const double v = chunk_sum(a, s, g, &n);
+                const float2 v = chunk_sum(a, s, g, &n);
                 if (lane == 0) {
                     // a slot is only ever this warp's
                     const int at = side * kSlots + static_cast<int>(g % kSlots);
-                    lead_slots[at] = __dadd_rn(g < kSlots ? 0.0 : lead_slots[at], v);
+                    lead_slots[at] = g < kSlots ? v : pair_add(lead_slots[at], v);
                     lead_counts[at] = (g < kSlots ? 0 : lead_counts[at]) + n;
                 }
             }
@@ -288,7 +300,7 @@ __global__ void __launch_bounds__(kThreads) k_preference(const PreferenceArgs a,
 }
 
 __global__ void __launch_bounds__(kThreads) k_preference_final(const PreferenceArgs a) {
-    __shared__ double tmp[kWarps];
+    __shared__ float2 tmp[kWarps];
     const bool bad = offsets_bad(a);
     ptx::grid_dependency_wait();
     preference_finish(a, a.out_pair_loss, bad, tmp);
@@ -352,7 +364,7 @@ __global__ void __launch_bounds__(kThreads) k_preference_chunks(const Preference
          i += static_cast<int64_t>(gridDim.x) * kWarps) {
         const int q = map.seq_of(i);
         int n;
-        const double v = chunk_sum(a, map.span[q], i - map.first[q], &n);
+        const float2 v = chunk_sum(a, map.span[q], i - map.first[q], &n);
         if ((threadIdx.x & 31) == 0) {
             a.chunk_sums[i] = v;
             a.chunk_counts[i] = n;
@@ -374,9 +386,9 @@ __global__ void __launch_bounds__(kThreads) k_preference_spread(const Preference
         __syncthreads();  // the previous pair's slopes have been read
         reduce_pair(a, pair, sp,
                     [&](int side, int j) {
-                        double v = 0.0;
                         const int64_t c = chunks_of(sp[side]);
-                        for (int64_t g = j; g < c; g += kSlots) v = __dadd_rn(v, a.chunk_sums[at[side] + g]);
+                        float2 v = a.chunk_sums[at[side] + j];
+                        for (int64_t g = j + kSlots; g < c; g += kSlots) v = pair_add(v, a.chunk_sums[at[side] + g]);
                         return v;
                     },
                     [&](int side, int j) {

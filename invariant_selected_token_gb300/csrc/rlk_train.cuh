@@ -30,7 +30,8 @@ struct PolicyArgs {
     float kl_coef;
     double scale, kl_coef64;
     int32_t* ticket;          // workspace of the two-launch path: CTAs that are done
-    int32_t* counts;          // workspace: active tokens per sequence or per block
+    int32_t* counts;          // workspace: active tokens per block (token_mean)
+    float* weights;           // workspace: weight of each sequence's tokens (seq_mean)
     float4* parts;            // workspace: one (policy, kl, clipped, -d) sum per unit
     float* out_loss;          // [1]
     float* out_stats;         // [4]
@@ -61,7 +62,7 @@ struct PreferenceArgs {
     float* grad;              // [T] or nullptr
     // workspace of the path over all chunks
     int32_t* ticket;          // CTAs that are done
-    double* chunk_sums;
+    float2* chunk_sums;       // as pairs
     int32_t* chunk_counts;
     int32_t* status;
 };
@@ -98,10 +99,11 @@ constexpr int kClipChunk = 16384;       // elements per partial sum
 constexpr int kClipSlots = 152 * 6;     // partial sums of a launch, CTAs of the large kernels
 constexpr int kClipClusterChunks = 48;  // largest set that one cluster does in one launch
 cudaError_t launch_clip_cluster(const ClipTableSmall& t, const ClipOut& o, cudaStream_t stream);
-cudaError_t launch_grad_sumsq(const ClipTable& t, double* slots, cudaStream_t stream);
-cudaError_t launch_grad_norm(const double* slots, int n, const ClipOut& o, cudaStream_t stream);
+// A launch's slots are pairs of floats.
+cudaError_t launch_grad_sumsq(const ClipTable& t, float2* slots, cudaStream_t stream);
+cudaError_t launch_grad_norm(const float2* slots, int n, const ClipOut& o, cudaStream_t stream);
 // write: this launch stores norm and scale
-cudaError_t launch_grad_scale(const ClipTable& t, const double* slots, int n, const ClipOut& o,
+cudaError_t launch_grad_scale(const ClipTable& t, const float2* slots, int n, const ClipOut& o,
                               bool write, cudaStream_t stream);
 
 struct RmsBwdArgs {
@@ -141,6 +143,28 @@ __device__ __forceinline__ void two_add(float2& acc, float x) {
     const float e = __fadd_rn(__fsub_rn(acc.x, __fsub_rn(s, t)), __fsub_rn(x, t));
     acc.x = s;
     acc.y = __fadd_rn(acc.y, fabsf(s) < CUDART_INF_F ? e : 0.0f);
+}
+
+// Sum of two such pairs.  GB300 adds fp64 at a small fraction of the fp32 rate (a warp's fp64
+// add takes tens of cycles of issue), so long sums are carried as pairs of floats, exact to about
+// 2^-46 of the larger operand; a + b and b + a give the same bits.
+__device__ __forceinline__ float2 pair_add(float2 a, float2 b) {
+    const float s = __fadd_rn(a.x, b.x);
+    const float t = __fsub_rn(s, a.x);
+    const float e = __fadd_rn(__fsub_rn(a.x, __fsub_rn(s, t)), __fsub_rn(b.x, t));
+    const float lo = __fadd_rn(__fadd_rn(a.y, b.y), e);
+    const float hi = __fadd_rn(s, lo);
+    return fabsf(s) < CUDART_INF_F ? make_float2(hi, __fsub_rn(lo, __fsub_rn(hi, s))) : make_float2(s, 0.0f);
+}
+__device__ __forceinline__ float2 pair_of(float v) { return make_float2(v, 0.0f); }
+__device__ __forceinline__ double pair_value(float2 v) {
+    return __dadd_rn(static_cast<double>(v.x), static_cast<double>(v.y));
+}
+__device__ __forceinline__ float2 warp_sum(float2 v) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+        v = pair_add(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+    return v;
 }
 
 __device__ __forceinline__ bool above(float2 d, float2 border) {
@@ -241,10 +265,4 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int o = 16; o >= 1; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
-__device__ __forceinline__ double warp_sum(double v) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v = __dadd_rn(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
-}
-
 }  // namespace rlk

@@ -3,7 +3,7 @@
 Tolerances (u = 2^-24): squares and their sums are positive, so every rounding on the way of a
 chunk's sum adds at most u of it; a chunk of 16384 elements is summed by 256 threads and trees of
 13 levels, at most 16384 / 256 + 13 = 77 roundings, and the root halves the relative error: 39 u
-for the norm with its own rounding 40 u.  The scale adds one rounding, the product another, and
+for the norm with its own rounding 40 u (the chunks are added as pairs of floats).  The scale adds one rounding, the product another, and
 the store half a step of the type (or of its smallest subnormal)."""
 import numpy as np
 import pytest

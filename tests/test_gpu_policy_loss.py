@@ -7,7 +7,7 @@ term and its gradient are within 12 u |w r A|.  The KL terms: u' = ref - lp is r
 which moves e^u' by |u'| u e^u'), the series or e^u' - 1 - u' then errs by at most
 4 u (e^u' + 1 + |u'|); the coefficient's rounding, w and the products add 8 u of the value.  A sum
 of n positive-weight terms by the kernel's tree adds at most 21 roundings in fp32 (8 in a thread,
-13 in the block's tree) of its absolute sum, then fp64 and one rounding."""
+13 in the block's tree) of its absolute sum, then sums as pairs of floats and one rounding."""
 import numpy as np
 import pytest
 import torch
