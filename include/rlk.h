@@ -383,8 +383,8 @@ rlk_status_t rlk_rmsnorm(const void* x, const void* residual, const void* gamma,
  * the gradient that reached residual_out from further on (NULL where there
  * is none); grad_x is then the gradient of both x and residual.  A row's
  * grad_x does not depend on the batch around it; grad_gamma is summed over
- * ranges of consecutive rows and then over the ranges, in an order that T
- * and H alone fix.
+ * ranges of consecutive rows and then over the ranges, in an order that T,
+ * H and the types fix.
  * (The blog's sections 3.3 and 4.2 ask for a backward with the forward's
  * numeric discipline; the strict-path table's "RMSNorm" row.)
  *
@@ -505,7 +505,7 @@ rlk_status_t rlk_preference_loss(const float* logprob, const float* ref_logprob,
  *   norm  = sqrt(sum of g^2 over all elements of all tensors)
  *   scale = max_norm / norm where norm is finite and above max_norm, else 1
  *   out   = RN(g * scale), rounded once to the tensor's type
- * Squares and the sums over each tensor's 16384-element chunks are fp32, the
+ * Squares and the sums over each tensor's 2048-element chunks are fp32, the
  * chunks are added as pairs of floats (a norm above 1.8e19 becomes infinite
  * and |g| below 1e-23 counts as 0); the order depends on the tensors' sizes and
  * types alone, not on their addresses.  A norm that is not finite leaves scale at 1 (the
@@ -519,7 +519,7 @@ rlk_status_t rlk_preference_loss(const float* logprob, const float* ref_logprob,
  *   max_norm      >= 0 (infinity allowed)
  *   out_norm, out_scale  device, float [1] each
  *   workspace     >= rlk_grad_norm_workspace_size(numels, n_tensors) bytes, 256-byte aligned; that
- *                 is 0 for small sets (48 chunks in 64 tensors), then NULL is allowed
+ *                 is 0 for small sets (384 chunks in 64 tensors), then NULL is allowed
  * The host arrays are read before the call returns.
  */
 size_t rlk_grad_norm_workspace_size(const int64_t* numels, int64_t n_tensors);

@@ -494,7 +494,7 @@ ClipPlan clip_plan_of(const int64_t* numels, int64_t n) {
     ClipPlan p;
     int64_t count = 0, chunks = 0;
     auto flush = [&] {
-        p.slots += chunks < rlk::kClipSlots ? chunks : rlk::kClipSlots;
+        p.slots += rlk::clip_launch_slots(chunks);
         count = chunks = 0;
     };
     for (int64_t i = 0; i < n; ++i) {
@@ -605,7 +605,7 @@ cudaError_t run_clip(const void* const* grads, void* const* outs, const int64_t*
     cudaError_t e = for_each_clip_table<rlk::ClipTable>(
         grads, outs, numels, dtypes, n, [&](const rlk::ClipTable& t) {
             const cudaError_t r = rlk::launch_grad_sumsq(t, slots + base, stream);
-            base += std::min<int64_t>(t.first[t.count], rlk::kClipSlots);
+            base += rlk::clip_launch_slots(t.first[t.count]);
             return r;
         });
     if (e != cudaSuccess) return e;
@@ -1008,7 +1008,7 @@ rlk_status_t rlk_rmsnorm(const void* x, const void* residual, const void* gamma,
 
 size_t rlk_rmsnorm_backward_workspace_size(int64_t T, int64_t H) {
     if (T < 0 || T > RLK_MAX_ROWS || H < 64 || H % 64 != 0 || H > 8192) return 0;
-    return align256(size_t(rlk::rmsnorm_backward_ranges(T, H)) * size_t(H) * sizeof(float));
+    return align256(size_t(rlk::rmsnorm_backward_ranges(T)) * size_t(H) * sizeof(float));
 }
 
 rlk_status_t rlk_rmsnorm_backward(const void* grad_out, int grad_out_dtype, const void* x,

@@ -8,8 +8,15 @@
 //   grad_gamma_i = sum over rows of dy_i x_i rstd
 //
 // A row's grad_x does not depend on the batch around it.  grad_gamma is
-// summed over at most 304 (152 for rows wider than 4096) ranges of consecutive
-// rows, one CTA each, then over the ranges, in an order that T and H fix.
+// summed over at most 152 ranges of consecutive rows, one CTA each, then over
+// the ranges, in an order that T, H and the types fix.
+//
+// Element i = 256 g + 8 l + j is lane l's j-th value of column group g, as in
+// the forward; a thread holds 16 features (two groups), so that the shuffles,
+// the barrier and the scalar arithmetic of a row are spread over twice as many
+// features as with 8.
+#include <cstdint>
+
 #include "rlk_contract.cuh"
 #include "rlk_ptx.cuh"
 #include "rlk_train.cuh"
@@ -17,20 +24,35 @@
 namespace rlk {
 namespace {
 
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// 16-byte pieces of 8 features
+template <int kType>
+constexpr int kPieces = kType == RLK_DTYPE_F32 ? 2 : 1;
+
+// Threads of a CTA, one CTA per SM: 24 warps, or 16 where a row takes as many or two stages of 24
+// warps' rows do not fit into shared memory.
+template <int kWarps, int kGo, int kGx>
+constexpr int kCtaThreads = kWarps == 16 || kPieces<kGo> + kPieces<kGx> == 4 ? 512 : 768;
+
+// Stages of a thread's ring: as many, at most 4, as fit into 227 KB.
+template <int kWarps, int kGo, int kGx>
+constexpr int kStages = 232448 / (kCtaThreads<kWarps, kGo, kGx> * 32 * (1 + kPieces<kGo> + kPieces<kGx>)) < 4
+                            ? 232448 / (kCtaThreads<kWarps, kGo, kGx> * 32 * (1 + kPieces<kGo> + kPieces<kGx>))
+                            : 4;
 
 template <int kType>
-__device__ __forceinline__ void store8(void* base, int64_t i, const float (&v)[8]) {
+__device__ __forceinline__ void store8(void* base, int64_t i, const uint64_t (&v)[4]) {
+    float e[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f2_unpack(v[k], e[2 * k], e[2 * k + 1]);
     if constexpr (kType == RLK_DTYPE_F32) {
         float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + i);
-        p[0] = make_float4(v[0], v[1], v[2], v[3]);
-        p[1] = make_float4(v[4], v[5], v[6], v[7]);
+        p[0] = make_float4(e[0], e[1], e[2], e[3]);
+        p[1] = make_float4(e[4], e[5], e[6], e[7]);
     } else {
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(e[2 * k], e[2 * k + 1]);
             w[k] = static_cast<uint32_t>(__bfloat16_as_ushort(b.x)) |
                    (static_cast<uint32_t>(__bfloat16_as_ushort(b.y)) << 16);
         }
@@ -38,121 +60,176 @@ __device__ __forceinline__ void store8(void* base, int64_t i, const float (&v)[8
     }
 }
 
-constexpr int cta_threads(int kWarps) { return kWarps == 32 ? 1024 : 512; }
+__device__ __forceinline__ void copy16(uint4* dst, const char* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(dst)), "l"(src) : "memory");
+}
 
+// Features (2p, 2p + 1) of 8 as they lie in memory.
 template <int kType>
-struct Raw8 {  // 8 features as loaded
-    uint4 w[kType == RLK_DTYPE_F32 ? 2 : 1];
-    __device__ __forceinline__ void load(const void* base, int64_t i) {
-        const char* p = static_cast<const char*>(base) + i * (kType == RLK_DTYPE_F32 ? 4 : 2);
-#pragma unroll
-        for (int k = 0; k < (kType == RLK_DTYPE_F32 ? 2 : 1); ++k) w[k] = reinterpret_cast<const uint4*>(p)[k];
-    }
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int k = 0; k < (kType == RLK_DTYPE_F32 ? 2 : 1); ++k) w[k] = make_uint4(0u, 0u, 0u, 0u);
-    }
-    __device__ __forceinline__ float at(int j) const {
-        const uint32_t* q = reinterpret_cast<const uint32_t*>(w);
-        if constexpr (kType == RLK_DTYPE_F32) return __uint_as_float(q[j]);
-        else return (j & 1) ? bf_hi(q[j / 2]) : bf_lo(q[j / 2]);
-    }
-};
+__device__ __forceinline__ uint64_t pair_at(const uint4 (&w)[kPieces<kType>], int p) {
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(w);
+    if constexpr (kType == RLK_DTYPE_F32)
+        return f2_pack(__uint_as_float(q[2 * p]), __uint_as_float(q[2 * p + 1]));
+    else
+        return f2_pack(__uint_as_float(q[p] << 16), __uint_as_float(q[p] & 0xFFFF0000u));
+}
 
-// A team of kWarps warps (a power of two, one thread per 8 features) takes a row, a CTA's teams
-// every kTeams-th row of its range.  The next row's x and grad_out are loaded before the current
-// one is reduced, so that the reduction and its barrier hide behind them.
+// A team of kWarps warps (a power of two) takes a row, a CTA's teams every kTeams-th row of its
+// range.  A thread copies its own features of the next kStages rows into its own ring of shared
+// memory, which no other thread reads: the copies need no barrier, and they fly while the current
+// row is reduced.  The arithmetic runs two features per instruction, each lane of which rounds
+// like the scalar one.
 template <int kWarps, int kGo, int kGx>
-__global__ void __launch_bounds__(cta_threads(kWarps), kWarps == 32 ? 1 : 2) k_rmsnorm_backward(const RmsBwdArgs a) {
-    constexpr int kThreads = cta_threads(kWarps), kTeams = kThreads / 32 / kWarps;
-    __shared__ float2 part[2][kThreads / 32];
-    __shared__ __align__(16) float dg_teams[kTeams > 1 ? kThreads * 8 : 1];
+__global__ void __launch_bounds__(kCtaThreads<kWarps, kGo, kGx>, 1) k_rmsnorm_backward(const RmsBwdArgs a) {
+    constexpr int kThreads = kCtaThreads<kWarps, kGo, kGx>, kTeams = kThreads / 32 / kWarps;
+    constexpr int kN = kStages<kWarps, kGo, kGx>;
+    constexpr int kGroup = 1 + kPieces<kGo> + kPieces<kGx>;  // pieces of 8 features
+    static_assert(kN >= 2, "a row flies while another is worked on");
+    extern __shared__ uint4 ring[];  // [stage][group][piece][thread]: x, grad_out, grad_residual
+    __shared__ __align__(16) float2 part[2][kThreads / 32];
     ptx::grid_dependents_launch();
     const int lane = threadIdx.x & 31, team = threadIdx.x / (32 * kWarps);
     const int warp = (threadIdx.x >> 5) % kWarps;
-    const int i0 = (warp * 32 + lane) * 8;
-    const bool in = i0 < a.H;
+    const int i0 = 512 * warp + 8 * lane;  // and i0 + 256
+    const bool in[2] = {i0 < a.H, i0 + 256 < a.H};
     const int64_t r0 = static_cast<int64_t>(a.T) * blockIdx.x / gridDim.x;
     const int64_t r1 = static_cast<int64_t>(a.T) * (blockIdx.x + 1) / gridDim.x;
-    const float inv_h_den = static_cast<float>(a.H);
-    Raw8<RLK_DTYPE_BF16> gam, x, x_next;
-    Raw8<kGo> dy, dy_next;
-    Raw8<kGx> res;
-    gam.clear();
-    x_next.clear();
-    dy_next.clear();
-    res.clear();
-    float dg[8] = {};
-    int64_t t = r0 + team;
-    if (in) {
-        gam.load(a.gamma, i0);
+    const bool pow2 = (a.H & (a.H - 1)) == 0;
+    const float h = static_cast<float>(a.H), inv_h = __fdiv_rn(1.0f, h);
+    auto piece = [&](int stage, int g, int k) { return ring + ((stage * 2 + g) * kGroup + k) * kThreads + threadIdx.x; };
+    auto fetch = [&](int64_t t, int stage) {
         if (t < r1) {
-            x_next.load(a.x, t * a.H + i0);
-            dy_next.load(a.grad_out, t * a.H + i0);
-        }
-    }
-    int slot = 0;
-    for (; t < r1; t += kTeams) {
-        x = x_next;
-        dy = dy_next;
-        if (in) {
-            if (a.grad_res) res.load(a.grad_res, t * a.H + i0);
-            if (t + kTeams < r1) {
-                x_next.load(a.x, (t + kTeams) * a.H + i0);
-                dy_next.load(a.grad_out, (t + kTeams) * a.H + i0);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                if (!in[g]) continue;
+                const int64_t i = t * a.H + i0 + 256 * g;
+                copy16(piece(stage, g, 0), reinterpret_cast<const char*>(a.x) + i * 2);
+#pragma unroll
+                for (int k = 0; k < kPieces<kGo>; ++k)
+                    copy16(piece(stage, g, 1 + k), static_cast<const char*>(a.grad_out) + i * (2 * kPieces<kGo>) + 16 * k);
+                if (a.grad_res) {
+#pragma unroll
+                    for (int k = 0; k < kPieces<kGx>; ++k)
+                        copy16(piece(stage, g, 1 + kPieces<kGo> + k),
+                               static_cast<const char*>(a.grad_res) + i * (2 * kPieces<kGx>) + 16 * k);
+                }
             }
         }
-        // the forward's tree: pairs of features, then lanes, then warps
-        float s2[4], d = 0.0f;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    uint4 gam[2][1] = {};
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            s2[k] = __fadd_rn(__fmul_rn(x.at(2 * k), x.at(2 * k)), __fmul_rn(x.at(2 * k + 1), x.at(2 * k + 1)));
-        float s = __fadd_rn(__fadd_rn(s2[0], s2[1]), __fadd_rn(s2[2], s2[3]));
+    for (int g = 0; g < 2; ++g)
+        if (in[g]) gam[g][0] = *reinterpret_cast<const uint4*>(a.gamma + i0 + 256 * g);
+    uint64_t dg[2][4] = {};
+    int64_t t = r0 + team;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) d = __fmaf_rn(__fmul_rn(dy.at(k), gam.at(k)), x.at(k), d);
+    for (int k = 0; k < kN; ++k) fetch(t + k * kTeams, k);
+    int slot = 0, stage = 0;
+    for (; t < r1; t += kTeams) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kN - 1) : "memory");
+        // the forward's tree over the squares: pairs of features, then lanes, groups and warps
+        float s[2];
+        uint64_t dot = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
+        for (int g = 0; g < 2; ++g) {
+            uint4 x[1] = {}, dy[kPieces<kGo>] = {};
+            if (in[g]) {
+                x[0] = *piece(stage, g, 0);
+#pragma unroll
+                for (int k = 0; k < kPieces<kGo>; ++k) dy[k] = *piece(stage, g, 1 + k);
+            }
+            float s2[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const uint64_t v = pair_at<RLK_DTYPE_BF16>(x, p);
+                float lo, hi;
+                f2_unpack(f2_mul(v, v), lo, hi);
+                s2[p] = __fadd_rn(lo, hi);
+                dot = f2_fma(f2_mul(pair_at<kGo>(dy, p), pair_at<RLK_DTYPE_BF16>(gam[g], p)), v, dot);
+            }
+            s[g] = __fadd_rn(__fadd_rn(s2[0], s2[1]), __fadd_rn(s2[2], s2[3]));
+        }
+        float d0, d1;
+        f2_unpack(dot, d0, d1);
+        float d = __fadd_rn(d0, d1);
+        // even lanes go on with the first group, odd ones with the second
+        const bool odd = lane & 1;
+        float q = __fadd_rn(odd ? s[1] : s[0], __shfl_xor_sync(0xffffffffu, odd ? s[0] : s[1], 1));
+        d = __fadd_rn(d, __shfl_xor_sync(0xffffffffu, d, 1));
+#pragma unroll
+        for (int o = 2; o < 32; o <<= 1) {
+            q = __fadd_rn(q, __shfl_xor_sync(0xffffffffu, q, o));
             d = __fadd_rn(d, __shfl_xor_sync(0xffffffffu, d, o));
         }
+        q = __fadd_rn(q, __shfl_xor_sync(0xffffffffu, q, 1));
         if constexpr (kWarps > 1) {
-            if (lane == 0) part[slot][team * kWarps + warp] = make_float2(s, d);
+            if (lane == 0) part[slot][team * kWarps + warp] = make_float2(q, d);
             asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * kWarps) : "memory");
-            const float2 p = part[slot][team * kWarps + lane % kWarps];
-            s = p.x;
-            d = p.y;
+            float2 p[kWarps];
 #pragma unroll
-            for (int o = 1; o < kWarps; o <<= 1) {
-                s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
-                d = __fadd_rn(d, __shfl_xor_sync(0xffffffffu, d, o));
+            for (int i = 0; i < kWarps / 2; ++i) {
+                const float4 two = reinterpret_cast<const float4*>(&part[slot][team * kWarps])[i];
+                p[2 * i] = make_float2(two.x, two.y);
+                p[2 * i + 1] = make_float2(two.z, two.w);
             }
+#pragma unroll
+            for (int n = kWarps / 2; n >= 1; n >>= 1) {
+#pragma unroll
+                for (int i = 0; i < n; ++i)
+                    p[i] = make_float2(__fadd_rn(p[2 * i].x, p[2 * i + 1].x), __fadd_rn(p[2 * i].y, p[2 * i + 1].y));
+            }
+            q = p[0].x;
+            d = p[0].y;
             slot ^= 1;  // a team's warps are never more than one row apart
         }
-        const float rstd = contract_rsqrt(__fadd_rn(__fdiv_rn(s, inv_h_den), a.eps));
-        const float c = __fdiv_rn(__fmul_rn(__fmul_rn(rstd, rstd), d), inv_h_den);
-        if (in) {
-            float o[8];
+        // a product with 1 / H is the quotient itself where H is a power of two
+        const float mean = pow2 ? __fmul_rn(q, inv_h) : __fdiv_rn(q, h);
+        const float rstd = contract_rsqrt(__fadd_rn(mean, a.eps));
+        const float c = __fmul_rn(__fmul_rn(rstd, rstd), __fmul_rn(d, inv_h));
+        const uint64_t rstd2 = f2_splat(rstd), neg_c2 = f2_splat(-c);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float up = __fmul_rn(dy.at(k), gam.at(k));
-                o[k] = __fmaf_rn(rstd, __fmaf_rn(-x.at(k), c, up), res.at(k));
-                dg[k] = __fmaf_rn(dy.at(k), __fmul_rn(x.at(k), rstd), dg[k]);
+        for (int g = 0; g < 2; ++g) {
+            if (!in[g]) continue;
+            uint4 x[1], dy[kPieces<kGo>], res[kPieces<kGx>] = {};
+            x[0] = *piece(stage, g, 0);
+#pragma unroll
+            for (int k = 0; k < kPieces<kGo>; ++k) dy[k] = *piece(stage, g, 1 + k);
+            if (a.grad_res) {
+#pragma unroll
+                for (int k = 0; k < kPieces<kGx>; ++k) res[k] = *piece(stage, g, 1 + kPieces<kGo> + k);
             }
-            store8<kGx>(a.grad_x, t * a.H + i0, o);
+            uint64_t o[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const uint64_t v = pair_at<RLK_DTYPE_BF16>(x, p), y = pair_at<kGo>(dy, p);
+                const uint64_t up = f2_mul(y, pair_at<RLK_DTYPE_BF16>(gam[g], p));
+                o[p] = f2_fma(rstd2, f2_fma(v, neg_c2, up), pair_at<kGx>(res, p));
+                dg[g][p] = f2_fma(y, f2_mul(v, rstd2), dg[g][p]);
+            }
+            store8<kGx>(a.grad_x, t * a.H + i0 + 256 * g, o);
         }
+        fetch(t + kN * kTeams, stage);  // everything in this stage has been used
+        stage = stage + 1 < kN ? stage + 1 : 0;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!a.grad_gamma) return;
     float* const out = a.parts + static_cast<int64_t>(blockIdx.x) * a.H;
     if constexpr (kTeams == 1) {
-        if (in) store8<RLK_DTYPE_F32>(out, i0, dg);
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+            if (in[g]) store8<RLK_DTYPE_F32>(out, i0 + 256 * g, dg[g]);
     } else {
-        // the teams' sums in ascending order
-        store8<RLK_DTYPE_F32>(dg_teams, team * kWarps * 256 + i0, dg);
+        // the teams' sums in ascending order; the ring is empty
+        float* const dg_teams = reinterpret_cast<float*>(ring);
+        __syncthreads();
+#pragma unroll
+        for (int g = 0; g < 2; ++g) store8<RLK_DTYPE_F32>(dg_teams, team * kWarps * 512 + i0 + 256 * g, dg[g]);
         __syncthreads();
         for (int i = threadIdx.x; i < a.H; i += kThreads) {
             float v = dg_teams[i];
 #pragma unroll
-            for (int k = 1; k < kTeams; ++k) v = __fadd_rn(v, dg_teams[k * kWarps * 256 + i]);
+            for (int k = 1; k < kTeams; ++k) v = __fadd_rn(v, dg_teams[k * kWarps * 512 + i]);
             out[i] = v;
         }
     }
@@ -174,38 +251,43 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_gamma_sum(const float* parts, 
     if (c == 0) out[blockIdx.x * 32 + row] = s;
 }
 
+template <int kWarps, int kGo, int kGx>
+cudaError_t launch_types(const RmsBwdArgs& a, int blocks, cudaStream_t stream) {
+    constexpr int kThreads = kCtaThreads<kWarps, kGo, kGx>;
+    constexpr size_t kSmem =
+        size_t(kStages<kWarps, kGo, kGx>) * 2 * (1 + kPieces<kGo> + kPieces<kGx>) * kThreads * sizeof(uint4);
+    // per device and kernel: the runtime keeps it
+    const cudaError_t e = cudaFuncSetAttribute(k_rmsnorm_backward<kWarps, kGo, kGx>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+    if (e != cudaSuccess) return e;
+    k_rmsnorm_backward<kWarps, kGo, kGx><<<blocks, kThreads, kSmem, stream>>>(a);
+    return cudaGetLastError();
+}
+
 template <int kWarps>
-void launch_row(const RmsBwdArgs& a, int blocks, cudaStream_t stream) {
-    constexpr int kThreads = cta_threads(kWarps);
-    if (a.go_dtype == RLK_DTYPE_F32) {
-        if (a.gx_dtype == RLK_DTYPE_F32)
-            k_rmsnorm_backward<kWarps, RLK_DTYPE_F32, RLK_DTYPE_F32><<<blocks, kThreads, 0, stream>>>(a);
-        else
-            k_rmsnorm_backward<kWarps, RLK_DTYPE_F32, RLK_DTYPE_BF16><<<blocks, kThreads, 0, stream>>>(a);
-    } else {
-        if (a.gx_dtype == RLK_DTYPE_F32)
-            k_rmsnorm_backward<kWarps, RLK_DTYPE_BF16, RLK_DTYPE_F32><<<blocks, kThreads, 0, stream>>>(a);
-        else
-            k_rmsnorm_backward<kWarps, RLK_DTYPE_BF16, RLK_DTYPE_BF16><<<blocks, kThreads, 0, stream>>>(a);
-    }
+cudaError_t launch_row(const RmsBwdArgs& a, int blocks, cudaStream_t stream) {
+    if (a.go_dtype == RLK_DTYPE_F32)
+        return a.gx_dtype == RLK_DTYPE_F32 ? launch_types<kWarps, RLK_DTYPE_F32, RLK_DTYPE_F32>(a, blocks, stream)
+                                           : launch_types<kWarps, RLK_DTYPE_F32, RLK_DTYPE_BF16>(a, blocks, stream);
+    return a.gx_dtype == RLK_DTYPE_F32 ? launch_types<kWarps, RLK_DTYPE_BF16, RLK_DTYPE_F32>(a, blocks, stream)
+                                       : launch_types<kWarps, RLK_DTYPE_BF16, RLK_DTYPE_BF16>(a, blocks, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_rmsnorm_backward(const RmsBwdArgs& a, cudaStream_t stream) {
-    const int blocks = rmsnorm_backward_ranges(a.T, a.H);
+    const int blocks = rmsnorm_backward_ranges(a.T);
     int warps = 1;
-    while (warps * 256 < a.H) warps *= 2;
+    while (warps * 512 < a.H) warps *= 2;
+    cudaError_t e = cudaSuccess;
     if (blocks > 0) switch (warps) {
-        case 1: launch_row<1>(a, blocks, stream); break;
-        case 2: launch_row<2>(a, blocks, stream); break;
-        case 4: launch_row<4>(a, blocks, stream); break;
-        case 8: launch_row<8>(a, blocks, stream); break;
-        case 16: launch_row<16>(a, blocks, stream); break;
-        case 32: launch_row<32>(a, blocks, stream); break;
+        case 1: e = launch_row<1>(a, blocks, stream); break;
+        case 2: e = launch_row<2>(a, blocks, stream); break;
+        case 4: e = launch_row<4>(a, blocks, stream); break;
+        case 8: e = launch_row<8>(a, blocks, stream); break;
+        case 16: e = launch_row<16>(a, blocks, stream); break;
         default: return cudaErrorInvalidValue;
     }
-    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !a.grad_gamma) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];

@@ -95,9 +95,14 @@ struct ClipOut {
     int32_t* status;
     double max_norm;
 };
-constexpr int kClipChunk = 16384;       // elements per partial sum
-constexpr int kClipSlots = 152 * 6;     // partial sums of a launch, CTAs of the large kernels
-constexpr int kClipClusterChunks = 48;  // largest set that one cluster does in one launch
+constexpr int kClipChunk = 2048;         // elements that a warp sums at a time
+constexpr int kClipSlots = 152 * 6;      // most CTAs of a launch, a partial sum each
+constexpr int kClipClusterChunks = 384;  // largest set that one cluster does in one launch
+// CTAs, and partial sums, of a launch over so many chunks: 8 warps each.
+inline int clip_launch_slots(int64_t chunks) {
+    const int64_t ctas = (chunks + 7) / 8;
+    return static_cast<int>(ctas < kClipSlots ? ctas : kClipSlots);
+}
 cudaError_t launch_clip_cluster(const ClipTableSmall& t, const ClipOut& o, cudaStream_t stream);
 // A launch's slots are pairs of floats.
 cudaError_t launch_grad_sumsq(const ClipTable& t, float2* slots, cudaStream_t stream);
@@ -118,12 +123,9 @@ struct RmsBwdArgs {
     int T, H;
     int go_dtype, gx_dtype;   // RLK_DTYPE_*
 };
-// Ranges of rows whose grad_gamma sums are formed apart, a CTA each: two 512-thread CTAs per SM,
-// or one of 1024 threads where a row needs that many.
-inline int rmsnorm_backward_ranges(int64_t T, int64_t H) {
-    const int most = H > 4096 ? 152 : 304;
-    return T < most ? static_cast<int>(T) : most;
-}
+// Ranges of rows whose grad_gamma sums are formed apart, a CTA per SM each.
+constexpr int kRmsBwdRanges = 152;
+inline int rmsnorm_backward_ranges(int64_t T) { return T < kRmsBwdRanges ? static_cast<int>(T) : kRmsBwdRanges; }
 cudaError_t launch_rmsnorm_backward(const RmsBwdArgs& a, cudaStream_t stream);
 
 // ---------------------------------------------------------------- device arithmetic

@@ -1,9 +1,9 @@
 """Global gradient norm and clipping on the GPU against the fp64 definition.
 
 Tolerances (u = 2^-24): squares and their sums are positive, so every rounding on the way of a
-chunk's sum adds at most u of it; a chunk of 16384 elements is summed by 256 threads and trees of
-13 levels, at most 16384 / 256 + 13 = 77 roundings, and the root halves the relative error: 39 u
-for the norm with its own rounding 40 u (the chunks are added as pairs of floats).  The scale adds one rounding, the product another, and
+chunk's sum adds at most u of it; a chunk of 2048 elements is summed by 32 lanes and trees of at
+most 8 levels, 2048 / 32 + 8 = 72 roundings, and the root halves the relative error: 36 u, for the
+norm with its own roundings below 40 u (the chunks are added as pairs of floats).  The scale adds one rounding, the product another, and
 the store half a step of the type (or of its smallest subnormal)."""
 import numpy as np
 import pytest
@@ -35,8 +35,10 @@ def f64(t):
 SETS = [
     ([1], [torch.float32]),
     ([0, 5, 0], [torch.float32, torch.bfloat16, torch.float16]),
-    ([7, 16383, 16384, 16385, 33001], [torch.float32] * 5),
-    ([7, 16383, 16384, 16385, 100003], [torch.bfloat16] * 5),
+    ([7, 2047, 2048, 2049, 16383, 33001], [torch.float32] * 6),
+    ([7, 2047, 2048, 2049, 100003], [torch.bfloat16] * 5),
+    ([786432 - 2048, 2048], [torch.float32, torch.bfloat16]),  # the last that one cluster takes
+    ([786432 - 2048, 2049], [torch.float32, torch.bfloat16]),
     ([64, 16391, 65, 40000], [torch.float16, torch.bfloat16, torch.float32, torch.float16]),
     ([3, 1000, 17, 257] * 400, [torch.bfloat16, torch.float32, torch.float16, torch.bfloat16] * 400),
     ([5000011, 12, 3000017], [torch.bfloat16, torch.float32, torch.float32]),

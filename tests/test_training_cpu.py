@@ -147,9 +147,9 @@ def test_grad_clip_refusals(L):
                dict(outs=(0x30002, 0x40000)), dict(ws=0x110)):
         refused(call, ALIGNMENT, **kw)
     refused(call, WORKSPACE, sizes=(1 << 20, 16), ptrs=(0x10000, 0x10000000), wsb=4)
-    small = (ctypes.c_int64 * 2)(47 * 16384, 16384)
+    small = (ctypes.c_int64 * 2)(383 * 2048, 2048)
     assert L.rlk_grad_norm_workspace_size(small, 2) == 0  # one launch, no workspace
-    small[1] = 16385
+    small[1] = 2049
     assert L.rlk_grad_norm_workspace_size(small, 2) >= 49 * 8
     sizes = (ctypes.c_int64 * 2)(-1, 4)
     assert L.rlk_grad_norm_workspace_size(sizes, 2) == 0
