@@ -505,24 +505,25 @@ rlk_status_t rlk_preference_loss(const float* logprob, const float* ref_logprob,
  *   norm  = sqrt(sum of g^2 over all elements of all tensors)
  *   scale = max_norm / norm where norm is finite and above max_norm, else 1
  *   out   = RN(g * scale), rounded once to the tensor's type
- * Squares and the sums over each tensor's 2048-element chunks are fp32, the
- * chunks are added as pairs of floats (a norm above 1.8e19 becomes infinite
- * and |g| below 1e-23 counts as 0); the order depends on the tensors' sizes and
- * types alone, not on their addresses.  A norm that is not finite leaves scale at 1 (the
+ * Squares are summed in fp32 by each thread, and those sums added by a fixed
+ * tree, at last as pairs of floats (a norm above 1.8e19 becomes infinite and
+ * |g| below 1e-23 counts as 0); the order depends on the tensors' sizes,
+ * types and places within 16 bytes alone.  A norm that is not finite leaves scale at 1 (the
  * gradients keep their values) and sets RLK_ERR_NONFINITE in *dev_status.
  *
  *   grads, outs   HOST arrays of n_tensors DEVICE pointers, each aligned to its element size.
  *                 outs[i] may be grads[i] (in place: nothing is written when scale is 1); any
  *                 other overlap of an output with an input or output is RLK_ERR_INVALID_ARG
- *   numels        HOST, elements per tensor (0 allowed; at most 2^40)
+ *   numels        HOST, elements per tensor (0 allowed; at most 2^38 in all)
  *   dtypes        HOST, RLK_DTYPE_F32, RLK_DTYPE_BF16 or RLK_DTYPE_F16 per tensor
  *   max_norm      >= 0 (infinity allowed)
  *   out_norm, out_scale  device, float [1] each
- *   workspace     >= rlk_grad_norm_workspace_size(numels, n_tensors) bytes, 256-byte aligned; that
- *                 is 0 for small sets (384 chunks in 64 tensors), then NULL is allowed
+ *   workspace     >= rlk_grad_norm_workspace_size() bytes, 256-byte aligned; that
+ *                 is 0 for small sets (about 1.5 MB in 64 tensors), then NULL is allowed
  * The host arrays are read before the call returns.
  */
-size_t rlk_grad_norm_workspace_size(const int64_t* numels, int64_t n_tensors);
+size_t rlk_grad_norm_workspace_size(const int64_t* numels, const int32_t* dtypes,
+                                    int64_t n_tensors);
 rlk_status_t rlk_grad_norm(const void* const* grads, const int64_t* numels,
                            const int32_t* dtypes, int64_t n_tensors, float* out_norm,
                            void* workspace, size_t workspace_bytes, int32_t* dev_status,

@@ -119,7 +119,7 @@ def lib() -> ctypes.CDLL:
         L.rlk_preference_loss_workspace_size.restype = sz
         L.rlk_preference_loss_workspace_size.argtypes = [i64, i64]
         L.rlk_grad_norm_workspace_size.restype = sz
-        L.rlk_grad_norm_workspace_size.argtypes = [P, i64]
+        L.rlk_grad_norm_workspace_size.argtypes = [P, P, i64]
         L.rlk_grad_norm.restype = i32
         L.rlk_grad_norm.argtypes = [P, P, P, i64, P, P, sz, P, P]
         L.rlk_grad_clip.restype = i32
@@ -764,7 +764,7 @@ def grad_norm(grads: Sequence[torch.Tensor], workspace: Optional[torch.Tensor] =
 
     def call(st):
         norm = torch.empty((), dtype=torch.float32, device=dev)
-        p_ws, ws_n, ws = _workspace(workspace, L.rlk_grad_norm_workspace_size(h_sizes, n), dev)
+        p_ws, ws_n, ws = _workspace(workspace, L.rlk_grad_norm_workspace_size(h_sizes, h_types, n), dev)
         _check(L.rlk_grad_norm(h_ptrs, h_sizes, h_types, n, norm.data_ptr(), p_ws, ws_n, a_status, st),
                "rlk_grad_norm")
         return norm
@@ -797,7 +797,7 @@ def clip_grads(grads: Sequence[torch.Tensor], max_norm: float,
     def call(st):
         norm = torch.empty((), dtype=torch.float32, device=dev)
         scale = torch.empty((), dtype=torch.float32, device=dev)
-        p_ws, ws_n, ws = _workspace(workspace, L.rlk_grad_norm_workspace_size(h_sizes, n), dev)
+        p_ws, ws_n, ws = _workspace(workspace, L.rlk_grad_norm_workspace_size(h_sizes, h_types, n), dev)
         _check(L.rlk_grad_clip(h_ptrs, h_outs, h_sizes, h_types, n, max_norm, norm.data_ptr(),
                                scale.data_ptr(), p_ws, ws_n, a_status, st), "rlk_grad_clip")
         return norm, scale

@@ -476,35 +476,40 @@ PreferenceLayout preference_layout_of(int64_t T, int64_t n_pairs) {
     return l;
 }
 
-int64_t clip_chunks(int64_t n) { return (n + rlk::kClipChunk - 1) / rlk::kClipChunk; }
-
 size_t clip_element_size(int dtype) { return dtype == RLK_DTYPE_F32 ? 4 : 2; }
 
-// How the tensors are spread over launches: a table is full at kClipTable tensors or 2^30 chunks.
+// Pieces of a tensor that starts `lead` bytes behind a 16-byte boundary.
+int64_t clip_pieces(int64_t n, int dtype, int64_t lead) {
+    return (lead + n * int64_t(clip_element_size(dtype)) + rlk::kClipPieceBytes - 1) / rlk::kClipPieceBytes;
+}
+
+// How the tensors are spread over launches (a table is full at 640 tensors), from their sizes and
+// types alone: pieces are counted as if every tensor started at the last byte of a 16-byte line.
 struct ClipPlan {
-    int64_t tensors = 0, chunks = 0, slots = 0;
+    int64_t tensors = 0, pieces = 0, slots = 0;
     bool one_launch() const {
-        return chunks <= rlk::kClipClusterChunks && tensors <= rlk::ClipTableSmall::kSize;
+        return pieces <= rlk::kClipClusterPieces && tensors <= rlk::ClipTableSmall::kSize;
     }
 };
 
-constexpr int64_t kClipMostChunks = int64_t(1) << 30;
+// Most elements of a set, so that pieces are 32-bit numbers.
+constexpr int64_t kClipMostElements = int64_t(1) << 38;
 
-ClipPlan clip_plan_of(const int64_t* numels, int64_t n) {
+ClipPlan clip_plan_of(const int64_t* numels, const int32_t* dtypes, int64_t n) {
     ClipPlan p;
-    int64_t count = 0, chunks = 0;
+    int64_t count = 0, pieces = 0;
     auto flush = [&] {
-        p.slots += rlk::clip_launch_slots(chunks);
-        count = chunks = 0;
+        p.slots += rlk::clip_launch_slots(pieces);
+        count = pieces = 0;
     };
     for (int64_t i = 0; i < n; ++i) {
         if (numels[i] == 0) continue;
-        const int64_t c = clip_chunks(numels[i]);
-        if (count == rlk::ClipTable::kSize || chunks + c > kClipMostChunks) flush();
+        if (count == rlk::ClipTable::kSize) flush();
+        const int64_t c = clip_pieces(numels[i], dtypes[i], 15);
         ++count;
-        chunks += c;
+        pieces += c;
         ++p.tensors;
-        p.chunks += c;
+        p.pieces += c;
     }
     flush();
     return p;
@@ -514,20 +519,30 @@ size_t clip_workspace_of(const ClipPlan& p) {
     return p.one_launch() ? 0 : align256(size_t(p.slots) * sizeof(float2));
 }
 
-rlk_status_t clip_checks(const void* const* grads, const int64_t* numels, const int32_t* dtypes,
-                         int64_t n, const void* workspace, size_t workspace_bytes, ClipPlan* plan) {
-    if (n < 0 || n > (int64_t(1) << 24)) return RLK_ERR_INVALID_ARG;
-    if (n > 0 && (!grads || !numels || !dtypes)) return RLK_ERR_INVALID_ARG;
+// The checks of sizes and types; fills *plan.
+rlk_status_t clip_sizes_check(const int64_t* numels, const int32_t* dtypes, int64_t n, ClipPlan* plan) {
+    if (n < 0 || n > (int64_t(1) << 24) || (n > 0 && (!numels || !dtypes))) return RLK_ERR_INVALID_ARG;
+    int64_t all = 0;
     for (int64_t i = 0; i < n; ++i) {
         if (numels[i] < 0) return RLK_ERR_INVALID_ARG;
-        if (numels[i] > (int64_t(1) << 40)) return RLK_ERR_UNSUPPORTED;
+        if (numels[i] > kClipMostElements || (all += numels[i]) > kClipMostElements) return RLK_ERR_UNSUPPORTED;
         if (dtypes[i] != RLK_DTYPE_F32 && dtypes[i] != RLK_DTYPE_BF16 && dtypes[i] != RLK_DTYPE_F16)
             return RLK_ERR_UNSUPPORTED;
+    }
+    *plan = clip_plan_of(numels, dtypes, n);
+    return RLK_OK;
+}
+
+rlk_status_t clip_checks(const void* const* grads, const int64_t* numels, const int32_t* dtypes,
+                         int64_t n, const void* workspace, size_t workspace_bytes, ClipPlan* plan) {
+    rlk_status_t s = clip_sizes_check(numels, dtypes, n, plan);
+    if (s != RLK_OK) return s;
+    if (n > 0 && !grads) return RLK_ERR_INVALID_ARG;
+    for (int64_t i = 0; i < n; ++i) {
         if (numels[i] == 0) continue;
         if (!grads[i]) return RLK_ERR_INVALID_ARG;
         if (!aligned(grads[i], clip_element_size(dtypes[i]))) return RLK_ERR_ALIGNMENT;
     }
-    *plan = clip_plan_of(numels, n);
     const size_t need = clip_workspace_of(*plan);
     if (need > 0 && !workspace) return RLK_ERR_INVALID_ARG;
     if (!aligned(workspace, 256)) return RLK_ERR_ALIGNMENT;
@@ -577,8 +592,8 @@ cudaError_t for_each_clip_table(const void* const* grads, void* const* outs, con
     t.first[0] = 0;
     for (int64_t i = 0; i < n; ++i) {
         if (numels[i] == 0) continue;
-        const int64_t c = clip_chunks(numels[i]);
-        if (t.count == Table::kSize || t.first[t.count] + c > kClipMostChunks) {
+        const int64_t c = clip_pieces(numels[i], dtypes[i], int64_t(reinterpret_cast<uintptr_t>(grads[i]) & 15));
+        if (t.count == Table::kSize) {
             const cudaError_t e = fn(t);
             if (e != cudaSuccess) return e;
             t.count = 0;
@@ -609,11 +624,11 @@ cudaError_t run_clip(const void* const* grads, void* const* outs, const int64_t*
             return r;
         });
     if (e != cudaSuccess) return e;
-    if (!o.scale) return rlk::launch_grad_norm(slots, int(plan.slots), o, stream);
+    if (!o.scale) return rlk::launch_grad_norm(slots, int(base), o, stream);
     bool write = true;
     return for_each_clip_table<rlk::ClipTable>(
         grads, outs, numels, dtypes, n, [&](const rlk::ClipTable& t) {
-            const cudaError_t r = rlk::launch_grad_scale(t, slots, int(plan.slots), o, write, stream);
+            const cudaError_t r = rlk::launch_grad_scale(t, slots, int(base), o, write, stream);
             write = false;
             return r;
         });
@@ -1192,11 +1207,10 @@ rlk_status_t rlk_preference_loss(const float* logprob, const float* ref_logprob,
                : RLK_ERR_CUDA;
 }
 
-size_t rlk_grad_norm_workspace_size(const int64_t* numels, int64_t n_tensors) {
-    if (n_tensors < 0 || (n_tensors > 0 && !numels)) return 0;
-    for (int64_t i = 0; i < n_tensors; ++i)
-        if (numels[i] < 0 || numels[i] > (int64_t(1) << 40)) return 0;
-    return clip_workspace_of(clip_plan_of(numels, n_tensors));
+size_t rlk_grad_norm_workspace_size(const int64_t* numels, const int32_t* dtypes,
+                                    int64_t n_tensors) {
+    ClipPlan plan;
+    return clip_sizes_check(numels, dtypes, n_tensors, &plan) == RLK_OK ? clip_workspace_of(plan) : 0;
 }
 
 rlk_status_t rlk_grad_norm(const void* const* grads, const int64_t* numels,

@@ -4,24 +4,21 @@
 //   scale = max_norm / norm where norm is finite and above max_norm, else 1
 //   out   = RN(g * scale), each element rounded once to its tensor's type
 //
-// Order of the sum, which depends on the tensors' sizes alone: a tensor is cut
-// into chunks of 2048 elements counted from its first, a warp's work each.
-// With E elements in 16 bytes, class i mod 32 E of a chunk's elements is
-// summed ascending in fp32, the classes by a fixed tree in fp32; chunk c of a
-// launch goes to warp c mod (912 * 8) in ascending order, and the warps' sums
-// are added by a fixed tree, these last two as pairs of floats.  An element's
-// class does not depend on its address: 16-byte loads take whole aligned
-// vectors wherever the tensor starts, and the lane that has a vector owns its
-// elements' classes; only where the classes then lie in the lane's registers
-// changes, and an exchange through shared memory undoes that.
+// Each tensor is cut into pieces of 16 KB, counted from the 16-byte line in
+// which it starts; CTA c takes pieces c, c + CTAs, ... of all tensors, a
+// thread the same four 16-byte vectors of each.  It loads its next piece's
+// vectors before it works on the current one's, whatever tensor and type they
+// belong to, and nothing but the end of the kernel needs a barrier.  A thread
+// keeps one fp32 sum per place in its vectors (emptied into a second one every
+// 16 pieces); a fixed tree adds them at the end, and the CTAs' sums are added
+// as pairs of floats.  So the order, and with it the last bits, depend on the
+// tensors' sizes, types and places within 16 bytes, and on nothing else.
 //
-// Sets of at most kClipClusterChunks chunks in at most 64 tensors run as one
+// Sets of at most kClipClusterPieces pieces in at most 64 tensors run as one
 // cluster of 8 CTAs in one launch: sums, norm and scaling.  Larger ones take a
 // launch for the sums and one for the scaling, whose CTAs each form the norm
-// from the at most 912 CTAs' sums; the second walks the chunks backwards, from
-// those that the first left in L2.  No CTA-wide barrier stands between a
-// warp's loads: chunks of 16384 elements by a whole CTA, with two barriers
-// each, reached 5.6 TB/s where warps alone reach %SUMSQ%.
+// from all CTAs' sums; the second takes the pieces in descending order, from
+// those that the first left in L2.
 #include <cooperative_groups.h>
 
 #include "rlk_ptx.cuh"
@@ -34,164 +31,210 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kVecs = kClipPieceBytes / 16 / kThreads;  // of a thread, in a piece
 constexpr int kClipCluster = 8;
+static_assert(kVecs == 4, "a thread's sums: two sets of four fp32, or one of eight 16-bit elements");
 
-template <int kType>
-struct Elem;
-template <>
-struct Elem<RLK_DTYPE_F32> {
-    using T = float;
-    static constexpr int kPer = 4;  // in 16 bytes
-    static __device__ __forceinline__ float get(T v) { return v; }
-    static __device__ __forceinline__ T put(float v) { return v; }
-};
-template <>
-struct Elem<RLK_DTYPE_BF16> {
-    using T = __nv_bfloat16;
-    static constexpr int kPer = 8;
-    static __device__ __forceinline__ float get(T v) { return __bfloat162float(v); }
-    static __device__ __forceinline__ T put(float v) { return __float2bfloat16_rn(v); }
-};
-template <>
-struct Elem<RLK_DTYPE_F16> {
-    using T = __half;
-    static constexpr int kPer = 8;
-    static __device__ __forceinline__ float get(T v) { return __half2float(v); }
-    static __device__ __forceinline__ T put(float v) { return __float2half_rn(v); }
+// A piece: bytes [lo, hi) of the 16 KB at `in`, which is 16-byte aligned and may start before the
+// tensor.  `out` is the output's counterpart of `in`, 16-byte aligned too or not.
+struct Piece {
+    const char* in;
+    char* out;
+    int lo, hi, type;
 };
 
-template <int kType>
-union Vec {
-    uint4 raw;
-    typename Elem<kType>::T e[Elem<kType>::kPer];
-    __device__ Vec() {}
-};
-
-// Elements [s, s + kPer) of p[0 .. len), 16-byte aligned; those outside are zero.
-template <int kType>
-__device__ __forceinline__ void load_vec(Vec<kType>& v, const typename Elem<kType>::T* p, int s, int len) {
-    constexpr int E = Elem<kType>::kPer;
-    if (s >= 0 && s + E <= len) {
-        v.raw = *reinterpret_cast<const uint4*>(p + s);
-    } else {
-        v.raw = make_uint4(0u, 0u, 0u, 0u);
-        if (s < len) {
-#pragma unroll
-            for (int r = 0; r < E; ++r)
-                if (s + r >= 0 && s + r < len) v.e[r] = p[s + r];
+// Piece c; `near`, the tensor that held the CTA's last piece, is tried first.
+template <typename Table>
+__device__ __forceinline__ Piece piece_of(const Table& t, int c, int& near) {
+    if (c < t.first[near] || c >= t.first[near + 1]) {
+        int lo = 0, hi = t.count - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (t.first[mid] <= c) lo = mid; else hi = mid - 1;
         }
+        near = lo;
     }
+    const ClipEntry& e = t.e[near];
+    const int lead = static_cast<int>(reinterpret_cast<uintptr_t>(e.in) & 15);
+    const int64_t at = static_cast<int64_t>(c - t.first[near]) * kClipPieceBytes;
+    const int64_t end = lead + e.n * (t.dtype[near] == RLK_DTYPE_F32 ? 4 : 2) - at;
+    Piece p;
+    p.in = static_cast<const char*>(e.in) - lead + at;
+    p.out = static_cast<char*>(e.out) - lead + at;
+    p.lo = at == 0 ? lead : 0;
+    p.hi = end < kClipPieceBytes ? static_cast<int>(end) : kClipPieceBytes;
+    p.type = t.dtype[near];
+    return p;
 }
 
-// How many elements before p the 16-byte line starts in which p lies.
-template <int kType>
-__device__ __forceinline__ int lead_of(const typename Elem<kType>::T* p) {
-    return static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15) / static_cast<int>(sizeof(*p));
-}
+__device__ __forceinline__ int vec_at(int m) { return (m * kThreads + static_cast<int>(threadIdx.x)) * 16; }
 
-// Sum of squares of one chunk p[0 .. len) by a warp, on every lane.
-template <int kType>
-__device__ __forceinline__ float chunk_sumsq(const void* base, int64_t at, int len, float* exchange) {
-    using El = Elem<kType>;
-    constexpr int E = El::kPer, kBatch = 4, kStep = 32 * E;
-    const int lane = threadIdx.x & 31;
-    const typename El::T* p = static_cast<const typename El::T*>(base) + at;
-    const int lead = lead_of<kType>(p);
-    float acc[E] = {};
-    for (int s0 = lane * E - lead; s0 < len; s0 += kBatch * kStep) {
-        Vec<kType> v[kBatch];
+struct Vecs {
+    uint4 v[kVecs];
+    // bytes outside [lo, hi) are zero
+    __device__ __forceinline__ void load(const Piece& p) {
 #pragma unroll
-        for (int m = 0; m < kBatch; ++m) load_vec<kType>(v[m], p, s0 + m * kStep, len);
-#pragma unroll
-        for (int m = 0; m < kBatch; ++m) {
-#pragma unroll
-            for (int r = 0; r < E; ++r) {
-                const float x = El::get(v[m].e[r]);
-                acc[r] = __fmaf_rn(x, x, acc[r]);
+        for (int m = 0; m < kVecs; ++m) {
+            const int b = vec_at(m);
+            if (b >= p.lo && b + 16 <= p.hi) {
+                v[m] = *reinterpret_cast<const uint4*>(p.in + b);
+            } else {
+                v[m] = b < p.hi ? edge(p.in + b, p.lo - b, p.hi - b) : make_uint4(0u, 0u, 0u, 0u);
             }
         }
     }
-    if (lead != 0) {
-        __syncwarp();
+    // the vector at q that the tensor starts or ends in: its bytes [lo, hi), kept apart from the
+    // whole ones' path (arguments and result in registers)
+    static __device__ __noinline__ uint4 edge(const char* q, int lo, int hi) {
+        uint32_t w[4];
 #pragma unroll
-        for (int r = 0; r < E; ++r) exchange[(lane * E + r - lead + kStep) % kStep] = acc[r];
-        __syncwarp();
-#pragma unroll
-        for (int r = 0; r < E; ++r) acc[r] = exchange[lane * E + r];
+        for (int r = 0; r < 4; ++r) {
+            w[r] = 4 * r >= lo && 4 * r < hi ? *reinterpret_cast<const uint16_t*>(q + 4 * r) : 0u;
+            if (4 * r + 2 >= lo && 4 * r + 2 < hi)
+                w[r] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(q + 4 * r + 2)) << 16;
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
-#pragma unroll
-    for (int n = E / 2; n >= 1; n >>= 1) {
-#pragma unroll
-        for (int i = 0; i < n; ++i) acc[i] = __fadd_rn(acc[2 * i], acc[2 * i + 1]);
-    }
-    return warp_sum(acc[0]);
+};
+
+__device__ __forceinline__ float2 halves(uint32_t w, int type) {
+    if (type == RLK_DTYPE_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-template <int kType>
-__device__ __forceinline__ void chunk_scale(const ClipEntry& t, int64_t at, int len, float scale) {
-    using El = Elem<kType>;
-    constexpr int E = El::kPer, kBatch = 4, kStep = 32 * E;
-    const int lane = threadIdx.x & 31;
-    const typename El::T* p = static_cast<const typename El::T*>(t.in) + at;
-    typename El::T* o = static_cast<typename El::T*>(t.out) + at;
-    const int lead = lead_of<kType>(p);
-    if (lead == lead_of<kType>(o)) {
-        for (int s0 = lane * E - lead; s0 < len; s0 += kBatch * kStep) {
-            Vec<kType> v[kBatch];
+struct Sums {
+    float low[8] = {}, high[8] = {};
+    __device__ __forceinline__ void add(const Vecs& x, int type) {
+        if (type == RLK_DTYPE_F32) {
 #pragma unroll
-            for (int m = 0; m < kBatch; ++m) load_vec<kType>(v[m], p, s0 + m * kStep, len);
+            for (int m = 0; m < kVecs; ++m) {
+                const uint32_t w[4] = {x.v[m].x, x.v[m].y, x.v[m].z, x.v[m].w};
 #pragma unroll
-            for (int m = 0; m < kBatch; ++m) {
-                const int s = s0 + m * kStep;
+                for (int r = 0; r < 4; ++r) {
+                    const float f = __uint_as_float(w[r]);
+                    low[(m & 1) * 4 + r] = __fmaf_rn(f, f, low[(m & 1) * 4 + r]);
+                }
+            }
+        } else {
 #pragma unroll
-                for (int r = 0; r < E; ++r) v[m].e[r] = El::put(__fmul_rn(El::get(v[m].e[r]), scale));
-                if (s >= 0 && s + E <= len) {
-                    __stcs(reinterpret_cast<uint4*>(o + s), v[m].raw);
-                } else if (s < len) {
+            for (int m = 0; m < kVecs; ++m) {
+                const uint32_t w[4] = {x.v[m].x, x.v[m].y, x.v[m].z, x.v[m].w};
 #pragma unroll
-                    for (int r = 0; r < E; ++r)
-                        if (s + r >= 0 && s + r < len) o[s + r] = v[m].e[r];
+                for (int r = 0; r < 4; ++r) {
+                    const float2 f = halves(w[r], type);
+                    low[2 * r] = __fmaf_rn(f.x, f.x, low[2 * r]);
+                    low[2 * r + 1] = __fmaf_rn(f.y, f.y, low[2 * r + 1]);
                 }
             }
         }
-    } else {
-        // input and output lie differently in their 16 bytes: element by element
-#pragma unroll 8
-        for (int i = lane; i < len; i += 32) o[i] = El::put(__fmul_rn(El::get(p[i]), scale));
+    }
+    __device__ __forceinline__ void empty() {
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            high[r] = __fadd_rn(high[r], low[r]);
+            low[r] = 0.0f;
+        }
+    }
+    __device__ __forceinline__ float2 total() {
+        empty();
+#pragma unroll
+        for (int n = 4; n >= 1; n >>= 1) {
+#pragma unroll
+            for (int i = 0; i < n; ++i) high[i] = __fadd_rn(high[2 * i], high[2 * i + 1]);
+        }
+        return pair_of(warp_sum(high[0]));
+    }
+};
+
+// Squares of pieces c0, c0 + step, ...: the sum of the warp's.
+template <typename Table>
+__device__ __forceinline__ float2 sum_pieces(const Table& t, int c0, int step) {
+    Sums sums;
+    const int total = t.first[t.count];
+    int near = 0, done = 0;
+    if (c0 < total) {
+        Piece p = piece_of(t, c0, near);
+        Vecs x, next;
+        x.load(p);
+        for (int c = c0; c < total; c += step) {
+            const int type = p.type;
+            if (c + step < total) {
+                p = piece_of(t, c + step, near);
+                next.load(p);
+            }
+            sums.add(x, type);
+            if ((++done & 15) == 0) sums.empty();
+            x = next;
+        }
+    }
+    return sums.total();
+}
+
+__device__ __forceinline__ uint32_t scaled_halves(uint32_t w, int type, float scale) {
+    const float2 f = halves(w, type);
+    const float a = __fmul_rn(f.x, scale), b = __fmul_rn(f.y, scale);
+    if (type == RLK_DTYPE_BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void store_piece(const Piece& p, Vecs& x, float scale) {
+#pragma unroll
+    for (int m = 0; m < kVecs; ++m) {
+        uint32_t w[4] = {x.v[m].x, x.v[m].y, x.v[m].z, x.v[m].w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            w[r] = p.type == RLK_DTYPE_F32 ? __float_as_uint(__fmul_rn(__uint_as_float(w[r]), scale))
+                                           : scaled_halves(w[r], p.type, scale);
+        x.v[m] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    const bool whole = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+#pragma unroll
+    for (int m = 0; m < kVecs; ++m) {
+        const int b = vec_at(m);
+        if (whole && b >= p.lo && b + 16 <= p.hi) {
+            __stcs(reinterpret_cast<uint4*>(p.out + b), x.v[m]);
+        } else if (b < p.hi) {
+            // the tensor starts or ends here, or the output lies differently in its 16 bytes
+            const uint32_t w[4] = {x.v[m].x, x.v[m].y, x.v[m].z, x.v[m].w};
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = b + 4 * r;
+                if (p.type == RLK_DTYPE_F32) {
+                    if (i >= p.lo && i < p.hi) *reinterpret_cast<uint32_t*>(p.out + i) = w[r];
+                } else {
+                    if (i >= p.lo && i < p.hi) *reinterpret_cast<uint16_t*>(p.out + i) = static_cast<uint16_t>(w[r]);
+                    if (i + 2 >= p.lo && i + 2 < p.hi)
+                        *reinterpret_cast<uint16_t*>(p.out + i + 2) = static_cast<uint16_t>(w[r] >> 16);
+                }
+            }
+        }
     }
 }
 
-// The tensor that holds chunk c; `near`, the one that held this warp's last chunk, is tried first.
+// Pieces c0, c0 - step, ... scaled; with a scale of 1 those in place stay as they are.
 template <typename Table>
-__device__ __forceinline__ int tensor_of(const Table& t, int c, int near) {
-    if (t.first[near] <= c && c < t.first[near + 1]) return near;
-    int lo = 0, hi = t.count - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (t.first[mid] <= c) lo = mid; else hi = mid - 1;
+__device__ __forceinline__ void scale_pieces(const Table& t, int c0, int step, float scale) {
+    int near = 0;
+    if (c0 < 0) return;
+    Piece p = piece_of(t, c0, near);
+    Vecs x, next;
+    bool skip = scale == 1.0f && p.in == p.out;
+    if (!skip) x.load(p);
+    for (int c = c0; c >= 0; c -= step) {
+        const Piece cur = p;
+        const bool cur_skip = skip;
+        if (c >= step) {
+            p = piece_of(t, c - step, near);
+            skip = scale == 1.0f && p.in == p.out;
+            if (!skip) next.load(p);
+        }
+        if (!cur_skip) store_piece(cur, x, scale);
+        x = next;
     }
-    return lo;
-}
-
-template <typename Table>
-__device__ __forceinline__ float table_sumsq(const Table& t, int c, int& near, float* exchange) {
-    const int k = near = tensor_of(t, c, near);
-    const int64_t at = static_cast<int64_t>(c - t.first[k]) * kClipChunk, left = t.e[k].n - at;
-    const int len = left < kClipChunk ? static_cast<int>(left) : kClipChunk;
-    return t.dtype[k] == RLK_DTYPE_F32    ? chunk_sumsq<RLK_DTYPE_F32>(t.e[k].in, at, len, exchange)
-           : t.dtype[k] == RLK_DTYPE_BF16 ? chunk_sumsq<RLK_DTYPE_BF16>(t.e[k].in, at, len, exchange)
-                                          : chunk_sumsq<RLK_DTYPE_F16>(t.e[k].in, at, len, exchange);
-}
-
-template <typename Table>
-__device__ __forceinline__ void table_scale(const Table& t, int c, int& near, float scale) {
-    const int k = near = tensor_of(t, c, near);
-    if (scale == 1.0f && t.e[k].in == t.e[k].out) return;
-    const int64_t at = static_cast<int64_t>(c - t.first[k]) * kClipChunk, left = t.e[k].n - at;
-    const int len = left < kClipChunk ? static_cast<int>(left) : kClipChunk;
-    if (t.dtype[k] == RLK_DTYPE_F32) chunk_scale<RLK_DTYPE_F32>(t.e[k], at, len, scale);
-    else if (t.dtype[k] == RLK_DTYPE_BF16) chunk_scale<RLK_DTYPE_BF16>(t.e[k], at, len, scale);
-    else chunk_scale<RLK_DTYPE_F16>(t.e[k], at, len, scale);
 }
 
 // A CTA's sum from its 8 warps', on thread 0.
@@ -227,53 +270,31 @@ __device__ __forceinline__ void write_norm(const ClipOut& o, float2 r) {
 }
 
 // ---------------------------------------------------------------- one launch
-// CTA r of the cluster stands for CTAs r, r + 8, ... of the launch for sums: its warps take those
-// CTAs' chunks, at most one each, so the sums meet in the same order.
 __global__ void __launch_bounds__(kThreads) k_clip_cluster(const __grid_constant__ ClipTableSmall t,
                                                            const ClipOut o) {
-    __shared__ float exchange[kWarps][32 * 8];
-    __shared__ float2 chunks[kClipClusterChunks];  // every chunk's sum, in every CTA
-    __shared__ float2 slots[kClipClusterChunks / kWarps];
+    __shared__ float2 slots[kClipCluster];  // every CTA's sum, in every CTA
     __shared__ float2 tmp[kWarps];
     cg::cluster_group cluster = cg::this_cluster();
     cluster.barrier_arrive();
-    const int rank = static_cast<int>(cluster.block_rank());
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int total = t.first[t.count];
-    int near = 0;
-    bool started = false;
-    for (int c = warp * kClipCluster + rank; c < total; c += kClipCluster * kWarps) {
-        const float s = table_sumsq(t, c, near, exchange[warp]);
-        if (!started) cluster.barrier_wait();  // every CTA has started: its shared memory may be written
-        started = true;
-        if (lane < kClipCluster) cluster.map_shared_rank(chunks, lane)[c] = pair_of(s);
+    const int rank = static_cast<int>(cluster.block_rank()), total = t.first[t.count];
+    const float2 sum = warps_sum(sum_pieces(t, rank, kClipCluster), tmp);
+    cluster.barrier_wait();  // every CTA has started: its shared memory may be written
+    if (threadIdx.x == 0) {
+        for (int c = 0; c < kClipCluster; ++c) cluster.map_shared_rank(slots, c)[rank] = sum;
     }
-    if (!started) cluster.barrier_wait();
     cluster.sync();
-    const int n = (total + kWarps - 1) / kWarps;
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        float2 v = chunks[i * kWarps];
-        for (int k = i * kWarps + 1; k < total && k < (i + 1) * kWarps; ++k) v = pair_add(v, chunks[k]);
-        slots[i] = v;
-    }
-    __syncthreads();
-    const float2 r = norm_and_scale(slots, n, o.max_norm, tmp);
-    if (rank == 0 && threadIdx.x == 0) write_norm(o, r);
-    if (!o.scale) return;
-    for (int c = warp * kClipCluster + rank; c < total; c += kClipCluster * kWarps) table_scale(t, c, near, r.y);
+    const float2 res = norm_and_scale(slots, kClipCluster, o.max_norm, tmp);
+    if (rank == 0 && threadIdx.x == 0) write_norm(o, res);
+    if (o.scale && total > rank)
+        scale_pieces(t, rank + (total - 1 - rank) / kClipCluster * kClipCluster, kClipCluster, res.y);
 }
 
 // ---------------------------------------------------------------- two launches
-__global__ void __launch_bounds__(kThreads, 6) k_grad_sumsq(const __grid_constant__ ClipTable t, float2* slots) {
-    __shared__ float exchange[kWarps][32 * 8];
+__global__ void __launch_bounds__(kThreads, kClipCtasPerSm) k_grad_sumsq(const __grid_constant__ ClipTable t,
+                                                                         float2* slots) {
     __shared__ float2 tmp[kWarps];
     ptx::grid_dependents_launch();
-    const int total = t.first[t.count], warp = threadIdx.x >> 5;
-    float2 sum = pair_of(0.0f);
-    int near = 0;
-    for (int c = blockIdx.x * kWarps + warp; c < total; c += kClipSlots * kWarps)
-        sum = pair_add(sum, pair_of(table_sumsq(t, c, near, exchange[warp])));
-    sum = warps_sum(sum, tmp);
+    const float2 sum = warps_sum(sum_pieces(t, blockIdx.x, gridDim.x), tmp);
     if (threadIdx.x == 0) slots[blockIdx.x] = sum;
 }
 
@@ -284,17 +305,13 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(const float2* slots, int
     if (threadIdx.x == 0) write_norm(o, r);
 }
 
-__global__ void __launch_bounds__(kThreads, 6) k_grad_scale(const __grid_constant__ ClipTable t, const float2* slots,
+__global__ void __launch_bounds__(kThreads, kClipCtasPerSm) k_grad_scale(const __grid_constant__ ClipTable t, const float2* slots,
                                                          int n, const ClipOut o, int write) {
     __shared__ float2 tmp[kThreads / 32];
     ptx::grid_dependency_wait();
     const float2 r = norm_and_scale(slots, n, o.max_norm, tmp);
-    const float scale = r.y;
     if (write && blockIdx.x == 0 && threadIdx.x == 0) write_norm(o, r);
-    int near = 0;
-    for (int c = t.first[t.count] - 1 - static_cast<int>(blockIdx.x * kWarps + (threadIdx.x >> 5)); c >= 0;
-         c -= static_cast<int>(gridDim.x) * kWarps)
-        table_scale(t, c, near, scale);
+    scale_pieces(t, t.first[t.count] - 1 - static_cast<int>(blockIdx.x), gridDim.x, r.y);
 }
 
 template <typename... Args>

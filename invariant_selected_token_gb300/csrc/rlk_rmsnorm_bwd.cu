@@ -74,10 +74,22 @@ __device__ __forceinline__ uint64_t pair_at(const uint4 (&w)[kPieces<kType>], in
         return f2_pack(__uint_as_float(q[p] << 16), __uint_as_float(q[p] & 0xFFFF0000u));
 }
 
+// fp32 features lie 32 bytes a thread: copied or stored 16 bytes at a time each thread for itself,
+// every access would touch half a 32-byte sector.  So lanes 2j and 2j + 1 take both halves of one
+// lane's features, then both of the other's: piece k holds lane 2j + k's features, the first four
+// in lane 2j's slot and the last four in lane 2j + 1's.
+__device__ __forceinline__ void read_f32(uint4 (&w)[2], const uint4* piece0, int threads) {
+    const bool odd = threadIdx.x & 1;
+    const uint4* const at = piece0 + (odd ? threads : 0);
+    const uint4 own = at[threadIdx.x], other = at[threadIdx.x ^ 1];
+    w[0] = odd ? other : own;
+    w[1] = odd ? own : other;
+}
+
 // A team of kWarps warps (a power of two) takes a row, a CTA's teams every kTeams-th row of its
-// range.  A thread copies its own features of the next kStages rows into its own ring of shared
-// memory, which no other thread reads: the copies need no barrier, and they fly while the current
-// row is reduced.  The arithmetic runs two features per instruction, each lane of which rounds
+// range.  A warp copies its own features of the next kStages rows into its own part of a ring of
+// shared memory: the copies need no CTA-wide barrier, and they fly while the current row is
+// reduced.  The arithmetic runs two features per instruction, each lane of which rounds
 // like the scalar one.
 template <int kWarps, int kGo, int kGx>
 __global__ void __launch_bounds__(kCtaThreads<kWarps, kGo, kGx>, 1) k_rmsnorm_backward(const RmsBwdArgs a) {
@@ -96,23 +108,28 @@ __global__ void __launch_bounds__(kCtaThreads<kWarps, kGo, kGx>, 1) k_rmsnorm_ba
     const int64_t r1 = static_cast<int64_t>(a.T) * (blockIdx.x + 1) / gridDim.x;
     const bool pow2 = (a.H & (a.H - 1)) == 0;
     const float h = static_cast<float>(a.H), inv_h = __fdiv_rn(1.0f, h);
-    auto piece = [&](int stage, int g, int k) { return ring + ((stage * 2 + g) * kGroup + k) * kThreads + threadIdx.x; };
+    const int odd = lane & 1;
+    auto piece = [&](int stage, int g, int k) { return ring + ((stage * 2 + g) * kGroup + k) * kThreads; };
+    // features i .. i + 7 of `base` into pieces k, k + 1
+    auto copy8 = [&](int type, const void* base, int64_t i, int stage, int g, int k) {
+        uint4* const to = piece(stage, g, k) + threadIdx.x;
+        if (type == RLK_DTYPE_F32) {
+            const char* const from = static_cast<const char*>(base) + (i - 8 * odd + 4 * odd) * 4;
+            copy16(to, from);
+            copy16(to + kThreads, from + 32);
+        } else {
+            copy16(to, static_cast<const char*>(base) + i * 2);
+        }
+    };
     auto fetch = [&](int64_t t, int stage) {
         if (t < r1) {
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
                 if (!in[g]) continue;
                 const int64_t i = t * a.H + i0 + 256 * g;
-                copy16(piece(stage, g, 0), reinterpret_cast<const char*>(a.x) + i * 2);
-#pragma unroll
-                for (int k = 0; k < kPieces<kGo>; ++k)
-                    copy16(piece(stage, g, 1 + k), static_cast<const char*>(a.grad_out) + i * (2 * kPieces<kGo>) + 16 * k);
-                if (a.grad_res) {
-#pragma unroll
-                    for (int k = 0; k < kPieces<kGx>; ++k)
-                        copy16(piece(stage, g, 1 + kPieces<kGo> + k),
-                               static_cast<const char*>(a.grad_res) + i * (2 * kPieces<kGx>) + 16 * k);
-                }
+                copy8(RLK_DTYPE_BF16, a.x, i, stage, g, 0);
+                copy8(kGo, a.grad_out, i, stage, g, 1);
+                if (a.grad_res) copy8(kGx, a.grad_res, i, stage, g, 1 + kPieces<kGo>);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -128,6 +145,7 @@ __global__ void __launch_bounds__(kCtaThreads<kWarps, kGo, kGx>, 1) k_rmsnorm_ba
     int slot = 0, stage = 0;
     for (; t < r1; t += kTeams) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kN - 1) : "memory");
+        __syncwarp();
         // the forward's tree over the squares: pairs of features, then lanes, groups and warps
         float s[2];
         uint64_t dot = 0;
@@ -135,9 +153,9 @@ __global__ void __launch_bounds__(kCtaThreads<kWarps, kGo, kGx>, 1) k_rmsnorm_ba
         for (int g = 0; g < 2; ++g) {
             uint4 x[1] = {}, dy[kPieces<kGo>] = {};
             if (in[g]) {
-                x[0] = *piece(stage, g, 0);
-#pragma unroll
-                for (int k = 0; k < kPieces<kGo>; ++k) dy[k] = *piece(stage, g, 1 + k);
+                x[0] = piece(stage, g, 0)[threadIdx.x];
+                if constexpr (kGo == RLK_DTYPE_F32) read_f32(dy, piece(stage, g, 1), kThreads);
+                else dy[0] = piece(stage, g, 1)[threadIdx.x];
             }
             float s2[4];
 #pragma unroll
@@ -154,7 +172,6 @@ __global__ void __launch_bounds__(kCtaThreads<kWarps, kGo, kGx>, 1) k_rmsnorm_ba
         f2_unpack(dot, d0, d1);
         float d = __fadd_rn(d0, d1);
         // even lanes go on with the first group, odd ones with the second
-        const bool odd = lane & 1;
         float q = __fadd_rn(odd ? s[1] : s[0], __shfl_xor_sync(0xffffffffu, odd ? s[0] : s[1], 1));
         d = __fadd_rn(d, __shfl_xor_sync(0xffffffffu, d, 1));
 #pragma unroll
@@ -190,14 +207,15 @@ __global__ void __launch_bounds__(kCtaThreads<kWarps, kGo, kGx>, 1) k_rmsnorm_ba
         const uint64_t rstd2 = f2_splat(rstd), neg_c2 = f2_splat(-c);
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-            if (!in[g]) continue;
-            uint4 x[1], dy[kPieces<kGo>], res[kPieces<kGx>] = {};
-            x[0] = *piece(stage, g, 0);
-#pragma unroll
-            for (int k = 0; k < kPieces<kGo>; ++k) dy[k] = *piece(stage, g, 1 + k);
-            if (a.grad_res) {
-#pragma unroll
-                for (int k = 0; k < kPieces<kGx>; ++k) res[k] = *piece(stage, g, 1 + kPieces<kGo> + k);
+            uint4 x[1] = {}, dy[kPieces<kGo>] = {}, res[kPieces<kGx>] = {};
+            if (in[g]) {
+                x[0] = piece(stage, g, 0)[threadIdx.x];
+                if constexpr (kGo == RLK_DTYPE_F32) read_f32(dy, piece(stage, g, 1), kThreads);
+                else dy[0] = piece(stage, g, 1)[threadIdx.x];
+                if (a.grad_res) {
+                    if constexpr (kGx == RLK_DTYPE_F32) read_f32(res, piece(stage, g, 1 + kPieces<kGo>), kThreads);
+                    else res[0] = piece(stage, g, 1 + kPieces<kGo>)[threadIdx.x];
+                }
             }
             uint64_t o[4];
 #pragma unroll
@@ -207,8 +225,28 @@ __global__ void __launch_bounds__(kCtaThreads<kWarps, kGo, kGx>, 1) k_rmsnorm_ba
                 o[p] = f2_fma(rstd2, f2_fma(v, neg_c2, up), pair_at<kGx>(res, p));
                 dg[g][p] = f2_fma(y, f2_mul(v, rstd2), dg[g][p]);
             }
-            store8<kGx>(a.grad_x, t * a.H + i0 + 256 * g, o);
+            const int64_t at = t * a.H + i0 + 256 * g;
+            if constexpr (kGx == RLK_DTYPE_F32) {
+                // even lanes hand their last four features over for the odd ones' first four
+                const uint64_t r0 = __shfl_xor_sync(0xffffffffu, odd ? o[0] : o[2], 1);
+                const uint64_t r1 = __shfl_xor_sync(0xffffffffu, odd ? o[1] : o[3], 1);
+                o[0] = odd ? r0 : o[0];
+                o[1] = odd ? r1 : o[1];
+                o[2] = odd ? o[2] : r0;
+                o[3] = odd ? o[3] : r1;
+                float e[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) f2_unpack(o[k], e[2 * k], e[2 * k + 1]);
+                if (in[g]) {
+                    float* const to = static_cast<float*>(a.grad_x) + at - 4 * odd;
+                    *reinterpret_cast<float4*>(to) = make_float4(e[0], e[1], e[2], e[3]);
+                    *reinterpret_cast<float4*>(to + 8) = make_float4(e[4], e[5], e[6], e[7]);
+                }
+            } else if (in[g]) {
+                store8<kGx>(a.grad_x, at, o);
+            }
         }
+        __syncwarp();
         fetch(t + kN * kTeams, stage);  // everything in this stage has been used
         stage = stage + 1 < kN ? stage + 1 : 0;
     }

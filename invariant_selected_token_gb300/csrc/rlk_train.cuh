@@ -83,7 +83,7 @@ template <int kMost>
 struct ClipTableOf {
     static constexpr int kSize = kMost;
     ClipEntry e[kMost];
-    int32_t first[kMost + 1];  // each tensor's first chunk within this launch
+    int32_t first[kMost + 1];  // each tensor's first piece within this launch
     uint8_t dtype[kMost];
     int count;
 };
@@ -95,14 +95,12 @@ struct ClipOut {
     int32_t* status;
     double max_norm;
 };
-constexpr int kClipChunk = 2048;         // elements that a warp sums at a time
-constexpr int kClipSlots = 152 * 6;      // most CTAs of a launch, a partial sum each
-constexpr int kClipClusterChunks = 384;  // largest set that one cluster does in one launch
-// CTAs, and partial sums, of a launch over so many chunks: 8 warps each.
-inline int clip_launch_slots(int64_t chunks) {
-    const int64_t ctas = (chunks + 7) / 8;
-    return static_cast<int>(ctas < kClipSlots ? ctas : kClipSlots);
-}
+constexpr int kClipPieceBytes = 16384;   // what a CTA works on at a time
+constexpr int kClipCtasPerSm = 4;
+constexpr int kClipSlots = 152 * kClipCtasPerSm;  // most CTAs of a launch, a partial sum each
+constexpr int kClipClusterPieces = 96;   // largest set that one cluster does in one launch
+// CTAs, and partial sums, of a launch over so many pieces.
+inline int clip_launch_slots(int64_t pieces) { return pieces < kClipSlots ? static_cast<int>(pieces) : kClipSlots; }
 cudaError_t launch_clip_cluster(const ClipTableSmall& t, const ClipOut& o, cudaStream_t stream);
 // A launch's slots are pairs of floats.
 cudaError_t launch_grad_sumsq(const ClipTable& t, float2* slots, cudaStream_t stream);

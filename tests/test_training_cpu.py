@@ -141,19 +141,22 @@ def test_grad_clip_refusals(L):
                dict(outs=(0x20000, 0x30000)),                   # an output over another's input
                dict(outs=(0x30000, 0x1003e))):                  # the input's last bytes
         refused(call, INVALID, **kw)
-    for kw in (dict(types=(0, 3)), dict(types=(-1, 0)), dict(sizes=((1 << 40) + 1, 1))):
+    for kw in (dict(types=(0, 3)), dict(types=(-1, 0)), dict(sizes=((1 << 38) + 1, 1)), dict(sizes=(1 << 37, (1 << 37) + 1))):
         refused(call, UNSUPPORTED, **kw)
     for kw in (dict(ptrs=(0x10002, 0x20000)), dict(ptrs=(0x10000, 0x20001)),
                dict(outs=(0x30002, 0x40000)), dict(ws=0x110)):
         refused(call, ALIGNMENT, **kw)
     refused(call, WORKSPACE, sizes=(1 << 20, 16), ptrs=(0x10000, 0x10000000), wsb=4)
-    small = (ctypes.c_int64 * 2)(383 * 2048, 2048)
-    assert L.rlk_grad_norm_workspace_size(small, 2) == 0  # one launch, no workspace
-    small[1] = 2049
-    assert L.rlk_grad_norm_workspace_size(small, 2) >= 49 * 8
-    sizes = (ctypes.c_int64 * 2)(-1, 4)
-    assert L.rlk_grad_norm_workspace_size(sizes, 2) == 0
-    assert L.rlk_grad_norm_workspace_size(None, 2) == 0
+    # 16 KB pieces, each tensor counted as if it started at the last byte of a 16-byte line
+    types = (ctypes.c_int32 * 2)(0, 1)
+    sizes = (ctypes.c_int64 * 2)(95 * 4096 - 4, 8192 - 8)
+    assert L.rlk_grad_norm_workspace_size(sizes, types, 2) == 0  # one launch, no workspace
+    sizes[1] += 1
+    assert L.rlk_grad_norm_workspace_size(sizes, types, 2) >= 97 * 8
+    sizes[0] = -1
+    assert L.rlk_grad_norm_workspace_size(sizes, types, 2) == 0
+    assert L.rlk_grad_norm_workspace_size(None, types, 2) == 0
+    assert L.rlk_grad_norm_workspace_size(sizes, None, 2) == 0
 
 
 def test_binding_refuses_host_tensors_and_wrong_types():
