@@ -514,6 +514,7 @@ GRAD_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _get_dtype = operator.attrgetter("dtype")
+_TENSOR_TYPES = {torch.Tensor, torch.nn.Parameter}
 
 
 def _choice(table, key, name: str) -> int:
@@ -727,7 +728,7 @@ def _grad_list(grads, name: str):
     device; lists of hundreds of tensors go through the C loops of map()."""
     if not grads:
         return None, [], [], []
-    if not all(isinstance(g, torch.Tensor) for g in grads):
+    if not set(map(type, grads)) <= _TENSOR_TYPES and not all(isinstance(g, torch.Tensor) for g in grads):
         raise TypeError("%s must be torch tensors" % name)
     dev = grads[0].device
     dtypes = list(map(_get_dtype, grads))

@@ -15,11 +15,14 @@
 // rounded ratio could go either way next to the border.
 //
 // The weights need counts of active tokens before the first gradient, so
-// the mask is read before anything else is formed.  Up to 4096 tokens one
+// the mask is read before anything else is formed.  Up to 1024 tokens one
 // CTA, up to 32768 one cluster of 8 does it all in one launch, its threads
-// holding their tokens meanwhile; beyond, a counting launch is followed by one
-// CTA per unit of 1024 tokens, the last of which adds up the units.  All add
-// the same numbers in the same order.
+// holding their tokens (one up to 8192, else four) meanwhile; beyond, a
+// counting launch is followed by one CTA per unit of 1024 tokens, the last of
+// which adds up the units.  All add the same numbers in the same order: a unit
+// is 8 spans of 128 consecutive tokens; lane l of a span adds RN(w x) of
+// tokens l, l + 32, l + 64, l + 96 pairwise, the lanes a shuffle tree, the
+// spans in order.
 #include <cooperative_groups.h>
 
 #include "rlk_ptx.cuh"
@@ -30,10 +33,9 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256;               // threads of a unit
-constexpr int kPer = kPolicyUnit / kThreads;
+constexpr int kThreads = 256;               // threads that a unit's sums are added by
+constexpr int kUnitWarps = kThreads / 32;
 constexpr int kCluster = 8;                 // most CTAs of the one-launch path
-constexpr int kGroups = 4;                  // units that one of them takes
 
 struct Bounds {
     int first, last;   // tokens outside [first, last) belong to no sequence
@@ -119,68 +121,78 @@ __device__ __forceinline__ TokenTerms token_terms(const PolicyArgs& a, float lp,
     return o;
 }
 
-// The tokens of one of a unit's 8 warps: 128 consecutive ones, lane l taking every 32nd.
-// Everything is loaded before anything is used, inactive tokens too (their values are dropped,
-// never multiplied).
-struct WarpTokens {
-    int64_t t0;
+// kPer of a lane's tokens, 32 apart.  Everything is loaded before anything is used, inactive
+// tokens too (their values are dropped, never multiplied).
+template <int kPer>
+struct Tokens {
+    int64_t t0;  // the first one
+    int left;    // tokens from it to the end of the batch
     float lp[kPer], old[kPer], ref[kPer], adv[kPer];
     bool on[kPer];
-    __device__ __forceinline__ int64_t token(int i) const { return t0 + i * 32 + (threadIdx.x & 31); }
-    __device__ __forceinline__ void load(const PolicyArgs& a, int64_t unit, int warp) {
-        t0 = unit * kPolicyUnit + warp * (kPer * 32);
+    __device__ __forceinline__ void load(const PolicyArgs& a, int64_t first) {
+        t0 = first;
+        left = first < a.T ? static_cast<int>(a.T - first) : 0;
+        const float *p_lp = a.logprob + t0, *p_old = a.old_logprob + t0;
+        const float *p_ref = a.ref_logprob + t0, *p_adv = a.advantages + t0;
+        const uint8_t* p_on = a.active + t0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const int64_t t = token(i);
-            const bool in = t < a.T;
-            lp[i] = in ? a.logprob[t] : 0.0f;
-            old[i] = in ? a.old_logprob[t] : 0.0f;
-            ref[i] = in && a.ref_logprob ? a.ref_logprob[t] : 0.0f;
-            adv[i] = in && !a.adv_per_seq ? a.advantages[t] : 0.0f;
-            on[i] = in && (!a.active || a.active[t] != 0);
+            const bool in = i * 32 < left;
+            lp[i] = in ? p_lp[i * 32] : 0.0f;
+            old[i] = in ? p_old[i * 32] : 0.0f;
+            ref[i] = in && a.ref_logprob ? p_ref[i * 32] : 0.0f;
+            adv[i] = in && !a.adv_per_seq ? p_adv[i * 32] : 0.0f;
+            on[i] = in && (!a.active || p_on[i * 32] != 0);
         }
     }
     // tokens of no sequence take no part
     __device__ __forceinline__ void cut(const Bounds& b) {
+        if (b.first <= t0 && b.last - t0 > (kPer - 1) * 32) return;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) on[i] = on[i] && token(i) >= b.first && token(i) < b.last;
+        for (int i = 0; i < kPer; ++i) on[i] = on[i] && t0 + i * 32 >= b.first && t0 + i * 32 < b.last;
     }
 };
 
-// Gradients of a warp's tokens out; its sums of the four stats, on every lane.  Every token is
+// Gradients of a lane's tokens out, and RN(w x) of the four stats x returned.  Every token is
 // worked on, the inactive ones with zeros for their values, so that the tokens' chains of
 // operations overlap; what an inactive one gives is dropped.
-__device__ __forceinline__ float4 policy_warp(const PolicyArgs& a, const WarpTokens& k, const float (&w)[kPer]) {
-    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+template <int kPer>
+__device__ __forceinline__ void policy_tokens(const PolicyArgs& a, const Tokens<kPer>& k, const float (&w)[kPer],
+                                              float4 (&out)[kPer]) {
     const float scale = static_cast<float>(a.scale);
+    float* const grad = a.grad + k.t0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const bool on = k.on[i];
         const TokenTerms o = token_terms(a, on ? k.lp[i] : 0.0f, on ? k.old[i] : 0.0f, on ? k.ref[i] : 0.0f,
                                          on ? k.adv[i] : 0.0f);
         const float wi = on ? w[i] : 0.0f;
-        sum.x = __fmaf_rn(wi, o.policy, sum.x);
-        sum.y = __fmaf_rn(wi, o.kl, sum.y);
-        sum.z = __fmaf_rn(wi, o.clipped, sum.z);
-        sum.w = __fmaf_rn(wi, o.neg_d, sum.w);
+        out[i] = make_float4(__fmul_rn(wi, o.policy), __fmul_rn(wi, o.kl), __fmul_rn(wi, o.clipped),
+                             __fmul_rn(wi, o.neg_d));
         const float g = on ? __fmul_rn(__fmul_rn(scale, wi), o.slope) : 0.0f;
-        if (a.grad && k.token(i) < a.T) a.grad[k.token(i)] = g;
+        if (a.grad && i * 32 < k.left) grad[i * 32] = g;
     }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        sum.x = __fadd_rn(sum.x, __shfl_xor_sync(0xffffffffu, sum.x, o));
-        sum.y = __fadd_rn(sum.y, __shfl_xor_sync(0xffffffffu, sum.y, o));
-        sum.z = __fadd_rn(sum.z, __shfl_xor_sync(0xffffffffu, sum.z, o));
-        sum.w = __fadd_rn(sum.w, __shfl_xor_sync(0xffffffffu, sum.w, o));
-    }
-    return sum;
 }
 
-// Component k of a unit's sum from its 8 warps' sums.
-__device__ __forceinline__ float unit_sum(const float4* warps, int k) {
+__device__ __forceinline__ float4 add4(const float4& a, const float4& b) {
+    return make_float4(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y), __fadd_rn(a.z, b.z), __fadd_rn(a.w, b.w));
+}
+
+// A span's sum from its lanes' four tokens.
+__device__ __forceinline__ float4 span_sum(const float4& p0, const float4& p1, const float4& p2, const float4& p3) {
+    float4 v = add4(add4(p0, p1), add4(p2, p3));
+#pragma unroll 1
+    for (int o = 16; o >= 1; o >>= 1)
+        v = add4(v, make_float4(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o),
+                                __shfl_xor_sync(0xffffffffu, v.z, o), __shfl_xor_sync(0xffffffffu, v.w, o)));
+    return v;
+}
+
+// Component k of a unit's sum from its 8 spans' sums.
+__device__ __forceinline__ float unit_sum(const float4* spans, int k) {
     float v = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) v = __fadd_rn(v, reinterpret_cast<const float*>(warps + i)[k]);
+    for (int i = 0; i < kUnitWarps; ++i) v = __fadd_rn(v, reinterpret_cast<const float*>(spans + i)[k]);
     return v;
 }
 
@@ -216,25 +228,25 @@ __device__ __forceinline__ int seq_in(const int32_t* offsets, int n, int t) {
     return lo;
 }
 
-// One cluster of kCtas CTAs, 4 units each: a thread holds its 4 tokens from the first load to
-// the gradient, and the counts that the weights need come from the masks it holds.
-template <int kCtas>
-__global__ void __launch_bounds__(kGroups * kThreads) k_policy_one(const PolicyArgs a) {
-    constexpr int kAll = kGroups * kThreads;
-    static_assert(kCtas * kGroups <= 32, "a lane per unit");
+// One cluster of kCtas CTAs of 1024 threads, kPer tokens a thread, which it holds from the first
+// load to the gradient; the counts that the weights need come from the masks it holds.
+template <int kCtas, int kPer>
+__global__ void __launch_bounds__(1024) k_policy_one(const PolicyArgs a) {
+    constexpr int kAll = 1024, kUnits = kPer;  // units of a CTA
+    static_assert(kCtas * kUnits <= 32, "a lane per unit");
+    static_assert(kPer == 1 || kPer == 4, "a warp is a quarter of a span, or one");
     __shared__ int32_t offsets[kLaunchSeqs + 1];
     __shared__ float adv[kLaunchSeqs];
     __shared__ int counts[kLaunchSeqs];
     __shared__ float weights[kLaunchSeqs];
     __shared__ float4 parts[32];           // the first CTA's are used
-    __shared__ float4 warps[kGroups][kThreads / 32];
+    __shared__ float4 spans[kUnits * kUnitWarps];
+    __shared__ float4 tokens[kPer == 1 ? kAll : 1];
     __shared__ int active_here;
     const int rank = kCtas > 1 ? static_cast<int>(blockIdx.x) : 0;
-    const int lane = threadIdx.x & 31, group = threadIdx.x / kThreads;
-    const int warp = (threadIdx.x % kThreads) >> 5;
-    const int unit = rank * kGroups + group;
-    WarpTokens k;
-    k.load(a, unit, warp);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Tokens<kPer> k;
+    k.load(a, (rank * (kAll / 32) + warp) * (32 * kPer) + lane);
     const bool masked = a.active != nullptr, by_mean = a.reduction == RLK_REDUCE_SEQ_MEAN;
     const bool by_seq = a.offsets && (a.adv_per_seq || by_mean);
     Bounds bd = {0, a.T};
@@ -256,14 +268,14 @@ __global__ void __launch_bounds__(kGroups * kThreads) k_policy_one(const PolicyA
     k.cut(bd);
     int seq[kPer] = {};
     if (by_seq) {
-        // a warp's 128 tokens: mostly of one sequence
-        const int64_t tl = k.t0 + kPer * 32 - 1;
-        const int lo = k.t0 < a.T ? seq_in(offsets, a.n_seqs, static_cast<int>(k.t0)) : 0;
-        const int hi = k.t0 < a.T ? seq_in(offsets, a.n_seqs, static_cast<int>(tl < a.T ? tl : a.T - 1)) : 0;
+        // a warp's tokens: mostly of one sequence
+        const int64_t tf = k.t0 - lane, tl = tf + kPer * 32 - 1;
+        const int lo = tf < a.T ? seq_in(offsets, a.n_seqs, static_cast<int>(tf)) : 0;
+        const int hi = tf < a.T ? seq_in(offsets, a.n_seqs, static_cast<int>(tl < a.T ? tl : a.T - 1)) : 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             seq[i] = lo;
-            if (hi > lo && k.on[i]) seq[i] = lo + seq_in(offsets + lo, hi - lo + 1, static_cast<int>(k.token(i)));
+            if (hi > lo && k.on[i]) seq[i] = lo + seq_in(offsets + lo, hi - lo + 1, static_cast<int>(k.t0) + i * 32);
         }
     }
     int n_all = bd.last - bd.first;
@@ -313,20 +325,32 @@ __global__ void __launch_bounds__(kGroups * kThreads) k_policy_one(const PolicyA
         w[i] = by_mean ? weights[seq[i]] : w_all;
         if (a.adv_per_seq) k.adv[i] = adv[seq[i]];
     }
-    const float4 s = policy_warp(a, k, w);
-    if (lane == 0) warps[group][warp] = s;
+    float4 terms[kPer];
+    policy_tokens(a, k, w, terms);
+    if constexpr (kPer == 4) {
+        const float4 s = span_sum(terms[0], terms[1], terms[2], terms[3]);
+        if (lane == 0) spans[warp] = s;
+    } else {
+        tokens[threadIdx.x] = terms[0];
+        __syncthreads();
+        if (warp < kUnitWarps) {
+            const float4* const p = tokens + warp * 128 + lane;
+            const float4 s = span_sum(p[0], p[32], p[64], p[96]);
+            if (lane == 0) spans[warp] = s;
+        }
+    }
     __syncthreads();
     float4* all_parts = parts;
     if constexpr (kCtas > 1) all_parts = cg::this_cluster().map_shared_rank(parts, 0);
-    if (threadIdx.x % kThreads < 4)
-        reinterpret_cast<float*>(all_parts + unit)[threadIdx.x % kThreads] =
-            unit_sum(warps[group], threadIdx.x % kThreads);
+    if (threadIdx.x < 4 * kUnits)
+        reinterpret_cast<float*>(all_parts + rank * kUnits)[threadIdx.x] =
+            unit_sum(spans + threadIdx.x / 4 * kUnitWarps, threadIdx.x % 4);
     if constexpr (kCtas > 1) cg::this_cluster().sync(); else __syncthreads();
     if (rank != 0 || threadIdx.x >= 3 * 32) return;
     // units 0 .. 31 are the first warp's slots of the order above; the rest of it adds zeros.
     // Warp 0 forms the loss and the two stats in it, warps 1 and 2 the others.
     const float* p = reinterpret_cast<const float*>(parts + lane);
-    const bool have = lane < kCtas * kGroups;
+    const bool have = lane < kCtas * kUnits;
     const int which = threadIdx.x >> 5;
     const float2 v = warp_sum(pair_of(have ? p[which == 0 ? 0 : which + 1] : 0.0f));
     if (which == 0) {
@@ -343,16 +367,20 @@ __global__ void __launch_bounds__(kGroups * kThreads) k_policy_one(const PolicyA
 
 // ---------------------------------------------------------------- two launches
 // Each sequence's weight (seq_mean), or the active tokens in each block's share of the sequences
-// (token_mean); and the main kernel's ticket set to 0.
+// (token_mean); and the main kernel's ticket set to 0.  Long sequences are counted by a cluster
+// each: one of 1.77 M tokens by a single CTA took 25 us.
 __global__ void __launch_bounds__(1024) k_policy_count(const PolicyArgs a) {
     __shared__ int smem[32];
+    __shared__ int counted;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int size = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
     const int threads = blockDim.x;
     ptx::grid_dependents_launch();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
     const bool per_seq = a.reduction == RLK_REDUCE_SEQ_MEAN;
     if (a.reduction == RLK_REDUCE_SUM || (!per_seq && !a.active)) return;
     const int rows = per_seq ? a.n_seqs : kPolicyCountBlocks;
-    for (int s = blockIdx.x; s < rows; s += gridDim.x) {
+    for (int s = blockIdx.x / size; s < rows; s += gridDim.x / size) {
         int64_t b = 0, e = a.T;
         if (per_seq) {
             if (a.offsets) {
@@ -368,14 +396,24 @@ __global__ void __launch_bounds__(1024) k_policy_count(const PolicyArgs a) {
         }
         int n = static_cast<int>(e - b);
         if (a.active) {
-            n = __reduce_add_sync(0xffffffffu, count_active(a.active, b, e, a.T, threadIdx.x, threads));
+            n = __reduce_add_sync(0xffffffffu, count_active(a.active, b, e, a.T, rank * threads + threadIdx.x,
+                                                            size * threads));
             if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = n;
             __syncthreads();
             n = 0;
             for (int i = 0; i < threads / 32; ++i) n += smem[i];
-            __syncthreads();
+            if (size > 1) {
+                if (threadIdx.x == 0) counted = n;
+                cluster.sync();
+                if (rank == 0 && threadIdx.x == 0) {
+                    for (int c = 1; c < size; ++c) n += *cluster.map_shared_rank(&counted, c);
+                }
+                cluster.sync();
+            } else {
+                __syncthreads();
+            }
         }
-        if (threadIdx.x == 0) {
+        if (rank == 0 && threadIdx.x == 0) {
             if (per_seq) a.weights[s] = seq_weight(a, n);
             else a.counts[s] = n;
         }
@@ -383,13 +421,15 @@ __global__ void __launch_bounds__(1024) k_policy_count(const PolicyArgs a) {
 }
 
 __global__ void __launch_bounds__(kThreads, 5) k_policy_main(const PolicyArgs a) {
-    __shared__ float4 warps[kThreads / 32];
+    constexpr int kPer = kPolicyUnit / kThreads;
+    __shared__ float4 spans[kUnitWarps];
     __shared__ float2 finish[kThreads / 32][4];
     __shared__ bool last_here;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t units = (static_cast<int64_t>(a.T) + kPolicyUnit - 1) / kPolicyUnit;
-    WarpTokens k;
-    k.load(a, blockIdx.x, warp);
+    const int at = warp * 32 * kPer + lane;
+    Tokens<kPer> k;
+    k.load(a, blockIdx.x * static_cast<int64_t>(kPolicyUnit) + at);
     const Bounds bd = bounds_of(a);
     const bool by_mean = a.reduction == RLK_REDUCE_SEQ_MEAN;
     const bool by_seq = a.offsets && (a.adv_per_seq || by_mean);
@@ -403,27 +443,29 @@ __global__ void __launch_bounds__(kThreads, 5) k_policy_main(const PolicyArgs a)
     }
     const float w_all = token_weight(a, n_all);
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        if (u != blockIdx.x) k.load(a, u, warp);
+        if (u != blockIdx.x) k.load(a, u * kPolicyUnit + at);
         k.cut(bd);
         float w[kPer];
         int lo = 0, hi = 0;
-        if (by_seq && k.t0 < a.T) {
-            const int64_t tl = k.t0 + kPer * 32 - 1;
-            lo = warp_find_seq(a.offsets, a.n_seqs, static_cast<int>(k.t0));
+        const int64_t tf = k.t0 - lane, tl = tf + kPer * 32 - 1;
+        if (by_seq && tf < a.T) {
+            lo = warp_find_seq(a.offsets, a.n_seqs, static_cast<int>(tf));
             hi = warp_find_seq(a.offsets, a.n_seqs, static_cast<int>(tl < a.T ? tl : a.T - 1));
         }
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             w[i] = w_all;
             if (!k.on[i]) continue;
-            const int s = hi > lo ? find_seq(a.offsets, lo, hi, static_cast<int>(k.token(i))) : lo;
+            const int s = hi > lo ? find_seq(a.offsets, lo, hi, static_cast<int>(k.t0) + i * 32) : lo;
             if (by_mean) w[i] = a.weights[s];
             if (a.adv_per_seq) k.adv[i] = a.advantages[s];
         }
-        const float4 s = policy_warp(a, k, w);
-        if (lane == 0) warps[warp] = s;
+        float4 terms[kPer];
+        policy_tokens(a, k, w, terms);
+        const float4 s = span_sum(terms[0], terms[1], terms[2], terms[3]);
+        if (lane == 0) spans[warp] = s;
         __syncthreads();
-        if (threadIdx.x < 4) reinterpret_cast<float*>(a.parts + u)[threadIdx.x] = unit_sum(warps, threadIdx.x);
+        if (threadIdx.x < 4) reinterpret_cast<float*>(a.parts + u)[threadIdx.x] = unit_sum(spans, threadIdx.x);
         __syncthreads();
     }
     // the last CTA to come here adds up the units
@@ -465,45 +507,54 @@ __global__ void __launch_bounds__(kThreads, 5) k_policy_main(const PolicyArgs a)
     }
 }
 
-template <int kCtas>
+template <int kCtas, int kPer>
 cudaError_t launch_one(const PolicyArgs& a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.stream = stream;
     cfg.gridDim = dim3(kCtas, 1, 1);
-    cfg.blockDim = dim3(kGroups * kThreads, 1, 1);
+    cfg.blockDim = dim3(1024, 1, 1);
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = kCtas;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = kCtas > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k_policy_one<kCtas>, a);
+    return cudaLaunchKernelEx(&cfg, k_policy_one<kCtas, kPer>, a);
 }
 
 }  // namespace
 
 bool policy_one_launch(int64_t T, int64_t n_seqs) {
-    return T <= kCluster * kGroups * kPolicyUnit && n_seqs <= kLaunchSeqs;
+    return T <= kCluster * 1024 * 4 && n_seqs <= kLaunchSeqs;
 }
 
 cudaError_t launch_policy_loss(const PolicyArgs& a, int num_sms, cudaStream_t stream) {
     if (policy_one_launch(a.T, a.n_seqs))
-        return a.T <= kGroups * kPolicyUnit ? launch_one<1>(a, stream) : launch_one<kCluster>(a, stream);
+        return a.T <= 1024              ? launch_one<1, 1>(a, stream)
+               : a.T <= kCluster * 1024 ? launch_one<kCluster, 1>(a, stream)
+                                        : launch_one<kCluster, 4>(a, stream);
     int rows = 1;
     if (a.reduction == RLK_REDUCE_SEQ_MEAN) rows = a.n_seqs;
     else if (a.active && a.reduction == RLK_REDUCE_TOKEN_MEAN) rows = kPolicyCountBlocks;
     const int most = num_sms * 8;
     if (rows > most) rows = most;
-    // a few long sequences want many threads each
-    const int threads = a.reduction == RLK_REDUCE_SEQ_MEAN && a.T / (a.n_seqs > 0 ? a.n_seqs : 1) > 16384 ? 1024 : kThreads;
-    k_policy_count<<<rows > 0 ? rows : 1, threads, 0, stream>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    const int64_t units = (static_cast<int64_t>(a.T) + kPolicyUnit - 1) / kPolicyUnit;
+    const bool lengthy = a.active && a.reduction == RLK_REDUCE_SEQ_MEAN && a.n_seqs > 0 && a.T / a.n_seqs > 16384;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const int size = lengthy ? kCluster : 1;
+    cfg.gridDim = dim3(static_cast<unsigned>((rows > 0 ? rows : 1) * size), 1, 1);
+    cfg.blockDim = dim3(lengthy ? 1024 : kThreads, 1, 1);
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_policy_count, a);
+    if (e != cudaSuccess) return e;
+    const int64_t units = (static_cast<int64_t>(a.T) + kPolicyUnit - 1) / kPolicyUnit;
     // a CTA per unit, as far as the ticket and the weights' loads stay small against the work
     const int64_t ctas = units < 4 * most ? units : 4 * most;
     cfg.gridDim = dim3(static_cast<unsigned>(ctas > 0 ? ctas : 1), 1, 1);

@@ -15,14 +15,14 @@
 // chunk g is added to slot g mod 1024 in ascending order, and the slots are
 // added by a fixed tree.  All sums are pairs of floats.
 //
-// Batches of up to kPreferenceClusterTokens tokens run as one cluster in one
-// launch: a pair is the work of a team of 1, 2, 4 or 8 of its CTAs, which
-// meet in the shared memory of the team's first one (slots in, the two
-// sequences' slopes out), and the first CTA adds up the pairs' losses.
-// Larger batches of many pairs run the same kernel with a team per pair and
-// add up in a second launch.  Larger batches of a few pairs, whose teams
-// would leave most of the device idle, take one launch over all chunks and
-// one over all tokens, whose CTAs each form the slopes they need.
+// Up to 8 pairs of up to kPreferenceClusterTokens tokens in all run as one
+// cluster in one launch: a pair is the work of a team of 1, 2, 4 or 8 of its
+// CTAs, which meet in the shared memory of the team's first one (slots in, the
+// two sequences' slopes out), and the first CTA adds up the pairs' losses.
+// More pairs or tokens run the same kernel with a team per pair and add up in
+// a second launch.  A few very long pairs, whose teams would leave most of the
+// device idle, take one launch over all chunks and one over all tokens, whose
+// CTAs each form the slopes they need.
 #include <cooperative_groups.h>
 
 #include "rlk_ptx.cuh"
@@ -33,12 +33,11 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kThreads = 512;            // of a CTA; 128 for short pairs
+constexpr int kWarps = kThreads / 32;    // warps of the sums' order, whatever the CTA has
 constexpr int kChunk = 256;
 constexpr int kSlots = 1024;
 constexpr int kCluster = 8;
-constexpr int kHeldPairs = 512;  // pairs whose losses one cluster keeps in shared memory
 
 struct Span {
     int64_t b, e;
@@ -120,7 +119,7 @@ __device__ __forceinline__ int64_t rejected_of(const PreferenceArgs& a, int pair
 __device__ __forceinline__ bool offsets_bad(const PreferenceArgs& a) {
     bool bad = false;
     const int64_t n = 2 * static_cast<int64_t>(a.n_pairs);
-    for (int64_t s = threadIdx.x; s <= n; s += kThreads) {
+    for (int64_t s = threadIdx.x; s <= n; s += blockDim.x) {
         const int b = a.offsets[s], e = s < n ? a.offsets[s + 1] : a.T;
         bad |= b < 0 || e < b || e > a.T;
     }
@@ -129,13 +128,13 @@ __device__ __forceinline__ bool offsets_bad(const PreferenceArgs& a) {
 
 // The loss from the pairs' losses, by a whole CTA.
 __device__ __forceinline__ void preference_finish(const PreferenceArgs& a, const float* losses, bool bad, float2* tmp) {
-    const int warp = threadIdx.x >> 5;
     bad = __syncthreads_or(bad);
-    if (warp * 32 < a.n_pairs) {  // the other warps would add zeros
+    // warp w of 16 takes losses 32 w + lane, + 512, ...; those without any would add zeros
+    for (int w = threadIdx.x >> 5; w < kWarps && w * 32 < a.n_pairs; w += blockDim.x >> 5) {
         float2 v = pair_of(0.0f);
-        for (int i = threadIdx.x; i < a.n_pairs; i += kThreads) v = pair_add(v, pair_of(losses[i]));
+        for (int i = w * 32 + (threadIdx.x & 31); i < a.n_pairs; i += kThreads) v = pair_add(v, pair_of(losses[i]));
         v = warp_sum(v);
-        if ((threadIdx.x & 31) == 0) tmp[warp] = v;
+        if ((threadIdx.x & 31) == 0) tmp[w] = v;
     }
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -159,20 +158,17 @@ __device__ __forceinline__ float2 chunk_sum(const PreferenceArgs& a, const Span&
         ref[i] = in && a.ref_logprob ? a.ref_logprob[t] : 0.0f;
         on[i] = in && (!a.active || a.active[t] != 0);
     }
-    float2 acc[kChunk / 32];
+    float2 acc = pair_of(0.0f);
     int n = 0;
 #pragma unroll
     for (int i = 0; i < kChunk / 32; ++i) {
         n += on[i];
-        acc[i] = two_diff(on[i] ? lp[i] : 0.0f, on[i] ? ref[i] : 0.0f);
-    }
-#pragma unroll
-    for (int m = kChunk / 64; m >= 1; m >>= 1) {
-#pragma unroll
-        for (int i = 0; i < m; ++i) acc[i] = pair_add(acc[2 * i], acc[2 * i + 1]);
+        const float2 d = two_diff(on[i] ? lp[i] : 0.0f, on[i] ? ref[i] : 0.0f);
+        two_add(acc, d.x);
+        acc.y = __fadd_rn(acc.y, d.y);
     }
     *count = __reduce_add_sync(0xffffffffu, n);
-    return warp_sum(acc[0]);
+    return warp_sum(pair_add(acc, pair_of(0.0f)));
 }
 
 __device__ __forceinline__ int64_t chunks_of(const Span& s) { return (s.e - s.b + kChunk - 1) / kChunk; }
@@ -188,24 +184,26 @@ struct PairScratch {
 template <typename SlotOf, typename CountOf>
 __device__ __forceinline__ void reduce_pair(const PreferenceArgs& a, int pair, const Span (&sp)[2], SlotOf slot,
                                             CountOf count, bool write, PairScratch& sc, float* slope, float* held_loss) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
     int held[2];
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
         const int64_t c = chunks_of(sp[side]);
         held[side] = c < kSlots ? static_cast<int>(c) : kSlots;
-        if (warp * 32 >= held[side]) continue;  // empty slots add zeros
-        float2 v = pair_of(0.0f);
-        int n = 0;
-        for (int i = threadIdx.x; i < held[side]; i += kThreads) {
-            v = pair_add(v, slot(side, i));
-            n += count(side, i);
-        }
-        v = warp_sum(v);
-        n = __reduce_add_sync(0xffffffffu, n);
-        if (lane == 0) {
-            sc.tmp[side][warp] = v;
-            sc.n[side][warp] = n;
+        // warp w of 16 takes slots 32 w + lane and + 512; those without any would add zeros
+        for (int w = threadIdx.x >> 5; w < kWarps && w * 32 < held[side]; w += blockDim.x >> 5) {
+            float2 v = pair_of(0.0f);
+            int n = 0;
+            for (int i = w * 32 + lane; i < held[side]; i += kThreads) {
+                v = pair_add(v, slot(side, i));
+                n += count(side, i);
+            }
+            v = warp_sum(v);
+            n = __reduce_add_sync(0xffffffffu, n);
+            if (lane == 0) {
+                sc.tmp[side][w] = v;
+                sc.n[side][w] = n;
+            }
         }
     }
     __syncthreads();
@@ -226,16 +224,16 @@ __device__ __forceinline__ void reduce_pair(const PreferenceArgs& a, int pair, c
 // ---------------------------------------------------------------- a team of CTAs per pair
 // One launch of clusters; every `team` CTAs of a cluster take a pair at a time.  alone: this is
 // the only cluster, and it also forms the loss.
-__global__ void __launch_bounds__(kThreads) k_preference(const PreferenceArgs a, int team, int alone) {
+__global__ void __launch_bounds__(kThreads, 2) k_preference(const PreferenceArgs a, int team, int alone) {
     __shared__ float2 slots[2][kSlots];
     __shared__ int counts[2][kSlots];
     __shared__ PairScratch scratch;
     __shared__ float slope[2];
-    __shared__ float losses[kHeldPairs];  // the first CTA's, when alone
+    __shared__ float losses[kCluster];  // the first CTA's, when alone
     cg::cluster_group cluster = cg::this_cluster();
     cluster.barrier_arrive();
     const int rank = static_cast<int>(cluster.block_rank()), size = static_cast<int>(cluster.num_blocks());
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int member = rank % team, lead = rank - member;
     const int teams = size / team;
     const int stride = gridDim.x / team;  // pairs in flight
@@ -258,7 +256,7 @@ __global__ void __launch_bounds__(kThreads) k_preference(const PreferenceArgs a,
 #pragma unroll 1
         for (int side = 0; side < 2; ++side) {
             const Span& s = sp[side];
-            for (int64_t g = member * kWarps + warp; s.b + g * kChunk < s.e; g += team * kWarps) {
+            for (int64_t g = member * warps + warp; s.b + g * kChunk < s.e; g += team * warps) {
                 int n;
                 const float2 v = chunk_sum(a, s, g, &n);
                 if (lane == 0) {
@@ -276,7 +274,7 @@ __global__ void __launch_bounds__(kThreads) k_preference(const PreferenceArgs a,
                         alone ? all_losses + pair : nullptr);
         if (team > 1) cluster.sync(); else __syncthreads();
         if (a.grad && work) {
-            const int who = member * kThreads + threadIdx.x, all = team * kThreads;
+            const int who = member * blockDim.x + threadIdx.x, all = team * blockDim.x;
 #pragma unroll
             for (int side = 0; side < 2; ++side) {
                 const float g = lead_slope[side];
@@ -438,12 +436,13 @@ __global__ void __launch_bounds__(kThreads) k_preference_spread(const Preference
     preference_finish(a, a.out_pair_loss, map.bad != 0, scratch.tmp[0]);
 }
 
-cudaError_t launch_clusters(const PreferenceArgs& a, int clusters, int size, int team, int alone, cudaStream_t stream) {
+cudaError_t launch_clusters(const PreferenceArgs& a, int clusters, int size, int team, int alone, int threads,
+                            cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.stream = stream;
     cfg.gridDim = dim3(static_cast<unsigned>(clusters * size), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -469,7 +468,7 @@ cudaError_t launch_after(void (*kernel)(PreferenceArgs), int blocks, const Prefe
 }  // namespace
 
 bool preference_split(int64_t T, int64_t n_pairs) {
-    return T > kPreferenceClusterTokens && 2 * n_pairs <= kSplitSeqs && n_pairs > 0;
+    return n_pairs > 0 && 2 * n_pairs <= kSplitSeqs && T / n_pairs >= kPreferenceSplitTokens;
 }
 
 int64_t preference_chunks(int64_t T, int64_t n_pairs) { return T / kChunk + 2 * n_pairs; }
@@ -480,10 +479,11 @@ cudaError_t launch_preference_loss(const PreferenceArgs& a, int num_sms, cudaStr
             const cudaError_t e = cudaMemsetAsync(a.grad, 0, size_t(a.T) * sizeof(float), stream);
             if (e != cudaSuccess) return e;
         }
-        return launch_clusters(a, 1, 1, 1, 1, stream);
+        return launch_clusters(a, 1, 1, 1, 1, 128, stream);
     }
     const int64_t mean = a.T / a.n_pairs;  // tokens of a pair, about
-    if (a.T <= kPreferenceClusterTokens && a.n_pairs <= kHeldPairs) {
+    const int threads = mean <= 1024 ? 128 : kThreads;
+    if (a.T <= kPreferenceClusterTokens && a.n_pairs <= kCluster) {
         // a CTA for every pair, and several where the pairs are long and few
         int size = 1, team = 1;
         while (size < kCluster && size < a.n_pairs) size *= 2;
@@ -491,7 +491,7 @@ cudaError_t launch_preference_loss(const PreferenceArgs& a, int num_sms, cudaStr
             size *= 2;
             team *= 2;
         }
-        return launch_clusters(a, 1, size, team, 1, stream);
+        return launch_clusters(a, 1, size, team, 1, threads, stream);
     }
     if (preference_split(a.T, a.n_pairs)) {
         const int64_t chunks = preference_chunks(a.T, a.n_pairs);
@@ -505,8 +505,9 @@ cudaError_t launch_preference_loss(const PreferenceArgs& a, int num_sms, cudaStr
     // CTAs per pair: enough to fill the device, and none with less than 4096 tokens
     int team = 1;
     while (team < kCluster && static_cast<int64_t>(a.n_pairs) * team < num_sms * 2 && mean / (2 * team) >= 4096) team *= 2;
-    const int64_t most = static_cast<int64_t>(num_sms) * 16 / team;
-    const cudaError_t e = launch_clusters(a, static_cast<int>(a.n_pairs < most ? a.n_pairs : most), team, team, 0, stream);
+    const int64_t most = static_cast<int64_t>(num_sms) * 64 / team;
+    const cudaError_t e = launch_clusters(a, static_cast<int>(a.n_pairs < most ? a.n_pairs : most), team, team, 0,
+                                          threads, stream);
     if (e != cudaSuccess) return e;
     return launch_after(k_preference_final, 1, a, stream);
 }

@@ -67,6 +67,7 @@ struct PreferenceArgs {
     int32_t* status;
 };
 constexpr int64_t kPreferenceClusterTokens = 32768;  // largest batch that one cluster does alone
+constexpr int64_t kPreferenceSplitTokens = 65536;    // smallest pairs of the path over all chunks
 // Whether a batch takes the path over all chunks, and how many of them it has at most.
 bool preference_split(int64_t T, int64_t n_pairs);
 int64_t preference_chunks(int64_t T, int64_t n_pairs);
@@ -161,7 +162,9 @@ __device__ __forceinline__ double pair_value(float2 v) {
     return __dadd_rn(static_cast<double>(v.x), static_cast<double>(v.y));
 }
 __device__ __forceinline__ float2 warp_sum(float2 v) {
-#pragma unroll
+    // not unrolled: a dependent chain either way, and small kernels pay for every line of code that
+    // they fetch for the first time
+#pragma unroll 1
     for (int o = 16; o >= 1; o >>= 1)
         v = pair_add(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
     return v;
@@ -209,9 +212,9 @@ __device__ __forceinline__ float exp_minus_1_minus(float u) {
     p = __fmaf_rn(p, u, 0x1.555556p-5f);   // 1/4!
     p = __fmaf_rn(p, u, 0x1.555556p-3f);   // 1/3!
     p = __fmaf_rn(p, u, 0.5f);             // 1/2!
-    const float near = __fmul_rn(__fmul_rn(u, u), p);
-    const float far = __fsub_rn(__fsub_rn(exp_any(u), 1.0f), u);
-    return fabsf(u) < 0.5f ? near : far;
+    p = __fmul_rn(__fmul_rn(u, u), p);
+    if (!(fabsf(u) < 0.5f)) p = __fsub_rn(__fsub_rn(exp_any(u), 1.0f), u);
+    return p;
 }
 
 // log(1 + e) for e in [0, 1]: 2 atanh(v), v = e / (2 + e) <= 1/3, by the odd series through

@@ -6,8 +6,9 @@ r A, w (two conversions, a product and a division: 4u), scale w and the last pro
 term and its gradient are within 12 u |w r A|.  The KL terms: u' = ref - lp is rounded (u |u'|,
 which moves e^u' by |u'| u e^u'), the series or e^u' - 1 - u' then errs by at most
 4 u (e^u' + 1 + |u'|); the coefficient's rounding, w and the products add 8 u of the value.  A sum
-of n positive-weight terms by the kernel's tree adds at most 21 roundings in fp32 (8 in a thread,
-13 in the block's tree) of its absolute sum, then sums as pairs of floats and one rounding."""
+of n positive-weight terms by the kernel's tree adds at most 16 roundings in fp32 (the product with
+w, 2 over a lane's tokens, 5 over the lanes, 8 over the spans) of its absolute sum, then sums as
+pairs of floats and one rounding."""
 import numpy as np
 import pytest
 import torch
@@ -189,6 +190,24 @@ def test_nothing_active(rlk, cuda_device, reduction):
     assert float(loss) == 0.0 and not stats.any() and not grad.any()
 
 
+@pytest.mark.parametrize("reduction", ["token_mean", "seq_mean"])
+def test_more_than_2_31_bytes(rlk, cuda_device, reduction):
+    """Positions whose byte offsets pass 32 bits: one sequence of 2^29 + 9 tokens, half of them
+    active, ratio 1 and advantage 1 but for the last token."""
+    T = 2 ** 29 + 9
+    lp = torch.full((T,), -1.0, device=cuda_device)
+    adv = torch.ones(T, device=cuda_device)
+    adv[-1] = -3.0
+    act = torch.ones(T, dtype=torch.uint8, device=cuda_device)
+    act[:T // 2] = 0
+    n = T - T // 2
+    loss, stats, grad = rlk.policy_loss(lp, lp, adv, active=act, reduction=reduction)
+    assert abs(float(loss) + (n - 4) / n) <= 40 * U and float(stats[2]) == 0.0
+    assert float(grad[T // 2 - 1]) == 0.0
+    for t, want in ((T // 2, -1 / n), (T - 2, -1 / n), (T - 1, 3 / n)):
+        assert abs(float(grad[t]) - want) <= 8 * U * abs(want)
+
+
 def test_no_tokens_and_no_sequences(rlk, cuda_device):
     e = torch.zeros(0, device=cuda_device)
     loss, stats, grad = rlk.policy_loss(e, e, e)
@@ -295,12 +314,13 @@ def test_binding_shape_checks(rlk, cuda_device):
 
 @pytest.mark.parametrize("reduction", ["sum", "token_mean", "seq_mean"])
 def test_every_launch_shape_gives_the_same_bits(rlk, cuda_device, reduction):
-    """The same sequences in batches of 4096, 32768 and 200000 tokens (the others behind the last
-    sequence), which one CTA, one cluster and two launches take; and among 2000 empty sequences."""
-    n, offsets = 4000, [3, 900, 900, 2500, 3990]
+    """The same sequences in batches of 1024 to 200000 tokens (the others behind the last
+    sequence), which one CTA, one cluster with one and with four tokens a thread and two launches
+    take; and among 2000 empty sequences."""
+    n, offsets = 1000, [3, 300, 300, 700, 990]
     b = batch(200000, offsets, seed=14, mask=0.7)
     results = []
-    for T in (4096, 4097, 32768, 32769, 200000):
+    for T in (1000, 1024, 1025, 8192, 8193, 32768, 32769, 200000):
         part = {k: (v[:T] if k in ("lp", "old", "ref", "adv_t", "active") else v) for k, v in b.items()}
         loss, stats, grad = run(rlk, cuda_device, part, True, kl_coef=0.1, reduction=reduction)
         assert not grad[n:].any()
@@ -309,7 +329,7 @@ def test_every_launch_shape_gives_the_same_bits(rlk, cuda_device, reduction):
         assert all(torch.equal(x, y) for x, y in zip(r, results[0]))
     if reduction != "seq_mean":  # where the number of sequences does not count
         many = {k: (v[:n] if k in ("lp", "old", "ref", "adv_t", "active") else v) for k, v in b.items()}
-        many["offsets"] = offsets + [3990] * 2000
+        many["offsets"] = offsets + [990] * 2000
         many["adv_s"] = np.concatenate([b["adv_s"], np.full(2000, np.nan, np.float32)])
         r = run(rlk, cuda_device, many, True, kl_coef=0.1, reduction=reduction)
         assert all(torch.equal(x, y) for x, y in zip(r, results[0]))

@@ -67,6 +67,7 @@ CASES = [
     (700, [3, 40, 296, 297, 553, 553, 690]),                  # 256-token chunks met exactly
     (9001, [0, 4096, 8999]),
     (30000, [0] + list(range(101, 29990, 467))[:63] + [30000]),
+    (3000, [0] + list(range(20, 2990, 3))[:599] + [3000]),     # hundreds of tiny pairs
     (600001, [0, 262144 + 1, 300000, 300001, 600000]),        # more than 1024 chunks in one
 ]
 
@@ -99,7 +100,8 @@ def test_gradient_against_differences(rlk, cuda_device):
         assert abs(num - grad[t]) <= h * h / 6 * 1e-4 + 16 * U / h
 
 
-@pytest.mark.parametrize("lengths", [(40, 3000, 700, 1), (70000, 9, 300, 5000)])
+@pytest.mark.parametrize("lengths", [(40, 3000, 700, 1), (70000, 9, 300, 5000), (130000, 9, 300, 5000),
+                                     (70000, 270000, 9, 0)])
 def test_a_pairs_bits_do_not_depend_on_its_place(rlk, cuda_device, lengths):
     """The same sequences alone, shifted, among others and with the other layout."""
     n = sum(lengths)
@@ -155,19 +157,39 @@ def test_one_sided_nan_stays_in_its_pair(rlk, cuda_device):
     assert np.isfinite(rew[[0, 2, 3]]).all() and np.isnan(rew[1])
 
 
+@pytest.mark.parametrize("T", [1000, 70000, 300000])
 @pytest.mark.parametrize("offsets", [[0, 700, 600, 800, 1000], [-1, 5, 5, 5, 5], [0, 1, 2, 3, 1001],
-                                     [9, 2 ** 31 - 1, -2 ** 31, 5, 10]])
-def test_bad_offsets_are_reported(rlk, cuda_device, offsets):
-    b = batch(1000, [0] * 5, seed=8)
+                                     [9, 2 ** 31 - 1, -2 ** 31, 5, 10], [0, 2 ** 31 - 1, 0, 2 ** 31 - 1, 0]])
+def test_bad_offsets_are_reported(rlk, cuda_device, T, offsets):
+    if offsets == [0, 1, 2, 3, 1001]:
+        offsets = [0, 1, 2, 3, T + 1]
+    b = batch(T, [0] * 5, seed=8)
     status = rlk.new_status(cuda_device)
-    guard = torch.full((1512,), 7.0, device=cuda_device)
+    guard = torch.full((T + 512,), 7.0, device=cuda_device)
     loss = rlk.preference_loss(dev(b["lp"], cuda_device), dev(offsets, cuda_device, np.int32),
                                ref_logprob=dev(b["ref"], cuda_device), status=status,
-                               grad_logprob=guard[256:1256])[0]
+                               grad_logprob=guard[256:256 + T])[0]
     with pytest.raises(rlk.RlkError) as e:
         rlk.raise_on_device_status(status)
     assert e.value.code == rlk.RLK_ERR_INVALID_ARG and torch.isnan(loss)
-    assert torch.all(guard[:256] == 7) and torch.all(guard[1256:] == 7)
+    assert torch.all(guard[:256] == 7) and torch.all(guard[256 + T:] == 7)
+
+
+def test_more_than_2_31_bytes(rlk, cuda_device):
+    """Positions whose byte offsets pass 32 bits: two sequences over 2^29 + 9 tokens."""
+    T = 2 ** 29 + 9
+    lp = torch.full((T,), -1.0, device=cuda_device)
+    ref = torch.full((T,), -1.5, device=cuda_device)
+    half = T // 2
+    off = torch.tensor([0, half, T], dtype=torch.int32, device=cuda_device)
+    loss, pair, rew, grad = rlk.preference_loss(lp, off, ref_logprob=ref, beta=1.0, margin=0.5)
+    # m = half / 2 and (half + 1) / 2: h = -0.5, z = -1
+    want = np.log1p(np.exp(1.0))
+    assert rew.tolist() == [float(np.float32(half / 2)), float(np.float32((T - half) / 2))]
+    assert abs(float(loss) - want) <= 16 * U
+    slope = -1 / (1 + np.exp(-1.0))
+    for t, s in ((0, 1), (half - 1, 1), (half, -1), (T - 1, -1)):
+        assert abs(float(grad[t]) - s * slope) <= 16 * U
 
 
 def test_no_pairs(rlk, cuda_device):

@@ -142,6 +142,31 @@ def test_in_place_and_canaries(rlk, cuda_device, H):
     assert torch.all(gg[:64] == 7) and torch.all(gg[64 + H:] == 7) and torch.all(ws[ws_n:] == 9)
 
 
+def test_in_place_fp32(rlk, cuda_device):
+    a = make(700, 4096, cuda_device, 15, F32, F32)
+    kw = dict(x=a["x"], gamma=a["gamma"])
+    want, _ = rlk.rmsnorm_backward(a["grad_out"], grad_residual=a["grad_residual"], **kw)
+    for name in ("grad_residual", "grad_out"):
+        buf = {k: a[k].clone() for k in ("grad_residual", "grad_out")}
+        got, _ = rlk.rmsnorm_backward(buf["grad_out"], grad_residual=buf["grad_residual"],
+                                      grad_x=buf[name], **kw)
+        assert torch.equal(got, want)
+
+
+def test_more_than_2_31_bytes(rlk, cuda_device):
+    """Row offsets past 32 bits: the last rows of a 2.5 G-element batch have their alone-bits."""
+    T, H = 300007, 8192
+    x = torch.zeros((T, H), dtype=BF16, device=cuda_device)
+    dy = torch.zeros((T, H), dtype=BF16, device=cuda_device)
+    a = make(5, H, cuda_device, 16, BF16)
+    x[-5:], dy[-5:] = a["x"], a["grad_out"]
+    gx, gg = rlk.rmsnorm_backward(dy, x, a["gamma"], grad_x=dy)
+    want, want_g = rlk.rmsnorm_backward(a["grad_out"], a["x"], a["gamma"])
+    assert torch.equal(gx[-5:], want) and not gx[:-5].any()
+    tol = 64 * U * n64((a["grad_out"].float() * a["x"].float()).abs().sum(0))
+    assert np.all(np.abs(n64(gg) - n64(want_g)) <= tol)
+
+
 def test_no_rows(rlk, cuda_device):
     x = torch.zeros((0, 128), dtype=BF16, device=cuda_device)
     gx, gg = rlk.rmsnorm_backward(x, x, torch.ones(128, dtype=BF16, device=cuda_device))

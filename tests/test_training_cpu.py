@@ -83,11 +83,11 @@ def test_preference_loss_refusals(L):
     for kw in (dict(lp=0x1001), dict(off=0x4002), dict(rew=0x7002), dict(ws=0x10010)):
         refused(call, ALIGNMENT, **kw)
     # few pairs of many tokens need a workspace
-    refused(call, INVALID, T=100000)
-    refused(call, WORKSPACE, T=100000, ws=0x10000, wsb=100)
-    assert L.rlk_preference_loss_workspace_size(100000, 3) >= 256 + 12 * (100000 // 256)
-    assert L.rlk_preference_loss_workspace_size(100000, 40) == 0
-    assert L.rlk_preference_loss_workspace_size(32768, 3) == 0
+    refused(call, INVALID, T=200000)
+    refused(call, WORKSPACE, T=200000, ws=0x10000, wsb=100)
+    assert L.rlk_preference_loss_workspace_size(200000, 3) >= 256 + 12 * (200000 // 256)
+    assert L.rlk_preference_loss_workspace_size(10 ** 8, 40) == 0
+    assert L.rlk_preference_loss_workspace_size(190000, 3) == 0
     assert L.rlk_preference_loss_workspace_size(-1, 3) == 0
 
 
