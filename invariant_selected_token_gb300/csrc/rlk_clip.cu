@@ -97,36 +97,37 @@ struct Vecs {
     }
 };
 
-__device__ __forceinline__ float2 halves(uint32_t w, int type) {
-    if (type == RLK_DTYPE_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+// The two elements of a word.
+template <int kType>
+__device__ __forceinline__ float2 halves(uint32_t w) {
+    if constexpr (kType == RLK_DTYPE_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    else return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
 struct Sums {
     float low[8] = {}, high[8] = {};
-    __device__ __forceinline__ void add(const Vecs& x, int type) {
-        if (type == RLK_DTYPE_F32) {
+    template <int kType>
+    __device__ __forceinline__ void add_as(const Vecs& x) {
 #pragma unroll
-            for (int m = 0; m < kVecs; ++m) {
-                const uint32_t w[4] = {x.v[m].x, x.v[m].y, x.v[m].z, x.v[m].w};
+        for (int m = 0; m < kVecs; ++m) {
+            const uint32_t w[4] = {x.v[m].x, x.v[m].y, x.v[m].z, x.v[m].w};
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
+            for (int r = 0; r < 4; ++r) {
+                if constexpr (kType == RLK_DTYPE_F32) {
                     const float f = __uint_as_float(w[r]);
                     low[(m & 1) * 4 + r] = __fmaf_rn(f, f, low[(m & 1) * 4 + r]);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int m = 0; m < kVecs; ++m) {
-                const uint32_t w[4] = {x.v[m].x, x.v[m].y, x.v[m].z, x.v[m].w};
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float2 f = halves(w[r], type);
+                } else {
+                    const float2 f = halves<kType>(w[r]);
                     low[2 * r] = __fmaf_rn(f.x, f.x, low[2 * r]);
                     low[2 * r + 1] = __fmaf_rn(f.y, f.y, low[2 * r + 1]);
                 }
             }
         }
+    }
+    __device__ __forceinline__ void add(const Vecs& x, int type) {
+        if (type == RLK_DTYPE_F32) add_as<RLK_DTYPE_F32>(x);
+        else if (type == RLK_DTYPE_BF16) add_as<RLK_DTYPE_BF16>(x);
+        else add_as<RLK_DTYPE_F16>(x);
     }
     __device__ __forceinline__ void empty() {
 #pragma unroll
@@ -170,27 +171,35 @@ __device__ __forceinline__ float2 sum_pieces(const Table& t, int c0, int step) {
     return sums.total();
 }
 
-__device__ __forceinline__ uint32_t scaled_halves(uint32_t w, int type, float scale) {
-    const float2 f = halves(w, type);
-    const float a = __fmul_rn(f.x, scale), b = __fmul_rn(f.y, scale);
-    if (type == RLK_DTYPE_BF16) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-__device__ __forceinline__ void store_piece(const Piece& p, Vecs& x, float scale) {
+template <int kType>
+__device__ __forceinline__ void scale_vecs(Vecs& x, float scale) {
 #pragma unroll
     for (int m = 0; m < kVecs; ++m) {
         uint32_t w[4] = {x.v[m].x, x.v[m].y, x.v[m].z, x.v[m].w};
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            w[r] = p.type == RLK_DTYPE_F32 ? __float_as_uint(__fmul_rn(__uint_as_float(w[r]), scale))
-                                           : scaled_halves(w[r], p.type, scale);
+        for (int r = 0; r < 4; ++r) {
+            if constexpr (kType == RLK_DTYPE_F32) {
+                w[r] = __float_as_uint(__fmul_rn(__uint_as_float(w[r]), scale));
+            } else {
+                const float2 f = halves<kType>(w[r]);
+                const float a = __fmul_rn(f.x, scale), b = __fmul_rn(f.y, scale);
+                if constexpr (kType == RLK_DTYPE_BF16) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+                    w[r] = *reinterpret_cast<const uint32_t*>(&h);
+                } else {
+                    const __half2 h = __floats2half2_rn(a, b);
+                    w[r] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+            }
+        }
         x.v[m] = make_uint4(w[0], w[1], w[2], w[3]);
     }
+}
+
+__device__ __forceinline__ void store_piece(const Piece& p, Vecs& x, float scale) {
+    if (p.type == RLK_DTYPE_F32) scale_vecs<RLK_DTYPE_F32>(x, scale);
+    else if (p.type == RLK_DTYPE_BF16) scale_vecs<RLK_DTYPE_BF16>(x, scale);
+    else scale_vecs<RLK_DTYPE_F16>(x, scale);
     const bool whole = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
 #pragma unroll
     for (int m = 0; m < kVecs; ++m) {

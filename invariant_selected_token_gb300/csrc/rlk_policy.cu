@@ -69,32 +69,24 @@ __device__ __forceinline__ int count_active(const uint8_t* active, int64_t b, in
     return n;
 }
 
+// kKl: 0 without a reference, else RLK_KL_K1 .. K3.
 struct TokenTerms {
     float policy, kl, clipped, neg_d, slope;
 };
 
-__device__ __forceinline__ TokenTerms token_terms(const PolicyArgs& a, float lp, float old,
-                                                  float ref, float A) {
+// From d as two floats, r = e^d, u = ref - lp and (k3) e^u - 1 - u.  The two clips are one test:
+// with a negative advantage both d and the border change sign.
+template <int kKl>
+__device__ __forceinline__ TokenTerms token_terms(const PolicyArgs& a, float2 d, float r, float u, float k3, float A) {
     TokenTerms o;
-    const float2 d = two_diff(lp, old);
-    float r = exp_any(d.x);
-    if (r < 3.0e38f) r = __fmaf_rn(r, d.y, r);
-    float held = r;
-    bool shut = false;
-    if (A > 0.0f) {
-        if (above(d, a.log_high)) {
-            shut = true;
-            held = a.ratio_high;
-        }
-    } else if (A < 0.0f) {
-        if (below(d, a.log_low)) {
-            shut = true;
-            held = a.ratio_low;
-        }
-        if (a.dual > 0.0f && above(d, a.log_dual)) {
-            shut = true;
-            held = a.dual;
-        }
+    const bool up = A > 0.0f;
+    const float2 side = up ? d : make_float2(-d.x, -d.y);
+    const float2 border = up ? a.log_high : make_float2(-a.log_low.x, -a.log_low.y);
+    bool shut = above(side, border) && A != 0.0f;
+    float held = shut ? (up ? a.ratio_high : a.ratio_low) : r;
+    if (a.dual > 0.0f && A < 0.0f && above(d, a.log_dual)) {
+        shut = true;
+        held = a.dual;
     }
     float s = __fmul_rn(held, A);
     if (A == 0.0f && r == CUDART_INF_F) s = 0.0f;  // the ratio is finite, its fp32 value is not
@@ -103,27 +95,73 @@ __device__ __forceinline__ TokenTerms token_terms(const PolicyArgs& a, float lp,
     o.neg_d = -d.x;
     o.slope = shut ? 0.0f : -s;
     o.kl = 0.0f;
-    if (a.ref_logprob) {
-        const float u = __fsub_rn(ref, lp);
-        float dk;
-        if (a.kl_kind == RLK_KL_K1) {
-            o.kl = -u;
-            dk = 1.0f;
-        } else if (a.kl_kind == RLK_KL_K2) {
-            o.kl = __fmul_rn(__fmul_rn(0.5f, u), u);
-            dk = -u;
-        } else {
-            o.kl = exp_minus_1_minus(u);
-            dk = -__fadd_rn(o.kl, u);
-        }
+    if constexpr (kKl != 0) {
+        const float dk = kKl == RLK_KL_K1 ? 1.0f : kKl == RLK_KL_K2 ? -u : -__fadd_rn(k3, u);
+        o.kl = kKl == RLK_KL_K1 ? -u : kKl == RLK_KL_K2 ? __fmul_rn(__fmul_rn(0.5f, u), u) : k3;
         o.slope = __fmaf_rn(a.kl_coef, dk, o.slope);
     }
     return o;
 }
 
+// e^(d.x + d.y): the rest of d to first order.
+__device__ __forceinline__ float ratio_of(float2 d) {
+    const float r = exp_any(d.x);
+    return r < 3.0e38f ? __fmaf_rn(r, d.y, r) : r;
+}
+
+// One token.
+template <int kKl>
+__device__ __forceinline__ TokenTerms token_one(const PolicyArgs& a, float lp, float old, float ref, float A) {
+    const float2 d = two_diff(lp, old);
+    const float u = __fsub_rn(ref, lp);
+    return token_terms<kKl>(a, d, ratio_of(d), u, kKl == RLK_KL_K3 ? exp_minus_1_minus(u) : 0.0f, A);
+}
+
+// Two tokens, two per instruction as far as the values allow: |d| <= 80, where 2^n only adds to
+// an exponent, and |u| < 1/2.  The same operations in the same order, so the same bits as
+// token_one; warps with other values in them run that.
+template <int kKl>
+__device__ __forceinline__ void token_two(const PolicyArgs& a, const float (&lp)[2], const float (&old)[2],
+                                          const float (&ref)[2], const float (&A)[2], TokenTerms (&o)[2]) {
+    const uint64_t l2 = f2_pack(lp[0], lp[1]);
+    const uint64_t neg_old = f2_pack(-old[0], -old[1]);
+    const uint64_t s = f2_add(l2, neg_old);
+    const uint64_t minus = f2_splat(-1.0f);
+    // two_diff: t = s - lp, e = (lp - (s - t)) - (old + t); products with -1 are exact
+    const uint64_t t = f2_fma(l2, minus, s);
+    const uint64_t e = f2_add(f2_fma(f2_fma(t, minus, s), minus, l2), f2_fma(t, minus, neg_old));
+    float d0, d1, e0, e1, u0 = 0.0f, u1 = 0.0f;
+    f2_unpack(s, d0, d1);
+    f2_unpack(e, e0, e1);
+    bool plain = fabsf(d0) <= 80.0f && fabsf(d1) <= 80.0f;
+    uint64_t u2 = 0;
+    if constexpr (kKl != 0) {
+        u2 = f2_fma(l2, minus, f2_pack(ref[0], ref[1]));
+        f2_unpack(u2, u0, u1);
+        if constexpr (kKl == RLK_KL_K3) plain = plain && fabsf(u0) < 0.5f && fabsf(u1) < 0.5f;
+    }
+    if (!__all_sync(0xffffffffu, plain)) {
+        o[0] = token_one<kKl>(a, lp[0], old[0], ref[0], A[0]);
+        o[1] = token_one<kKl>(a, lp[1], old[1], ref[1], A[1]);
+        return;
+    }
+    uint64_t r = contract_exp_x2<false>(s);
+    r = f2_fma(r, e, r);
+    float r0, r1, k0 = 0.0f, k1 = 0.0f;
+    f2_unpack(r, r0, r1);
+    if constexpr (kKl == RLK_KL_K3) {
+        uint64_t p = f2_splat(exp_tail(0));
+#pragma unroll
+        for (int i = 1; i < 8; ++i) p = f2_fma(p, u2, f2_splat(exp_tail(i)));
+        f2_unpack(f2_mul(f2_mul(u2, u2), p), k0, k1);
+    }
+    o[0] = token_terms<kKl>(a, make_float2(d0, e0), r0, u0, k0, A[0]);
+    o[1] = token_terms<kKl>(a, make_float2(d1, e1), r1, u1, k1, A[1]);
+}
+
 // kPer of a lane's tokens, 32 apart.  Everything is loaded before anything is used, inactive
 // tokens too (their values are dropped, never multiplied).
-template <int kPer>
+template <int kKl, int kPer>
 struct Tokens {
     int64_t t0;  // the first one
     int left;    // tokens from it to the end of the batch
@@ -140,7 +178,7 @@ struct Tokens {
             const bool in = i * 32 < left;
             lp[i] = in ? p_lp[i * 32] : 0.0f;
             old[i] = in ? p_old[i * 32] : 0.0f;
-            ref[i] = in && a.ref_logprob ? p_ref[i * 32] : 0.0f;
+            ref[i] = kKl && in ? p_ref[i * 32] : 0.0f;
             adv[i] = in && !a.adv_per_seq ? p_adv[i * 32] : 0.0f;
             on[i] = in && (!a.active || p_on[i * 32] != 0);
         }
@@ -156,36 +194,53 @@ struct Tokens {
 // Gradients of a lane's tokens out, and RN(w x) of the four stats x returned.  Every token is
 // worked on, the inactive ones with zeros for their values, so that the tokens' chains of
 // operations overlap; what an inactive one gives is dropped.
-template <int kPer>
-__device__ __forceinline__ void policy_tokens(const PolicyArgs& a, const Tokens<kPer>& k, const float (&w)[kPer],
+template <int kKl, int kPer>
+__device__ __forceinline__ void policy_tokens(const PolicyArgs& a, const Tokens<kKl, kPer>& k, const float (&w)[kPer],
                                               float4 (&out)[kPer]) {
     const float scale = static_cast<float>(a.scale);
     float* const grad = a.grad + k.t0;
+    constexpr int kStep = kPer == 1 ? 1 : 2;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const bool on = k.on[i];
-        const TokenTerms o = token_terms(a, on ? k.lp[i] : 0.0f, on ? k.old[i] : 0.0f, on ? k.ref[i] : 0.0f,
-                                         on ? k.adv[i] : 0.0f);
-        const float wi = on ? w[i] : 0.0f;
-        out[i] = make_float4(__fmul_rn(wi, o.policy), __fmul_rn(wi, o.kl), __fmul_rn(wi, o.clipped),
-                             __fmul_rn(wi, o.neg_d));
-        const float g = on ? __fmul_rn(__fmul_rn(scale, wi), o.slope) : 0.0f;
-        if (a.grad && i * 32 < k.left) grad[i * 32] = g;
+    for (int i = 0; i < kPer; i += kStep) {
+        TokenTerms o[kStep];
+        float lp[kStep], old[kStep], ref[kStep], adv[kStep];
+#pragma unroll
+        for (int c = 0; c < kStep; ++c) {
+            const bool on = k.on[i + c];
+            lp[c] = on ? k.lp[i + c] : 0.0f;
+            old[c] = on ? k.old[i + c] : 0.0f;
+            ref[c] = on ? k.ref[i + c] : 0.0f;
+            adv[c] = on ? k.adv[i + c] : 0.0f;
+        }
+        if constexpr (kStep == 1) o[0] = token_one<kKl>(a, lp[0], old[0], ref[0], adv[0]);
+        else token_two<kKl>(a, lp, old, ref, adv, o);
+#pragma unroll
+        for (int c = 0; c < kStep; ++c) {
+            const float wi = k.on[i + c] ? w[i + c] : 0.0f;
+            out[i + c] = make_float4(__fmul_rn(wi, o[c].policy), __fmul_rn(wi, o[c].kl), __fmul_rn(wi, o[c].clipped),
+                                     __fmul_rn(wi, o[c].neg_d));
+            if (a.grad && (i + c) * 32 < k.left)
+                grad[(i + c) * 32] = k.on[i + c] ? __fmul_rn(__fmul_rn(scale, wi), o[c].slope) : 0.0f;
+        }
     }
 }
 
-__device__ __forceinline__ float4 add4(const float4& a, const float4& b) {
-    return make_float4(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y), __fadd_rn(a.z, b.z), __fadd_rn(a.w, b.w));
-}
+struct Stats {  // (policy, kl) and (clipped, -d)
+    uint64_t a, b;
+};
+__device__ __forceinline__ Stats stats_of(const float4& v) { return {f2_pack(v.x, v.y), f2_pack(v.z, v.w)}; }
+__device__ __forceinline__ Stats add_stats(const Stats& x, const Stats& y) { return {f2_add(x.a, y.a), f2_add(x.b, y.b)}; }
 
 // A span's sum from its lanes' four tokens.
 __device__ __forceinline__ float4 span_sum(const float4& p0, const float4& p1, const float4& p2, const float4& p3) {
-    float4 v = add4(add4(p0, p1), add4(p2, p3));
-#pragma unroll 1
+    Stats v = add_stats(add_stats(stats_of(p0), stats_of(p1)), add_stats(stats_of(p2), stats_of(p3)));
+#pragma unroll
     for (int o = 16; o >= 1; o >>= 1)
-        v = add4(v, make_float4(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o),
-                                __shfl_xor_sync(0xffffffffu, v.z, o), __shfl_xor_sync(0xffffffffu, v.w, o)));
-    return v;
+        v = add_stats(v, {__shfl_xor_sync(0xffffffffu, v.a, o), __shfl_xor_sync(0xffffffffu, v.b, o)});
+    float4 f;
+    f2_unpack(v.a, f.x, f.y);
+    f2_unpack(v.b, f.z, f.w);
+    return f;
 }
 
 // Component k of a unit's sum from its 8 spans' sums.
@@ -230,7 +285,7 @@ __device__ __forceinline__ int seq_in(const int32_t* offsets, int n, int t) {
 
 // One cluster of kCtas CTAs of 1024 threads, kPer tokens a thread, which it holds from the first
 // load to the gradient; the counts that the weights need come from the masks it holds.
-template <int kCtas, int kPer>
+template <int kKl, int kCtas, int kPer>
 __global__ void __launch_bounds__(1024) k_policy_one(const PolicyArgs a) {
     constexpr int kAll = 1024, kUnits = kPer;  // units of a CTA
     static_assert(kCtas * kUnits <= 32, "a lane per unit");
@@ -245,7 +300,7 @@ __global__ void __launch_bounds__(1024) k_policy_one(const PolicyArgs a) {
     __shared__ int active_here;
     const int rank = kCtas > 1 ? static_cast<int>(blockIdx.x) : 0;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Tokens<kPer> k;
+    Tokens<kKl, kPer> k;
     k.load(a, (rank * (kAll / 32) + warp) * (32 * kPer) + lane);
     const bool masked = a.active != nullptr, by_mean = a.reduction == RLK_REDUCE_SEQ_MEAN;
     const bool by_seq = a.offsets && (a.adv_per_seq || by_mean);
@@ -326,7 +381,7 @@ __global__ void __launch_bounds__(1024) k_policy_one(const PolicyArgs a) {
         if (a.adv_per_seq) k.adv[i] = adv[seq[i]];
     }
     float4 terms[kPer];
-    policy_tokens(a, k, w, terms);
+    policy_tokens<kKl>(a, k, w, terms);
     if constexpr (kPer == 4) {
         const float4 s = span_sum(terms[0], terms[1], terms[2], terms[3]);
         if (lane == 0) spans[warp] = s;
@@ -420,6 +475,7 @@ __global__ void __launch_bounds__(1024) k_policy_count(const PolicyArgs a) {
     }
 }
 
+template <int kKl>
 __global__ void __launch_bounds__(kThreads, 5) k_policy_main(const PolicyArgs a) {
     constexpr int kPer = kPolicyUnit / kThreads;
     __shared__ float4 spans[kUnitWarps];
@@ -428,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 5) k_policy_main(const PolicyArgs a)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t units = (static_cast<int64_t>(a.T) + kPolicyUnit - 1) / kPolicyUnit;
     const int at = warp * 32 * kPer + lane;
-    Tokens<kPer> k;
+    Tokens<kKl, kPer> k;
     k.load(a, blockIdx.x * static_cast<int64_t>(kPolicyUnit) + at);
     const Bounds bd = bounds_of(a);
     const bool by_mean = a.reduction == RLK_REDUCE_SEQ_MEAN;
@@ -461,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 5) k_policy_main(const PolicyArgs a)
             if (a.adv_per_seq) k.adv[i] = a.advantages[s];
         }
         float4 terms[kPer];
-        policy_tokens(a, k, w, terms);
+        policy_tokens<kKl>(a, k, w, terms);
         const float4 s = span_sum(terms[0], terms[1], terms[2], terms[3]);
         if (lane == 0) spans[warp] = s;
         __syncthreads();
@@ -507,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 5) k_policy_main(const PolicyArgs a)
     }
 }
 
-template <int kCtas, int kPer>
+template <int kKl, int kCtas, int kPer>
 cudaError_t launch_one(const PolicyArgs& a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -520,7 +576,7 @@ cudaError_t launch_one(const PolicyArgs& a, cudaStream_t stream) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = kCtas > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k_policy_one<kCtas, kPer>, a);
+    return cudaLaunchKernelEx(&cfg, k_policy_one<kKl, kCtas, kPer>, a);
 }
 
 }  // namespace
@@ -529,11 +585,12 @@ bool policy_one_launch(int64_t T, int64_t n_seqs) {
     return T <= kCluster * 1024 * 4 && n_seqs <= kLaunchSeqs;
 }
 
-cudaError_t launch_policy_loss(const PolicyArgs& a, int num_sms, cudaStream_t stream) {
+template <int kKl>
+cudaError_t launch_kl(const PolicyArgs& a, int num_sms, cudaStream_t stream) {
     if (policy_one_launch(a.T, a.n_seqs))
-        return a.T <= 1024              ? launch_one<1, 1>(a, stream)
-               : a.T <= kCluster * 1024 ? launch_one<kCluster, 1>(a, stream)
-                                        : launch_one<kCluster, 4>(a, stream);
+        return a.T <= 1024              ? launch_one<kKl, 1, 1>(a, stream)
+               : a.T <= kCluster * 1024 ? launch_one<kKl, kCluster, 1>(a, stream)
+                                        : launch_one<kKl, kCluster, 4>(a, stream);
     int rows = 1;
     if (a.reduction == RLK_REDUCE_SEQ_MEAN) rows = a.n_seqs;
     else if (a.active && a.reduction == RLK_REDUCE_TOKEN_MEAN) rows = kPolicyCountBlocks;
@@ -563,7 +620,14 @@ cudaError_t launch_policy_loss(const PolicyArgs& a, int num_sms, cudaStream_t st
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_policy_main, a);
+    return cudaLaunchKernelEx(&cfg, k_policy_main<kKl>, a);
+}
+
+cudaError_t launch_policy_loss(const PolicyArgs& a, int num_sms, cudaStream_t stream) {
+    if (!a.ref_logprob) return launch_kl<0>(a, num_sms, stream);
+    return a.kl_kind == RLK_KL_K1   ? launch_kl<RLK_KL_K1>(a, num_sms, stream)
+           : a.kl_kind == RLK_KL_K2 ? launch_kl<RLK_KL_K2>(a, num_sms, stream)
+                                    : launch_kl<RLK_KL_K3>(a, num_sms, stream);
 }
 
 }  // namespace rlk

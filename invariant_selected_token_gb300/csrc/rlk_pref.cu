@@ -137,9 +137,10 @@ __device__ __forceinline__ void preference_finish(const PreferenceArgs& a, const
         if ((threadIdx.x & 31) == 0) tmp[w] = v;
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        float2 v = pair_of(0.0f);
-        for (int i = 0; i < kWarps && i * 32 < a.n_pairs; ++i) v = pair_add(v, tmp[i]);
+    if (threadIdx.x < 32) {
+        const int w = threadIdx.x;
+        const float2 v = warp_sum(w < kWarps && w * 32 < a.n_pairs ? tmp[w] : pair_of(0.0f));
+        if (w != 0) return;
         *a.out_loss = bad ? CUDART_NAN_F : static_cast<float>(__dmul_rn(a.scale_per_pair, pair_value(v)));
         if (bad) report_status(a.status, RLK_ERR_INVALID_ARG);
     }
@@ -207,17 +208,21 @@ __device__ __forceinline__ void reduce_pair(const PreferenceArgs& a, int pair, c
         }
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        float2 v[2] = {pair_of(0.0f), pair_of(0.0f)};
-        int n[2] = {0, 0};
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {
-            for (int i = 0; i < kWarps && i * 32 < held[side]; ++i) {
-                v[side] = pair_add(v[side], sc.tmp[side][i]);
-                n[side] += sc.n[side][i];
-            }
+    if (threadIdx.x < 32) {
+        // lanes 0 .. 15 add the chosen side's warps, lanes 16 .. 31 the rejected one's
+        const int side = lane >> 4, w = lane & 15;
+        const bool have = w * 32 < (side ? held[1] : held[0]);
+        float2 v = have ? sc.tmp[side][w] : pair_of(0.0f);
+        int n = have ? sc.n[side][w] : 0;
+#pragma unroll 1
+        for (int o = 8; o >= 1; o >>= 1) {
+            v = pair_add(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+            n += __shfl_xor_sync(0xffffffffu, n, o);
         }
-        pair_terms(a, pair, chosen_of(a, pair), rejected_of(a, pair), v[0], v[1], n[0], n[1], write, slope, held_loss);
+        const float2 v1 = make_float2(__shfl_sync(0xffffffffu, v.x, 16), __shfl_sync(0xffffffffu, v.y, 16));
+        const int n1 = __shfl_sync(0xffffffffu, n, 16);
+        if (lane == 0)
+            pair_terms(a, pair, chosen_of(a, pair), rejected_of(a, pair), v, v1, n, n1, write, slope, held_loss);
     }
 }
 
@@ -398,12 +403,16 @@ __global__ void __launch_bounds__(kThreads) k_preference_spread(const Preference
                     write, scratch, slope, nullptr);
         __syncthreads();
     };
-    // the pairs' own outputs
-    for (int pair = blockIdx.x; pair < a.n_pairs; pair += gridDim.x) slopes_of(pair, true);
+    // a pair's own outputs are written by CTA pair mod grid, which keeps its slopes in case its
+    // tokens belong to the same pair
+    int have = -1;
+    for (int pair = blockIdx.x; pair < a.n_pairs; pair += gridDim.x) {
+        slopes_of(pair, true);
+        have = pair;
+    }
     if (a.grad) {
         const int64_t total = map.first[kSplitSeqs];
         const int64_t i0 = total * blockIdx.x / gridDim.x, i1 = total * (blockIdx.x + 1) / gridDim.x;
-        int have = -1;
         for (int64_t i = i0; i < i1;) {
             const int q = map.seq_of(i);
             const int64_t next = map.first[q + 1] < i1 ? map.first[q + 1] : i1;

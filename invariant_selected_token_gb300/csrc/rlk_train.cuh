@@ -10,6 +10,7 @@
 #include <math_constants.h>
 
 #include "../../include/rlk.h"
+#include "rlk_contract.cuh"
 
 namespace rlk {
 
@@ -201,20 +202,20 @@ __device__ __forceinline__ float exp_any(float x) {
     return x != x ? x : p;
 }
 
-// e^u - 1 - u.  Near 0 the difference cancels, so there it is its Taylor series
-// u^2 (1/2 + u/6 + ... + u^7/9!): the first term left out is below 2^-28 of the sum.
+// e^u - 1 - u for |u| < 1/2, where that difference cancels: its Taylor series
+// u^2 (1/2 + u/6 + ... + u^7/9!), the first term left out below 2^-28 of the sum.
+__device__ constexpr float exp_tail(int i) {  // 1/9! .. 1/2!
+    constexpr float c[8] = {0x1.71de3ap-19f, 0x1.a01a02p-16f, 0x1.a01a02p-13f, 0x1.6c16c2p-10f,
+                            0x1.111112p-7f,  0x1.555556p-5f,  0x1.555556p-3f,  0.5f};
+    return c[i];
+}
+// and for any u
 __device__ __forceinline__ float exp_minus_1_minus(float u) {
-    float p = 0x1.71de3ap-19f;             // 1/9!
-    p = __fmaf_rn(p, u, 0x1.a01a02p-16f);  // 1/8!
-    p = __fmaf_rn(p, u, 0x1.a01a02p-13f);  // 1/7!
-    p = __fmaf_rn(p, u, 0x1.6c16c2p-10f);  // 1/6!
-    p = __fmaf_rn(p, u, 0x1.111112p-7f);   // 1/5!
-    p = __fmaf_rn(p, u, 0x1.555556p-5f);   // 1/4!
-    p = __fmaf_rn(p, u, 0x1.555556p-3f);   // 1/3!
-    p = __fmaf_rn(p, u, 0.5f);             // 1/2!
-    p = __fmul_rn(__fmul_rn(u, u), p);
-    if (!(fabsf(u) < 0.5f)) p = __fsub_rn(__fsub_rn(exp_any(u), 1.0f), u);
-    return p;
+    if (!(fabsf(u) < 0.5f)) return __fsub_rn(__fsub_rn(exp_any(u), 1.0f), u);
+    float p = exp_tail(0);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) p = __fmaf_rn(p, u, exp_tail(i));
+    return __fmul_rn(__fmul_rn(u, u), p);
 }
 
 // log(1 + e) for e in [0, 1]: 2 atanh(v), v = e / (2 + e) <= 1/3, by the odd series through
