@@ -118,7 +118,7 @@ __device__ __forceinline__ TokenTerms token_one(const PolicyArgs& a, float lp, f
 }
 
 // Two tokens, two per instruction as far as the values allow: |d| <= 80, where 2^n only adds to
-// an exponent, and |u| < 1/2.  The same operations in the same order, so the same bits as
+// an exponent, and |u| < 1.  The same operations in the same order, so the same bits as
 // token_one; warps with other values in them run that.
 template <int kKl>
 __device__ __forceinline__ void token_two(const PolicyArgs& a, const float (&lp)[2], const float (&old)[2],
@@ -138,7 +138,7 @@ __device__ __forceinline__ void token_two(const PolicyArgs& a, const float (&lp)
     if constexpr (kKl != 0) {
         u2 = f2_fma(l2, minus, f2_pack(ref[0], ref[1]));
         f2_unpack(u2, u0, u1);
-        if constexpr (kKl == RLK_KL_K3) plain = plain && fabsf(u0) < 0.5f && fabsf(u1) < 0.5f;
+        if constexpr (kKl == RLK_KL_K3) plain = plain && fabsf(u0) < 1.0f && fabsf(u1) < 1.0f;
     }
     if (!__all_sync(0xffffffffu, plain)) {
         o[0] = token_one<kKl>(a, lp[0], old[0], ref[0], A[0]);
@@ -152,7 +152,7 @@ __device__ __forceinline__ void token_two(const PolicyArgs& a, const float (&lp)
     if constexpr (kKl == RLK_KL_K3) {
         uint64_t p = f2_splat(exp_tail(0));
 #pragma unroll
-        for (int i = 1; i < 8; ++i) p = f2_fma(p, u2, f2_splat(exp_tail(i)));
+        for (int i = 1; i < kExpTail; ++i) p = f2_fma(p, u2, f2_splat(exp_tail(i)));
         f2_unpack(f2_mul(f2_mul(u2, u2), p), k0, k1);
     }
     o[0] = token_terms<kKl>(a, make_float2(d0, e0), r0, u0, k0, A[0]);

@@ -180,30 +180,40 @@ struct PairScratch {
 };
 
 // Slots of both sequences -> the pair's terms, by a whole CTA; `slope` and the outputs are set
-// by thread 0, so a barrier has to follow.  slot(side, j) and count(side, j) give a slot's sum
-// and its active tokens; slots from chunks_of() on are empty.
-template <typename SlotOf, typename CountOf>
+// by thread 0, so a barrier has to follow.  slot(side, j, n) gives a slot's sum and its active
+// tokens; slots from chunks_of() on are empty.
+template <typename SlotOf>
 __device__ __forceinline__ void reduce_pair(const PreferenceArgs& a, int pair, const Span (&sp)[2], SlotOf slot,
-                                            CountOf count, bool write, PairScratch& sc, float* slope, float* held_loss) {
+                                            bool write, PairScratch& sc, float* slope, float* held_loss) {
     const int lane = threadIdx.x & 31;
     int held[2];
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
         const int64_t c = chunks_of(sp[side]);
         held[side] = c < kSlots ? static_cast<int>(c) : kSlots;
-        // warp w of 16 takes slots 32 w + lane and + 512; those without any would add zeros
-        for (int w = threadIdx.x >> 5; w < kWarps && w * 32 < held[side]; w += blockDim.x >> 5) {
-            float2 v = pair_of(0.0f);
-            int n = 0;
-            for (int i = w * 32 + lane; i < held[side]; i += kThreads) {
-                v = pair_add(v, slot(side, i));
-                n += count(side, i);
+    }
+    // warp w of 16 takes slots 32 w + lane and + 512; those without any would add zeros
+    const int most = held[0] > held[1] ? held[0] : held[1];
+    for (int w = threadIdx.x >> 5; w < kWarps && w * 32 < most; w += blockDim.x >> 5) {
+        float2 v[2][2];
+        int n[2][2];
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int i = w * 32 + lane + k * kThreads;
+                v[side][k] = pair_of(0.0f);
+                n[side][k] = 0;
+                if (i < held[side]) v[side][k] = slot(side, i, n[side][k]);
             }
-            v = warp_sum(v);
-            n = __reduce_add_sync(0xffffffffu, n);
+        }
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+            const float2 sum = warp_sum(pair_add(v[side][0], v[side][1]));
+            const int count = __reduce_add_sync(0xffffffffu, n[side][0] + n[side][1]);
             if (lane == 0) {
-                sc.tmp[side][w] = v;
-                sc.n[side][w] = n;
+                sc.tmp[side][w] = sum;
+                sc.n[side][w] = count;
             }
         }
     }
@@ -274,9 +284,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_preference(const PreferenceArgs
         }
         if (team > 1) cluster.sync(); else __syncthreads();
         if (member == 0 && work)
-            reduce_pair(a, pair, sp, [&](int side, int j) { return slots[side][j]; },
-                        [&](int side, int j) { return counts[side][j]; }, true, scratch, slope,
-                        alone ? all_losses + pair : nullptr);
+            reduce_pair(a, pair, sp,
+                        [&](int side, int j, int& n) {
+                            n = counts[side][j];
+                            return slots[side][j];
+                        },
+                        true, scratch, slope, alone ? all_losses + pair : nullptr);
         if (team > 1) cluster.sync(); else __syncthreads();
         if (a.grad && work) {
             const int who = member * blockDim.x + threadIdx.x, all = team * blockDim.x;
@@ -388,17 +401,14 @@ __global__ void __launch_bounds__(kThreads) k_preference_spread(const Preference
         const int64_t at[2] = {map.first[q0], map.first[q1]};
         __syncthreads();  // the previous pair's slopes have been read
         reduce_pair(a, pair, sp,
-                    [&](int side, int j) {
-                        const int64_t c = chunks_of(sp[side]);
+                    [&](int side, int j, int& n) {
                         float2 v = a.chunk_sums[at[side] + j];
-                        for (int64_t g = j + kSlots; g < c; g += kSlots) v = pair_add(v, a.chunk_sums[at[side] + g]);
+                        n = a.chunk_counts[at[side] + j];
+                        for (int64_t g = j + kSlots, c = chunks_of(sp[side]); g < c; g += kSlots) {
+                            v = pair_add(v, a.chunk_sums[at[side] + g]);
+                            n += a.chunk_counts[at[side] + g];
+                        }
                         return v;
-                    },
-                    [&](int side, int j) {
-                        int n = 0;
-                        const int64_t c = chunks_of(sp[side]);
-                        for (int64_t g = j; g < c; g += kSlots) n += a.chunk_counts[at[side] + g];
-                        return n;
                     },
                     write, scratch, slope, nullptr);
         __syncthreads();

@@ -202,19 +202,21 @@ __device__ __forceinline__ float exp_any(float x) {
     return x != x ? x : p;
 }
 
-// e^u - 1 - u for |u| < 1/2, where that difference cancels: its Taylor series
-// u^2 (1/2 + u/6 + ... + u^7/9!), the first term left out below 2^-28 of the sum.
-__device__ constexpr float exp_tail(int i) {  // 1/9! .. 1/2!
-    constexpr float c[8] = {0x1.71de3ap-19f, 0x1.a01a02p-16f, 0x1.a01a02p-13f, 0x1.6c16c2p-10f,
-                            0x1.111112p-7f,  0x1.555556p-5f,  0x1.555556p-3f,  0.5f};
+// e^u - 1 - u for |u| < 1, where that difference cancels: its Taylor series
+// u^2 (1/2 + u/6 + ... + u^9/11!), the first term left out below 2^-27 of the sum.
+constexpr int kExpTail = 10;
+__device__ constexpr float exp_tail(int i) {  // 1/11! .. 1/2!
+    constexpr float c[kExpTail] = {0x1.ae6456p-26f, 0x1.27e4fcp-22f, 0x1.71de3ap-19f, 0x1.a01a02p-16f,
+                                   0x1.a01a02p-13f, 0x1.6c16c2p-10f, 0x1.111112p-7f,  0x1.555556p-5f,
+                                   0x1.555556p-3f,  0.5f};
     return c[i];
 }
 // and for any u
 __device__ __forceinline__ float exp_minus_1_minus(float u) {
-    if (!(fabsf(u) < 0.5f)) return __fsub_rn(__fsub_rn(exp_any(u), 1.0f), u);
+    if (!(fabsf(u) < 1.0f)) return __fsub_rn(__fsub_rn(exp_any(u), 1.0f), u);
     float p = exp_tail(0);
 #pragma unroll
-    for (int i = 1; i < 8; ++i) p = __fmaf_rn(p, u, exp_tail(i));
+    for (int i = 1; i < kExpTail; ++i) p = __fmaf_rn(p, u, exp_tail(i));
     return __fmul_rn(__fmul_rn(u, u), p);
 }
 
