@@ -396,8 +396,8 @@ rlk_status_t rlk_rmsnorm(const void* x, const void* residual, const void* gamma,
  *   grad_x         device, [T][H] of grad_x_dtype (RLK_DTYPE_F32 or RLK_DTYPE_BF16); may be
  *                  grad_residual, or grad_out where the types are the same
  *   grad_gamma     device, float [H], or NULL to skip; all zeros when T == 0
- *   workspace      >= rlk_rmsnorm_backward_workspace_size(T, H) bytes, 256-byte aligned
- *                  (NULL allowed when grad_gamma is NULL)
+ *   workspace      >= rlk_rmsnorm_backward_workspace_size(T, H) bytes, 256-byte aligned; that
+ *                  is 0 for T <= 16, and nothing is needed when grad_gamma is NULL
  *   H              multiple of 64, at most 8192; every pointer 16-byte aligned
  */
 size_t rlk_rmsnorm_backward_workspace_size(int64_t T, int64_t H);

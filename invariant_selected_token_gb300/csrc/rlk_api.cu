@@ -1023,6 +1023,7 @@ rlk_status_t rlk_rmsnorm(const void* x, const void* residual, const void* gamma,
 
 size_t rlk_rmsnorm_backward_workspace_size(int64_t T, int64_t H) {
     if (T < 0 || T > RLK_MAX_ROWS || H < 64 || H % 64 != 0 || H > 8192) return 0;
+    if (rlk::rmsnorm_backward_one_launch(T)) return 0;
     return align256(size_t(rlk::rmsnorm_backward_ranges(T)) * size_t(H) * sizeof(float));
 }
 
@@ -1038,14 +1039,14 @@ rlk_status_t rlk_rmsnorm_backward(const void* grad_out, int grad_out_dtype, cons
         return RLK_ERR_UNSUPPORTED;
     if (!(eps > 0.0f) || !(eps < 3.0e38f)) return RLK_ERR_INVALID_ARG;
     if (T > 0 && (!grad_out || !x || !gamma || !grad_x)) return RLK_ERR_INVALID_ARG;
-    if (T > 0 && grad_gamma && !workspace) return RLK_ERR_INVALID_ARG;
+    const size_t need = grad_gamma ? rlk_rmsnorm_backward_workspace_size(T, H) : 0;
+    if (need > 0 && !workspace) return RLK_ERR_INVALID_ARG;
     if (grad_x == grad_out && grad_x && grad_x_dtype != grad_out_dtype) return RLK_ERR_INVALID_ARG;
     if (!aligned(grad_out, 16) || !aligned(x, 16) || !aligned(gamma, 16) ||
         !aligned(grad_residual, 16) || !aligned(grad_x, 16) || !aligned(grad_gamma, 16) ||
         !aligned(workspace, 256))
         return RLK_ERR_ALIGNMENT;
-    if (grad_gamma && workspace_bytes < rlk_rmsnorm_backward_workspace_size(T, H))
-        return RLK_ERR_WORKSPACE;
+    if (workspace_bytes < need) return RLK_ERR_WORKSPACE;
     if (T == 0 && !grad_gamma) return RLK_OK;
     DeviceState* dev = nullptr;
     rlk_status_t s = device_check(&dev);

@@ -9,12 +9,14 @@
 //
 // A row's grad_x does not depend on the batch around it.  grad_gamma is
 // summed over at most 152 ranges of consecutive rows, one CTA each, then over
-// the ranges, in an order that T, H and the types fix.
+// the ranges by a second launch, in an order that T, H and the types fix.  Up
+// to kRmsBwdClusterRows rows one cluster of 8 CTAs does both in one launch.
 //
 // Element i = 256 g + 8 l + j is lane l's j-th value of column group g, as in
 // the forward; a thread holds 16 features (two groups), so that the shuffles,
 // the barrier and the scalar arithmetic of a row are spread over twice as many
 // features as with 8.
+#include <cooperative_groups.h>
 #include <cstdint>
 
 #include "rlk_contract.cuh"
@@ -23,6 +25,8 @@
 
 namespace rlk {
 namespace {
+
+namespace cg = cooperative_groups;
 
 // 16-byte pieces of 8 features
 template <int kType>
@@ -252,24 +256,37 @@ __global__ void __launch_bounds__(kCtaThreads<kWarps, kGo, kGx>, 1) k_rmsnorm_ba
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!a.grad_gamma) return;
-    float* const out = a.parts + static_cast<int64_t>(blockIdx.x) * a.H;
+    // the range's sums: the teams' in ascending order.  The ring is empty and holds them.
+    float* const teams = reinterpret_cast<float*>(ring);
+    float* const sums = teams + kThreads * 16;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ctas = static_cast<int>(cluster.num_blocks());
+    float* const out = ctas > 1 ? sums : a.parts + static_cast<int64_t>(blockIdx.x) * a.H;
     if constexpr (kTeams == 1) {
 #pragma unroll
         for (int g = 0; g < 2; ++g)
             if (in[g]) store8<RLK_DTYPE_F32>(out, i0 + 256 * g, dg[g]);
     } else {
-        // the teams' sums in ascending order; the ring is empty
-        float* const dg_teams = reinterpret_cast<float*>(ring);
         __syncthreads();
 #pragma unroll
-        for (int g = 0; g < 2; ++g) store8<RLK_DTYPE_F32>(dg_teams, team * kWarps * 512 + i0 + 256 * g, dg[g]);
+        for (int g = 0; g < 2; ++g) store8<RLK_DTYPE_F32>(teams, team * kWarps * 512 + i0 + 256 * g, dg[g]);
         __syncthreads();
         for (int i = threadIdx.x; i < a.H; i += kThreads) {
-            float v = dg_teams[i];
+            float v = teams[i];
 #pragma unroll
-            for (int k = 1; k < kTeams; ++k) v = __fadd_rn(v, dg_teams[k * kWarps * 512 + i]);
+            for (int k = 1; k < kTeams; ++k) v = __fadd_rn(v, teams[k * kWarps * 512 + i]);
             out[i] = v;
         }
+    }
+    if (ctas > 1) {
+        // one cluster: each CTA adds a share of the features over the CTAs, ascending
+        cluster.sync();
+        for (int i = static_cast<int>(cluster.block_rank()) * kThreads + threadIdx.x; i < a.H; i += ctas * kThreads) {
+            float v = cluster.map_shared_rank(sums, 0)[i];
+            for (int c = 1; c < ctas; ++c) v = __fadd_rn(v, cluster.map_shared_rank(sums, c)[i]);
+            a.grad_gamma[i] = v;
+        }
+        cluster.sync();  // nobody leaves while its shared memory may be read
     }
 }
 
@@ -298,8 +315,19 @@ cudaError_t launch_types(const RmsBwdArgs& a, int blocks, cudaStream_t stream) {
     const cudaError_t e = cudaFuncSetAttribute(k_rmsnorm_backward<kWarps, kGo, kGx>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
     if (e != cudaSuccess) return e;
-    k_rmsnorm_backward<kWarps, kGo, kGx><<<blocks, kThreads, kSmem, stream>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(blocks, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = rmsnorm_backward_one_launch(a.T) && a.grad_gamma ? blocks : 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_rmsnorm_backward<kWarps, kGo, kGx>, a);
 }
 
 template <int kWarps>
@@ -314,7 +342,8 @@ cudaError_t launch_row(const RmsBwdArgs& a, int blocks, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_rmsnorm_backward(const RmsBwdArgs& a, cudaStream_t stream) {
-    const int blocks = rmsnorm_backward_ranges(a.T);
+    const bool one = rmsnorm_backward_one_launch(a.T) && a.grad_gamma;
+    const int blocks = one ? 8 : rmsnorm_backward_ranges(a.T);
     int warps = 1;
     while (warps * 512 < a.H) warps *= 2;
     cudaError_t e = cudaSuccess;
@@ -326,7 +355,7 @@ cudaError_t launch_rmsnorm_backward(const RmsBwdArgs& a, cudaStream_t stream) {
         case 16: e = launch_row<16>(a, blocks, stream); break;
         default: return cudaErrorInvalidValue;
     }
-    if (e != cudaSuccess || !a.grad_gamma) return e;
+    if (e != cudaSuccess || !a.grad_gamma || one) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3(a.H / 32, 1, 1);

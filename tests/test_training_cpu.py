@@ -92,7 +92,7 @@ def test_preference_loss_refusals(L):
 
 
 def test_rmsnorm_backward_refusals(L):
-    ok = dict(go=0x10000, god=0, x=0x20000, gamma=0x30000, eps=1e-6, res=None, T=4, H=4096,
+    ok = dict(go=0x10000, god=0, x=0x20000, gamma=0x30000, eps=1e-6, res=None, T=100, H=4096,
               gx=0x40000, gxd=1, gg=0x50000, ws=0x60000, wsb=1 << 20)
 
     def call(**kw):
@@ -111,7 +111,9 @@ def test_rmsnorm_backward_refusals(L):
         refused(call, ALIGNMENT, **kw)
     refused(call, WORKSPACE, wsb=10)
     refused(call, OK, T=0, gg=None)
-    assert L.rlk_rmsnorm_backward_workspace_size(4, 100) == 0
+    assert L.rlk_rmsnorm_backward_workspace_size(100, 100) == 0
+    assert L.rlk_rmsnorm_backward_workspace_size(16, 4096) == 0  # one launch, no workspace
+    assert L.rlk_rmsnorm_backward_workspace_size(17, 4096) >= 17 * 4096 * 4
 
 
 def _arrays(ptrs, sizes, types):
