@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(kCtaThreads<kWarps, kGo, kGx>, 1) k_rmsnorm_ba
     constexpr int kN = kStages<kWarps, kGo, kGx>;
     constexpr int kGroup = 1 + kPieces<kGo> + kPieces<kGx>;  // pieces of 8 features
     static_assert(kN >= 2, "a row flies while another is worked on");
+    static_assert(kWarps == 1 || kTeams <= 15, "a named barrier (1 .. 15) per team");
     extern __shared__ uint4 ring[];  // [stage][group][piece][thread]: x, grad_out, grad_residual
     __shared__ __align__(16) float2 part[2][kThreads / 32];
     ptx::grid_dependents_launch();
