@@ -40,6 +40,10 @@
  *   - Pointers named as device pointers must point to device memory of the
  *     current CUDA device; the caller owns every buffer.  The library keeps
  *     no per-call state and allocates no device memory.
+ *   - A workspace serves one call at a time: calls that may overlap on the
+ *     GPU (on unordered streams, or in graphs replayed side by side) need
+ *     one each.  Outputs must not overlap inputs, other outputs or the
+ *     workspace except where a call says so.
  *   - Calls are asynchronous and stream-ordered on `stream` (NULL = legacy
  *     default stream); outputs are valid once the stream reaches them.
  *   - Host-detectable errors are returned before anything is launched.

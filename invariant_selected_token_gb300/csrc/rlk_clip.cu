@@ -19,6 +19,14 @@
 // launch for the sums and one for the scaling, whose CTAs each form the norm
 // from all CTAs' sums; the second takes the pieces in descending order, from
 // those that the first left in L2.
+//
+// What bounds it: three passes over HBM (in, in again, out) for sets larger
+// than L2.  grad_W [151936, 4096] in fp32: 7.47 GB in 1.12 ms, 6.66 TB/s, the
+// rate of a plain copy; 290 ragged bf16 and fp32 tensors: 1.42 GB in 229 us,
+// 6.2 TB/s; 12 tensors of 40001 elements in all: 7.3 us, latency.  Measured
+// and dropped for the two large sets: one element a load 1607 and 660 us; a
+// barrier after every 16384 elements 1107 and 233; warps alone on 2048
+// elements 1143 and 235; one unbroken run of elements a CTA 1121 and 283.
 #include <cooperative_groups.h>
 
 #include "rlk_ptx.cuh"

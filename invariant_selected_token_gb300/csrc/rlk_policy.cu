@@ -23,6 +23,13 @@
 // is 8 spans of 128 consecutive tokens; lane l of a span adds RN(w x) of
 // tokens l, l + 32, l + 64, l + 96 pairwise, the lanes a shuffle tree, the
 // spans in order.
+//
+// What bounds it.  Up to some 10^5 tokens latency: 4.3 us a call on the device
+// at 512 tokens, 5.8 at 8192, of which one launch, one round trip to memory
+// and the first fetch of the code make most.  At 1.77 M tokens (37 MB, 5.6 us
+// of HBM) 19.6 us: 6 us of the counting launch, then about 150 instructions a
+// token, two tokens per instruction where the values allow.  Sums in fp64
+// instead of pairs of floats made it 27, the branching form of a token 23 us.
 #include <cooperative_groups.h>
 
 #include "rlk_ptx.cuh"

@@ -23,6 +23,12 @@
 // a second launch.  A few very long pairs, whose teams would leave most of the
 // device idle, take one launch over all chunks and one over all tokens, whose
 // CTAs each form the slopes they need.
+//
+// What bounds it: latency.  7.3 us a call on the device for 4 pairs of 255
+// tokens, 10.1 for 64 pairs of 2048 (1.7 MB), 17 for 4 pairs of 262144 (13.6
+// MB, 2.0 us of HBM): a launch, the offsets, the tokens, three barriers and
+// about thirty dependent fp64 operations one after the other.  With fp64 sums
+// over the tokens the three took 14, 14 and 43 us.
 #include <cooperative_groups.h>
 
 #include "rlk_ptx.cuh"

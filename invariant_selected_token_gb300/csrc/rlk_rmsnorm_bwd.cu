@@ -16,6 +16,13 @@
 // the forward; a thread holds 16 features (two groups), so that the shuffles,
 // the barrier and the scalar arithmetic of a row are spread over twice as many
 // features as with 8.
+//
+// What bounds it: HBM.  8191 x 8192 in bf16 with residual: 537 MB in 82 us,
+// 6.55 TB/s, 0.98 of a plain copy; 4096 x 4096 from fp32 into bf16 with
+// residual: 168 MB in 34 us, 0.74 (at 16384 rows 0.87: the rest is the start,
+// the tail and the second launch); 64 rows: 5.1 us, latency.  On the way the
+// first two took 162 and 66 us with one row at a time, 111 and 37 with the
+// next row in registers, 88 and 38 with 16 features a thread and the ring.
 #include <cooperative_groups.h>
 #include <cstdint>
 

@@ -87,7 +87,7 @@ def test_preference_loss_refusals(L):
     refused(call, WORKSPACE, T=200000, ws=0x10000, wsb=100)
     assert L.rlk_preference_loss_workspace_size(200000, 3) >= 256 + 12 * (200000 // 256)
     assert L.rlk_preference_loss_workspace_size(10 ** 8, 40) == 0
-    assert L.rlk_preference_loss_workspace_size(190000, 3) == 0
+    assert L.rlk_preference_loss_workspace_size(98000, 3) == 0
     assert L.rlk_preference_loss_workspace_size(-1, 3) == 0
 
 
