@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import functools
 import operator
 import os
 from typing import List, Optional, Sequence, Tuple
@@ -505,14 +506,16 @@ def rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6,
 # ----------------------------------------------------------------- training step
 # Small batches of these calls take a few microseconds on the device, so their marshalling is
 # kept short: one check per tensor that passes its address on as a plain integer, and no device
-# or stream context where the tensors' device is current and the stream is its current one.
+# or stream context where the tensors' device is current and the stream is its current one.  A
+# call that is to run elsewhere enters the context and starts over.
 KL_KINDS = {"k1": 1, "k2": 2, "k3": 3}
 REDUCTIONS = {"sum": 0, "token_mean": 1, "seq_mean": 2}
 PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "ipo": 2}
 PAIR_LAYOUTS = {"adjacent": 0, "halves": 1}
 GRAD_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+               or (lambda index: torch.cuda.current_stream(index).cuda_stream))
 _get_dtype = operator.attrgetter("dtype")
 _TENSOR_TYPES = {torch.Tensor, torch.nn.Parameter}
 
@@ -544,16 +547,26 @@ def _status_addr(status: Optional[torch.Tensor], index: int):
     return status.data_ptr()
 
 
-def _call_on(device, stream, call):
-    """call(raw stream), on the device and with `stream` current: what the call allocates then
-    belongs to the stream that uses it, and torch does not hand it out again too early."""
-    if stream is None and _raw_stream is not None and _current_device() == device.index:
-        return call(_raw_stream(device.index))
-    with _on(device):
-        if stream is None:
-            return call(torch.cuda.current_stream(device).cuda_stream)
-        with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
+def _elsewhere(device, stream) -> bool:
+    """Whether a call has to be made inside _context(): on a device that is not current, or on a
+    stream that is not its current one."""
+    return stream is not None or _current_device() != device.index
+
+
+class _context:
+    """The device, and `stream` if given, made current: what the call allocates then belongs to
+    the stream that uses it, and torch does not hand it out again too early."""
+
+    def __init__(self, device, stream):
+        self.on = [_on(device)] + ([] if stream is None else [torch.cuda.stream(stream)])
+
+    def __enter__(self):
+        for c in self.on:
+            c.__enter__()
+
+    def __exit__(self, *exc):
+        for c in reversed(self.on):
+            c.__exit__(*exc)
 
 
 def _workspace(given: Optional[torch.Tensor], n: int, device):
@@ -565,6 +578,11 @@ def _workspace(given: Optional[torch.Tensor], n: int, device):
         return None, 0, None
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     return ws.data_ptr(), n, ws
+
+
+@functools.lru_cache(maxsize=1024)
+def rmsnorm_backward_workspace_size(T: int, H: int) -> int:
+    return int(lib().rlk_rmsnorm_backward_workspace_size(T, H))
 
 
 def rmsnorm_backward(grad_out: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor,
@@ -581,6 +599,10 @@ def rmsnorm_backward(grad_out: torch.Tensor, x: torch.Tensor, gamma: torch.Tenso
     is the gradient of both x and the residual.  grad_x may be grad_residual itself."""
     _require(x, torch.bfloat16, "x", ndim=2)
     dev = x.device
+    if _elsewhere(dev, stream):
+        with _context(dev, stream):
+            return rmsnorm_backward(grad_out, x, gamma, eps, grad_residual, want_gamma, grad_dtype,
+                                    grad_x, grad_gamma, workspace)
     idx, shape = dev.index, x.shape
     T, H = shape
     go_code = DTYPES.get(getattr(grad_out, "dtype", None))
@@ -594,28 +616,23 @@ def rmsnorm_backward(grad_out: torch.Tensor, x: torch.Tensor, gamma: torch.Tenso
     a_go = _addr(grad_out, grad_out.dtype, "grad_out", idx, shape)
     a_gamma = _addr(gamma, torch.bfloat16, "gamma", idx, (H,))
     a_res = _opt_addr(grad_residual, grad_dtype, "grad_residual", idx, shape)
-    a_gx = _opt_addr(grad_x, grad_dtype, "grad_x", idx, shape)
-    a_gg = _opt_addr(grad_gamma, torch.float32, "grad_gamma", idx, (H,)) if want_gamma else None
-    L = lib()
-
-    def call(st):
-        gx, gg, p_gx, p_gg = grad_x, grad_gamma if want_gamma else None, a_gx, a_gg
-        if gx is None:
-            gx = torch.empty(shape, dtype=grad_dtype, device=dev)
-            p_gx = gx.data_ptr()
-        p_ws = ws_n = 0
-        if want_gamma:
-            if gg is None:
-                gg = torch.empty(H, dtype=torch.float32, device=dev)
-                p_gg = gg.data_ptr()
-            p_ws, ws_n, ws = _workspace(workspace, L.rlk_rmsnorm_backward_workspace_size(T, H), dev)
-        _check(L.rlk_rmsnorm_backward(a_go, go_code, x.data_ptr(), a_gamma, eps, a_res, T, H,
-                                      p_gx, gx_code, p_gg, p_ws, ws_n, st),
-               "rlk_rmsnorm_backward")
-        return gx, gg
-    return _call_on(dev, stream, call)
+    if grad_x is None:
+        grad_x = torch.empty(shape, dtype=grad_dtype, device=dev)
+    a_gx = _addr(grad_x, grad_dtype, "grad_x", idx, shape)
+    a_gg = p_ws = None
+    ws_n = 0
+    if want_gamma:
+        if grad_gamma is None:
+            grad_gamma = torch.empty(H, dtype=torch.float32, device=dev)
+        a_gg = _addr(grad_gamma, torch.float32, "grad_gamma", idx, (H,))
+        p_ws, ws_n, ws = _workspace(workspace, rmsnorm_backward_workspace_size(T, H), dev)
+    _check(lib().rlk_rmsnorm_backward(a_go, go_code, x.data_ptr(), a_gamma, eps, a_res, T, H, a_gx,
+                                      gx_code, a_gg, p_ws, ws_n, _raw_stream(idx)),
+           "rlk_rmsnorm_backward")
+    return grad_x, (grad_gamma if want_gamma else None)
 
 
+@functools.lru_cache(maxsize=1024)
 def policy_loss_workspace_size(T: int, n_seqs: int = 1) -> int:
     return int(lib().rlk_policy_loss_workspace_size(T, n_seqs))
 
@@ -639,6 +656,11 @@ def policy_loss(logprob: torch.Tensor, old_logprob: torch.Tensor, advantages: to
     f32 = torch.float32
     _require(logprob, f32, "logprob", ndim=1)
     dev, shape = logprob.device, logprob.shape
+    if _elsewhere(dev, stream):
+        with _context(dev, stream):
+            return policy_loss(logprob, old_logprob, advantages, ref_logprob, active, seq_offsets,
+                               advantages_per_seq, clip_low, clip_high, dual_clip, kl, kl_coef,
+                               reduction, scale, want_grad, grad_logprob, workspace, status)
     idx, T = dev.index, shape[0]
     n_seqs, a_off = 1, None
     if seq_offsets is not None:
@@ -648,27 +670,24 @@ def policy_loss(logprob: torch.Tensor, old_logprob: torch.Tensor, advantages: to
     a_adv = _addr(advantages, f32, "advantages", idx, (n_seqs,) if advantages_per_seq else shape)
     a_ref = _opt_addr(ref_logprob, f32, "ref_logprob", idx, shape)
     a_act = _opt_addr(active, torch.uint8, "active", idx, shape)
-    a_grad = _opt_addr(grad_logprob, f32, "grad_logprob", idx, shape) if want_grad else None
     a_status = _status_addr(status, idx)
     kl_code, red = _choice(KL_KINDS, kl, "kl"), _choice(REDUCTIONS, reduction, "reduction")
-    L = lib()
-
-    def call(st):
-        loss = torch.empty((), dtype=f32, device=dev)
-        stats = torch.empty(4, dtype=f32, device=dev)
-        grad, p_grad = grad_logprob if want_grad else None, a_grad
-        if want_grad and grad is None:
-            grad = torch.empty(T, dtype=f32, device=dev)
-            p_grad = grad.data_ptr()
-        p_ws, ws_n, ws = _workspace(workspace, L.rlk_policy_loss_workspace_size(T, n_seqs), dev)
-        _check(L.rlk_policy_loss(logprob.data_ptr(), a_old, a_ref, a_adv, advantages_per_seq,
+    a_grad = None
+    if want_grad:
+        if grad_logprob is None:
+            grad_logprob = torch.empty(T, dtype=f32, device=dev)
+        a_grad = _addr(grad_logprob, f32, "grad_logprob", idx, shape)
+    loss = torch.empty((), dtype=f32, device=dev)
+    stats = torch.empty(4, dtype=f32, device=dev)
+    p_ws, ws_n, ws = _workspace(workspace, policy_loss_workspace_size(T, n_seqs), dev)
+    _check(lib().rlk_policy_loss(logprob.data_ptr(), a_old, a_ref, a_adv, advantages_per_seq,
                                  a_act, a_off, n_seqs, T, clip_low, clip_high, dual_clip, kl_code,
-                                 kl_coef, red, scale, loss.data_ptr(), stats.data_ptr(), p_grad,
-                                 p_ws, ws_n, a_status, st), "rlk_policy_loss")
-        return loss, stats, grad
-    return _call_on(dev, stream, call)
+                                 kl_coef, red, scale, loss.data_ptr(), stats.data_ptr(), a_grad,
+                                 p_ws, ws_n, a_status, _raw_stream(idx)), "rlk_policy_loss")
+    return loss, stats, (grad_logprob if want_grad else None)
 
 
+@functools.lru_cache(maxsize=1024)
 def preference_loss_workspace_size(T: int, n_pairs: int) -> int:
     return int(lib().rlk_preference_loss_workspace_size(T, n_pairs))
 
@@ -691,6 +710,11 @@ def preference_loss(logprob: torch.Tensor, seq_offsets: torch.Tensor,
     f32 = torch.float32
     _require(logprob, f32, "logprob", ndim=1)
     dev, shape = logprob.device, logprob.shape
+    if _elsewhere(dev, stream):
+        with _context(dev, stream):
+            return preference_loss(logprob, seq_offsets, ref_logprob, active, beta, kind,
+                                   label_smoothing, margin, length_normalize, layout, scale,
+                                   want_grad, grad_logprob, workspace, status)
     idx, T = dev.index, shape[0]
     _require(seq_offsets, torch.int32, "seq_offsets", dev, 1)
     n_seqs = seq_offsets.shape[0] - 1
@@ -699,28 +723,24 @@ def preference_loss(logprob: torch.Tensor, seq_offsets: torch.Tensor,
     P = n_seqs // 2
     a_ref = _opt_addr(ref_logprob, f32, "ref_logprob", idx, shape)
     a_act = _opt_addr(active, torch.uint8, "active", idx, shape)
-    a_grad = _opt_addr(grad_logprob, f32, "grad_logprob", idx, shape) if want_grad else None
     a_status = _status_addr(status, idx)
     kind_code = _choice(PREFERENCE_KINDS, kind, "kind")
     layout_code = _choice(PAIR_LAYOUTS, layout, "layout")
-    L = lib()
-
-    def call(st):
-        loss = torch.empty((), dtype=f32, device=dev)
-        pair_loss = torch.empty(P, dtype=f32, device=dev)
-        rewards = torch.empty(n_seqs, dtype=f32, device=dev)
-        grad, p_grad = grad_logprob if want_grad else None, a_grad
-        if want_grad and grad is None:
-            grad = torch.empty(T, dtype=f32, device=dev)
-            p_grad = grad.data_ptr()
-        p_ws, ws_n, ws = _workspace(workspace, L.rlk_preference_loss_workspace_size(T, P), dev)
-        _check(L.rlk_preference_loss(logprob.data_ptr(), a_ref, a_act, seq_offsets.data_ptr(), P,
+    a_grad = None
+    if want_grad:
+        if grad_logprob is None:
+            grad_logprob = torch.empty(T, dtype=f32, device=dev)
+        a_grad = _addr(grad_logprob, f32, "grad_logprob", idx, shape)
+    loss = torch.empty((), dtype=f32, device=dev)
+    pair_loss = torch.empty(P, dtype=f32, device=dev)
+    rewards = torch.empty(n_seqs, dtype=f32, device=dev)
+    p_ws, ws_n, ws = _workspace(workspace, preference_loss_workspace_size(T, P), dev)
+    _check(lib().rlk_preference_loss(logprob.data_ptr(), a_ref, a_act, seq_offsets.data_ptr(), P,
                                      T, layout_code, kind_code, beta, label_smoothing, margin,
                                      length_normalize, scale, loss.data_ptr(),
-                                     pair_loss.data_ptr(), rewards.data_ptr(), p_grad, p_ws, ws_n,
-                                     a_status, st), "rlk_preference_loss")
-        return loss, pair_loss, rewards, grad
-    return _call_on(dev, stream, call)
+                                     pair_loss.data_ptr(), rewards.data_ptr(), a_grad, p_ws, ws_n,
+                                     a_status, _raw_stream(idx)), "rlk_preference_loss")
+    return loss, pair_loss, rewards, (grad_logprob if want_grad else None)
 
 
 def _grad_list(grads, name: str):
@@ -754,22 +774,23 @@ def grad_norm(grads: Sequence[torch.Tensor], workspace: Optional[torch.Tensor] =
               status: Optional[torch.Tensor] = None, device=None, stream=None) -> torch.Tensor:
     """sqrt of the sum of squares over all the tensors (fp32, bf16 or fp16, contiguous) as a
     0-dim fp32 tensor.  `device` says where an empty list's norm goes."""
-    dev, sizes, dtypes, ptrs = _grad_list(list(grads), "grads")
+    grads = list(grads)
+    dev, sizes, dtypes, ptrs = _grad_list(grads, "grads")
     if dev is None:
         dev = _cuda_device(device)
+    if _elsewhere(dev, stream):
+        with _context(dev, stream):
+            return grad_norm(grads, workspace, status, dev)
     a_status = _status_addr(status, dev.index)
     n = len(sizes)
     sizes, types = _host_arrays(sizes, dtypes)
     h_ptrs, h_sizes, h_types = (_host_addr(a) for a in (ptrs, sizes, types))
     L = lib()
-
-    def call(st):
-        norm = torch.empty((), dtype=torch.float32, device=dev)
-        p_ws, ws_n, ws = _workspace(workspace, L.rlk_grad_norm_workspace_size(h_sizes, h_types, n), dev)
-        _check(L.rlk_grad_norm(h_ptrs, h_sizes, h_types, n, norm.data_ptr(), p_ws, ws_n, a_status, st),
-               "rlk_grad_norm")
-        return norm
-    return _call_on(dev, stream, call)
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    p_ws, ws_n, ws = _workspace(workspace, L.rlk_grad_norm_workspace_size(h_sizes, h_types, n), dev)
+    _check(L.rlk_grad_norm(h_ptrs, h_sizes, h_types, n, norm.data_ptr(), p_ws, ws_n, a_status,
+                           _raw_stream(dev.index)), "rlk_grad_norm")
+    return norm
 
 
 def clip_grads(grads: Sequence[torch.Tensor], max_norm: float,
@@ -779,9 +800,13 @@ def clip_grads(grads: Sequence[torch.Tensor], max_norm: float,
     """Scale the gradients by min(1, max_norm / norm), in place or into the tensors of `out`
     (same sizes and types) -> (norm [], scale []).  With a norm that is not finite the values
     stay as they are, scale is 1 and the status word gets RLK_ERR_NONFINITE."""
-    dev, sizes, dtypes, ptrs = _grad_list(list(grads), "grads")
+    grads = list(grads)
+    dev, sizes, dtypes, ptrs = _grad_list(grads, "grads")
     if dev is None:
         dev = _cuda_device(device)
+    if _elsewhere(dev, stream):
+        with _context(dev, stream):
+            return clip_grads(grads, max_norm, out, workspace, status, dev)
     outs = ptrs
     if out is not None:
         out_dev, out_sizes, out_dtypes, outs = _grad_list(list(out), "out")
@@ -794,15 +819,13 @@ def clip_grads(grads: Sequence[torch.Tensor], max_norm: float,
     sizes, types = _host_arrays(sizes, dtypes)
     h_ptrs, h_outs, h_sizes, h_types = (_host_addr(a) for a in (ptrs, outs, sizes, types))
     L = lib()
-
-    def call(st):
-        norm = torch.empty((), dtype=torch.float32, device=dev)
-        scale = torch.empty((), dtype=torch.float32, device=dev)
-        p_ws, ws_n, ws = _workspace(workspace, L.rlk_grad_norm_workspace_size(h_sizes, h_types, n), dev)
-        _check(L.rlk_grad_clip(h_ptrs, h_outs, h_sizes, h_types, n, max_norm, norm.data_ptr(),
-                               scale.data_ptr(), p_ws, ws_n, a_status, st), "rlk_grad_clip")
-        return norm, scale
-    return _call_on(dev, stream, call)
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    scale = torch.empty((), dtype=torch.float32, device=dev)
+    p_ws, ws_n, ws = _workspace(workspace, L.rlk_grad_norm_workspace_size(h_sizes, h_types, n), dev)
+    _check(L.rlk_grad_clip(h_ptrs, h_outs, h_sizes, h_types, n, max_norm, norm.data_ptr(),
+                           scale.data_ptr(), p_ws, ws_n, a_status, _raw_stream(dev.index)),
+           "rlk_grad_clip")
+    return norm, scale
 
 
 def _cuda_device(device) -> torch.device:
