@@ -429,7 +429,8 @@ rlk_status_t rlk_rmsnorm_backward(const void* grad_out, int grad_out_dtype, cons
  *
  * A token takes part if its mask is nonzero and it lies in
  * [seq_offsets[0], seq_offsets[n_seqs]); any other token's inputs are not
- * used (they may be NaN) and its grad is 0.  Per-token terms are fp32; their
+ * used (they may be NaN) and its grad is 0; a value that is not finite of a
+ * token that takes part goes into the loss and its own grad.  Per-token terms are fp32; their
  * sums run over fixed ranges of 1024 tokens in fp32 and then as pairs of
  * floats, so the results are the same bits on every run.  T == 0 gives loss and stats 0.
  *
@@ -442,6 +443,7 @@ rlk_status_t rlk_rmsnorm_backward(const void* grad_out, int grad_out_dtype, cons
  *                 RLK_ERR_INVALID_ARG in *dev_status and make loss and stats NaN
  *   clip_low, clip_high  >= 0;  dual_clip  0 (off) or > 1;  kl_kind  RLK_KL_K1 .. RLK_KL_K3
  *   out_loss      device, float [1]
+ *   kl_coef       finite; with 0 the KL term is only reported in out_stats
  *   out_stats     device, float [4]: sums (with weights w_t, without scale) of -s, of k, of the
  *                 clipped tokens and of old_logprob - logprob
  *   grad_logprob  device, float [T], or NULL for the loss alone

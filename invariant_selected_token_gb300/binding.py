@@ -558,6 +558,8 @@ class _context:
     the stream that uses it, and torch does not hand it out again too early."""
 
     def __init__(self, device, stream):
+        if stream is not None and stream.device != device:
+            raise ValueError("stream is on %s, the tensors are on %s" % (stream.device, device))
         self.on = [_on(device)] + ([] if stream is None else [torch.cuda.stream(stream)])
 
     def __enter__(self):

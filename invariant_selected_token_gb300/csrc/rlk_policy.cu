@@ -108,7 +108,7 @@ __device__ __forceinline__ TokenTerms token_terms(const PolicyArgs& a, float2 d,
     if constexpr (kKl != 0) {
         const float dk = kKl == RLK_KL_K1 ? 1.0f : kKl == RLK_KL_K2 ? -u : -__fadd_rn(k3, u);
         o.kl = kKl == RLK_KL_K1 ? -u : kKl == RLK_KL_K2 ? __fmul_rn(__fmul_rn(0.5f, u), u) : k3;
-        o.slope = __fmaf_rn(a.kl_coef, dk, o.slope);
+        if (a.kl_coef != 0.0f) o.slope = __fmaf_rn(a.kl_coef, dk, o.slope);  // else k may overflow unharmed
     }
     return o;
 }
@@ -275,7 +275,8 @@ __device__ __forceinline__ void write_stat(const PolicyArgs& a, int k, float2 v,
     a.out_stats[k] = bad ? CUDART_NAN_F : __fadd_rn(v.x, v.y);
 }
 __device__ __forceinline__ void write_loss(const PolicyArgs& a, float2 policy, float2 kl, bool bad) {
-    const double sum = __fma_rn(a.kl_coef64, pair_value(kl), pair_value(policy));
+    double sum = pair_value(policy);
+    if (a.kl_coef64 != 0.0) sum = __fma_rn(a.kl_coef64, pair_value(kl), sum);
     *a.out_loss = bad ? CUDART_NAN_F : static_cast<float>(__dmul_rn(a.scale, sum));
     if (bad) report_status(a.status, RLK_ERR_INVALID_ARG);
 }

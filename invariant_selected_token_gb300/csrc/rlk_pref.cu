@@ -98,7 +98,10 @@ __device__ __forceinline__ void pair_terms(const PreferenceArgs& a, int pair, in
             const float large = __fdiv_rn(1.0f, __fadd_rn(1.0f, e));
             const float near = soft, far = __fadd_rn(soft, fabsf(z));  // -log sig(|z|), -log sig(-|z|)
             const bool up = z >= 0.0f;
-            loss = __fadd_rn(__fmul_rn(keep, up ? near : far), __fmul_rn(eps, up ? far : near));
+            // a part with weight 0 is 0 even where its log is infinite
+            loss = __fadd_rn(keep != 0.0f ? __fmul_rn(keep, up ? near : far) : 0.0f,
+                             eps != 0.0f ? __fmul_rn(eps, up ? far : near) : 0.0f);
+            if (z != z) loss = z;
             // sig(z) - (1 - eps) = eps sig(z) - (1 - eps) sig(-z)
             dh = __fmul_rn(beta, __fsub_rn(__fmul_rn(eps, up ? large : small), __fmul_rn(keep, up ? small : large)));
         }

@@ -277,7 +277,7 @@ def test_a_tokens_gradient_does_not_depend_on_the_batch(rlk, cuda_device):
         assert torch.equal(run(rlk, cuda_device, part, kl_coef=0.1, reduction="sum")[2], full[lo:hi])
 
 
-@pytest.mark.parametrize("T", [600, 50000])
+@pytest.mark.parametrize("T", [600, 5000, 20000, 50000])
 def test_graph_replay(rlk, cuda_device, T):
     bs = [batch(T, [0, T // 3, T], seed=s) for s in (11, 12)]
     eager = [run(rlk, cuda_device, b, kl_coef=0.1) for b in bs]
@@ -297,6 +297,17 @@ def test_graph_replay(rlk, cuda_device, T):
         assert torch.equal(loss, e[0]) and torch.equal(stats, e[1]) and torch.equal(grad, e[2])
 
 
+def test_a_reported_kl_may_overflow(rlk, cuda_device):
+    """ref - lp = 200: k3 is beyond fp32, and with kl_coef 0 only the report is."""
+    lp = torch.tensor([-200.0, -1.0], device=cuda_device)
+    ref = torch.tensor([0.0, -1.0], device=cuda_device)
+    for T in (2, 9000, 40000):  # every launch shape
+        pad = torch.zeros(T - 2, device=cuda_device)
+        x, r = torch.cat([lp, pad]), torch.cat([ref, pad])
+        loss, stats, g = rlk.policy_loss(x, x, torch.ones_like(x), ref_logprob=r, reduction="sum")
+        assert float(loss) == -T and torch.all(g == -1) and torch.isinf(stats[1])
+
+
 def test_binding_shape_checks(rlk, cuda_device):
     x = torch.zeros(8, device=cuda_device)
     off = torch.tensor([0, 4, 8], dtype=torch.int32, device=cuda_device)
@@ -306,6 +317,10 @@ def test_binding_shape_checks(rlk, cuda_device):
                  lambda: rlk.policy_loss(x, x, x, grad_logprob=x[:3])):
         with pytest.raises(ValueError):
             call()
+    class Elsewhere:  # a stream of another device
+        device = torch.device("cuda", x.get_device() + 1)
+    with pytest.raises(ValueError):
+        rlk.policy_loss(x, x, x, stream=Elsewhere())
     with pytest.raises(TypeError):
         rlk.policy_loss(x, x, x, seq_offsets=off.long())
     with pytest.raises(rlk.RlkError):

@@ -149,6 +149,18 @@ def test_far_margins_do_not_overflow(rlk, cuda_device):
     assert grad.tolist() == [0.0, 0.0, -0.5, 0.5]
 
 
+def test_infinite_margins(rlk, cuda_device):
+    """A token of probability 0 on either side: the loss is 0 or infinite, its slope 0 or beta."""
+    inf = np.inf
+    b = dict(lp=np.array([-1.0, -inf, -inf, -1.0], np.float32), ref=None, active=None,
+             offsets=[0, 1, 2, 3, 4])
+    _, pair, rew, grad = run(rlk, cuda_device, b, beta=1.0)
+    assert pair.tolist() == [0.0, inf] and rew.tolist() == [-1.0, -inf, -inf, -1.0]
+    assert grad.tolist() == [0.0, 0.0, -0.5, 0.5]
+    _, pair, _, _ = run(rlk, cuda_device, b, beta=1.0, label_smoothing=1.0)
+    assert pair.tolist() == [inf, 0.0]
+
+
 def test_one_sided_nan_stays_in_its_pair(rlk, cuda_device):
     b = batch(400, [0, 100, 200, 300, 400], seed=7, mask=1.0)
     b["lp"][150] = np.nan

@@ -111,3 +111,38 @@ def test_the_step_in_a_graph(rlk, cuda_device, loss_kind):
         for k in e:
             assert torch.equal(out[k], e[k]), k
     rlk.raise_on_device_status(status)
+
+
+def test_calls_at_once_on_two_streams(rlk, cuda_device):
+    """Every operator on two streams at a time, small and large sizes mixed, each with its own
+    buffers: the bits of the calls made one after the other."""
+    g = torch.Generator(device=cuda_device)
+    g.manual_seed(31)
+    r = lambda *s: torch.randn(*s, generator=g, device=cuda_device)  # noqa: E731
+
+    def calls(T, H):
+        lp, old, adv = -r(T).abs(), -r(T).abs(), r(T)
+        off = torch.tensor([0, T // 5, T // 2, T // 2 + 1, T], dtype=torch.int32, device=cuda_device)
+        act = (r(T) < 1).to(torch.uint8)
+        x, dy = r(T % 977 + 3, H).to(torch.bfloat16), r(T % 977 + 3, H)
+        gamma = r(H).to(torch.bfloat16)
+        grads = [r(T), r(3 * T + 1).to(torch.bfloat16), r(7)]
+        return [lambda: rlk.policy_loss(lp, old, adv, ref_logprob=old, active=act, seq_offsets=off, kl_coef=0.1,
+                                        reduction="seq_mean"),
+                lambda: rlk.preference_loss(lp, off, ref_logprob=old, active=act),
+                lambda: rlk.rmsnorm_backward(dy, x, gamma),
+                lambda: (*rlk.clip_grads(grads, 1.0, out=[torch.empty_like(t) for t in grads]), )]
+    work = [calls(T, H) for T, H in ((700, 256), (9000, 1024), (300000, 4096))]
+    want = [[f() for f in fs] for fs in work]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(cuda_device) for _ in range(2)]
+    got = []
+    for rep in range(4):
+        for fs in work:
+            for k, s in enumerate(streams):
+                with torch.cuda.stream(s):
+                    got.append([f() for f in (fs if k else fs[::-1])][::1 if k else -1])
+    torch.cuda.synchronize()
+    for i, outs in enumerate(got):
+        for a, b in zip(outs, want[i // 2 % 3]):
+            assert all(torch.equal(x, y) for x, y in zip(a, b) if x is not None)
