@@ -1098,7 +1098,8 @@ rlk_status_t rlk_policy_loss(const float* logprob, const float* old_logprob,
     if (reduction < RLK_REDUCE_SUM || reduction > RLK_REDUCE_SEQ_MEAN) return RLK_ERR_UNSUPPORTED;
     if (!aligned(logprob, 4) || !aligned(old_logprob, 4) || !aligned(ref_logprob, 4) ||
         !aligned(advantages, 4) || !aligned(seq_offsets, 4) || !aligned(out_loss, 4) ||
-        !aligned(out_stats, 4) || !aligned(grad_logprob, 4) || !aligned(workspace, 256))
+        !aligned(out_stats, 4) || !aligned(grad_logprob, 4) || !aligned(workspace, 256) ||
+        !aligned(dev_status, 4))
         return RLK_ERR_ALIGNMENT;
     const PolicyLayout l = policy_layout_of(T, n_seqs);
     if (l.total > 0 && !workspace) return RLK_ERR_INVALID_ARG;
@@ -1170,7 +1171,7 @@ rlk_status_t rlk_preference_loss(const float* logprob, const float* ref_logprob,
         return RLK_ERR_INVALID_ARG;
     if (!aligned(logprob, 4) || !aligned(ref_logprob, 4) || !aligned(seq_offsets, 4) ||
         !aligned(out_loss, 4) || !aligned(out_pair_loss, 4) || !aligned(out_rewards, 4) ||
-        !aligned(grad_logprob, 4) || !aligned(workspace, 256))
+        !aligned(grad_logprob, 4) || !aligned(workspace, 256) || !aligned(dev_status, 4))
         return RLK_ERR_ALIGNMENT;
     const PreferenceLayout l = preference_layout_of(T, n_pairs);
     if (l.total > 0 && !workspace) return RLK_ERR_INVALID_ARG;
@@ -1222,7 +1223,7 @@ rlk_status_t rlk_grad_norm(const void* const* grads, const int64_t* numels,
     ClipPlan plan;
     rlk_status_t s = clip_checks(grads, numels, dtypes, n_tensors, workspace, workspace_bytes, &plan);
     if (s != RLK_OK) return s;
-    if (!aligned(out_norm, 4)) return RLK_ERR_ALIGNMENT;
+    if (!aligned(out_norm, 4) || !aligned(dev_status, 4)) return RLK_ERR_ALIGNMENT;
     DeviceState* dev = nullptr;
     if ((s = device_check(&dev)) != RLK_OK) return s;
     const rlk::ClipOut o = {out_norm, nullptr, dev_status, 0.0};
@@ -1242,7 +1243,8 @@ rlk_status_t rlk_grad_clip(const void* const* grads, void* const* outs, const in
     ClipPlan plan;
     rlk_status_t s = clip_checks(grads, numels, dtypes, n_tensors, workspace, workspace_bytes, &plan);
     if (s != RLK_OK) return s;
-    if (!aligned(out_norm, 4) || !aligned(out_scale, 4)) return RLK_ERR_ALIGNMENT;
+    if (!aligned(out_norm, 4) || !aligned(out_scale, 4) || !aligned(dev_status, 4))
+        return RLK_ERR_ALIGNMENT;
     for (int64_t i = 0; i < n_tensors; ++i) {
         if (numels[i] == 0) continue;
         if (!outs[i]) return RLK_ERR_INVALID_ARG;

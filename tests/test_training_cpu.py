@@ -34,14 +34,14 @@ def test_status_name(L):
 def test_policy_loss_refusals(L):
     ok = dict(lp=0x1000, old=0x2000, ref=0x3000, adv=0x4000, per_seq=0, act=0x5000, off=0x6000,
               S=2, T=100000, cl=0.2, ch=0.2, dual=0.0, kl=3, klc=0.1, red=1, scale=1.0, loss=0x7000,
-              stats=0x8000, grad=0x9000, ws=0x10000, wsb=1 << 20)
+              stats=0x8000, grad=0x9000, ws=0x10000, wsb=1 << 20, status=None)
 
     def call(**kw):
         a = dict(ok, **kw)
         return L.rlk_policy_loss(a["lp"], a["old"], a["ref"], a["adv"], a["per_seq"], a["act"],
                                  a["off"], a["S"], a["T"], a["cl"], a["ch"], a["dual"], a["kl"],
                                  a["klc"], a["red"], a["scale"], a["loss"], a["stats"], a["grad"],
-                                 a["ws"], a["wsb"], None, None)
+                                 a["ws"], a["wsb"], a["status"], None)
     for kw in (dict(lp=None), dict(old=None), dict(adv=None), dict(loss=None), dict(stats=None),
                dict(ws=None), dict(T=-1), dict(T=MAX_ROWS + 1), dict(S=-1), dict(off=None),
                dict(cl=-0.1), dict(ch=-0.1), dict(cl=math.nan), dict(ch=math.inf), dict(dual=0.5),
@@ -50,7 +50,8 @@ def test_policy_loss_refusals(L):
         refused(call, INVALID, **kw)
     for kw in (dict(kl=0), dict(kl=4), dict(red=3), dict(red=-1)):
         refused(call, UNSUPPORTED, **kw)
-    for kw in (dict(lp=0x1002), dict(off=0x6001), dict(ws=0x10010), dict(grad=0x9002)):
+    for kw in (dict(lp=0x1002), dict(off=0x6001), dict(ws=0x10010), dict(grad=0x9002),
+               dict(status=0x11002)):
         refused(call, ALIGNMENT, **kw)
     refused(call, WORKSPACE, wsb=100)
     assert L.rlk_policy_loss_workspace_size(-1, 1) == 0
@@ -64,14 +65,14 @@ def test_policy_loss_refusals(L):
 def test_preference_loss_refusals(L):
     ok = dict(lp=0x1000, ref=0x2000, act=0x3000, off=0x4000, P=3, T=10, layout=0, kind=0, beta=0.1,
               eps=0.0, margin=0.0, scale=1.0, loss=0x5000, pair=0x6000, rew=0x7000, grad=0x8000, ws=None,
-              wsb=0)
+              wsb=0, status=None)
 
     def call(**kw):
         a = dict(ok, **kw)
         return L.rlk_preference_loss(a["lp"], a["ref"], a["act"], a["off"], a["P"], a["T"],
                                      a["layout"], a["kind"], a["beta"], a["eps"], a["margin"], 0,
                                      a["scale"], a["loss"], a["pair"], a["rew"], a["grad"],
-                                     a["ws"], a["wsb"], None, None)
+                                     a["ws"], a["wsb"], a["status"], None)
     for kw in (dict(lp=None), dict(off=None), dict(loss=None), dict(pair=None), dict(rew=None),
                dict(T=-1), dict(T=MAX_ROWS + 1), dict(P=-1), dict(P=(1 << 30) + 1), dict(beta=0.0),
                dict(beta=-1.0), dict(beta=math.inf), dict(beta=math.nan), dict(eps=-0.1),
@@ -80,7 +81,8 @@ def test_preference_loss_refusals(L):
         refused(call, INVALID, **kw)
     for kw in (dict(layout=2), dict(kind=3), dict(kind=-1)):
         refused(call, UNSUPPORTED, **kw)
-    for kw in (dict(lp=0x1001), dict(off=0x4002), dict(rew=0x7002), dict(ws=0x10010)):
+    for kw in (dict(lp=0x1001), dict(off=0x4002), dict(rew=0x7002), dict(ws=0x10010),
+               dict(status=0x11001)):
         refused(call, ALIGNMENT, **kw)
     # few pairs of many tokens need a workspace
     refused(call, INVALID, T=200000)
@@ -124,12 +126,12 @@ def _arrays(ptrs, sizes, types):
 
 def test_grad_clip_refusals(L):
     def call(ptrs=(0x10000, 0x20000), outs=None, sizes=(16, 16), types=(0, 1), max_norm=1.0,
-             norm=0x1000, scale=0x2000, ws=0x100, wsb=1 << 20, norm_only=False):
+             norm=0x1000, scale=0x2000, ws=0x100, wsb=1 << 20, norm_only=False, status=None):
         p, s, t, n = _arrays(ptrs, sizes, types)
         o = p if outs is None else (ctypes.c_void_p * n)(*outs)
         if norm_only:
-            return L.rlk_grad_norm(p, s, t, n, norm, ws, wsb, None, None)
-        return L.rlk_grad_clip(p, o, s, t, n, max_norm, norm, scale, ws, wsb, None, None)
+            return L.rlk_grad_norm(p, s, t, n, norm, ws, wsb, status, None)
+        return L.rlk_grad_clip(p, o, s, t, n, max_norm, norm, scale, ws, wsb, status, None)
     for kw in (dict(ptrs=(None, 0x20000)), dict(sizes=(-1, 16)), dict(norm=None),
                dict(sizes=(1 << 20, 16), ws=None)):
         refused(call, INVALID, **kw)
@@ -146,8 +148,9 @@ def test_grad_clip_refusals(L):
     for kw in (dict(types=(0, 3)), dict(types=(-1, 0)), dict(sizes=((1 << 38) + 1, 1)), dict(sizes=(1 << 37, (1 << 37) + 1))):
         refused(call, UNSUPPORTED, **kw)
     for kw in (dict(ptrs=(0x10002, 0x20000)), dict(ptrs=(0x10000, 0x20001)),
-               dict(outs=(0x30002, 0x40000)), dict(ws=0x110)):
+               dict(outs=(0x30002, 0x40000)), dict(ws=0x110), dict(status=0x3002)):
         refused(call, ALIGNMENT, **kw)
+    refused(call, ALIGNMENT, norm_only=True, status=0x3002)
     refused(call, WORKSPACE, sizes=(1 << 20, 16), ptrs=(0x10000, 0x10000000), wsb=4)
     # 16 KB pieces, each tensor counted as if it started at the last byte of a 16-byte line
     types = (ctypes.c_int32 * 2)(0, 1)
