@@ -86,7 +86,7 @@ struct TokenTerms {
 
 // From d as two floats, r = e^d, u = ref - lp and (k3) e^u - 1 - u.  The two clips are one test:
 // with a negative advantage both d and the border change sign.
-template <int kKl>
+template <int kKl, bool kPlain>
 __device__ __forceinline__ TokenTerms token_terms(const PolicyArgs& a, float2 d, float r, float u, float k3, float A) {
     TokenTerms o;
     const bool up = A > 0.0f;
@@ -99,7 +99,7 @@ __device__ __forceinline__ TokenTerms token_terms(const PolicyArgs& a, float2 d,
         held = a.dual;
     }
     float s = __fmul_rn(held, A);
-    if (A == 0.0f && r == CUDART_INF_F) s = 0.0f;  // the ratio is finite, its fp32 value is not
+    if (!kPlain && A == 0.0f && r == CUDART_INF_F) s = 0.0f;  // the ratio is finite, its fp32 value is not
     o.policy = -s;
     o.clipped = shut ? 1.0f : 0.0f;
     o.neg_d = -d.x;
@@ -124,7 +124,7 @@ template <int kKl>
 __device__ __forceinline__ TokenTerms token_one(const PolicyArgs& a, float lp, float old, float ref, float A) {
     const float2 d = two_diff(lp, old);
     const float u = __fsub_rn(ref, lp);
-    return token_terms<kKl>(a, d, ratio_of(d), u, kKl == RLK_KL_K3 ? exp_minus_1_minus(u) : 0.0f, A);
+    return token_terms<kKl, false>(a, d, ratio_of(d), u, kKl == RLK_KL_K3 ? exp_minus_1_minus(u) : 0.0f, A);
 }
 
 // Two tokens, two per instruction as far as the values allow: |d| <= 80, where 2^n only adds to
@@ -165,8 +165,8 @@ __device__ __forceinline__ void token_two(const PolicyArgs& a, const float (&lp)
         for (int i = 1; i < kExpTail; ++i) p = f2_fma(p, u2, f2_splat(exp_tail(i)));
         f2_unpack(f2_mul(f2_mul(u2, u2), p), k0, k1);
     }
-    o[0] = token_terms<kKl>(a, make_float2(d0, e0), r0, u0, k0, A[0]);
-    o[1] = token_terms<kKl>(a, make_float2(d1, e1), r1, u1, k1, A[1]);
+    o[0] = token_terms<kKl, true>(a, make_float2(d0, e0), r0, u0, k0, A[0]);
+    o[1] = token_terms<kKl, true>(a, make_float2(d1, e1), r1, u1, k1, A[1]);
 }
 
 // kPer of a lane's tokens, 32 apart.  Everything is loaded before anything is used, inactive
@@ -226,9 +226,11 @@ __device__ __forceinline__ void policy_tokens(const PolicyArgs& a, const Tokens<
         else token_two<kKl>(a, lp, old, ref, adv, o);
 #pragma unroll
         for (int c = 0; c < kStep; ++c) {
-            const float wi = k.on[i + c] ? w[i + c] : 0.0f;
-            out[i + c] = make_float4(__fmul_rn(wi, o[c].policy), __fmul_rn(wi, o[c].kl), __fmul_rn(wi, o[c].clipped),
-                                     __fmul_rn(wi, o[c].neg_d));
+            // an inactive token's four terms are zeros, and its weight is finite
+            const float wi = w[i + c];
+            float4& x = out[i + c];
+            f2_unpack(f2_mul(f2_splat(wi), f2_pack(o[c].policy, o[c].kl)), x.x, x.y);
+            f2_unpack(f2_mul(f2_splat(wi), f2_pack(o[c].clipped, o[c].neg_d)), x.z, x.w);
             if (a.grad && (i + c) * 32 < k.left)
                 grad[(i + c) * 32] = k.on[i + c] ? __fmul_rn(__fmul_rn(scale, wi), o[c].slope) : 0.0f;
         }
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(1024) k_policy_one(const PolicyArgs a) {
     const float w_all = token_weight(a, n_all);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        w[i] = by_mean ? weights[seq[i]] : w_all;
+        w[i] = by_mean && a.n_seqs > 0 ? weights[seq[i]] : w_all;
         if (a.adv_per_seq) k.adv[i] = adv[seq[i]];
     }
     float4 terms[kPer];
@@ -508,25 +510,37 @@ __global__ void __launch_bounds__(kThreads, kMainCtasPerSm) k_policy_main(const 
         const int4 c1 = reinterpret_cast<const int4*>(a.counts)[lane + 32];
         n_all = __reduce_add_sync(0xffffffffu, c0.x + c0.y + c0.z + c0.w + c1.x + c1.y + c1.z + c1.w);
     }
-    const float w_all = token_weight(a, n_all);
+    // a sequence mean over one sequence without offsets has one weight too
+    const float w_all = by_mean && !a.offsets ? a.weights[0] : token_weight(a, n_all);
     int slot = 0;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         if (u != blockIdx.x) k.load(a, u * kPolicyUnit + at);
         k.cut(bd);
         float w[kPer];
-        int lo = 0, hi = 0;
-        const int64_t tf = k.t0 - lane, tl = tf + kPer * 32 - 1;
-        if (by_seq && tf < a.T) {
-            lo = warp_find_seq(a.offsets, a.n_seqs, static_cast<int>(tf));
-            hi = warp_find_seq(a.offsets, a.n_seqs, static_cast<int>(tl < a.T ? tl : a.T - 1));
-        }
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            w[i] = w_all;
-            if (!k.on[i]) continue;
-            const int s = hi > lo ? find_seq(a.offsets, lo, hi, static_cast<int>(k.t0) + i * 32) : lo;
-            if (by_mean) w[i] = a.weights[s];
-            if (a.adv_per_seq) k.adv[i] = a.advantages[s];
+        for (int i = 0; i < kPer; ++i) w[i] = w_all;
+        const int64_t tf = k.t0 - lane, tl = tf + kPer * 32 - 1;
+        if (by_seq && tf < a.T && a.n_seqs > 0) {
+            const int last = static_cast<int>(tl < a.T ? tl : a.T - 1);
+            const int lo = warp_find_seq(a.offsets, a.n_seqs, static_cast<int>(tf));
+            if (lo + 1 >= a.n_seqs || a.offsets[lo + 1] > last) {
+                // one sequence, as in most warps
+                const float ws = by_mean ? a.weights[lo] : w_all;
+                const float as = a.adv_per_seq ? a.advantages[lo] : 0.0f;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    w[i] = ws;
+                    if (a.adv_per_seq) k.adv[i] = as;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    if (!k.on[i]) continue;
+                    const int s = find_seq(a.offsets, lo, a.n_seqs - 1, static_cast<int>(k.t0) + i * 32);
+                    if (by_mean) w[i] = a.weights[s];
+                    if (a.adv_per_seq) k.adv[i] = a.advantages[s];
+                }
+            }
         }
         float4 terms[kPer];
         policy_tokens<kKl>(a, k, w, terms);
