@@ -21,8 +21,8 @@
 // counting launch is followed by one CTA per unit of 1024 tokens, the last of
 // which adds up the units.  All add the same numbers in the same order: a unit
 // is 8 spans of 128 consecutive tokens; lane l of a span adds RN(w x) of
-// tokens l, l + 32, l + 64, l + 96 pairwise, the lanes a shuffle tree, the
-// spans in order.
+// tokens 4 l .. 4 l + 3 pairwise, the lanes a shuffle tree, the spans in
+// order.
 //
 // What bounds it.  Up to some 10^5 tokens latency: 4.3 us a call on the device
 // at 512 tokens, 5.8 at 8192, of which one launch, one round trip to memory
@@ -47,11 +47,15 @@ constexpr int kCluster = 8;                 // most CTAs of the one-launch path
 // 22.8 us a call; a CTA per unit 21.9; loading the next unit ahead 20.7 us.
 constexpr int kMainCtasPerSm = 4;
 
+struct PolicyCall : PolicyArgs {
+    bool wide;  // four tokens' values can be loaded and stored at a time
+};
+
 struct Bounds {
     int first, last;   // tokens outside [first, last) belong to no sequence
 };
 
-__device__ __forceinline__ Bounds bounds_of(const PolicyArgs& a) {
+__device__ __forceinline__ Bounds bounds_of(const PolicyCall& a) {
     Bounds b;
     b.first = a.offsets ? a.offsets[0] : 0;
     b.last = a.offsets ? a.offsets[a.n_seqs] : a.T;
@@ -87,7 +91,7 @@ struct TokenTerms {
 // From d as two floats, r = e^d, u = ref - lp and (k3) e^u - 1 - u.  The two clips are one test:
 // with a negative advantage both d and the border change sign.
 template <int kKl, bool kPlain>
-__device__ __forceinline__ TokenTerms token_terms(const PolicyArgs& a, float2 d, float r, float u, float k3, float A) {
+__device__ __forceinline__ TokenTerms token_terms(const PolicyCall& a, float2 d, float r, float u, float k3, float A) {
     TokenTerms o;
     const bool up = A > 0.0f;
     const float2 side = up ? d : make_float2(-d.x, -d.y);
@@ -121,7 +125,7 @@ __device__ __forceinline__ float ratio_of(float2 d) {
 
 // One token.
 template <int kKl>
-__device__ __forceinline__ TokenTerms token_one(const PolicyArgs& a, float lp, float old, float ref, float A) {
+__device__ __forceinline__ TokenTerms token_one(const PolicyCall& a, float lp, float old, float ref, float A) {
     const float2 d = two_diff(lp, old);
     const float u = __fsub_rn(ref, lp);
     return token_terms<kKl, false>(a, d, ratio_of(d), u, kKl == RLK_KL_K3 ? exp_minus_1_minus(u) : 0.0f, A);
@@ -131,7 +135,7 @@ __device__ __forceinline__ TokenTerms token_one(const PolicyArgs& a, float lp, f
 // an exponent, and |u| < 1.  The same operations in the same order, so the same bits as
 // token_one; warps with other values in them run that.
 template <int kKl>
-__device__ __forceinline__ void token_two(const PolicyArgs& a, const float (&lp)[2], const float (&old)[2],
+__device__ __forceinline__ void token_two(const PolicyCall& a, const float (&lp)[2], const float (&old)[2],
                                           const float (&ref)[2], const float (&A)[2], TokenTerms (&o)[2]) {
     const uint64_t l2 = f2_pack(lp[0], lp[1]);
     const uint64_t neg_old = f2_pack(-old[0], -old[1]);
@@ -169,7 +173,7 @@ __device__ __forceinline__ void token_two(const PolicyArgs& a, const float (&lp)
     o[1] = token_terms<kKl, true>(a, make_float2(d1, e1), r1, u1, k1, A[1]);
 }
 
-// kPer of a lane's tokens, 32 apart.  Everything is loaded before anything is used, inactive
+// A lane's token, or four consecutive ones.  Everything is loaded before anything is used, inactive
 // tokens too (their values are dropped, never multiplied).
 template <int kKl, int kPer>
 struct Tokens {
@@ -177,27 +181,45 @@ struct Tokens {
     int left;    // tokens from it to the end of the batch
     float lp[kPer], old[kPer], ref[kPer], adv[kPer];
     bool on[kPer];
-    __device__ __forceinline__ void load(const PolicyArgs& a, int64_t first) {
+    __device__ __forceinline__ bool whole(const PolicyCall& a) const { return kPer == 4 && a.wide && left >= 4; }
+    __device__ __forceinline__ void load(const PolicyCall& a, int64_t first) {
         t0 = first;
         left = first < a.T ? static_cast<int>(a.T - first) : 0;
         const float *p_lp = a.logprob + t0, *p_old = a.old_logprob + t0;
         const float *p_ref = a.ref_logprob + t0, *p_adv = a.advantages + t0;
         const uint8_t* p_on = a.active + t0;
+        if constexpr (kPer == 4) {
+            if (whole(a)) {
+                load4(lp, p_lp);
+                load4(old, p_old);
+                if (kKl) load4(ref, p_ref);
+                if (!a.adv_per_seq) load4(adv, p_adv);
+                else adv[0] = adv[1] = adv[2] = adv[3] = 0.0f;
+                const uint32_t m = a.active ? *reinterpret_cast<const uint32_t*>(p_on) : 0x01010101u;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) on[i] = (m & (0xFFu << (8 * i))) != 0;
+                return;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const bool in = i * 32 < left;
-            lp[i] = in ? p_lp[i * 32] : 0.0f;
-            old[i] = in ? p_old[i * 32] : 0.0f;
-            ref[i] = kKl && in ? p_ref[i * 32] : 0.0f;
-            adv[i] = in && !a.adv_per_seq ? p_adv[i * 32] : 0.0f;
-            on[i] = in && (!a.active || p_on[i * 32] != 0);
+            const bool in = i < left;
+            lp[i] = in ? p_lp[i] : 0.0f;
+            old[i] = in ? p_old[i] : 0.0f;
+            ref[i] = kKl && in ? p_ref[i] : 0.0f;
+            adv[i] = in && !a.adv_per_seq ? p_adv[i] : 0.0f;
+            on[i] = in && (!a.active || p_on[i] != 0);
         }
+    }
+    static __device__ __forceinline__ void load4(float (&v)[kPer], const float* p) {
+        const float4 q = *reinterpret_cast<const float4*>(p);
+        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
     }
     // tokens of no sequence take no part
     __device__ __forceinline__ void cut(const Bounds& b) {
-        if (b.first <= t0 && b.last - t0 > (kPer - 1) * 32) return;
+        if (b.first <= t0 && b.last - t0 >= kPer) return;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) on[i] = on[i] && t0 + i * 32 >= b.first && t0 + i * 32 < b.last;
+        for (int i = 0; i < kPer; ++i) on[i] = on[i] && t0 + i >= b.first && t0 + i < b.last;
     }
 };
 
@@ -205,10 +227,10 @@ struct Tokens {
 // worked on, the inactive ones with zeros for their values, so that the tokens' chains of
 // operations overlap; what an inactive one gives is dropped.
 template <int kKl, int kPer>
-__device__ __forceinline__ void policy_tokens(const PolicyArgs& a, const Tokens<kKl, kPer>& k, const float (&w)[kPer],
+__device__ __forceinline__ void policy_tokens(const PolicyCall& a, const Tokens<kKl, kPer>& k, const float (&w)[kPer],
                                               float4 (&out)[kPer]) {
     const float scale = static_cast<float>(a.scale);
-    float* const grad = a.grad + k.t0;
+    float g[kPer];
     constexpr int kStep = kPer == 1 ? 1 : 2;
 #pragma unroll
     for (int i = 0; i < kPer; i += kStep) {
@@ -231,10 +253,20 @@ __device__ __forceinline__ void policy_tokens(const PolicyArgs& a, const Tokens<
             float4& x = out[i + c];
             f2_unpack(f2_mul(f2_splat(wi), f2_pack(o[c].policy, o[c].kl)), x.x, x.y);
             f2_unpack(f2_mul(f2_splat(wi), f2_pack(o[c].clipped, o[c].neg_d)), x.z, x.w);
-            if (a.grad && (i + c) * 32 < k.left)
-                grad[(i + c) * 32] = k.on[i + c] ? __fmul_rn(__fmul_rn(scale, wi), o[c].slope) : 0.0f;
+            g[i + c] = k.on[i + c] ? __fmul_rn(__fmul_rn(scale, wi), o[c].slope) : 0.0f;
         }
     }
+    if (!a.grad) return;
+    float* const grad = a.grad + k.t0;
+    if constexpr (kPer == 4) {
+        if (k.whole(a)) {
+            *reinterpret_cast<float4*>(grad) = make_float4(g[0], g[1], g[2], g[3]);
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        if (i < k.left) grad[i] = g[i];
 }
 
 struct Stats {  // (policy, kl) and (clipped, -d)
@@ -264,19 +296,19 @@ __device__ __forceinline__ float unit_sum(const float4* spans, int k) {
 }
 
 // Weight of the tokens of a sequence with n active ones.
-__device__ __forceinline__ float seq_weight(const PolicyArgs& a, int n) {
+__device__ __forceinline__ float seq_weight(const PolicyCall& a, int n) {
     return __fdiv_rn(1.0f, __fmul_rn(static_cast<float>(a.n_seqs), static_cast<float>(n > 1 ? n : 1)));
 }
-__device__ __forceinline__ float token_weight(const PolicyArgs& a, int n) {
+__device__ __forceinline__ float token_weight(const PolicyCall& a, int n) {
     return a.reduction == RLK_REDUCE_TOKEN_MEAN ? __fdiv_rn(1.0f, static_cast<float>(n > 1 ? n : 1)) : 1.0f;
 }
 
 // The units' sums are added like this: slot j takes units j, j + 256, ... in ascending order, the
 // 32 slots of a warp are added by a shuffle tree, the 8 warps' sums in order, all as pairs.
-__device__ __forceinline__ void write_stat(const PolicyArgs& a, int k, float2 v, bool bad) {
+__device__ __forceinline__ void write_stat(const PolicyCall& a, int k, float2 v, bool bad) {
     a.out_stats[k] = bad ? CUDART_NAN_F : __fadd_rn(v.x, v.y);
 }
-__device__ __forceinline__ void write_loss(const PolicyArgs& a, float2 policy, float2 kl, bool bad) {
+__device__ __forceinline__ void write_loss(const PolicyCall& a, float2 policy, float2 kl, bool bad) {
     double sum = pair_value(policy);
     if (a.kl_coef64 != 0.0) sum = __fma_rn(a.kl_coef64, pair_value(kl), sum);
     *a.out_loss = bad ? CUDART_NAN_F : static_cast<float>(__dmul_rn(a.scale, sum));
@@ -299,7 +331,7 @@ __device__ __forceinline__ int seq_in(const int32_t* offsets, int n, int t) {
 // One cluster of kCtas CTAs of 1024 threads, kPer tokens a thread, which it holds from the first
 // load to the gradient; the counts that the weights need come from the masks it holds.
 template <int kKl, int kCtas, int kPer>
-__global__ void __launch_bounds__(1024) k_policy_one(const PolicyArgs a) {
+__global__ void __launch_bounds__(1024) k_policy_one(const PolicyCall a) {
     constexpr int kAll = 1024, kUnits = kPer;  // units of a CTA
     static_assert(kCtas * kUnits <= 32, "a lane per unit");
     static_assert(kPer == 1 || kPer == 4, "a warp is a quarter of a span, or one");
@@ -309,12 +341,12 @@ __global__ void __launch_bounds__(1024) k_policy_one(const PolicyArgs a) {
     __shared__ float weights[kLaunchSeqs];
     __shared__ float4 parts[32];           // the first CTA's are used
     __shared__ float4 spans[kUnits * kUnitWarps];
-    __shared__ float4 tokens[kPer == 1 ? kAll : 1];
+    __shared__ float4 tokens[kPer == 1 ? kUnitWarps : 1][4][34];  // [span][token mod 4][lane]
     __shared__ int active_here;
     const int rank = kCtas > 1 ? static_cast<int>(blockIdx.x) : 0;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     Tokens<kKl, kPer> k;
-    k.load(a, (rank * (kAll / 32) + warp) * (32 * kPer) + lane);
+    k.load(a, static_cast<int64_t>(rank * kAll + threadIdx.x) * kPer);
     const bool masked = a.active != nullptr, by_mean = a.reduction == RLK_REDUCE_SEQ_MEAN;
     const bool by_seq = a.offsets && (a.adv_per_seq || by_mean);
     Bounds bd = {0, a.T};
@@ -337,13 +369,13 @@ __global__ void __launch_bounds__(1024) k_policy_one(const PolicyArgs a) {
     int seq[kPer] = {};
     if (by_seq) {
         // a warp's tokens: mostly of one sequence
-        const int64_t tf = k.t0 - lane, tl = tf + kPer * 32 - 1;
+        const int64_t tf = k.t0 - lane * kPer, tl = tf + kPer * 32 - 1;
         const int lo = tf < a.T ? seq_in(offsets, a.n_seqs, static_cast<int>(tf)) : 0;
         const int hi = tf < a.T ? seq_in(offsets, a.n_seqs, static_cast<int>(tl < a.T ? tl : a.T - 1)) : 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             seq[i] = lo;
-            if (hi > lo && k.on[i]) seq[i] = lo + seq_in(offsets + lo, hi - lo + 1, static_cast<int>(k.t0) + i * 32);
+            if (hi > lo && k.on[i]) seq[i] = lo + seq_in(offsets + lo, hi - lo + 1, static_cast<int>(k.t0) + i);
         }
     }
     int n_all = bd.last - bd.first;
@@ -399,11 +431,11 @@ __global__ void __launch_bounds__(1024) k_policy_one(const PolicyArgs a) {
         const float4 s = span_sum(terms[0], terms[1], terms[2], terms[3]);
         if (lane == 0) spans[warp] = s;
     } else {
-        tokens[threadIdx.x] = terms[0];
+        tokens[threadIdx.x >> 7][threadIdx.x & 3][(threadIdx.x & 127) >> 2] = terms[0];
         __syncthreads();
         if (warp < kUnitWarps) {
-            const float4* const p = tokens + warp * 128 + lane;
-            const float4 s = span_sum(p[0], p[32], p[64], p[96]);
+            const float4(*const p)[34] = tokens[warp];
+            const float4 s = span_sum(p[0][lane], p[1][lane], p[2][lane], p[3][lane]);
             if (lane == 0) spans[warp] = s;
         }
     }
@@ -437,7 +469,7 @@ __global__ void __launch_bounds__(1024) k_policy_one(const PolicyArgs a) {
 // Each sequence's weight (seq_mean), or the active tokens in each block's share of the sequences
 // (token_mean); and the main kernel's ticket set to 0.  Long sequences are counted by a cluster
 // each: one of 1.77 M tokens by a single CTA took 25 us.
-__global__ void __launch_bounds__(1024) k_policy_count(const PolicyArgs a) {
+__global__ void __launch_bounds__(1024) k_policy_count(const PolicyCall a) {
     __shared__ int smem[32];
     __shared__ int counted;
     cg::cluster_group cluster = cg::this_cluster();
@@ -489,14 +521,14 @@ __global__ void __launch_bounds__(1024) k_policy_count(const PolicyArgs a) {
 }
 
 template <int kKl>
-__global__ void __launch_bounds__(kThreads, kMainCtasPerSm) k_policy_main(const PolicyArgs a) {
+__global__ void __launch_bounds__(kThreads, kMainCtasPerSm) k_policy_main(const PolicyCall a) {
     constexpr int kPer = kPolicyUnit / kThreads;
     __shared__ float4 spans[2][kUnitWarps];
     __shared__ float2 finish[kThreads / 32][4];
     __shared__ bool last_here;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t units = (static_cast<int64_t>(a.T) + kPolicyUnit - 1) / kPolicyUnit;
-    const int at = warp * 32 * kPer + lane;
+    const int at = threadIdx.x * kPer;
     Tokens<kKl, kPer> k;
     k.load(a, blockIdx.x * static_cast<int64_t>(kPolicyUnit) + at);
     const Bounds bd = bounds_of(a);
@@ -519,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, kMainCtasPerSm) k_policy_main(const 
         float w[kPer];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) w[i] = w_all;
-        const int64_t tf = k.t0 - lane, tl = tf + kPer * 32 - 1;
+        const int64_t tf = k.t0 - lane * kPer, tl = tf + kPer * 32 - 1;
         if (by_seq && tf < a.T && a.n_seqs > 0) {
             const int last = static_cast<int>(tl < a.T ? tl : a.T - 1);
             const int lo = warp_find_seq(a.offsets, a.n_seqs, static_cast<int>(tf));
@@ -536,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, kMainCtasPerSm) k_policy_main(const 
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) {
                     if (!k.on[i]) continue;
-                    const int s = find_seq(a.offsets, lo, a.n_seqs - 1, static_cast<int>(k.t0) + i * 32);
+                    const int s = find_seq(a.offsets, lo, a.n_seqs - 1, static_cast<int>(k.t0) + i);
                     if (by_mean) w[i] = a.weights[s];
                     if (a.adv_per_seq) k.adv[i] = a.advantages[s];
                 }
@@ -590,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, kMainCtasPerSm) k_policy_main(const 
 }
 
 template <int kKl, int kCtas, int kPer>
-cudaError_t launch_one(const PolicyArgs& a, cudaStream_t stream) {
+cudaError_t launch_one(const PolicyCall& a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.stream = stream;
@@ -612,7 +644,7 @@ bool policy_one_launch(int64_t T, int64_t n_seqs) {
 }
 
 template <int kKl>
-cudaError_t launch_kl(const PolicyArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_kl(const PolicyCall& a, int num_sms, cudaStream_t stream) {
     if (policy_one_launch(a.T, a.n_seqs))
         return a.T <= 1024              ? launch_one<kKl, 1, 1>(a, stream)
                : a.T <= kCluster * 1024 ? launch_one<kKl, kCluster, 1>(a, stream)
@@ -649,7 +681,12 @@ cudaError_t launch_kl(const PolicyArgs& a, int num_sms, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, k_policy_main<kKl>, a);
 }
 
-cudaError_t launch_policy_loss(const PolicyArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_policy_loss(const PolicyArgs& args, int num_sms, cudaStream_t stream) {
+    PolicyCall a;
+    static_cast<PolicyArgs&>(a) = args;
+    auto places = [](const void* p) { return static_cast<unsigned>(reinterpret_cast<uintptr_t>(p) & 15); };
+    a.wide = ((places(a.logprob) | places(a.old_logprob) | places(a.ref_logprob) | places(a.grad) |
+               (a.adv_per_seq ? 0u : places(a.advantages)) | (places(a.active) & 3)) == 0);
     if (!a.ref_logprob) return launch_kl<0>(a, num_sms, stream);
     return a.kl_kind == RLK_KL_K1   ? launch_kl<RLK_KL_K1>(a, num_sms, stream)
            : a.kl_kind == RLK_KL_K2 ? launch_kl<RLK_KL_K2>(a, num_sms, stream)
