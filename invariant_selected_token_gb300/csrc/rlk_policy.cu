@@ -27,9 +27,11 @@
 // What bounds it.  Up to some 10^5 tokens latency: 4.3 us a call on the device
 // at 512 tokens, 5.8 at 8192, of which one launch, one round trip to memory
 // and the first fetch of the code make most.  At 1.77 M tokens (37 MB, 5.6 us
-// of HBM) 19.6 us: 6 us of the counting launch, then about 150 instructions a
-// token, two tokens per instruction where the values allow.  Sums in fp64
-// instead of pairs of floats made it 27, the branching form of a token 23 us.
+// of HBM) 16.1 us: 2 us of the counting launch that nothing hides, 3 of the last
+// CTA's tail, and instructions, two tokens in one where the values allow.  Sums in fp64
+// instead of pairs of floats made it 27, the branching form of a token 23, a
+// look-up of both ends of a warp's span and of every token 19.7, tokens loaded one
+// by one 18.8 us.
 #include <cooperative_groups.h>
 
 #include "rlk_ptx.cuh"
@@ -43,8 +45,8 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 256;               // threads that a unit's sums are added by
 constexpr int kUnitWarps = kThreads / 32;
 constexpr int kCluster = 8;                 // most CTAs of the one-launch path
-// CTAs of the main kernel per SM, all resident.  At 1.77 M tokens: 3 24.1, 4 19.7, 5 (spilling)
-// 22.8 us a call; a CTA per unit 21.9; loading the next unit ahead 20.7 us.
+// CTAs of the main kernel per SM, all resident.  At 1.77 M tokens: 3 17.2, 4 16.1, 5 (spilling)
+// 17.2 us a call.  Loading the next unit ahead, into registers or shared memory, costs 1 us.
 constexpr int kMainCtasPerSm = 4;
 
 struct PolicyCall : PolicyArgs {
@@ -304,7 +306,7 @@ __device__ __forceinline__ float token_weight(const PolicyCall& a, int n) {
 }
 
 // The units' sums are added like this: slot j takes units j, j + 256, ... in ascending order, the
-// 32 slots of a warp are added by a shuffle tree, the 8 warps' sums in order, all as pairs.
+// 32 slots of a warp are added by a shuffle tree, the 8 warps' sums by another, all as pairs.
 __device__ __forceinline__ void write_stat(const PolicyCall& a, int k, float2 v, bool bad) {
     a.out_stats[k] = bad ? CUDART_NAN_F : __fadd_rn(v.x, v.y);
 }
@@ -529,6 +531,15 @@ __global__ void __launch_bounds__(kThreads, kMainCtasPerSm) k_policy_main(const 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t units = (static_cast<int64_t>(a.T) + kPolicyUnit - 1) / kPolicyUnit;
     const int at = threadIdx.x * kPer;
+    // offsets that descend or leave [0, T]: a share of them per CTA
+    bool bad = false;
+    if (a.offsets) {
+        for (int64_t s = blockIdx.x + static_cast<int64_t>(threadIdx.x) * gridDim.x; s <= a.n_seqs;
+             s += static_cast<int64_t>(kThreads) * gridDim.x) {
+            const int b = a.offsets[s], e = s < a.n_seqs ? a.offsets[s + 1] : a.T;
+            bad |= b < 0 || e < b || e > a.T;
+        }
+    }
     Tokens<kKl, kPer> k;
     k.load(a, blockIdx.x * static_cast<int64_t>(kPolicyUnit) + at);
     const Bounds bd = bounds_of(a);
@@ -578,47 +589,56 @@ __global__ void __launch_bounds__(kThreads, kMainCtasPerSm) k_policy_main(const 
         policy_tokens<kKl>(a, k, w, terms);
         const float4 s = span_sum(terms[0], terms[1], terms[2], terms[3]);
         if (lane == 0) spans[slot][warp] = s;
-        __syncthreads();
-        if (threadIdx.x < 4) reinterpret_cast<float*>(a.parts + u)[threadIdx.x] = unit_sum(spans[slot], threadIdx.x);
+        bad = __syncthreads_or(bad);
+        if (threadIdx.x < 4)
+            reinterpret_cast<float*>(a.parts + u)[threadIdx.x] = bad ? CUDART_NAN_F : unit_sum(spans[slot], threadIdx.x);
         slot ^= 1;
     }
-    // the last CTA to come here adds up the units
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) last_here = atomicAdd(a.ticket, 1) == static_cast<int>(gridDim.x) - 1;
-    __syncthreads();
-    if (!last_here) return;
-    __threadfence();
-    bool bad = false;
-    if (a.offsets) {
-        for (int64_t s = threadIdx.x; s <= a.n_seqs; s += kThreads) {
-            const int b = a.offsets[s], e = s < a.n_seqs ? a.offsets[s + 1] : a.T;
-            bad |= b < 0 || e < b || e > a.T;
-        }
+    // the last CTA to come here adds up the units; its tail is nobody's company, so it is kept short
+    // (4.9 us at 1.77 M tokens with a fence by every thread, the offsets checked here, four loads at
+    // a time and the stats one after the other)
+    if (warp == 0) {
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) last_here = atomicAdd(a.ticket, 1) == static_cast<int>(gridDim.x) - 1;
     }
     bad = __syncthreads_or(bad);
+    if (bad && threadIdx.x == 0) report_status(a.status, RLK_ERR_INVALID_ARG);
+    if (!last_here) return;
+    __threadfence();
     float2 v[4] = {};
-#pragma unroll 4
-    for (int64_t u = threadIdx.x; u < units; u += kThreads) {
-        const float4 p = a.parts[u];
-        v[0] = pair_add(v[0], pair_of(p.x));
-        v[1] = pair_add(v[1], pair_of(p.y));
-        v[2] = pair_add(v[2], pair_of(p.z));
-        v[3] = pair_add(v[3], pair_of(p.w));
-    }
+    for (int64_t u0 = threadIdx.x; u0 < units; u0 += 8 * kThreads) {
+        float4 p[8];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        v[c] = warp_sum(v[c]);
-        if (lane == 0) finish[warp][c] = v[c];
+        for (int i = 0; i < 8; ++i)
+            p[i] = u0 + i * kThreads < units ? __ldcg(a.parts + u0 + i * kThreads) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            two_add(v[0], p[i].x);
+            two_add(v[1], p[i].y);
+            two_add(v[2], p[i].z);
+            two_add(v[3], p[i].w);
+        }
     }
+#pragma unroll 1
+    for (int o = 16; o >= 1; o >>= 1) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            v[c] = pair_add(v[c], make_float2(__shfl_xor_sync(0xffffffffu, v[c].x, o),
+                                              __shfl_xor_sync(0xffffffffu, v[c].y, o)));
+    }
+    if (lane < 4) finish[warp][lane] = lane == 0 ? v[0] : lane == 1 ? v[1] : lane == 2 ? v[2] : v[3];
     __syncthreads();
-    if (threadIdx.x < 4) {
-        float2 s = finish[0][threadIdx.x];
-        for (int i = 1; i < kThreads / 32; ++i) s = pair_add(s, finish[i][threadIdx.x]);
-        write_stat(a, threadIdx.x, s, bad);
-        const float2 kl = make_float2(__shfl_sync(0xfu, s.x, 1), __shfl_sync(0xfu, s.y, 1));
-        if (threadIdx.x == 0) write_loss(a, s, kl, bad);
-    }
+    if (warp != 0) return;
+    // lane 8 c + w: stat c of warp w
+    static_assert(kUnitWarps == 8, "eight lanes a stat");
+    float2 s = finish[lane & 7][lane >> 3];
+#pragma unroll 1
+    for (int o = 4; o >= 1; o >>= 1)
+        s = pair_add(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o)));
+    const float2 kl = make_float2(__shfl_sync(0xffffffffu, s.x, 8), __shfl_sync(0xffffffffu, s.y, 8));
+    if ((lane & 7) == 0) write_stat(a, lane >> 3, s, bad);
+    if (lane == 0) write_loss(a, s, kl, bad);
 }
 
 template <int kKl, int kCtas, int kPer>
