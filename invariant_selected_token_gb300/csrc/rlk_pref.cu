@@ -138,7 +138,17 @@ __device__ __forceinline__ bool offsets_bad(const PreferenceArgs& a) {
 // The loss from the pairs' losses, by a whole CTA.
 __device__ __forceinline__ void preference_finish(const PreferenceArgs& a, const float* losses, bool bad, float2* tmp) {
     bad = __syncthreads_or(bad);
+    auto finish = [&](float2 v) {
+        if (threadIdx.x != 0) return;
+        *a.out_loss = bad ? CUDART_NAN_F : static_cast<float>(__dmul_rn(a.scale_per_pair, pair_value(v)));
+        if (bad) report_status(a.status, RLK_ERR_INVALID_ARG);
+    };
     // warp w of 16 takes losses 32 w + lane, + 512, ...; those without any would add zeros
+    if (a.n_pairs <= 32) {
+        const int i = threadIdx.x;
+        if (i < 32) finish(warp_sum(pair_of(i < a.n_pairs ? losses[i] : 0.0f)));
+        return;
+    }
     for (int w = threadIdx.x >> 5; w < kWarps && w * 32 < a.n_pairs; w += blockDim.x >> 5) {
         float2 v = pair_of(0.0f);
         for (int i = w * 32 + (threadIdx.x & 31); i < a.n_pairs; i += kThreads) v = pair_add(v, pair_of(losses[i]));
@@ -148,10 +158,7 @@ __device__ __forceinline__ void preference_finish(const PreferenceArgs& a, const
     __syncthreads();
     if (threadIdx.x < 32) {
         const int w = threadIdx.x;
-        const float2 v = warp_sum(w < kWarps && w * 32 < a.n_pairs ? tmp[w] : pair_of(0.0f));
-        if (w != 0) return;
-        *a.out_loss = bad ? CUDART_NAN_F : static_cast<float>(__dmul_rn(a.scale_per_pair, pair_value(v)));
-        if (bad) report_status(a.status, RLK_ERR_INVALID_ARG);
+        finish(warp_sum(w < kWarps && w * 32 < a.n_pairs ? tmp[w] : pair_of(0.0f)));
     }
 }
 
@@ -216,12 +223,19 @@ __device__ __forceinline__ void reduce_pair(const PreferenceArgs& a, int pair, c
                 if (i < held[side]) v[side][k] = slot(side, i, n[side][k]);
             }
         }
+        float2 sum[2] = {pair_add(v[0][0], v[0][1]), pair_add(v[1][0], v[1][1])};
+#pragma unroll 1
+        for (int o = 16; o >= 1; o >>= 1) {
+#pragma unroll
+            for (int side = 0; side < 2; ++side)
+                sum[side] = pair_add(sum[side], make_float2(__shfl_xor_sync(0xffffffffu, sum[side].x, o),
+                                                            __shfl_xor_sync(0xffffffffu, sum[side].y, o)));
+        }
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
-            const float2 sum = warp_sum(pair_add(v[side][0], v[side][1]));
             const int count = __reduce_add_sync(0xffffffffu, n[side][0] + n[side][1]);
             if (lane == 0) {
-                sc.tmp[side][w] = sum;
+                sc.tmp[side][w] = sum[side];
                 sc.n[side][w] = count;
             }
         }
@@ -277,18 +291,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_preference(const PreferenceArgs
             sp[0] = span_of(a, chosen_of(a, pair));
             sp[1] = span_of(a, rejected_of(a, pair));
         }
-#pragma unroll 1
-        for (int side = 0; side < 2; ++side) {
-            const Span& s = sp[side];
-            for (int64_t g = member * warps + warp; s.b + g * kChunk < s.e; g += team * warps) {
-                int n;
-                const float2 v = chunk_sum(a, s, g, &n);
-                if (lane == 0) {
-                    // a slot is only ever this warp's
-                    const int at = side * kSlots + static_cast<int>(g % kSlots);
-                    lead_slots[at] = g < kSlots ? v : pair_add(lead_slots[at], v);
-                    lead_counts[at] = (g < kSlots ? 0 : lead_counts[at]) + n;
-                }
+        // the two sequences' chunks one after the other
+        const int64_t c0 = chunks_of(sp[0]), c01 = c0 + chunks_of(sp[1]);
+        for (int64_t j = member * warps + warp; j < c01; j += team * warps) {
+            const int side = j >= c0;
+            const int64_t g = side ? j - c0 : j;
+            int n;
+            const float2 v = chunk_sum(a, side ? sp[1] : sp[0], g, &n);
+            if (lane == 0) {
+                // a slot is only ever this warp's: the warps of a team are a power of two
+                const int at = side * kSlots + static_cast<int>(g % kSlots);
+                lead_slots[at] = g < kSlots ? v : pair_add(lead_slots[at], v);
+                lead_counts[at] = (g < kSlots ? 0 : lead_counts[at]) + n;
             }
         }
         if (team > 1) cluster.sync(); else __syncthreads();
@@ -422,42 +436,48 @@ __global__ void __launch_bounds__(kThreads) k_preference_spread(const Preference
                     write, scratch, slope, nullptr);
         __syncthreads();
     };
-    // a pair's own outputs are written by CTA pair mod grid, which keeps its slopes in case its
-    // tokens belong to the same pair
+    // a pair's own outputs are written by the CTA that has its chosen sequence's first chunk, or,
+    // where that sequence is empty, by CTA pair mod grid
     int have = -1;
     for (int pair = blockIdx.x; pair < a.n_pairs; pair += gridDim.x) {
+        if (chunks_of(map.span[chosen_of(a, pair)]) > 0) continue;
         slopes_of(pair, true);
         have = pair;
     }
-    if (a.grad) {
-        const int64_t total = map.first[kSplitSeqs];
-        const int64_t i0 = total * blockIdx.x / gridDim.x, i1 = total * (blockIdx.x + 1) / gridDim.x;
-        for (int64_t i = i0; i < i1;) {
-            const int q = map.seq_of(i);
-            const int64_t next = map.first[q + 1] < i1 ? map.first[q + 1] : i1;
-            const int pair = a.halves ? q % a.n_pairs : q / 2;
-            const int side = a.halves ? q / a.n_pairs : q % 2;
-            if (pair != have) slopes_of(pair, false);
+    const int64_t total = map.first[kSplitSeqs];
+    const int64_t i0 = total * blockIdx.x / gridDim.x, i1 = total * (blockIdx.x + 1) / gridDim.x;
+    for (int64_t i = i0; i < i1;) {
+        const int q = map.seq_of(i);
+        const int64_t next = map.first[q + 1] < i1 ? map.first[q + 1] : i1;
+        const int pair = a.halves ? q % a.n_pairs : q / 2;
+        const int side = a.halves ? q / a.n_pairs : q % 2;
+        const bool write = side == 0 && i == map.first[q];
+        if (write || (a.grad && pair != have)) {
+            slopes_of(pair, write);
             have = pair;
-            const float g = slope[side];
-            const int64_t b = map.span[q].b + (i - map.first[q]) * kChunk;
-            int64_t e = map.span[q].b + (next - map.first[q]) * kChunk;
-            if (e > map.span[q].e) e = map.span[q].e;
-#pragma unroll 4
-            for (int64_t t = b + threadIdx.x; t < e; t += kThreads)
-                a.grad[t] = (a.active && a.active[t] == 0) ? 0.0f : g;
-            i = next;
         }
+        const int64_t b = map.span[q].b + (i - map.first[q]) * kChunk;
+        int64_t e = map.span[q].b + (next - map.first[q]) * kChunk;
+        if (e > map.span[q].e) e = map.span[q].e;
+        i = next;
+        if (!a.grad) continue;
+        const float g = slope[side];
+#pragma unroll 4
+        for (int64_t t = b + threadIdx.x; t < e; t += kThreads)
+            a.grad[t] = (a.active && a.active[t] == 0) ? 0.0f : g;
+    }
+    if (a.grad) {
         // tokens before the first and behind the last sequence
         const int64_t who = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
         const int64_t all = static_cast<int64_t>(gridDim.x) * kThreads;
         for (int64_t t = who, e = map.span[0].b; t < e; t += all) a.grad[t] = 0.0f;
         for (int64_t t = map.span[2 * a.n_pairs - 1].e + who; t < a.T; t += all) a.grad[t] = 0.0f;
     }
-    // the last CTA to come here adds up the pairs
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) last_here = atomicAdd(a.ticket, 1) == static_cast<int>(gridDim.x) - 1;
+    // the last CTA to come here adds up the pairs, whose losses the CTAs' first threads have written
+    if (threadIdx.x == 0) {
+        __threadfence();
+        last_here = atomicAdd(a.ticket, 1) == static_cast<int>(gridDim.x) - 1;
+    }
     __syncthreads();
     if (!last_here) return;
     __threadfence();
