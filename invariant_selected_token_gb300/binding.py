@@ -540,6 +540,14 @@ def _opt_addr(t: Optional[torch.Tensor], dtype, name: str, index: int, shape):
     return None if t is None else _addr(t, dtype, name, index, shape)
 
 
+def _output(t: Optional[torch.Tensor], dtype, name: str, device, shape):
+    """(tensor, address) of the caller's output or of a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    return t, _addr(t, dtype, name, device.index, shape)
+
+
 def _status_addr(status: Optional[torch.Tensor], index: int):
     if status is None:
         return None
@@ -618,15 +626,11 @@ def rmsnorm_backward(grad_out: torch.Tensor, x: torch.Tensor, gamma: torch.Tenso
     a_go = _addr(grad_out, grad_out.dtype, "grad_out", idx, shape)
     a_gamma = _addr(gamma, torch.bfloat16, "gamma", idx, (H,))
     a_res = _opt_addr(grad_residual, grad_dtype, "grad_residual", idx, shape)
-    if grad_x is None:
-        grad_x = torch.empty(shape, dtype=grad_dtype, device=dev)
-    a_gx = _addr(grad_x, grad_dtype, "grad_x", idx, shape)
+    grad_x, a_gx = _output(grad_x, grad_dtype, "grad_x", dev, shape)
     a_gg = p_ws = None
     ws_n = 0
     if want_gamma:
-        if grad_gamma is None:
-            grad_gamma = torch.empty(H, dtype=torch.float32, device=dev)
-        a_gg = _addr(grad_gamma, torch.float32, "grad_gamma", idx, (H,))
+        grad_gamma, a_gg = _output(grad_gamma, torch.float32, "grad_gamma", dev, (H,))
         p_ws, ws_n, ws = _workspace(workspace, rmsnorm_backward_workspace_size(T, H), dev)
     _check(lib().rlk_rmsnorm_backward(a_go, go_code, x.data_ptr(), a_gamma, eps, a_res, T, H, a_gx,
                                       gx_code, a_gg, p_ws, ws_n, _raw_stream(idx)),
@@ -676,9 +680,7 @@ def policy_loss(logprob: torch.Tensor, old_logprob: torch.Tensor, advantages: to
     kl_code, red = _choice(KL_KINDS, kl, "kl"), _choice(REDUCTIONS, reduction, "reduction")
     a_grad = None
     if want_grad:
-        if grad_logprob is None:
-            grad_logprob = torch.empty(T, dtype=f32, device=dev)
-        a_grad = _addr(grad_logprob, f32, "grad_logprob", idx, shape)
+        grad_logprob, a_grad = _output(grad_logprob, f32, "grad_logprob", dev, shape)
     loss = torch.empty((), dtype=f32, device=dev)
     stats = torch.empty(4, dtype=f32, device=dev)
     p_ws, ws_n, ws = _workspace(workspace, policy_loss_workspace_size(T, n_seqs), dev)
@@ -730,9 +732,7 @@ def preference_loss(logprob: torch.Tensor, seq_offsets: torch.Tensor,
     layout_code = _choice(PAIR_LAYOUTS, layout, "layout")
     a_grad = None
     if want_grad:
-        if grad_logprob is None:
-            grad_logprob = torch.empty(T, dtype=f32, device=dev)
-        a_grad = _addr(grad_logprob, f32, "grad_logprob", idx, shape)
+        grad_logprob, a_grad = _output(grad_logprob, f32, "grad_logprob", dev, shape)
     loss = torch.empty((), dtype=f32, device=dev)
     pair_loss = torch.empty(P, dtype=f32, device=dev)
     rewards = torch.empty(n_seqs, dtype=f32, device=dev)
@@ -746,10 +746,10 @@ def preference_loss(logprob: torch.Tensor, seq_offsets: torch.Tensor,
 
 
 def _grad_list(grads, name: str):
-    """(device, sizes, types and pointers as lists) of a list of contiguous gradients on one
-    device; lists of hundreds of tensors go through the C loops of map()."""
+    """(device, sizes, types, pointers) of a list of contiguous gradients on one device, the last
+    three as arrays; lists of hundreds of tensors go through the C loops of map()."""
     if not grads:
-        return None, [], [], []
+        return None, array.array("q"), array.array("i"), array.array("Q")
     if not set(map(type, grads)) <= _TENSOR_TYPES and not all(isinstance(g, torch.Tensor) for g in grads):
         raise TypeError("%s must be torch tensors" % name)
     dev = grads[0].device
@@ -760,16 +760,13 @@ def _grad_list(grads, name: str):
             if g.dtype not in GRAD_DTYPES:
                 raise TypeError("%s must be float32, bfloat16 or float16 tensors" % name)
             _require(g, g.dtype, name, dev)
-    return (dev, list(map(torch.Tensor.numel, grads)), dtypes,
-            array.array("Q", map(torch.Tensor.data_ptr, grads)))
+    return (dev, array.array("q", list(map(torch.Tensor.numel, grads))),
+            array.array("i", list(map(GRAD_DTYPES.__getitem__, dtypes))),
+            array.array("Q", list(map(torch.Tensor.data_ptr, grads))))
 
 
 def _host_addr(a):
     return a.buffer_info()[0] if len(a) else None
-
-
-def _host_arrays(sizes, dtypes):
-    return array.array("q", sizes), array.array("i", map(GRAD_DTYPES.__getitem__, dtypes))
 
 
 def grad_norm(grads: Sequence[torch.Tensor], workspace: Optional[torch.Tensor] = None,
@@ -777,7 +774,7 @@ def grad_norm(grads: Sequence[torch.Tensor], workspace: Optional[torch.Tensor] =
     """sqrt of the sum of squares over all the tensors (fp32, bf16 or fp16, contiguous) as a
     0-dim fp32 tensor.  `device` says where an empty list's norm goes."""
     grads = list(grads)
-    dev, sizes, dtypes, ptrs = _grad_list(grads, "grads")
+    dev, sizes, types, ptrs = _grad_list(grads, "grads")
     if dev is None:
         dev = _cuda_device(device)
     if _elsewhere(dev, stream):
@@ -785,7 +782,6 @@ def grad_norm(grads: Sequence[torch.Tensor], workspace: Optional[torch.Tensor] =
             return grad_norm(grads, workspace, status, dev)
     a_status = _status_addr(status, dev.index)
     n = len(sizes)
-    sizes, types = _host_arrays(sizes, dtypes)
     h_ptrs, h_sizes, h_types = (_host_addr(a) for a in (ptrs, sizes, types))
     L = lib()
     norm = torch.empty((), dtype=torch.float32, device=dev)
@@ -803,7 +799,7 @@ def clip_grads(grads: Sequence[torch.Tensor], max_norm: float,
     (same sizes and types) -> (norm [], scale []).  With a norm that is not finite the values
     stay as they are, scale is 1 and the status word gets RLK_ERR_NONFINITE."""
     grads = list(grads)
-    dev, sizes, dtypes, ptrs = _grad_list(grads, "grads")
+    dev, sizes, types, ptrs = _grad_list(grads, "grads")
     if dev is None:
         dev = _cuda_device(device)
     if _elsewhere(dev, stream):
@@ -811,14 +807,13 @@ def clip_grads(grads: Sequence[torch.Tensor], max_norm: float,
             return clip_grads(grads, max_norm, out, workspace, status, dev)
     outs = ptrs
     if out is not None:
-        out_dev, out_sizes, out_dtypes, outs = _grad_list(list(out), "out")
-        if out_sizes != sizes or out_dtypes != dtypes:
+        out_dev, out_sizes, out_types, outs = _grad_list(list(out), "out")
+        if out_sizes != sizes or out_types != types:
             raise ValueError("out must hold one tensor of the same size and type per gradient")
         if out_dev is not None and out_dev != dev:
             raise ValueError("out is on %s, expected %s" % (out_dev, dev))
     a_status = _status_addr(status, dev.index)
     n = len(sizes)
-    sizes, types = _host_arrays(sizes, dtypes)
     h_ptrs, h_outs, h_sizes, h_types = (_host_addr(a) for a in (ptrs, outs, sizes, types))
     L = lib()
     norm = torch.empty((), dtype=torch.float32, device=dev)

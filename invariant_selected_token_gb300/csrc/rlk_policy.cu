@@ -678,8 +678,6 @@ cudaError_t launch_kl(const PolicyCall& a, int num_sms, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     const int size = lengthy ? kCluster : 1;
     cfg.gridDim = dim3(static_cast<unsigned>((rows > 0 ? rows : 1) * size), 1, 1);
     cfg.blockDim = dim3(lengthy ? 1024 : kThreads, 1, 1);
@@ -687,6 +685,8 @@ cudaError_t launch_kl(const PolicyCall& a, int num_sms, cudaStream_t stream) {
     attr[0].val.clusterDim.x = size;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = size > 1 ? 1 : 0;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, k_policy_count, a);
     if (e != cudaSuccess) return e;
     const int64_t units = (static_cast<int64_t>(a.T) + kPolicyUnit - 1) / kPolicyUnit;

@@ -23,6 +23,7 @@
 // the tail and the second launch); 64 rows: 5.1 us, latency.  On the way the
 // first two took 162 and 66 us with one row at a time, 111 and 37 with the
 // next row in registers, 88 and 38 with 16 features a thread and the ring.
+#include <atomic>
 #include <cooperative_groups.h>
 #include <cstdint>
 
@@ -319,10 +320,18 @@ cudaError_t launch_types(const RmsBwdArgs& a, int blocks, cudaStream_t stream) {
     constexpr int kThreads = kCtaThreads<kWarps, kGo, kGx>;
     constexpr size_t kSmem =
         size_t(kStages<kWarps, kGo, kGx>) * 2 * (1 + kPieces<kGo> + kPieces<kGx>) * kThreads * sizeof(uint4);
-    // per device and kernel: the runtime keeps it
-    const cudaError_t e = cudaFuncSetAttribute(k_rmsnorm_backward<kWarps, kGo, kGx>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+    // once per device and kernel: the runtime keeps it, and asking each time costs the host 1 us
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (!(ready.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(k_rmsnorm_backward<kWarps, kGo, kGx>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 int(kSmem));
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_release);
+    }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3(blocks, 1, 1);
@@ -330,11 +339,11 @@ cudaError_t launch_types(const RmsBwdArgs& a, int blocks, cudaStream_t stream) {
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = rmsnorm_backward_one_launch(a.T) && a.grad_gamma ? blocks : 1;
+    attr[0].val.clusterDim.x = blocks;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = rmsnorm_backward_one_launch(a.T) && a.grad_gamma ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, k_rmsnorm_backward<kWarps, kGo, kGx>, a);
 }
 
