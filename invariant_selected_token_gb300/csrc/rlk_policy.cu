@@ -50,7 +50,8 @@ constexpr int kCluster = 8;                 // most CTAs of the one-launch path
 constexpr int kMainCtasPerSm = 4;
 
 struct PolicyCall : PolicyArgs {
-    bool wide;  // four tokens' values can be loaded and stored at a time
+    bool wide;      // four tokens' values can be loaded and stored at a time
+    float scale32;  // rounded on the host: a conversion from fp64 is as slow as fp64 itself
 };
 
 struct Bounds {
@@ -231,7 +232,7 @@ struct Tokens {
 template <int kKl, int kPer>
 __device__ __forceinline__ void policy_tokens(const PolicyCall& a, const Tokens<kKl, kPer>& k, const float (&w)[kPer],
                                               float4 (&out)[kPer]) {
-    const float scale = static_cast<float>(a.scale);
+    const float scale = a.scale32;
     float g[kPer];
     constexpr int kStep = kPer == 1 ? 1 : 2;
 #pragma unroll
@@ -704,6 +705,7 @@ cudaError_t launch_kl(const PolicyCall& a, int num_sms, cudaStream_t stream) {
 cudaError_t launch_policy_loss(const PolicyArgs& args, int num_sms, cudaStream_t stream) {
     PolicyCall a;
     static_cast<PolicyArgs&>(a) = args;
+    a.scale32 = static_cast<float>(a.scale);
     auto places = [](const void* p) { return static_cast<unsigned>(reinterpret_cast<uintptr_t>(p) & 15); };
     a.wide = ((places(a.logprob) | places(a.old_logprob) | places(a.ref_logprob) | places(a.grad) |
                (a.adv_per_seq ? 0u : places(a.advantages)) | (places(a.active) & 3)) == 0);

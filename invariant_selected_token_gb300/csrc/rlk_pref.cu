@@ -45,11 +45,17 @@ constexpr int kChunk = 256;
 constexpr int kSlots = 1024;
 constexpr int kCluster = 8;
 
+// The parameters that the kernels want in fp32 are rounded on the host: a conversion from fp64 is
+// as slow as fp64 itself.
+struct PreferenceCall : PreferenceArgs {
+    float beta32, smooth32, keep32, step32;  // beta, label_smoothing, 1 - it, scale / n_pairs
+};
+
 struct Span {
     int64_t b, e;
 };
 
-__device__ __forceinline__ Span span_of(const PreferenceArgs& a, int64_t q) {
+__device__ __forceinline__ Span span_of(const PreferenceCall& a, int64_t q) {
     Span s;
     s.b = a.offsets[q];
     s.e = a.offsets[q + 1];
@@ -59,9 +65,10 @@ __device__ __forceinline__ Span span_of(const PreferenceArgs& a, int64_t q) {
     return s;
 }
 
-// A pair's loss, rewards and slopes from its two sums and counts, by one thread.  What cancels
-// (the two sums, z, the distance from 1 / (2 beta)) is formed in fp64, the rest in fp32.
-__device__ __forceinline__ void pair_terms(const PreferenceArgs& a, int pair, int64_t q0, int64_t q1,
+// A pair's loss, rewards and slopes from its two sums and counts, by two lanes, each of which
+// writes one of the rewards.  What cancels (the two sums, z, the distance from 1 / (2 beta)) is
+// formed in fp64, the rest in fp32.
+__device__ __forceinline__ void pair_terms(const PreferenceCall& a, int pair, int64_t q0, int64_t q1,
                                            float2 s0, float2 s1, int n0, int n1, bool write,
                                            float* slope, float* held_loss) {
     double m0 = pair_value(s0), m1 = pair_value(s1);
@@ -76,7 +83,7 @@ __device__ __forceinline__ void pair_terms(const PreferenceArgs& a, int pair, in
         m1 = __dmul_rn(m1, __fma_rn(r1, __fma_rn(-c1, r1, 1.0), r1));
     }
     const double h = __dsub_rn(m0, m1);
-    const float beta = static_cast<float>(a.beta);
+    const float beta = a.beta32;
     float loss, dh;
     if (a.kind == RLK_PREF_IPO) {
         const float off = static_cast<float>(__dsub_rn(h, a.half_over_beta));
@@ -90,8 +97,7 @@ __device__ __forceinline__ void pair_terms(const PreferenceArgs& a, int pair, in
             dh = zd < 1.0 ? -beta : (zd == zd ? 0.0f : gap);
         } else {
             // sig(z), sig(-z) and the two logs from e^-|z|, none of which cancels
-            const float z = static_cast<float>(zd), eps = static_cast<float>(a.label_smoothing);
-            const float keep = static_cast<float>(1.0 - a.label_smoothing);
+            const float z = static_cast<float>(zd), eps = a.smooth32, keep = a.keep32;
             const float e = exp_any(-fabsf(z));
             const float soft = log_1_plus(e);
             const float small = __fdiv_rn(e, __fadd_rn(1.0f, e));  // sig(-|z|)
@@ -106,26 +112,25 @@ __device__ __forceinline__ void pair_terms(const PreferenceArgs& a, int pair, in
             dh = __fmul_rn(beta, __fsub_rn(__fmul_rn(eps, up ? large : small), __fmul_rn(keep, up ? small : large)));
         }
     }
-    if (write) {
-        a.out_pair_loss[pair] = loss;
-        a.out_rewards[q0] = static_cast<float>(__dmul_rn(a.beta, m0));
-        a.out_rewards[q1] = static_cast<float>(__dmul_rn(a.beta, m1));
-    }
+    const int lane = threadIdx.x & 31;
+    if (write) a.out_rewards[lane == 0 ? q0 : q1] = static_cast<float>(__dmul_rn(a.beta, lane == 0 ? m0 : m1));
+    if (lane != 0) return;
+    if (write) a.out_pair_loss[pair] = loss;
     if (held_loss) *held_loss = loss;
-    const float step = __fmul_rn(static_cast<float>(a.scale_per_pair), dh);
+    const float step = __fmul_rn(a.step32, dh);
     slope[0] = __fmul_rn(step, inv0);
     slope[1] = -__fmul_rn(step, inv1);
 }
 
-__device__ __forceinline__ int64_t chosen_of(const PreferenceArgs& a, int pair) {
+__device__ __forceinline__ int64_t chosen_of(const PreferenceCall& a, int pair) {
     return a.halves ? pair : 2 * static_cast<int64_t>(pair);
 }
-__device__ __forceinline__ int64_t rejected_of(const PreferenceArgs& a, int pair) {
+__device__ __forceinline__ int64_t rejected_of(const PreferenceCall& a, int pair) {
     return a.halves ? a.n_pairs + static_cast<int64_t>(pair) : 2 * static_cast<int64_t>(pair) + 1;
 }
 
 // Offsets that descend or leave [0, T], as far as this thread sees.
-__device__ __forceinline__ bool offsets_bad(const PreferenceArgs& a) {
+__device__ __forceinline__ bool offsets_bad(const PreferenceCall& a) {
     bool bad = false;
     const int64_t n = 2 * static_cast<int64_t>(a.n_pairs);
     for (int64_t s = threadIdx.x; s <= n; s += blockDim.x) {
@@ -136,7 +141,7 @@ __device__ __forceinline__ bool offsets_bad(const PreferenceArgs& a) {
 }
 
 // The loss from the pairs' losses, by a whole CTA.
-__device__ __forceinline__ void preference_finish(const PreferenceArgs& a, const float* losses, bool bad, float2* tmp) {
+__device__ __forceinline__ void preference_finish(const PreferenceCall& a, const float* losses, bool bad, float2* tmp) {
     bad = __syncthreads_or(bad);
     auto finish = [&](float2 v) {
         if (threadIdx.x != 0) return;
@@ -163,7 +168,7 @@ __device__ __forceinline__ void preference_finish(const PreferenceArgs& a, const
 }
 
 // Sum and active tokens of chunk g of a sequence, by a warp, on every lane.
-__device__ __forceinline__ float2 chunk_sum(const PreferenceArgs& a, const Span& sp, int64_t g, int* count) {
+__device__ __forceinline__ float2 chunk_sum(const PreferenceCall& a, const Span& sp, int64_t g, int* count) {
     const int lane = threadIdx.x & 31;
     float lp[kChunk / 32], ref[kChunk / 32];
     bool on[kChunk / 32];
@@ -199,7 +204,7 @@ struct PairScratch {
 // by thread 0, so a barrier has to follow.  slot(side, j, n) gives a slot's sum and its active
 // tokens; slots from chunks_of() on are empty.
 template <typename SlotOf>
-__device__ __forceinline__ void reduce_pair(const PreferenceArgs& a, int pair, const Span (&sp)[2], SlotOf slot,
+__device__ __forceinline__ void reduce_pair(const PreferenceCall& a, int pair, const Span (&sp)[2], SlotOf slot,
                                             bool write, PairScratch& sc, float* slope, float* held_loss) {
     const int lane = threadIdx.x & 31;
     int held[2];
@@ -254,7 +259,7 @@ __device__ __forceinline__ void reduce_pair(const PreferenceArgs& a, int pair, c
         }
         const float2 v1 = make_float2(__shfl_sync(0xffffffffu, v.x, 16), __shfl_sync(0xffffffffu, v.y, 16));
         const int n1 = __shfl_sync(0xffffffffu, n, 16);
-        if (lane == 0)
+        if (lane < 2)
             pair_terms(a, pair, chosen_of(a, pair), rejected_of(a, pair), v, v1, n, n1, write, slope, held_loss);
     }
 }
@@ -262,7 +267,7 @@ __device__ __forceinline__ void reduce_pair(const PreferenceArgs& a, int pair, c
 // ---------------------------------------------------------------- a team of CTAs per pair
 // One launch of clusters; every `team` CTAs of a cluster take a pair at a time.  alone: this is
 // the only cluster, and it also forms the loss.
-__global__ void __launch_bounds__(kThreads, 2) k_preference(const PreferenceArgs a, int team, int alone) {
+__global__ void __launch_bounds__(kThreads, 2) k_preference(const PreferenceCall a, int team, int alone) {
     __shared__ float2 slots[2][kSlots];
     __shared__ int counts[2][kSlots];
     __shared__ PairScratch scratch;
@@ -338,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_preference(const PreferenceArgs
     if (alone && rank == 0) preference_finish(a, losses, bad, scratch.tmp[0]);
 }
 
-__global__ void __launch_bounds__(kThreads) k_preference_final(const PreferenceArgs a) {
+__global__ void __launch_bounds__(kThreads) k_preference_final(const PreferenceCall a) {
     __shared__ float2 tmp[kWarps];
     const bool bad = offsets_bad(a);
     ptx::grid_dependency_wait();
@@ -354,7 +359,7 @@ struct SplitMap {
     Span span[kSplitSeqs];
     int64_t first[kSplitSeqs + 1];
     int bad;
-    __device__ __forceinline__ void build(const PreferenceArgs& a) {
+    __device__ __forceinline__ void build(const PreferenceCall& a) {
         const int n = 2 * a.n_pairs;
         if (threadIdx.x == 0) bad = 0;
         __syncthreads();
@@ -393,7 +398,7 @@ struct SplitMap {
     }
 };
 
-__global__ void __launch_bounds__(kThreads) k_preference_chunks(const PreferenceArgs a) {
+__global__ void __launch_bounds__(kThreads) k_preference_chunks(const PreferenceCall a) {
     __shared__ SplitMap map;
     ptx::grid_dependents_launch();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
@@ -411,7 +416,7 @@ __global__ void __launch_bounds__(kThreads) k_preference_chunks(const Preference
     }
 }
 
-__global__ void __launch_bounds__(kThreads) k_preference_spread(const PreferenceArgs a) {
+__global__ void __launch_bounds__(kThreads) k_preference_spread(const PreferenceCall a) {
     __shared__ SplitMap map;
     __shared__ PairScratch scratch;
     __shared__ float slope[2];
@@ -484,7 +489,7 @@ __global__ void __launch_bounds__(kThreads) k_preference_spread(const Preference
     preference_finish(a, a.out_pair_loss, map.bad != 0, scratch.tmp[0]);
 }
 
-cudaError_t launch_clusters(const PreferenceArgs& a, int clusters, int size, int team, int alone, int threads,
+cudaError_t launch_clusters(const PreferenceCall& a, int clusters, int size, int team, int alone, int threads,
                             cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -500,7 +505,7 @@ cudaError_t launch_clusters(const PreferenceArgs& a, int clusters, int size, int
     return cudaLaunchKernelEx(&cfg, k_preference, a, team, alone);
 }
 
-cudaError_t launch_after(void (*kernel)(PreferenceArgs), int blocks, const PreferenceArgs& a, cudaStream_t stream) {
+cudaError_t launch_after(void (*kernel)(PreferenceCall), int blocks, const PreferenceCall& a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.stream = stream;
@@ -521,7 +526,13 @@ bool preference_split(int64_t T, int64_t n_pairs) {
 
 int64_t preference_chunks(int64_t T, int64_t n_pairs) { return T / kChunk + 2 * n_pairs; }
 
-cudaError_t launch_preference_loss(const PreferenceArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_preference_loss(const PreferenceArgs& args, int num_sms, cudaStream_t stream) {
+    PreferenceCall a;
+    static_cast<PreferenceArgs&>(a) = args;
+    a.beta32 = static_cast<float>(a.beta);
+    a.smooth32 = static_cast<float>(a.label_smoothing);
+    a.keep32 = static_cast<float>(1.0 - a.label_smoothing);
+    a.step32 = static_cast<float>(a.scale_per_pair);
     if (a.n_pairs == 0) {
         if (a.grad && a.T > 0) {
             const cudaError_t e = cudaMemsetAsync(a.grad, 0, size_t(a.T) * sizeof(float), stream);
