@@ -24,11 +24,12 @@
 // device idle, take one launch over all chunks and one over all tokens, whose
 // CTAs each form the slopes they need.
 //
-// What bounds it: latency.  7.3 us a call on the device for 4 pairs of 255
-// tokens, 10.1 for 64 pairs of 2048 (1.7 MB), 17 for 4 pairs of 262144 (13.6
+// What bounds it: latency.  5.8 us a call on the device for 4 pairs of 255
+// tokens, 8.9 for 64 pairs of 2048 (1.7 MB), 16.3 for 4 pairs of 262144 (13.6
 // MB, 2.0 us of HBM): a launch, the offsets, the tokens, three barriers and
-// about thirty dependent fp64 operations one after the other.  With fp64 sums
-// over the tokens the three took 14, 14 and 43 us.
+// about twenty dependent fp64 operations one after the other.  With fp64 sums
+// over the tokens the three took 14, 14 and 43 us; with the rejected
+// sequence's tokens read after the chosen one's 7.5, 10.4 and 17.1.
 #include <cooperative_groups.h>
 
 #include "rlk_ptx.cuh"

@@ -67,13 +67,13 @@ struct PreferenceArgs {
     int32_t* chunk_counts;
     int32_t* status;
 };
-// Largest batch that one cluster does alone: 11.6 us at one pair of 32768 tokens, where two
-// launches take 11.8.
+// Largest batch that one cluster does alone: 9.6 us at one pair of 32768 tokens, where two
+// launches take 11.1; at 65536 12.6 against 11.4.
 constexpr int64_t kPreferenceClusterTokens = 32768;
 // Tokens a pair from which the path over all chunks is taken.  Against a team of up to 8 CTAs a
-// pair: 16.4 and 13.3 us at 20000 tokens (four pairs), 15.0 and 15.2 at 50000, 12.1 and 15.3 at
-// 60000 (one pair); the million tokens of four pairs took 42 us by teams and take 17.
-constexpr int64_t kPreferenceSplitTokens = 32768;
+// pair: 11.4 and 11.1 us at 32768 tokens, 11.2 and 12.5 at 50000, 11.6 and 16.8 at 100000 (one
+// pair); 13.5 and 11.8, 13.7 and 13.3 at 32768 and 50000 (four pairs).
+constexpr int64_t kPreferenceSplitTokens = 40960;
 // Whether a batch takes the path over all chunks, and how many of them it has at most.
 bool preference_split(int64_t T, int64_t n_pairs);
 int64_t preference_chunks(int64_t T, int64_t n_pairs);

@@ -212,10 +212,16 @@ def test_no_tokens_and_no_sequences(rlk, cuda_device):
     e = torch.zeros(0, device=cuda_device)
     loss, stats, grad = rlk.policy_loss(e, e, e)
     assert float(loss) == 0.0 and not stats.any() and grad.numel() == 0
-    x = torch.full((9,), -1.0, device=cuda_device)
-    loss, _, grad = rlk.policy_loss(x, x, e, advantages_per_seq=True,
-                                    seq_offsets=torch.zeros(1, dtype=torch.int32, device=cuda_device))
-    assert float(loss) == 0.0 and not grad.any()
+    for T in (9, 9000, 40000):
+        for reduction in ("sum", "token_mean", "seq_mean"):
+            x = torch.full((T,), -1.0, device=cuda_device)
+            loss, stats, grad = rlk.policy_loss(x, x, e, advantages_per_seq=True, reduction=reduction,
+                                                seq_offsets=torch.zeros(1, dtype=torch.int32, device=cuda_device))
+            assert float(loss) == 0.0 and not stats.any() and not grad.any()
+    # no tokens in more sequences than one launch takes
+    loss, stats, _ = rlk.policy_loss(e, e, torch.ones(2000, device=cuda_device), advantages_per_seq=True,
+                                     seq_offsets=torch.zeros(2001, dtype=torch.int32, device=cuda_device))
+    assert float(loss) == 0.0 and not stats.any()
 
 
 def test_extreme_ratios(rlk, cuda_device):
@@ -249,8 +255,31 @@ def test_bad_offsets_are_reported(rlk, cuda_device, offsets, reduction):
     assert torch.all(guard[:256] == 7) and torch.all(guard[1256:] == 7)
 
 
-def test_repeats_views_and_streams_give_the_same_bits(rlk, cuda_device):
-    b = batch(9001, [0, 10, 4000, 9001], seed=9)
+@pytest.mark.parametrize("T", [0, 50000, 300000])
+@pytest.mark.parametrize("place", [0, 1, 777, 1999, 2000])
+def test_one_bad_offset_among_many_is_reported(rlk, cuda_device, T, place):
+    """2001 offsets, of which one leaves [0, T] or descends; without tokens too."""
+    off = torch.linspace(0, T, 2001, device=cuda_device).to(torch.int32)
+    off[-1] = T
+    x = torch.full((T,), -1.0, device=cuda_device)
+    adv = torch.ones(2000, device=cuda_device)
+    good = rlk.policy_loss(x, x, adv, seq_offsets=off, advantages_per_seq=True, reduction="seq_mean")
+    assert torch.isfinite(good[0])
+    for value in (-1, T + 1, 2 ** 31 - 1):
+        bad = off.clone()
+        bad[place] = value
+        status = rlk.new_status(cuda_device)
+        loss, stats, _ = rlk.policy_loss(x, x, adv, seq_offsets=bad, advantages_per_seq=True,
+                                         reduction="seq_mean", status=status)
+        with pytest.raises(rlk.RlkError) as e:
+            rlk.raise_on_device_status(status)
+        assert e.value.code == rlk.RLK_ERR_INVALID_ARG
+        assert torch.isnan(loss) and torch.isnan(stats).all()
+
+
+@pytest.mark.parametrize("T", [801, 9001, 60001])
+def test_repeats_views_and_streams_give_the_same_bits(rlk, cuda_device, T):
+    b = batch(T, [0, 10, 400, T], seed=9)
     first = run(rlk, cuda_device, b, kl_coef=0.1, reduction="seq_mean")
     again = run(rlk, cuda_device, b, kl_coef=0.1, reduction="seq_mean")
     # inputs at odd places of larger buffers, on another stream

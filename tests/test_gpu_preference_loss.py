@@ -69,6 +69,8 @@ CASES = [
     (30000, [0] + list(range(101, 29990, 467))[:63] + [30000]),
     (3000, [0] + list(range(20, 2990, 3))[:599] + [3000]),     # hundreds of tiny pairs
     (600001, [0, 262144 + 1, 300000, 300001, 600000]),        # more than 1024 chunks in one
+    (400003, [7, 7, 200000, 200000, 400000]),                 # long pairs with empty sides
+    (300000, [9, 9, 9, 9, 9]),
 ]
 
 
@@ -81,6 +83,17 @@ CASES = [
 def test_preference_loss_parity(rlk, cuda_device, T, offsets, kw, mask, ref):
     b = batch(T, offsets, seed=T, mask=mask, ref=ref)
     check(run(rlk, cuda_device, b, **kw), b, **kw)
+
+
+@pytest.mark.parametrize("T,offsets", [CASES[2], CASES[4], CASES[6], CASES[7]])
+@pytest.mark.parametrize("layout", ["adjacent", "halves"])
+def test_the_loss_alone(rlk, cuda_device, T, offsets, layout):
+    b = batch(T, offsets, seed=T)
+    args = (dev(b["lp"], cuda_device), dev(b["offsets"], cuda_device, np.int32))
+    kw = dict(ref_logprob=dev(b["ref"], cuda_device), active=dev(b["active"], cuda_device), layout=layout)
+    full = rlk.preference_loss(*args, **kw)
+    alone = rlk.preference_loss(*args, want_grad=False, **kw)
+    assert alone[3] is None and all(torch.equal(x, y) for x, y in zip(full[:3], alone[:3]))
 
 
 def test_gradient_against_differences(rlk, cuda_device):
