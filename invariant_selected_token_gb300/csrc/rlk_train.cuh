@@ -130,10 +130,10 @@ struct RmsBwdArgs {
 };
 // Ranges of rows whose grad_gamma sums are formed apart, a CTA per SM each.
 constexpr int kRmsBwdRanges = 152;
-// Rows that one cluster of 8 CTAs takes alone, grad_gamma and all: a launch less for the host (17
-// against 22 us a call at H = 4096) for little more time on the device (6.0 against 4.6 us at 16
+// Rows that one cluster of 8 CTAs takes alone, grad_gamma and all: a launch less for the host (13.4
+// against 18.2 us a call at H = 4096) for little more time on the device (5.9 against 4.5 us at 16
 // rows) as long as every team has one row; at 32 and 64 rows it would be 7.7 and 11.2 us against
-// 4.9 and 5.1 for the two launches.
+// 4.9 and 5.0 for the two launches.
 constexpr int64_t kRmsBwdClusterRows = 16;
 inline bool rmsnorm_backward_one_launch(int64_t T) { return T > 0 && T <= kRmsBwdClusterRows; }
 inline int rmsnorm_backward_ranges(int64_t T) { return T < kRmsBwdRanges ? static_cast<int>(T) : kRmsBwdRanges; }
