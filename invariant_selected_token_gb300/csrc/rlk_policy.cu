@@ -27,7 +27,7 @@
 // What bounds it.  Up to some 10^5 tokens latency: 4.3 us a call on the device
 // at 512 tokens, 5.8 at 8192, of which one launch, one round trip to memory
 // and the first fetch of the code make most.  At 1.77 M tokens (37 MB, 5.6 us
-// of HBM) 16.1 us: 2 us of the counting launch that nothing hides, 3 of the last
+// of HBM) 15.6 us: 2 us of the counting launch that nothing hides, 3 of the last
 // CTA's tail, and instructions, two tokens in one where the values allow.  Sums in fp64
 // instead of pairs of floats made it 27, the branching form of a token 23, a
 // look-up of both ends of a warp's span and of every token 19.7, tokens loaded one
@@ -485,22 +485,24 @@ __global__ void __launch_bounds__(1024) k_policy_count(const PolicyCall a) {
     const int rows = per_seq ? a.n_seqs : kPolicyCountBlocks;
     for (int s = blockIdx.x / size; s < rows; s += gridDim.x / size) {
         int64_t b = 0, e = a.T;
-        if (per_seq) {
-            if (a.offsets) {
-                b = a.offsets[s];
-                e = a.offsets[s + 1];
-            }
-        } else {
-            const Bounds bd = bounds_of(a);
-            const int64_t len = static_cast<int64_t>(bd.last) - bd.first;
-            const int64_t share = ((len + kPolicyCountBlocks - 1) / kPolicyCountBlocks + 15) / 16 * 16;
-            b = bd.first + s * share;
-            e = b + share < bd.last ? b + share : bd.last;
+        Bounds bd = {0, a.T};
+        if (!per_seq) {
+            // shares of the whole batch, so that the mask need not wait for the offsets
+            const int64_t share = ((static_cast<int64_t>(a.T) + kPolicyCountBlocks - 1) / kPolicyCountBlocks + 15) / 16 * 16;
+            bd = bounds_of(a);
+            b = s * share;
+            e = b + share < a.T ? b + share : a.T;
+        } else if (a.offsets) {
+            b = a.offsets[s];
+            e = a.offsets[s + 1];
         }
         int n = static_cast<int>(e - b);
         if (a.active) {
-            n = __reduce_add_sync(0xffffffffu, count_active(a.active, b, e, a.T, rank * threads + threadIdx.x,
-                                                            size * threads));
+            const int who = rank * threads + threadIdx.x, all = size * threads;
+            n = count_active(a.active, b, e, a.T, who, all);
+            if (!per_seq && (b < bd.first || e > bd.last))  // some lie outside all sequences
+                n = count_active(a.active, b > bd.first ? b : bd.first, e < bd.last ? e : bd.last, a.T, who, all);
+            n = __reduce_add_sync(0xffffffffu, n);
             if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = n;
             __syncthreads();
             n = 0;
@@ -681,7 +683,7 @@ cudaError_t launch_kl(const PolicyCall& a, int num_sms, cudaStream_t stream) {
     cfg.stream = stream;
     const int size = lengthy ? kCluster : 1;
     cfg.gridDim = dim3(static_cast<unsigned>((rows > 0 ? rows : 1) * size), 1, 1);
-    cfg.blockDim = dim3(lengthy ? 1024 : kThreads, 1, 1);
+    cfg.blockDim = dim3(lengthy ? 1024 : a.reduction == RLK_REDUCE_TOKEN_MEAN ? 512 : kThreads, 1, 1);
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = size;
     attr[0].val.clusterDim.y = 1;
