@@ -24,8 +24,8 @@
 // device idle, take one launch over all chunks and one over all tokens, whose
 // CTAs each form the slopes they need.
 //
-// What bounds it: latency.  5.8 us a call on the device for 4 pairs of 255
-// tokens, 8.9 for 64 pairs of 2048 (1.7 MB), 16.3 for 4 pairs of 262144 (13.6
+// What bounds it: latency.  5.6 us a call on the device for 4 pairs of 255
+// tokens, 8.0 for 64 pairs of 2048 (1.7 MB), 16.3 for 4 pairs of 262144 (13.6
 // MB, 2.0 us of HBM): a launch, the offsets, the tokens, three barriers and
 // about twenty dependent fp64 operations one after the other.  With fp64 sums
 // over the tokens the three took 14, 14 and 43 us; with the rejected
@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_preference(const PreferenceCall
     __shared__ float slope[2];
     __shared__ float losses[kCluster];  // the first CTA's, when alone
     cg::cluster_group cluster = cg::this_cluster();
+    ptx::grid_dependents_launch();
     cluster.barrier_arrive();
     const int rank = static_cast<int>(cluster.block_rank()), size = static_cast<int>(cluster.num_blocks());
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
