@@ -19,10 +19,11 @@
 //
 // What bounds it: HBM.  8191 x 8192 in bf16 with residual: 537 MB in 82 us,
 // 6.55 TB/s, 0.98 of a plain copy; 4096 x 4096 from fp32 into bf16 with
-// residual: 168 MB in 34 us, 0.74 (at 16384 rows 0.87: the rest is the start,
-// the tail and the second launch); 64 rows: 5.1 us, latency.  On the way the
+// residual: 168 MB in 31 us, 0.80 (at 16384 rows 0.94: the rest is the start,
+// the tail and the second launch); 64 rows: 5.0 us, latency.  On the way the
 // first two took 162 and 66 us with one row at a time, 111 and 37 with the
-// next row in registers, 88 and 38 with 16 features a thread and the ring.
+// next row in registers, 88 and 38 with 16 features a thread and the ring, the
+// second 34 with each lane pair copying its own fp32 sectors.
 #include <atomic>
 #include <cooperative_groups.h>
 #include <cstdint>
@@ -86,16 +87,15 @@ __device__ __forceinline__ uint64_t pair_at(const uint4 (&w)[kPieces<kType>], in
         return f2_pack(__uint_as_float(q[p] << 16), __uint_as_float(q[p] & 0xFFFF0000u));
 }
 
-// fp32 features lie 32 bytes a thread: copied or stored 16 bytes at a time each thread for itself,
-// every access would touch half a 32-byte sector.  So lanes 2j and 2j + 1 take both halves of one
-// lane's features, then both of the other's: piece k holds lane 2j + k's features, the first four
-// in lane 2j's slot and the last four in lane 2j + 1's.
-__device__ __forceinline__ void read_f32(uint4 (&w)[2], const uint4* piece0, int threads) {
-    const bool odd = threadIdx.x & 1;
-    const uint4* const at = piece0 + (odd ? threads : 0);
-    const uint4 own = at[threadIdx.x], other = at[threadIdx.x ^ 1];
-    w[0] = odd ? other : own;
-    w[1] = odd ? own : other;
+// fp32 features lie 32 bytes a lane.  A warp copies them as they lie in memory, 512 bytes an
+// instruction, into two pieces of its own, 64 vectors in a row, of which every other 8 have their
+// neighbours exchanged: so the 8 lanes that a shared-memory access serves at a time find one half
+// of their features in 8 different places.
+__device__ __forceinline__ int f32_place(int vec) { return vec ^ ((vec >> 3) & 1); }
+__device__ __forceinline__ void read_f32(uint4 (&w)[2], const uint4* own) {
+    const int at = f32_place(2 * (threadIdx.x & 31));
+    w[0] = own[at];
+    w[1] = own[at ^ 1];
 }
 
 // A team of kWarps warps (a power of two) takes a row, a CTA's teams every kTeams-th row of its
@@ -123,26 +123,31 @@ __global__ void __launch_bounds__(kCtaThreads<kWarps, kGo, kGx>, 1) k_rmsnorm_ba
     const float h = static_cast<float>(a.H), inv_h = __fdiv_rn(1.0f, h);
     const int odd = lane & 1;
     auto piece = [&](int stage, int g, int k) { return ring + ((stage * 2 + g) * kGroup + k) * kThreads; };
-    // features i .. i + 7 of `base` into pieces k, k + 1
-    auto copy8 = [&](int type, const void* base, int64_t i, int stage, int g, int k) {
-        uint4* const to = piece(stage, g, k) + threadIdx.x;
-        if (type == RLK_DTYPE_F32) {
-            const char* const from = static_cast<const char*>(base) + (i - 8 * odd + 4 * odd) * 4;
-            copy16(to, from);
-            copy16(to + kThreads, from + 32);
-        } else {
-            copy16(to, static_cast<const char*>(base) + i * 2);
-        }
+    // features i .. i + 7, this lane's own, of a bf16 tensor into piece k
+    auto copy_bf16 = [&](const void* base, int64_t i, int stage, int g, int k) {
+        copy16(piece(stage, g, k) + threadIdx.x, static_cast<const char*>(base) + i * 2);
+    };
+    // this lane's share of the 256 features of an fp32 one into pieces k, k + 1; H ends at multiples
+    // of 64
+    auto copy_f32 = [&](const void* base, int64_t i, int stage, int g, int k) {
+        uint4* const to = piece(stage, g, k) + (threadIdx.x >> 5) * 64 + f32_place(lane);
+        const char* const from = static_cast<const char*>(base) + (i - 4 * lane) * 4;
+        const int left = a.H - 512 * warp - 256 * g - 4 * lane;
+        if (left > 0) copy16(to, from);
+        if (left > 128) copy16(to + 32, from + 512);
     };
     auto fetch = [&](int64_t t, int stage) {
         if (t < r1) {
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                if (!in[g]) continue;
                 const int64_t i = t * a.H + i0 + 256 * g;
-                copy8(RLK_DTYPE_BF16, a.x, i, stage, g, 0);
-                copy8(kGo, a.grad_out, i, stage, g, 1);
-                if (a.grad_res) copy8(kGx, a.grad_res, i, stage, g, 1 + kPieces<kGo>);
+                if (in[g]) {
+                    copy_bf16(a.x, i, stage, g, 0);
+                    if (kGo == RLK_DTYPE_BF16) copy_bf16(a.grad_out, i, stage, g, 1);
+                    if (kGx == RLK_DTYPE_BF16 && a.grad_res) copy_bf16(a.grad_res, i, stage, g, 1 + kPieces<kGo>);
+                }
+                if (kGo == RLK_DTYPE_F32) copy_f32(a.grad_out, i, stage, g, 1);
+                if (kGx == RLK_DTYPE_F32 && a.grad_res) copy_f32(a.grad_res, i, stage, g, 1 + kPieces<kGo>);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -167,7 +172,7 @@ __global__ void __launch_bounds__(kCtaThreads<kWarps, kGo, kGx>, 1) k_rmsnorm_ba
             uint4 x[1] = {}, dy[kPieces<kGo>] = {};
             if (in[g]) {
                 x[0] = piece(stage, g, 0)[threadIdx.x];
-                if constexpr (kGo == RLK_DTYPE_F32) read_f32(dy, piece(stage, g, 1), kThreads);
+                if constexpr (kGo == RLK_DTYPE_F32) read_f32(dy, piece(stage, g, 1) + (threadIdx.x >> 5) * 64);
                 else dy[0] = piece(stage, g, 1)[threadIdx.x];
             }
             float s2[4];
@@ -223,10 +228,10 @@ __global__ void __launch_bounds__(kCtaThreads<kWarps, kGo, kGx>, 1) k_rmsnorm_ba
             uint4 x[1] = {}, dy[kPieces<kGo>] = {}, res[kPieces<kGx>] = {};
             if (in[g]) {
                 x[0] = piece(stage, g, 0)[threadIdx.x];
-                if constexpr (kGo == RLK_DTYPE_F32) read_f32(dy, piece(stage, g, 1), kThreads);
+                if constexpr (kGo == RLK_DTYPE_F32) read_f32(dy, piece(stage, g, 1) + (threadIdx.x >> 5) * 64);
                 else dy[0] = piece(stage, g, 1)[threadIdx.x];
                 if (a.grad_res) {
-                    if constexpr (kGx == RLK_DTYPE_F32) read_f32(res, piece(stage, g, 1 + kPieces<kGo>), kThreads);
+                    if constexpr (kGx == RLK_DTYPE_F32) read_f32(res, piece(stage, g, 1 + kPieces<kGo>) + (threadIdx.x >> 5) * 64);
                     else res[0] = piece(stage, g, 1 + kPieces<kGo>)[threadIdx.x];
                 }
             }
