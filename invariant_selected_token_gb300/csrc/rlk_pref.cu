@@ -25,7 +25,7 @@
 // CTAs each form the slopes they need.
 //
 // What bounds it: latency.  5.6 us a call on the device for 4 pairs of 255
-// tokens, 8.0 for 64 pairs of 2048 (1.7 MB), 16.3 for 4 pairs of 262144 (13.6
+// tokens, 8.0 for 64 pairs of 2048 (1.7 MB), 15.5 for 4 pairs of 262144 (13.6
 // MB, 2.0 us of HBM): a launch, the offsets, the tokens, three barriers and
 // about twenty dependent fp64 operations one after the other.  With fp64 sums
 // over the tokens the three took 14, 14 and 43 us; with the rejected
@@ -400,17 +400,55 @@ struct SplitMap {
     }
 };
 
+// The same map over a warp's lanes, two sequences each: nothing to wait for but the offsets.
+struct LaneMap {
+    int b[2], e[2], first[2], total;
+    __device__ __forceinline__ void build(const PreferenceCall& a) {
+        const int lane = threadIdx.x & 31, n = 2 * a.n_pairs;
+        int o[3];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) o[k] = a.offsets[2 * lane + k < n ? 2 * lane + k : n];
+        const bool bad = __any_sync(0xffffffffu, o[0] < 0 || o[1] < o[0] || o[2] < o[1] || o[2] > a.T);
+        int c[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            b[k] = o[k];
+            e[k] = bad ? o[k] : o[k + 1];
+            c[k] = bad ? 0 : static_cast<int>((static_cast<int64_t>(o[k + 1]) - o[k] + kChunk - 1) / kChunk);
+        }
+        int v = c[0] + c[1];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, v, d);
+            if (lane >= d) v += u;
+        }
+        first[0] = v - c[0] - c[1];
+        first[1] = v - c[1];
+        total = __shfl_sync(0xffffffffu, v, 31);
+    }
+    // the tokens of the sequence that holds chunk i, and the chunk's place in it
+    __device__ __forceinline__ Span span_with(int i, int* place) const {
+        const unsigned m0 = __ballot_sync(0xffffffffu, first[0] <= i), m1 = __ballot_sync(0xffffffffu, first[1] <= i);
+        const int k0 = 31 - __clz(m0), k1 = 31 - __clz(m1);  // m0 has lane 0; an empty m1 gives -1
+        const bool second = k1 >= k0;
+        const int from = second ? k1 : k0;
+        Span s;
+        s.b = __shfl_sync(0xffffffffu, second ? b[1] : b[0], from);
+        s.e = __shfl_sync(0xffffffffu, second ? e[1] : e[0], from);
+        *place = i - __shfl_sync(0xffffffffu, second ? first[1] : first[0], from);
+        return s;
+    }
+};
+
 __global__ void __launch_bounds__(kThreads) k_preference_chunks(const PreferenceCall a) {
-    __shared__ SplitMap map;
     ptx::grid_dependents_launch();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
+    LaneMap map;
     map.build(a);
-    const int64_t total = map.first[kSplitSeqs];
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < total;
-         i += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const int q = map.seq_of(i);
-        int n;
-        const float2 v = chunk_sum(a, map.span[q], i - map.first[q], &n);
+    for (int i = blockIdx.x * kWarps + (threadIdx.x >> 5); i < map.total; i += gridDim.x * kWarps) {
+        int n, g;
+        const Span s = map.span_with(i, &g);
+        const float2 v = chunk_sum(a, s, g, &n);
         if ((threadIdx.x & 31) == 0) {
             a.chunk_sums[i] = v;
             a.chunk_counts[i] = n;
