@@ -61,6 +61,7 @@ __device__ __forceinline__ Span span_of(const PreferenceCall& a, int64_t q) {
     s.b = a.offsets[q];
     s.e = a.offsets[q + 1];
     if (s.b < 0) s.b = 0;
+    if (s.b > a.T) s.b = a.T;
     if (s.e > a.T) s.e = a.T;
     if (s.e < s.b) s.e = s.b;
     return s;

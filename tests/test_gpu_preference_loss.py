@@ -184,7 +184,9 @@ def test_one_sided_nan_stays_in_its_pair(rlk, cuda_device):
 
 @pytest.mark.parametrize("T", [1000, 70000, 300000])
 @pytest.mark.parametrize("offsets", [[0, 700, 600, 800, 1000], [-1, 5, 5, 5, 5], [0, 1, 2, 3, 1001],
-                                     [9, 2 ** 31 - 1, -2 ** 31, 5, 10], [0, 2 ** 31 - 1, 0, 2 ** 31 - 1, 0]])
+                                     [9, 2 ** 31 - 1, -2 ** 31, 5, 10], [0, 2 ** 31 - 1, 0, 2 ** 31 - 1, 0],
+                                     [300400, 300400, 300400, 300400, 300400],
+                                     [2 ** 31 - 1, 2 ** 31 - 1, 9, 9, 9], [0, 0, 0, -2 ** 31, -2 ** 31]])
 def test_bad_offsets_are_reported(rlk, cuda_device, T, offsets):
     if offsets == [0, 1, 2, 3, 1001]:
         offsets = [0, 1, 2, 3, T + 1]
