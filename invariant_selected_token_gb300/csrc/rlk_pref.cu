@@ -25,7 +25,7 @@
 // CTAs each form the slopes they need.
 //
 // What bounds it: latency.  5.6 us a call on the device for 4 pairs of 255
-// tokens, 8.0 for 64 pairs of 2048 (1.7 MB), 15.5 for 4 pairs of 262144 (13.6
+// tokens, 8.0 for 64 pairs of 2048 (1.7 MB), 15.1 for 4 pairs of 262144 (13.6
 // MB, 2.0 us of HBM): a launch, the offsets, the tokens, three barriers and
 // about twenty dependent fp64 operations one after the other.  With fp64 sums
 // over the tokens the three took 14, 14 and 43 us; with the rejected
@@ -354,68 +354,27 @@ __global__ void __launch_bounds__(kThreads) k_preference_final(const PreferenceC
 }
 
 // ---------------------------------------------------------------- all CTAs over all pairs
-constexpr int kSplitSeqs = 64;  // most sequences of this path
+constexpr int kSplitSeqs = 64;  // most sequences of this path: two a lane
 
-// Each sequence's tokens and first chunk in the launches' common numbering; no chunk at all where
-// the offsets descend (the numbering would outgrow the workspace).
-struct SplitMap {
-    Span span[kSplitSeqs];
-    int64_t first[kSplitSeqs + 1];
-    int bad;
-    __device__ __forceinline__ void build(const PreferenceCall& a) {
-        const int n = 2 * a.n_pairs;
-        if (threadIdx.x == 0) bad = 0;
-        __syncthreads();
-        if (offsets_bad(a)) bad = 1;
-        __syncthreads();
-        if (threadIdx.x < n) {
-            span[threadIdx.x] = span_of(a, threadIdx.x);
-            if (bad) span[threadIdx.x].e = span[threadIdx.x].b;
-        }
-        __syncthreads();
-        if (threadIdx.x < 32) {
-            // two sequences a lane, an inclusive scan over the lanes
-            const int l = threadIdx.x;
-            const int64_t c0 = 2 * l < n ? chunks_of(span[2 * l]) : 0;
-            const int64_t c1 = 2 * l + 1 < n ? chunks_of(span[2 * l + 1]) : 0;
-            int64_t v = c0 + c1;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-                if (l >= o) v += u;
-            }
-            first[2 * l] = v - c0 - c1;
-            first[2 * l + 1] = v - c1;
-            if (l == 31) first[kSplitSeqs] = v;
-        }
-        __syncthreads();
-    }
-    // the sequence that holds chunk i (empty ones hold none)
-    __device__ __forceinline__ int seq_of(int64_t i) const {
-        int lo = 0, hi = kSplitSeqs - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (first[mid] <= i) lo = mid; else hi = mid - 1;
-        }
-        return lo;
-    }
-};
-
-// The same map over a warp's lanes, two sequences each: nothing to wait for but the offsets.
-struct LaneMap {
-    int b[2], e[2], first[2], total;
+// Each sequence's tokens and first chunk in the launches' common numbering, held by the lanes of
+// every warp, so that nothing but the offsets is waited for; no chunk at all where the offsets
+// descend (the numbering would outgrow the workspace).
+struct ChunkMap {
+    Span span[2];  // of sequences 2 lane and 2 lane + 1
+    int first[2], total;
+    bool bad;
     __device__ __forceinline__ void build(const PreferenceCall& a) {
         const int lane = threadIdx.x & 31, n = 2 * a.n_pairs;
         int o[3];
 #pragma unroll
         for (int k = 0; k < 3; ++k) o[k] = a.offsets[2 * lane + k < n ? 2 * lane + k : n];
-        const bool bad = __any_sync(0xffffffffu, o[0] < 0 || o[1] < o[0] || o[2] < o[1] || o[2] > a.T);
+        bad = __any_sync(0xffffffffu, o[0] < 0 || o[1] < o[0] || o[2] < o[1] || o[2] > a.T);
         int c[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            b[k] = o[k];
-            e[k] = bad ? o[k] : o[k + 1];
-            c[k] = bad ? 0 : static_cast<int>((static_cast<int64_t>(o[k + 1]) - o[k] + kChunk - 1) / kChunk);
+            span[k].b = bad ? 0 : o[k];
+            span[k].e = bad ? 0 : o[k + 1];
+            c[k] = static_cast<int>(chunks_of(span[k]));
         }
         int v = c[0] + c[1];
 #pragma unroll
@@ -427,16 +386,19 @@ struct LaneMap {
         first[1] = v - c[1];
         total = __shfl_sync(0xffffffffu, v, 31);
     }
-    // the tokens of the sequence that holds chunk i, and the chunk's place in it
-    __device__ __forceinline__ Span span_with(int i, int* place) const {
+    // The rest by whole warps.  The sequence that holds chunk i < total (empty ones hold none):
+    __device__ __forceinline__ int seq_of(int i) const {
         const unsigned m0 = __ballot_sync(0xffffffffu, first[0] <= i), m1 = __ballot_sync(0xffffffffu, first[1] <= i);
         const int k0 = 31 - __clz(m0), k1 = 31 - __clz(m1);  // m0 has lane 0; an empty m1 gives -1
-        const bool second = k1 >= k0;
-        const int from = second ? k1 : k0;
+        return k1 >= k0 ? 2 * k1 + 1 : 2 * k0;
+    }
+    __device__ __forceinline__ int first_of(int q) const {
+        return __shfl_sync(0xffffffffu, q & 1 ? first[1] : first[0], q >> 1);
+    }
+    __device__ __forceinline__ Span span_at(int q) const {
         Span s;
-        s.b = __shfl_sync(0xffffffffu, second ? b[1] : b[0], from);
-        s.e = __shfl_sync(0xffffffffu, second ? e[1] : e[0], from);
-        *place = i - __shfl_sync(0xffffffffu, second ? first[1] : first[0], from);
+        s.b = __shfl_sync(0xffffffffu, static_cast<int>(q & 1 ? span[1].b : span[0].b), q >> 1);
+        s.e = __shfl_sync(0xffffffffu, static_cast<int>(q & 1 ? span[1].e : span[0].e), q >> 1);
         return s;
     }
 };
@@ -444,12 +406,12 @@ struct LaneMap {
 __global__ void __launch_bounds__(kThreads) k_preference_chunks(const PreferenceCall a) {
     ptx::grid_dependents_launch();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
-    LaneMap map;
+    ChunkMap map;
     map.build(a);
     for (int i = blockIdx.x * kWarps + (threadIdx.x >> 5); i < map.total; i += gridDim.x * kWarps) {
-        int n, g;
-        const Span s = map.span_with(i, &g);
-        const float2 v = chunk_sum(a, s, g, &n);
+        const int q = map.seq_of(i);
+        int n;
+        const float2 v = chunk_sum(a, map.span_at(q), i - map.first_of(q), &n);
         if ((threadIdx.x & 31) == 0) {
             a.chunk_sums[i] = v;
             a.chunk_counts[i] = n;
@@ -458,16 +420,16 @@ __global__ void __launch_bounds__(kThreads) k_preference_chunks(const Preference
 }
 
 __global__ void __launch_bounds__(kThreads) k_preference_spread(const PreferenceCall a) {
-    __shared__ SplitMap map;
     __shared__ PairScratch scratch;
     __shared__ float slope[2];
     __shared__ bool last_here;
+    ChunkMap map;
     map.build(a);
     ptx::grid_dependency_wait();
     auto slopes_of = [&](int pair, bool write) {
         const int q0 = static_cast<int>(chosen_of(a, pair)), q1 = static_cast<int>(rejected_of(a, pair));
-        const Span sp[2] = {map.span[q0], map.span[q1]};
-        const int64_t at[2] = {map.first[q0], map.first[q1]};
+        const Span sp[2] = {map.span_at(q0), map.span_at(q1)};
+        const int at[2] = {map.first_of(q0), map.first_of(q1)};
         __syncthreads();  // the previous pair's slopes have been read
         reduce_pair(a, pair, sp,
                     [&](int side, int j, int& n) {
@@ -486,25 +448,26 @@ __global__ void __launch_bounds__(kThreads) k_preference_spread(const Preference
     // where that sequence is empty, by CTA pair mod grid
     int have = -1;
     for (int pair = blockIdx.x; pair < a.n_pairs; pair += gridDim.x) {
-        if (chunks_of(map.span[chosen_of(a, pair)]) > 0) continue;
+        if (chunks_of(map.span_at(static_cast<int>(chosen_of(a, pair)))) > 0) continue;
         slopes_of(pair, true);
         have = pair;
     }
-    const int64_t total = map.first[kSplitSeqs];
-    const int64_t i0 = total * blockIdx.x / gridDim.x, i1 = total * (blockIdx.x + 1) / gridDim.x;
-    for (int64_t i = i0; i < i1;) {
-        const int q = map.seq_of(i);
-        const int64_t next = map.first[q + 1] < i1 ? map.first[q + 1] : i1;
+    const int i0 = static_cast<int>(static_cast<int64_t>(map.total) * blockIdx.x / gridDim.x);
+    const int i1 = static_cast<int>(static_cast<int64_t>(map.total) * (blockIdx.x + 1) / gridDim.x);
+    for (int i = i0; i < i1;) {
+        const int q = map.seq_of(i), first = map.first_of(q);
+        const Span sp = map.span_at(q);
+        const int end = first + static_cast<int>(chunks_of(sp)), next = end < i1 ? end : i1;
         const int pair = a.halves ? q % a.n_pairs : q / 2;
         const int side = a.halves ? q / a.n_pairs : q % 2;
-        const bool write = side == 0 && i == map.first[q];
+        const bool write = side == 0 && i == first;
         if (write || (a.grad && pair != have)) {
             slopes_of(pair, write);
             have = pair;
         }
-        const int64_t b = map.span[q].b + (i - map.first[q]) * kChunk;
-        int64_t e = map.span[q].b + (next - map.first[q]) * kChunk;
-        if (e > map.span[q].e) e = map.span[q].e;
+        const int64_t b = sp.b + static_cast<int64_t>(i - first) * kChunk;
+        int64_t e = sp.b + static_cast<int64_t>(next - first) * kChunk;
+        if (e > sp.e) e = sp.e;
         i = next;
         if (!a.grad) continue;
         const float g = slope[side];
@@ -516,8 +479,9 @@ __global__ void __launch_bounds__(kThreads) k_preference_spread(const Preference
         // tokens before the first and behind the last sequence
         const int64_t who = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
         const int64_t all = static_cast<int64_t>(gridDim.x) * kThreads;
-        for (int64_t t = who, e = map.span[0].b; t < e; t += all) a.grad[t] = 0.0f;
-        for (int64_t t = map.span[2 * a.n_pairs - 1].e + who; t < a.T; t += all) a.grad[t] = 0.0f;
+        const int64_t head = map.span_at(0).b, tail = map.span_at(2 * a.n_pairs - 1).e;
+        for (int64_t t = who; t < head; t += all) a.grad[t] = 0.0f;
+        for (int64_t t = tail + who; t < a.T; t += all) a.grad[t] = 0.0f;
     }
     // the last CTA to come here adds up the pairs, whose losses the CTAs' first threads have written
     if (threadIdx.x == 0) {
@@ -527,7 +491,7 @@ __global__ void __launch_bounds__(kThreads) k_preference_spread(const Preference
     __syncthreads();
     if (!last_here) return;
     __threadfence();
-    preference_finish(a, a.out_pair_loss, map.bad != 0, scratch.tmp[0]);
+    preference_finish(a, a.out_pair_loss, map.bad, scratch.tmp[0]);
 }
 
 cudaError_t launch_clusters(const PreferenceCall& a, int clusters, int size, int team, int alone, int threads,
