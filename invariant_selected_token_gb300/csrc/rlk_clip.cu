@@ -23,10 +23,11 @@
 // What bounds it: three passes over HBM (in, in again, out) for sets larger
 // than L2.  grad_W [151936, 4096] in fp32: 7.47 GB in 1.12 ms, 6.66 TB/s, the
 // rate of a plain copy; 290 ragged bf16 and fp32 tensors: 1.42 GB in 229 us,
-// 6.2 TB/s; 12 tensors of 40001 elements in all: 7.3 us, latency.  Measured
+// 6.2 TB/s; 12 tensors of 40001 elements in all: 6.6 us, latency.  Measured
 // and dropped for the two large sets: one element a load 1607 and 660 us; a
 // barrier after every 16384 elements 1107 and 233; warps alone on 2048
 // elements 1143 and 235; one unbroken run of elements a CTA 1121 and 283.
+#include <cmath>
 #include <cooperative_groups.h>
 
 #include "rlk_ptx.cuh"
@@ -254,33 +255,42 @@ __device__ __forceinline__ void scale_pieces(const Table& t, int c0, int step, f
     }
 }
 
-// A CTA's sum from its 8 warps', on thread 0.
-__device__ __forceinline__ float2 warps_sum(float2 v, float2* smem) {
-    if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = v;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < kWarps; ++i) v = pair_add(v, smem[i]);
-    }
+// The limit in fp32 (a conversion from fp64 on the device is as slow as fp64 itself): an fp32 norm
+// is above max_norm where it is above the largest fp32 number that is not.
+struct ClipCall : ClipOut {
+    float limit, max32;
+};
+
+// The sum of what eight lanes in a row hold, on each of them.
+__device__ __forceinline__ float2 sum_of_8(float2 v) {
+#pragma unroll 1
+    for (int o = 4; o >= 1; o >>= 1)
+        v = pair_add(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
     return v;
 }
 
-// The slots' sum by a CTA of 256 threads, and from it (norm, scale); every thread gets them.
-__device__ __forceinline__ float2 norm_and_scale(const float2* slots, int n, double max_norm, float2* smem) {
-    __shared__ float2 result;
+// A CTA's sum from its 8 warps', on every thread.
+__device__ __forceinline__ float2 warps_sum(float2 v, float2* smem) {
+    static_assert(kWarps == 8, "a lane a warp");
+    if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = v;
+    __syncthreads();
+    return sum_of_8(smem[threadIdx.x & 7]);
+}
+
+// (norm, scale) from the sum of all squares.
+__device__ __forceinline__ float2 norm_and_scale(float2 sum, const ClipCall& o) {
+    const float norm = __fsqrt_rn(__fadd_rn(sum.x, sum.y));
+    return make_float2(norm, norm < CUDART_INF_F && norm > o.limit ? __fdiv_rn(o.max32, norm) : 1.0f);
+}
+// and from the slots, by a CTA of 256 threads, each of which gets them.
+__device__ __forceinline__ float2 norm_and_scale(const float2* slots, int n, const ClipCall& o, float2* smem) {
     float2 v = pair_of(0.0f);
 #pragma unroll 4
     for (int i = threadIdx.x; i < n; i += kThreads) v = pair_add(v, slots[i]);
-    v = warps_sum(warp_sum(v), smem);
-    if (threadIdx.x == 0) {
-        const float norm = __fsqrt_rn(__fadd_rn(v.x, v.y));
-        const bool shrink = norm < CUDART_INF_F && static_cast<double>(norm) > max_norm;
-        result = make_float2(norm, shrink ? __fdiv_rn(static_cast<float>(max_norm), norm) : 1.0f);
-    }
-    __syncthreads();
-    return result;
+    return norm_and_scale(warps_sum(warp_sum(v), smem), o);
 }
 
-__device__ __forceinline__ void write_norm(const ClipOut& o, float2 r) {
+__device__ __forceinline__ void write_norm(const ClipCall& o, float2 r) {
     *o.norm = r.x;
     if (o.scale) *o.scale = r.y;
     if (!(r.x < CUDART_INF_F)) report_status(o.status, RLK_ERR_NONFINITE);
@@ -288,7 +298,7 @@ __device__ __forceinline__ void write_norm(const ClipOut& o, float2 r) {
 
 // ---------------------------------------------------------------- one launch
 __global__ void __launch_bounds__(kThreads) k_clip_cluster(const __grid_constant__ ClipTableSmall t,
-                                                           const ClipOut o) {
+                                                           const ClipCall o) {
     __shared__ float2 slots[kClipCluster];  // every CTA's sum, in every CTA
     __shared__ float2 tmp[kWarps];
     cg::cluster_group cluster = cg::this_cluster();
@@ -296,11 +306,10 @@ __global__ void __launch_bounds__(kThreads) k_clip_cluster(const __grid_constant
     const int rank = static_cast<int>(cluster.block_rank()), total = t.first[t.count];
     const float2 sum = warps_sum(sum_pieces(t, rank, kClipCluster), tmp);
     cluster.barrier_wait();  // every CTA has started: its shared memory may be written
-    if (threadIdx.x == 0) {
-        for (int c = 0; c < kClipCluster; ++c) cluster.map_shared_rank(slots, c)[rank] = sum;
-    }
+    if (threadIdx.x < kClipCluster) cluster.map_shared_rank(slots, threadIdx.x)[rank] = sum;
     cluster.sync();
-    const float2 res = norm_and_scale(slots, kClipCluster, o.max_norm, tmp);
+    static_assert(kClipCluster == 8, "a lane a CTA");
+    const float2 res = norm_and_scale(sum_of_8(slots[threadIdx.x & 7]), o);
     if (rank == 0 && threadIdx.x == 0) write_norm(o, res);
     if (o.scale && total > rank)
         scale_pieces(t, rank + (total - 1 - rank) / kClipCluster * kClipCluster, kClipCluster, res.y);
@@ -315,20 +324,28 @@ __global__ void __launch_bounds__(kThreads, kClipCtasPerSm) k_grad_sumsq(const _
     if (threadIdx.x == 0) slots[blockIdx.x] = sum;
 }
 
-__global__ void __launch_bounds__(kThreads) k_grad_norm(const float2* slots, int n, const ClipOut o) {
+__global__ void __launch_bounds__(kThreads) k_grad_norm(const float2* slots, int n, const ClipCall o) {
     __shared__ float2 tmp[kThreads / 32];
     ptx::grid_dependency_wait();
-    const float2 r = norm_and_scale(slots, n, o.max_norm, tmp);
+    const float2 r = norm_and_scale(slots, n, o, tmp);
     if (threadIdx.x == 0) write_norm(o, r);
 }
 
 __global__ void __launch_bounds__(kThreads, kClipCtasPerSm) k_grad_scale(const __grid_constant__ ClipTable t, const float2* slots,
-                                                         int n, const ClipOut o, int write) {
+                                                         int n, const ClipCall o, int write) {
     __shared__ float2 tmp[kThreads / 32];
     ptx::grid_dependency_wait();
-    const float2 r = norm_and_scale(slots, n, o.max_norm, tmp);
+    const float2 r = norm_and_scale(slots, n, o, tmp);
     if (write && blockIdx.x == 0 && threadIdx.x == 0) write_norm(o, r);
     scale_pieces(t, t.first[t.count] - 1 - static_cast<int>(blockIdx.x), gridDim.x, r.y);
+}
+
+ClipCall call_of(const ClipOut& o) {
+    ClipCall c;
+    static_cast<ClipOut&>(c) = o;
+    c.limit = c.max32 = static_cast<float>(o.max_norm);
+    if (static_cast<double>(c.limit) > o.max_norm) c.limit = std::nextafterf(c.limit, 0.0f);
+    return c;
 }
 
 template <typename... Args>
@@ -359,7 +376,7 @@ cudaError_t launch_clip_cluster(const ClipTableSmall& t, const ClipOut& o, cudaS
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_clip_cluster, t, o);
+    return cudaLaunchKernelEx(&cfg, k_clip_cluster, t, call_of(o));
 }
 
 cudaError_t launch_grad_sumsq(const ClipTable& t, float2* slots, cudaStream_t stream) {
@@ -368,12 +385,12 @@ cudaError_t launch_grad_sumsq(const ClipTable& t, float2* slots, cudaStream_t st
 }
 
 cudaError_t launch_grad_norm(const float2* slots, int n, const ClipOut& o, cudaStream_t stream) {
-    return launch_after(k_grad_norm, 1, stream, slots, n, o);
+    return launch_after(k_grad_norm, 1, stream, slots, n, call_of(o));
 }
 
 cudaError_t launch_grad_scale(const ClipTable& t, const float2* slots, int n, const ClipOut& o, bool write,
                               cudaStream_t stream) {
-    return launch_after(k_grad_scale, clip_launch_slots(t.first[t.count]), stream, t, slots, n, o, int(write));
+    return launch_after(k_grad_scale, clip_launch_slots(t.first[t.count]), stream, t, slots, n, call_of(o), int(write));
 }
 
 }  // namespace rlk

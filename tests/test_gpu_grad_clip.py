@@ -87,6 +87,23 @@ def test_below_the_limit_nothing_changes(rlk, cuda_device):
     assert float(scale) == 0.0 and not any(g.any() for g in grads)
 
 
+@pytest.mark.parametrize("sizes", [[5], [300000, 300000]])  # one launch and two
+def test_limits_next_to_the_norm(rlk, cuda_device, sizes):
+    """The norm, an fp32 number, is compared with max_norm itself, not with its rounded value."""
+    g = [torch.zeros(n, device=cuda_device) for n in sizes]
+    g[0][:2] = torch.tensor([3.0, 4.0])  # norm 5 exactly
+    for limit, shrinks in ((5.0, False), (5.0 - 1e-12, True), (5.0 + 1e-12, False), (1e300, False),
+                           (float("inf"), False), (0.0, True), (1e-60, True)):
+        out = [torch.empty_like(t) for t in g]
+        norm, scale = rlk.clip_grads(g, limit, out=out)
+        assert float(norm) == 5.0
+        # a limit that rounds to the norm gives a scale of 1 either way
+        assert float(scale) == (np.float32(limit) / np.float32(5.0) if shrinks else 1.0)
+        assert torch.equal(out[0], g[0] * scale)
+    big = [t * 1e25 for t in g]  # squares beyond fp32
+    assert float(rlk.grad_norm(big)) == float("inf")
+
+
 def test_zero_gradients(rlk, cuda_device):
     grads = [torch.zeros(100, device=cuda_device)]
     norm, scale = rlk.clip_grads(grads, 0.0)
