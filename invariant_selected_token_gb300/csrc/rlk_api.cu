@@ -440,13 +440,6 @@ rlk_status_t backward_gemms(const void* hidden, const void* W, int64_t T, int64_
 }
 
 // ---------------------------------------------------------------- training-step operators
-// A double as the sum of two floats (2^-48 relative).
-float2 split_two(double v) {
-    const float hi = float(v);
-    const float lo = std::isfinite(hi) ? float(v - double(hi)) : 0.0f;
-    return make_float2(hi, lo);
-}
-
 struct PolicyLayout {
     size_t ticket, counts, parts, total;
 };
@@ -1120,9 +1113,9 @@ rlk_status_t rlk_policy_loss(const float* logprob, const float* old_logprob,
     a.kl_kind = kl_kind;
     a.reduction = reduction;
     const double none = -std::numeric_limits<double>::infinity();
-    a.log_high = split_two(std::log1p(clip_high));
-    a.log_low = split_two(clip_low < 1.0 ? std::log1p(-clip_low) : none);
-    a.log_dual = split_two(dual_clip > 0.0 ? std::log(dual_clip) : none);
+    a.log_high = rlk::split_two(std::log1p(clip_high));
+    a.log_low = rlk::split_two(clip_low < 1.0 ? std::log1p(-clip_low) : none);
+    a.log_dual = rlk::split_two(dual_clip > 0.0 ? std::log(dual_clip) : none);
     a.ratio_high = float(1.0 + clip_high);
     a.ratio_low = float(1.0 - clip_low);
     a.dual = float(dual_clip);

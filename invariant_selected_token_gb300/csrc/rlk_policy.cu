@@ -24,10 +24,10 @@
 // tokens 4 l .. 4 l + 3 pairwise, the lanes a shuffle tree, the spans in
 // order.
 //
-// What bounds it.  Up to some 10^5 tokens latency: 4.3 us a call on the device
-// at 512 tokens, 5.8 at 8192, of which one launch, one round trip to memory
+// What bounds it.  Up to some 10^5 tokens latency: 4.0 us a call on the device
+// at 512 tokens, 5.4 at 8192, of which one launch, one round trip to memory
 // and the first fetch of the code make most.  At 1.77 M tokens (37 MB, 5.6 us
-// of HBM) 15.6 us: 2 us of the counting launch that nothing hides, 3 of the last
+// of HBM) 15.4 us: 2 us of the counting launch that nothing hides, 3 of the last
 // CTA's tail, and instructions, two tokens in one where the values allow.  Sums in fp64
 // instead of pairs of floats made it 27, the branching form of a token 23, a
 // look-up of both ends of a warp's span and of every token 19.7, tokens loaded one
@@ -51,7 +51,7 @@ constexpr int kMainCtasPerSm = 4;
 
 struct PolicyCall : PolicyArgs {
     bool wide;      // four tokens' values can be loaded and stored at a time
-    float scale32;  // rounded on the host: a conversion from fp64 is as slow as fp64 itself
+    float2 scale2, coef2;  // scale and kl_coef
 };
 
 struct Bounds {
@@ -232,7 +232,7 @@ struct Tokens {
 template <int kKl, int kPer>
 __device__ __forceinline__ void policy_tokens(const PolicyCall& a, const Tokens<kKl, kPer>& k, const float (&w)[kPer],
                                               float4 (&out)[kPer]) {
-    const float scale = a.scale32;
+    const float scale = a.scale2.x;
     float g[kPer];
     constexpr int kStep = kPer == 1 ? 1 : 2;
 #pragma unroll
@@ -312,9 +312,9 @@ __device__ __forceinline__ void write_stat(const PolicyCall& a, int k, float2 v,
     a.out_stats[k] = bad ? CUDART_NAN_F : __fadd_rn(v.x, v.y);
 }
 __device__ __forceinline__ void write_loss(const PolicyCall& a, float2 policy, float2 kl, bool bad) {
-    double sum = pair_value(policy);
-    if (a.kl_coef64 != 0.0) sum = __fma_rn(a.kl_coef64, pair_value(kl), sum);
-    *a.out_loss = bad ? CUDART_NAN_F : static_cast<float>(__dmul_rn(a.scale, sum));
+    // in fp64 this would be 0.3 us of dependent operations
+    const float2 sum = a.coef2.x != 0.0f ? pair_add(policy, pair_mul(a.coef2, kl)) : policy;
+    *a.out_loss = bad ? CUDART_NAN_F : pair_mul(a.scale2, sum).x;
     if (bad) report_status(a.status, RLK_ERR_INVALID_ARG);
 }
 
@@ -707,7 +707,8 @@ cudaError_t launch_kl(const PolicyCall& a, int num_sms, cudaStream_t stream) {
 cudaError_t launch_policy_loss(const PolicyArgs& args, int num_sms, cudaStream_t stream) {
     PolicyCall a;
     static_cast<PolicyArgs&>(a) = args;
-    a.scale32 = static_cast<float>(a.scale);
+    a.scale2 = split_two(a.scale);
+    a.coef2 = split_two(a.kl_coef64);
     auto places = [](const void* p) { return static_cast<unsigned>(reinterpret_cast<uintptr_t>(p) & 15); };
     a.wide = ((places(a.logprob) | places(a.old_logprob) | places(a.ref_logprob) | places(a.grad) |
                (a.adv_per_seq ? 0u : places(a.advantages)) | (places(a.active) & 3)) == 0);

@@ -24,13 +24,15 @@
 // device idle, take one launch over all chunks and one over all tokens, whose
 // CTAs each form the slopes they need.
 //
-// What bounds it: latency.  5.6 us a call on the device for 4 pairs of 255
-// tokens, 8.0 for 64 pairs of 2048 (1.7 MB), 15.1 for 4 pairs of 262144 (13.6
-// MB, 2.0 us of HBM): a launch, the offsets, the tokens, three barriers and
-// about twenty dependent fp64 operations one after the other.  With fp64 sums
-// over the tokens the three took 14, 14 and 43 us; with the rejected
-// sequence's tokens read after the chosen one's 7.5, 10.4 and 17.1.
+// What bounds it: latency.  5.4 us a call on the device for 4 pairs of 255
+// tokens, 7.7 for 64 pairs of 2048 (1.7 MB), 14.5 for 4 pairs of 262144 (13.6
+// MB, 2.0 us of HBM): a launch, the offsets, the tokens, three barriers and a
+// pair's terms one after the other.  With fp64 sums over the tokens the three
+// took 14, 14 and 43 us; with the rejected sequence's tokens read after the
+// chosen one's 7.5, 10.4 and 17.1; with a pair's terms in fp64 5.8, 8.1 and
+// 15.1.
 #include <cooperative_groups.h>
+#include <limits>
 
 #include "rlk_ptx.cuh"
 #include "rlk_train.cuh"
@@ -46,10 +48,9 @@ constexpr int kChunk = 256;
 constexpr int kSlots = 1024;
 constexpr int kCluster = 8;
 
-// The parameters that the kernels want in fp32 are rounded on the host: a conversion from fp64 is
-// as slow as fp64 itself.
 struct PreferenceCall : PreferenceArgs {
-    float beta32, smooth32, keep32, step32;  // beta, label_smoothing, 1 - it, scale / n_pairs
+    float smooth32, keep32;                       // label_smoothing and 1 - it
+    float2 beta2, margin2, half_over_beta2, scale2;  // the last one scale / n_pairs
 };
 
 struct Span {
@@ -67,59 +68,66 @@ __device__ __forceinline__ Span span_of(const PreferenceCall& a, int64_t q) {
     return s;
 }
 
+// A sequence's mean from its sum, and 1 / (its active tokens).
+__device__ __forceinline__ float2 mean_of(float2 sum, int n, float& inv) {
+    const int c = n > 1 ? n : 1;
+    const float hi = static_cast<float>(c), lo = static_cast<float>(c - static_cast<int64_t>(hi));
+    inv = __fdiv_rn(1.0f, hi);
+    // a quotient within a few steps, and the remainder's
+    const float q = __fmul_rn(sum.x, inv);
+    const float r = __fmaf_rn(-q, lo, __fadd_rn(__fmaf_rn(-q, hi, sum.x), sum.y));
+    const float e = __fmul_rn(r, inv), m = __fadd_rn(q, e);
+    return fabsf(q) < CUDART_INF_F ? make_float2(m, __fsub_rn(e, __fsub_rn(m, q))) : pair_of(q);
+}
+
 // A pair's loss, rewards and slopes from its two sums and counts, by two lanes, each of which
 // writes one of the rewards.  What cancels (the two sums, z, the distance from 1 / (2 beta)) is
-// formed in fp64, the rest in fp32.
+// formed as pairs of floats, the rest in fp32; in fp64 it took 1 us, one operation after another.
 __device__ __forceinline__ void pair_terms(const PreferenceCall& a, int pair, int64_t q0, int64_t q1,
                                            float2 s0, float2 s1, int n0, int n1, bool write,
                                            float* slope, float* held_loss) {
-    double m0 = pair_value(s0), m1 = pair_value(s1);
+    float2 m0 = s0, m1 = s1;
     float inv0 = 1.0f, inv1 = 1.0f;
     if (a.length_normalize) {
-        const double c0 = n0 > 1 ? n0 : 1, c1 = n1 > 1 ? n1 : 1;
-        inv0 = __fdiv_rn(1.0f, static_cast<float>(c0));
-        inv1 = __fdiv_rn(1.0f, static_cast<float>(c1));
-        // one Newton step takes the reciprocals from 2^-24 to 2^-47
-        const double r0 = inv0, r1 = inv1;
-        m0 = __dmul_rn(m0, __fma_rn(r0, __fma_rn(-c0, r0, 1.0), r0));
-        m1 = __dmul_rn(m1, __fma_rn(r1, __fma_rn(-c1, r1, 1.0), r1));
+        m0 = mean_of(s0, n0, inv0);
+        m1 = mean_of(s1, n1, inv1);
     }
-    const double h = __dsub_rn(m0, m1);
-    const float beta = a.beta32;
+    const float2 h = pair_add(m0, pair_negated(m1));
+    const float beta = a.beta2.x;
     float loss, dh;
     if (a.kind == RLK_PREF_IPO) {
-        const float off = static_cast<float>(__dsub_rn(h, a.half_over_beta));
+        const float off = pair_add(h, pair_negated(a.half_over_beta2)).x;
         loss = __fmul_rn(off, off);
         dh = __fmul_rn(2.0f, off);
+    } else if (a.kind == RLK_PREF_HINGE) {
+        // whether z < 1 is a decision, on sums that may well be whole numbers: beta itself, in fp64
+        const double z = __fma_rn(a.beta, __dadd_rn(static_cast<double>(h.x), static_cast<double>(h.y)), -a.margin);
+        const float gap = static_cast<float>(__dsub_rn(1.0, z));
+        loss = gap > 0.0f ? gap : (gap == gap ? 0.0f : gap);
+        dh = z < 1.0 ? -beta : (z == z ? 0.0f : gap);
     } else {
-        const double zd = __fma_rn(a.beta, h, -a.margin);
-        if (a.kind == RLK_PREF_HINGE) {
-            const float gap = static_cast<float>(__dsub_rn(1.0, zd));
-            loss = gap > 0.0f ? gap : (gap == gap ? 0.0f : gap);
-            dh = zd < 1.0 ? -beta : (zd == zd ? 0.0f : gap);
-        } else {
-            // sig(z), sig(-z) and the two logs from e^-|z|, none of which cancels
-            const float z = static_cast<float>(zd), eps = a.smooth32, keep = a.keep32;
-            const float e = exp_any(-fabsf(z));
-            const float soft = log_1_plus(e);
-            const float small = __fdiv_rn(e, __fadd_rn(1.0f, e));  // sig(-|z|)
-            const float large = __fdiv_rn(1.0f, __fadd_rn(1.0f, e));
-            const float near = soft, far = __fadd_rn(soft, fabsf(z));  // -log sig(|z|), -log sig(-|z|)
-            const bool up = z >= 0.0f;
-            // a part with weight 0 is 0 even where its log is infinite
-            loss = __fadd_rn(keep != 0.0f ? __fmul_rn(keep, up ? near : far) : 0.0f,
-                             eps != 0.0f ? __fmul_rn(eps, up ? far : near) : 0.0f);
-            if (z != z) loss = z;
-            // sig(z) - (1 - eps) = eps sig(z) - (1 - eps) sig(-z)
-            dh = __fmul_rn(beta, __fsub_rn(__fmul_rn(eps, up ? large : small), __fmul_rn(keep, up ? small : large)));
-        }
+        // sig(z), sig(-z) and the two logs from e^-|z|, none of which cancels
+        const float z = pair_add(pair_mul(a.beta2, h), pair_negated(a.margin2)).x;
+        const float eps = a.smooth32, keep = a.keep32;
+        const float e = exp_any(-fabsf(z));
+        const float soft = log_1_plus(e);
+        const float small = __fdiv_rn(e, __fadd_rn(1.0f, e));  // sig(-|z|)
+        const float large = __fdiv_rn(1.0f, __fadd_rn(1.0f, e));
+        const float near = soft, far = __fadd_rn(soft, fabsf(z));  // -log sig(|z|), -log sig(-|z|)
+        const bool up = z >= 0.0f;
+        // a part with weight 0 is 0 even where its log is infinite
+        loss = __fadd_rn(keep != 0.0f ? __fmul_rn(keep, up ? near : far) : 0.0f,
+                         eps != 0.0f ? __fmul_rn(eps, up ? far : near) : 0.0f);
+        if (z != z) loss = z;
+        // sig(z) - (1 - eps) = eps sig(z) - (1 - eps) sig(-z)
+        dh = __fmul_rn(beta, __fsub_rn(__fmul_rn(eps, up ? large : small), __fmul_rn(keep, up ? small : large)));
     }
     const int lane = threadIdx.x & 31;
-    if (write) a.out_rewards[lane == 0 ? q0 : q1] = static_cast<float>(__dmul_rn(a.beta, lane == 0 ? m0 : m1));
+    if (write) a.out_rewards[lane == 0 ? q0 : q1] = pair_mul(a.beta2, lane == 0 ? m0 : m1).x;
     if (lane != 0) return;
     if (write) a.out_pair_loss[pair] = loss;
     if (held_loss) *held_loss = loss;
-    const float step = __fmul_rn(a.step32, dh);
+    const float step = __fmul_rn(a.scale2.x, dh);
     slope[0] = __fmul_rn(step, inv0);
     slope[1] = -__fmul_rn(step, inv1);
 }
@@ -147,7 +155,7 @@ __device__ __forceinline__ void preference_finish(const PreferenceCall& a, const
     bad = __syncthreads_or(bad);
     auto finish = [&](float2 v) {
         if (threadIdx.x != 0) return;
-        *a.out_loss = bad ? CUDART_NAN_F : static_cast<float>(__dmul_rn(a.scale_per_pair, pair_value(v)));
+        *a.out_loss = bad ? CUDART_NAN_F : pair_mul(a.scale2, v).x;
         if (bad) report_status(a.status, RLK_ERR_INVALID_ARG);
     };
     // warp w of 16 takes losses 32 w + lane, + 512, ...; those without any would add zeros
@@ -534,10 +542,15 @@ int64_t preference_chunks(int64_t T, int64_t n_pairs) { return T / kChunk + 2 * 
 cudaError_t launch_preference_loss(const PreferenceArgs& args, int num_sms, cudaStream_t stream) {
     PreferenceCall a;
     static_cast<PreferenceArgs&>(a) = args;
-    a.beta32 = static_cast<float>(a.beta);
     a.smooth32 = static_cast<float>(a.label_smoothing);
     a.keep32 = static_cast<float>(1.0 - a.label_smoothing);
-    a.step32 = static_cast<float>(a.scale_per_pair);
+    // a beta or margin beyond fp32 is its largest number: it must not meet an infinite sum as one
+    const double largest = std::numeric_limits<float>::max();
+    auto bounded = [&](double v) { return split_two(v > largest ? largest : v < -largest ? -largest : v); };
+    a.beta2 = bounded(a.beta);
+    a.margin2 = bounded(a.margin);
+    a.half_over_beta2 = bounded(a.half_over_beta);
+    a.scale2 = split_two(a.scale_per_pair);
     if (a.n_pairs == 0) {
         if (a.grad && a.T > 0) {
             const cudaError_t e = cudaMemsetAsync(a.grad, 0, size_t(a.T) * sizeof(float), stream);

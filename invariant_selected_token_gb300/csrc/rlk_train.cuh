@@ -3,6 +3,7 @@
 // dispatcher and their kernels, and the device arithmetic they have in common.
 #pragma once
 
+#include <cmath>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -139,6 +140,14 @@ inline bool rmsnorm_backward_one_launch(int64_t T) { return T > 0 && T <= kRmsBw
 inline int rmsnorm_backward_ranges(int64_t T) { return T < kRmsBwdRanges ? static_cast<int>(T) : kRmsBwdRanges; }
 cudaError_t launch_rmsnorm_backward(const RmsBwdArgs& a, cudaStream_t stream);
 
+// A parameter as the sum of two floats (2^-48 relative), formed on the host: a conversion from fp64
+// on the device is as slow as fp64 itself.
+inline float2 split_two(double v) {
+    const float hi = static_cast<float>(v);
+    const float lo = std::isfinite(hi) ? static_cast<float>(v - static_cast<double>(hi)) : 0.0f;
+    return make_float2(hi, lo);
+}
+
 // ---------------------------------------------------------------- device arithmetic
 // a - b as the unevaluated sum of its rounded value and the rounding error, exactly
 // (Moller-Knuth two-sum); the error is 0 where the difference is not finite.
@@ -170,8 +179,13 @@ __device__ __forceinline__ float2 pair_add(float2 a, float2 b) {
     return fabsf(s) < CUDART_INF_F ? make_float2(hi, __fsub_rn(lo, __fsub_rn(hi, s))) : make_float2(s, 0.0f);
 }
 __device__ __forceinline__ float2 pair_of(float v) { return make_float2(v, 0.0f); }
-__device__ __forceinline__ double pair_value(float2 v) {
-    return __dadd_rn(static_cast<double>(v.x), static_cast<double>(v.y));
+__device__ __forceinline__ float2 pair_negated(float2 v) { return make_float2(-v.x, -v.y); }
+// Product of two such pairs, to about 2^-45; its first part is the product rounded to fp32.
+__device__ __forceinline__ float2 pair_mul(float2 a, float2 b) {
+    const float p = __fmul_rn(a.x, b.x);
+    const float e = __fmaf_rn(a.y, b.x, __fmaf_rn(a.x, b.y, __fmaf_rn(a.x, b.x, -p)));
+    const float hi = __fadd_rn(p, e);
+    return fabsf(p) < CUDART_INF_F ? make_float2(hi, __fsub_rn(e, __fsub_rn(hi, p))) : make_float2(p, 0.0f);
 }
 __device__ __forceinline__ float2 warp_sum(float2 v) {
     // not unrolled: a dependent chain either way, and small kernels pay for every line of code that
