@@ -85,6 +85,20 @@ def test_preference_loss_parity(rlk, cuda_device, T, offsets, kw, mask, ref):
     check(run(rlk, cuda_device, b, **kw), b, **kw)
 
 
+@pytest.mark.parametrize("beta,h", [(0.1, 10), (0.2, 5), (0.05, 20), (0.3, 4), (0.1, 9), (0.7, 2)])
+def test_hinge_of_whole_numbers(rlk, cuda_device, beta, h):
+    """Sums that are whole numbers may meet the border z = 1 exactly: the decision is that of beta
+    itself, not of its value in fp32."""
+    margin = round(beta * h - 1.0, 6)
+    lp = np.array([-1.0] * h + [-2.0] * h, np.float32)
+    b = dict(lp=lp, ref=np.full(2 * h, -1.5, np.float32), active=None, offsets=[0, h, 2 * h])
+    kw = dict(kind="hinge", beta=beta, margin=margin)
+    out = run(rlk, cuda_device, b, **kw)
+    z = beta * h - margin
+    assert out[3].any() == (z < 1.0)
+    check(out, b, **kw)
+
+
 @pytest.mark.parametrize("T,offsets", [CASES[2], CASES[4], CASES[6], CASES[7]])
 @pytest.mark.parametrize("layout", ["adjacent", "halves"])
 def test_the_loss_alone(rlk, cuda_device, T, offsets, layout):
