@@ -68,12 +68,12 @@ struct PreferenceArgs {
     int32_t* chunk_counts;
     int32_t* status;
 };
-// Largest batch that one cluster does alone: 9.6 us at one pair of 32768 tokens, where two
-// launches take 11.1; at 65536 12.6 against 11.4.
+// Largest batch that one cluster does alone: 9.2 us at one pair of 32768 tokens, where two
+// launches take 9.6; at 65536 12.1 against 9.8.
 constexpr int64_t kPreferenceClusterTokens = 32768;
 // Tokens a pair from which the path over all chunks is taken.  Against a team of up to 8 CTAs a
-// pair: 11.4 and 11.1 us at 32768 tokens, 11.2 and 12.5 at 50000, 11.6 and 16.8 at 100000 (one
-// pair); 13.5 and 11.8, 13.7 and 13.3 at 32768 and 50000 (four pairs).
+// pair: 9.7 and 9.6 us at 32768 tokens, 9.6 and 11.1 at 50000, 9.9 and 15.7 at 100000 (one pair);
+// 11.8 and 10.5, 11.9 and 12.1 at 32768 and 50000 (four pairs).
 constexpr int64_t kPreferenceSplitTokens = 40960;
 // Whether a batch takes the path over all chunks, and how many of them it has at most.
 bool preference_split(int64_t T, int64_t n_pairs);
@@ -132,9 +132,9 @@ struct RmsBwdArgs {
 // Ranges of rows whose grad_gamma sums are formed apart, a CTA per SM each.
 constexpr int kRmsBwdRanges = 152;
 // Rows that one cluster of 8 CTAs takes alone, grad_gamma and all: a launch less for the host (13.4
-// against 18.2 us a call at H = 4096) for little more time on the device (5.9 against 4.5 us at 16
+// against 18.2 us a call at H = 4096) for little more time on the device (5.6 against 4.3 us at 16
 // rows) as long as every team has one row; at 32 and 64 rows it would be 7.7 and 11.2 us against
-// 4.9 and 5.0 for the two launches.
+// 4.7 and 4.9 for the two launches.
 constexpr int64_t kRmsBwdClusterRows = 16;
 inline bool rmsnorm_backward_one_launch(int64_t T) { return T > 0 && T <= kRmsBwdClusterRows; }
 inline int rmsnorm_backward_ranges(int64_t T) { return T < kRmsBwdRanges ? static_cast<int>(T) : kRmsBwdRanges; }
