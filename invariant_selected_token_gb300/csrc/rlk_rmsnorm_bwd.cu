@@ -273,13 +273,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_rmsnorm_backward(const RmsBwdAr
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!a.grad_gamma) return;
-    // the range's sums: the teams' in ascending order.  The ring is empty and holds them.
+    // the range's sums: the teams' in ascending order.  The ring holds them, once every warp has
+    // read its last row out of it.
     float* const teams = reinterpret_cast<float*>(ring);
     float* const sums = teams + kThreads * 16;
     cg::cluster_group cluster = cg::this_cluster();
     const int ctas = static_cast<int>(cluster.num_blocks());
     float* const out = ctas > 1 ? sums : a.parts + static_cast<int64_t>(blockIdx.x) * a.H;
     if constexpr (kTeams == 1) {
+        if (ctas > 1) __syncthreads();  // `out` lies over other warps' pieces
 #pragma unroll
         for (int g = 0; g < 2; ++g)
             if (in[g]) store8<RLK_DTYPE_F32>(out, i0 + 256 * g, dg[g]);

@@ -68,6 +68,23 @@ def test_rmsnorm_backward_parity(rlk, cuda_device, T, H, go, gx, res):
     assert none is None and torch.equal(only, grad_x)
 
 
+@pytest.mark.parametrize("go,gx", [(F32, F32), (F32, BF16), (BF16, F32), (BF16, BF16)])
+@pytest.mark.parametrize("H", [4160, 8192])
+def test_wide_rows_in_one_cluster_keep_their_bits(rlk, cuda_device, H, go, gx):
+    """Up to 16 rows wider than 4096 features: the sums for grad_gamma lie where the rows' inputs
+    did, and no warp may put its own there before the slowest one has read its row.  grad_x has the
+    bits of the call that forms no such sums, and grad_gamma the same ones each time."""
+    for T in range(1, 17):
+        a = make(T, H, cuda_device, 100 * T + 1, go, gx)
+        call = lambda **kw: rlk.rmsnorm_backward(a["grad_out"], a["x"], a["gamma"],  # noqa: E731
+                                                 grad_residual=a["grad_residual"], grad_dtype=gx, **kw)
+        want, _ = call(want_gamma=False)
+        outs = [call() for _ in range(20)]
+        check(a, 1e-6, *outs[0])
+        for grad_x, grad_gamma in outs:
+            assert torch.equal(grad_x, want) and torch.equal(grad_gamma, outs[0][1])
+
+
 @pytest.mark.parametrize("eps,x_std", [(1e-5, 1e-4), (1.0, 0.1), (1e-6, 300.0)])
 def test_eps_and_scale(rlk, cuda_device, eps, x_std):
     a = make(40, 512, cuda_device, 5, x_std=x_std)
