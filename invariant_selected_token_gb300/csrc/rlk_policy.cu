@@ -92,14 +92,15 @@ struct TokenTerms {
 };
 
 // From d as two floats, r = e^d, u = ref - lp and (k3) e^u - 1 - u.  The two clips are one test:
-// with a negative advantage both d and the border change sign.
+// with a negative advantage both d and the border change sign.  An advantage of 0 or NaN is not
+// clipped.
 template <int kKl, bool kPlain>
 __device__ __forceinline__ TokenTerms token_terms(const PolicyCall& a, float2 d, float r, float u, float k3, float A) {
     TokenTerms o;
     const bool up = A > 0.0f;
     const float2 side = up ? d : make_float2(-d.x, -d.y);
     const float2 border = up ? a.log_high : make_float2(-a.log_low.x, -a.log_low.y);
-    bool shut = above(side, border) && A != 0.0f;
+    bool shut = above(side, border) && fabsf(A) > 0.0f;
     float held = shut ? (up ? a.ratio_high : a.ratio_low) : r;
     if (a.dual > 0.0f && A < 0.0f && above(d, a.log_dual)) {
         shut = true;

@@ -236,6 +236,30 @@ def test_extreme_ratios(rlk, cuda_device):
     assert abs(float(loss) - 5.6) <= 8 * U * 8 and not g[:3].any() and float(stats[2]) == 4.0
 
 
+@pytest.mark.parametrize("T", [6, 9000, 40000])  # every launch shape
+@pytest.mark.parametrize("per_seq", [False, True])
+def test_an_advantage_that_is_nan_reaches_its_own_gradient(rlk, cuda_device, T, per_seq):
+    """Whether the ratio lies below, within or above the clip's range; a NaN advantage is clipped
+    by neither side.  Nothing else of the batch changes but the sum."""
+    d = np.zeros(T, np.float32)
+    d[:6] = [-1.0, 0.0, 1.0, -1.0, 0.0, 1.0]
+    adv = np.ones(T, np.float32)
+    offsets = [0, 1, 2, 3, 4, 5, T]
+    kw = dict(reduction="sum", dual_clip=3.0, advantages_per_seq=per_seq,
+              seq_offsets=dev(offsets, cuda_device, np.int32))
+    lp, old = dev(d, cuda_device), dev(np.zeros(T, np.float32), cuda_device)
+    held = adv[:6] if per_seq else adv
+    _, clean_stats, clean = rlk.policy_loss(lp, old, dev(held, cuda_device), **kw)
+    for t in range(5):
+        bad = held.copy()
+        bad[t] = np.nan
+        loss, stats, grad = rlk.policy_loss(lp, old, dev(bad, cuda_device), **kw)
+        assert torch.isnan(loss) and torch.isnan(stats[0]) and torch.isnan(grad[t])
+        assert float(stats[2]) == float(clean_stats[2]) - (d[t] > 0) and stats[3] == clean_stats[3]
+        grad[t] = clean[t]
+        assert torch.equal(grad, clean)
+
+
 @pytest.mark.parametrize("offsets", [[0, 700, 600, 1000], [-1, 500, 1000, 1000], [0, 500, 900, 1001],
                                      [5, 2 ** 31 - 1, -2 ** 31, 1000]])
 @pytest.mark.parametrize("reduction", ["token_mean", "seq_mean"])
