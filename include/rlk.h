@@ -429,8 +429,10 @@ rlk_status_t rlk_rmsnorm_backward(const void* grad_out, int grad_out_dtype, cons
  *
  * A token takes part if its mask is nonzero and it lies in
  * [seq_offsets[0], seq_offsets[n_seqs]); any other token's inputs are not
- * used (they may be NaN) and its grad is 0; a value that is not finite of a
- * token that takes part goes into the loss and its own grad.  Per-token terms are fp32; their
+ * used (they may be NaN) and its grad is 0; a NaN of a token that takes part
+ * goes into the loss and its own grad, an infinity counts as the formulas say
+ * (a clipped ratio may be infinite; infinity times an advantage of 0 is NaN).
+ * Per-token terms are fp32; their
  * sums run over fixed ranges of 1024 tokens in fp32 and then as pairs of
  * floats, so the results are the same bits on every run.  T == 0 gives loss and stats 0.
  *

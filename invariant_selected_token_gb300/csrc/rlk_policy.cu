@@ -94,7 +94,7 @@ struct TokenTerms {
 // From d as two floats, r = e^d, u = ref - lp and (k3) e^u - 1 - u.  The two clips are one test:
 // with a negative advantage both d and the border change sign.  An advantage of 0 or NaN is not
 // clipped.
-template <int kKl, bool kPlain>
+template <int kKl>
 __device__ __forceinline__ TokenTerms token_terms(const PolicyCall& a, float2 d, float r, float u, float k3, float A) {
     TokenTerms o;
     const bool up = A > 0.0f;
@@ -106,8 +106,7 @@ __device__ __forceinline__ TokenTerms token_terms(const PolicyCall& a, float2 d,
         shut = true;
         held = a.dual;
     }
-    float s = __fmul_rn(held, A);
-    if (!kPlain && A == 0.0f && r == CUDART_INF_F) s = 0.0f;  // the ratio is finite, its fp32 value is not
+    const float s = __fmul_rn(held, A);
     o.policy = -s;
     o.clipped = shut ? 1.0f : 0.0f;
     o.neg_d = -d.x;
@@ -132,7 +131,10 @@ template <int kKl>
 __device__ __forceinline__ TokenTerms token_one(const PolicyCall& a, float lp, float old, float ref, float A) {
     const float2 d = two_diff(lp, old);
     const float u = __fsub_rn(ref, lp);
-    return token_terms<kKl, false>(a, d, ratio_of(d), u, kKl == RLK_KL_K3 ? exp_minus_1_minus(u) : 0.0f, A);
+    float r = ratio_of(d);
+    // a ratio that is finite but beyond fp32 makes nothing of an advantage of 0
+    if (A == 0.0f && r == CUDART_INF_F && fabsf(lp) < CUDART_INF_F && fabsf(old) < CUDART_INF_F) r = 1.0f;
+    return token_terms<kKl>(a, d, r, u, kKl == RLK_KL_K3 ? exp_minus_1_minus(u) : 0.0f, A);
 }
 
 // Two tokens, two per instruction as far as the values allow: |d| <= 80, where 2^n only adds to
@@ -173,8 +175,8 @@ __device__ __forceinline__ void token_two(const PolicyCall& a, const float (&lp)
         for (int i = 1; i < kExpTail; ++i) p = f2_fma(p, u2, f2_splat(exp_tail(i)));
         f2_unpack(f2_mul(f2_mul(u2, u2), p), k0, k1);
     }
-    o[0] = token_terms<kKl, true>(a, make_float2(d0, e0), r0, u0, k0, A[0]);
-    o[1] = token_terms<kKl, true>(a, make_float2(d1, e1), r1, u1, k1, A[1]);
+    o[0] = token_terms<kKl>(a, make_float2(d0, e0), r0, u0, k0, A[0]);
+    o[1] = token_terms<kKl>(a, make_float2(d1, e1), r1, u1, k1, A[1]);
 }
 
 // A lane's token, or four consecutive ones.  Everything is loaded before anything is used, inactive

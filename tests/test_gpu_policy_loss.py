@@ -260,6 +260,32 @@ def test_an_advantage_that_is_nan_reaches_its_own_gradient(rlk, cuda_device, T, 
         assert torch.equal(grad, clean)
 
 
+@pytest.mark.parametrize("T", [6, 9000, 40000])  # every launch shape
+def test_zero_advantages(rlk, cuda_device, T):
+    """A ratio that is finite but beyond fp32 makes nothing of an advantage of 0, and no token with
+    one is clipped; an old_logprob of -inf gives NaN as infinity times 0 does."""
+    lp, old = np.zeros(T, np.float32), np.zeros(T, np.float32)
+    old[:5] = [-200.0, 200.0, -1.0, 1.0, -2.0e38]
+    for adv in (0.0, -0.0):
+        a = np.full(T, adv, np.float32)
+        kw = dict(reduction="sum", dual_clip=3.0)
+        loss, stats, grad = rlk.policy_loss(dev(lp, cuda_device), dev(old, cuda_device), dev(a, cuda_device), **kw)
+        want = TR.policy_loss(lp[:4], old[:4], a[:4], **kw)  # beyond that e^d leaves fp64 too
+        assert float(loss) == want[0] == 0.0 and float(stats[2]) == want[1][2] == 0.0 and not grad.any()
+        # the largest finite values: the difference is beyond fp32, and still finite
+        far_lp, far = lp.copy(), old.copy()
+        far_lp[4], far[4] = 3.0e38, -3.0e38
+        loss, stats, grad = rlk.policy_loss(dev(far_lp, cuda_device), dev(far, cuda_device), dev(a, cuda_device), **kw)
+        assert float(loss) == 0.0 and float(stats[2]) == 0.0 and not grad.any()
+        for t in (0, 5):
+            inf = old.copy()
+            inf[t] = -np.inf
+            loss, stats, grad = rlk.policy_loss(dev(lp, cuda_device), dev(inf, cuda_device), dev(a, cuda_device), **kw)
+            assert torch.isnan(loss) and torch.isnan(grad[t]) and float(stats[2]) == 0.0
+            grad[t] = 0.0
+            assert not grad.any()
+
+
 @pytest.mark.parametrize("offsets", [[0, 700, 600, 1000], [-1, 500, 1000, 1000], [0, 500, 900, 1001],
                                      [5, 2 ** 31 - 1, -2 ** 31, 1000]])
 @pytest.mark.parametrize("reduction", ["token_mean", "seq_mean"])
