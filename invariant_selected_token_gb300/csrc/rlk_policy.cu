@@ -123,7 +123,7 @@ __device__ __forceinline__ TokenTerms token_terms(const PolicyCall& a, float2 d,
 // e^(d.x + d.y): the rest of d to first order.
 __device__ __forceinline__ float ratio_of(float2 d) {
     const float r = exp_any(d.x);
-    return r < 3.0e38f ? __fmaf_rn(r, d.y, r) : r;
+    return r < CUDART_INF_F ? __fmaf_rn(r, d.y, r) : r;
 }
 
 // One token.

@@ -286,6 +286,23 @@ def test_zero_advantages(rlk, cuda_device, T):
             assert not grad.any()
 
 
+@pytest.mark.parametrize("T", [6, 9000, 40000])  # every launch shape
+def test_ratios_next_to_the_largest_number(rlk, cuda_device, T):
+    """d = 88.62 .. 88.72, a large part of whose last bits lies in its second float: the ratio is as
+    exact as any other's, up to the largest fp32 number."""
+    n = 64
+    lp, old, adv = (np.zeros(T, np.float32) for _ in range(3))
+    k = min(T, n)
+    lp[:k] = np.linspace(88.62, 88.72, n)[:k]
+    old[:k] = (np.random.default_rng(15).random(n) * 2.0 ** -17)[:k]
+    adv[:k] = -1e-10
+    want = 1e-10 * np.exp(lp[:k].astype(np.float64) - old[:k])
+    _, _, grad = rlk.policy_loss(dev(lp, cuda_device), dev(old, cuda_device), dev(adv, cuda_device),
+                                 reduction="sum")
+    adv32 = float(np.float32(1e-10)) / 1e-10
+    assert np.all(np.abs(grad.cpu().numpy()[:k] - want * adv32) <= 12 * U * want)
+
+
 @pytest.mark.parametrize("offsets", [[0, 700, 600, 1000], [-1, 500, 1000, 1000], [0, 500, 900, 1001],
                                      [5, 2 ** 31 - 1, -2 ** 31, 1000]])
 @pytest.mark.parametrize("reduction", ["token_mean", "seq_mean"])
