@@ -432,9 +432,9 @@ rlk_status_t rlk_rmsnorm_backward(const void* grad_out, int grad_out_dtype, cons
  * used (they may be NaN) and its grad is 0; a NaN of a token that takes part
  * goes into the loss and its own grad, an infinity counts as the formulas say
  * (a clipped ratio may be infinite; infinity times an advantage of 0 is NaN).
- * Per-token terms are fp32; their
- * sums run over fixed ranges of 1024 tokens in fp32 and then as pairs of
- * floats, so the results are the same bits on every run.  T == 0 gives loss and stats 0.
+ * Per-token terms are fp32; their sums run over fixed ranges of 1024 tokens in
+ * fp32 and then as pairs of floats, so the results are the same bits on every
+ * run.  T == 0 gives loss and stats 0.
  *
  *   logprob, old_logprob  device, float [T]
  *   ref_logprob   device, float [T], or NULL (then kl_coef must be 0)
@@ -443,9 +443,11 @@ rlk_status_t rlk_rmsnorm_backward(const void* grad_out, int grad_out_dtype, cons
  *   seq_offsets   device, int32 [n_seqs + 1], ascending within [0, T], or NULL for one sequence
  *                 of all T tokens (n_seqs must be 1); offsets that are not ascending set
  *                 RLK_ERR_INVALID_ARG in *dev_status and make loss and stats NaN
- *   clip_low, clip_high  >= 0;  dual_clip  0 (off) or > 1;  kl_kind  RLK_KL_K1 .. RLK_KL_K3
+ *   clip_low, clip_high  >= 0;  dual_clip  0 (off) or > 1;  kl_kind  RLK_KL_K1 .. RLK_KL_K3;
+ *                 clip_low finite; clip_high, dual_clip, |kl_coef| and |scale| at most the
+ *                 largest fp32 number
  *   out_loss      device, float [1]
- *   kl_coef       finite; with 0 the KL term is only reported in out_stats
+ *   kl_coef       with 0 the KL term is only reported in out_stats
  *   out_stats     device, float [4]: sums (with weights w_t, without scale) of -s, of k, of the
  *                 clipped tokens and of old_logprob - logprob
  *   grad_logprob  device, float [T], or NULL for the loss alone
@@ -485,7 +487,8 @@ rlk_status_t rlk_policy_loss(const float* logprob, const float* old_logprob,
  *   ref_logprob   device, float [T], or NULL (no reference: its terms are 0)
  *   seq_offsets   device, int32 [2 * n_pairs + 1], ascending within [0, T], else
  *                 RLK_ERR_INVALID_ARG in *dev_status and loss NaN
- *   beta          > 0;  label_smoothing in [0, 1], 0 unless SIGMOID;  margin 0 with IPO
+ *   beta          > 0;  label_smoothing in [0, 1], 0 unless SIGMOID;  margin 0 with IPO;  beta,
+ *                 |margin| and |scale| at most the largest fp32 number
  *   out_loss      device, float [1];  out_pair_loss  device, float [n_pairs]
  *   out_rewards   device, float [2 * n_pairs]: beta m_q, in sequence order
  *   grad_logprob  device, float [T], or NULL; 0 for inactive tokens and those of no sequence

@@ -440,6 +440,9 @@ rlk_status_t backward_gemms(const void* hidden, const void* W, int64_t T, int64_
 }
 
 // ---------------------------------------------------------------- training-step operators
+// A parameter that the kernels can hold in fp32 (NaN and infinities are none).
+bool within_fp32(double v) { return std::fabs(v) <= double(std::numeric_limits<float>::max()); }
+
 struct PolicyLayout {
     size_t ticket, counts, parts, total;
 };
@@ -1082,9 +1085,9 @@ rlk_status_t rlk_policy_loss(const float* logprob, const float* old_logprob,
     if (!advantages && (advantages_per_seq ? n_seqs : T) > 0) return RLK_ERR_INVALID_ARG;
     if (!out_loss || !out_stats) return RLK_ERR_INVALID_ARG;
     if (!(clip_low >= 0.0) || !(clip_high >= 0.0) || !std::isfinite(clip_low) ||
-        !std::isfinite(clip_high) || !std::isfinite(kl_coef) || !std::isfinite(scale))
+        !within_fp32(clip_high) || !within_fp32(kl_coef) || !within_fp32(scale))
         return RLK_ERR_INVALID_ARG;
-    if (dual_clip != 0.0 && (!(dual_clip > 1.0) || !std::isfinite(dual_clip)))
+    if (dual_clip != 0.0 && (!(dual_clip > 1.0) || !within_fp32(dual_clip)))
         return RLK_ERR_INVALID_ARG;
     if (!ref_logprob && kl_coef != 0.0 && T > 0) return RLK_ERR_INVALID_ARG;
     if (kl_kind < RLK_KL_K1 || kl_kind > RLK_KL_K3) return RLK_ERR_UNSUPPORTED;
@@ -1156,7 +1159,7 @@ rlk_status_t rlk_preference_loss(const float* logprob, const float* ref_logprob,
     if (kind < RLK_PREF_SIGMOID || kind > RLK_PREF_IPO) return RLK_ERR_UNSUPPORTED;
     if (!seq_offsets || !out_loss || (T > 0 && !logprob)) return RLK_ERR_INVALID_ARG;
     if (n_pairs > 0 && (!out_pair_loss || !out_rewards)) return RLK_ERR_INVALID_ARG;
-    if (!(beta > 0.0) || !std::isfinite(beta) || !std::isfinite(margin) || !std::isfinite(scale))
+    if (!(beta > 0.0) || !within_fp32(beta) || !within_fp32(margin) || !within_fp32(scale))
         return RLK_ERR_INVALID_ARG;
     if (!(label_smoothing >= 0.0 && label_smoothing <= 1.0)) return RLK_ERR_INVALID_ARG;
     if ((kind != RLK_PREF_SIGMOID && label_smoothing != 0.0) ||

@@ -544,12 +544,10 @@ cudaError_t launch_preference_loss(const PreferenceArgs& args, int num_sms, cuda
     static_cast<PreferenceArgs&>(a) = args;
     a.smooth32 = static_cast<float>(a.label_smoothing);
     a.keep32 = static_cast<float>(1.0 - a.label_smoothing);
-    // a beta or margin beyond fp32 is its largest number: it must not meet an infinite sum as one
-    const double largest = std::numeric_limits<float>::max();
-    auto bounded = [&](double v) { return split_two(v > largest ? largest : v < -largest ? -largest : v); };
-    a.beta2 = bounded(a.beta);
-    a.margin2 = bounded(a.margin);
-    a.half_over_beta2 = bounded(a.half_over_beta);
+    a.beta2 = split_two(a.beta);
+    a.margin2 = split_two(a.margin);
+    // 1 / (2 beta) beyond fp32 is its largest number: it must not meet an infinite h as infinity
+    a.half_over_beta2 = split_two(fmin(a.half_over_beta, double(std::numeric_limits<float>::max())));
     a.scale2 = split_two(a.scale_per_pair);
     if (a.n_pairs == 0) {
         if (a.grad && a.T > 0) {
