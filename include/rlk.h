@@ -395,7 +395,7 @@ rlk_status_t rlk_rmsnorm(const void* x, const void* residual, const void* gamma,
  *   grad_out       device, [T][H] of grad_out_dtype (RLK_DTYPE_F32 -- rlk_linear_logprob_backward's
  *                  grad_hidden -- or RLK_DTYPE_BF16)
  *   x, gamma       device, bf16 [T][H] and [H]
- *   eps            as in the forward
+ *   eps            as in the forward, and a normal number (2^-126 or more)
  *   grad_residual  device, [T][H] of grad_x_dtype, or NULL
  *   grad_x         device, [T][H] of grad_x_dtype (RLK_DTYPE_F32 or RLK_DTYPE_BF16); may be
  *                  grad_residual, or grad_out where the types are the same

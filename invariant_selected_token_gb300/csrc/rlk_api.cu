@@ -1033,7 +1033,8 @@ rlk_status_t rlk_rmsnorm_backward(const void* grad_out, int grad_out_dtype, cons
     if ((grad_out_dtype != RLK_DTYPE_F32 && grad_out_dtype != RLK_DTYPE_BF16) ||
         (grad_x_dtype != RLK_DTYPE_F32 && grad_x_dtype != RLK_DTYPE_BF16))
         return RLK_ERR_UNSUPPORTED;
-    if (!(eps > 0.0f) || !(eps < 3.0e38f)) return RLK_ERR_INVALID_ARG;
+    // 1 / eps, the most that rstd^2 can be, has to be a number too
+    if (!(eps >= std::numeric_limits<float>::min()) || !(eps < 3.0e38f)) return RLK_ERR_INVALID_ARG;
     if (T > 0 && (!grad_out || !x || !gamma || !grad_x)) return RLK_ERR_INVALID_ARG;
     const size_t need = grad_gamma ? rlk_rmsnorm_backward_workspace_size(T, H) : 0;
     if (need > 0 && !workspace) return RLK_ERR_INVALID_ARG;

@@ -100,6 +100,14 @@ def test_zero_rows(rlk, cuda_device):
     assert torch.isfinite(grad_x).all()
 
 
+def test_zero_rows_with_the_smallest_eps(rlk, cuda_device):
+    a = make(9, 256, cuda_device, 17)
+    a["x"][::2] = 0
+    grad_x, grad_gamma = rlk.rmsnorm_backward(a["grad_out"], a["x"], a["gamma"], 2.0 ** -126)
+    check(a, 2.0 ** -126, grad_x, grad_gamma)
+    assert torch.isfinite(grad_x).all()
+
+
 def test_gradient_against_differences_of_the_forward(rlk, cuda_device):
     """Directional difference of sum dy * rmsnorm(x) along v.  The forward rounds y to bf16, so a
     difference of outputs errs by up to 2 * 2^-9 * |y| per element over 2h; with 64 rows of one

@@ -145,6 +145,14 @@ def test_rmsnorm_backward_refusals(L):
     assert L.rlk_rmsnorm_backward_workspace_size(17, 4096) >= 17 * 4096 * 4
 
 
+@pytest.mark.parametrize("eps,code", [(2.0 ** -149, INVALID), (2.0 ** -127, INVALID), (-1e-6, INVALID),
+                                      (2.0 ** -126, ALIGNMENT), (1e-6, ALIGNMENT)])
+def test_rmsnorm_backward_refuses_subnormal_eps(L, eps, code):
+    """A row of zeros has rstd^2 = 1 / eps, which would be infinite."""
+    assert L.rlk_rmsnorm_backward(0x10008, 0, 0x20000, 0x30000, eps, None, 100, 4096, 0x40000, 1,
+                                  0x50000, 0x60000, 1 << 20, None) == code
+
+
 def _arrays(ptrs, sizes, types):
     n = len(ptrs)
     return ((ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*sizes),
