@@ -387,8 +387,8 @@ rlk_status_t rlk_rmsnorm(const void* x, const void* residual, const void* gamma,
  * the gradient that reached residual_out from further on (NULL where there
  * is none); grad_x is then the gradient of both x and residual.  A row's
  * grad_x does not depend on the batch around it; grad_gamma is summed over
- * ranges of consecutive rows and then over the ranges, in an order that T,
- * H and the types fix.
+ * ranges of consecutive rows, in chains of 64 rows, and then over the ranges,
+ * in an order that T, H and the types fix.
  * (The blog's sections 3.3 and 4.2 ask for a backward with the forward's
  * numeric discipline; the strict-path table's "RMSNorm" row.)
  *

@@ -8,8 +8,9 @@
 //   grad_gamma_i = sum over rows of dy_i x_i rstd
 //
 // A row's grad_x does not depend on the batch around it.  grad_gamma is
-// summed over at most 152 ranges of consecutive rows, one CTA each, then over
-// the ranges by a second launch, in an order that T, H and the types fix.  Up
+// summed over at most 152 ranges of consecutive rows, one CTA each, in chains
+// of 64 rows a team, then over the ranges by a second launch, in an order that
+// T, H and the types fix.  Up
 // to kRmsBwdClusterRows rows one cluster of 8 CTAs does both in one launch.
 //
 // Element i = 256 g + 8 l + j is lane l's j-th value of column group g, as in
@@ -48,11 +49,17 @@ constexpr int kThreads = 512;
 template <int kWarps>
 constexpr bool kKeep = kWarps < 16;
 
+// A team's sums for grad_gamma move from registers to shared memory, 64 bytes a thread, every so
+// many rows: additions one after the other round alike where the rows are alike, and drift (2000
+// equal rows a team: 494 half-steps off, 25 so).
+constexpr int kChain = 64;
+constexpr size_t kHeldBytes = size_t(kThreads) * 16 * sizeof(float);
+
 // Stages of a thread's ring: as many, at most 4, as fit into 227 KB.
 template <int kGo, int kGx>
-constexpr int kStages = 232448 / (kThreads * 32 * (1 + kPieces<kGo> + kPieces<kGx>)) < 4
-                            ? 232448 / (kThreads * 32 * (1 + kPieces<kGo> + kPieces<kGx>))
-                            : 4;
+constexpr int kRoomFor = (232448 - int(kHeldBytes) - 256) / (kThreads * 32 * (1 + kPieces<kGo> + kPieces<kGx>));
+template <int kGo, int kGx>
+constexpr int kStages = kRoomFor<kGo, kGx> < 4 ? kRoomFor<kGo, kGx> : 4;
 
 template <int kType>
 __device__ __forceinline__ void store8(void* base, int64_t i, const uint64_t (&v)[4]) {
@@ -104,8 +111,10 @@ __device__ __forceinline__ void read_f32(uint4 (&w)[2], const uint4* own) {
 // range.  A warp copies its own features of the next kStages rows into its own part of a ring of
 // shared memory: the copies need no CTA-wide barrier, and they fly while the current row is
 // reduced.  The arithmetic runs two features per instruction, each lane of which rounds
-// like the scalar one.
-template <int kWarps, int kGo, int kGx>
+// like the scalar one.  kChained: a team may have more than one chain of rows (65536 x 8192 in bf16
+// 572 against 561 us without; instances of their own, since the same code for fewer rows took
+// 15.5 instead of 15.2 us at 8192 x 1024).
+template <int kWarps, int kGo, int kGx, bool kChained>
 __global__ void __launch_bounds__(kThreads, 1) k_rmsnorm_backward(const RmsBwdArgs a) {
     constexpr int kTeams = kThreads / 32 / kWarps, kN = kStages<kGo, kGx>;
     constexpr int kGroup = 1 + kPieces<kGo> + kPieces<kGx>;  // pieces of 8 features
@@ -158,7 +167,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_rmsnorm_backward(const RmsBwdAr
     for (int g = 0; g < 2; ++g)
         if (in[g]) gam[g][0] = *reinterpret_cast<const uint4*>(a.gamma + i0 + 256 * g);
     uint64_t dg[2][4] = {};
-    int64_t t = r0 + team;
+    ulonglong2* const held = reinterpret_cast<ulonglong2*>(ring + kN * 2 * kGroup * kThreads) + threadIdx.x;
+    auto add_held = [&] {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const ulonglong2 v = held[k * kThreads];
+            dg[k >> 1][2 * (k & 1)] = f2_add(v.x, dg[k >> 1][2 * (k & 1)]);
+            dg[k >> 1][2 * (k & 1) + 1] = f2_add(v.y, dg[k >> 1][2 * (k & 1) + 1]);
+        }
+    };
+    auto move_to_held = [&] {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            held[k * kThreads] = make_ulonglong2(dg[k >> 1][2 * (k & 1)], dg[k >> 1][2 * (k & 1) + 1]);
+            dg[k >> 1][2 * (k & 1)] = dg[k >> 1][2 * (k & 1) + 1] = 0;
+        }
+    };
+    if (kChained) move_to_held();  // zeros
+    int64_t t = r0 + team, chain_end = t + kChain * kTeams;
 #pragma unroll
     for (int k = 0; k < kN; ++k) fetch(t + k * kTeams, k);
     int slot = 0, stage = 0;
@@ -270,9 +296,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_rmsnorm_backward(const RmsBwdAr
         __syncwarp();
         fetch(t + kN * kTeams, stage);  // everything in this stage has been used
         stage = stage + 1 < kN ? stage + 1 : 0;
+        if (kChained && t + kTeams == chain_end) {
+            add_held();
+            move_to_held();
+            chain_end += kChain * kTeams;
+        }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!a.grad_gamma) return;
+    if (kChained) add_held();
     // the range's sums: the teams' in ascending order.  The ring holds them, once every warp has
     // read its last row out of it.
     float* const teams = reinterpret_cast<float*>(ring);
@@ -325,10 +357,11 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_gamma_sum(const float* parts, 
     if (c == 0) out[blockIdx.x * 32 + row] = s;
 }
 
-template <int kWarps, int kGo, int kGx>
-cudaError_t launch_types(const RmsBwdArgs& a, int blocks, cudaStream_t stream) {
+template <int kWarps, int kGo, int kGx, bool kChained>
+cudaError_t launch_chained(const RmsBwdArgs& a, int blocks, cudaStream_t stream) {
     constexpr size_t kSmem =
-        size_t(kStages<kGo, kGx>) * 2 * (1 + kPieces<kGo> + kPieces<kGx>) * kThreads * sizeof(uint4);
+        size_t(kStages<kGo, kGx>) * 2 * (1 + kPieces<kGo> + kPieces<kGx>) * kThreads * sizeof(uint4) +
+        (kChained ? kHeldBytes : 0);
     // once per device and kernel: the runtime keeps it, and asking each time costs the host 1 us
     static std::atomic<uint64_t> ready{0};
     int dev = 0;
@@ -336,8 +369,8 @@ cudaError_t launch_types(const RmsBwdArgs& a, int blocks, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
     if (!(ready.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(k_rmsnorm_backward<kWarps, kGo, kGx>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 int(kSmem));
+        e = cudaFuncSetAttribute(k_rmsnorm_backward<kWarps, kGo, kGx, kChained>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);
     }
@@ -353,7 +386,14 @@ cudaError_t launch_types(const RmsBwdArgs& a, int blocks, cudaStream_t stream) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = rmsnorm_backward_one_launch(a.T) && a.grad_gamma ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k_rmsnorm_backward<kWarps, kGo, kGx>, a);
+    return cudaLaunchKernelEx(&cfg, k_rmsnorm_backward<kWarps, kGo, kGx, kChained>, a);
+}
+
+template <int kWarps, int kGo, int kGx>
+cudaError_t launch_types(const RmsBwdArgs& a, int blocks, cudaStream_t stream) {
+    const bool chained = a.grad_gamma && (a.T + int64_t(blocks) - 1) / blocks > kChain * (kThreads / 32 / kWarps);
+    return chained ? launch_chained<kWarps, kGo, kGx, true>(a, blocks, stream)
+                   : launch_chained<kWarps, kGo, kGx, false>(a, blocks, stream);
 }
 
 template <int kWarps>

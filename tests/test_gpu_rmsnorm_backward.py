@@ -193,6 +193,23 @@ def test_more_than_2_31_bytes(rlk, cuda_device):
     assert np.all(np.abs(n64(gg) - n64(want_g)) <= tol)
 
 
+@pytest.mark.parametrize("T,H,go", [(304003, 4160, BF16), (2 ** 21 + 3, 64, F32), (400000, 2048, BF16)])
+def test_grad_gamma_of_many_rows(rlk, cuda_device, T, H, go):
+    """The same row of positive products T times, so that a long chain of additions would round the
+    same way each time and drift.  A chain has at most 64 rows (64 roundings), a team adds up one
+    sum per chain, at most 16 teams share a range, and 152 ranges follow."""
+    g = torch.Generator(device=cuda_device)
+    g.manual_seed(18)
+    row = lambda: torch.rand(1, H, generator=g, device=cuda_device) + 0.5  # noqa: E731
+    x1, dy1 = row().to(BF16), row().to(go)
+    x, dy = x1.expand(T, H).contiguous(), dy1.expand(T, H).contiguous()
+    _, gg = rlk.rmsnorm_backward(dy, x, torch.ones(H, dtype=BF16, device=cuda_device), grad_dtype=BF16)
+    teams = max(1, 16 // max(1, 1 << ((H - 1) // 512).bit_length()))
+    chains = -(-T // (152 * teams * 64))
+    want = T * (n64(dy1) * n64(x1) / np.sqrt((n64(x1) ** 2).mean() + 1e-6))[0]
+    assert np.all(np.abs(n64(gg) - want) <= (12 + 64 + chains + 1 + teams + 10) * U * want)
+
+
 def test_no_rows(rlk, cuda_device):
     x = torch.zeros((0, 128), dtype=BF16, device=cuda_device)
     gx, gg = rlk.rmsnorm_backward(x, x, torch.ones(128, dtype=BF16, device=cuda_device))
