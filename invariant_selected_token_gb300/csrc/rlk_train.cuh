@@ -199,9 +199,6 @@ __device__ __forceinline__ float2 warp_sum(float2 v) {
 __device__ __forceinline__ bool above(float2 d, float2 border) {
     return d.x > border.x || (d.x == border.x && d.y > border.y);
 }
-__device__ __forceinline__ bool below(float2 d, float2 border) {
-    return d.x < border.x || (d.x == border.x && d.y < border.y);
-}
 
 // exp over the whole fp32 range, NaN kept: the contract's reduction and polynomial (Cody-Waite,
 // degree-7 Taylor), scaled by 2^n in two factors so that n = 128 and subnormal results are
