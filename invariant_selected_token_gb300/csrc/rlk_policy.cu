@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(1024) k_policy_one(const PolicyCall a) {
 // ---------------------------------------------------------------- two launches
 // Each sequence's weight (seq_mean), or the active tokens in each block's share of the sequences
 // (token_mean); and the main kernel's ticket set to 0.  Long sequences are counted by a cluster
-// each: one of 1.77 M tokens by a single CTA took 25 us.
+// each.
 __global__ void __launch_bounds__(1024) k_policy_count(const PolicyCall a) {
     __shared__ int smem[32];
     __shared__ int counted;
@@ -647,6 +647,13 @@ __global__ void __launch_bounds__(kThreads, kMainCtasPerSm) k_policy_main(const 
     if (lane == 0) write_loss(a, s, kl, bad);
 }
 
+// Mean length from which a sequence is counted by a cluster of 8 CTAs of 1024 threads instead of
+// one CTA of 256.  A sequence mean's whole call: 26.1 against 24.4 us at 49152 tokens each, 22.0
+// against 22.7 at 58982 (1.77 M tokens in all); 10.5 against 10.3 at 32768, 10.3 against 12.3 at
+// 65536 (262144 in all); 20.9 against 123 for one sequence of 1.77 M.  The lengths themselves are
+// on the device: one long sequence among many short ones is counted by one CTA.
+constexpr int kClusterCountTokens = 49152;
+
 template <int kKl, int kCtas, int kPer>
 cudaError_t launch_one(const PolicyCall& a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
@@ -680,7 +687,7 @@ cudaError_t launch_kl(const PolicyCall& a, int num_sms, cudaStream_t stream) {
     else if (a.active && a.reduction == RLK_REDUCE_TOKEN_MEAN) rows = kPolicyCountBlocks;
     const int most = num_sms * 8;
     if (rows > most) rows = most;
-    const bool lengthy = a.active && a.reduction == RLK_REDUCE_SEQ_MEAN && a.n_seqs > 0 && a.T / a.n_seqs > 16384;
+    const bool lengthy = a.active && a.reduction == RLK_REDUCE_SEQ_MEAN && a.n_seqs > 0 && a.T / a.n_seqs > kClusterCountTokens;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.stream = stream;
