@@ -380,7 +380,7 @@ rlk_status_t rlk_rmsnorm(const void* x, const void* residual, const void* gamma,
  * residual_out where it added a residual, its x where it did not) and rstd the
  * forward's own (same tree, same rsqrt, same bits), per row
  *   up_i    = grad_out_i * gamma_i
- *   c       = rstd^2 / H * sum_i up_i * x_i           (fp32, pairwise over the features)
+ *   c       = rstd^2 / H * sum_i up_i * x_i           (fp32, chains of 8, then a tree)
  *   grad_x_i = rstd * (up_i - x_i * c) + grad_residual_i
  *   grad_gamma_i = sum over the rows of grad_out_i * x_i * rstd
  * in fp32, each grad_x element rounded once to its type.  grad_residual is

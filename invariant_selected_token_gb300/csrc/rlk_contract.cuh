@@ -111,9 +111,10 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
 // low bits of t directly: with t = 1.5 * 2^23 + n exactly, the scalar's
 // (bits(t) - bits(1.5 * 2^23) + 127) << 23 equals bits(t) * 2^23 + bits(1.0f)
 // modulo 2^32, because bits(1.5 * 2^23) * 2^23 vanishes modulo 2^32.
-// kUnderflow = false is for arguments known to lie in [-86, 0] (numbers, not
-// NaN): no select is needed, and since p is a normal number in [0.7, 1.5]
-// and n >= -124, p * 2^n is normal and exact, i.e. n added to p's exponent
+// kUnderflow = false is for arguments known to lie in [-86, 88] (numbers, not
+// NaN; the contract's own are at most 0, the policy loss's within +-80): no
+// select is needed, and since p is a normal number in [0.7, 1.5] and n lies in
+// [-124, 127], p * 2^n is normal and exact, i.e. n added to p's exponent
 // field -- bits(p) + bits(t) * 2^23 modulo 2^32 (same reasoning as for the
 // scale) -- an integer shift and add instead of forming 2^n and
 // multiplying.  The shift is a funnel shift, which runs on the integer ALU
