@@ -26,11 +26,14 @@
 // sum of the absolute terms, next to the dozen that each term has.  The units
 // are added as pairs of floats.
 //
-// What bounds it.  Up to some 10^5 tokens latency: 4.0 us a call on the device
-// at 512 tokens, 5.4 at 8192, of which one launch, one round trip to memory
-// and the first fetch of the code make most.  At 1.77 M tokens (37 MB, 5.6 us
-// of HBM) 15.4 us: 2 us of the counting launch that nothing hides, 3 of the last
-// CTA's tail, and instructions, two tokens in one where the values allow.  Sums in fp64
+// What bounds it: latency.  4.0 us a call on the device at 512 tokens, 5.4 at
+// 8192, of which one launch, one round trip to memory and the first fetch of
+// the code make most.  At 1.77 M tokens (37 MB, 5.6 us of HBM) 15.4 us: 2 us of
+// the counting launch that nothing hides, 3 of the last CTA's tail, and between
+// them three units a CTA, each load, terms, barrier one after the other.  Its 8
+// warps a scheduler use 56 % of the issue slots (cold caches); for every issue
+// 3.8 warps wait for a load, 2.0 for an operation's fixed latency, 1.8 at the
+// unit's barrier, 0.9 for a full pipe.  Sums in fp64
 // instead of pairs of floats made it 27, the branching form of a token 23, a
 // look-up of both ends of a warp's span and of every token 19.7, tokens loaded one
 // by one 18.8 us.
