@@ -444,7 +444,7 @@ rlk_status_t rlk_rmsnorm_backward(const void* grad_out, int grad_out_dtype, cons
  *                 of all T tokens (n_seqs must be 1); offsets that are not ascending set
  *                 RLK_ERR_INVALID_ARG in *dev_status and make loss and stats NaN
  *   clip_low, clip_high  >= 0;  dual_clip  0 (off) or > 1;  kl_kind  RLK_KL_K1 .. RLK_KL_K3;
- *                 clip_low finite; clip_high, dual_clip, |kl_coef| and |scale| at most the
+ *                 all finite (a large one clips nothing);  |kl_coef| and |scale| at most the
  *                 largest fp32 number
  *   out_loss      device, float [1]
  *   kl_coef       with 0 the KL term is only reported in out_stats

@@ -1086,9 +1086,9 @@ rlk_status_t rlk_policy_loss(const float* logprob, const float* old_logprob,
     if (!advantages && (advantages_per_seq ? n_seqs : T) > 0) return RLK_ERR_INVALID_ARG;
     if (!out_loss || !out_stats) return RLK_ERR_INVALID_ARG;
     if (!(clip_low >= 0.0) || !(clip_high >= 0.0) || !std::isfinite(clip_low) ||
-        !within_fp32(clip_high) || !within_fp32(kl_coef) || !within_fp32(scale))
+        !std::isfinite(clip_high) || !within_fp32(kl_coef) || !within_fp32(scale))
         return RLK_ERR_INVALID_ARG;
-    if (dual_clip != 0.0 && (!(dual_clip > 1.0) || !within_fp32(dual_clip)))
+    if (dual_clip != 0.0 && (!(dual_clip > 1.0) || !std::isfinite(dual_clip)))
         return RLK_ERR_INVALID_ARG;
     if (!ref_logprob && kl_coef != 0.0 && T > 0) return RLK_ERR_INVALID_ARG;
     if (kl_kind < RLK_KL_K1 || kl_kind > RLK_KL_K3) return RLK_ERR_UNSUPPORTED;

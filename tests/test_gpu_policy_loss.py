@@ -303,6 +303,18 @@ def test_ratios_next_to_the_largest_number(rlk, cuda_device, T):
     assert np.all(np.abs(grad.cpu().numpy()[:k] - want * adv32) <= 12 * U * want)
 
 
+@pytest.mark.parametrize("T", [6, 9000, 40000])  # every launch shape
+def test_clip_limits_beyond_fp32_clip_nothing(rlk, cuda_device, T):
+    b = batch(T, [0, T], seed=16, mask=1.0, spread=2.0)
+    args = [dev(b[k], cuda_device) for k in ("lp", "old", "adv_t")]
+    for big in (1e39, 1e308):
+        loss, stats, grad = rlk.policy_loss(*args, clip_low=big, clip_high=big, dual_clip=big, reduction="sum")
+        ref = TR.policy_loss(b["lp"], b["old"], b["adv_t"], clip_low=1e30, clip_high=1e30, reduction="sum")
+        g_tol, s_tol = bounds(b, ref, False, False, "k3", 0.0, 1.0)
+        assert float(stats[2]) == 0.0 and np.all(np.abs(grad.cpu().numpy() - ref[2]) <= g_tol)
+        assert abs(float(loss) - ref[0]) <= s_tol[0] + U * abs(ref[0])
+
+
 @pytest.mark.parametrize("offsets", [[0, 700, 600, 1000], [-1, 500, 1000, 1000], [0, 500, 900, 1001],
                                      [5, 2 ** 31 - 1, -2 ** 31, 1000]])
 @pytest.mark.parametrize("reduction", ["token_mean", "seq_mean"])

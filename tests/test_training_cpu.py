@@ -95,8 +95,7 @@ def test_preference_loss_refusals(L):
 
 
 @pytest.mark.parametrize("name,kw", [
-    ("scale", {}), ("klc", {}), ("ch", {}), ("dual", {}), ("scale", dict(preference=True)),
-    ("beta", dict(preference=True)), ("margin", dict(preference=True))])
+    ("scale", {}), ("klc", {}), ("scale", dict(preference=True)), ("beta", dict(preference=True)), ("margin", dict(preference=True))])
 def test_loss_parameters_beyond_fp32_are_refused(L, name, kw):
     """The kernels hold them in fp32, where they would be infinite: 0 times such a scale is NaN.
     The largest fp32 number itself passes this check (and the call fails at a later one)."""
@@ -109,15 +108,15 @@ def test_loss_parameters_beyond_fp32_are_refused(L, name, kw):
             return L.rlk_preference_loss(0x1000, 0x2000, 0x3000, 0x4000, 3, 10, 0, 0, a["beta"], 0.0,
                                          a["margin"], 0, a["scale"], 0x5000, 0x6000, 0x7000, 0x8001,
                                          None, 0, None, None)
-        a = dict(ch=0.2, dual=0.0, klc=0.1, scale=1.0)
+        a = dict(klc=0.1, scale=1.0)
         a[name] = value
         return L.rlk_policy_loss(0x1000, 0x2000, 0x3000, 0x4000, 0, 0x5000, 0x6000, 2, 100, 0.2,
-                                 a["ch"], a["dual"], 3, a["klc"], 1, a["scale"], 0x7000, 0x8000,
+                                 0.2, 0.0, 3, a["klc"], 1, a["scale"], 0x7000, 0x8000,
                                  0x9001, None, 0, None, None)
     for sign in (1.0, -1.0) if name in ("scale", "klc", "margin") else (1.0,):
         assert call(sign * 1.0001 * top) == INVALID and call(sign * 1e300) == INVALID
         assert call(sign * top) == ALIGNMENT  # of the misplaced grad_logprob
-    assert call(0.5 if name != "dual" else 1.5) == ALIGNMENT
+    assert call(0.5) == ALIGNMENT
 
 
 def test_rmsnorm_backward_refusals(L):
