@@ -545,6 +545,180 @@ rlk_status_t rlk_grad_clip(const void* const* grads, void* const* outs, const in
                            size_t workspace_bytes, int32_t* dev_status, rlk_stream_t stream);
 
 /*
+ * Activation checkpoints in 8 bits.  A row's features lie in blocks of 32 that
+ * share a power of two, kept as one byte; with b the block's byte and c a
+ * feature's code, the feature is
+ *   RLK_SAVED_INT8   c * 2^(b - 133), c in -127 .. 127
+ *   RLK_SAVED_E4M3   c * 2^(b - 127), c an e4m3 number (4 exponent, 3 mantissa bits, no infinities)
+ * (the shared-exponent blocks of the OCP microscaling formats).  Every such
+ * value is a bf16 number, so restoring a checkpoint rounds nothing.
+ * rlk_act_quantize takes, with e the exponent of the block's largest
+ * magnitude m = f 2^e, b = e + 127 (INT8) and b = e + 119, one more where f >
+ * 1.75 (E4M3; not below 0), and rounds each feature to the nearest code, ties
+ * to the even one: within half a step, that is 2^-7 of 2^e (INT8), and 2^-4 of
+ * the feature or 2^-10 of 2^(b - 127) (E4M3).  At e = 127 magnitudes above 1.75 * 2^127 become that
+ * (E4M3).  A block with an infinity or NaN gets b = 255 and comes back as NaN throughout.
+ *
+ *   x, out       device, bf16 [T][H], 16-byte aligned
+ *   format       RLK_SAVED_INT8 or RLK_SAVED_E4M3
+ *   codes        device, one byte a feature [T][H], 16-byte aligned
+ *   scales       device, uint8 [T][H / 32]
+ *   H            multiple of 64, at most 2^20
+ * Codes that the quantiser does not write (INT8 -128, E4M3 0x7F and 0xFF) are taken as -128 and
+ * +-480.
+ */
+#define RLK_SAVED_BF16 0              /* not a checkpoint: the bf16 tensor itself */
+#define RLK_SAVED_INT8 1
+#define RLK_SAVED_E4M3 2
+rlk_status_t rlk_act_quantize(const void* x, int format, int64_t T, int64_t H, void* codes,
+                              uint8_t* scales, rlk_stream_t stream);
+rlk_status_t rlk_act_dequantize(const void* codes, const uint8_t* scales, int format, int64_t T,
+                                int64_t H, void* out, rlk_stream_t stream);
+
+/*
+ * The norms before and after a block of the trunk, with the block's gate and
+ * the residual stream's scales, in one pass (the strict-path table's
+ * "RMSNorm" row with its residual add, for trunks that norm a block's output
+ * too or scale and gate it).  Per row, in fp32:
+ *   n   = block * rstd(block) * gamma_post       (block itself where gamma_post is NULL)
+ *   x'  = bf16_RN(fma(residual_scale, residual, block_scale * (n * gate(g))))
+ *   out = rlk_rmsnorm of x' with gamma_pre, the same bits
+ * with rstd as in rlk_rmsnorm and gate(g) = 1, g or 1 / (1 + e^-g).  Without
+ * gamma_post and gate, and with both scales 1, x' too has rlk_rmsnorm's bits.
+ * A row's result does not depend on the batch around it.
+ *
+ * With saved_format RLK_SAVED_INT8 or RLK_SAVED_E4M3 the pass also stores
+ * checkpoints (rlk_act_quantize's, the same bits) of what the backward needs:
+ * x', and where codes and scales are given, block and gate.
+ *
+ *   block, residual  device, bf16 [T][H];  gate  device, bf16 [T][H], or NULL
+ *   gate_kind        RLK_GATE_IDENTITY or RLK_GATE_SIGMOID (of no effect without a gate)
+ *   gamma_post       device, bf16 [H], or NULL;  gamma_pre  device, bf16 [H]
+ *   residual_scale, block_scale  finite;  eps  > 0, of both norms
+ *   out, residual_out  device, bf16 [T][H]: the normed rows and x'
+ *   saved_x          {codes, scales} of x';  saved_block, saved_gate  of block and gate, both
+ *                    NULL where not wanted;  none of them with RLK_SAVED_BF16
+ *   H                multiple of 64, at most 8192; every pointer but scales 16-byte aligned
+ * residual_out may be residual, and out may be block (in place); no other overlap is allowed.
+ */
+#define RLK_GATE_IDENTITY 1
+#define RLK_GATE_SIGMOID 2
+rlk_status_t rlk_block_norm(const void* block, const void* gamma_post, const void* gate,
+                            int gate_kind, const void* residual, float residual_scale,
+                            float block_scale, const void* gamma_pre, float eps, int64_t T,
+                            int64_t H, void* out, void* residual_out, int saved_format,
+                            void* saved_x, uint8_t* saved_x_scales, void* saved_block,
+                            uint8_t* saved_block_scales, void* saved_gate,
+                            uint8_t* saved_gate_scales, rlk_stream_t stream);
+
+/*
+ * Backward of rlk_block_norm.  With dx the gradient of x',
+ *   dx            = rlk_rmsnorm_backward(grad_out; x', gamma_pre) + grad_residual_out
+ *   grad_residual = residual_scale * dx
+ *   dn            = block_scale * dx
+ *   grad_gate     = dn * n * gate'(g)
+ *   grad_block    = rmsnorm_backward(dn * gate(g); block, gamma_post), or dn * gate(g) itself
+ *                   where gamma_post is NULL
+ * and both norms' grad_gamma, in fp32, each gradient of the batch rounded once to
+ * its type.  x, block and gate are bf16 tensors (saved_format RLK_SAVED_BF16, scales
+ * NULL) or checkpoints, all three alike; from a checkpoint the call has the bits that it has from the
+ * restored tensor.  A row's gradients do not depend on the batch around it; the grad_gammas are
+ * summed over ranges of consecutive rows, in chains of 64 rows, and then over the ranges, in an
+ * order that T and H fix.
+ *
+ *   grad_out       device, [T][H] of grad_out_dtype (RLK_DTYPE_F32 or RLK_DTYPE_BF16)
+ *   grad_residual_out  device, [T][H] of grad_dtype: the gradient that reached x' from further
+ *                  on, or NULL
+ *   x              x' as the forward stored it
+ *   block, gate    as in the forward; block is not read, and may be NULL, where gamma_post and
+ *                  gate are NULL
+ *   grad_residual, grad_block, grad_gate  device, [T][H] of grad_dtype (RLK_DTYPE_F32 or
+ *                  RLK_DTYPE_BF16), each NULL where not wanted (grad_gate where there is no gate)
+ *   grad_gamma_pre, grad_gamma_post  device, float [H], or NULL; all zeros when T == 0
+ *   eps            as in the forward, and a normal number (2^-126 or more)
+ *   workspace      >= rlk_block_norm_backward_workspace_size(T, H) bytes, 256-byte aligned;
+ *                  nothing is needed when both grad_gammas are NULL
+ *   H              multiple of 64, at most 8192; every pointer but scales 16-byte aligned
+ * grad_residual may be grad_residual_out, or one of the three gradients grad_out where the types
+ * are the same; no other overlap is allowed.
+ */
+size_t rlk_block_norm_backward_workspace_size(int64_t T, int64_t H);
+rlk_status_t rlk_block_norm_backward(
+    const void* grad_out, int grad_out_dtype, const void* grad_residual_out, int saved_format,
+    const void* x, const uint8_t* x_scales, const void* block, const uint8_t* block_scales,
+    const void* gate, const uint8_t* gate_scales, int gate_kind, const void* gamma_post,
+    const void* gamma_pre, float residual_scale, float block_scale, float eps, int64_t T,
+    int64_t H, void* grad_residual, void* grad_block, void* grad_gate, int grad_dtype,
+    float* grad_gamma_pre, float* grad_gamma_post, void* workspace, size_t workspace_bytes,
+    rlk_stream_t stream);
+
+/*
+ * rlk_rmsnorm_backward from an 8-bit checkpoint of x: grad_x has the bits of
+ * that call on the restored tensor; grad_gamma is its sum in this call's order
+ * (as rlk_block_norm_backward's).
+ *   format, codes, scales  rlk_act_quantize's
+ *   workspace      >= rlk_block_norm_backward_workspace_size(T, H) bytes, 256-byte aligned;
+ *                  nothing is needed when grad_gamma is NULL
+ * Other arguments as rlk_rmsnorm_backward.
+ */
+rlk_status_t rlk_rmsnorm_backward_q8(const void* grad_out, int grad_out_dtype, int format,
+                                     const void* codes, const uint8_t* scales, const void* gamma,
+                                     float eps, const void* grad_residual, int64_t T, int64_t H,
+                                     void* grad_x, int grad_x_dtype, float* grad_gamma,
+                                     void* workspace, size_t workspace_bytes,
+                                     rlk_stream_t stream);
+
+/*
+ * Verification of drafted tokens against the target's probabilities, from
+ * given random numbers, with the strict logprob of every token it emits (the
+ * rollout's side of the logprobs that training recomputes).  Sequence s has
+ * n_s = draft_offsets[s + 1] - draft_offsets[s] drafted tokens, which may be
+ * none, and n_s + 1 rows of target logits, from row draft_offsets[s] + s on: row i of them is
+ * the target's distribution for the token at place i.  With p_i = softmax of that row and q_i the
+ * draft's distribution, e^(draft_logits - draft_lse),
+ *   the i-th drafted token x_i is accepted where all before it were and u_i q_i(x_i) < p_i(x_i);
+ *   at the first one that is not (place i), the token is argmax_v max(p_i(v) - q_i(v), 0) / e(v);
+ *   behind the last accepted draft (i = n_s), it is argmax_v p_i(v) / e(v)
+ * with u the call's uniform numbers and e the sequence's noise.  With u uniform in
+ * [0, 1) and e exponentially distributed the emitted tokens are distributed as the
+ * target's own.  Without draft_logits the draft is certain of its tokens: q_i(x_i) = 1, 0 elsewhere.
+ * Ties go to the lowest token; where p_i exceeds q_i nowhere the token is drawn from p_i.
+ * p is formed from the contract's (m, s) pair of the row and decisions do not depend on the batch;
+ * a token's logprob has the bits that rlk_logits_logprob gives for that row and token.
+ *
+ *   target_logits  device, [n_draft + n_seqs][ld_target] of target_dtype (RLK_DTYPE_F32 or
+ *                  RLK_DTYPE_BF16), aligned to its element size; columns [0, V) are read
+ *   draft_logits   device, [n_draft][ld_draft] of draft_dtype, or NULL (certain drafts)
+ *   draft_lse      device, float [n_draft] (rlk_logits_logprob's out_lse of the drafting step),
+ *                  or NULL: draft_logits are log-probabilities (rlk_log_softmax's out)
+ *   draft_tokens   device, int32 [n_draft];  uniforms  device, float [n_draft]
+ *   noise          device, float [n_seqs][ld_noise], positive; columns [0, V) are read
+ *   draft_offsets  device, int32 [n_seqs + 1], ascending within [0, n_draft]
+ *   active_mask    device, uint8 [n_seqs] (nonzero = active), or NULL; an inactive sequence
+ *                  gets out_accepted 0, tokens -1 and logprobs 0, whatever its inputs hold
+ *   out_accepted   device, int32 [n_seqs]: how many drafts were accepted
+ *   out_tokens     device, int32 [n_draft + n_seqs], rows as target_logits: the accepted drafts,
+ *                  the drawn token, then -1
+ *   out_logprob    device, float [n_draft + n_seqs]: of those tokens, 0 behind the drawn one
+ *   workspace      >= rlk_draft_verify_workspace_size(n_draft, n_seqs, V) bytes, 256-byte aligned
+ * A drafted token outside [0, V) is not accepted, and reports RLK_ERR_TARGET_RANGE where it is
+ * the first one refused.  A row that has to be drawn from and whose sum is not a number
+ * (a NaN or +infinity in it, or nothing but -infinity) or that has no positive weight gives token -1, logprob NaN and
+ * RLK_ERR_NONFINITE.  A sequence whose offsets descend or leave [0, n_draft] gets
+ * out_accepted -1 and reports RLK_ERR_INVALID_ARG; its tokens are not written (and no row of the outputs
+ * that belongs to no sequence is).  n_seqs == 0 is a no-op.
+ */
+size_t rlk_draft_verify_workspace_size(int64_t n_draft, int64_t n_seqs, int64_t V);
+rlk_status_t rlk_draft_verify(const void* target_logits, int target_dtype, int64_t ld_target,
+                              const int32_t* draft_tokens, const void* draft_logits,
+                              int draft_dtype, int64_t ld_draft, const float* draft_lse,
+                              const float* uniforms, const float* noise, int64_t ld_noise,
+                              const int32_t* draft_offsets, const uint8_t* active_mask,
+                              int64_t n_draft, int64_t n_seqs, int64_t V, int32_t* out_accepted,
+                              int32_t* out_tokens, float* out_logprob, void* workspace,
+                              size_t workspace_bytes, int32_t* dev_status, rlk_stream_t stream);
+
+/*
  * Same result as rlk_linear_logprob (same kernels, same bits), for callers
  * that cannot allocate device memory when they call: e.g. a rollout engine
  * that reserved almost all GPU memory for its KV cache at start-up, or a

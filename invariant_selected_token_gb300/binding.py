@@ -14,7 +14,7 @@ import ctypes
 import functools
 import operator
 import os
-from typing import List, Optional, Sequence, Tuple
+from typing import List, NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
 
@@ -40,7 +40,9 @@ EXPORTED = ["rlk_contract_id", "rlk_build_fingerprint", "rlk_status_string", "rl
             "rlk_linear_logprob_backward_from_logits", "rlk_rmsnorm_backward_workspace_size",
             "rlk_rmsnorm_backward", "rlk_policy_loss_workspace_size", "rlk_policy_loss",
             "rlk_preference_loss", "rlk_preference_loss_workspace_size", "rlk_grad_norm_workspace_size", "rlk_grad_norm",
-            "rlk_grad_clip"]
+            "rlk_grad_clip", "rlk_act_quantize", "rlk_act_dequantize", "rlk_block_norm",
+            "rlk_block_norm_backward_workspace_size", "rlk_block_norm_backward",
+            "rlk_rmsnorm_backward_q8", "rlk_draft_verify_workspace_size", "rlk_draft_verify"]
 DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
@@ -125,6 +127,27 @@ def lib() -> ctypes.CDLL:
         L.rlk_grad_norm.argtypes = [P, P, P, i64, P, P, sz, P, P]
         L.rlk_grad_clip.restype = i32
         L.rlk_grad_clip.argtypes = [P, P, P, P, i64, dbl, P, P, P, sz, P, P]
+        f32 = ctypes.c_float
+        L.rlk_act_quantize.restype = i32
+        L.rlk_act_quantize.argtypes = [P, i32, i64, i64, P, P, P]
+        L.rlk_act_dequantize.restype = i32
+        L.rlk_act_dequantize.argtypes = [P, P, i32, i64, i64, P, P]
+        L.rlk_block_norm.restype = i32
+        L.rlk_block_norm.argtypes = [P, P, P, i32, P, f32, f32, P, f32, i64, i64, P, P, i32, P, P, P,
+                                     P, P, P, P]
+        L.rlk_block_norm_backward_workspace_size.restype = sz
+        L.rlk_block_norm_backward_workspace_size.argtypes = [i64, i64]
+        L.rlk_block_norm_backward.restype = i32
+        L.rlk_block_norm_backward.argtypes = [P, i32, P, i32, P, P, P, P, P, P, i32, P, P, f32, f32,
+                                              f32, i64, i64, P, P, P, i32, P, P, P, sz, P]
+        L.rlk_rmsnorm_backward_q8.restype = i32
+        L.rlk_rmsnorm_backward_q8.argtypes = [P, i32, i32, P, P, P, f32, P, i64, i64, P, i32, P, P, sz,
+                                              P]
+        L.rlk_draft_verify_workspace_size.restype = sz
+        L.rlk_draft_verify_workspace_size.argtypes = [i64, i64, i64]
+        L.rlk_draft_verify.restype = i32
+        L.rlk_draft_verify.argtypes = [P, i32, i64, P, P, i32, i64, P, P, P, i64, P, P, i64, i64, i64,
+                                       P, P, P, P, sz, P, P]
         _lib = L
     return _lib
 
@@ -823,6 +846,318 @@ def clip_grads(grads: Sequence[torch.Tensor], max_norm: float,
                            scale.data_ptr(), p_ws, ws_n, a_status, _raw_stream(dev.index)),
            "rlk_grad_clip")
     return norm, scale
+
+
+# ----------------------------------------------------------------- 8-bit checkpoints, block norms
+class Saved(NamedTuple):
+    """An activation checkpoint in 8 bits: codes [T, H] (int8 or float8_e4m3fn) and a scale byte
+    per 32 features, uint8 [T, H / 32]."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+class SavedBlock(NamedTuple):
+    """What block_norm saved for its backward; None where that does not need it."""
+    x: Optional[Saved]
+    block: Optional[Saved]
+    gate: Optional[Saved]
+
+
+class BlockNormGrads(NamedTuple):
+    """block_norm_backward's gradients, None where there is none or none was wanted."""
+    grad_block: Optional[torch.Tensor]
+    grad_residual: Optional[torch.Tensor]
+    grad_gate: Optional[torch.Tensor]
+    grad_gamma_pre: Optional[torch.Tensor]
+    grad_gamma_post: Optional[torch.Tensor]
+
+
+SAVED_FORMATS = {"int8": 1, "e4m3": 2}
+SAVED_DTYPES = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
+_SAVED_CODES = {torch.int8: 1, torch.float8_e4m3fn: 2}
+GATE_KINDS = {"identity": 1, "sigmoid": 2}
+
+
+def _gate_code(gate, kind: str) -> int:
+    """"none" may stand for the kind where there is no gate."""
+    return 1 if gate is None and kind == "none" else _choice(GATE_KINDS, kind, "gate_kind")
+
+
+def _new_saved(fmt: str, device, shape) -> Saved:
+    T, H = shape
+    return Saved(torch.empty(shape, dtype=SAVED_DTYPES[fmt], device=device),
+                 torch.empty((T, H // 32), dtype=torch.uint8, device=device))
+
+
+def _saved_addrs(s, name: str, index: int, shape):
+    """(format, address, scales' address) of a bf16 tensor or of a checkpoint."""
+    if isinstance(s, torch.Tensor):
+        return 0, _addr(s, torch.bfloat16, name, index, shape), None
+    if not isinstance(s, Saved) or not isinstance(s.codes, torch.Tensor):
+        raise TypeError("%s must be a bfloat16 tensor or a Saved checkpoint" % name)
+    fmt = _SAVED_CODES.get(s.codes.dtype)
+    if fmt is None:
+        raise TypeError("%s.codes must be int8 or float8_e4m3fn" % name)
+    return (fmt, _addr(s.codes, s.codes.dtype, name + ".codes", index, shape),
+            _addr(s.scales, torch.uint8, name + ".scales", index, (shape[0], shape[1] // 32)))
+
+
+def act_quantize(x: torch.Tensor, fmt: str = "int8", out: Optional[Saved] = None,
+                 stream=None) -> Saved:
+    """8-bit checkpoint of a bf16 tensor [T, H]: blocks of 32 features share a power of two; codes
+    are int8 (within 1/128 of the block's largest power of two) or e4m3 (within 1/16 of each
+    feature).  out: a checkpoint to write over."""
+    _require(x, torch.bfloat16, "x", ndim=2)
+    dev = x.device
+    code = _choice(SAVED_FORMATS, fmt, "fmt")
+    if _elsewhere(dev, stream):
+        with _context(dev, stream):
+            return act_quantize(x, fmt, out)
+    T, H = x.shape
+    if out is None:
+        out = _new_saved(fmt, dev, x.shape)
+    got, a_codes, a_scales = _saved_addrs(out, "out", dev.index, x.shape)
+    if got != code:
+        raise TypeError("out must hold %s codes" % fmt)
+    _check(lib().rlk_act_quantize(x.data_ptr(), code, T, H, a_codes, a_scales, _raw_stream(dev.index)),
+           "rlk_act_quantize")
+    return out
+
+
+def act_dequantize(saved: Saved, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The bf16 tensor [T, H] that a checkpoint stands for (exactly: nothing is rounded)."""
+    if not isinstance(saved, Saved) or not isinstance(saved.codes, torch.Tensor):
+        raise TypeError("saved must be a Saved checkpoint")
+    _require(saved.codes, saved.codes.dtype, "saved.codes", ndim=2)
+    dev, shape = saved.codes.device, saved.codes.shape
+    if _elsewhere(dev, stream):
+        with _context(dev, stream):
+            return act_dequantize(saved, out)
+    fmt, a_codes, a_scales = _saved_addrs(saved, "saved", dev.index, shape)
+    out, a_out = _output(out, torch.bfloat16, "out", dev, shape)
+    _check(lib().rlk_act_dequantize(a_codes, a_scales, fmt, shape[0], shape[1], a_out,
+                                    _raw_stream(dev.index)), "rlk_act_dequantize")
+    return out
+
+
+def block_norm(block: torch.Tensor, residual: torch.Tensor, gamma_pre: torch.Tensor,
+               gamma_post: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+               gate_kind: str = "sigmoid", residual_scale: float = 1.0, block_scale: float = 1.0,
+               eps: float = 1e-6, save: Optional[str] = None, out: Optional[torch.Tensor] = None,
+               residual_out: Optional[torch.Tensor] = None, stream=None):
+    """The norms before and after a block, its gate and the residual stream's scales in one pass ->
+    (out bf16 [T, H], residual_out bf16 [T, H], SavedBlock or None).
+
+    residual_out = bf16(residual_scale * residual + block_scale * gate * rmsnorm(block, gamma_post))
+    and out = rmsnorm(residual_out, gamma_pre), with rmsnorm's bits.  Without gamma_post the block's
+    output is taken as it is; the gate, a bf16 [T, H], multiplies as it is ("identity") or through a
+    sigmoid.  save ("int8" or "e4m3") also stores 8-bit checkpoints of what block_norm_backward needs.
+    residual_out may be residual, and out may be block."""
+    bf16 = torch.bfloat16
+    _require(residual, bf16, "residual", ndim=2)
+    dev, shape = residual.device, residual.shape
+    if _elsewhere(dev, stream):
+        with _context(dev, stream):
+            return block_norm(block, residual, gamma_pre, gamma_post, gate, gate_kind, residual_scale,
+                              block_scale, eps, save, out, residual_out)
+    idx, (T, H) = dev.index, shape
+    a_block = _addr(block, bf16, "block", idx, shape)
+    a_pre = _addr(gamma_pre, bf16, "gamma_pre", idx, (H,))
+    a_post = _opt_addr(gamma_post, bf16, "gamma_post", idx, (H,))
+    a_gate = _opt_addr(gate, bf16, "gate", idx, shape)
+    kind = _gate_code(gate, gate_kind)
+    out, a_out = _output(out, bf16, "out", dev, shape)
+    residual_out, a_res = _output(residual_out, bf16, "residual_out", dev, shape)
+    fmt, saved, addrs = 0, None, (None,) * 6
+    if save is not None:
+        fmt = _choice(SAVED_FORMATS, save, "save")
+        needed = gamma_post is not None or gate is not None
+        saved = SavedBlock(_new_saved(save, dev, shape), _new_saved(save, dev, shape) if needed else None,
+                           _new_saved(save, dev, shape) if gate is not None else None)
+        addrs = [t.data_ptr() if s is not None else None for s in saved for t in (s or (None, None))]
+    _check(lib().rlk_block_norm(a_block, a_post, a_gate, kind, residual.data_ptr(), residual_scale,
+                                block_scale, a_pre, eps, T, H, a_out, a_res, fmt, *addrs,
+                                _raw_stream(idx)), "rlk_block_norm")
+    return out, residual_out, saved
+
+
+@functools.lru_cache(maxsize=1024)
+def block_norm_backward_workspace_size(T: int, H: int) -> int:
+    return int(lib().rlk_block_norm_backward_workspace_size(T, H))
+
+
+def block_norm_backward(grad_out: torch.Tensor, x: Union[torch.Tensor, Saved], gamma_pre: torch.Tensor,
+                        block: Union[torch.Tensor, Saved, None] = None,
+                        gamma_post: Optional[torch.Tensor] = None,
+                        gate: Union[torch.Tensor, Saved, None] = None, gate_kind: str = "sigmoid",
+                        residual_scale: float = 1.0, block_scale: float = 1.0, eps: float = 1e-6,
+                        grad_residual_out: Optional[torch.Tensor] = None,
+                        grad_dtype: Optional[torch.dtype] = None, want_block: bool = True,
+                        want_residual: bool = True, want_gate: bool = True, want_gammas: bool = True,
+                        grad_residual: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None) -> BlockNormGrads:
+    """Backward of block_norm.  x is its residual_out; x, block and gate are bf16 tensors, or the
+    checkpoints that block_norm saved.  grad_out is fp32 or bf16; grad_residual_out, the gradient
+    that reached residual_out from further on, and the gradients have grad_dtype (fp32 or bf16;
+    grad_out's type by default).  grad_residual (to write into) may be grad_residual_out."""
+    _require(grad_out, getattr(grad_out, "dtype", None), "grad_out", ndim=2)
+    dev, shape = grad_out.device, grad_out.shape
+    if _elsewhere(dev, stream):
+        with _context(dev, stream):
+            return block_norm_backward(grad_out, x, gamma_pre, block, gamma_post, gate, gate_kind,
+                                       residual_scale, block_scale, eps, grad_residual_out, grad_dtype,
+                                       want_block, want_residual, want_gate, want_gammas, grad_residual,
+                                       workspace)
+    idx, (T, H) = dev.index, shape
+    go_code = DTYPES.get(grad_out.dtype)
+    if go_code is None:
+        raise TypeError("grad_out must be a float32 or bfloat16 tensor")
+    if grad_dtype is None:
+        grad_dtype = grad_out.dtype if grad_residual is None else grad_residual.dtype
+    gx_code = DTYPES.get(grad_dtype)
+    if gx_code is None:
+        raise TypeError("grad_dtype must be float32 or bfloat16")
+    bf16, f32 = torch.bfloat16, torch.float32
+    fmt, a_x, s_x = _saved_addrs(x, "x", idx, shape)
+    if block is None and (gamma_post is not None or gate is not None):
+        raise ValueError("block is needed for gamma_post's and the gate's gradients")
+    f_b, a_b, s_b = (fmt, None, None) if block is None else _saved_addrs(block, "block", idx, shape)
+    f_g, a_g, s_g = (fmt, None, None) if gate is None else _saved_addrs(gate, "gate", idx, shape)
+    if f_b != fmt or f_g != fmt:
+        raise TypeError("x, block and gate must be all bfloat16 tensors or checkpoints of one format")
+    a_pre = _addr(gamma_pre, bf16, "gamma_pre", idx, (H,))
+    a_post = _opt_addr(gamma_post, bf16, "gamma_post", idx, (H,))
+    a_res = _opt_addr(grad_residual_out, grad_dtype, "grad_residual_out", idx, shape)
+    kind = _gate_code(gate, gate_kind)
+    grads, addrs = [None] * 5, [None] * 5
+    if want_block:
+        grads[0], addrs[0] = _output(None, grad_dtype, "grad_block", dev, shape)
+    if want_residual:
+        grads[1], addrs[1] = _output(grad_residual, grad_dtype, "grad_residual", dev, shape)
+    if want_gate and gate is not None:
+        grads[2], addrs[2] = _output(None, grad_dtype, "grad_gate", dev, shape)
+    p_ws, ws_n, ws = None, 0, None
+    if want_gammas:
+        grads[3], addrs[3] = _output(None, f32, "grad_gamma_pre", dev, (H,))
+        if gamma_post is not None:
+            grads[4], addrs[4] = _output(None, f32, "grad_gamma_post", dev, (H,))
+        p_ws, ws_n, ws = _workspace(workspace, block_norm_backward_workspace_size(T, H), dev)
+    _check(lib().rlk_block_norm_backward(
+        grad_out.data_ptr(), go_code, a_res, fmt, a_x, s_x, a_b, s_b, a_g, s_g, kind, a_post, a_pre,
+        residual_scale, block_scale, eps, T, H, addrs[1], addrs[0], addrs[2], gx_code, addrs[3],
+        addrs[4], p_ws, ws_n, _raw_stream(idx)), "rlk_block_norm_backward")
+    return BlockNormGrads(*grads)
+
+
+def rmsnorm_backward_q8(grad_out: torch.Tensor, x: Saved, gamma: torch.Tensor, eps: float = 1e-6,
+                        grad_residual: Optional[torch.Tensor] = None, want_gamma: bool = True,
+                        grad_dtype: Optional[torch.dtype] = None,
+                        grad_x: Optional[torch.Tensor] = None,
+                        grad_gamma: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None):
+    """rmsnorm_backward from an 8-bit checkpoint of x -> (grad_x [T, H], grad_gamma fp32 [H] or None);
+    grad_x has the bits of rmsnorm_backward on act_dequantize(x)."""
+    _require(grad_out, getattr(grad_out, "dtype", None), "grad_out", ndim=2)
+    dev, shape = grad_out.device, grad_out.shape
+    if _elsewhere(dev, stream):
+        with _context(dev, stream):
+            return rmsnorm_backward_q8(grad_out, x, gamma, eps, grad_residual, want_gamma, grad_dtype,
+                                       grad_x, grad_gamma, workspace)
+    idx, (T, H) = dev.index, shape
+    go_code = DTYPES.get(grad_out.dtype)
+    if go_code is None:
+        raise TypeError("grad_out must be a float32 or bfloat16 tensor")
+    if grad_dtype is None:
+        grad_dtype = grad_out.dtype if grad_x is None else grad_x.dtype
+    gx_code = DTYPES.get(grad_dtype)
+    if gx_code is None:
+        raise TypeError("grad_x must be float32 or bfloat16")
+    if not isinstance(x, Saved):
+        raise TypeError("x must be a Saved checkpoint")
+    fmt, a_x, s_x = _saved_addrs(x, "x", idx, shape)
+    a_gamma = _addr(gamma, torch.bfloat16, "gamma", idx, (H,))
+    a_res = _opt_addr(grad_residual, grad_dtype, "grad_residual", idx, shape)
+    grad_x, a_gx = _output(grad_x, grad_dtype, "grad_x", dev, shape)
+    a_gg = p_ws = None
+    ws_n = 0
+    if want_gamma:
+        grad_gamma, a_gg = _output(grad_gamma, torch.float32, "grad_gamma", dev, (H,))
+        p_ws, ws_n, ws = _workspace(workspace, block_norm_backward_workspace_size(T, H), dev)
+    _check(lib().rlk_rmsnorm_backward_q8(grad_out.data_ptr(), go_code, fmt, a_x, s_x, a_gamma, eps,
+                                         a_res, T, H, a_gx, gx_code, a_gg, p_ws, ws_n,
+                                         _raw_stream(idx)), "rlk_rmsnorm_backward_q8")
+    return grad_x, (grad_gamma if want_gamma else None)
+
+
+# ----------------------------------------------------------------- drafted tokens
+@functools.lru_cache(maxsize=1024)
+def draft_verify_workspace_size(n_draft: int, n_seqs: int, V: int) -> int:
+    return int(lib().rlk_draft_verify_workspace_size(n_draft, n_seqs, V))
+
+
+def _rows_addr(t: torch.Tensor, dtypes, name: str, index: int, shape):
+    """(type code, address, row stride) of a matrix whose rows may be padded."""
+    code = dtypes.get(getattr(t, "dtype", None))
+    if code is None:
+        raise TypeError("%s must be one of %s" % (name, ", ".join(str(d) for d in dtypes)))
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or t.get_device() != index:
+        raise ValueError("%s must be 2-D with unit column stride on cuda:%d" % (name, index))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    return code, t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def draft_verify(target_logits: torch.Tensor, draft_tokens: torch.Tensor, uniforms: torch.Tensor,
+                 noise: torch.Tensor, draft_offsets: torch.Tensor,
+                 draft_logits: Optional[torch.Tensor] = None,
+                 draft_lse: Optional[torch.Tensor] = None, active: Optional[torch.Tensor] = None,
+                 accepted: Optional[torch.Tensor] = None, tokens: Optional[torch.Tensor] = None,
+                 logprob: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                 status: Optional[torch.Tensor] = None, stream=None
+                 ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Drafted tokens against the target's probabilities -> (accepted int32 [S], tokens int32
+    [D + S], logprob fp32 [D + S]).
+
+    Sequence s has drafts draft_offsets[s] .. draft_offsets[s + 1] (int32 [S + 1] on the device) of
+    the D draft_tokens (int32), and one row more of target_logits [D + S, V] (fp32 or bf16, rows may
+    be padded), from row draft_offsets[s] + s on.  draft_logits [D, V] with draft_lse [D] are the
+    draft's distributions (log-probabilities without draft_lse; certain drafts without either).
+    uniforms fp32 [D] in [0, 1), noise fp32 [S, V] exponentially distributed.  tokens holds, in the
+    target's rows, the accepted drafts, the token drawn behind them and -1; logprob theirs, with the
+    bits of logits_logprob."""
+    if not isinstance(target_logits, torch.Tensor) or not target_logits.is_cuda or target_logits.dim() != 2:
+        raise ValueError("target_logits must be a 2-D tensor on a CUDA device")
+    dev = target_logits.device
+    if _elsewhere(dev, stream):
+        with _context(dev, stream):
+            return draft_verify(target_logits, draft_tokens, uniforms, noise, draft_offsets, draft_logits,
+                                draft_lse, active, accepted, tokens, logprob, workspace, status)
+    i32, f32, idx = torch.int32, torch.float32, dev.index
+    _require(draft_tokens, i32, "draft_tokens", dev, 1)
+    _require(draft_offsets, i32, "draft_offsets", dev, 1)
+    D, S, V = draft_tokens.shape[0], draft_offsets.shape[0] - 1, target_logits.shape[1]
+    if S < 0:
+        raise ValueError("draft_offsets must hold one number more than there are sequences")
+    t_code, a_target, ld_t = _rows_addr(target_logits, DTYPES, "target_logits", idx, (D + S, V))
+    _, a_noise, ld_n = _rows_addr(noise, {f32: 0}, "noise", idx, (S, V))
+    d_code, a_draft, ld_d = 0, None, 0
+    if draft_logits is not None:
+        d_code, a_draft, ld_d = _rows_addr(draft_logits, DTYPES, "draft_logits", idx, (D, V))
+    a_lse = _opt_addr(draft_lse, f32, "draft_lse", idx, (D,))
+    if D == 0:  # empty tensors may or may not have an address
+        a_draft = a_lse = None
+    a_u = _addr(uniforms, f32, "uniforms", idx, (D,))
+    a_act = _opt_addr(active, torch.uint8, "active", idx, (S,))
+    a_status = _status_addr(status, idx)
+    accepted, a_acc = _output(accepted, i32, "accepted", dev, (S,))
+    tokens, a_tok = _output(tokens, i32, "tokens", dev, (D + S,))
+    logprob, a_lp = _output(logprob, f32, "logprob", dev, (D + S,))
+    p_ws, ws_n, ws = _workspace(workspace, draft_verify_workspace_size(D, S, V), dev)
+    _check(lib().rlk_draft_verify(a_target, t_code, ld_t, draft_tokens.data_ptr(), a_draft, d_code,
+                                  ld_d, a_lse, a_u, a_noise, ld_n, draft_offsets.data_ptr(), a_act, D,
+                                  S, V, a_acc, a_tok, a_lp, p_ws, ws_n, a_status, _raw_stream(idx)),
+           "rlk_draft_verify")
+    return accepted, tokens, logprob
 
 
 def _cuda_device(device) -> torch.device:

@@ -18,6 +18,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include "rlk_block.cuh"
 #include "rlk_internal.h"
 #include "rlk_train.cuh"
 
@@ -470,6 +471,43 @@ PreferenceLayout preference_layout_of(int64_t T, int64_t n_pairs) {
     l.counts = l.sums + align256(chunks * sizeof(float2));
     l.total = l.counts + align256(chunks * sizeof(int32_t));
     return l;
+}
+
+struct VerifyLayout {
+    Layout rows;
+    size_t lse, total;
+};
+
+VerifyLayout verify_layout_of(int64_t n_draft, int64_t n_seqs, int64_t V) {
+    VerifyLayout l;
+    l.rows = layout_of(n_draft + n_seqs, V, 1);
+    l.lse = l.rows.total;
+    l.total = l.lse + align256(size_t(n_draft + n_seqs) * sizeof(float));
+    return l;
+}
+
+bool saved_format_known(int format) { return format == RLK_SAVED_INT8 || format == RLK_SAVED_E4M3; }
+
+// Checks shared by the calls that turn a tensor into a checkpoint and back.
+rlk_status_t act_checks(const void* in, const void* out, const void* scales, int format, int64_t T, int64_t H) {
+    if (T < 0 || T > RLK_MAX_ROWS) return RLK_ERR_INVALID_ARG;
+    if (H < 64 || H % 64 != 0 || H > (int64_t(1) << 20)) return RLK_ERR_UNSUPPORTED;
+    if (!saved_format_known(format)) return RLK_ERR_UNSUPPORTED;
+    if (T > 0 && (!in || !out || !scales)) return RLK_ERR_INVALID_ARG;
+    if (!aligned(in, 16) || !aligned(out, 16)) return RLK_ERR_ALIGNMENT;
+    return RLK_OK;
+}
+
+// A saved activation is a bf16 tensor without scales, or codes with them.
+bool saved_whole(int format, const void* data, const uint8_t* scales) {
+    return format == RLK_SAVED_BF16 ? !scales : (data != nullptr) == (scales != nullptr);
+}
+
+rlk_status_t run_block_bwd(const rlk::BlockBwdArgs& a, int format, cudaStream_t stream) {
+    const cudaError_t e = format == RLK_SAVED_BF16   ? rlk::launch_block_bwd_bf16(a, stream)
+                          : format == RLK_SAVED_INT8 ? rlk::launch_block_bwd_int8(a, stream)
+                                                     : rlk::launch_block_bwd_e4m3(a, stream);
+    return e == cudaSuccess ? RLK_OK : RLK_ERR_CUDA;
 }
 
 size_t clip_element_size(int dtype) { return dtype == RLK_DTYPE_F32 ? 4 : 2; }
@@ -1270,6 +1308,246 @@ rlk_status_t rlk_debug_primitive_hash(int which, uint32_t first, uint64_t count,
                                       reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? RLK_OK
                : RLK_ERR_CUDA;
+}
+
+rlk_status_t rlk_act_quantize(const void* x, int format, int64_t T, int64_t H, void* codes,
+                              uint8_t* scales, rlk_stream_t stream) {
+    rlk_status_t s = act_checks(x, codes, scales, format, T, H);
+    if (s != RLK_OK || T == 0) return s;
+    DeviceState* dev = nullptr;
+    if ((s = device_check(&dev)) != RLK_OK) return s;
+    return rlk::launch_act_quantize(static_cast<const uint16_t*>(x), format, T * H, {codes, scales},
+                                    dev->sm_count, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? RLK_OK
+               : RLK_ERR_CUDA;
+}
+
+rlk_status_t rlk_act_dequantize(const void* codes, const uint8_t* scales, int format, int64_t T,
+                                int64_t H, void* out, rlk_stream_t stream) {
+    rlk_status_t s = act_checks(codes, out, scales, format, T, H);
+    if (s != RLK_OK || T == 0) return s;
+    DeviceState* dev = nullptr;
+    if ((s = device_check(&dev)) != RLK_OK) return s;
+    return rlk::launch_act_dequantize({codes, scales}, format, T * H, static_cast<uint16_t*>(out),
+                                      dev->sm_count, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? RLK_OK
+               : RLK_ERR_CUDA;
+}
+
+rlk_status_t rlk_block_norm(const void* block, const void* gamma_post, const void* gate,
+                            int gate_kind, const void* residual, float residual_scale,
+                            float block_scale, const void* gamma_pre, float eps, int64_t T,
+                            int64_t H, void* out, void* residual_out, int saved_format,
+                            void* saved_x, uint8_t* saved_x_scales, void* saved_block,
+                            uint8_t* saved_block_scales, void* saved_gate,
+                            uint8_t* saved_gate_scales, rlk_stream_t stream) {
+    if (T < 0 || T > RLK_MAX_ROWS) return RLK_ERR_INVALID_ARG;
+    if (H < 64 || H % 64 != 0 || H > 8192) return RLK_ERR_UNSUPPORTED;
+    if (gate_kind != RLK_GATE_IDENTITY && gate_kind != RLK_GATE_SIGMOID) return RLK_ERR_UNSUPPORTED;
+    if (saved_format != RLK_SAVED_BF16 && !saved_format_known(saved_format)) return RLK_ERR_UNSUPPORTED;
+    if (!(eps > 0.0f) || !(eps < 3.0e38f)) return RLK_ERR_INVALID_ARG;
+    if (!std::isfinite(residual_scale) || !std::isfinite(block_scale)) return RLK_ERR_INVALID_ARG;
+    if (T == 0) return RLK_OK;
+    if (!block || !residual || !gamma_pre || !out || !residual_out) return RLK_ERR_INVALID_ARG;
+    if (saved_format == RLK_SAVED_BF16) {
+        if (saved_x || saved_x_scales || saved_block || saved_block_scales || saved_gate || saved_gate_scales)
+            return RLK_ERR_INVALID_ARG;
+    } else if (!saved_x || !saved_x_scales || !saved_block != !saved_block_scales ||
+               !saved_gate != !saved_gate_scales || (saved_gate && !gate)) {
+        return RLK_ERR_INVALID_ARG;
+    }
+    if (out == residual_out || out == residual || residual_out == block) return RLK_ERR_INVALID_ARG;
+    for (const void* p : {block, gamma_post, gate, residual, gamma_pre, static_cast<const void*>(out),
+                          static_cast<const void*>(residual_out), static_cast<const void*>(saved_x),
+                          static_cast<const void*>(saved_block), static_cast<const void*>(saved_gate)})
+        if (!aligned(p, 16)) return RLK_ERR_ALIGNMENT;
+    DeviceState* dev = nullptr;
+    rlk_status_t s = device_check(&dev);
+    if (s != RLK_OK) return s;
+    rlk::BlockNormArgs a;
+    a.block = static_cast<const uint16_t*>(block);
+    a.gamma_post = static_cast<const uint16_t*>(gamma_post);
+    a.gate = static_cast<const uint16_t*>(gate);
+    a.residual = static_cast<const uint16_t*>(residual);
+    a.gamma_pre = static_cast<const uint16_t*>(gamma_pre);
+    a.out = static_cast<uint16_t*>(out);
+    a.residual_out = static_cast<uint16_t*>(residual_out);
+    a.saved_x = {saved_x, saved_x_scales};
+    a.saved_block = {saved_block, saved_block_scales};
+    a.saved_gate = {saved_gate, saved_gate_scales};
+    a.residual_scale = residual_scale;
+    a.block_scale = block_scale;
+    a.eps = eps;
+    a.gate_kind = gate_kind;
+    a.saved_format = saved_format;
+    a.T = int(T);
+    a.H = int(H);
+    return rlk::launch_block_norm(a, dev->sm_count, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? RLK_OK
+               : RLK_ERR_CUDA;
+}
+
+size_t rlk_block_norm_backward_workspace_size(int64_t T, int64_t H) {
+    if (T < 0 || T > RLK_MAX_ROWS || H < 64 || H % 64 != 0 || H > 8192) return 0;
+    return align256(size_t(rlk::block_bwd_ranges(T)) * 2 * size_t(H) * sizeof(float));
+}
+
+rlk_status_t rlk_block_norm_backward(
+    const void* grad_out, int grad_out_dtype, const void* grad_residual_out, int saved_format,
+    const void* x, const uint8_t* x_scales, const void* block, const uint8_t* block_scales,
+    const void* gate, const uint8_t* gate_scales, int gate_kind, const void* gamma_post,
+    const void* gamma_pre, float residual_scale, float block_scale, float eps, int64_t T,
+    int64_t H, void* grad_residual, void* grad_block, void* grad_gate, int grad_dtype,
+    float* grad_gamma_pre, float* grad_gamma_post, void* workspace, size_t workspace_bytes,
+    rlk_stream_t stream) {
+    if (T < 0 || T > RLK_MAX_ROWS) return RLK_ERR_INVALID_ARG;
+    if (H < 64 || H % 64 != 0 || H > 8192) return RLK_ERR_UNSUPPORTED;
+    if ((grad_out_dtype != RLK_DTYPE_F32 && grad_out_dtype != RLK_DTYPE_BF16) ||
+        (grad_dtype != RLK_DTYPE_F32 && grad_dtype != RLK_DTYPE_BF16))
+        return RLK_ERR_UNSUPPORTED;
+    if (gate_kind != RLK_GATE_IDENTITY && gate_kind != RLK_GATE_SIGMOID) return RLK_ERR_UNSUPPORTED;
+    if (saved_format != RLK_SAVED_BF16 && !saved_format_known(saved_format)) return RLK_ERR_UNSUPPORTED;
+    // 1 / eps, the most that rstd^2 can be, has to be a number too
+    if (!(eps >= std::numeric_limits<float>::min()) || !(eps < 3.0e38f)) return RLK_ERR_INVALID_ARG;
+    if (!std::isfinite(residual_scale) || !std::isfinite(block_scale)) return RLK_ERR_INVALID_ARG;
+    if (T > 0 && !grad_residual && !grad_block && !grad_gate && !grad_gamma_pre && !grad_gamma_post)
+        return RLK_ERR_INVALID_ARG;
+    const bool branch = gamma_post || gate;
+    if ((grad_gamma_post && !gamma_post) || (grad_gate && !gate)) return RLK_ERR_INVALID_ARG;
+    if (T > 0 && (!grad_out || !x || !gamma_pre || (branch && !block))) return RLK_ERR_INVALID_ARG;
+    if (!saved_whole(saved_format, x, x_scales) || !saved_whole(saved_format, block, block_scales) ||
+        !saved_whole(saved_format, gate, gate_scales))
+        return RLK_ERR_INVALID_ARG;
+    const bool gammas = grad_gamma_pre || grad_gamma_post;
+    const size_t need = gammas ? rlk_block_norm_backward_workspace_size(T, H) : 0;
+    if (need > 0 && !workspace) return RLK_ERR_INVALID_ARG;
+    for (const void* p : {grad_residual, grad_block, grad_gate}) {
+        if (!p) continue;
+        if (p == grad_out && grad_dtype != grad_out_dtype) return RLK_ERR_INVALID_ARG;
+        if (p == grad_residual_out && p != grad_residual) return RLK_ERR_INVALID_ARG;
+    }
+    if ((grad_residual && (grad_residual == grad_block || grad_residual == grad_gate)) ||
+        (grad_block && grad_block == grad_gate))
+        return RLK_ERR_INVALID_ARG;
+    for (const void* p : {grad_out, grad_residual_out, x, block, gate, gamma_post, gamma_pre,
+                          static_cast<const void*>(grad_residual), static_cast<const void*>(grad_block),
+                          static_cast<const void*>(grad_gate), static_cast<const void*>(grad_gamma_pre),
+                          static_cast<const void*>(grad_gamma_post)})
+        if (!aligned(p, 16)) return RLK_ERR_ALIGNMENT;
+    if (!aligned(workspace, 256)) return RLK_ERR_ALIGNMENT;
+    if (workspace_bytes < need) return RLK_ERR_WORKSPACE;
+    if (T == 0 && !gammas) return RLK_OK;
+    DeviceState* dev = nullptr;
+    rlk_status_t s = device_check(&dev);
+    if (s != RLK_OK) return s;
+    rlk::BlockBwdArgs a;
+    a.grad_out = grad_out;
+    a.grad_res = grad_residual_out;
+    a.x = {x, x_scales};
+    a.block = {branch ? block : nullptr, block_scales};
+    a.gate = {gate, gate_scales};
+    a.gamma_post = static_cast<const uint16_t*>(gamma_post);
+    a.gamma_pre = static_cast<const uint16_t*>(gamma_pre);
+    a.grad_residual = grad_residual;
+    a.grad_block = grad_block;
+    a.grad_gate = grad_gate;
+    a.grad_pre = grad_gamma_pre;
+    a.grad_post = grad_gamma_post;
+    a.parts = gammas ? static_cast<float*>(workspace) : nullptr;
+    a.residual_scale = residual_scale;
+    a.block_scale = block_scale;
+    a.eps = eps;
+    a.gate_kind = gate_kind;
+    a.go_dtype = grad_out_dtype;
+    a.gx_dtype = grad_dtype;
+    a.T = int(T);
+    a.H = int(H);
+    return run_block_bwd(a, saved_format, reinterpret_cast<cudaStream_t>(stream));
+}
+
+rlk_status_t rlk_rmsnorm_backward_q8(const void* grad_out, int grad_out_dtype, int format,
+                                     const void* codes, const uint8_t* scales, const void* gamma,
+                                     float eps, const void* grad_residual, int64_t T, int64_t H,
+                                     void* grad_x, int grad_x_dtype, float* grad_gamma,
+                                     void* workspace, size_t workspace_bytes,
+                                     rlk_stream_t stream) {
+    if (!saved_format_known(format)) return RLK_ERR_UNSUPPORTED;
+    if (T > 0 && !grad_x) return RLK_ERR_INVALID_ARG;
+    // the block norms' backward without a block
+    return rlk_block_norm_backward(grad_out, grad_out_dtype, grad_residual, format, codes, scales, nullptr,
+                                   nullptr, nullptr, nullptr, RLK_GATE_IDENTITY, nullptr, gamma, 1.0f, 1.0f,
+                                   eps, T, H, grad_x, nullptr, nullptr, grad_x_dtype, grad_gamma, nullptr,
+                                   workspace, workspace_bytes, stream);
+}
+
+size_t rlk_draft_verify_workspace_size(int64_t n_draft, int64_t n_seqs, int64_t V) {
+    if (n_draft < 0 || n_seqs < 0 || n_draft > RLK_MAX_ROWS || n_seqs > RLK_MAX_ROWS ||
+        n_draft + n_seqs > RLK_MAX_ROWS || shard_check(V, 1) != RLK_OK)
+        return 0;
+    return verify_layout_of(n_draft, n_seqs, V).total;
+}
+
+rlk_status_t rlk_draft_verify(const void* target_logits, int target_dtype, int64_t ld_target,
+                              const int32_t* draft_tokens, const void* draft_logits,
+                              int draft_dtype, int64_t ld_draft, const float* draft_lse,
+                              const float* uniforms, const float* noise, int64_t ld_noise,
+                              const int32_t* draft_offsets, const uint8_t* active_mask,
+                              int64_t n_draft, int64_t n_seqs, int64_t V, int32_t* out_accepted,
+                              int32_t* out_tokens, float* out_logprob, void* workspace,
+                              size_t workspace_bytes, int32_t* dev_status, rlk_stream_t stream) {
+    if (n_draft < 0 || n_seqs < 0 || n_draft > RLK_MAX_ROWS || n_seqs > RLK_MAX_ROWS)
+        return RLK_ERR_INVALID_ARG;
+    const int64_t rows = n_draft + n_seqs;
+    rlk_status_t s = mat_checks(target_logits, target_dtype, ld_target, rows, V);
+    if (s != RLK_OK) return s;
+    if (draft_logits && (s = mat_checks(draft_logits, draft_dtype, ld_draft, n_draft, V)) != RLK_OK) return s;
+    if (n_seqs == 0) return n_draft == 0 ? RLK_OK : RLK_ERR_INVALID_ARG;
+    if (draft_lse && !draft_logits) return RLK_ERR_INVALID_ARG;
+    if (n_draft > 0 && (!draft_tokens || !uniforms)) return RLK_ERR_INVALID_ARG;
+    if (!noise || ld_noise < V || !draft_offsets || !out_accepted || !out_tokens || !out_logprob || !workspace)
+        return RLK_ERR_INVALID_ARG;
+    if (!aligned(draft_tokens, 4) || !aligned(draft_lse, 4) || !aligned(uniforms, 4) || !aligned(noise, 4) ||
+        !aligned(draft_offsets, 4) || !aligned(out_accepted, 4) || !aligned(out_tokens, 4) ||
+        !aligned(out_logprob, 4) || !aligned(workspace, 256) || !aligned(dev_status, 4))
+        return RLK_ERR_ALIGNMENT;
+    const VerifyLayout l = verify_layout_of(n_draft, n_seqs, V);
+    if (workspace_bytes < l.total) return RLK_ERR_WORKSPACE;
+    DeviceState* dev = nullptr;
+    if ((s = device_check(&dev)) != RLK_OK) return s;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    float* lse = reinterpret_cast<float*>(ws + l.lse);
+    if (rlk::launch_mat_tile_partials(target_logits, target_dtype, ld_target, nullptr, nullptr, int(rows),
+                                      int(V), reinterpret_cast<float2*>(ws + l.rows.partials),
+                                      reinterpret_cast<float*>(ws + l.rows.tgt),
+                                      dev->sm_count * dev->mat_ctas_per_sm[target_dtype], st) != cudaSuccess)
+        return RLK_ERR_CUDA;
+    if ((s = run_tile_tree(nullptr, nullptr, rows, V, 1, nullptr, lse, ws, l.rows, dev_status, st, dev)) != RLK_OK)
+        return s;
+    rlk::VerifyArgs a;
+    a.target = target_logits;
+    a.draft = draft_logits;
+    a.draft_lse = draft_lse;
+    a.tokens = draft_tokens;
+    a.uniforms = uniforms;
+    a.noise = noise;
+    a.offsets = draft_offsets;
+    a.active = active_mask;
+    a.rows = reinterpret_cast<const rlk_partial_t*>(ws + l.rows.records);
+    a.lse = lse;
+    a.ld_target = ld_target;
+    a.ld_draft = ld_draft;
+    a.ld_noise = ld_noise;
+    a.target_dtype = target_dtype;
+    a.draft_dtype = draft_dtype;
+    a.n_draft = int(n_draft);
+    a.n_seqs = int(n_seqs);
+    a.V = int(V);
+    a.out_accepted = out_accepted;
+    a.out_tokens = out_tokens;
+    a.out_logprob = out_logprob;
+    a.status = dev_status;
+    return rlk::launch_draft_verify(a, dev->sm_count, st) == cudaSuccess ? RLK_OK : RLK_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -1,0 +1,214 @@
+// The norms before and after a block, its gate and the residual stream's
+// scales in one pass.  Per row, in fp32,
+//
+//   n   = RN(RN(b rstd(b)) gamma_post)        (b itself without gamma_post)
+//   x'  = bf16_RN(fma(rs, r, bs (n gate)))
+//   out = bf16_RN(RN(RN(x' rstd(x')) gamma_pre))
+//
+// with rstd by the strict RMSNorm's tree and rsqrt, so that out has the bits of
+// rlk_rmsnorm on x'.  The checkpoints for the backward are formed from the same
+// registers.
+//
+// Element i = 512 w + 256 g + 8 l + j is warp w's lane l's j-th value of its
+// column group g: a lane reads 16 contiguous bytes, four lanes hold a
+// checkpoint's block of 32, and the tree's levels fall as in the RMSNorm: over j
+// in the lane, over l across lanes, over the two groups, then over the warps.
+//
+// What bounds it: HBM.
+#include <cstdint>
+
+#include "rlk_block.cuh"
+#include "rlk_train.cuh"
+
+namespace rlk {
+namespace {
+
+constexpr int cta_threads(int warps) { return 32 * warps > 128 ? 32 * warps : 128; }
+
+// 1 / (1 + e^-z), from e^-|z|, which does not overflow.
+__device__ __forceinline__ float sigmoid(float z) {
+    const float e = exp_any(-fabsf(z));
+    return __fdiv_rn(z < 0.0f ? e : 1.0f, __fadd_rn(1.0f, e));
+}
+
+template <int kSaved>
+__device__ __forceinline__ void save_group(const SavedOut& to, uint4 x, int64_t at, bool in) {
+    uint32_t m = amax8(x);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const uint32_t byte = saved_byte<kSaved>(m);
+    if (!in) return;
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(to.codes) + at) = saved_encode8<kSaved>(x, byte);
+    if (!(threadIdx.x & 3)) to.scales[at >> 5] = static_cast<uint8_t>(byte);
+}
+
+// A team of kWarps warps per row.
+template <int kWarps, int kSaved>
+__global__ void __launch_bounds__(cta_threads(kWarps)) k_block_norm(const BlockNormArgs a) {
+    constexpr int kTeams = cta_threads(kWarps) / (32 * kWarps);
+    __shared__ float part[kTeams][2][kWarps];  // [team][slot][warp]
+    const int lane = threadIdx.x & 31, team = threadIdx.x / (32 * kWarps);
+    const int warp = (threadIdx.x >> 5) % kWarps;
+    const int i0 = 512 * warp + 8 * lane;  // and i0 + 256
+    const bool in[2] = {i0 < a.H, i0 + 256 < a.H};
+    const int odd = lane & 1;
+    const float h = static_cast<float>(a.H);
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kTeams;
+
+    // rstd of the row whose 16 features are v: the contract's tree
+    auto rstd_of = [&](const uint64_t (&v)[2][4], int slot) {
+        float s[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            float s2[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                float lo, hi;
+                f2_unpack(f2_mul(v[g][p], v[g][p]), lo, hi);
+                s2[p] = __fadd_rn(lo, hi);
+            }
+            s[g] = __fadd_rn(__fadd_rn(s2[0], s2[1]), __fadd_rn(s2[2], s2[3]));
+        }
+        // even lanes go on with the first group, odd ones with the second
+        float q = __fadd_rn(odd ? s[1] : s[0], __shfl_xor_sync(0xffffffffu, odd ? s[0] : s[1], 1));
+#pragma unroll
+        for (int o = 2; o < 32; o <<= 1) q = __fadd_rn(q, __shfl_xor_sync(0xffffffffu, q, o));
+        q = __fadd_rn(q, __shfl_xor_sync(0xffffffffu, q, 1));
+        if constexpr (kWarps > 1) {
+            // two slots alternate: a team's warps are never more than one sum apart
+            if (lane == 0) part[team][slot][warp] = q;
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * kWarps) : "memory");
+            float p[kWarps];
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) p[i] = part[team][slot][i];
+#pragma unroll
+            for (int n = kWarps / 2; n >= 1; n >>= 1) {
+#pragma unroll
+                for (int i = 0; i < n; ++i) p[i] = __fadd_rn(p[2 * i], p[2 * i + 1]);
+            }
+            q = p[0];
+        }
+        return contract_rsqrt(__fadd_rn(__fdiv_rn(q, h), a.eps));
+    };
+    auto load = [&](const uint16_t* base, int64_t row, uint4 (&w)[2]) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+            w[g] = in[g] ? *reinterpret_cast<const uint4*>(base + row + i0 + 256 * g) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    auto pairs = [](const uint4 (&w)[2], uint64_t (&v)[2][4]) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const uint32_t q[4] = {w[g].x, w[g].y, w[g].z, w[g].w};
+#pragma unroll
+            for (int p = 0; p < 4; ++p) v[g][p] = unpack_bf16x2(q[p]);
+        }
+    };
+
+    int slot = 0;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kTeams + team; t < a.T; t += stride) {
+        const int64_t row = t * a.H;
+        uint4 wb[2], wr[2], wg[2];
+        load(a.block, row, wb);
+        load(a.residual, row, wr);
+        if (a.gate) load(a.gate, row, wg);
+        if constexpr (kSaved != RLK_SAVED_BF16) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                if (a.saved_block.codes) save_group<kSaved>(a.saved_block, wb[g], row + i0 + 256 * g, in[g]);
+                if (a.saved_gate.codes) save_group<kSaved>(a.saved_gate, wg[g], row + i0 + 256 * g, in[g]);
+            }
+        }
+        uint64_t n[2][4];
+        pairs(wb, n);
+        if (a.gamma_post) {
+            const uint64_t rstd = f2_splat(rstd_of(n, slot));
+            slot ^= 1;
+            uint4 w[2];
+            uint64_t gam[2][4];
+            load(a.gamma_post, 0, w);
+            pairs(w, gam);
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int p = 0; p < 4; ++p) n[g][p] = f2_mul(f2_mul(n[g][p], rstd), gam[g][p]);
+        }
+        if (a.gate) {
+            uint64_t z[2][4];
+            pairs(wg, z);
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    if (a.gate_kind == RLK_GATE_SIGMOID) {
+                        float lo, hi;
+                        f2_unpack(z[g][p], lo, hi);
+                        z[g][p] = f2_pack(sigmoid(lo), sigmoid(hi));
+                    }
+                    n[g][p] = f2_mul(n[g][p], z[g][p]);
+                }
+        }
+        uint64_t x[2][4];
+        pairs(wr, x);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            uint32_t o[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                o[p] = pack_bf16x2(f2_fma(f2_splat(a.residual_scale), x[g][p], f2_mul(n[g][p], f2_splat(a.block_scale))));
+                x[g][p] = unpack_bf16x2(o[p]);  // the norm's input is the stream as it is stored
+            }
+            const uint4 w = make_uint4(o[0], o[1], o[2], o[3]);
+            const int64_t at = row + i0 + 256 * g;
+            if (in[g]) *reinterpret_cast<uint4*>(a.residual_out + at) = w;
+            if constexpr (kSaved != RLK_SAVED_BF16) save_group<kSaved>(a.saved_x, w, at, in[g]);
+        }
+        const uint64_t rstd = f2_splat(rstd_of(x, slot));
+        slot ^= 1;
+        uint4 w[2];
+        uint64_t gam[2][4];
+        load(a.gamma_pre, 0, w);
+        pairs(w, gam);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            uint32_t o[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) o[p] = pack_bf16x2(f2_mul(f2_mul(x[g][p], rstd), gam[g][p]));
+            if (in[g]) *reinterpret_cast<uint4*>(a.out + row + i0 + 256 * g) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+}
+
+template <int kWarps, int kSaved>
+cudaError_t launch(const BlockNormArgs& a, int num_sms, cudaStream_t stream) {
+    constexpr int kTeams = cta_threads(kWarps) / (32 * kWarps);
+    int64_t blocks = (static_cast<int64_t>(a.T) + kTeams - 1) / kTeams;
+    if (blocks > static_cast<int64_t>(num_sms) * 32) blocks = static_cast<int64_t>(num_sms) * 32;
+    k_block_norm<kWarps, kSaved><<<static_cast<int>(blocks), cta_threads(kWarps), 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <int kSaved>
+cudaError_t launch_saved(const BlockNormArgs& a, int num_sms, cudaStream_t stream) {
+    int warps = 1;
+    while (warps * 512 < a.H) warps *= 2;
+    switch (warps) {
+        case 1: return launch<1, kSaved>(a, num_sms, stream);
+        case 2: return launch<2, kSaved>(a, num_sms, stream);
+        case 4: return launch<4, kSaved>(a, num_sms, stream);
+        case 8: return launch<8, kSaved>(a, num_sms, stream);
+        case 16: return launch<16, kSaved>(a, num_sms, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_block_norm(const BlockNormArgs& a, int num_sms, cudaStream_t stream) {
+    switch (a.saved_format) {
+        case RLK_SAVED_BF16: return launch_saved<RLK_SAVED_BF16>(a, num_sms, stream);
+        case RLK_SAVED_INT8: return launch_saved<RLK_SAVED_INT8>(a, num_sms, stream);
+        default: return launch_saved<RLK_SAVED_E4M3>(a, num_sms, stream);
+    }
+}
+
+}  // namespace rlk

@@ -1,0 +1,88 @@
+// Activation checkpoints in 8 bits: a bf16 tensor to codes with a byte per 32
+// features, and back.  Per block of 32 features, with m the largest magnitude,
+// the byte is m's exponent (shifted by what the code's own range takes) and a
+// code is x / 2^(byte - bias) to the nearest, ties to even.
+//
+// A thread takes 16 features, a pair of lanes a block, so that a thread's
+// reads and writes are 16 bytes; the tensor is one run of blocks, H being a
+// multiple of 32.  What bounds it: HBM.
+#include <cstdint>
+
+#include "rlk_block.cuh"
+
+namespace rlk {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <int kSaved>
+__global__ void __launch_bounds__(kThreads)
+    k_act_quantize(const uint16_t* x, int64_t chunks, uint8_t* codes, uint8_t* scales) {
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
+    const int lane = threadIdx.x & 31;
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x - lane; first < chunks; first += stride) {
+        const int64_t c = first + lane;
+        const bool in = c < chunks;
+        uint4 a = {}, b = {};
+        if (in) {
+            a = reinterpret_cast<const uint4*>(x)[2 * c];
+            b = reinterpret_cast<const uint4*>(x)[2 * c + 1];
+        }
+        uint32_t m = max(amax8(a), amax8(b));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        const uint32_t byte = saved_byte<kSaved>(m);
+        const uint2 lo = saved_encode8<kSaved>(a, byte), hi = saved_encode8<kSaved>(b, byte);
+        if (in) reinterpret_cast<uint4*>(codes)[c] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        if (in && !(lane & 1)) scales[c >> 1] = static_cast<uint8_t>(byte);
+    }
+}
+
+template <int kSaved>
+__global__ void __launch_bounds__(kThreads)
+    k_act_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t chunks, uint16_t* out) {
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
+    for (int64_t c = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; c < chunks; c += stride) {
+        const uint4 q = reinterpret_cast<const uint4*>(codes)[c];
+        const float scale = saved_scale<kSaved>(scales[c >> 1]);
+        uint64_t v[4];
+        saved_decode8<kSaved>(make_uint2(q.x, q.y), scale, v);
+        reinterpret_cast<uint4*>(out)[2 * c] =
+            make_uint4(pack_bf16x2(v[0]), pack_bf16x2(v[1]), pack_bf16x2(v[2]), pack_bf16x2(v[3]));
+        saved_decode8<kSaved>(make_uint2(q.z, q.w), scale, v);
+        reinterpret_cast<uint4*>(out)[2 * c + 1] =
+            make_uint4(pack_bf16x2(v[0]), pack_bf16x2(v[1]), pack_bf16x2(v[2]), pack_bf16x2(v[3]));
+    }
+}
+
+int blocks_for(int64_t chunks, int num_sms) {
+    const int64_t need = (chunks + kThreads - 1) / kThreads, most = static_cast<int64_t>(num_sms) * 32;
+    return static_cast<int>(need < most ? need : most);
+}
+
+}  // namespace
+
+cudaError_t launch_act_quantize(const uint16_t* x, int format, int64_t n, SavedOut out, int num_sms,
+                                cudaStream_t stream) {
+    const int64_t chunks = n / 16;
+    if (chunks == 0) return cudaSuccess;
+    const int blocks = blocks_for(chunks, num_sms);
+    if (format == RLK_SAVED_INT8)
+        k_act_quantize<RLK_SAVED_INT8><<<blocks, kThreads, 0, stream>>>(x, chunks, static_cast<uint8_t*>(out.codes), out.scales);
+    else
+        k_act_quantize<RLK_SAVED_E4M3><<<blocks, kThreads, 0, stream>>>(x, chunks, static_cast<uint8_t*>(out.codes), out.scales);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_act_dequantize(SavedIn in, int format, int64_t n, uint16_t* out, int num_sms,
+                                  cudaStream_t stream) {
+    const int64_t chunks = n / 16;
+    if (chunks == 0) return cudaSuccess;
+    const int blocks = blocks_for(chunks, num_sms);
+    if (format == RLK_SAVED_INT8)
+        k_act_dequantize<RLK_SAVED_INT8><<<blocks, kThreads, 0, stream>>>(static_cast<const uint8_t*>(in.data), in.scales, chunks, out);
+    else
+        k_act_dequantize<RLK_SAVED_E4M3><<<blocks, kThreads, 0, stream>>>(static_cast<const uint8_t*>(in.data), in.scales, chunks, out);
+    return cudaGetLastError();
+}
+
+}  // namespace rlk
