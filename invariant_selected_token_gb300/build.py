@@ -27,7 +27,9 @@ INCLUDE = os.path.join(ROOT, "include")
 SOURCES = ["rlk_logits.cu", "rlk_logits_mat.cu", "rlk_merge.cu", "rlk_gemm.cu", "rlk_rmsnorm.cu",
            "rlk_api.cu", "rlk_static_ws.cu", "rlk_debug.cu", "rlk_policy.cu", "rlk_pref.cu",
            "rlk_clip.cu", "rlk_rmsnorm_bwd.cu", "rlk_ckpt.cu", "rlk_block_norm.cu",
-           "rlk_block_bwd_bf16.cu", "rlk_block_bwd_int8.cu", "rlk_block_bwd_e4m3.cu", "rlk_verify.cu"]
+           "rlk_block_bwd.cu", "rlk_block_bwd_bf16_f32.cu", "rlk_block_bwd_bf16_bf16.cu",
+           "rlk_block_bwd_int8_f32.cu", "rlk_block_bwd_int8_bf16.cu", "rlk_block_bwd_e4m3_f32.cu",
+           "rlk_block_bwd_e4m3_bf16.cu", "rlk_verify.cu"]
 HEADERS = ["rlk_ptx.cuh", "rlk_contract.cuh", "rlk_internal.h", "rlk_train.cuh", "rlk_block.cuh",
            "rlk_block_bwd.cuh"]
 

@@ -503,13 +503,6 @@ bool saved_whole(int format, const void* data, const uint8_t* scales) {
     return format == RLK_SAVED_BF16 ? !scales : (data != nullptr) == (scales != nullptr);
 }
 
-rlk_status_t run_block_bwd(const rlk::BlockBwdArgs& a, int format, cudaStream_t stream) {
-    const cudaError_t e = format == RLK_SAVED_BF16   ? rlk::launch_block_bwd_bf16(a, stream)
-                          : format == RLK_SAVED_INT8 ? rlk::launch_block_bwd_int8(a, stream)
-                                                     : rlk::launch_block_bwd_e4m3(a, stream);
-    return e == cudaSuccess ? RLK_OK : RLK_ERR_CUDA;
-}
-
 size_t clip_element_size(int dtype) { return dtype == RLK_DTYPE_F32 ? 4 : 2; }
 
 // Pieces of a tensor that starts `lead` bytes behind a 16-byte boundary.
@@ -1462,7 +1455,9 @@ rlk_status_t rlk_block_norm_backward(
     a.gx_dtype = grad_dtype;
     a.T = int(T);
     a.H = int(H);
-    return run_block_bwd(a, saved_format, reinterpret_cast<cudaStream_t>(stream));
+    return rlk::launch_block_bwd(a, saved_format, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? RLK_OK
+               : RLK_ERR_CUDA;
 }
 
 rlk_status_t rlk_rmsnorm_backward_q8(const void* grad_out, int grad_out_dtype, int format,

@@ -63,10 +63,18 @@ struct BlockBwdArgs {
 // Ranges of rows whose grad_gamma sums are formed apart, a CTA per SM each.
 constexpr int kBlockBwdRanges = 152;
 inline int block_bwd_ranges(int64_t T) { return T < kBlockBwdRanges ? static_cast<int>(T) : kBlockBwdRanges; }
-// one translation unit for each kind of saved activation
-cudaError_t launch_block_bwd_bf16(const BlockBwdArgs& a, cudaStream_t stream);
-cudaError_t launch_block_bwd_int8(const BlockBwdArgs& a, cudaStream_t stream);
-cudaError_t launch_block_bwd_e4m3(const BlockBwdArgs& a, cudaStream_t stream);
+// Whether a team has more than one chain of 64 rows.
+__host__ __device__ inline bool block_bwd_chained(int64_t T, int64_t blocks, int teams) {
+    return (T + blocks - 1) / blocks > 64 * int64_t(teams);
+}
+cudaError_t launch_block_bwd(const BlockBwdArgs& a, int format, cudaStream_t stream);
+// a translation unit for each kind of saved activation and each type of grad_out
+cudaError_t launch_block_bwd_bf16_f32(const BlockBwdArgs& a, int blocks, cudaStream_t stream);
+cudaError_t launch_block_bwd_bf16_bf16(const BlockBwdArgs& a, int blocks, cudaStream_t stream);
+cudaError_t launch_block_bwd_int8_f32(const BlockBwdArgs& a, int blocks, cudaStream_t stream);
+cudaError_t launch_block_bwd_int8_bf16(const BlockBwdArgs& a, int blocks, cudaStream_t stream);
+cudaError_t launch_block_bwd_e4m3_f32(const BlockBwdArgs& a, int blocks, cudaStream_t stream);
+cudaError_t launch_block_bwd_e4m3_bf16(const BlockBwdArgs& a, int blocks, cudaStream_t stream);
 
 struct VerifyArgs {
     const void* target;          // [rows][ld_target]
@@ -89,17 +97,70 @@ struct VerifyArgs {
 };
 cudaError_t launch_draft_verify(const VerifyArgs& a, int num_sms, cudaStream_t stream);
 
+// ---------------------------------------------------------------- bf16 pairs
+__device__ __forceinline__ uint32_t pack_bf16x2(uint64_t v) {
+    float lo, hi;
+    f2_unpack(v, lo, hi);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ uint64_t unpack_bf16x2(uint32_t w) {
+    return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ void pairs_of(uint4 w, uint64_t (&v)[4]) {
+    v[0] = unpack_bf16x2(w.x);
+    v[1] = unpack_bf16x2(w.y);
+    v[2] = unpack_bf16x2(w.z);
+    v[3] = unpack_bf16x2(w.w);
+}
+__device__ __forceinline__ uint4 words_of(const uint64_t (&v)[4]) {
+    return make_uint4(pack_bf16x2(v[0]), pack_bf16x2(v[1]), pack_bf16x2(v[2]), pack_bf16x2(v[3]));
+}
+// The contract's tree over the squares of 8 features.
+__device__ __forceinline__ float squares_of(const uint64_t (&v)[4]) {
+    float s2[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        float lo, hi;
+        f2_unpack(f2_mul(v[p], v[p]), lo, hi);
+        s2[p] = __fadd_rn(lo, hi);
+    }
+    return __fadd_rn(__fadd_rn(s2[0], s2[1]), __fadd_rn(s2[2], s2[3]));
+}
+
+// e^-|z| (which does not overflow) and 1 / (1 + e^-|z|) of a pair: the sigmoid is the second, or
+// for a negative z the product of both, and its slope the first times the second's square.  The
+// reciprocal of a number in [1, 2] is the hardware's approximation, a step of 2^-23 off at most,
+// after one Newton step: within 1.02 times half a step.
+__device__ __forceinline__ void sigmoid_parts(uint64_t z, uint64_t& e, uint64_t& r) {
+    float lo, hi, a, b;
+    f2_unpack(z, lo, hi);
+    e = contract_exp_x2(f2_pack(-fabsf(lo), -fabsf(hi)));
+    const uint64_t d = f2_add(e, f2_splat(1.0f));
+    f2_unpack(d, lo, hi);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(lo));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(hi));
+    const uint64_t r0 = f2_pack(a, b);
+    const uint64_t off = f2_fma(f2_pack(-lo, -hi), r0, f2_splat(1.0f));
+    r = f2_fma(r0, off, r0);
+}
+// v where z is negative, else w, a pair
+__device__ __forceinline__ uint64_t if_negative(uint64_t z, uint64_t v, uint64_t w) {
+    float z0, z1, v0, v1, w0, w1;
+    f2_unpack(z, z0, z1);
+    f2_unpack(v, v0, v1);
+    f2_unpack(w, w0, w1);
+    return f2_pack(z0 < 0.0f ? v0 : w0, z1 < 0.0f ? v1 : w1);
+}
+
 // ---------------------------------------------------------------- 8-bit checkpoints
-// What a block's byte multiplies its codes by.  Both stay exact: a code has at most 7 bits, the
-// product is a bf16 number (a subnormal one near the bottom of the range), and 255 is NaN.
+// What a block's byte multiplies its codes by: 2^(b - 133) or 2^(b - 127), the smallest ones
+// subnormal, and infinity for 255, whose codes are 0, so that the features come out as NaN.  Codes
+// have at most 7 bits, so every product is exact and a bf16 number.
 template <int kSaved>
 __device__ __forceinline__ float saved_scale(uint32_t b) {
-    uint32_t bits;
-    if (kSaved == RLK_SAVED_INT8)
-        bits = b >= 7 ? (b - 6) << 23 : 1u << (b + 16);      // 2^(b - 133)
-    else
-        bits = b > 0 ? b << 23 : 0x00400000u;                // 2^(b - 127)
-    return __uint_as_float(b == 255 ? 0x7FFFFFFFu : bits);
+    const float s = __uint_as_float(max(b << 23, 0x00400000u));
+    return kSaved == RLK_SAVED_INT8 ? __fmul_rn(s, 0x1p-6f) : s;
 }
 
 // 8 codes times their block's scale, as 4 packed pairs.
@@ -128,17 +189,6 @@ __device__ __forceinline__ void saved_decode8(uint2 codes, float scale, uint64_t
     }
 }
 
-__device__ __forceinline__ uint32_t pack_bf16x2(uint64_t v) {
-    float lo, hi;
-    f2_unpack(v, lo, hi);
-    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-    return static_cast<uint32_t>(__bfloat16_as_ushort(b.x)) |
-           (static_cast<uint32_t>(__bfloat16_as_ushort(b.y)) << 16);
-}
-__device__ __forceinline__ uint64_t unpack_bf16x2(uint32_t w) {
-    return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-}
-
 // The largest magnitude of 8 bf16 numbers, as its bits; NaN counts as the largest of all.
 __device__ __forceinline__ uint32_t amax8(uint4 w) {
     const uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
@@ -155,30 +205,102 @@ __device__ __forceinline__ uint32_t saved_byte(uint32_t amax) {
     return static_cast<uint32_t>(b > 0 ? b : 0);
 }
 
-// 8 bf16 numbers of a block with this byte, as codes.
+// 8 bf16 numbers of a block with this largest magnitude and byte, as codes.  Called by whole warps.
 template <int kSaved>
-__device__ __forceinline__ uint2 saved_encode8(uint4 x, uint32_t b) {
-    if (b == 255) return make_uint2(0u, 0u);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t q[2] = {0u, 0u};
-    // 1 / scale, in two factors where it is beyond fp32 (INT8, b below 6)
-    const int up = (kSaved == RLK_SAVED_INT8 ? 133 : 127) - static_cast<int>(b);
-    const int first = up < 127 ? up : 127;
-    const float by = __int_as_float((first + 127) << 23), more = __int_as_float((up - first + 127) << 23);
+__device__ __forceinline__ uint2 saved_encode8(uint4 x, uint32_t amax, uint32_t b) {
+    uint64_t v[4];
+    pairs_of(x, v);
+    uint32_t q[2];
+    if (kSaved == RLK_SAVED_INT8) {
+        // the code in the low bits of 1.5 * 2^23 + code, rounded to it by the addition
+        float w[8];
+        // a block that may hold 127.5 steps, which would be 128, one whose 1 / scale is beyond fp32,
+        // or one that is not finite: seldom, and then the warp takes care of all of them
+        const bool special = b < 6 || (amax & 0x7Fu) == 0x7Fu || b == 255;
+        if (__any_sync(0xffffffffu, special)) {
+            const int up = 133 - static_cast<int>(b), first = up < 127 ? up : 127;
+            const uint64_t by = f2_splat(__int_as_float((first + 127) << 23));
+            const uint64_t more = f2_splat(__int_as_float((up - first + 127) << 23));
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        const float lo = __fmul_rn(__fmul_rn(__uint_as_float(w[p] << 16), by), more);
-        const float hi = __fmul_rn(__fmul_rn(__uint_as_float(w[p] & 0xFFFF0000u), by), more);
-        uint32_t two;
-        if (kSaved == RLK_SAVED_INT8) {
-            const int a = max(-127, min(127, __float2int_rn(lo))), c = max(-127, min(127, __float2int_rn(hi)));
-            two = (static_cast<uint32_t>(a) & 0xFFu) | ((static_cast<uint32_t>(c) & 0xFFu) << 8);
+            for (int p = 0; p < 4; ++p) {
+                f2_unpack(f2_fma(f2_mul(v[p], more), by, f2_splat(0x1.8p+23f)), w[2 * p], w[2 * p + 1]);
+#pragma unroll
+                for (int k = 2 * p; k < 2 * p + 2; ++k)
+                    w[k] = b == 255 ? 0.0f : fminf(fmaxf(w[k], 0x1.8p+23f - 127.0f), 0x1.8p+23f + 127.0f);
+            }
         } else {
-            two = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+            const uint64_t by = f2_splat(__uint_as_float((260u - b) << 23));
+#pragma unroll
+            for (int p = 0; p < 4; ++p) f2_unpack(f2_fma(v[p], by, f2_splat(0x1.8p+23f)), w[2 * p], w[2 * p + 1]);
         }
-        q[p >> 1] |= two << (16 * (p & 1));
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            q[k] = __byte_perm(__byte_perm(__float_as_uint(w[4 * k]), __float_as_uint(w[4 * k + 1]), 0x0040),
+                               __byte_perm(__float_as_uint(w[4 * k + 2]), __float_as_uint(w[4 * k + 3]), 0x0040), 0x5410);
+    } else {
+        const uint64_t by = f2_splat(__uint_as_float((254u - b) << 23));
+        uint32_t two[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            float lo, hi;
+            f2_unpack(f2_mul(v[p], by), lo, hi);
+            two[p] = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+        }
+        q[0] = b == 255 ? 0u : __byte_perm(two[0], two[1], 0x5410);
+        q[1] = b == 255 ? 0u : __byte_perm(two[2], two[3], 0x5410);
     }
     return make_uint2(q[0], q[1]);
+}
+
+// ---------------------------------------------------------------- sums over a row
+// A team of kWarps warps (a power of two) adds up to three sums at once, and each of its threads
+// gets them.  The warp's part: `x` and `b` hold a lane's sums of column groups 0 and 1, `d` a single
+// one.  Each level halves the lanes that work on a sum while there is another to take the other half,
+// so three trees cost little more shuffles than one.  Every tree has the contract's shape: lanes
+// 1, 2, .. 16 apart, then the two groups, then the warps pairwise; the sum of two does not depend on
+// which is left.  Afterwards lane 0 has x's sum, lane 2 b's, lane 4 d's.
+template <bool kThree>
+__device__ __forceinline__ float warp_sums(const float (&x)[2], const float (&b)[2], float d) {
+    const int lane = threadIdx.x & 31;
+    const bool one = lane & 1, two = lane & 2, four = lane & 4;
+    const auto far = [](float v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); };
+    float v = __fadd_rn(one ? x[1] : x[0], far(one ? x[0] : x[1], 1));
+    if (kThree) {
+        const float w = __fadd_rn(one ? b[1] : b[0], far(one ? b[0] : b[1], 1));
+        v = __fadd_rn(two ? w : v, far(two ? v : w, 2));
+    } else {
+        v = __fadd_rn(v, far(v, 2));
+    }
+    d = __fadd_rn(d, far(d, 1));
+    d = __fadd_rn(d, far(d, 2));
+    v = __fadd_rn(four ? d : v, far(four ? v : d, 4));
+    v = __fadd_rn(v, far(v, 8));
+    v = __fadd_rn(v, far(v, 16));
+    const float w = __fadd_rn(v, far(v, 1));  // every lane shuffles
+    return four ? v : w;
+}
+
+// The warps' parts of a team, kept as rows of four floats: this lane's one of them, added over the
+// warps.  Sum `which` ends up in lane which * kWarps (of 16 warps sums 0 and 1 alone, at lanes 0 and 16).
+template <int kWarps>
+__device__ __forceinline__ float team_sums(const float4* part) {
+    const int lane = threadIdx.x & 31;
+    float v = reinterpret_cast<const float*>(part + (lane & (kWarps - 1)))[(lane / kWarps) & 3];
+#pragma unroll
+    for (int o = 1; o < kWarps; o <<= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+// One of the sums alone, in every lane.
+template <int kWarps>
+__device__ __forceinline__ float team_sum(const float4* part, int which) {
+    float v = reinterpret_cast<const float*>(part + (threadIdx.x & (kWarps - 1)))[which];
+#pragma unroll
+    for (int o = 1; o < kWarps; o <<= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+template <int kWarps>
+__device__ __forceinline__ void team_barrier(int team) {
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * kWarps) : "memory");
 }
 
 }  // namespace rlk

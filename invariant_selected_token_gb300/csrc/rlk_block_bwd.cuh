@@ -33,165 +33,198 @@ namespace rlk {
 namespace {
 
 constexpr int kThreads = 512;  // of a CTA, one CTA per SM
-constexpr int kStages = 2;     // a row flies while another is worked on
+constexpr int kMostStages = 4; // rows of a team in flight or at work
 constexpr int kChain = 64;     // rows that a team adds one after the other before it starts a new sum
-constexpr size_t kHeldBytes = size_t(kThreads) * 32 * sizeof(float);
+
+// What a call has of the branch: nothing (the RMSNorm's own backward), a block, or a block and a gate.
+enum Form { kNoBranch = 0, kBlock = 1, kGated = 2 };
 
 // 16-byte places of a thread's ring in one stage: 16 features of each tensor.
-template <int kGo, int kSaved>
+template <int kGo, int kSaved, int kForm>
 struct Ring {
-    static constexpr int kGoPlaces = kGo == RLK_DTYPE_F32 ? 4 : 2;
     static constexpr int kSavedPlaces = kSaved == RLK_SAVED_BF16 ? 2 : 1;
-    static constexpr int kX = kGoPlaces, kBlock = kX + kSavedPlaces, kGate = kBlock + kSavedPlaces;
-    static constexpr int kRes = kGate + kSavedPlaces;
-    // where all of them do not fit into 227 KB the residual's gradient is read as it is needed
-    static constexpr bool kHasRes = !(kGo == RLK_DTYPE_F32 && kSaved == RLK_SAVED_BF16);
+    static constexpr int kX = kGo == RLK_DTYPE_F32 ? 4 : 2, kB = kX + kSavedPlaces;
+    static constexpr int kGate = kB + (kForm >= kBlock ? kSavedPlaces : 0);
+    static constexpr int kRes = kGate + (kForm == kGated ? kSavedPlaces : 0);
+    static constexpr size_t kPlaceBytes = size_t(kThreads) * sizeof(uint4);
+    static constexpr size_t kHeldBytes = size_t(kThreads) * (kForm == kNoBranch ? 16 : 32) * sizeof(float);
+    static constexpr size_t kRoom = 232448 - 2048;  // 227 KB less what is declared shared
+    // beside two rows of sums, and a gate or scales, the gammas do not fit into 128 registers: then they
+    // are kept in shared memory where there is room (4096 x 4096, gated, int8: 66 against 84 us; a bf16
+    // block without a gate, 8191 x 8192: 137 against 132)
+    static constexpr int kGammaPlaces =
+        (kForm == kGated || (kForm == kBlock && kSaved != RLK_SAVED_BF16)) &&
+                (2 * kRes + 4) * kPlaceBytes + kHeldBytes <= kRoom ? 4 : 0;
+    // where all of them do not fit twice beside the sums the residual's gradient is read as it is needed
+    static constexpr bool kHasRes = (2 * (kRes + 2) + kGammaPlaces) * kPlaceBytes + kHeldBytes <= kRoom;
     static constexpr int kPlaces = kRes + (kHasRes ? 2 : 0);
-    static constexpr size_t kBytes = size_t(kStages) * kPlaces * kThreads * sizeof(uint4);
-    static_assert(kBytes + kHeldBytes + 1024 <= 232448, "the ring and the sums fit into shared memory");
+    static constexpr size_t kStageBytes = kPlaces * kPlaceBytes;
+    static_assert(2 * kStageBytes + kGammaPlaces * kPlaceBytes + kHeldBytes <= kRoom, "a row flies while another is worked on");
+    static constexpr int stages(bool chained) {
+        const int n = int((kRoom - kGammaPlaces * kPlaceBytes - (chained ? kHeldBytes : 0)) / kStageBytes);
+        return n < kMostStages ? n : kMostStages;
+    }
 };
 
-__device__ __forceinline__ void copy16(void* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(dst)), "l"(src) : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void copy8(void* dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ptx::smem_addr(dst)), "l"(src) : "memory");
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+// All but the newest n groups of copies have landed.
+__device__ __forceinline__ void wait_copies(int n) {
+    if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else asm volatile("cp.async.wait_group 3;" ::: "memory");
 }
 
-__device__ __forceinline__ void pairs_of(uint4 w, uint64_t (&v)[4]) {
-    v[0] = unpack_bf16x2(w.x);
-    v[1] = unpack_bf16x2(w.y);
-    v[2] = unpack_bf16x2(w.z);
-    v[3] = unpack_bf16x2(w.w);
+__device__ __forceinline__ void pairs_of_f32(uint4 lo, uint4 hi, uint64_t (&v)[4]) {
+    v[0] = f2_pack(__uint_as_float(lo.x), __uint_as_float(lo.y));
+    v[1] = f2_pack(__uint_as_float(lo.z), __uint_as_float(lo.w));
+    v[2] = f2_pack(__uint_as_float(hi.x), __uint_as_float(hi.y));
+    v[3] = f2_pack(__uint_as_float(hi.z), __uint_as_float(hi.w));
 }
-__device__ __forceinline__ uint64_t pair_of_words(uint32_t lo, uint32_t hi) {
-    return f2_pack(__uint_as_float(lo), __uint_as_float(hi));
-}
+// fp32 features lie 32 bytes a lane.  A warp copies them as they lie in memory, 512 bytes an
+// instruction, into two places of its own, 64 vectors in a row, of which every other 8 have their
+// neighbours exchanged: so the 8 lanes that a shared-memory access serves at a time find one half
+// of their features in 8 different places.
+__device__ __forceinline__ int f32_place(int vec) { return vec ^ ((vec >> 3) & 1); }
 
 // 8 features of a gradient at element i.
 __device__ __forceinline__ void load_grad(const void* base, int dtype, int64_t i, uint64_t (&v)[4]) {
     if (dtype == RLK_DTYPE_F32) {
         const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + i);
-        const uint4 a = p[0], b = p[1];
-        v[0] = pair_of_words(a.x, a.y);
-        v[1] = pair_of_words(a.z, a.w);
-        v[2] = pair_of_words(b.x, b.y);
-        v[3] = pair_of_words(b.z, b.w);
+        pairs_of_f32(p[0], p[1], v);
     } else {
         pairs_of(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i), v);
     }
 }
-__device__ __forceinline__ void store_grad(void* base, int dtype, int64_t i, const uint64_t (&v)[4]) {
-    if (dtype == RLK_DTYPE_F32) {
-        float e[8];
+__device__ __forceinline__ void store_f32(float* to, const uint64_t (&v)[4]) {
+    float e[8];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) f2_unpack(v[p], e[2 * p], e[2 * p + 1]);
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + i);
-        p[0] = make_float4(e[0], e[1], e[2], e[3]);
-        p[1] = make_float4(e[4], e[5], e[6], e[7]);
-    } else {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + i) =
-            make_uint4(pack_bf16x2(v[0]), pack_bf16x2(v[1]), pack_bf16x2(v[2]), pack_bf16x2(v[3]));
-    }
+    for (int p = 0; p < 4; ++p) f2_unpack(v[p], e[2 * p], e[2 * p + 1]);
+    reinterpret_cast<float4*>(to)[0] = make_float4(e[0], e[1], e[2], e[3]);
+    reinterpret_cast<float4*>(to)[1] = make_float4(e[4], e[5], e[6], e[7]);
 }
-
-// gate(z) and gate'(z) for a pair.  With e = e^-|z|, which does not overflow, the sigmoid is 1 or
-// e over 1 + e and its slope e over (1 + e)^2.
-__device__ __forceinline__ void gate_of(int kind, uint64_t z, uint64_t& gate, uint64_t& slope) {
-    if (kind != RLK_GATE_SIGMOID) {
-        gate = z;
-        slope = f2_splat(1.0f);
-        return;
+// Called by whole warps; a pair of lanes is in or out together.
+__device__ __forceinline__ void store_grad(void* base, int dtype, int64_t i, bool in, const uint64_t (&v)[4]) {
+    if (dtype == RLK_DTYPE_F32) {
+        // even lanes hand their last four features over for the odd ones' first four, so that a lane
+        // pair stores whole sectors
+        const bool odd = threadIdx.x & 1;
+        const uint64_t r0 = __shfl_xor_sync(0xffffffffu, odd ? v[0] : v[2], 1);
+        const uint64_t r1 = __shfl_xor_sync(0xffffffffu, odd ? v[1] : v[3], 1);
+        float e[8];
+        f2_unpack(odd ? r0 : v[0], e[0], e[1]);
+        f2_unpack(odd ? r1 : v[1], e[2], e[3]);
+        f2_unpack(odd ? v[2] : r0, e[4], e[5]);
+        f2_unpack(odd ? v[3] : r1, e[6], e[7]);
+        if (in) {
+            float* const to = static_cast<float*>(base) + i - (odd ? 4 : 0);
+            *reinterpret_cast<float4*>(to) = make_float4(e[0], e[1], e[2], e[3]);
+            *reinterpret_cast<float4*>(to + 8) = make_float4(e[4], e[5], e[6], e[7]);
+        }
+    } else if (in) {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + i) = words_of(v);
     }
-    float v[2], g[2], s[2];
-    f2_unpack(z, v[0], v[1]);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const float e = exp_any(-fabsf(v[k])), r = __fdiv_rn(1.0f, __fadd_rn(1.0f, e));
-        g[k] = v[k] < 0.0f ? __fmul_rn(e, r) : r;
-        s[k] = __fmul_rn(__fmul_rn(e, r), r);
-    }
-    gate = f2_pack(g[0], g[1]);
-    slope = f2_pack(s[0], s[1]);
 }
 
 // A team of kWarps warps (a power of two) takes a row, a CTA's teams every kTeams-th row of its
-// range.  A thread copies its own features of the next row into its own places of a ring of shared
-// memory, which needs no barrier; the copies fly while the current row is reduced.
-template <int kWarps, int kGo, int kSaved>
-__global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const BlockBwdArgs a) {
-    using R = Ring<kGo, kSaved>;
+// range.  A thread copies its own features of the next rows into its own places of a ring of shared
+// memory, which needs no barrier; the copies fly while the current row is reduced.  Places of features
+// behind the row's end hold zeros.
+template <int kWarps, int kGo, int kSaved, int kForm>
+__global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const BlockBwdArgs a, const int stages) {
+    using R = Ring<kGo, kSaved, kForm>;
     constexpr int kTeams = kThreads / 32 / kWarps;
+    constexpr bool kPlain = kSaved == RLK_SAVED_BF16;
     static_assert(kWarps == 1 || kTeams <= 15, "a named barrier (1 .. 15) per team");
     extern __shared__ uint4 ring[];  // [stage][place][thread]
     __shared__ __align__(16) float4 part[2][kThreads / 32];
     ptx::grid_dependents_launch();
     const int lane = threadIdx.x & 31, team = threadIdx.x / (32 * kWarps);
-    const int warp = (threadIdx.x >> 5) % kWarps;
+    const int warp_of_cta = threadIdx.x >> 5, warp = warp_of_cta % kWarps;
     const int i0 = 512 * warp + 8 * lane;  // and i0 + 256
+    const int f32_left = a.H - 512 * warp - 4 * lane;  // from this lane's first vector of fp32 features on
     const bool in[2] = {i0 < a.H, i0 + 256 < a.H};
-    const int64_t r0 = static_cast<int64_t>(a.T) * blockIdx.x / gridDim.x;
-    const int64_t r1 = static_cast<int64_t>(a.T) * (blockIdx.x + 1) / gridDim.x;
+    // rows stay below 2^31 - 2^20, and a team looks at most 64 rows past the last
+    const int r0 = static_cast<int>(static_cast<int64_t>(a.T) * blockIdx.x / gridDim.x);
+    const int r1 = static_cast<int>(static_cast<int64_t>(a.T) * (blockIdx.x + 1) / gridDim.x);
     const bool pow2 = (a.H & (a.H - 1)) == 0;
     const float h = static_cast<float>(a.H), inv_h = __fdiv_rn(1.0f, h);
-    const int odd = lane & 1;
-    const bool branch = a.block.data != nullptr, post = a.gamma_post != nullptr, gated = a.gate.data != nullptr;
+    const bool post = kForm != kNoBranch && a.gamma_post != nullptr;
     const bool res_in_ring = R::kHasRes && a.grad_res && a.gx_dtype == RLK_DTYPE_BF16;
+    for (int k = 0; k < stages * R::kPlaces; ++k) ring[k * kThreads + threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t mine = ptx::smem_addr(ring + threadIdx.x);
     auto place = [&](int stage, int k) { return ring + (stage * R::kPlaces + k) * kThreads + threadIdx.x; };
 
-    auto fetch_saved = [&](const SavedIn& s, int64_t i, int stage, int k, int g) {
-        if (kSaved == RLK_SAVED_BF16)
-            copy16(place(stage, k + g), static_cast<const uint16_t*>(s.data) + i);
-        else
-            copy8(reinterpret_cast<uint2*>(place(stage, k)) + g, static_cast<const uint8_t*>(s.data) + i);
+    // i: this thread's first element of the row, t the row
+    auto fetch_saved = [&](const SavedIn& s, int64_t i, uint32_t to, int g) {
+        if (kPlain) copy16(to + g * (kThreads * 16), static_cast<const uint16_t*>(s.data) + i + 256 * g);
+        else copy8(to + g * 8, static_cast<const uint8_t*>(s.data) + i + 256 * g);
     };
-    auto fetch = [&](int64_t t, int stage) {
+    auto fetch = [&](int t, int64_t i, int stage) {
         if (t < r1) {
+            const uint32_t to = mine + static_cast<uint32_t>(stage) * uint32_t(R::kStageBytes);
+            constexpr uint32_t kStep = kThreads * 16;
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                if (!in[g]) continue;
-                const int64_t i = t * a.H + i0 + 256 * g;
                 if (kGo == RLK_DTYPE_F32) {
-                    copy16(place(stage, 2 * g), static_cast<const float*>(a.grad_out) + i);
-                    copy16(place(stage, 2 * g + 1), static_cast<const float*>(a.grad_out) + i + 4);
-                } else {
-                    copy16(place(stage, g), static_cast<const uint16_t*>(a.grad_out) + i);
+                    // the warp's 64 vectors of this group, two places; this lane's share are lane and lane + 32
+                    const float* from = static_cast<const float*>(a.grad_out) + i + 256 * g - 4 * lane;
+                    const uint32_t at = to + 2 * g * kStep + (32 * warp_of_cta + f32_place(lane) - lane) * 16;
+                    if (f32_left > 256 * g) copy16(at, from);
+                    if (f32_left > 256 * g + 128) copy16(at + 32 * 16, from + 128);
                 }
-                fetch_saved(a.x, i, stage, R::kX, g);
-                if (branch) fetch_saved(a.block, i, stage, R::kBlock, g);
-                if (gated) fetch_saved(a.gate, i, stage, R::kGate, g);
-                if (res_in_ring) copy16(place(stage, R::kRes + g), static_cast<const uint16_t*>(a.grad_res) + i);
+                if (!in[g]) continue;
+                if (kGo == RLK_DTYPE_BF16) copy16(to + g * kStep, static_cast<const uint16_t*>(a.grad_out) + i + 256 * g);
+                fetch_saved(a.x, i, to + R::kX * kStep, g);
+                if constexpr (kForm >= kBlock) fetch_saved(a.block, i, to + R::kB * kStep, g);
+                if constexpr (kForm == kGated) fetch_saved(a.gate, i, to + R::kGate * kStep, g);
+                if (res_in_ring) copy16(to + (R::kRes + g) * kStep, static_cast<const uint16_t*>(a.grad_res) + i + 256 * g);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     // the bytes of this thread's blocks of 32 features, a row ahead
     uint32_t next[3][2] = {};
-    auto fetch_scales = [&](int64_t t) {
-        if constexpr (kSaved != RLK_SAVED_BF16) {
+    auto fetch_scales = [&](int t, int64_t i) {
+        if constexpr (!kPlain) {
+            if (t >= r1) return;
+            const int64_t k = i >> 5;
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                if (!in[g] || t >= r1) continue;
-                const int64_t k = (t * a.H + i0 + 256 * g) >> 5;
-                next[0][g] = a.x.scales[k];
-                if (branch) next[1][g] = a.block.scales[k];
-                if (gated) next[2][g] = a.gate.scales[k];
+                if (!in[g]) continue;
+                next[0][g] = a.x.scales[k + 8 * g];
+                if constexpr (kForm >= kBlock) next[1][g] = a.block.scales[k + 8 * g];
+                if constexpr (kForm == kGated) next[2][g] = a.gate.scales[k + 8 * g];
             }
         }
     };
-    uint4 gam_pre[2] = {}, gam_post[2] = {};
+    uint4 gam[4] = {};  // pre, post
+    uint4* const gammas = ring + stages * R::kPlaces * kThreads + threadIdx.x;
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-        if (in[g]) gam_pre[g] = *reinterpret_cast<const uint4*>(a.gamma_pre + i0 + 256 * g);
-        if (in[g] && post) gam_post[g] = *reinterpret_cast<const uint4*>(a.gamma_post + i0 + 256 * g);
+        if (in[g]) gam[g] = *reinterpret_cast<const uint4*>(a.gamma_pre + i0 + 256 * g);
+        if (in[g] && post) gam[2 + g] = *reinterpret_cast<const uint4*>(a.gamma_post + i0 + 256 * g);
     }
+    if constexpr (R::kGammaPlaces != 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) gammas[k * kThreads] = gam[k];
+    }
+    auto read_gamma = [&](int k, uint64_t (&v)[4]) {
+        if constexpr (R::kGammaPlaces != 0) pairs_of(gammas[k * kThreads], v);
+        else pairs_of(gam[k], v);
+    };
     uint64_t d_pre[2][4] = {}, d_post[2][4] = {};
-    ulonglong2* const held = reinterpret_cast<ulonglong2*>(ring + kStages * R::kPlaces * kThreads) + threadIdx.x;
+    ulonglong2* const held = reinterpret_cast<ulonglong2*>(gammas + R::kGammaPlaces * kThreads);
     auto each_held = [&](auto fn) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             fn(held[k * kThreads], d_pre[k >> 1][2 * (k & 1)], d_pre[k >> 1][2 * (k & 1) + 1]);
-            fn(held[(4 + k) * kThreads], d_post[k >> 1][2 * (k & 1)], d_post[k >> 1][2 * (k & 1) + 1]);
+            if constexpr (kForm != kNoBranch)
+                fn(held[(4 + k) * kThreads], d_post[k >> 1][2 * (k & 1)], d_post[k >> 1][2 * (k & 1) + 1]);
         }
     };
     auto add_held = [&] {
@@ -206,118 +239,85 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
             x = y = 0;
         });
     };
-    const bool chained = (a.T + static_cast<int64_t>(gridDim.x) - 1) / gridDim.x > kChain * kTeams;
+    const bool chained = block_bwd_chained(a.T, gridDim.x, kTeams);
     if (chained) move_to_held();  // zeros
-    int64_t t = r0 + team, chain_end = t + kChain * kTeams;
-#pragma unroll
-    for (int k = 0; k < kStages; ++k) fetch(t + k * kTeams, k);
-    fetch_scales(t);
+    int t = r0 + team, chain_end = t + kChain * kTeams;
+    int64_t i = static_cast<int64_t>(t) * a.H + i0;
+    const int64_t step = static_cast<int64_t>(kTeams) * a.H;
+    for (int k = 0; k < kMostStages; ++k)
+        if (k < stages) fetch(t + k * kTeams, i + k * step, k);
+    fetch_scales(t, i);
     int slot = 0, stage = 0;
-    for (; t < r1; t += kTeams) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-        uint32_t bytes[3][2];
+    for (; t < r1; t += kTeams, i += step) {
+        wait_copies(stages - 1);
+        if (kGo == RLK_DTYPE_F32) __syncwarp();  // the lanes of a warp share what they copied
+        float scale[3][2];
+        if constexpr (!kPlain) {
 #pragma unroll
-        for (int k = 0; k < 3; ++k) bytes[k][0] = next[k][0], bytes[k][1] = next[k][1];
-        fetch_scales(t + kTeams);
+            for (int k = 0; k < 3; ++k)
+#pragma unroll
+                for (int g = 0; g < 2; ++g) scale[k][g] = saved_scale<kSaved>(next[k][g]);
+            fetch_scales(t + kTeams, i + step);
+        }
         auto read_dy = [&](int g, uint64_t (&v)[4]) {
-            if (kGo == RLK_DTYPE_F32) {
-                const uint4 lo = in[g] ? *place(stage, 2 * g) : uint4{}, hi = in[g] ? *place(stage, 2 * g + 1) : uint4{};
-                v[0] = pair_of_words(lo.x, lo.y);
-                v[1] = pair_of_words(lo.z, lo.w);
-                v[2] = pair_of_words(hi.x, hi.y);
-                v[3] = pair_of_words(hi.z, hi.w);
+            if constexpr (kGo == RLK_DTYPE_F32) {
+                const uint4* const own = place(stage, 2 * g) + 32 * warp_of_cta - lane;  // the warp's 64 vectors
+                const int at = f32_place(2 * lane);
+                pairs_of_f32(own[at], own[at ^ 1], v);
             } else {
-                pairs_of(in[g] ? *place(stage, g) : uint4{}, v);
+                pairs_of(*place(stage, g), v);
             }
         };
         auto read_saved = [&](int which, int k, int g, uint64_t (&v)[4]) {
-            if (kSaved == RLK_SAVED_BF16) {
-                pairs_of(in[g] ? *place(stage, k + g) : uint4{}, v);
-            } else {
-                const uint2 q = in[g] ? reinterpret_cast<const uint2*>(place(stage, k))[g] : uint2{};
-                saved_decode8<kSaved>(q, saved_scale<kSaved>(bytes[which][g]), v);
-            }
-        };
-        auto squares = [](const uint64_t (&v)[4]) {
-            float s2[4];
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                float lo, hi;
-                f2_unpack(f2_mul(v[p], v[p]), lo, hi);
-                s2[p] = __fadd_rn(lo, hi);
-            }
-            return __fadd_rn(__fadd_rn(s2[0], s2[1]), __fadd_rn(s2[2], s2[3]));
+            if constexpr (kPlain) pairs_of(*place(stage, k + g), v);
+            else saved_decode8<kSaved>(reinterpret_cast<const uint2*>(place(stage, k))[g], scale[which][g], v);
         };
         // the forward's tree over the squares of x and of the block, and up . x
-        float sx[2], sb[2] = {0.0f, 0.0f};
+        float sx[2], sb[2] = {0.0f, 0.0f}, d0, d1;
         uint64_t dot = 0;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
             uint64_t x[4], dy[4], gam[4];
             read_saved(0, R::kX, g, x);
             read_dy(g, dy);
-            pairs_of(gam_pre[g], gam);
-            sx[g] = squares(x);
+            read_gamma(g, gam);
+            sx[g] = squares_of(x);
 #pragma unroll
             for (int p = 0; p < 4; ++p) dot = f2_fma(f2_mul(dy[p], gam[p]), x[p], dot);
             if (post) {
-                read_saved(1, R::kBlock, g, x);
-                sb[g] = squares(x);
+                read_saved(1, R::kB, g, x);
+                sb[g] = squares_of(x);
             }
         }
-        auto across = [&](float s0, float s1) {  // both groups over the lanes, then one group and the other
-            float q = __fadd_rn(odd ? s1 : s0, __shfl_xor_sync(0xffffffffu, odd ? s0 : s1, 1));
-#pragma unroll
-            for (int o = 2; o < 32; o <<= 1) q = __fadd_rn(q, __shfl_xor_sync(0xffffffffu, q, o));
-            return __fadd_rn(q, __shfl_xor_sync(0xffffffffu, q, 1));
-        };
-        float d0, d1;
         f2_unpack(dot, d0, d1);
-        float q = across(sx[0], sx[1]), qb = post ? across(sb[0], sb[1]) : 0.0f;
-        float d = __fadd_rn(d0, d1);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) d = __fadd_rn(d, __shfl_xor_sync(0xffffffffu, d, o));
-        if constexpr (kWarps > 1) {
-            if (lane == 0) part[slot][team * kWarps + warp] = make_float4(q, d, qb, 0.0f);
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * kWarps) : "memory");
-            float4 p[kWarps];
-#pragma unroll
-            for (int i = 0; i < kWarps; ++i) p[i] = part[slot][team * kWarps + i];
-#pragma unroll
-            for (int n = kWarps / 2; n >= 1; n >>= 1) {
-#pragma unroll
-                for (int i = 0; i < n; ++i) {
-                    p[i].x = __fadd_rn(p[2 * i].x, p[2 * i + 1].x);
-                    p[i].y = __fadd_rn(p[2 * i].y, p[2 * i + 1].y);
-                    p[i].z = __fadd_rn(p[2 * i].z, p[2 * i + 1].z);
-                }
-            }
-            q = p[0].x;
-            d = p[0].y;
-            qb = p[0].z;
-            slot ^= 1;  // a team's warps are never more than one sum apart
+        float sums = warp_sums<kForm != kNoBranch>(sx, sb, __fadd_rn(d0, d1));
+        float d;
+        if constexpr (kWarps == 1) {
+            d = __shfl_sync(0xffffffffu, sums, 4);
+        } else {
+            if (lane < 6 && !(lane & 1)) reinterpret_cast<float*>(&part[slot][team * kWarps + warp])[lane >> 1] = sums;
+            team_barrier<kWarps>(team);
+            sums = team_sums<kWarps>(&part[slot][team * kWarps]);
+            d = kWarps <= 8 ? __shfl_sync(0xffffffffu, sums, (2 * kWarps) & 31) : team_sum<kWarps>(&part[slot][team * kWarps], 2);
         }
         // a product with 1 / H is the quotient itself where H is a power of two
-        auto rstd_of = [&](float sum) {
-            return contract_rsqrt(__fadd_rn(pow2 ? __fmul_rn(sum, inv_h) : __fdiv_rn(sum, h), a.eps));
-        };
-        const float rstd = rstd_of(q);
+        const float root = contract_rsqrt(__fadd_rn(pow2 ? __fmul_rn(sums, inv_h) : __fdiv_rn(sums, h), a.eps));
+        const float rstd = __shfl_sync(0xffffffffu, root, 0);
+        const float rstd_b = post ? __shfl_sync(0xffffffffu, root, kWarps == 1 ? 2 : kWarps) : 1.0f;
         const float c = __fmul_rn(__fmul_rn(rstd, rstd), __fmul_rn(d, inv_h));
-        const uint64_t rstd2 = f2_splat(rstd), neg_c2 = f2_splat(-c);
-        const float rstd_b = post ? rstd_of(qb) : 1.0f;
-        const uint64_t rstd_b2 = f2_splat(rstd_b);
+        const uint64_t rstd2 = f2_splat(rstd), neg_c2 = f2_splat(-c), rstd_b2 = f2_splat(rstd_b);
         uint64_t v[2][4];  // the gradient that reaches the branch's norm, times gamma_post
         uint64_t dot_b = 0;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-            const int64_t at = t * a.H + i0 + 256 * g;
+            const int64_t at = i + 256 * g;
             uint64_t dx[4];
             {
                 uint64_t x[4], dy[4], gam[4], res[4] = {};
                 read_saved(0, R::kX, g, x);
                 read_dy(g, dy);
-                pairs_of(gam_pre[g], gam);
-                if (res_in_ring) pairs_of(in[g] ? *place(stage, R::kRes + g) : uint4{}, res);
+                read_gamma(g, gam);
+                if (res_in_ring) pairs_of(*place(stage, R::kRes + g), res);
                 else if (a.grad_res && in[g]) load_grad(a.grad_res, a.gx_dtype, at, res);
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
@@ -325,30 +325,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
                     d_pre[g][p] = f2_fma(dy[p], f2_mul(x[p], rstd2), d_pre[g][p]);
                 }
             }
-            if (a.grad_residual && in[g]) {
+            if (a.grad_residual) {
                 uint64_t o[4];
 #pragma unroll
                 for (int p = 0; p < 4; ++p) o[p] = f2_mul(f2_splat(a.residual_scale), dx[p]);
-                store_grad(a.grad_residual, a.gx_dtype, at, o);
+                store_grad(a.grad_residual, a.gx_dtype, at, in[g], o);
             }
 #pragma unroll
             for (int p = 0; p < 4; ++p) v[g][p] = f2_mul(f2_splat(a.block_scale), dx[p]);
-            if (branch) {
+            if constexpr (kForm != kNoBranch) {
                 uint64_t b[4], gam[4];
-                read_saved(1, R::kBlock, g, b);
-                pairs_of(gam_post[g], gam);
-                if (gated) {
+                read_saved(1, R::kB, g, b);
+                read_gamma(2 + g, gam);
+                if constexpr (kForm == kGated) {
                     uint64_t z[4], o[4];
                     read_saved(2, R::kGate, g, z);
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
-                        uint64_t gate, slope;
-                        gate_of(a.gate_kind, z[p], gate, slope);
                         const uint64_t n = post ? f2_mul(f2_mul(b[p], rstd_b2), gam[p]) : b[p];
-                        o[p] = f2_mul(f2_mul(v[g][p], n), slope);
-                        v[g][p] = f2_mul(v[g][p], gate);
+                        o[p] = f2_mul(v[g][p], n);
+                        if (a.gate_kind == RLK_GATE_SIGMOID) {
+                            uint64_t e, r;
+                            sigmoid_parts(z[p], e, r);
+                            const uint64_t er = f2_mul(e, r);
+                            o[p] = f2_mul(o[p], f2_mul(er, r));
+                            z[p] = if_negative(z[p], er, r);
+                        }
+                        v[g][p] = f2_mul(v[g][p], z[p]);
                     }
-                    if (a.grad_gate && in[g]) store_grad(a.grad_gate, a.gx_dtype, at, o);
+                    if (a.grad_gate) store_grad(a.grad_gate, a.gx_dtype, at, in[g], o);
                 }
                 if (post) {
 #pragma unroll
@@ -359,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
                     }
                 }
             }
-            if (!post && a.grad_block && in[g]) store_grad(a.grad_block, a.gx_dtype, at, v[g]);
+            if (!post && a.grad_block) store_grad(a.grad_block, a.gx_dtype, at, in[g], v[g]);
         }
         if (post && a.grad_block) {
             f2_unpack(dot_b, d0, d1);
@@ -367,31 +372,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) k = __fadd_rn(k, __shfl_xor_sync(0xffffffffu, k, o));
             if constexpr (kWarps > 1) {
-                if (lane == 0) part[slot][team * kWarps + warp].x = k;
-                asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * kWarps) : "memory");
-                float p[kWarps];
-#pragma unroll
-                for (int i = 0; i < kWarps; ++i) p[i] = part[slot][team * kWarps + i].x;
-#pragma unroll
-                for (int n = kWarps / 2; n >= 1; n >>= 1) {
-#pragma unroll
-                    for (int i = 0; i < n; ++i) p[i] = __fadd_rn(p[2 * i], p[2 * i + 1]);
-                }
-                k = p[0];
-                slot ^= 1;
+                // a place of its own in this row's slot; the next row takes the other one
+                if (lane == 0) part[slot][team * kWarps + warp].w = k;
+                team_barrier<kWarps>(team);
+                k = team_sum<kWarps>(&part[slot][team * kWarps], 3);
             }
             const uint64_t neg_k2 = f2_splat(-__fmul_rn(__fmul_rn(rstd_b, rstd_b), __fmul_rn(k, inv_h)));
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
                 uint64_t b[4], o[4];
-                read_saved(1, R::kBlock, g, b);
+                read_saved(1, R::kB, g, b);
 #pragma unroll
                 for (int p = 0; p < 4; ++p) o[p] = f2_mul(rstd_b2, f2_fma(b[p], neg_k2, v[g][p]));
-                if (in[g]) store_grad(a.grad_block, a.gx_dtype, t * a.H + i0 + 256 * g, o);
+                store_grad(a.grad_block, a.gx_dtype, i + 256 * g, in[g], o);
             }
         }
-        fetch(t + kStages * kTeams, stage);  // everything in this stage has been used
-        stage = stage + 1 < kStages ? stage + 1 : 0;
+        slot ^= 1;  // a team's warps are never more than one row apart
+        if (kGo == RLK_DTYPE_F32) __syncwarp();
+        fetch(t + stages * kTeams, i + stages * step, stage);  // everything in this stage has been used
+        stage = stage + 1 < stages ? stage + 1 : 0;
         if (chained && t + kTeams == chain_end) {
             add_held();
             move_to_held();
@@ -406,48 +405,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
     float* const teams = reinterpret_cast<float*>(ring);
     float* const out = a.parts + static_cast<int64_t>(blockIdx.x) * 2 * a.H;
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
+    for (int which = 0; which < (kForm == kNoBranch ? 1 : 2); ++which) {
         uint64_t(&sum)[2][4] = which == 0 ? d_pre : d_post;
         if constexpr (kTeams == 1) {
 #pragma unroll
             for (int g = 0; g < 2; ++g)
-                if (in[g]) store_grad(out + which * a.H, RLK_DTYPE_F32, i0 + 256 * g, sum[g]);
+                if (in[g]) store_f32(out + which * a.H + i0 + 256 * g, sum[g]);
         } else {
             __syncthreads();
 #pragma unroll
-            for (int g = 0; g < 2; ++g) store_grad(teams, RLK_DTYPE_F32, team * kWarps * 512 + i0 + 256 * g, sum[g]);
+            for (int g = 0; g < 2; ++g) store_f32(teams + team * kWarps * 512 + i0 + 256 * g, sum[g]);
             __syncthreads();
-            for (int i = threadIdx.x; i < a.H; i += kThreads) {
-                float s = teams[i];
+            for (int k = threadIdx.x; k < a.H; k += kThreads) {
+                float s = teams[k];
 #pragma unroll
-                for (int k = 1; k < kTeams; ++k) s = __fadd_rn(s, teams[k * kWarps * 512 + i]);
-                out[which * a.H + i] = s;
+                for (int n = 1; n < kTeams; ++n) s = __fadd_rn(s, teams[n * kWarps * 512 + k]);
+                out[which * a.H + k] = s;
             }
         }
     }
 }
 
-// The grad_gammas from the ranges' sums: 32 threads per feature, each taking every 32nd range in
-// ascending order, then pairwise.
-__global__ void __launch_bounds__(1024)
-    k_gamma_sums(const float* parts, int ranges, int H, float* grad_pre, float* grad_post) {
-    __shared__ float smem[32][33];
-    const int c = threadIdx.x & 31, row = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
-    ptx::grid_dependency_wait();
-    float s = 0.0f;
-#pragma unroll 5
-    for (int r = row; r < ranges; r += 32) s = __fadd_rn(s, parts[static_cast<int64_t>(r) * 2 * H + col]);
-    smem[row][c] = s;
-    __syncthreads();
-    s = warp_sum(smem[c][row]);  // feature `row` of the CTA's 32, one range class per lane
-    const int at = blockIdx.x * 32 + row;
-    if (c == 0 && at < H && grad_pre) grad_pre[at] = s;
-    if (c == 0 && at >= H && grad_post) grad_post[at - H] = s;
-}
-
-template <int kWarps, int kGo, int kSaved>
-cudaError_t launch_row(const BlockBwdArgs& a, int blocks, cudaStream_t stream) {
-    constexpr size_t kSmem = Ring<kGo, kSaved>::kBytes + kHeldBytes;
+template <int kWarps, int kGo, int kSaved, int kForm>
+cudaError_t launch_form(const BlockBwdArgs& a, int blocks, cudaStream_t stream) {
+    using R = Ring<kGo, kSaved, kForm>;
+    const bool chained = block_bwd_chained(a.T, blocks, kThreads / 32 / kWarps);
+    const int stages = R::stages(chained);
     // once per device and kernel: the runtime keeps it, and asking each time costs the host 1 us
     static std::atomic<uint64_t> ready{0};
     int dev = 0;
@@ -455,46 +438,36 @@ cudaError_t launch_row(const BlockBwdArgs& a, int blocks, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
     if (!(ready.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(k_block_norm_backward<kWarps, kGo, kSaved>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+        e = cudaFuncSetAttribute(k_block_norm_backward<kWarps, kGo, kSaved, kForm>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, int(R::kRoom));
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);
     }
-    k_block_norm_backward<kWarps, kGo, kSaved><<<blocks, kThreads, kSmem, stream>>>(a);
+    const size_t smem = stages * R::kStageBytes + R::kGammaPlaces * R::kPlaceBytes + (chained ? R::kHeldBytes : 0);
+    k_block_norm_backward<kWarps, kGo, kSaved, kForm><<<blocks, kThreads, smem, stream>>>(a, stages);
     return cudaGetLastError();
 }
 
-template <int kSaved>
-cudaError_t launch_block_bwd(const BlockBwdArgs& a, cudaStream_t stream) {
-    const int blocks = block_bwd_ranges(a.T);
+template <int kWarps, int kGo, int kSaved>
+cudaError_t launch_row(const BlockBwdArgs& a, int blocks, cudaStream_t stream) {
+    if (!a.block.data) return launch_form<kWarps, kGo, kSaved, kNoBranch>(a, blocks, stream);
+    return a.gate.data ? launch_form<kWarps, kGo, kSaved, kGated>(a, blocks, stream)
+                       : launch_form<kWarps, kGo, kSaved, kBlock>(a, blocks, stream);
+}
+
+// grad_out's types apart, a translation unit each
+template <int kGo, int kSaved>
+cudaError_t launch_rows(const BlockBwdArgs& a, int blocks, cudaStream_t stream) {
     int warps = 1;
     while (warps * 512 < a.H) warps *= 2;
-    cudaError_t e = cudaSuccess;
-#define RLK_ROW(W)                                                                                  \
-    case W:                                                                                         \
-        e = a.go_dtype == RLK_DTYPE_F32 ? launch_row<W, RLK_DTYPE_F32, kSaved>(a, blocks, stream)   \
-                                        : launch_row<W, RLK_DTYPE_BF16, kSaved>(a, blocks, stream); \
-        break
-    if (blocks > 0) switch (warps) {
-        RLK_ROW(1);
-        RLK_ROW(2);
-        RLK_ROW(4);
-        RLK_ROW(8);
-        RLK_ROW(16);
+    switch (warps) {
+        case 1: return launch_row<1, kGo, kSaved>(a, blocks, stream);
+        case 2: return launch_row<2, kGo, kSaved>(a, blocks, stream);
+        case 4: return launch_row<4, kGo, kSaved>(a, blocks, stream);
+        case 8: return launch_row<8, kGo, kSaved>(a, blocks, stream);
+        case 16: return launch_row<16, kGo, kSaved>(a, blocks, stream);
         default: return cudaErrorInvalidValue;
     }
-#undef RLK_ROW
-    if (e != cudaSuccess || (!a.grad_pre && !a.grad_post)) return e;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3(2 * a.H / 32, 1, 1);
-    cfg.blockDim = dim3(1024, 1, 1);
-    cfg.stream = stream;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_gamma_sums, static_cast<const float*>(a.parts), blocks, a.H, a.grad_pre, a.grad_post);
 }
 
 }  // namespace

@@ -1,0 +1,10 @@
+// The block norms' backward from bf16 activations, bf16 grad_out.
+#include "rlk_block_bwd.cuh"
+
+namespace rlk {
+
+cudaError_t launch_block_bwd_bf16_bf16(const BlockBwdArgs& a, int blocks, cudaStream_t stream) {
+    return launch_rows<RLK_DTYPE_BF16, RLK_SAVED_BF16>(a, blocks, stream);
+}
+
+}  // namespace rlk

@@ -18,18 +18,11 @@
 #include <cstdint>
 
 #include "rlk_block.cuh"
-#include "rlk_train.cuh"
 
 namespace rlk {
 namespace {
 
 constexpr int cta_threads(int warps) { return 32 * warps > 128 ? 32 * warps : 128; }
-
-// 1 / (1 + e^-z), from e^-|z|, which does not overflow.
-__device__ __forceinline__ float sigmoid(float z) {
-    const float e = exp_any(-fabsf(z));
-    return __fdiv_rn(z < 0.0f ? e : 1.0f, __fadd_rn(1.0f, e));
-}
 
 template <int kSaved>
 __device__ __forceinline__ void save_group(const SavedOut& to, uint4 x, int64_t at, bool in) {
@@ -37,8 +30,9 @@ __device__ __forceinline__ void save_group(const SavedOut& to, uint4 x, int64_t 
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const uint32_t byte = saved_byte<kSaved>(m);
+    const uint2 codes = saved_encode8<kSaved>(x, m, byte);
     if (!in) return;
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(to.codes) + at) = saved_encode8<kSaved>(x, byte);
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(to.codes) + at) = codes;
     if (!(threadIdx.x & 3)) to.scales[at >> 5] = static_cast<uint8_t>(byte);
 }
 
@@ -52,43 +46,28 @@ __global__ void __launch_bounds__(cta_threads(kWarps)) k_block_norm(const BlockN
     const int i0 = 512 * warp + 8 * lane;  // and i0 + 256
     const bool in[2] = {i0 < a.H, i0 + 256 < a.H};
     const int odd = lane & 1;
-    const float h = static_cast<float>(a.H);
+    const bool pow2 = (a.H & (a.H - 1)) == 0;
+    const float h = static_cast<float>(a.H), inv_h = __fdiv_rn(1.0f, h);
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kTeams;
 
     // rstd of the row whose 16 features are v: the contract's tree
     auto rstd_of = [&](const uint64_t (&v)[2][4], int slot) {
-        float s[2];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            float s2[4];
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                float lo, hi;
-                f2_unpack(f2_mul(v[g][p], v[g][p]), lo, hi);
-                s2[p] = __fadd_rn(lo, hi);
-            }
-            s[g] = __fadd_rn(__fadd_rn(s2[0], s2[1]), __fadd_rn(s2[2], s2[3]));
-        }
+        const float s0 = squares_of(v[0]), s1 = squares_of(v[1]);
         // even lanes go on with the first group, odd ones with the second
-        float q = __fadd_rn(odd ? s[1] : s[0], __shfl_xor_sync(0xffffffffu, odd ? s[0] : s[1], 1));
+        float q = __fadd_rn(odd ? s1 : s0, __shfl_xor_sync(0xffffffffu, odd ? s0 : s1, 1));
 #pragma unroll
         for (int o = 2; o < 32; o <<= 1) q = __fadd_rn(q, __shfl_xor_sync(0xffffffffu, q, o));
         q = __fadd_rn(q, __shfl_xor_sync(0xffffffffu, q, 1));
         if constexpr (kWarps > 1) {
             // two slots alternate: a team's warps are never more than one sum apart
             if (lane == 0) part[team][slot][warp] = q;
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * kWarps) : "memory");
-            float p[kWarps];
+            team_barrier<kWarps>(team);
+            q = part[team][slot][lane & (kWarps - 1)];
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) p[i] = part[team][slot][i];
-#pragma unroll
-            for (int n = kWarps / 2; n >= 1; n >>= 1) {
-#pragma unroll
-                for (int i = 0; i < n; ++i) p[i] = __fadd_rn(p[2 * i], p[2 * i + 1]);
-            }
-            q = p[0];
+            for (int o = 1; o < kWarps; o <<= 1) q = __fadd_rn(q, __shfl_xor_sync(0xffffffffu, q, o));
         }
-        return contract_rsqrt(__fadd_rn(__fdiv_rn(q, h), a.eps));
+        // a product with 1 / H is the quotient itself where H is a power of two
+        return contract_rsqrt(__fadd_rn(pow2 ? __fmul_rn(q, inv_h) : __fdiv_rn(q, h), a.eps));
     };
     auto load = [&](const uint16_t* base, int64_t row, uint4 (&w)[2]) {
 #pragma unroll
@@ -96,12 +75,8 @@ __global__ void __launch_bounds__(cta_threads(kWarps)) k_block_norm(const BlockN
             w[g] = in[g] ? *reinterpret_cast<const uint4*>(base + row + i0 + 256 * g) : make_uint4(0u, 0u, 0u, 0u);
     };
     auto pairs = [](const uint4 (&w)[2], uint64_t (&v)[2][4]) {
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            const uint32_t q[4] = {w[g].x, w[g].y, w[g].z, w[g].w};
-#pragma unroll
-            for (int p = 0; p < 4; ++p) v[g][p] = unpack_bf16x2(q[p]);
-        }
+        pairs_of(w[0], v[0]);
+        pairs_of(w[1], v[1]);
     };
 
     int slot = 0;
@@ -140,9 +115,9 @@ __global__ void __launch_bounds__(cta_threads(kWarps)) k_block_norm(const BlockN
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
                     if (a.gate_kind == RLK_GATE_SIGMOID) {
-                        float lo, hi;
-                        f2_unpack(z[g][p], lo, hi);
-                        z[g][p] = f2_pack(sigmoid(lo), sigmoid(hi));
+                        uint64_t e, r;
+                        sigmoid_parts(z[g][p], e, r);
+                        z[g][p] = if_negative(z[g][p], f2_mul(e, r), r);
                     }
                     n[g][p] = f2_mul(n[g][p], z[g][p]);
                 }

@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(kThreads)
         uint32_t m = max(amax8(a), amax8(b));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         const uint32_t byte = saved_byte<kSaved>(m);
-        const uint2 lo = saved_encode8<kSaved>(a, byte), hi = saved_encode8<kSaved>(b, byte);
+        const uint2 lo = saved_encode8<kSaved>(a, m, byte), hi = saved_encode8<kSaved>(b, m, byte);
         if (in) reinterpret_cast<uint4*>(codes)[c] = make_uint4(lo.x, lo.y, hi.x, hi.y);
         if (in && !(lane & 1)) scales[c >> 1] = static_cast<uint8_t>(byte);
     }
@@ -46,11 +46,9 @@ __global__ void __launch_bounds__(kThreads)
         const float scale = saved_scale<kSaved>(scales[c >> 1]);
         uint64_t v[4];
         saved_decode8<kSaved>(make_uint2(q.x, q.y), scale, v);
-        reinterpret_cast<uint4*>(out)[2 * c] =
-            make_uint4(pack_bf16x2(v[0]), pack_bf16x2(v[1]), pack_bf16x2(v[2]), pack_bf16x2(v[3]));
+        reinterpret_cast<uint4*>(out)[2 * c] = words_of(v);
         saved_decode8<kSaved>(make_uint2(q.z, q.w), scale, v);
-        reinterpret_cast<uint4*>(out)[2 * c + 1] =
-            make_uint4(pack_bf16x2(v[0]), pack_bf16x2(v[1]), pack_bf16x2(v[2]), pack_bf16x2(v[3]));
+        reinterpret_cast<uint4*>(out)[2 * c + 1] = words_of(v);
     }
 }
 
