@@ -31,7 +31,7 @@ SOURCES = ["rlk_logits.cu", "rlk_logits_mat.cu", "rlk_merge.cu", "rlk_gemm.cu", 
            "rlk_block_bwd_int8_f32.cu", "rlk_block_bwd_int8_bf16.cu", "rlk_block_bwd_e4m3_f32.cu",
            "rlk_block_bwd_e4m3_bf16.cu", "rlk_verify.cu"]
 HEADERS = ["rlk_ptx.cuh", "rlk_contract.cuh", "rlk_internal.h", "rlk_train.cuh", "rlk_block.cuh",
-           "rlk_block_bwd.cuh"]
+           "rlk_block_bwd.cuh", "rlk_tree.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CONTRACT_FLAGS = ["-ftz=false", "-prec-div=true", "-prec-sqrt=true", "-fmad=false"]

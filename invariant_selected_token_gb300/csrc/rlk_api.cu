@@ -473,17 +473,9 @@ PreferenceLayout preference_layout_of(int64_t T, int64_t n_pairs) {
     return l;
 }
 
-struct VerifyLayout {
-    Layout rows;
-    size_t lse, total;
-};
-
-VerifyLayout verify_layout_of(int64_t n_draft, int64_t n_seqs, int64_t V) {
-    VerifyLayout l;
-    l.rows = layout_of(n_draft + n_seqs, V, 1);
-    l.lse = l.rows.total;
-    l.total = l.lse + align256(size_t(n_draft + n_seqs) * sizeof(float));
-    return l;
+// The rows' tile pairs, as in rlk_linear_logprob's workspace, and no more.
+size_t verify_workspace_of(int64_t n_draft, int64_t n_seqs, int64_t V) {
+    return align256(size_t(n_draft + n_seqs) * size_t(n_tiles_of(V)) * sizeof(float2));
 }
 
 bool saved_format_known(int format) { return format == RLK_SAVED_INT8 || format == RLK_SAVED_E4M3; }
@@ -1479,7 +1471,7 @@ size_t rlk_draft_verify_workspace_size(int64_t n_draft, int64_t n_seqs, int64_t 
     if (n_draft < 0 || n_seqs < 0 || n_draft > RLK_MAX_ROWS || n_seqs > RLK_MAX_ROWS ||
         n_draft + n_seqs > RLK_MAX_ROWS || shard_check(V, 1) != RLK_OK)
         return 0;
-    return verify_layout_of(n_draft, n_seqs, V).total;
+    return verify_workspace_of(n_draft, n_seqs, V);
 }
 
 rlk_status_t rlk_draft_verify(const void* target_logits, int target_dtype, int64_t ld_target,
@@ -1505,20 +1497,14 @@ rlk_status_t rlk_draft_verify(const void* target_logits, int target_dtype, int64
         !aligned(draft_offsets, 4) || !aligned(out_accepted, 4) || !aligned(out_tokens, 4) ||
         !aligned(out_logprob, 4) || !aligned(workspace, 256) || !aligned(dev_status, 4))
         return RLK_ERR_ALIGNMENT;
-    const VerifyLayout l = verify_layout_of(n_draft, n_seqs, V);
-    if (workspace_bytes < l.total) return RLK_ERR_WORKSPACE;
+    if (workspace_bytes < verify_workspace_of(n_draft, n_seqs, V)) return RLK_ERR_WORKSPACE;
     DeviceState* dev = nullptr;
     if ((s = device_check(&dev)) != RLK_OK) return s;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    float* lse = reinterpret_cast<float*>(ws + l.lse);
     if (rlk::launch_mat_tile_partials(target_logits, target_dtype, ld_target, nullptr, nullptr, int(rows),
-                                      int(V), reinterpret_cast<float2*>(ws + l.rows.partials),
-                                      reinterpret_cast<float*>(ws + l.rows.tgt),
+                                      int(V), static_cast<float2*>(workspace), nullptr,
                                       dev->sm_count * dev->mat_ctas_per_sm[target_dtype], st) != cudaSuccess)
         return RLK_ERR_CUDA;
-    if ((s = run_tile_tree(nullptr, nullptr, rows, V, 1, nullptr, lse, ws, l.rows, dev_status, st, dev)) != RLK_OK)
-        return s;
     rlk::VerifyArgs a;
     a.target = target_logits;
     a.draft = draft_logits;
@@ -1528,8 +1514,9 @@ rlk_status_t rlk_draft_verify(const void* target_logits, int target_dtype, int64
     a.noise = noise;
     a.offsets = draft_offsets;
     a.active = active_mask;
-    a.rows = reinterpret_cast<const rlk_partial_t*>(ws + l.rows.records);
-    a.lse = lse;
+    a.partials = static_cast<const float2*>(workspace);
+    a.n_tiles = int(n_tiles_of(V));
+    a.depth = tree_depth(a.n_tiles);
     a.ld_target = ld_target;
     a.ld_draft = ld_draft;
     a.ld_noise = ld_noise;

@@ -85,8 +85,8 @@ struct VerifyArgs {
     const float* noise;          // [n_seqs][ld_noise]
     const int32_t* offsets;      // [n_seqs + 1]
     const uint8_t* active;       // [n_seqs] or nullptr
-    const rlk_partial_t* rows;   // [n_draft + n_seqs]: the rows' (m, s)
-    const float* lse;            // [n_draft + n_seqs]
+    const float2* partials;      // [n_draft + n_seqs][n_tiles]: the rows' tile pairs
+    int n_tiles, depth;          // of the tile tree: leaves, and ceil(log2) of them
     int64_t ld_target, ld_draft, ld_noise;
     int target_dtype, draft_dtype;
     int n_draft, n_seqs, V;

@@ -89,8 +89,10 @@ struct Pitch {
 // elements).  Aligned rows use asynchronous 16-byte copies, all in flight
 // at once: lane l's i-th copy is chunk l + 32 i, and since 32 chunks span
 // whole tiles, its source advances 512 bytes and its destination a fixed
-// number of tile pitches per step.  A row tail or an unaligned row falls
-// back to plain loads.  The asynchronous copies are complete after
+// number of tile pitches per step.  Rows that start elsewhere are copied word
+// by word, asynchronously too where a word's elements lie in one word of the
+// row (V = 50257, 291 rows of fp32: 12 us instead of 56 element by element).
+// A row's tail takes plain loads.  The asynchronous copies are complete after
 // stage_wait().
 template <int kDtype>
 __device__ __forceinline__ void stage_issue(const void* row, int64_t c0, int ncols_total, int lane,
@@ -101,18 +103,48 @@ __device__ __forceinline__ void stage_issue(const void* row, int64_t c0, int nco
     constexpr uint32_t kDstStep = (32 * kPerChunk / kVocabTile) * kPitch * kElem;
     const uint8_t* src = static_cast<const uint8_t*>(row) + c0 * kElem;
     uint8_t* sm = static_cast<uint8_t*>(sm_raw);
-    const int full_chunks = vec ? ncols_total / kPerChunk : 0;
-    const int e0 = lane * kPerChunk;
-    uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(
-        sm + ((e0 / kVocabTile) * kPitch + e0 % kVocabTile) * kElem));
-    const uint8_t* from = src + e0 * kElem;
-    for (int ch = lane; ch < full_chunks; ch += 32) {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from) : "memory");
-        dst += kDstStep;
-        from += 512;
+    int staged = 0;  // elements that are on their way or written
+    if (vec) {
+        const int full_chunks = ncols_total / kPerChunk;
+        const int e0 = lane * kPerChunk;
+        uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(
+            sm + ((e0 / kVocabTile) * kPitch + e0 % kVocabTile) * kElem));
+        const uint8_t* from = src + e0 * kElem;
+        for (int ch = lane; ch < full_chunks; ch += 32) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from) : "memory");
+            dst += kDstStep;
+            from += 512;
+        }
+        staged = full_chunks * kPerChunk;
+    } else if (kDtype == RLK_DTYPE_F32 || (reinterpret_cast<uintptr_t>(src) & 3) == 0) {
+        // words of one fp32 or two bf16 elements, 128 bytes a warp
+        constexpr int kPer = 4 / kElem;
+        const int words = ncols_total / kPer;
+        for (int k = lane; k < words; k += 32) {
+            const int e = k * kPer;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(
+                             sm + ((e / kVocabTile) * kPitch + e % kVocabTile) * kElem))),
+                         "l"(src + e * kElem)
+                         : "memory");
+        }
+        staged = words * kPer;
+    } else {
+        // a bf16 row that starts in the middle of a word: element pairs from the halves of two words
+        // each.  The first pair's lower word and the last one's upper may lie outside the row.
+        const uint32_t* word = reinterpret_cast<const uint32_t*>(src - 2);  // word k: elements 2k - 1, 2k
+        const int pairs = (ncols_total - 1) / 2;                            // pair p needs element 2p + 2's word
+#pragma unroll 4
+        for (int p = lane == 0 ? 32 : lane; p < pairs; p += 32) {
+            const int e = 2 * p;
+            *reinterpret_cast<uint32_t*>(sm + ((e / kVocabTile) * kPitch + e % kVocabTile) * kElem) =
+                __funnelshift_r(word[p], word[p + 1], 16);
+        }
+        if (lane < 2 && lane < ncols_total)
+            reinterpret_cast<uint16_t*>(sm)[lane] = reinterpret_cast<const uint16_t*>(src)[lane];
+        staged = pairs > 0 ? 2 * pairs : min(2, ncols_total);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    for (int e = full_chunks * kPerChunk + lane; e < ncols_total; e += 32) {
+    for (int e = staged + lane; e < ncols_total; e += 32) {
         uint8_t* d = sm + ((e / kVocabTile) * kPitch + e % kVocabTile) * kElem;
         if (kDtype == RLK_DTYPE_F32)
             *reinterpret_cast<float*>(d) = reinterpret_cast<const float*>(src)[e];

@@ -356,7 +356,7 @@ def test_binding_checks(rlk, cuda_device):
         with pytest.raises(ValueError):
             call(**kw)
     for kw in (dict(draft_logits=None), dict(noise=a["noise"][:1].expand(2, 500)),
-               dict(workspace=torch.empty(256, dtype=torch.uint8, device=cuda_device))):
+               dict(workspace=torch.empty(255, dtype=torch.uint8, device=cuda_device))):
         with pytest.raises(rlk.RlkError):
             call(**kw)
     none = make(cuda_device, [0, 0, 0], 500, 24)
