@@ -916,9 +916,11 @@ def act_quantize(x: torch.Tensor, fmt: str = "int8", out: Optional[Saved] = None
     T, H = x.shape
     if out is None:
         out = _new_saved(fmt, dev, x.shape)
-    got, a_codes, a_scales = _saved_addrs(out, "out", dev.index, x.shape)
-    if got != code:
-        raise TypeError("out must hold %s codes" % fmt)
+        a_codes, a_scales = out.codes.data_ptr(), out.scales.data_ptr()
+    else:
+        got, a_codes, a_scales = _saved_addrs(out, "out", dev.index, x.shape)
+        if got != code:
+            raise TypeError("out must hold %s codes" % fmt)
     _check(lib().rlk_act_quantize(x.data_ptr(), code, T, H, a_codes, a_scales, _raw_stream(dev.index)),
            "rlk_act_quantize")
     return out

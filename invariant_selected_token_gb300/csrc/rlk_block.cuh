@@ -128,14 +128,15 @@ __device__ __forceinline__ float squares_of(const uint64_t (&v)[4]) {
     return __fadd_rn(__fadd_rn(s2[0], s2[1]), __fadd_rn(s2[2], s2[3]));
 }
 
-// e^-|z| (which does not overflow) and 1 / (1 + e^-|z|) of a pair: the sigmoid is the second, or
-// for a negative z the product of both, and its slope the first times the second's square.  The
-// reciprocal of a number in [1, 2] is the hardware's approximation, a step of 2^-23 off at most,
-// after one Newton step: within 1.02 times half a step.
-__device__ __forceinline__ void sigmoid_parts(uint64_t z, uint64_t& e, uint64_t& r) {
+// e^-z and the sigmoid 1 / (1 + e^-z) of a pair; the slope is the first times the second's square.
+// Below -87 z counts as -87, where the sigmoid is 2^-125.  The reciprocal is the hardware's
+// approximation, a step of 2^-23 off at most, after one Newton step: within 1.02 times half a step.
+__device__ __forceinline__ void sigmoid_of(uint64_t z, uint64_t& e, uint64_t& r) {
     float lo, hi, a, b;
     f2_unpack(z, lo, hi);
-    e = contract_exp_x2(f2_pack(-fabsf(lo), -fabsf(hi)));
+    asm("min.NaN.f32 %0, %1, 0f42AE0000;" : "=f"(lo) : "f"(-lo));  // 87
+    asm("min.NaN.f32 %0, %1, 0f42AE0000;" : "=f"(hi) : "f"(-hi));
+    e = contract_exp_x2(f2_pack(lo, hi));
     const uint64_t d = f2_add(e, f2_splat(1.0f));
     f2_unpack(d, lo, hi);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(lo));
@@ -143,14 +144,6 @@ __device__ __forceinline__ void sigmoid_parts(uint64_t z, uint64_t& e, uint64_t&
     const uint64_t r0 = f2_pack(a, b);
     const uint64_t off = f2_fma(f2_pack(-lo, -hi), r0, f2_splat(1.0f));
     r = f2_fma(r0, off, r0);
-}
-// v where z is negative, else w, a pair
-__device__ __forceinline__ uint64_t if_negative(uint64_t z, uint64_t v, uint64_t w) {
-    float z0, z1, v0, v1, w0, w1;
-    f2_unpack(z, z0, z1);
-    f2_unpack(v, v0, v1);
-    f2_unpack(w, w0, w1);
-    return f2_pack(z0 < 0.0f ? v0 : w0, z1 < 0.0f ? v1 : w1);
 }
 
 // ---------------------------------------------------------------- 8-bit checkpoints

@@ -345,11 +345,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
                         const uint64_t n = post ? f2_mul(f2_mul(b[p], rstd_b2), gam[p]) : b[p];
                         o[p] = f2_mul(v[g][p], n);
                         if (a.gate_kind == RLK_GATE_SIGMOID) {
-                            uint64_t e, r;
-                            sigmoid_parts(z[p], e, r);
-                            const uint64_t er = f2_mul(e, r);
-                            o[p] = f2_mul(o[p], f2_mul(er, r));
-                            z[p] = if_negative(z[p], er, r);
+                            uint64_t e;
+                            sigmoid_of(z[p], e, z[p]);
+                            o[p] = f2_mul(o[p], f2_mul(f2_mul(e, z[p]), z[p]));
                         }
                         v[g][p] = f2_mul(v[g][p], z[p]);
                     }

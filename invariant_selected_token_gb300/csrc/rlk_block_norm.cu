@@ -116,8 +116,8 @@ __global__ void __launch_bounds__(cta_threads(kWarps)) k_block_norm(const BlockN
                 for (int p = 0; p < 4; ++p) {
                     if (a.gate_kind == RLK_GATE_SIGMOID) {
                         uint64_t e, r;
-                        sigmoid_parts(z[g][p], e, r);
-                        z[g][p] = if_negative(z[g][p], f2_mul(e, r), r);
+                        sigmoid_of(z[g][p], e, r);
+                        z[g][p] = r;
                     }
                     n[g][p] = f2_mul(n[g][p], z[g][p]);
                 }

@@ -117,15 +117,23 @@ __device__ __forceinline__ void stage_issue(const void* row, int64_t c0, int nco
         }
         staged = full_chunks * kPerChunk;
     } else if (kDtype == RLK_DTYPE_F32 || (reinterpret_cast<uintptr_t>(src) & 3) == 0) {
-        // words of one fp32 or two bf16 elements, 128 bytes a warp
-        constexpr int kPer = 4 / kElem;
-        const int words = ncols_total / kPer;
-        for (int k = lane; k < words; k += 32) {
-            const int e = k * kPer;
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(
-                             sm + ((e / kVocabTile) * kPitch + e % kVocabTile) * kElem))),
-                         "l"(src + e * kElem)
-                         : "memory");
+        // words of one fp32 or two bf16 elements, 128 bytes a warp: whole tiles first
+        constexpr int kPer = 4 / kElem, kTileBytes = kVocabTile * kElem;
+        const int words = ncols_total / kPer, tiles = ncols_total / kVocabTile;
+        uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(sm)) + 4 * lane;
+        const uint8_t* from = src + 4 * lane;
+#pragma unroll 2
+        for (int t = 0; t < tiles; ++t) {
+#pragma unroll
+            for (int b = 0; b < kTileBytes; b += 128)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + b), "l"(from + b) : "memory");
+            dst += kPitch * kElem;
+            from += kTileBytes;
+        }
+        for (int k = tiles * (kVocabTile / kPer) + lane; k < words; k += 32) {  // of the last, shorter one
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(from) : "memory");
+            dst += 128;
+            from += 128;
         }
         staged = words * kPer;
     } else {
