@@ -692,7 +692,8 @@ rlk_status_t rlk_rmsnorm_backward_q8(const void* grad_out, int grad_out_dtype, i
  *   draft_lse      device, float [n_draft] (rlk_logits_logprob's out_lse of the drafting step),
  *                  or NULL: draft_logits are log-probabilities (rlk_log_softmax's out)
  *   draft_tokens   device, int32 [n_draft];  uniforms  device, float [n_draft]
- *   noise          device, float [n_seqs][ld_noise], positive; columns [0, V) are read
+ *   noise          device, float [n_seqs][ld_noise], positive (a token whose noise is NaN or
+ *                  negative, or whose draft logit is NaN, is never drawn); columns [0, V) are read
  *   draft_offsets  device, int32 [n_seqs + 1], ascending within [0, n_draft]
  *   active_mask    device, uint8 [n_seqs] (nonzero = active), or NULL; an inactive sequence
  *                  gets out_accepted 0, tokens -1 and logprobs 0, whatever its inputs hold

@@ -110,18 +110,18 @@ constexpr float kLog2e = 0x1.715476p+0f, kMore = 0x1.715p-13f, kLess = -0x1.716p
 struct Scale {
     float m, log_more, draft_lse;
 };
-// At least w / e, or a number below 0 where w is 0.
+// At least w / e, or -1 where w is 0, or the noise or the draft's logit not a number.
 template <bool kDraft>
 __device__ __forceinline__ float bound_of(float l, float e, float d, const Scale& c) {
     float p = approx_exp2(__fmaf_rn(__fsub_rn(l, c.m), kLog2e, c.log_more));
     if (kDraft) p = __fsub_rn(p, approx_exp2(__fmaf_rn(__fsub_rn(d, c.draft_lse), kLog2e, kLess)));
-    return __fmul_rn(p, approx_rcp(e));
+    return fmaxf(__fmul_rn(p, approx_rcp(e)), -1.0f);  // of NaN and -1 the latter
 }
 // Whether a factor of the bound may have been flushed to 0, so that it says nothing.  (p and q that cancel
-// give a bound of 0 too, which is one.)  Below -105 p itself is 0.
+// give a bound of 0 too, which is one.)  Below -105 p itself is 0, and infinite noise leaves no weight.
 __device__ __forceinline__ bool unsure(float l, float e, const Scale& c) {
     const float d = __fsub_rn(l, c.m);
-    return d >= -105.0f && (approx_exp2(__fmaf_rn(d, kLog2e, c.log_more)) < 0x1p-100f || !(e < 0x1p100f));
+    return d >= -105.0f && (approx_exp2(__fmaf_rn(d, kLog2e, c.log_more)) < 0x1p-100f || (e >= 0x1p100f && e < CUDART_INF_F));
 }
 
 // The three largest bounds of a thread's tokens, and whose the first two are.  (With one token kept, a
@@ -138,43 +138,40 @@ struct Seen {
         top = fmaxf(top, bound);
     }
 };
-template <bool kVec, bool kDraft>
-__device__ __forceinline__ void see_chunk(const Scale& c, int base, int v1, const float (&l)[kAhead], const float (&e)[kAhead],
-                                          const float (&d)[kAhead], Seen& seen) {
-    float bound[kAhead], least = CUDART_INF_F;
+// Tokens k0, k0 + 1, .. of a thread's part of a chunk.
+template <bool kVec, bool kDraft, int kN>
+__device__ __forceinline__ void see_tokens(const Scale& c, int base, int k0, int v1, const float (&l)[kN], const float (&e)[kN],
+                                           const float (&d)[kN], Seen& seen) {
+    float bound[kN], least = CUDART_INF_F;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
+    for (int k = 0; k < kN; ++k) {
         bound[k] = bound_of<kDraft>(l[k], e[k], d[k], c);
-        if (!kVec && token_at<kVec>(base, k) >= v1) bound[k] = -1.0f;
+        if (!kVec && token_at<kVec>(base, k0 + k) >= v1) bound[k] = -1.0f;
         least = fminf(least, fabsf(bound[k]));
     }
     if (least < 0x1p-100f) {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if ((kVec || token_at<kVec>(base, k) < v1) && unsure(l[k], e[k], c)) seen.third = CUDART_INF_F;
+        for (int k = 0; k < kN; ++k)
+            if ((kVec || token_at<kVec>(base, k0 + k) < v1) && unsure(l[k], e[k], c)) seen.third = CUDART_INF_F;
     }
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) seen.see(bound[k], token_at<kVec>(base, k));
+    for (int k = 0; k < kN; ++k) seen.see(bound[k], token_at<kVec>(base, k0 + k));
 }
 
+// 4 consecutive values of a row, as they lie in memory.
 template <int kDtype>
-struct Vectors {  // a thread's 8 values of a row, as they lie in memory
-    using Four = typename std::conditional<kDtype == RLK_DTYPE_F32, float4, uint2>::type;
-    Four half[2];
-    __device__ __forceinline__ void load(const uint8_t* row, int base) {
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-            half[g] = *reinterpret_cast<const Four*>(row + static_cast<int64_t>(token_at<true>(base, 4 * g)) * (sizeof(Four) / 4));
+struct Four {
+    using Words = typename std::conditional<kDtype == RLK_DTYPE_F32, float4, uint2>::type;
+    Words w;
+    __device__ __forceinline__ void load(const uint8_t* row, int v) {
+        w = *reinterpret_cast<const Words*>(row + static_cast<int64_t>(v) * (sizeof(Words) / 4));
     }
-    __device__ __forceinline__ void values(float (&x)[kAhead]) const {
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            if constexpr (kDtype == RLK_DTYPE_F32) {
-                x[4 * g] = half[g].x, x[4 * g + 1] = half[g].y, x[4 * g + 2] = half[g].z, x[4 * g + 3] = half[g].w;
-            } else {
-                x[4 * g] = __uint_as_float(half[g].x << 16), x[4 * g + 1] = __uint_as_float(half[g].x & 0xFFFF0000u);
-                x[4 * g + 2] = __uint_as_float(half[g].y << 16), x[4 * g + 3] = __uint_as_float(half[g].y & 0xFFFF0000u);
-            }
+    __device__ __forceinline__ void values(float (&x)[4]) const {
+        if constexpr (kDtype == RLK_DTYPE_F32) {
+            x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+        } else {
+            x[0] = __uint_as_float(w.x << 16), x[1] = __uint_as_float(w.x & 0xFFFF0000u);
+            x[2] = __uint_as_float(w.y << 16), x[3] = __uint_as_float(w.y & 0xFFFF0000u);
         }
     }
 };
@@ -188,26 +185,31 @@ __device__ __forceinline__ Seen look_vec(const uint8_t* target, const uint8_t* n
     const Scale c = {m, log_more, draft_lse};
     constexpr int kD = kDraft == kNoDraft ? RLK_DTYPE_BF16 : kDraft;
     Seen seen;
-    Vectors<kTarget> t, next_t;
-    Vectors<RLK_DTYPE_F32> n, next_n;
-    Vectors<kD> q, next_q;
-    next_t.load(target, v0);
-    next_n.load(noise, v0);
-    if (kDraft != kNoDraft) next_q.load(draft, v0);
+    Four<kTarget> t[2];
+    Four<RLK_DTYPE_F32> n[2];
+    Four<kD> q[2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        const int v = token_at<true>(v0, 4 * g);
+        t[g].load(target, v);
+        n[g].load(noise, v);
+        if (kDraft != kNoDraft) q[g].load(draft, v);
+    }
 #pragma unroll 1
     for (int base = v0; base < v1; base += kChunk) {
-        t = next_t;
-        n = next_n;
-        if (kDraft != kNoDraft) q = next_q;
         const int next = base + kChunk < v1 ? base + kChunk : base;  // the last chunk once more
-        next_t.load(target, next);
-        next_n.load(noise, next);
-        if (kDraft != kNoDraft) next_q.load(draft, next);
-        float l[kAhead], e[kAhead], d[kAhead];
-        t.values(l);
-        n.values(e);
-        if (kDraft != kNoDraft) q.values(d);
-        see_chunk<true, kDraft != kNoDraft>(c, base, v1, l, e, d, seen);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            float l[4], e[4], d[4];
+            t[g].values(l);
+            n[g].values(e);
+            if (kDraft != kNoDraft) q[g].values(d);
+            const int v = token_at<true>(next, 4 * g);
+            t[g].load(target, v);
+            n[g].load(noise, v);
+            if (kDraft != kNoDraft) q[g].load(draft, v);
+            see_tokens<true, kDraft != kNoDraft>(c, base, 4 * g, v1, l, e, d, seen);
+        }
     }
     return seen;
 }
@@ -226,8 +228,8 @@ __device__ __noinline__ Seen look_plain(const VerifyArgs& a, const Draw& r, floa
             e[k] = noise[v];
             d[k] = draft ? logit_at(draft, a.draft_dtype, v) : 0.0f;
         }
-        if (draft) see_chunk<false, true>(c, base, v1, l, e, d, seen);
-        else see_chunk<false, false>(c, base, v1, l, e, d, seen);
+        if (draft) see_tokens<false, true>(c, base, 0, v1, l, e, d, seen);
+        else see_tokens<false, false>(c, base, 0, v1, l, e, d, seen);
     }
     return seen;
 }

@@ -200,6 +200,32 @@ def test_noise_of_any_positive_size(rlk, cuda_device):
     assert rlk.draft_verify(**a)[1].tolist() == [1234, 2345, 77, 9]
 
 
+@pytest.mark.parametrize("V", [3001, 50000])
+def test_tokens_without_a_noise_or_a_draft_are_never_drawn(rlk, cuda_device, V):
+    """NaN in the noise, or in the refused draft's row, takes those tokens out; where all are, none is
+    drawn."""
+    a = make(cuda_device, [2, 1, 0, 3], V, 25)
+    a["uniforms"].fill_(1e30)
+    bad = torch.rand(V, device=cuda_device) < 0.7
+    for name, rows in (("noise", 4), ("draft_logits", 6)):
+        b = dict(a, **{name: a[name].clone()})
+        b[name][:, bad] = float("nan")
+        status = rlk.new_status(cuda_device)
+        acc, tok, _ = rlk.draft_verify(**b, status=status)
+        rlk.raise_on_device_status(status)
+        drawn = tok[tok >= 0].long()
+        drawn = drawn if name == "noise" else tok[[0, 3, 6]].long()
+        assert not acc.any() and not bad[drawn].any()
+        # the same as with those tokens' noise beyond all others
+        c = dict(a, noise=a["noise"].masked_fill(bad[None], float("inf")))
+        same = rlk.draft_verify(**c)[1]
+        assert torch.equal(tok, same) if name == "noise" else torch.equal(tok[[0, 3, 6]], same[[0, 3, 6]])
+    b = dict(a, noise=torch.full_like(a["noise"], float("nan")))
+    status = rlk.new_status(cuda_device)
+    acc, tok, lp = rlk.draft_verify(**b, status=status)
+    assert int(status) == 1 << rlk.RLK_ERR_NONFINITE and torch.all(tok == -1)
+
+
 def test_tokens_and_offsets_out_of_range(rlk, cuda_device):
     V = 900
     a = make(cuda_device, [2, 3, 1], V, 15)
