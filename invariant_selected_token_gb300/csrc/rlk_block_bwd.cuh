@@ -36,8 +36,9 @@ constexpr int kThreads = 512;  // of a CTA, one CTA per SM
 constexpr int kMostStages = 4; // rows of a team in flight or at work
 constexpr int kChain = 64;     // rows that a team adds one after the other before it starts a new sum
 
-// What a call has of the branch: nothing (the RMSNorm's own backward), a block, or a block and a gate.
-enum Form { kNoBranch = 0, kBlock = 1, kGated = 2 };
+// What a call has of the branch: nothing (the RMSNorm's own backward), a block, or a block and a gate
+// that multiplies as it is or through a sigmoid.
+enum Form { kNoBranch = 0, kBlock = 1, kGated = 2, kSigmoid = 3 };
 
 // 16-byte places of a thread's ring in one stage: 16 features of each tensor.
 template <int kGo, int kSaved, int kForm>
@@ -45,7 +46,7 @@ struct Ring {
     static constexpr int kSavedPlaces = kSaved == RLK_SAVED_BF16 ? 2 : 1;
     static constexpr int kX = kGo == RLK_DTYPE_F32 ? 4 : 2, kB = kX + kSavedPlaces;
     static constexpr int kGate = kB + (kForm >= kBlock ? kSavedPlaces : 0);
-    static constexpr int kRes = kGate + (kForm == kGated ? kSavedPlaces : 0);
+    static constexpr int kRes = kGate + (kForm >= kGated ? kSavedPlaces : 0);
     static constexpr size_t kPlaceBytes = size_t(kThreads) * sizeof(uint4);
     static constexpr size_t kHeldBytes = size_t(kThreads) * (kForm == kNoBranch ? 16 : 32) * sizeof(float);
     static constexpr size_t kRoom = 232448 - 2048;  // 227 KB less what is declared shared
@@ -53,7 +54,7 @@ struct Ring {
     // are kept in shared memory where there is room (4096 x 4096, gated, int8: 66 against 84 us; a bf16
     // block without a gate, 8191 x 8192: 137 against 132)
     static constexpr int kGammaPlaces =
-        (kForm == kGated || (kForm == kBlock && kSaved != RLK_SAVED_BF16)) &&
+        (kForm >= kGated || (kForm == kBlock && kSaved != RLK_SAVED_BF16)) &&
                 (2 * kRes + 4) * kPlaceBytes + kHeldBytes <= kRoom ? 4 : 0;
     // where all of them do not fit twice beside the sums the residual's gradient is read as it is needed
     static constexpr bool kHasRes = (2 * (kRes + 2) + kGammaPlaces) * kPlaceBytes + kHeldBytes <= kRoom;
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
                 if (kGo == RLK_DTYPE_BF16) copy16(to + g * kStep, static_cast<const uint16_t*>(a.grad_out) + i + 256 * g);
                 fetch_saved(a.x, i, to + R::kX * kStep, g);
                 if constexpr (kForm >= kBlock) fetch_saved(a.block, i, to + R::kB * kStep, g);
-                if constexpr (kForm == kGated) fetch_saved(a.gate, i, to + R::kGate * kStep, g);
+                if constexpr (kForm >= kGated) fetch_saved(a.gate, i, to + R::kGate * kStep, g);
                 if (res_in_ring) copy16(to + (R::kRes + g) * kStep, static_cast<const uint16_t*>(a.grad_res) + i + 256 * g);
             }
         }
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
                 if (!in[g]) continue;
                 next[0][g] = a.x.scales[k + 8 * g];
                 if constexpr (kForm >= kBlock) next[1][g] = a.block.scales[k + 8 * g];
-                if constexpr (kForm == kGated) next[2][g] = a.gate.scales[k + 8 * g];
+                if constexpr (kForm >= kGated) next[2][g] = a.gate.scales[k + 8 * g];
             }
         }
     };
@@ -337,14 +338,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
                 uint64_t b[4], gam[4];
                 read_saved(1, R::kB, g, b);
                 read_gamma(2 + g, gam);
-                if constexpr (kForm == kGated) {
+                if constexpr (kForm >= kGated) {
                     uint64_t z[4], o[4];
                     read_saved(2, R::kGate, g, z);
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
                         const uint64_t n = post ? f2_mul(f2_mul(b[p], rstd_b2), gam[p]) : b[p];
                         o[p] = f2_mul(v[g][p], n);
-                        if (a.gate_kind == RLK_GATE_SIGMOID) {
+                        if constexpr (kForm == kSigmoid) {
                             uint64_t e;
                             sigmoid_of(z[p], e, z[p]);
                             o[p] = f2_mul(o[p], f2_mul(f2_mul(e, z[p]), z[p]));
@@ -449,8 +450,9 @@ cudaError_t launch_form(const BlockBwdArgs& a, int blocks, cudaStream_t stream) 
 template <int kWarps, int kGo, int kSaved>
 cudaError_t launch_row(const BlockBwdArgs& a, int blocks, cudaStream_t stream) {
     if (!a.block.data) return launch_form<kWarps, kGo, kSaved, kNoBranch>(a, blocks, stream);
-    return a.gate.data ? launch_form<kWarps, kGo, kSaved, kGated>(a, blocks, stream)
-                       : launch_form<kWarps, kGo, kSaved, kBlock>(a, blocks, stream);
+    if (!a.gate.data) return launch_form<kWarps, kGo, kSaved, kBlock>(a, blocks, stream);
+    return a.gate_kind == RLK_GATE_SIGMOID ? launch_form<kWarps, kGo, kSaved, kSigmoid>(a, blocks, stream)
+                                           : launch_form<kWarps, kGo, kSaved, kGated>(a, blocks, stream);
 }
 
 // grad_out's types apart, a translation unit each
