@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
     const bool post = kForm != kNoBranch && a.gamma_post != nullptr;
     const bool res_in_ring = R::kHasRes && a.grad_res && a.gx_dtype == RLK_DTYPE_BF16;
     for (int k = 0; k < stages * R::kPlaces; ++k) ring[k * kThreads + threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+    if (kGo == RLK_DTYPE_F32) __syncthreads();  // a warp's fp32 vectors lie in places that other warps cleared
     const uint32_t mine = ptx::smem_addr(ring + threadIdx.x);
     auto place = [&](int stage, int k) { return ring + (stage * R::kPlaces + k) * kThreads + threadIdx.x; };
 

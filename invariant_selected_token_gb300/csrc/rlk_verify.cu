@@ -23,7 +23,6 @@
 // over its tokens again, which is seldom.
 //
 // What bounds it: HBM for large batches, latency for small ones.
-#include <atomic>
 #include <cooperative_groups.h>
 #include <cstdint>
 #include <type_traits>
@@ -444,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_draft_verify(const __grid_const
         cluster.sync();
         best = *cluster.map_shared_rank(&cta_best, lane < ctas ? lane : 0);
 #pragma unroll
-        for (int o = 8; o >= 1; o >>= 1) best = max_key(best, __shfl_xor_sync(0xffffffffu, best, o));
+        for (int o = 4; o >= 1; o >>= 1) best = max_key(best, __shfl_xor_sync(0xffffffffu, best, o));
         best = __shfl_sync(0xffffffffu, best, 0);
     }
     if (rank == 0) {
@@ -466,17 +465,6 @@ __global__ void __launch_bounds__(kThreads, 4) k_draft_verify(const __grid_const
 
 template <int kLogL, int kTarget, int kDraft>
 cudaError_t launch(const VerifyArgs& a, int ctas, cudaStream_t stream) {
-    // clusters of more than 8 CTAs have to be asked for, once per device
-    static std::atomic<uint64_t> ready{0};
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err != cudaSuccess) return err;
-    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-    if (!(ready.load(std::memory_order_acquire) & bit)) {
-        err = cudaFuncSetAttribute(k_draft_verify<kLogL, kTarget, kDraft>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (err != cudaSuccess) return err;
-        ready.fetch_or(bit, std::memory_order_release);
-    }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3(static_cast<unsigned>(a.n_seqs) * ctas, 1, 1);
@@ -507,7 +495,10 @@ cudaError_t launch_types(const VerifyArgs& a, int ctas, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_draft_verify(const VerifyArgs& a, int num_sms, cudaStream_t stream) {
-    int ctas = 16;
+    // up to 8 CTAs a sequence, as long as all of them are resident at once (4 per SM).  Against 4 and 16
+    // of them: one sequence at V = 151936 16.8 us (22.0, 15.8), at V = 1000 11.7 (12.3, 12.9), 16 at V =
+    // 32000 17.0 (18.3, 20.7), 32 at V = 2000 14.0 (13.7, 21.1).
+    int ctas = 8;
     while (ctas > 1 && static_cast<int64_t>(a.n_seqs) * ctas > 4 * static_cast<int64_t>(num_sms)) ctas /= 2;
     const bool draft_f32 = a.draft_dtype == RLK_DTYPE_F32;
     if (a.target_dtype == RLK_DTYPE_F32)

@@ -282,7 +282,7 @@ def test_inactive_sequences(rlk, cuda_device):
 
 @pytest.mark.parametrize("V", [515, 50257])
 def test_a_sequence_does_not_depend_on_the_batch(rlk, cuda_device, V):
-    """One sequence alone (eight CTAs) and among hundreds (one): the same bits."""
+    """One sequence alone (eight CTAs) and among hundreds (one or two): the same bits."""
     lens = [3, 1, 0, 5] * 80 if V < 1000 else [3, 1, 0, 5] * 20
     a = make(cuda_device, lens, V, 18)
     acc, tok, lp = rlk.draft_verify(**a)
