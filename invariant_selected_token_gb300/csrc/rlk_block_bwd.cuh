@@ -50,12 +50,11 @@ struct Ring {
     static constexpr size_t kPlaceBytes = size_t(kThreads) * sizeof(uint4);
     static constexpr size_t kHeldBytes = size_t(kThreads) * (kForm == kNoBranch ? 16 : 32) * sizeof(float);
     static constexpr size_t kRoom = 232448 - 2048;  // 227 KB less what is declared shared
-    // beside two rows of sums, and a gate or scales, the gammas do not fit into 128 registers: then they
-    // are kept in shared memory where there is room (4096 x 4096, gated, int8: 66 against 84 us; a bf16
-    // block without a gate, 8191 x 8192: 137 against 132)
+    // beside two rows of sums the gammas do not fit into 128 registers: they are kept in shared memory
+    // where there is room (4096 x 4096, gated, int8: 66 against 84 us, of which most went to spilled
+    // registers, since the ring leaves next to no first-level cache for them)
     static constexpr int kGammaPlaces =
-        (kForm >= kGated || (kForm == kBlock && kSaved != RLK_SAVED_BF16)) &&
-                (2 * kRes + 4) * kPlaceBytes + kHeldBytes <= kRoom ? 4 : 0;
+        kForm != kNoBranch && (2 * kRes + 4) * kPlaceBytes + kHeldBytes <= kRoom ? 4 : 0;
     // where all of them do not fit twice beside the sums the residual's gradient is read as it is needed
     static constexpr bool kHasRes = (2 * (kRes + 2) + kGammaPlaces) * kPlaceBytes + kHeldBytes <= kRoom;
     static constexpr int kPlaces = kRes + (kHasRes ? 2 : 0);
@@ -153,15 +152,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
     const int r0 = static_cast<int>(static_cast<int64_t>(a.T) * blockIdx.x / gridDim.x);
     const int r1 = static_cast<int>(static_cast<int64_t>(a.T) * (blockIdx.x + 1) / gridDim.x);
     const bool pow2 = (a.H & (a.H - 1)) == 0;
-    const float h = static_cast<float>(a.H), inv_h = __fdiv_rn(1.0f, h);
+    const float inv_h = __fdiv_rn(1.0f, static_cast<float>(a.H));
     const bool post = kForm != kNoBranch && a.gamma_post != nullptr;
     const bool res_in_ring = R::kHasRes && a.grad_res && a.gx_dtype == RLK_DTYPE_BF16;
-    for (int k = 0; k < stages * R::kPlaces; ++k) ring[k * kThreads + threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
-    if (kGo == RLK_DTYPE_F32) __syncthreads();  // a warp's fp32 vectors lie in places that other warps cleared
+    if (512 * (warp + 1) > a.H) {  // features behind the row's end are read as zeros
+        for (int k = 0; k < stages * R::kPlaces; ++k) {
+            // a warp's fp32 vectors of a group, 64 in a row over two places, or a thread's own place
+            const int r = k % R::kPlaces, half = r & 1;
+            const int at = kGo == RLK_DTYPE_F32 && r < R::kX ? (k - half) * kThreads + 64 * warp_of_cta + 32 * half + lane
+                                                             : k * kThreads + threadIdx.x;
+            ring[at] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        __syncwarp();
+    }
     const uint32_t mine = ptx::smem_addr(ring + threadIdx.x);
     auto place = [&](int stage, int k) { return ring + (stage * R::kPlaces + k) * kThreads + threadIdx.x; };
 
-    // i: this thread's first element of the row, t the row
+    // i: this thread's first element of row t.  The distance between a team's rows is kept where there are
+    // registers to spare (32771 x 1024 from e4m3: 45 against 49 us).
+    const int64_t step = static_cast<int64_t>(kTeams) * a.H;
+    auto ahead = [&](int rows) { return kForm == kNoBranch ? rows * step : static_cast<int64_t>(rows * kTeams) * a.H; };
     auto fetch_saved = [&](const SavedIn& s, int64_t i, uint32_t to, int g) {
         if (kPlain) copy16(to + g * (kThreads * 16), static_cast<const uint16_t*>(s.data) + i + 256 * g);
         else copy8(to + g * 8, static_cast<const uint8_t*>(s.data) + i + 256 * g);
@@ -245,12 +255,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
     if (chained) move_to_held();  // zeros
     int t = r0 + team, chain_end = t + kChain * kTeams;
     int64_t i = static_cast<int64_t>(t) * a.H + i0;
-    const int64_t step = static_cast<int64_t>(kTeams) * a.H;
-    for (int k = 0; k < kMostStages; ++k)
-        if (k < stages) fetch(t + k * kTeams, i + k * step, k);
+    for (int k = 0; k < stages; ++k) fetch(t + k * kTeams, i + ahead(k), k);
     fetch_scales(t, i);
     int slot = 0, stage = 0;
-    for (; t < r1; t += kTeams, i += step) {
+    for (; t < r1; t += kTeams, i += ahead(1)) {
         wait_copies(stages - 1);
         if (kGo == RLK_DTYPE_F32) __syncwarp();  // the lanes of a warp share what they copied
         float scale[3][2];
@@ -259,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
             for (int k = 0; k < 3; ++k)
 #pragma unroll
                 for (int g = 0; g < 2; ++g) scale[k][g] = saved_scale<kSaved>(next[k][g]);
-            fetch_scales(t + kTeams, i + step);
+            fetch_scales(t + kTeams, i + ahead(1));
         }
         auto read_dy = [&](int g, uint64_t (&v)[4]) {
             if constexpr (kGo == RLK_DTYPE_F32) {
@@ -303,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
             d = kWarps <= 8 ? __shfl_sync(0xffffffffu, sums, (2 * kWarps) & 31) : team_sum<kWarps>(&part[slot][team * kWarps], 2);
         }
         // a product with 1 / H is the quotient itself where H is a power of two
-        const float root = contract_rsqrt(__fadd_rn(pow2 ? __fmul_rn(sums, inv_h) : __fdiv_rn(sums, h), a.eps));
+        const float root = contract_rsqrt(__fadd_rn(pow2 ? __fmul_rn(sums, inv_h) : __fdiv_rn(sums, static_cast<float>(a.H)), a.eps));
         const float rstd = __shfl_sync(0xffffffffu, root, 0);
         const float rstd_b = post ? __shfl_sync(0xffffffffu, root, kWarps == 1 ? 2 : kWarps) : 1.0f;
         const float c = __fmul_rn(__fmul_rn(rstd, rstd), __fmul_rn(d, inv_h));
@@ -389,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
         }
         slot ^= 1;  // a team's warps are never more than one row apart
         if (kGo == RLK_DTYPE_F32) __syncwarp();
-        fetch(t + stages * kTeams, i + stages * step, stage);  // everything in this stage has been used
+        fetch(t + stages * kTeams, i + ahead(stages), stage);  // everything in this stage has been used
         stage = stage + 1 < stages ? stage + 1 : 0;
         if (chained && t + kTeams == chain_end) {
             add_held();
