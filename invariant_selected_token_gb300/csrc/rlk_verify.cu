@@ -109,12 +109,18 @@ constexpr float kLog2e = 0x1.715476p+0f, kMore = 0x1.715p-13f, kLess = -0x1.716p
 struct Scale {
     float m, log_more, draft_lse;
 };
-// At least w / e, or -1 where w is 0, or the noise or the draft's logit not a number.
+// At least w / e, NaN where the noise or the draft's logit is not a number (or p was flushed to 0 and e's
+// reciprocal is infinite).
 template <bool kDraft>
 __device__ __forceinline__ float bound_of(float l, float e, float d, const Scale& c) {
     float p = approx_exp2(__fmaf_rn(__fsub_rn(l, c.m), kLog2e, c.log_more));
     if (kDraft) p = __fsub_rn(p, approx_exp2(__fmaf_rn(__fsub_rn(d, c.draft_lse), kLog2e, kLess)));
-    return fmaxf(__fmul_rn(p, approx_rcp(e)), -1.0f);  // of NaN and -1 the latter
+    return __fmul_rn(p, approx_rcp(e));
+}
+__device__ __forceinline__ float min_or_nan(float a, float b) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
 }
 // Whether a factor of the bound may have been flushed to 0, so that it says nothing.  (p and q that cancel
 // give a bound of 0 too, which is one.)  Below -105 p itself is 0, and infinite noise leaves no weight.
@@ -145,10 +151,11 @@ __device__ __forceinline__ void see_tokens(const Scale& c, int base, int k0, int
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
         bound[k] = bound_of<kDraft>(l[k], e[k], d[k], c);
+        least = min_or_nan(least, fabsf(bound[k]));
+        bound[k] = fmaxf(bound[k], -1.0f);  // no token: of NaN and -1 the latter
         if (!kVec && token_at<kVec>(base, k0 + k) >= v1) bound[k] = -1.0f;
-        least = fminf(least, fabsf(bound[k]));
     }
-    if (least < 0x1p-100f) {
+    if (!(least >= 0x1p-100f)) {
 #pragma unroll
         for (int k = 0; k < kN; ++k)
             if ((kVec || token_at<kVec>(base, k0 + k) < v1) && unsure(l[k], e[k], c)) seen.third = CUDART_INF_F;

@@ -200,6 +200,28 @@ def test_noise_of_any_positive_size(rlk, cuda_device):
     assert rlk.draft_verify(**a)[1].tolist() == [1234, 2345, 77, 9]
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [3001, 50000])
+def test_subnormal_noise_on_subnormal_probabilities(rlk, cuda_device, V, dtype):
+    """p = e^-94 is a subnormal number and so is the token's noise: their quotient, 1.1, is the largest weight
+    by far, by p alone and from a draft that gives the token less."""
+    a = make(cuda_device, [0, 1, 1], V, 26, dtype)
+    a["target_logits"].fill_(-94.0)
+    a["target_logits"][:, 11] = 0.0
+    a["noise"].fill_(1.0)
+    a["noise"][:, 11] = 1.0e4
+    a["draft_logits"].fill_(-100.0)
+    a["draft_logits"][:, 11] = 0.0
+    a["draft_lse"].zero_()
+    a["draft_tokens"].fill_(11)
+    a["uniforms"].copy_(torch.tensor([0.0, 1e30], device=cuda_device))
+    for at in (0, 1000, V - 1):
+        noise = a["noise"].clone()
+        noise[:, at] = 1.4e-41
+        acc, tok, _ = rlk.draft_verify(**dict(a, noise=noise))
+        assert acc.tolist() == [0, 1, 0] and tok.tolist() == [at, 11, at, at, -1]
+
+
 @pytest.mark.parametrize("V", [3001, 50000])
 def test_tokens_without_a_noise_or_a_draft_are_never_drawn(rlk, cuda_device, V):
     """NaN in the noise, or in the refused draft's row, takes those tokens out; where all are, none is
