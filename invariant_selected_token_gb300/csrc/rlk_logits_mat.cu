@@ -91,8 +91,9 @@ struct Pitch {
 // whole tiles, its source advances 512 bytes and its destination a fixed
 // number of tile pitches per step.  Rows that start elsewhere are copied word
 // by word, asynchronously too where a word's elements lie in one word of the
-// row (V = 50257, 291 rows of fp32: 12 us instead of 56 element by element).
-// A row's tail takes plain loads.  The asynchronous copies are complete after
+// row (a call with V = 50257: 291 rows of fp32 22.6 us instead of 58.6 element
+// by element, of bf16 24.1 instead of 42.1; 4096 rows 182 and 196 instead of 521
+// and 346).  A row's tail takes plain loads.  The asynchronous copies are complete after
 // stage_wait().
 template <int kDtype>
 __device__ __forceinline__ void stage_issue(const void* row, int64_t c0, int ncols_total, int lane,

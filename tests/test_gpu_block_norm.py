@@ -1,11 +1,13 @@
 """The block norms and their backward on the GPU against the fp64 definition.
 
 Tolerances (u = 2^-24).  rstd errs by 10 u (tests of the RMSNorm backward).  Forward: n = b rstd
-gamma 12 u; the sigmoid: e^-|z| 2 u, 1 + e and the quotient (or reciprocal and product) 4 u: 6 u;
-products with gate and scale 1 u each: t = bs n gate 20 u; the fma rounds once, the store by half a
-step of bf16 (eps / 2).  out is compared with rlk_rmsnorm's bits on the stored x'.
-Backward: dx errs by E = u [14 rstd |up| + 56 rstd^3 |x| sum|up x| / H] + u (|res| + |dx|), as the RMSNorm's;
-a product passes its operands' errors on and adds u of itself; sigmoid' = e r r errs by 10 u; a dot of
+gamma 12 u; the sigmoid 1 / (1 + e^-z): e^-z 2 u, of which the sum keeps at most that and adds u, the
+reciprocal 1.02 u: 4.02 u, within the 6 u counted; products with gate and scale 1 u each: t = bs n
+gate 20 u; the fma rounds once, the store by half a step of bf16 (eps / 2).  out is compared with
+rlk_rmsnorm's bits on the stored x'.
+Backward: dx errs by E = u [14 rstd |up| + 56 rstd^3 |x| sum|up x| / H] + u (|res| + |dx|), as the
+RMSNorm's; a product passes its operands' errors on and adds u of itself; sigmoid' = e r r errs by 10 u
+at most (8.04: e's 2 u once, since e and r r move against each other, 2.02 for each r, two products); a dot of
 H terms adds 18 u of the sum of their magnitudes (8 in a lane's chain, at most 10 levels above);
 rstd^2 / H 24 u; stores half a step.  grad_gammas: chains of 64 rows, one sum per chain, at most 16
 teams, 152 ranges in 5 + 5 levels."""
