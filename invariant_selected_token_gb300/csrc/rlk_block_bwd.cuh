@@ -24,13 +24,13 @@
 // decoded where it is used, up to three times, rather than held.
 //
 // What bounds it: with bf16 activations HBM (8191 x 8192, a block without a gate,
-// 138 us, 0.87 of the copy rate; 4096 x 4096 with a gate 70 us, 0.57).  From 8-bit
-// checkpoints it is the instructions: 4096 x 4096, a sigmoid gate, int8, takes 64 us
-// (0.51): 82 instructions a feature at 61 % of the issue slots, half of them in
-// the FMA pipe, where a packed pair takes two cycles; 16 warps an SM and two
-// barriers a row leave the rest idle.  Without a gate it is 45 us (0.56), without a
-// branch 32 (0.71; 4096 x 4096 int8, fp32 grad_out).  64 rows are 7 us: one row's latency
-// and the second launch's.
+// 138 us, 0.87 of the copy rate; 4096 x 4096 with a gate 51 us, 0.79, a sigmoid one
+// 56, 0.72).  From 8-bit checkpoints it is the instructions: 4096 x 4096, a sigmoid
+// gate, int8, takes 61 us (0.54): 82 instructions a feature at 61 % of the issue slots,
+// half of them in the FMA pipe, where a packed pair takes two cycles; 16 warps an SM
+// and two barriers a row leave the rest idle.  Without a gate it is 45 us (0.56), without
+// a branch 32 (0.71; fp32 grad_out).  64 rows are 7 us: one row's latency and the second
+// launch's.
 #pragma once
 
 #include <atomic>
@@ -52,7 +52,7 @@ constexpr int kChain = 64;     // rows that a team adds one after the other befo
 enum Form { kNoBranch = 0, kBlock = 1, kGated = 2, kSigmoid = 3 };
 
 // 16-byte places of a thread's ring in one stage: 16 features of each tensor.
-template <int kGo, int kSaved, int kForm>
+template <int kGo, int kSaved, int kForm, int kGx>
 struct Ring {
     static constexpr int kSavedPlaces = kSaved == RLK_SAVED_BF16 ? 2 : 1;
     static constexpr int kX = kGo == RLK_DTYPE_F32 ? 4 : 2, kB = kX + kSavedPlaces;
@@ -66,8 +66,12 @@ struct Ring {
     // registers, since the ring leaves next to no first-level cache for them)
     static constexpr int kGammaPlaces =
         kForm != kNoBranch && (2 * kRes + 4) * kPlaceBytes + kHeldBytes <= kRoom ? 4 : 0;
-    // where all of them do not fit twice beside the sums the residual's gradient is read as it is needed
-    static constexpr bool kHasRes = (2 * (kRes + 2) + kGammaPlaces) * kPlaceBytes + kHeldBytes <= kRoom;
+    // Where all of them do not fit twice beside the sums the residual's gradient is fetched into the
+    // second-level cache with the rest and read from there while the sums over its row are formed, as it is in
+    // fp32.  Read where it is needed, that cost 64 us instead of 53 (4096 x 4096, gated, bf16); for those
+    // that fit, early reads cost 155 instead of 138 us (8191 x 8192, bf16).
+    static constexpr bool kHasRes =
+        kGx == RLK_DTYPE_BF16 && (2 * (kRes + 2) + kGammaPlaces) * kPlaceBytes + kHeldBytes <= kRoom;
     static constexpr int kPlaces = kRes + (kHasRes ? 2 : 0);
     static constexpr size_t kStageBytes = kPlaces * kPlaceBytes;
     static_assert(2 * kStageBytes + kGammaPlaces * kPlaceBytes + kHeldBytes <= kRoom, "a row flies while another is worked on");
@@ -102,15 +106,10 @@ __device__ __forceinline__ void pairs_of_f32(uint4 lo, uint4 hi, uint64_t (&v)[4
 // of their features in 8 different places.
 __device__ __forceinline__ int f32_place(int vec) { return vec ^ ((vec >> 3) & 1); }
 
-// 8 features of a gradient at element i.
-__device__ __forceinline__ void load_grad(const void* base, int dtype, int64_t i, uint64_t (&v)[4]) {
-    if (dtype == RLK_DTYPE_F32) {
-        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + i);
-        pairs_of_f32(p[0], p[1], v);
-    } else {
-        pairs_of(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i), v);
-    }
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
 }
+
 __device__ __forceinline__ void store_f32(float* to, const uint64_t (&v)[4]) {
     float e[8];
 #pragma unroll
@@ -118,9 +117,10 @@ __device__ __forceinline__ void store_f32(float* to, const uint64_t (&v)[4]) {
     reinterpret_cast<float4*>(to)[0] = make_float4(e[0], e[1], e[2], e[3]);
     reinterpret_cast<float4*>(to)[1] = make_float4(e[4], e[5], e[6], e[7]);
 }
-// Called by whole warps; a pair of lanes is in or out together.
-__device__ __forceinline__ void store_grad(void* base, int dtype, int64_t i, bool in, const uint64_t (&v)[4]) {
-    if (dtype == RLK_DTYPE_F32) {
+// 8 features of a gradient at element i.  Called by whole warps; a pair of lanes is in or out together.
+template <int kDtype>
+__device__ __forceinline__ void store_grad(void* base, int64_t i, bool in, const uint64_t (&v)[4]) {
+    if (kDtype == RLK_DTYPE_F32) {
         // even lanes hand their last four features over for the odd ones' first four, so that a lane
         // pair stores whole sectors
         const bool odd = threadIdx.x & 1;
@@ -145,9 +145,9 @@ __device__ __forceinline__ void store_grad(void* base, int dtype, int64_t i, boo
 // range.  A thread copies its own features of the next rows into its own places of a ring of shared
 // memory, which needs no barrier; the copies fly while the current row is reduced.  Places of features
 // behind the row's end hold zeros.
-template <int kWarps, int kGo, int kSaved, int kForm>
+template <int kWarps, int kGo, int kSaved, int kForm, int kGx>
 __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const BlockBwdArgs a, const int stages) {
-    using R = Ring<kGo, kSaved, kForm>;
+    using R = Ring<kGo, kSaved, kForm, kGx>;
     constexpr int kTeams = kThreads / 32 / kWarps;
     constexpr bool kPlain = kSaved == RLK_SAVED_BF16;
     static_assert(kWarps == 1 || kTeams <= 15, "a named barrier (1 .. 15) per team");
@@ -165,7 +165,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
     const bool pow2 = (a.H & (a.H - 1)) == 0;
     const float inv_h = __fdiv_rn(1.0f, static_cast<float>(a.H));
     const bool post = kForm != kNoBranch && a.gamma_post != nullptr;
-    const bool res_in_ring = R::kHasRes && a.grad_res && a.gx_dtype == RLK_DTYPE_BF16;
+    const bool res_in_ring = R::kHasRes && a.grad_res;
+    const bool res_early = !R::kHasRes && a.grad_res;
+    constexpr int kResVecs = kGx == RLK_DTYPE_F32 ? 2 : 1;  // of 16 bytes, 8 features
+    auto res_at = [&](int64_t i) {
+        return reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.grad_res) + i * (2 * kResVecs));
+    };
     if (512 * (warp + 1) > a.H) {  // features behind the row's end are read as zeros
         for (int k = 0; k < stages * R::kPlaces; ++k) {
             // a warp's fp32 vectors of a group, 64 in a row over two places, or a thread's own place
@@ -206,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
                 if constexpr (kForm >= kBlock) fetch_saved(a.block, i, to + R::kB * kStep, g);
                 if constexpr (kForm >= kGated) fetch_saved(a.gate, i, to + R::kGate * kStep, g);
                 if (res_in_ring) copy16(to + (R::kRes + g) * kStep, static_cast<const uint16_t*>(a.grad_res) + i + 256 * g);
+                if (res_early) prefetch_l2(res_at(i + 256 * g));
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -310,11 +316,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
                 sb[g] = squares_of(x);
             }
         }
+        uint4 early[2][kResVecs] = {};  // on their way while the sums are formed
+        if (res_early) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int k = 0; k < kResVecs; ++k)
+                    if (in[g]) early[g][k] = res_at(i + 256 * g)[k];
+        }
         f2_unpack(dot, d0, d1);
         float sums = warp_sums<kForm != kNoBranch>(sx, sb, __fadd_rn(d0, d1));
         float d;
         if constexpr (kWarps == 1) {
             d = __shfl_sync(0xffffffffu, sums, 4);
+            // nothing read so far is kept, as behind the other teams' barrier: there are no registers for it
+            // (60000 x 512, gated, int8: 75 us instead of 95)
+            asm volatile("" ::: "memory");
         } else {
             if (lane < 6 && !(lane & 1)) reinterpret_cast<float*>(&part[slot][team * kWarps + warp])[lane >> 1] = sums;
             team_barrier<kWarps>(team);
@@ -339,7 +356,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
                 read_dy(g, dy);
                 read_gamma(g, gam);
                 if (res_in_ring) pairs_of(*place(stage, R::kRes + g), res);
-                else if (a.grad_res && in[g]) load_grad(a.grad_res, a.gx_dtype, at, res);
+                else if (res_early && kResVecs == 1) pairs_of(early[g][0], res);
+                else if (res_early) pairs_of_f32(early[g][0], early[g][kResVecs - 1], res);
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
                     dx[p] = f2_fma(rstd2, f2_fma(x[p], neg_c2, f2_mul(dy[p], gam[p])), res[p]);
@@ -350,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
                 uint64_t o[4];
 #pragma unroll
                 for (int p = 0; p < 4; ++p) o[p] = f2_mul(f2_splat(a.residual_scale), dx[p]);
-                store_grad(a.grad_residual, a.gx_dtype, at, in[g], o);
+                store_grad<kGx>(a.grad_residual, at, in[g], o);
             }
 #pragma unroll
             for (int p = 0; p < 4; ++p) v[g][p] = f2_mul(f2_splat(a.block_scale), dx[p]);
@@ -372,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
                         }
                         v[g][p] = f2_mul(v[g][p], z[p]);
                     }
-                    if (a.grad_gate) store_grad(a.grad_gate, a.gx_dtype, at, in[g], o);
+                    if (a.grad_gate) store_grad<kGx>(a.grad_gate, at, in[g], o);
                 }
                 if (post) {
 #pragma unroll
@@ -383,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
                     }
                 }
             }
-            if (!post && a.grad_block) store_grad(a.grad_block, a.gx_dtype, at, in[g], v[g]);
+            if (!post && a.grad_block) store_grad<kGx>(a.grad_block, at, in[g], v[g]);
         }
         if (post && a.grad_block) {
             f2_unpack(dot_b, d0, d1);
@@ -395,6 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
                 if (lane == 0) part[slot][team * kWarps + warp].w = k;
                 team_barrier<kWarps>(team);
                 k = team_sum<kWarps>(&part[slot][team * kWarps], 3);
+            } else {
+                asm volatile("" ::: "memory");  // as above
             }
             const uint64_t neg_k2 = f2_splat(-__fmul_rn(__fmul_rn(rstd_b, rstd_b), __fmul_rn(k, inv_h)));
 #pragma unroll
@@ -403,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
                 read_saved(1, R::kB, g, b);
 #pragma unroll
                 for (int p = 0; p < 4; ++p) o[p] = f2_mul(rstd_b2, f2_fma(b[p], neg_k2, v[g][p]));
-                store_grad(a.grad_block, a.gx_dtype, i + 256 * g, in[g], o);
+                store_grad<kGx>(a.grad_block, i + 256 * g, in[g], o);
             }
         }
         slot ^= 1;  // a team's warps are never more than one row apart
@@ -445,9 +465,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_norm_backward(const Block
     }
 }
 
-template <int kWarps, int kGo, int kSaved, int kForm>
-cudaError_t launch_form(const BlockBwdArgs& a, int blocks, cudaStream_t stream) {
-    using R = Ring<kGo, kSaved, kForm>;
+template <int kWarps, int kGo, int kSaved, int kForm, int kGx>
+cudaError_t launch_gx(const BlockBwdArgs& a, int blocks, cudaStream_t stream) {
+    using R = Ring<kGo, kSaved, kForm, kGx>;
     const bool chained = block_bwd_chained(a.T, blocks, kThreads / 32 / kWarps);
     const int stages = R::stages(chained);
     // once per device and kernel: the runtime keeps it, and asking each time costs the host 1 us
@@ -457,14 +477,20 @@ cudaError_t launch_form(const BlockBwdArgs& a, int blocks, cudaStream_t stream) 
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
     if (!(ready.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(k_block_norm_backward<kWarps, kGo, kSaved, kForm>,
+        e = cudaFuncSetAttribute(k_block_norm_backward<kWarps, kGo, kSaved, kForm, kGx>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, int(R::kRoom));
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);
     }
     const size_t smem = stages * R::kStageBytes + R::kGammaPlaces * R::kPlaceBytes + (chained ? R::kHeldBytes : 0);
-    k_block_norm_backward<kWarps, kGo, kSaved, kForm><<<blocks, kThreads, smem, stream>>>(a, stages);
+    k_block_norm_backward<kWarps, kGo, kSaved, kForm, kGx><<<blocks, kThreads, smem, stream>>>(a, stages);
     return cudaGetLastError();
+}
+
+template <int kWarps, int kGo, int kSaved, int kForm>
+cudaError_t launch_form(const BlockBwdArgs& a, int blocks, cudaStream_t stream) {
+    return a.gx_dtype == RLK_DTYPE_F32 ? launch_gx<kWarps, kGo, kSaved, kForm, RLK_DTYPE_F32>(a, blocks, stream)
+                                       : launch_gx<kWarps, kGo, kSaved, kForm, RLK_DTYPE_BF16>(a, blocks, stream);
 }
 
 template <int kWarps, int kGo, int kSaved>
