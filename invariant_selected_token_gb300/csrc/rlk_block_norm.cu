@@ -16,11 +16,12 @@
 // 16 features a thread keep a row in registers between the two norms, so that it
 // is read once.
 //
-// What bounds it: HBM.  16384 x 4096 takes 83 us (0.96 of the copy rate on the
-// bytes it has to move), 8191 x 8192 91 us (0.89), 4096 x 4096 with a sigmoid gate 32
-// (0.79, start and tail of a short launch); with three int8 checkpoints 40 (0.82, and 72 % of
-// the issue slots: 61 instructions a feature, a third of them for codes and scales).
-// 8 rows are 2.6 us of latency: two loads and two sums over a row, one after the other.
+// What bounds it: HBM.  16384 x 4096 takes 82 us (0.98 of the copy rate on the
+// bytes it has to move), 8191 x 8192 92 us (0.87), 4096 x 4096 24 (0.84) and with a
+// sigmoid gate 32 (0.79, start and tail of a short launch; 0.92 at 16384 rows); with three
+// int8 checkpoints and their restoring 64 (0.87; 72 % of the issue slots, 61 instructions a
+// feature, a third of them for codes and scales).  8 rows are 2.3 us of latency: two
+// loads and two sums over a row, one after the other.
 #include <cstdint>
 
 #include "rlk_block.cuh"
@@ -28,7 +29,10 @@
 namespace rlk {
 namespace {
 
-constexpr int cta_threads(int warps) { return 32 * warps > 128 ? 32 * warps : 128; }
+// Teams of one and two warps share a CTA of 256 threads: with 128 32768 x 1024 takes 53 us instead of 46, with
+// three checkpoints and their restoring 147 instead of 122, 60000 x 512 the same within 2 %; two teams of four
+// warps (16384 x 2048) take 47 instead of 43 for one.
+constexpr int cta_threads(int warps) { return warps <= 2 ? 256 : 32 * warps; }
 
 template <int kSaved>
 __device__ __forceinline__ void save_group(const SavedOut& to, uint4 x, int64_t at, bool in) {
@@ -102,11 +106,11 @@ __global__ void __launch_bounds__(cta_threads(kWarps)) k_block_norm(const BlockN
         uint64_t n[2][4];
         pairs(wb, n);
         if (a.gamma_post) {
+            uint4 w[2];
+            load(a.gamma_post, 0, w);  // on its way while the sum is formed
             const uint64_t rstd = f2_splat(rstd_of(n, slot));
             slot ^= 1;
-            uint4 w[2];
             uint64_t gam[2][4];
-            load(a.gamma_post, 0, w);
             pairs(w, gam);
 #pragma unroll
             for (int g = 0; g < 2; ++g)
@@ -143,11 +147,11 @@ __global__ void __launch_bounds__(cta_threads(kWarps)) k_block_norm(const BlockN
             if (in[g]) *reinterpret_cast<uint4*>(a.residual_out + at) = w;
             if constexpr (kSaved != RLK_SAVED_BF16) save_group<kSaved>(a.saved_x, w, at, in[g]);
         }
+        uint4 w[2];
+        load(a.gamma_pre, 0, w);
         const uint64_t rstd = f2_splat(rstd_of(x, slot));
         slot ^= 1;
-        uint4 w[2];
         uint64_t gam[2][4];
-        load(a.gamma_pre, 0, w);
         pairs(w, gam);
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
@@ -163,7 +167,9 @@ template <int kWarps, int kSaved>
 cudaError_t launch(const BlockNormArgs& a, int num_sms, cudaStream_t stream) {
     constexpr int kTeams = cta_threads(kWarps) / (32 * kWarps);
     int64_t blocks = (static_cast<int64_t>(a.T) + kTeams - 1) / kTeams;
-    if (blocks > static_cast<int64_t>(num_sms) * 32) blocks = static_cast<int64_t>(num_sms) * 32;
+    // several rows a team only from 64 CTAs an SM on: with 32 16384 x 4096 takes 83.3 instead of 82.5 us, 8191 x
+    // 8192 with three int8 checkpoints and their restoring 253 instead of 246, without them 91 instead of 92
+    if (blocks > static_cast<int64_t>(num_sms) * 64) blocks = static_cast<int64_t>(num_sms) * 64;
     k_block_norm<kWarps, kSaved><<<static_cast<int>(blocks), cta_threads(kWarps), 0, stream>>>(a);
     return cudaGetLastError();
 }
