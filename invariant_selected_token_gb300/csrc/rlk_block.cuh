@@ -90,6 +90,7 @@ struct VerifyArgs {
     int64_t ld_target, ld_draft, ld_noise;
     int target_dtype, draft_dtype;
     int n_draft, n_seqs, V;
+    bool fetch_noise;            // ahead, into the second-level cache
     int32_t* out_accepted;
     int32_t* out_tokens;
     float* out_logprob;
