@@ -296,6 +296,29 @@ def test_in_place_and_canaries(rlk, cuda_device, H, gx):
     assert torch.equal(g3.grad_residual, g.grad_residual) and torch.equal(g3.grad_block, g.grad_block)
 
 
+@pytest.mark.parametrize("H", [320, 4096])
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("go", [BF16, F32])
+@pytest.mark.parametrize("gx", [BF16, F32])
+def test_the_residuals_gradient_in_place(rlk, cuda_device, H, fmt, go, gx):
+    """Every way in which the residual's gradient is read, from more rows than are under way at once."""
+    T = 152 * 40 + 11
+    a = make(T, H, cuda_device, 29)
+    x = a["residual"]
+    kept = dict(x=x, block=a["block"], gate=a["gate"])
+    if fmt != "bf16":
+        kept = {k: rlk.act_quantize(t, fmt) for k, t in kept.items()}
+    dy, res = torch.randn(T, H, device=cuda_device).to(go), torch.randn(T, H, device=cuda_device).to(gx)
+    kw = dict(gamma_pre=a["gamma_pre"], gamma_post=a["gamma_post"], **kept)
+    want = rlk.block_norm_backward(dy, **kw, grad_residual_out=res, grad_dtype=gx)
+    for k in range(2):
+        mine = res.clone()
+        got = rlk.block_norm_backward(dy, **kw, grad_residual_out=mine, grad_residual=mine)
+        assert got.grad_residual.data_ptr() == mine.data_ptr()
+        for p, q in zip(got, want):
+            assert torch.equal(p, q)
+
+
 def test_no_rows(rlk, cuda_device):
     x = torch.zeros((0, 128), dtype=BF16, device=cuda_device)
     gamma = torch.ones(128, dtype=BF16, device=cuda_device)
