@@ -13,6 +13,15 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "slow: long-running (still part of the default run)")
 
 
+@pytest.fixture(autouse=True)
+def _tensors_by_value(monkeypatch):
+    """Queues of spawned ranks carry tensors by value: a rank may leave before its parent reads."""
+    from multiprocessing.context import SpawnContext
+
+    from rank_queue import new_queue
+    monkeypatch.setattr(SpawnContext, "Queue", new_queue, raising=False)
+
+
 @pytest.fixture(scope="session")
 def cuda_device():
     import torch
