@@ -683,7 +683,9 @@ rlk_status_t rlk_rmsnorm_backward_q8(const void* grad_out, int grad_out_dtype, i
  * with u the call's uniform numbers and e the sequence's noise.  With u uniform in
  * [0, 1) and e exponentially distributed the emitted tokens are distributed as the
  * target's own.  Without draft_logits the draft is certain of its tokens: q_i(x_i) = 1, 0 elsewhere.
- * Ties go to the lowest token; where p_i exceeds q_i nowhere the token is drawn from p_i.
+ * Ties go to the lowest token; where p_i exceeds q_i nowhere the token is drawn from p_i.  A token whose
+ * q_i is NaN (its draft logit or its row's draft_lse is) is never drawn, nor is one whose noise is NaN or
+ * negative.
  * p is formed from the contract's (m, s) pair of the row and decisions do not depend on the batch;
  * a token's logprob has the bits that rlk_logits_logprob gives for that row and token.
  *
@@ -693,8 +695,7 @@ rlk_status_t rlk_rmsnorm_backward_q8(const void* grad_out, int grad_out_dtype, i
  *   draft_lse      device, float [n_draft] (rlk_logits_logprob's out_lse of the drafting step),
  *                  or NULL: draft_logits are log-probabilities (rlk_log_softmax's out)
  *   draft_tokens   device, int32 [n_draft];  uniforms  device, float [n_draft]
- *   noise          device, float [n_seqs][ld_noise], positive (a token whose noise is NaN or
- *                  negative, or whose draft logit is NaN, is never drawn); columns [0, V) are read
+ *   noise          device, float [n_seqs][ld_noise], positive; columns [0, V) are read
  *   draft_offsets  device, int32 [n_seqs + 1], ascending within [0, n_draft]
  *   active_mask    device, uint8 [n_seqs] (nonzero = active), or NULL; an inactive sequence
  *                  gets out_accepted 0, tokens -1 and logprobs 0, whatever its inputs hold

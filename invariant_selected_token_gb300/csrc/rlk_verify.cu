@@ -88,14 +88,22 @@ struct Draw {
     const float* noise;
     float m, s, draft_lse;
     int certain;            // token with q = 1, or -1
+    bool from_target;       // p exceeds q nowhere: drawn from p, where q is a number
+
+    // the draft's row as far as the bounds go
+    __device__ __forceinline__ const uint8_t* taken_off() const { return from_target ? nullptr : draft; }
 };
 
 // The weight of a token, exactly as defined, over its noise; 0 where there is none.
 __device__ __noinline__ float weight_of(const VerifyArgs& a, const Draw& r, int v) {
     const float l = logit_at(r.target, a.target_dtype, v), e = r.noise[v];
     float w = __fdiv_rn(exp_diff(l, r.m), r.s);
-    if (r.draft) w = __fsub_rn(w, exp_diff(logit_at(r.draft, a.draft_dtype, v), r.draft_lse));
-    else if (v == r.certain) w = __fsub_rn(w, 1.0f);
+    if (r.draft) {
+        const float q = exp_diff(logit_at(r.draft, a.draft_dtype, v), r.draft_lse);
+        if (!r.from_target || q != q) w = __fsub_rn(w, q);  // NaN is no weight
+    } else if (v == r.certain) {
+        w = __fsub_rn(w, 1.0f);
+    }
     return w > 0.0f ? __fdiv_rn(w, e) : 0.0f;
 }
 
@@ -228,7 +236,7 @@ __device__ __forceinline__ Seen look_vec(const uint8_t* target, const uint8_t* n
 // Looks any tokens [v0, v1) over.
 __device__ __noinline__ Seen look_plain(const VerifyArgs& a, const Draw& r, float log_more, int v0, int v1, Seen seen) {
     const Scale c = {r.m, log_more, r.draft_lse};
-    const uint8_t *const target = r.target, *const draft = r.draft;
+    const uint8_t *const target = r.target, *const draft = r.taken_off();
     const float* const noise = r.noise;
 #pragma unroll 1
     for (int base = v0; base < v1; base += kChunk) {
@@ -257,7 +265,8 @@ __device__ __noinline__ uint64_t look_again(const VerifyArgs& a, const Draw& r, 
         for (int k = 0; k < kAhead; ++k) {
             const int v = token_at<kVec>(base, k), at = min(v, v1 - 1);
             const float l = logit_at(r.target, a.target_dtype, at), e = r.noise[at];
-            const float b = r.draft ? bound_of<true>(l, e, logit_at(r.draft, a.draft_dtype, at), c) : bound_of<false>(l, e, 0.0f, c);
+            const float b = r.taken_off() ? bound_of<true>(l, e, logit_at(r.draft, a.draft_dtype, at), c)
+                                          : bound_of<false>(l, e, 0.0f, c);
             may |= v < v1 && ((b >= 0.0f && b >= known) || unsure(l, e, c)) ? 1u << k : 0u;
         }
         for (; may; may &= may - 1) {
@@ -412,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_draft_verify(const __grid_const
                   : nullptr;
     r.draft_lse = r.draft && a.draft_lse ? a.draft_lse[o0 + acc] : 0.0f;
     r.certain = a.draft ? -1 : refused;
+    r.from_target = false;
     const bool vec = ((reinterpret_cast<uintptr_t>(r.target) | reinterpret_cast<uintptr_t>(r.noise) |
                        reinterpret_cast<uintptr_t>(r.draft)) & 15) == 0;
     // not a distribution: a NaN or +infinity in the row, or nothing but -infinity
@@ -420,11 +430,11 @@ __global__ void __launch_bounds__(kThreads, 4) k_draft_verify(const __grid_const
     const int by_vec = vec ? v0 + (v1 - v0) / kChunk * kChunk : v0;
     const float log_more = __fmaf_rn(-kLog2e, usable ? contract_log(r.s) : 0.0f, kMore);
     uint64_t best = 0;
-    // a second time from p alone where p exceeds q nowhere
+    // a second time from p where p exceeds q nowhere
     for (int pass = 0; usable && pass < 2 && best == 0; ++pass) {
         if (pass == 1) {
             if (acc == n) break;
-            r.draft = nullptr;
+            r.from_target = true;
             r.certain = -1;
             cluster.sync();  // everyone has read the first pass's keys
         }
@@ -436,8 +446,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_draft_verify(const __grid_const
         Seen seen;
         if (by_vec > v0) {
             const uint8_t* const noise = reinterpret_cast<const uint8_t*>(r.noise);
-            seen = r.draft ? look_vec<kTarget, kDraft>(r.target, noise, r.draft, r.m, log_more, r.draft_lse, v0, by_vec)
-                           : look_vec<kTarget, kNoDraft>(r.target, noise, nullptr, r.m, log_more, 0.0f, v0, by_vec);
+            seen = r.taken_off() ? look_vec<kTarget, kDraft>(r.target, noise, r.draft, r.m, log_more, r.draft_lse, v0, by_vec)
+                                 : look_vec<kTarget, kNoDraft>(r.target, noise, nullptr, r.m, log_more, 0.0f, v0, by_vec);
         }
         if (by_vec < v1) seen = look_plain(a, shared_draw, log_more, by_vec, v1, seen);
         uint64_t mine = 0;

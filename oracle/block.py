@@ -145,9 +145,13 @@ def draft_verify(target, tokens, uniforms, noise, offsets, draft=None, draft_lse
                     out[at], logprob[at] = x, row[x] - lse
                     accepted[s] += 1
                     continue
-                w = np.maximum(p - q, 0.0)
+                number = ~np.isnan(q)  # a token whose q is none is never drawn
+                w = np.where(number, np.maximum(p - np.where(number, q, 0.0), 0.0), 0.0)
                 if not (w > 0).any():
-                    w = p
+                    w = np.where(number, p, 0.0)
+                if not (w > 0).any():
+                    logprob[at] = np.nan
+                    break
             else:
                 w = p
             race = w / noise[s]
