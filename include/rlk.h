@@ -550,8 +550,8 @@ rlk_status_t rlk_grad_clip(const void* const* grads, void* const* outs, const in
  * feature's code, the feature is
  *   RLK_SAVED_INT8   c * 2^(b - 133), c in -127 .. 127
  *   RLK_SAVED_E4M3   c * 2^(b - 127), c an e4m3 number (4 exponent, 3 mantissa bits, no infinities)
- * (the shared-exponent blocks of the OCP microscaling formats).  Every such
- * value is a bf16 number, so restoring a checkpoint rounds nothing.
+ * (the shared-exponent blocks of the OCP microscaling formats).  Every value that
+ * rlk_act_quantize writes is a bf16 number, so restoring its checkpoints rounds nothing.
  * rlk_act_quantize takes, with e the exponent of the block's largest
  * magnitude m = f 2^e, b = e + 127 (INT8) and b = e + 119, one more where f >
  * 1.75 (E4M3; not below 0), and rounds each feature to the nearest code, ties
@@ -564,8 +564,10 @@ rlk_status_t rlk_grad_clip(const void* const* grads, void* const* outs, const in
  *   codes        device, one byte a feature [T][H], 16-byte aligned
  *   scales       device, uint8 [T][H / 32]
  *   H            multiple of 64, at most 2^20
- * Codes that the quantiser does not write (INT8 -128, E4M3 0x7F and 0xFF) are taken as -128 and
- * +-480.
+ * Of codes that the quantiser does not write, INT8 -128 and E4M3 0x7F and 0xFF are taken as -128 and
+ * +-480; E4M3 codes that under the bytes 0, 1 and 2 are no multiple of 2^-133, bf16's smallest step,
+ * are restored to the nearest bf16 number, ties to even; from 2^128 on, and with b = 255, values are
+ * infinite.
  */
 #define RLK_SAVED_BF16 0              /* not a checkpoint: the bf16 tensor itself */
 #define RLK_SAVED_INT8 1
@@ -622,8 +624,9 @@ rlk_status_t rlk_block_norm(const void* block, const void* gamma_post, const voi
  *                   where gamma_post is NULL
  * and both norms' grad_gamma, in fp32, each gradient of the batch rounded once to
  * its type.  x, block and gate are bf16 tensors (saved_format RLK_SAVED_BF16, scales
- * NULL) or checkpoints, all three alike; from a checkpoint the call has the bits that it has from the
- * restored tensor.  A row's gradients do not depend on the batch around it; the grad_gammas are
+ * NULL) or checkpoints, all three alike; from a checkpoint of rlk_act_quantize or rlk_block_norm the
+ * call has the bits that it has from the restored tensor.  (Other codes may stand for values that a bf16
+ * tensor would round; the call takes them as they are.)  A row's gradients do not depend on the batch around it; the grad_gammas are
  * summed over ranges of consecutive rows, in chains of 64 rows, and then over the ranges, in an
  * order that T and H fix.
  *
@@ -654,8 +657,8 @@ rlk_status_t rlk_block_norm_backward(
     rlk_stream_t stream);
 
 /*
- * rlk_rmsnorm_backward from an 8-bit checkpoint of x: grad_x has the bits of
- * that call on the restored tensor; grad_gamma is its sum in this call's order
+ * rlk_rmsnorm_backward from an 8-bit checkpoint of x, rlk_act_quantize's or rlk_block_norm's:
+ * grad_x has the bits of that call on the restored tensor; grad_gamma is its sum in this call's order
  * (as rlk_block_norm_backward's).
  *   format, codes, scales  rlk_act_quantize's
  *   workspace      >= rlk_block_norm_backward_workspace_size(T, H) bytes, 256-byte aligned;

@@ -927,7 +927,8 @@ def act_quantize(x: torch.Tensor, fmt: str = "int8", out: Optional[Saved] = None
 
 
 def act_dequantize(saved: Saved, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """The bf16 tensor [T, H] that a checkpoint stands for (exactly: nothing is rounded)."""
+    """The bf16 tensor [T, H] that a checkpoint stands for (exactly: nothing that act_quantize or
+    block_norm wrote is rounded)."""
     if not isinstance(saved, Saved) or not isinstance(saved.codes, torch.Tensor):
         raise TypeError("saved must be a Saved checkpoint")
     _require(saved.codes, saved.codes.dtype, "saved.codes", ndim=2)

@@ -150,7 +150,8 @@ __device__ __forceinline__ void sigmoid_of(uint64_t z, uint64_t& e, uint64_t& r)
 // ---------------------------------------------------------------- 8-bit checkpoints
 // What a block's byte multiplies its codes by: 2^(b - 133) or 2^(b - 127), the smallest ones
 // subnormal, and infinity for 255, whose codes are 0, so that the features come out as NaN.  Codes
-// have at most 7 bits, so every product is exact and a bf16 number.
+// have at most 7 bits, so every product is exact, and a bf16 number unless it is no multiple of 2^-133
+// (some e4m3 codes under the bytes 0 to 2, which the quantiser does not write).
 template <int kSaved>
 __device__ __forceinline__ float saved_scale(uint32_t b) {
     const float s = __uint_as_float(max(b << 23, 0x00400000u));
