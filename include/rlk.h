@@ -87,7 +87,8 @@ typedef enum rlk_status {
     RLK_ERR_CUDA = 5,          /* a CUDA runtime/driver call failed (launch, device query) */
     RLK_ERR_TARGET_RANGE = 6,  /* device-detected: active row whose target no shard owns */
     RLK_ERR_TIMEOUT = 7,       /* device-detected: a bounded pipeline wait gave up */
-    RLK_ERR_NONFINITE = 8      /* device-detected: the gradient norm is infinite or NaN */
+    RLK_ERR_NONFINITE = 8      /* device-detected: the gradient norm is infinite or NaN, or a row
+                                * to draw a token from is no distribution */
 } rlk_status_t;
 
 /* Per-token record of one vocabulary shard (16 bytes). */
@@ -586,7 +587,7 @@ rlk_status_t rlk_act_dequantize(const void* codes, const uint8_t* scales, int fo
  *   x'  = bf16_RN(fma(residual_scale, residual, block_scale * (n * gate(g))))
  *   out = rlk_rmsnorm of x' with gamma_pre, the same bits
  * with rstd as in rlk_rmsnorm and gate(g) = 1, g or 1 / (1 + e^-g), where g below -87 counts as
- * -87 (a gate of 2^-125).  Without
+ * -87 (a gate of 2^-125) and e^-g counts as 0 for g above 86.  Without
  * gamma_post and gate, and with both scales 1, x' too has rlk_rmsnorm's bits.
  * A row's result does not depend on the batch around it.
  *
@@ -701,7 +702,9 @@ rlk_status_t rlk_rmsnorm_backward_q8(const void* grad_out, int grad_out_dtype, i
  *   noise          device, float [n_seqs][ld_noise], positive; columns [0, V) are read
  *   draft_offsets  device, int32 [n_seqs + 1], ascending within [0, n_draft]
  *   active_mask    device, uint8 [n_seqs] (nonzero = active), or NULL; an inactive sequence
- *                  gets out_accepted 0, tokens -1 and logprobs 0, whatever its inputs hold
+ *                  gets out_accepted 0, tokens -1 and logprobs 0, whatever its rows, drafts and noise
+ *                  hold.  (Its target rows are read all the same: an inactive sequence saves its draw,
+ *                  not the sums over its rows, which are the larger part of a large batch.)
  *   out_accepted   device, int32 [n_seqs]: how many drafts were accepted
  *   out_tokens     device, int32 [n_draft + n_seqs], rows as target_logits: the accepted drafts,
  *                  the drawn token, then -1
@@ -712,7 +715,8 @@ rlk_status_t rlk_rmsnorm_backward_q8(const void* grad_out, int grad_out_dtype, i
  * (a NaN or +infinity in it, or nothing but -infinity) or that has no positive weight gives token -1, logprob NaN and
  * RLK_ERR_NONFINITE.  A sequence whose offsets descend or leave [0, n_draft] gets
  * out_accepted -1 and reports RLK_ERR_INVALID_ARG; its tokens are not written (and no row of the outputs
- * that belongs to no sequence is).  n_seqs == 0 is a no-op.
+ * that belongs to no sequence is).  n_seqs == 0, with n_draft == 0, is a no-op.  No output may overlap
+ * an input or another output.
  */
 size_t rlk_draft_verify_workspace_size(int64_t n_draft, int64_t n_seqs, int64_t V);
 rlk_status_t rlk_draft_verify(const void* target_logits, int target_dtype, int64_t ld_target,

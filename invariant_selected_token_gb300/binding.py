@@ -1127,7 +1127,8 @@ def draft_verify(target_logits: torch.Tensor, draft_tokens: torch.Tensor, unifor
     draft's distributions (log-probabilities without draft_lse; certain drafts without either).
     uniforms fp32 [D] in [0, 1), noise fp32 [S, V] exponentially distributed.  tokens holds, in the
     target's rows, the accepted drafts, the token drawn behind them and -1; logprob theirs, with the
-    bits of logits_logprob."""
+    bits of logits_logprob.  active uint8 [S]: sequences that are off are not drawn for, but their
+    target rows are read."""
     if not isinstance(target_logits, torch.Tensor) or not target_logits.is_cuda or target_logits.dim() != 2:
         raise ValueError("target_logits must be a 2-D tensor on a CUDA device")
     dev = target_logits.device
