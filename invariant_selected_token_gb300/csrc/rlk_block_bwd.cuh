@@ -26,11 +26,13 @@
 // What bounds it: with bf16 activations HBM (8191 x 8192, a block without a gate,
 // 138 us, 0.87 of the copy rate; 4096 x 4096 with a gate 51 us, 0.79, a sigmoid one
 // 56, 0.72).  From 8-bit checkpoints it is the instructions: 4096 x 4096, a sigmoid
-// gate, int8, takes 61 us (0.54): 82 instructions a feature at 61 % of the issue slots,
+// gate, int8, takes 61 us (0.54), e4m3 65 (0.51): 82 instructions a feature at 64 % of the issue slots,
 // half of them in the FMA pipe, where a packed pair takes two cycles; 16 warps an SM
 // and two barriers a row leave the rest idle.  Without a gate it is 45 us (0.56), without
-// a branch 32 (0.71; fp32 grad_out).  64 rows are 7 us: one row's latency and the second
-// launch's.
+// a branch 32 (0.71; fp32 grad_out); with fp32 gradients in and out, e4m3, 69 to 87
+// (0.66 to 0.72).  64 rows are 7 us: one row's latency and the second launch's.
+// Rows of fewer than 512 features leave lanes idle: 120000 x 192 takes 87 us without a gate in
+// bf16, 160 with a sigmoid one from int8, 194 from e4m3 with fp32 gradients (floors 41, 45, 80).
 #pragma once
 
 #include <atomic>
@@ -141,6 +143,9 @@ __device__ __forceinline__ void store_grad(void* base, int64_t i, bool in, const
     }
 }
 
+// 128 registers a thread hold two sums and a row's work, but for some instances with a gate: for rows of
+// one warp and of 16 warps up to 40 bytes are spilled, for the widths between none.
+//
 // A team of kWarps warps (a power of two) takes a row, a CTA's teams every kTeams-th row of its
 // range.  A thread copies its own features of the next rows into its own places of a ring of shared
 // memory, which needs no barrier; the copies fly while the current row is reduced.  Places of features

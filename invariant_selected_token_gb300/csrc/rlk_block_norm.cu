@@ -17,11 +17,11 @@
 // is read once.
 //
 // What bounds it: HBM.  16384 x 4096 takes 82 us (0.98 of the copy rate on the
-// bytes it has to move), 8191 x 8192 92 us (0.87), 4096 x 4096 24 (0.84) and with a
-// sigmoid gate 32 (0.79, start and tail of a short launch; 0.92 at 16384 rows); with three
-// int8 checkpoints and their restoring 64 (0.87; 72 % of the issue slots, 61 instructions a
-// feature, a third of them for codes and scales).  8 rows are 2.3 us of latency: two
-// loads and two sums over a row, one after the other.
+// bytes it has to move), 8191 x 8192 92 us (0.87), 4096 x 4096 24 (0.83) and with a
+// sigmoid gate 32 (0.79, start and tail of a short launch; 0.92 at 16384 rows); storing three
+// checkpoints 40 of either kind (0.83; 72 % of the issue slots, 61 instructions a
+// feature, a third of them for codes and scales), without a gate two 30 (0.83).  8 rows are 2.5 us of
+// latency: two loads and two sums over a row, one after the other.
 #include <cstdint>
 
 #include "rlk_block.cuh"
@@ -29,7 +29,7 @@
 namespace rlk {
 namespace {
 
-// Teams of one and two warps share a CTA of 256 threads: with 128 32768 x 1024 takes 53 us instead of 46, with
+// Teams of one and two warps share a CTA of 256 threads: with 128 32768 x 1024 takes 53 us instead of 47, with
 // three checkpoints and their restoring 147 instead of 122, 60000 x 512 the same within 2 %; two teams of four
 // warps (16384 x 2048) take 47 instead of 43 for one.
 constexpr int cta_threads(int warps) { return warps <= 2 ? 256 : 32 * warps; }

@@ -25,8 +25,10 @@
 // What bounds it: for large batches HBM first and the draw's instructions next
 // (256 sequences of up to 8 drafts, V = 151936, fp32: 230 us with the row sums, 137 of
 // them theirs, 0.70 of the copy rate on the bytes of both); for small ones latency:
-// one sequence of 4 bf16 drafts 16.6 us, 5 of them the row sums', 64 sequences of
-// up to 7 looked-up drafts at V = 50257 37.3, 23 of them the row sums'.  Splitting a
+// one sequence of 4 bf16 drafts 17 us, 5 of them the row sums', 64 sequences of
+// up to 7 looked-up drafts at V = 50257 37.5, 23 of them the row sums'; 8 and 32 sequences of up to 8 at V =
+// 151936 21 and 38 in bf16, 30 and 50 in fp32; 256 in bf16 167 (floor 92), with the draft's log-probabilities in
+// fp32 172 (102).  Splitting a
 // sequence over a cluster and not over the grid keeps the draw's meeting in distributed
 // shared memory, in the same launch.
 #include <cooperative_groups.h>
@@ -285,6 +287,8 @@ struct Found {
     RowSum sum, last;
 };
 
+// Four CTAs an SM leave 64 registers: with target and draft in fp32 (and without a draft, whose type is taken as
+// fp32) 24 to 32 bytes a thread are spilled, with one of them in fp32 8 to 16.
 template <int kLogL, int kTarget, int kDraft>
 __global__ void __launch_bounds__(kThreads, 4) k_draft_verify(const __grid_constant__ VerifyArgs a) {
     __shared__ MaxSum node[kWarps][kWarps];  // [row][warp]
@@ -537,8 +541,8 @@ cudaError_t launch_draft_verify(const VerifyArgs& args, int num_sms, cudaStream_
     // at V = 50257 37.3 instead of 38.3 us, 16 at V = 151936 36.6 instead of 37.4
     a.fetch_noise = static_cast<int64_t>(a.n_seqs) * a.V <= (int64_t(1) << 24);
     // up to 8 CTAs a sequence, as long as all of them are resident at once (4 per SM).  Against 4 and 16
-    // of them: one sequence at V = 151936 16.8 us (22.0, 15.8), at V = 1000 11.7 (12.3, 12.9), 16 at V =
-    // 32000 17.0 (18.3, 20.7), 32 at V = 2000 14.0 (13.7, 21.1).
+    // of them, side by side: one sequence at V = 151936 16.8 us (22.0, 15.8), at V = 1000 11.7 (12.3, 12.9), 16
+    // at V = 32000 17.0 (18.3, 20.7), 32 at V = 2000 14.0 (13.7, 21.1).
     int ctas = 8;
     while (ctas > 1 && static_cast<int64_t>(a.n_seqs) * ctas > 4 * static_cast<int64_t>(num_sms)) ctas /= 2;
     const bool draft_f32 = a.draft_dtype == RLK_DTYPE_F32;
