@@ -24,9 +24,9 @@
 // decoded where it is used, up to three times, rather than held.
 //
 // What bounds it: with bf16 activations HBM (8191 x 8192, a block without a gate,
-// 138 us, 0.87 of the copy rate; 4096 x 4096 with a gate 51 us, 0.79, a sigmoid one
+// 139 us, 0.87 of the copy rate; 4096 x 4096 with a gate 51 us, 0.79, a sigmoid one
 // 56, 0.72).  From 8-bit checkpoints it is the instructions: 4096 x 4096, a sigmoid
-// gate, int8, takes 61 us (0.54), e4m3 65 (0.51): 82 instructions a feature at 64 % of the issue slots,
+// gate, int8, takes 61 us (0.54), e4m3 65 (0.51): 82 instructions a feature at 62 % of the issue slots,
 // half of them in the FMA pipe, where a packed pair takes two cycles; 16 warps an SM
 // and two barriers a row leave the rest idle.  Without a gate it is 45 us (0.56), without
 // a branch 32 (0.71; fp32 grad_out); with fp32 gradients in and out, e4m3, 69 to 87

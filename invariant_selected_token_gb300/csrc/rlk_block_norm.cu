@@ -19,7 +19,7 @@
 // What bounds it: HBM.  16384 x 4096 takes 82 us (0.98 of the copy rate on the
 // bytes it has to move), 8191 x 8192 92 us (0.87), 4096 x 4096 24 (0.83) and with a
 // sigmoid gate 32 (0.79, start and tail of a short launch; 0.92 at 16384 rows); storing three
-// checkpoints 40 of either kind (0.83; 72 % of the issue slots, 61 instructions a
+// checkpoints 40 of either kind (0.83; 71 % of the issue slots, 61 instructions a
 // feature, a third of them for codes and scales), without a gate two 30 (0.83).  8 rows are 2.5 us of
 // latency: two loads and two sums over a row, one after the other.
 #include <cstdint>
